@@ -44,6 +44,12 @@ MFA_PLAN_CHECK = 0x1
 MFA_PLAN_NO_COMBINE = 0x2
 MFA_PLAN_EARLY_METADATA = 0x4
 
+MFA_ROPE_HALF = 0
+MFA_ROPE_ADJACENT = 1
+MFA_ROPE_MAX_AXES = 4
+MFA_ROPE_INTERLEAVED = 0x1
+MFA_ROPE_OWN_SPECTRUM = 0x2
+
 NUM_Q_HEADS = 64
 HEAD_DIM = 256
 PAGE_SIZE = 64
@@ -52,7 +58,8 @@ PAGE_SIZE = 64
 EXPORTED_SYMBOLS = ("mfa_decode_plan", "mfa_decode_run", "mfa_combine", "mfa_read_device_status",
                     "mfa_status_string", "mfa_abi_version", "mfa_last_cuda_error",
                     "mfa_decode_run_static_workspace", "mfa_kv_append", "mfa_decode_run_host",
-                    "mfa_decode_append_run")
+                    "mfa_decode_append_run", "mfa_block_decode_plan", "mfa_block_decode_run", "mfa_block_kv_append",
+                    "mfa_rope_table", "mfa_rope_run")
 
 # Size of the library's own scratch array used by mfa_decode_run_static_workspace.
 MFA_STATIC_WORKSPACE_BYTES = 24 * 1024 * 1024
@@ -74,6 +81,21 @@ class MfaPlan(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("num_sms", ctypes.c_int32),
                 ("total_tiles", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
                 ("tokens_per_seq", ctypes.c_int32)]
+
+
+class MfaRopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * MFA_ROPE_MAX_AXES), ("pairing", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("theta", ctypes.c_double), ("position_scale", ctypes.c_double)]
+
+
+class MfaRopePair(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64), ("axis", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MfaRopeRows(ctypes.Structure):
+    _fields_ = [("data_in", ctypes.c_void_p), ("data_out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
 
 
 class MfaError(RuntimeError):
@@ -125,6 +147,20 @@ def load_library(path: str = LIB_PATH):
     lib.mfa_decode_append_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), P, P, P, P, P, P, P,
                                           P, P, P, P, P, P, ctypes.c_uint64, P]
     lib.mfa_decode_append_run.restype = ctypes.c_int
+    lib.mfa_block_decode_plan.argtypes = [ctypes.POINTER(MfaProblem), ctypes.c_int32, P, ctypes.c_int32,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_uint32, ctypes.POINTER(MfaPlan)]
+    lib.mfa_block_decode_plan.restype = ctypes.c_int
+    lib.mfa_block_decode_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, P,
+                                         P, P, P, P, P, P, P, ctypes.c_uint64, P]
+    lib.mfa_block_decode_run.restype = ctypes.c_int
+    lib.mfa_block_kv_append.argtypes = [ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, ctypes.c_int32, P,
+                                        ctypes.c_int32, P, P, P, P, P, P, P, P]
+    lib.mfa_block_kv_append.restype = ctypes.c_int
+    lib.mfa_rope_table.argtypes = [ctypes.POINTER(MfaRopeConfig), P]
+    lib.mfa_rope_table.restype = ctypes.c_int
+    lib.mfa_rope_run.argtypes = [ctypes.POINTER(MfaRopeConfig), P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                 ctypes.POINTER(MfaRopeRows), ctypes.POINTER(MfaRopeRows), P]
+    lib.mfa_rope_run.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -290,6 +326,65 @@ def mfa_kv_append(problem: MfaProblem, k_new, v_new, positions, block_table, k_c
     _check(st, "mfa_kv_append")
 
 
+def mfa_block_decode_plan(problem: MfaProblem, scale_tokens: int, host_seq_lens: Optional[Sequence[int]] = None,
+                          max_seq_len: int = 0, num_sms: int = 0, force_ctas: int = 0, flags: int = 0) -> MfaPlan:
+    """Split the work of mfa_block_decode_run (host only); see include/mfa.h."""
+    lib = load_library()
+    plan = MfaPlan()
+    lens_arr = None
+    if host_seq_lens is not None:
+        vals = [int(v) for v in host_seq_lens]
+        if len(vals) != problem.batch:
+            raise ValueError(f"host_seq_lens holds {len(vals)} lengths, the batch is {problem.batch}")
+        lens_arr = (ctypes.c_int32 * max(1, len(vals)))(*vals)
+    st = lib.mfa_block_decode_plan(ctypes.byref(problem), int(scale_tokens), lens_arr, int(max_seq_len), int(num_sms),
+                                   int(force_ctas), int(flags), ctypes.byref(plan))
+    _check(st, "mfa_block_decode_plan")
+    return plan
+
+
+def mfa_block_decode_run(plan: MfaPlan, problem: MfaProblem, scale_tokens: int, q, k_cache, v_cache, k_scale, v_scale,
+                         block_table, seq_lens, out, lse, workspace, stream=None,
+                         workspace_bytes: Optional[int] = None) -> None:
+    """One decode step over a block-scaled 8-bit cache (see include/mfa.h)."""
+    lib = load_library()
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    st = lib.mfa_block_decode_run(ctypes.byref(plan), ctypes.byref(problem), scale_tokens, _ptr(q), _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+                                  _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check(st, "mfa_block_decode_run")
+
+
+def mfa_block_kv_append(problem: MfaProblem, scale_tokens: int, k_new, v_new, num_new: int, new_offsets, max_new: int,
+                        positions, block_table, k_cache, v_cache, k_scale, v_scale, device_status=None,
+                        stream=None) -> None:
+    """Quantise new key/value rows into a block-scaled 8-bit cache (see include/mfa.h)."""
+    lib = load_library()
+    st = lib.mfa_block_kv_append(ctypes.byref(problem), scale_tokens, _ptr(k_new), _ptr(v_new), num_new,
+                                 _ptr(new_offsets), max_new, _ptr(positions), _ptr(block_table), _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(device_status), _stream(stream))
+    _check(st, "mfa_block_kv_append")
+
+
+def mfa_rope_table(config: MfaRopeConfig):
+    """The table of ``config``'s rotary pairs as a host array (rotary_dim / 2 entries)."""
+    lib = load_library()
+    table = (MfaRopePair * max(1, config.rotary_dim // 2))()
+    _check(lib.mfa_rope_table(ctypes.byref(config), ctypes.cast(table, ctypes.c_void_p)), "mfa_rope_table")
+    return table
+
+
+def mfa_rope_run(config: MfaRopeConfig, table, positions, num_rows: int, dtype: int, inverse: int,
+                 q: Optional[MfaRopeRows], k: Optional[MfaRopeRows], stream=None) -> None:
+    """Turn query and key rows by their positions (see include/mfa.h)."""
+    lib = load_library()
+    st = lib.mfa_rope_run(ctypes.byref(config), _ptr(table), _ptr(positions), num_rows, dtype, inverse,
+                          None if q is None else ctypes.byref(q), None if k is None else ctypes.byref(k),
+                          _stream(stream))
+    _check(st, "mfa_rope_run")
+
+
 def mfa_read_device_status(workspace, clear: bool = True, stream=None) -> int:
     lib = load_library()
     word = ctypes.c_uint32(0)
@@ -362,3 +457,180 @@ class Decoder:
         mfa_decode_run_host(self.plan, self.problem, q_host, block_table_host, seq_lens_host, out_host, lse_host,
                             st["q"], st["table"], st["lens"], st["out"], None if lse_host is None else st["lse"],
                             k_cache, v_cache, k_scale, v_scale, self.workspace, stream)
+
+
+def _is(x, name: str, dtype, shape, device) -> None:
+    """x must be a contiguous tensor of this dtype and shape on this device."""
+    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+class _OnDevice:
+    """Makes a device current for a call on its tensors; used where another one is current."""
+
+    def __init__(self, device):
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("expected a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _run(self, call, stream):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            return call(_stream(stream))
+        with torch.cuda.device(self.device):
+            return call(_stream(stream))
+
+
+class BlockDecoder(_OnDevice):
+    """Decode and append over a block-scaled 8-bit cache: plan and workspace for one batch shape.
+
+    The cache: ``k_cache``, ``v_cache`` uint8 [num_blocks, num_kv_heads, 64, head_dim] (e4m3
+    codes), ``k_scale``, ``v_scale`` fp32 [num_blocks, num_kv_heads, 64 // scale_tokens];
+    ``block_table`` int32 [batch, max_pages_per_seq].  Device buffers come from PyTorch's
+    allocator.  Calls that may overlap on the GPU need a decoder (a workspace) each.
+    """
+
+    def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, num_q_heads: int = NUM_Q_HEADS,
+                 num_kv_heads: int = 1, head_dim: int = HEAD_DIM, scale_tokens: int = 64,
+                 softmax_scale: Optional[float] = None, host_seq_lens=None, max_seq_len: int = 0, force_ctas: int = 0,
+                 flags: int = 0, device=None, out_dtype: int = MFA_OUT_BF16, tokens_per_seq: int = 1):
+        import torch
+        super().__init__(device)
+        self.scale_tokens = int(scale_tokens)
+        self.problem = make_problem(batch, max_pages_per_seq, num_blocks, MFA_KV_FP8_E4M3, softmax_scale,
+                                    num_q_heads=num_q_heads, head_dim=head_dim, out_dtype=out_dtype,
+                                    tokens_per_seq=tokens_per_seq, num_kv_heads=num_kv_heads)
+        if host_seq_lens is None and max_seq_len == 0:
+            max_seq_len = max_pages_per_seq * PAGE_SIZE
+        with torch.cuda.device(self.device):
+            self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
+                                              force_ctas, flags)
+            self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+        rows = batch * tokens_per_seq
+        self._q_shape = (rows, num_q_heads, head_dim)
+        self._cache_shape = (num_blocks, num_kv_heads, PAGE_SIZE, head_dim)
+        self._scale_shape = (num_blocks, num_kv_heads, PAGE_SIZE // self.scale_tokens)
+        self._table_shape = (batch, max_pages_per_seq)
+        self._out_dtype = torch.float32 if out_dtype == MFA_OUT_FP32 else torch.bfloat16
+
+    def _check_cache(self, k_cache, v_cache, k_scale, v_scale, block_table):
+        import torch
+        _is(k_cache, "k_cache", torch.uint8, self._cache_shape, self.device)
+        _is(v_cache, "v_cache", torch.uint8, self._cache_shape, self.device)
+        _is(k_scale, "k_scale", torch.float32, self._scale_shape, self.device)
+        _is(v_scale, "v_scale", torch.float32, self._scale_shape, self.device)
+        _is(block_table, "block_table", torch.int32, self._table_shape, self.device)
+
+    def __call__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None, lse=None, stream=None):
+        """One decode step: (out [batch * tokens, num_q_heads, head_dim], lse [.., num_q_heads])."""
+        import torch
+        _is(q, "q", torch.bfloat16, self._q_shape, self.device)
+        self._check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+        _is(seq_lens, "seq_lens", torch.int32, self._table_shape[:1], self.device)
+        if out is None:
+            out = torch.empty(self._q_shape, dtype=self._out_dtype, device=self.device)
+        else:
+            _is(out, "out", self._out_dtype, self._q_shape, self.device)
+        if lse is None:
+            lse = torch.empty(self._q_shape[:2], dtype=torch.float32, device=self.device)
+        else:
+            _is(lse, "lse", torch.float32, self._q_shape[:2], self.device)
+        lib = load_library()
+        st = self._run(lambda s: lib.mfa_block_decode_run(
+            self.plan, self.problem, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes, s), stream)
+        _check(st, "mfa_block_decode_run")
+        return out, lse
+
+    def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
+               max_new: int = 0, device_status=None, stream=None):
+        """Quantise new rows into the cache: bf16 ``k_new``, ``v_new`` [rows, num_kv_heads, head_dim], sequence b's
+        being rows offsets[b] .. offsets[b + 1] - 1 (``offsets`` int32 [batch + 1], ``max_new`` their largest
+        count), or ``tokens_per_seq`` each.  ``device_status``: the decoder's workspace by default, so that
+        mfa_read_device_status(decoder.workspace) reports both steps."""
+        import torch
+        rows = int(k_new.shape[0])
+        shape = (rows,) + self._cache_shape[1:4:2]
+        _is(k_new, "k_new", torch.bfloat16, shape, self.device)
+        _is(v_new, "v_new", torch.bfloat16, shape, self.device)
+        self._check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+        _is(positions, "positions", torch.int32, self._table_shape[:1], self.device)
+        if offsets is not None:
+            _is(offsets, "offsets", torch.int32, (self._table_shape[0] + 1,), self.device)
+        status = self.workspace if device_status is None else device_status
+        lib = load_library()
+        st = self._run(lambda s: lib.mfa_block_kv_append(
+            self.problem, self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
+            None if offsets is None else offsets.data_ptr(), int(max_new), positions.data_ptr(),
+            block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            _ptr(status), s), stream)
+        _check(st, "mfa_block_kv_append")
+
+
+class Rope(_OnDevice):
+    """Rotary positions with one to four axes for query heads and new key rows.
+
+    ``sections``: rotary pairs of each axis (their sum is half the rotated width, at most
+    head_dim / 2).  ``pairing``: "half" (elements i and i + rotated / 2) or "adjacent" (2 i and
+    2 i + 1).  ``interleaved``: the axes are dealt to the pairs in turn instead of one run each;
+    ``own_spectrum``: each axis has frequencies of its own.  See include/mfa.h.
+    """
+
+    def __init__(self, head_dim: int, sections: Sequence[int], theta: float = 1e4, pairing: str = "half",
+                 interleaved: bool = False, own_spectrum: bool = False, position_scale: float = 1.0, device=None):
+        import torch
+        super().__init__(device)
+        if pairing not in ("half", "adjacent"):
+            raise ValueError(f"pairing: expected 'half' or 'adjacent', got {pairing!r}")
+        if not 1 <= len(sections) <= MFA_ROPE_MAX_AXES:
+            raise ValueError(f"sections: expected 1 to {MFA_ROPE_MAX_AXES} axes, got {len(sections)}")
+        self.head_dim, self.axes = int(head_dim), len(sections)
+        self.config = MfaRopeConfig(self.head_dim, 2 * int(sum(sections)), self.axes,
+                                    (ctypes.c_int32 * MFA_ROPE_MAX_AXES)(*[int(n) for n in sections]),
+                                    MFA_ROPE_HALF if pairing == "half" else MFA_ROPE_ADJACENT,
+                                    (MFA_ROPE_INTERLEAVED if interleaved else 0) |
+                                    (MFA_ROPE_OWN_SPECTRUM if own_spectrum else 0), float(theta), float(position_scale))
+        table = mfa_rope_table(self.config)
+        self.table = torch.frombuffer(bytearray(bytes(table)), dtype=torch.uint8).to(self.device)
+
+    def _rows(self, x, out, name: str, rows: int, dtype) -> MfaRopeRows:
+        for t, what in ((x, name), (out, name + "_out")):
+            if t.dtype is not dtype or t.dim() != 3 or t.shape[0] != rows or t.shape[2] != self.head_dim or \
+                    t.shape != x.shape or t.device != self.device or \
+                    (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim))):
+                raise ValueError(f"{what}: expected {dtype} [{rows}, heads, {self.head_dim}] on {self.device} with "
+                                 f"each row's heads side by side, got {t.dtype} {tuple(t.shape)} strides {t.stride()} "
+                                 f"on {t.device}")
+        least = x.shape[1] * self.head_dim   # (a single row has no stride of its own)
+        return MfaRopeRows(x.data_ptr(), out.data_ptr(), max(x.stride(0), least) if rows < 2 else x.stride(0),
+                           max(out.stride(0), least) if rows < 2 else out.stride(0), x.shape[1])
+
+    def __call__(self, q, k, positions, inverse: bool = False, q_out=None, k_out=None, stream=None):
+        """Turned rows (q_out, k_out) of q and k, [rows, heads, head_dim] in bf16 or fp32 (either may be None; rows
+        may be strided, as columns of one projection); positions int32 [axes, rows].  Pass q_out = q and k_out = k
+        to turn in place.  ``inverse``: by the negative angles, which is the gradient of the forward call."""
+        import torch
+        some = k if q is None else q
+        if some is None:
+            raise ValueError("expected q or k")
+        rows, dtype = int(some.shape[0]), some.dtype
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise ValueError(f"expected bf16 or fp32 rows, got {dtype}")
+        _is(positions, "positions", torch.int32, (self.axes, rows), self.device)
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=self.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype, device=self.device)
+        rq = None if q is None else self._rows(q, q_out, "q", rows, dtype)
+        rk = None if k is None else self._rows(k, k_out, "k", rows, dtype)
+        lib = load_library()
+        st = self._run(lambda s: lib.mfa_rope_run(
+            self.config, self.table.data_ptr(), positions.data_ptr(), rows,
+            MFA_OUT_BF16 if dtype is torch.bfloat16 else MFA_OUT_FP32, 1 if inverse else 0, rq, rk, s), stream)
+        _check(st, "mfa_rope_run")
+        return q_out, k_out

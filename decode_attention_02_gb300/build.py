@@ -9,7 +9,8 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmfa.so")
-SOURCES = [os.path.join(PKG, "csrc", "mfa_decode.cu"), os.path.join(PKG, "csrc", "mfa_kv_append.cu")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in
+           ("mfa_decode.cu", "mfa_kv_append.cu", "mfa_block_decode.cu", "mfa_block_append.cu", "mfa_rope.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,12 +38,23 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=()) ->
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-           "-I" + os.path.join(ROOT, "include"), "-o", tmp, *SOURCES, *extra_flags]
+    flags = [*ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
+             "-I" + os.path.join(ROOT, "include"), *extra_flags]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+        flags.insert(0, "-Xptxas=-v")
+        print(" ".join(flags))
+    # one compiler process per source, side by side; then the link
+    objects = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    jobs = [subprocess.Popen([_nvcc(), *flags, "-c", "-o", obj, src]) for src, obj in zip(SOURCES, objects)]
+    try:
+        failed = [src for src, job in zip(SOURCES, jobs) if job.wait() != 0]
+        if failed:
+            raise RuntimeError("nvcc failed on " + ", ".join(failed))
+        subprocess.check_call([_nvcc(), *ARCH, "-shared", "-o", tmp, *objects])
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, LIB)
     return LIB
 

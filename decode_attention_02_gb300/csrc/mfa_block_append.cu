@@ -1,0 +1,294 @@
+// KV append to a block-scaled 8-bit cache (GB300, sm_103a): new bf16 key and value rows are
+// written as e4m3 codes under one fp32 scale for each block of tokens and head.
+//
+// For a block that gets rows, a = the largest finite |x| of its new rows (one head):
+//     need = 2^e, the smallest power of two with a <= 448 * 2^e;
+//     s    = need, or max(need, s_old) where the block holds older rows;
+//     code = e4m3(x / s);  where s > s_old the older codes become e4m3(value * (s_old / s)).
+// Powers of two: e4m3 has an exponent of its own, so that its precision does not depend on
+// where in an octave the maximum falls, and a rise of the scale shifts the older codes'
+// exponents without rounding them again (except below e4m3's smallest step).
+//
+// An item is one (block, head, K or V): its new rows are read once, into registers; their
+// maximum gives the scale; the codes are written.  Items share nothing, so the work is one
+// pass over the data with no atomics but error flags.
+//   - Prompts: one CTA of 256 threads an item, the rows of a whole block (up to 64 x 256
+//     elements) in 8 registers of 8 elements a thread, all loads in flight together.
+//   - Few rows a sequence (a decode step): one warp an item, up to 4 rows; 8 items a CTA.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "mfa.h"
+#include "mfa_host.h"
+#include "ptx.cuh"
+#include "mfa_append_row.cuh"
+
+namespace mfa {
+
+constexpr int kBlkPage = 64;
+constexpr int kBlkThreads = 256;
+constexpr int kFewRows = 4;           // most new rows a block gets on the warp path
+constexpr int kChunks = 8;            // 8-element chunks a thread holds
+static_assert(kChunks * kBlkThreads * 8 >= 64 * 256, "a CTA holds a whole block of 64 rows of 256");
+static_assert(kChunks * 32 * 8 >= kFewRows * 256, "a warp holds the few rows");
+
+struct BlockAppendParams {
+  const uint4* k_new;        // bf16 [num_new, G, d] as 8-element chunks
+  const uint4* v_new;
+  const int32_t* offsets;    // may be null: `tokens` rows a sequence
+  const int32_t* positions;
+  const int32_t* block_table;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;
+  float* v_scale;
+  unsigned int* status;      // may be null
+  int batch, tokens, num_new, max_new;
+  int most_blocks;           // blocks a sequence's new rows can touch
+  int heads;                 // G
+  int log_chunks;            // log2(d / 8)
+  int log_scale;             // log2(scale_tokens)
+  int max_pages, num_blocks;
+};
+
+// The smallest power of two s = 2^e, e >= -126, with a <= 448 s (a finite, >= 0): with
+// a = 2^E (1 + f), 448 = 1.75 * 2^8, so e = E - 8 while 1 + f <= 1.75, else E - 7.
+__device__ __forceinline__ float pow2_scale(float a) {
+  const uint32_t bits = __float_as_uint(a);
+  int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  if (bits == 0u || e < -126) e = -126;
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Eight bf16 values to eight e4m3 codes of x / s.  Where s is a power of two with a normal
+// reciprocal the product with it is the quotient, exactly (a quotient below the normal range
+// rounds to a zero code either way).
+__device__ __forceinline__ uint2 encode_chunk(uint4 x, float s, float inv, bool exact_inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = bf16_bits_lo(w[i]), hi = bf16_bits_hi(w[i]);
+    c[i] = exact_inv ? e4m3x2_rn_sat(lo * inv, hi * inv) : e4m3x2_rn_sat(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Four e4m3 codes times r, rounded back to e4m3 (e4m3 values are exact in f16).
+__device__ __forceinline__ uint32_t recode4(uint32_t codes, float r) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes >> (16 * i))));
+    const __half2 h2 = *reinterpret_cast<const __half2*>(&h);
+    out |= e4m3x2_rn_sat(__low2float(h2) * r, __high2float(h2) * r) << (16 * i);
+  }
+  return out;
+}
+
+// kItemThreads = 256: an item a CTA; 32: an item a warp.
+template <int kItemThreads>
+__global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __grid_constant__ BlockAppendParams p) {
+  constexpr int kItems = kBlkThreads / kItemThreads;
+  __shared__ float wmax[kBlkThreads / 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int it = threadIdx.x % kItemThreads;
+  // item = ((sequence, touched block m), head, K or V)
+  const long long items = static_cast<long long>(p.batch) * p.most_blocks * p.heads * 2;
+  const long long item = static_cast<long long>(blockIdx.x) * kItems + threadIdx.x / kItemThreads;
+  if (item >= items) return;   // (the last CTA of the warp path: whole warps leave)
+  const bool is_v = (item & 1) != 0;
+  const long long bh = item >> 1;
+  const int g = static_cast<int>(bh % p.heads);
+  const int m = static_cast<int>((bh / p.heads) % p.most_blocks);
+  const int b = static_cast<int>(bh / p.heads / p.most_blocks);
+  const bool reporter = it == 0 && !is_v && g == 0 && p.status != nullptr;
+
+  const int t0 = p.positions[b];
+  int r0 = b * p.tokens, n = p.tokens;   // the sequence's rows r0 .. r0 + n - 1
+  if (p.offsets != nullptr) {
+    r0 = p.offsets[b];
+    const int r1 = p.offsets[b + 1];
+    if (r0 < 0 || r1 < r0 || r1 > p.num_new) {
+      if (reporter && m == 0) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
+      return;
+    }
+    n = r1 - r0;
+  }
+  if (t0 < 0 || n == 0) return;
+  const long long cap = static_cast<long long>(p.max_pages) * kBlkPage;
+  const long long fit = cap > t0 ? cap - t0 : 0;
+  if (n > p.max_new || n > fit) {
+    if (reporter && m == 0) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
+    n = static_cast<int>(min(static_cast<long long>(min(n, p.max_new)), fit));
+    if (n == 0) return;   // (t0 may lie far past the table)
+  }
+  const int bt = 1 << p.log_scale;
+  const int first = ((t0 >> p.log_scale) + m) << p.log_scale;   // first token of this block
+  if (first >= t0 + n) return;
+  const int lo = max(t0, first), hi = min(t0 + n, first + bt);  // new tokens [lo, hi) of the block
+  const int blk = p.block_table[static_cast<size_t>(b) * p.max_pages + first / kBlkPage];
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (reporter) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
+    return;
+  }
+  const size_t ph = static_cast<size_t>(blk) * p.heads + g;      // (page, head)
+  float* scale = (is_v ? p.v_scale : p.k_scale) + (ph << (6 - p.log_scale)) + ((first % kBlkPage) >> p.log_scale);
+  uint8_t* rows = (is_v ? p.v_cache : p.k_cache) + (((ph * kBlkPage) << p.log_chunks) << 3);
+  const bool begun = lo > first;
+  const float s_old = begun ? *scale : 0.f;
+
+  // the new rows, in registers
+  const uint4* src = (is_v ? p.v_new : p.k_new);
+  const int chunks = (hi - lo) << p.log_chunks;
+  uint4 x[kChunks];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = it + i * kItemThreads;
+    if (c < chunks) {
+      const size_t r = static_cast<size_t>(r0 + (lo - t0) + (c >> p.log_chunks)) * p.heads + g;
+      x[i] = __ldg(src + (r << p.log_chunks) + (c & ((1 << p.log_chunks) - 1)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    if (it + i * kItemThreads < chunks) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float u = fabsf(bf16_bits_lo(w[k])), v = fabsf(bf16_bits_hi(w[k]));
+        a = fmaxf(a, u < INFINITY ? u : 0.f);   // (false for NaN too)
+        a = fmaxf(a, v < INFINITY ? v : 0.f);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if constexpr (kItemThreads > 32) {
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
+    __syncthreads();   // (and every thread has read s_old)
+#pragma unroll
+    for (int w = 0; w < kItemThreads / 32; ++w) a = fmaxf(a, wmax[w]);
+  }
+  const float need = pow2_scale(a);
+  const float s = begun ? fmaxf(s_old, need) : need;
+  const uint32_t sb = __float_as_uint(s);
+  const bool exact_inv = (sb & 0x7FFFFFu) == 0u && sb >= (1u << 23) && sb <= (253u << 23);
+  const float inv = __uint_as_float((254u << 23) - sb);   // 1 / s there
+  uint2* dst = reinterpret_cast<uint2*>(rows);
+  const int at = ((lo % kBlkPage) << p.log_chunks);       // first new row's chunk in the page
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = it + i * kItemThreads;
+    if (c < chunks) dst[at + c] = encode_chunk(x[i], s, inv, exact_inv);
+  }
+  if (begun && s > s_old) {
+    const float r = __fdiv_rn(s_old, s);
+    const int from = (first % kBlkPage) << p.log_chunks;
+    for (int c = from + it; c < at; c += kItemThreads) {
+      const uint2 old = dst[c];
+      dst[c] = make_uint2(recode4(old.x, r), recode4(old.y, r));
+    }
+  }
+  if (it == 0 && !(begun && s == s_old)) *scale = s;
+}
+
+mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens) {
+  if (pr == nullptr) return MFA_ERR_INVALID_ARG;
+  if (pr->batch < 0 || pr->max_pages_per_seq < 1 || pr->num_blocks < 1) return MFA_ERR_INVALID_ARG;
+  if (pr->tokens_per_seq < 1 || pr->tokens_per_seq > 4) return MFA_ERR_INVALID_ARG;
+  if (pr->num_q_heads < 1 || pr->num_kv_heads < 1 || pr->head_dim < 1 || pr->page_size < 1 || scale_tokens < 1)
+    return MFA_ERR_INVALID_ARG;
+  if (pr->kv_dtype != MFA_KV_BF16 && pr->kv_dtype != MFA_KV_FP8_E4M3 && pr->kv_dtype != MFA_KV_MXFP4)
+    return MFA_ERR_INVALID_ARG;
+  if (pr->kv_shared != 0 && pr->kv_shared != 1) return MFA_ERR_INVALID_ARG;
+  if (pr->out_dtype != MFA_OUT_BF16 && pr->out_dtype != MFA_OUT_FP32) return MFA_ERR_INVALID_ARG;
+  if (!(pr->softmax_scale > 0.f && pr->softmax_scale <= 3.4028235e38f)) return MFA_ERR_INVALID_ARG;
+  if (pr->num_q_heads % pr->num_kv_heads != 0) return MFA_ERR_INVALID_ARG;
+  if (pr->kv_dtype != MFA_KV_FP8_E4M3 || pr->kv_shared != 0) return MFA_ERR_UNSUPPORTED;
+  if (pr->page_size != kBlkPage || (pr->head_dim != 128 && pr->head_dim != 256)) return MFA_ERR_UNSUPPORTED;
+  if (scale_tokens != 16 && scale_tokens != 32 && scale_tokens != 64) return MFA_ERR_UNSUPPORTED;
+  if (pr->num_q_heads / pr->num_kv_heads > 64) return MFA_ERR_UNSUPPORTED;
+  // sizes that 32-bit indices of tokens, rows and (page, head) pairs reach
+  if (static_cast<long long>(pr->max_pages_per_seq) * kBlkPage > INT_MAX / 2) return MFA_ERR_INVALID_ARG;
+  if (static_cast<long long>(pr->num_blocks) * pr->num_kv_heads > INT_MAX / 2) return MFA_ERR_INVALID_ARG;
+  if (static_cast<long long>(pr->batch) * pr->tokens_per_seq > INT_MAX / 2 / pr->num_q_heads) return MFA_ERR_INVALID_ARG;
+  return MFA_OK;
+}
+
+}  // namespace mfa
+
+using namespace mfa;
+
+extern "C" mfa_status mfa_block_kv_append(const mfa_problem* pr, int32_t scale_tokens, const void* k_new,
+                                          const void* v_new, int32_t num_new, const int32_t* new_offsets,
+                                          int32_t max_new, const int32_t* positions, const int32_t* block_table,
+                                          void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                          uint32_t* device_status, void* stream_ptr) {
+  const mfa_status st = check_block_problem(pr, scale_tokens);
+  if (st != MFA_OK) return st;
+  if (num_new < 0 || (device_status && !aligned(device_status, 4))) return MFA_ERR_INVALID_ARG;
+  if (new_offsets == nullptr) {
+    if (static_cast<long long>(pr->batch) * pr->tokens_per_seq != num_new) return MFA_ERR_INVALID_ARG;
+    max_new = pr->tokens_per_seq;
+  }
+  if (pr->batch == 0 || num_new == 0) return MFA_OK;
+  if (max_new < 1) return MFA_ERR_INVALID_ARG;
+  if (!k_new || !v_new || !positions || !block_table || !k_cache || !v_cache || !k_scale || !v_scale)
+    return MFA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(positions, 4) || !aligned(block_table, 4) ||
+      (new_offsets && !aligned(new_offsets, 4)))
+    return MFA_ERR_INVALID_ARG;
+  const int most_rows = std::min(max_new, num_new);
+  // a run of n rows touches 1 + floor((n + scale_tokens - 2) / scale_tokens) blocks at most
+  const long long most =
+      std::min<long long>((static_cast<long long>(most_rows) + scale_tokens - 2) / scale_tokens + 1,
+                          static_cast<long long>(pr->max_pages_per_seq) * (kBlkPage / scale_tokens));
+  const bool few = most_rows <= kFewRows;
+  const long long items = pr->batch * most * pr->num_kv_heads * 2;
+  const long long ctas = few ? (items + 7) / 8 : items;
+  if (ctas > INT_MAX) return MFA_ERR_INVALID_ARG;
+  BlockAppendParams p;
+  p.k_new = static_cast<const uint4*>(k_new);
+  p.v_new = static_cast<const uint4*>(v_new);
+  p.offsets = new_offsets;
+  p.positions = positions;
+  p.block_table = block_table;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = device_status;
+  p.batch = pr->batch;
+  p.tokens = pr->tokens_per_seq;
+  p.num_new = num_new;
+  p.max_new = most_rows;
+  p.most_blocks = static_cast<int>(most);
+  p.heads = pr->num_kv_heads;
+  p.log_chunks = pr->head_dim == 256 ? 5 : 4;
+  p.log_scale = scale_tokens == 64 ? 6 : scale_tokens == 32 ? 5 : 4;
+  p.max_pages = pr->max_pages_per_seq;
+  p.num_blocks = pr->num_blocks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kBlkThreads, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream_ptr);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, mfa_block_append_kernel<32>, p)
+                            : cudaLaunchKernelEx(&cfg, mfa_block_append_kernel<256>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "block append launch");
+  return MFA_OK;
+}

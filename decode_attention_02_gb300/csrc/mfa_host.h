@@ -18,6 +18,9 @@ mfa_status check_problem(const mfa_problem* pr);
 // 2 shared latent.
 int problem_shape(const mfa_problem* pr);
 
+// Shape, dtype and range checks of a problem over a block-scaled cache (MFA_OK, or the error).
+mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens);
+
 // True when p is a multiple of a bytes.
 bool aligned(const void* p, uintptr_t a);
 

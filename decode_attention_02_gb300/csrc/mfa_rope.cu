@@ -1,0 +1,323 @@
+// Rotary positions with several axes for query heads and new key rows (GB300, sm_103a).
+//
+// Pair i of a head turns by the angle position[axis(i)] * frequency(i):
+//     a' = a cos - b sin,   b' = b cos + a sin.
+// Angles: the table holds each frequency as a 64-bit fraction of a turn, and position times
+// fraction modulo 2^64 is the angle modulo one turn, exact to 2^-53 of a turn at any 32-bit
+// position, in two integer multiplies; sincospif of its top 32 bits gives cos and sin to fp32.
+// (A product in fp32 is off by 2^-24 of the whole angle, 0.008 rad at position 131072.)
+//
+// Every element is read once and written once, with some 3 operations for each: HBM-bound for
+// a prompt, launch-bound for a decode step.  A CTA turns all heads of one row, so that the
+// row's angles are computed once, by as many threads as there are pairs, and shared; each
+// thread owns one place in a head (8 elements of a pair's first half and 8 of its second) and
+// keeps its 8 cosines and sines in registers over its heads.  The loads of all its heads go
+// out before the angles are computed.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "mfa.h"
+#include "mfa_host.h"
+#include "ptx.cuh"
+
+namespace mfa {
+
+constexpr int kRopeMaxDim = 512;
+constexpr int kRopeHeads = 4;        // heads a thread turns, all loaded before the first is used
+constexpr int kRopeMaxThreads = 512;
+
+struct RopeSide {
+  const void* in;
+  void* out;
+  long long in_stride, out_stride;
+  int heads;
+};
+
+struct RopeParams {
+  RopeSide q, k;
+  const mfa_rope_pair* table;
+  const int32_t* positions;
+  int rows, axes, pairs, head_dim;
+  int turned_units, units;   // a head's units: turned ones first, then (out of place) copied ones
+  int inverse;
+};
+
+// kVec elements, widened to fp32
+template <typename T, int kVec>
+struct RopeVec {
+  float v[kVec];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kVec == 8 && sizeof(T) == 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(p);
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(e[i] << 16);
+        v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+      }
+    } else if constexpr (kVec == 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = static_cast<float>(p[i]);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kVec == 8 && sizeof(T) == 2) {
+      uint32_t e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        e[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
+    } else if constexpr (kVec == 8) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) p[i] = static_cast<T>(v[i]);
+    }
+  }
+};
+
+// kVec = 8: a unit is 8 elements of the first half and the 8 of the second that pair with them
+// (half pairing), or 8 elements of 4 adjacent pairs; kVec = 1: one pair.  threadIdx.x is the
+// unit, threadIdx.y and blockIdx.y the heads, blockIdx.x the row.
+template <typename T, int kVec, bool kHalf>
+__global__ void __launch_bounds__(kRopeMaxThreads) mfa_rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr bool kTwo = kHalf || kVec == 1;            // a unit is two vectors, else one
+  constexpr int kPairs = kTwo ? kVec : kVec / 2;       // pairs of a unit
+  __shared__ __align__(16) float cs[2][kRopeMaxDim / 2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int u = threadIdx.x;
+  const bool turned = u < p.turned_units;
+  const long long row = blockIdx.x;
+  // offset of the unit's first and second vector in its head
+  int a0, b0;
+  if (turned) {
+    a0 = kHalf ? kVec * u : (kVec == 1 ? 2 * u : kVec * u);
+    b0 = kHalf ? a0 + p.pairs : a0 + 1;
+  } else {
+    a0 = 2 * p.pairs + (u - p.turned_units) * kVec;
+    b0 = a0;
+  }
+  RopeVec<T, kVec> a[kRopeHeads], b[kRopeHeads];
+  const int heads = p.q.heads + p.k.heads;
+  const int h0 = blockIdx.y * (blockDim.y * kRopeHeads) + threadIdx.y;
+#pragma unroll
+  for (int i = 0; i < kRopeHeads; ++i) {
+    const int h = h0 + i * blockDim.y;
+    if (h < heads) {
+      const bool is_q = h < p.q.heads;
+      const T* src = static_cast<const T*>(is_q ? p.q.in : p.k.in) + row * (is_q ? p.q.in_stride : p.k.in_stride) +
+                     static_cast<long long>(is_q ? h : h - p.q.heads) * p.head_dim;
+      a[i].load(src + a0);
+      if (kTwo && turned) b[i].load(src + b0);
+    }
+  }
+  {
+    int32_t pos[MFA_ROPE_MAX_AXES];
+#pragma unroll
+    for (int x = 0; x < MFA_ROPE_MAX_AXES; ++x)
+      pos[x] = x < p.axes ? p.positions[static_cast<long long>(x) * p.rows + row] : 0;
+    for (int i = threadIdx.y * blockDim.x + u; i < p.pairs; i += blockDim.x * blockDim.y) {
+      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(p.table + i);
+      const int axis = static_cast<int>(e.y & 3u);
+      const int32_t at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+      const uint64_t turn = e.x * static_cast<uint64_t>(static_cast<int64_t>(at));
+      // the top 32 bits as a signed fraction in [-1/2, 1/2) turns; 2^-31 of it is half turns
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+      float s, c;
+      sincospif(half_turns, &s, &c);
+      cs[0][i] = c;
+      cs[1][i] = p.inverse ? -s : s;
+    }
+  }
+  __syncthreads();
+  float c[kPairs], s[kPairs];
+  if (turned) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      c[i] = cs[0][kPairs * u + i];
+      s[i] = cs[1][kPairs * u + i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRopeHeads; ++i) {
+    const int h = h0 + i * blockDim.y;
+    if (h >= heads) continue;
+    const bool is_q = h < p.q.heads;
+    T* dst = static_cast<T*>(is_q ? p.q.out : p.k.out) + row * (is_q ? p.q.out_stride : p.k.out_stride) +
+             static_cast<long long>(is_q ? h : h - p.q.heads) * p.head_dim;
+    if (!turned) {
+      a[i].store(dst + a0);
+      continue;
+    }
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float x = a[i].v[j], y = b[i].v[j];
+        a[i].v[j] = x * c[j] - y * s[j];
+        b[i].v[j] = y * c[j] + x * s[j];
+      }
+      a[i].store(dst + a0);
+      b[i].store(dst + b0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const float x = a[i].v[2 * j], y = a[i].v[2 * j + 1];
+        a[i].v[2 * j] = x * c[j] - y * s[j];
+        a[i].v[2 * j + 1] = y * c[j] + x * s[j];
+      }
+      a[i].store(dst + a0);
+    }
+  }
+}
+
+static mfa_status check_rope(const mfa_rope_config* c) {
+  if (c == nullptr) return MFA_ERR_INVALID_ARG;
+  if (c->head_dim < 1 || c->rotary_dim < 2 || (c->rotary_dim & 1) || c->rotary_dim > c->head_dim)
+    return MFA_ERR_INVALID_ARG;
+  if (c->head_dim > kRopeMaxDim) return MFA_ERR_UNSUPPORTED;
+  if (c->num_axes < 1 || c->num_axes > MFA_ROPE_MAX_AXES) return MFA_ERR_INVALID_ARG;
+  long long sum = 0;
+  for (int i = 0; i < MFA_ROPE_MAX_AXES; ++i) {
+    if (c->sections[i] < 0 || (i >= c->num_axes && c->sections[i] != 0)) return MFA_ERR_INVALID_ARG;
+    sum += c->sections[i];
+  }
+  if (2 * sum != c->rotary_dim) return MFA_ERR_INVALID_ARG;
+  if (c->pairing != MFA_ROPE_HALF && c->pairing != MFA_ROPE_ADJACENT) return MFA_ERR_INVALID_ARG;
+  if (c->flags & ~(MFA_ROPE_INTERLEAVED | MFA_ROPE_OWN_SPECTRUM)) return MFA_ERR_INVALID_ARG;
+  if (!(std::isfinite(c->theta) && c->theta >= 1.0)) return MFA_ERR_INVALID_ARG;
+  if (!(std::isfinite(c->position_scale) && c->position_scale > 0.0 && c->position_scale <= 16.0))
+    return MFA_ERR_INVALID_ARG;
+  return MFA_OK;
+}
+
+static mfa_status check_side(const mfa_rope_rows* s, const mfa_rope_config* c, int rows, int esz) {
+  if (s == nullptr || s->heads == 0) return MFA_OK;
+  if (s->heads < 0 || s->heads > INT_MAX / 4 / kRopeMaxDim) return MFA_ERR_INVALID_ARG;
+  if (rows == 0) return MFA_OK;
+  if (s->in == nullptr || s->out == nullptr || !aligned(s->in, esz) || !aligned(s->out, esz)) return MFA_ERR_INVALID_ARG;
+  const int64_t least = static_cast<int64_t>(s->heads) * c->head_dim;
+  constexpr int64_t kMost = int64_t{1} << 40;   // rows * stride * size stays far inside 64 bits
+  if (s->in_stride < least || s->out_stride < least || s->in_stride > kMost || s->out_stride > kMost)
+    return MFA_ERR_INVALID_ARG;
+  // in place means the same rows; anything between would be read after it is written
+  if (s->in == s->out) return s->in_stride == s->out_stride ? MFA_OK : MFA_ERR_INVALID_ARG;
+  const uintptr_t i0 = reinterpret_cast<uintptr_t>(s->in), o0 = reinterpret_cast<uintptr_t>(s->out);
+  const uintptr_t i1 = i0 + ((rows - 1) * s->in_stride + least) * esz, o1 = o0 + ((rows - 1) * s->out_stride + least) * esz;
+  if (i0 < o1 && o0 < i1) {
+    // overlapping ranges are fine only as columns of one wider row (q and k of one projection):
+    // equal strides, and the two column ranges apart
+    if (s->in_stride != s->out_stride) return MFA_ERR_INVALID_ARG;
+    const uintptr_t stride = static_cast<uintptr_t>(s->in_stride) * esz, len = static_cast<uintptr_t>(least) * esz;
+    const uintptr_t apart = (o0 > i0 ? o0 - i0 : stride - (i0 - o0) % stride) % stride;
+    if (apart < len || stride - apart < len) return MFA_ERR_INVALID_ARG;
+  }
+  return MFA_OK;
+}
+
+// The wide path needs 16-byte aligned vectors of 8 elements everywhere.
+static bool wide_side(const mfa_rope_rows* s) {
+  return s == nullptr || s->heads == 0 ||
+         (aligned(s->in, 16) && aligned(s->out, 16) && s->in_stride % 8 == 0 && s->out_stride % 8 == 0);
+}
+
+static RopeSide side_of(const mfa_rope_rows* s) {
+  RopeSide r = {};
+  if (s != nullptr && s->heads > 0) r = {s->in, s->out, s->in_stride, s->out_stride, s->heads};
+  return r;
+}
+
+template <typename T>
+static void (*rope_kernel(bool wide, bool half))(RopeParams) {
+  if (wide) return half ? mfa_rope_kernel<T, 8, true> : mfa_rope_kernel<T, 8, false>;
+  return half ? mfa_rope_kernel<T, 1, true> : mfa_rope_kernel<T, 1, false>;
+}
+
+}  // namespace mfa
+
+using namespace mfa;
+
+extern "C" mfa_status mfa_rope_table(const mfa_rope_config* c, mfa_rope_pair* table) {
+  const mfa_status st = check_rope(c);
+  if (st != MFA_OK) return st;
+  if (table == nullptr) return MFA_ERR_INVALID_ARG;
+  const int pairs = c->rotary_dim / 2;
+  int used[MFA_ROPE_MAX_AXES] = {0, 0, 0, 0};
+  int axis = 0;
+  for (int i = 0; i < pairs; ++i) {
+    // the next pair's axis: the current run's, or the next in turn, skipping those that are full
+    while (used[axis] == c->sections[axis]) axis = (axis + 1) % c->num_axes;
+    const double power = (c->flags & MFA_ROPE_OWN_SPECTRUM)
+                             ? static_cast<double>(used[axis]) / c->sections[axis]
+                             : 2.0 * i / c->rotary_dim;
+    const double turns = std::pow(c->theta, -power) * c->position_scale * 0.15915494309189535;   // 1 / (2 pi)
+    const double part = turns - std::floor(turns);
+    // 2^64 * part, exact up to the double's own rounding; part < 1, and 2^64 itself is one turn
+    const double scaled = std::ldexp(part, 64);
+    table[i].turns = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+    table[i].axis = axis;
+    table[i].reserved = 0;
+    ++used[axis];
+    if (c->flags & MFA_ROPE_INTERLEAVED) axis = (axis + 1) % c->num_axes;
+  }
+  return MFA_OK;
+}
+
+extern "C" mfa_status mfa_rope_run(const mfa_rope_config* c, const mfa_rope_pair* table, const int32_t* positions,
+                                   int32_t num_rows, int32_t dtype, int32_t inverse, const mfa_rope_rows* q,
+                                   const mfa_rope_rows* k, void* stream_ptr) {
+  mfa_status st = check_rope(c);
+  if (st != MFA_OK) return st;
+  if (num_rows < 0 || (dtype != MFA_OUT_BF16 && dtype != MFA_OUT_FP32) || (inverse != 0 && inverse != 1))
+    return MFA_ERR_INVALID_ARG;
+  const int esz = dtype == MFA_OUT_BF16 ? 2 : 4;
+  if ((st = check_side(q, c, num_rows, esz)) != MFA_OK || (st = check_side(k, c, num_rows, esz)) != MFA_OK) return st;
+  RopeParams p = {};
+  p.q = side_of(q);
+  p.k = side_of(k);
+  const long long heads = static_cast<long long>(p.q.heads) + p.k.heads;
+  if (num_rows == 0 || heads == 0) return MFA_OK;
+  if (table == nullptr || positions == nullptr || !aligned(table, 16) || !aligned(positions, 4)) return MFA_ERR_INVALID_ARG;
+  const bool half = c->pairing == MFA_ROPE_HALF;
+  const bool wide = c->head_dim % 8 == 0 && c->rotary_dim % (half ? 16 : 8) == 0 && wide_side(q) && wide_side(k);
+  const int vec = wide ? 8 : 1;
+  p.table = table;
+  p.positions = positions;
+  p.rows = num_rows;
+  p.axes = c->num_axes;
+  p.pairs = c->rotary_dim / 2;
+  p.head_dim = c->head_dim;
+  p.turned_units = (half || !wide) ? p.pairs / vec : c->rotary_dim / vec;
+  const bool in_place = (p.q.heads == 0 || p.q.in == p.q.out) && (p.k.heads == 0 || p.k.in == p.k.out);
+  p.units = p.turned_units + (in_place ? 0 : (c->head_dim - c->rotary_dim) / vec);
+  p.inverse = inverse;
+  // threads: a head's units by as many heads as a CTA can take, each thread kRopeHeads of them
+  const int most = std::max(1, kRopeMaxThreads / p.units);
+  const int ny = static_cast<int>(std::min<long long>(most, (heads + kRopeHeads - 1) / kRopeHeads));
+  const long long gy = (heads + static_cast<long long>(ny) * kRopeHeads - 1) / (static_cast<long long>(ny) * kRopeHeads);
+  if (gy > 65535) return MFA_ERR_INVALID_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_rows), static_cast<unsigned>(gy), 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(p.units), static_cast<unsigned>(ny), 1);
+  cfg.stream = static_cast<cudaStream_t>(stream_ptr);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, dtype == MFA_OUT_BF16 ? rope_kernel<__nv_bfloat16>(wide, half)
+                                                                       : rope_kernel<float>(wide, half), p);
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return MFA_OK;
+}

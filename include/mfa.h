@@ -373,6 +373,171 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
                                  void* out, float* lse, void* workspace, uint64_t workspace_bytes,
                                  void* stream);
 
+/*
+ * ------------------------------------------------------------------ block-scaled 8-bit cache
+ *
+ * A paged cache of OCP e4m3 codes with one fp32 scale for each block of tokens and key/value
+ * head, for keys and for values: 8-bit KV (Step-3 page section 5 "Model-System Co-design")
+ * whose scales cost next to nothing.  A page holds each head's 64 rows one after the other:
+ *   k_cache, v_cache : uint8 [num_blocks, G, 64, d], the e4m3 codes;
+ *   k_scale, v_scale : fp32 [num_blocks, G, 64 / scale_tokens], positive and finite;
+ * the value of element i of token t, head g, is e4m3(code) * scale, with page
+ * block_table[b][t / 64], slot s = t % 64 and scale s / scale_tokens of that page and head.
+ * The calls take an mfa_problem with kv_dtype MFA_KV_FP8_E4M3 and these shapes:
+ *   head_dim d    : 128 or 256;
+ *   num_kv_heads  : G >= 1, a divisor of num_q_heads, with at most 64 query heads for each;
+ *                   query head h reads key/value head h / (num_q_heads / G);
+ *   kv_shared     : 0;   tokens_per_seq : T in 1..4;   page_size : 64;
+ *   scale_tokens  : 16, 32 or 64 tokens a scale (an argument of each call).
+ * Anything else is MFA_ERR_UNSUPPORTED (MFA_ERR_INVALID_ARG where no meaning could be given).
+ * The conventions at the top of this file hold.
+ */
+
+/*
+ * Choose the split of the decode's work, as mfa_decode_plan does for the other caches (same
+ * arguments; MFA_PLAN_NO_COMBINE is refused).  The plan is for mfa_block_decode_run alone.
+ * plan->max_tiles_per_cta is the most 128-token tiles that a CTA can get and is not limited.
+ */
+mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
+                                 const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
+                                 int32_t force_ctas, uint32_t flags, mfa_plan* plan);
+
+/*
+ * Enqueue one decode step over a block-scaled cache: the operation of mfa_decode_run (several
+ * new tokens a sequence and empty sequences included), for the shapes above.
+ *   q            : device bf16 [B, T, num_q_heads, d], 16-byte aligned.  A row (one token and
+ *                  head) with an infinity or NaN gives unspecified results in its own row only.
+ *   k_cache, v_cache : the pools, 16-byte aligned.   k_scale, v_scale : 16-byte aligned.
+ *   block_table  : device int32 [B, max_pages_per_seq]; entries past ceil(L_b/64) are not read.
+ *   seq_lens     : device int32 [B].
+ *   out          : device [B, T, num_q_heads, d], 16-byte aligned, bf16 or fp32 (out_dtype).
+ *   lse          : device fp32 [B, T, num_q_heads], or NULL.
+ *   workspace    : device, >= plan->workspace_bytes, 256-byte aligned; the status word at offset
+ *                  0 is that of mfa_read_device_status.  Two calls that may overlap on the GPU
+ *                  need a workspace each.
+ * Slots past a sequence's length, the scales of blocks without a token and unused pages may
+ * hold any bits.  A block id outside the pool reads as a page of zeros and sets
+ * MFA_DEV_BAD_BLOCK; a length outside [0, max_pages*64] is clamped and sets MFA_DEV_BAD_LENGTH;
+ * lengths that need more of a CTA than the plan allows leave outputs unwritten and set
+ * MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
+ */
+mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_problem* problem, int32_t scale_tokens,
+                                const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Enqueue the append of new key and value rows to a block-scaled cache: one row a sequence (a
+ * decode step), a few (several new tokens) or many (a prompt or its next chunk).  Sequence b's
+ * rows are n_b consecutive rows of k_new and v_new; row i goes to token positions[b] + i.
+ * For each block of scale_tokens tokens and each head that gets rows, with a the largest
+ * finite |x| among its new rows and head:
+ *   need  = the smallest power of two 2^e with a <= 448 * 2^e, e >= -126 (2^-126 for a = 0);
+ *   scale = need if the block holds no token before positions[b], else max(its scale, need);
+ *   each new x is stored as the e4m3 code of x / scale (rounded to nearest even);
+ *   where the block's scale rose from s to s', each of its older codes c is stored again as
+ *   the e4m3 code of e4m3(c) * (s / s'), both fp32.  With power-of-two scales that loses
+ *   nothing but what falls below e4m3's smallest step under the new scale.
+ * Powers of two cost no precision (e4m3 has a floating point of its own) and let a block's
+ * scale rise without rounding its older rows twice.  An infinity is stored as +-448 * scale, a
+ * NaN as e4m3 NaN; neither moves the scale.  Slots past the new rows keep their bits.
+ *   problem      : batch, G, d, table width and pool size are used.
+ *   k_new, v_new : device bf16 [num_new, G, d], 16-byte aligned.
+ *   num_new      : rows in k_new and in v_new.
+ *   new_offsets  : device int32 [B + 1]: sequence b's rows are new_offsets[b] ..
+ *                  new_offsets[b+1] - 1; or NULL: T rows each, num_new = B * T.
+ *   max_new      : a bound of n_b, > 0 where num_new > 0 (NULL offsets: ignored, T).
+ *   positions    : device int32 [B]; a negative entry: no new rows for that sequence.
+ *   block_table  : device int32 [B, max_pages_per_seq]; must hold the pages of the new rows.
+ *                  A page that gets rows belongs to one sequence alone.
+ *   k_cache .. v_scale : the pools, 16-byte aligned, written in place.
+ *   device_status: device uint32, or NULL.  Rows at or past max_pages*64, rows past max_new and
+ *                  offsets outside [0, num_new] are not written and set MFA_DEV_BAD_LENGTH; a
+ *                  page id outside the pool sets MFA_DEV_BAD_BLOCK and its rows are not written.
+ */
+mfa_status mfa_block_kv_append(const mfa_problem* problem, int32_t scale_tokens,
+                               const void* k_new, const void* v_new, int32_t num_new,
+                               const int32_t* new_offsets, int32_t max_new,
+                               const int32_t* positions, const int32_t* block_table,
+                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                               uint32_t* device_status, void* stream);
+
+/*
+ * ------------------------------------------------------------------ rotary positions
+ *
+ * Rotary positions with one to four axes (text: one; images and video: time, height, width),
+ * for query heads and new key rows before the append.  The first rotary_dim elements of a head
+ * are rotary_dim / 2 pairs; pair i turns by the angle position[axis(i)] * frequency(i):
+ *     a' = a cos - b sin,   b' = b cos + a sin.
+ * Elements past rotary_dim pass through.
+ */
+typedef enum mfa_rope_pairing {
+    MFA_ROPE_HALF = 0,         /* pair i: elements i and i + rotary_dim / 2 */
+    MFA_ROPE_ADJACENT = 1      /* pair i: elements 2 i and 2 i + 1 */
+} mfa_rope_pairing;
+
+#define MFA_ROPE_MAX_AXES 4
+/* Config flags. */
+#define MFA_ROPE_INTERLEAVED 0x1u   /* axes dealt to the pairs in turn (an axis that has all its
+                                       pairs drops out), instead of one run of pairs each */
+#define MFA_ROPE_OWN_SPECTRUM 0x2u  /* each axis has frequencies of its own: theta^(-j / n) for the
+                                       j-th of its n pairs, instead of theta^(-2 i / rotary_dim)
+                                       by the pair's index i */
+
+typedef struct mfa_rope_config {
+    int32_t head_dim;          /* 1..512 */
+    int32_t rotary_dim;        /* even, 2..head_dim: twice the sum of the sections */
+    int32_t num_axes;          /* 1..MFA_ROPE_MAX_AXES */
+    int32_t sections[MFA_ROPE_MAX_AXES];   /* pairs of each axis, >= 0; 0 past num_axes */
+    int32_t pairing;           /* mfa_rope_pairing */
+    uint32_t flags;            /* MFA_ROPE_* */
+    double theta;              /* base, finite, >= 1 */
+    double position_scale;     /* positions are multiplied by it: 1, or less to stretch the
+                                  range a model was trained on; finite, > 0, at most 16 */
+} mfa_rope_config;
+
+/* One pair's row of the table that mfa_rope_run reads. */
+typedef struct mfa_rope_pair {
+    uint64_t turns;            /* turns per position, in units of 2^-64, modulo 1 */
+    int32_t axis;
+    int32_t reserved;          /* 0 */
+} mfa_rope_pair;
+
+/*
+ * Fill `table` (host, rotary_dim / 2 entries).  Host only.  The caller copies it to the device
+ * once and keeps it.  Angles are 64-bit fractions of a turn, so that a position of any size has
+ * the angle of its exact product with the frequency (fp32 products are off by 0.01 rad at
+ * position 131072).
+ */
+mfa_status mfa_rope_table(const mfa_rope_config* config, mfa_rope_pair* table);
+
+/* The rows that mfa_rope_run turns: `heads` heads of head_dim elements, one after the other,
+ * in each of the call's rows; strides in elements from one row to the next. */
+typedef struct mfa_rope_rows {
+    const void* in;            /* aligned to the element; NULL with heads = 0 */
+    void* out;                 /* = in (with the same stride) to turn in place, or no overlap */
+    int64_t in_stride;         /* >= heads * head_dim */
+    int64_t out_stride;
+    int32_t heads;             /* >= 0 */
+} mfa_rope_rows;
+
+/*
+ * Enqueue the rotation of num_rows rows of q and of k (one launch).
+ *   table     : device, as filled by mfa_rope_table for `config`, 16-byte aligned.
+ *   positions : device int32 [num_axes, num_rows]; any values, negative ones included.
+ *   dtype     : MFA_OUT_BF16 or MFA_OUT_FP32, of q and k, in and out (fp32 arithmetic, one
+ *               rounding).
+ *   inverse   : 1 turns by the negative angles: the gradient of the call with 0, or its undoing.
+ *   q, k      : the rows; either may be NULL or have no heads.  All-16-byte-aligned rows with
+ *               head_dim and the pairs in multiples of 8 elements take the wide path, all
+ *               others one pair at a time.  q's rows and k's must not overlap.
+ */
+mfa_status mfa_rope_run(const mfa_rope_config* config, const mfa_rope_pair* table,
+                        const int32_t* positions, int32_t num_rows, int32_t dtype, int32_t inverse,
+                        const mfa_rope_rows* q, const mfa_rope_rows* k, void* stream);
+
 /* MFA_ABI_VERSION of the loaded library. */
 int32_t mfa_abi_version(void);
 
