@@ -5,11 +5,14 @@
 //     s_t = softmax_scale * sk_t * dot(q, k_t),  out = sum_t e^(s_t) sv_t v_t / sum_t e^(s_t),
 //     lse = ln sum_t e^(s_t),
 // k_t and v_t being the e4m3 codes' values and sk_t, sv_t their blocks' scales.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cstring>
@@ -18,6 +21,7 @@
 #include "mfa.h"
 #include "mfa_host.h"
 #include "ptx.cuh"
+#include "mfa_device.cuh"
 
 namespace mfa {
 
@@ -28,6 +32,18 @@ constexpr int kBCostTile = 4;         // schedule: cost of a tile
 constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's range
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
+constexpr int kBThreads = 320;        // producer warp, MMA warp, eight softmax warps
+constexpr int kBSoftmaxWarps = 8;
+constexpr int kBCombineThreads = 256;
+constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
+constexpr int kBMisc = 8192;          // of it, behind the ring: segments, scratch, barriers (the last 256)
+// A row's reference maximum moves when a score passes it by more than 2^3.  A value scale s_v
+// is folded into its token's weights as s_v 2^(4 - E), E the segment's reference exponent
+// (s_v < 2^(E + 1) for all so far), so that weights stay below 2^3 * 2 * 2^4 = 256, inside
+// e4m3's 448, and ordinary ones lie near 1, where both e4m3 parts are normal numbers.
+constexpr float kBThreshold = 3.0f;
+constexpr int kBPvShift = 4;
+constexpr int kBEMin = -120;          // floor of E (2^(kBPvShift - E) stays a normal fp32 number)
 
 // The work of one problem: a unit is (sequence, key/value head, group of new tokens); its rows
 // are the group's new tokens x the query heads that read that head.
@@ -57,110 +73,884 @@ static uint64_t block_workspace_bytes(long long partials, int rows, int d) {
   return (block_lse_offset(partials, rows, d) + static_cast<uint64_t>(partials) * rows * 4 + 255) / 256 * 256;
 }
 
+// Shared memory and tensor memory of an instance: kDim the head width, kNR the unit's rows
+// padded to 16, 32 or 64 (the MMAs' N).
+template <int kDim, int kNR>
+struct BlockLayout {
+  static constexpr int kHalves = kDim / 128;            // 128-byte swizzle rows of a cache row
+  static constexpr int kC = kNR / 2;                    // rows a softmax warpgroup owns
+  static constexpr int kBoxes = 2 * kHalves;            // TMA boxes [64 tokens x 128 B] of a tile of K or V
+  static constexpr int kGroupBytes = kBoxes * 8192;     // a ring slot: one tile of K or of V
+  static constexpr int kPBufs = (kDim == 256 && kNR == 64) ? 1 : 2;
+  static constexpr int kOffQ = 0;                       // q: kHalves boxes of [kNR hi rows, kNR lo rows][128 B]
+  static constexpr int kOffP = 2 * kNR * kDim;          // weights: [128 tokens][kNR hi, kNR lo], 128-byte rows
+  static constexpr int kOffRing = kOffP + kPBufs * 16384;
+  static constexpr int kGroups = (kBSmem - kBMisc - kOffRing) / kGroupBytes;
+  static constexpr int kOffMisc = kOffRing + kGroups * kGroupBytes;
+  static constexpr uint32_t kTmemS = 0;                 // S^T, two buffers of kNR columns
+  static constexpr uint32_t kTmemO = 2 * kNR;           // O^T, for each half kNR hi and kNR lo columns
+  static constexpr uint32_t kTmemUsed = 2 * kNR * (1 + kHalves);
+  static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512 && kGroups >= 4 && kOffP % 1024 == 0 && kOffRing % 1024 == 0, "layout");
+};
+
 struct BlockDecodeParams {
+  CUtensorMap tm_k, tm_v;    // codes [pages * heads][64][d], boxes of one page and head, 128 bytes wide
   const __nv_bfloat16* q;
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
   const float* k_scale;
   const float* v_scale;
   const int32_t* block_table;
   const int32_t* seq_lens;
   void* out;
   float* lse;
+  float* part_o;             // [partials][rows][d]
+  float* part_lse;           // [partials][rows]
   unsigned int* status;
   int batch, tokens, heads, kv_heads;
-  int log_scale;       // log2(scale_tokens)
+  int group, unit_tokens, token_groups, readers, rows;   // BlockShape
+  int log_scale;             // log2(scale_tokens)
   int max_pages, num_blocks;
-  float scale_log2;    // softmax_scale * log2(e)
+  float scale_log2;          // softmax_scale * log2(e)
   int out_f32;
+  int early_metadata;
 };
 
-// One CTA per (sequence, new token, query head); each warp walks every eighth token with a
-// running maximum and sum, and the eight states are merged at the end.
-template <int kDim>
-__global__ void __launch_bounds__(256) mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
-  constexpr int kPer = kDim / 32;
-  __shared__ float sm[8], sl[8], so[8][kDim];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int x = blockIdx.x, h = blockIdx.y, b = x / p.tokens, i = x % p.tokens;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = h / (p.heads / p.kv_heads);
-  int L = p.seq_lens[b];
-  if (L < 0 || L > p.max_pages * kBPage) {
-    if (threadIdx.x == 0) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
-    L = min(max(L, 0), p.max_pages * kBPage);
+// ------------------------------------------------------------------ schedule
+//
+// The units of the batch lie end to end, reader-major (reader r = head * token groups + token
+// group; unit (b, r) at position r B + b): tile k of a unit sits at cost 4 k past the unit's
+// base, and the next unit's base is 4 T + c further (T tiles, c = kBCostUnit for the boundary;
+// nothing for an empty sequence).  CTA g of G owns the tiles whose cost lies in
+// [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.
+struct BlockCost {
+  long long per_reader;   // cost of one reader of every sequence
+  long long total;        // C
+};
+__device__ __forceinline__ BlockCost block_cost(long long packed, int readers) {
+  const long long tiles = packed & 0xFFFFFFFFFll, n = packed >> 36;
+  BlockCost c;
+  c.per_reader = kBCostTile * tiles + kBCostUnit * n;
+  c.total = n > 0 ? c.per_reader * readers - kBCostUnit : 0;
+  return c;
+}
+// tiles in the low 36 bits, non-empty sequences above
+__device__ __forceinline__ long long pack_tiles(int tiles) {
+  return static_cast<long long>(tiles) | (static_cast<long long>(tiles > 0) << 36);
+}
+__device__ __forceinline__ long long cost_before(long long packed) {
+  return kBCostTile * (packed & 0xFFFFFFFFFll) + kBCostUnit * (packed >> 36);
+}
+// first of a unit's T tiles at cost >= X
+__device__ __forceinline__ int first_tile_at(long long X, long long base, int T) {
+  return X <= base ? 0 : static_cast<int>(min(static_cast<long long>(T), (X - base + kBCostTile - 1) / kBCostTile));
+}
+__device__ __forceinline__ int block_tiles(int L) { return (L + kBTile - 1) / kBTile; }
+
+// Reduce kC per-thread values over the 32 lanes: halving exchanges while values are left,
+// then whole exchanges of the last one.  Lane l ends with column l / (32 / kC).
+template <int kC, bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
+  const int lane = threadIdx.x & 31;
+  auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+  int step = 16;
+#pragma unroll
+  for (int n = kC / 2; n >= 1; n /= 2, step /= 2) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool hi = lane & step;
+      const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, step));
+    }
   }
-  const int n = max(0, L - (p.tokens - 1) + i);
-  const size_t row = static_cast<size_t>(x) * p.heads + h;
-  float q[kPer], acc[kPer];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    q[e] = __bfloat162float(p.q[row * kDim + lane * kPer + e]);
-    acc[e] = 0.f;
+  for (; step >= 1; step /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], step));
+  return v[0];
+}
+
+// A role's place in its CTA's run of tiles.
+struct BlockTile {
+  int s, j, end;      // segment, tile of the sequence, end of the segment
+  int b, r, L;        // sequence, reader, length
+  __device__ __forceinline__ void load(const int4* seg, const int* seg_len, int at) {
+    const int4 x = seg[at];
+    s = at;
+    b = x.x;
+    r = x.y;
+    j = x.z;
+    end = x.w;
+    L = seg_len[at];
   }
-  float m = -INFINITY, l = 0.f;
-  auto load = [&](const uint8_t* base, float (&v)[kPer]) {
-#pragma unroll
-    for (int e = 0; e < kPer; e += 4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + lane * kPer + e);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t f;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(static_cast<uint16_t>(w >> (16 * k))));
-        const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
-        v[e + 2 * k] = __low2float(f2);
-        v[e + 2 * k + 1] = __high2float(f2);
+  // the next tile; false past the last
+  __device__ __forceinline__ bool next(const int4* seg, const int* seg_len, int nseg) {
+    if (++j < end) return true;
+    if (s + 1 >= nseg) return false;
+    load(seg, seg_len, s + 1);
+    return true;
+  }
+  __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
+};
+
+// ------------------------------------------------------------------ decode kernel
+template <int kDim, int kNR>
+__global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+  using Lay = BlockLayout<kDim, kNR>;
+  constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes, kGroups = Lay::kGroups;
+  constexpr int kPBufs = Lay::kPBufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint8_t* misc = smem + Lay::kOffMisc;
+  int4* seg = reinterpret_cast<int4*>(misc);                         // {sequence, reader, first tile, end tile}
+  int* seg_len = reinterpret_cast<int*>(misc + 16 * kBMaxSeg);
+  float* red = reinterpret_cast<float*>(misc + 20 * kBMaxSeg);       // [2 warpgroups][4 quarters][32]
+  int* red_e = reinterpret_cast<int*>(red + 256);                    // [2][4]
+  float* q_inv = reinterpret_cast<float*>(red_e + 8);                // [2 segments][64] what undoes a row's q scaling
+  int* row_off = reinterpret_cast<int*>(q_inv + 128);                // [64] element offset of a row's output
+  int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
+  long long* scan = reinterpret_cast<long long*>(row_tok + 64);      // [16]
+  int* iscan = reinterpret_cast<int*>(scan + 16);                    // [16]
+  int* ctl = iscan + 16;                                             // tensor memory, abort flag, tiles of this CTA
+  volatile int* abort_flag = ctl + 1;
+  const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 256;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  constexpr int kFull = 0, kEmpty = kGroups, kSFull = 2 * kGroups, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                kQReady = kPvDone + 2, kQEmpty = kQReady + 1, kOEmpty = kQEmpty + 1, kDrain = kOEmpty + 1,
+                kBars = kDrain + 1;
+  static_assert(kBars * 8 <= 256, "barrier area");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == 0) {
+    for (int i = lane; i < kBars; i += 32) {
+      // arrivals a phase: one for each box of a slot; one for each softmax warp; else one commit
+      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty;
+      mbar_init(bar(i), i < kEmpty ? kBoxes : by_warps ? kBSoftmaxWarps : 1);
+    }
+    if (lane == 0) {
+      ctl[1] = 0;
+      ctl[2] = 0;
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(ctl), Lay::kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid >= 64 && tid < 64 + kNR) {
+    const int row = tid - 64, tok = row / p.group;
+    row_off[row] = (tok * p.heads + row % p.group) * kDim;
+    row_tok[row] = tok;
+  }
+  if (tid == 64) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  // nothing that the preceding kernel may write is read before this; with early metadata the
+  // lengths and the block table are (the caller says that it does not write them)
+  if (!p.early_metadata) grid_dep_wait();
+
+  // ---------------- this CTA's segments
+  const int cap = p.max_pages * kBPage;
+  int nseg = 0;
+  {
+    bool bad = false;
+    const int L0 = tid < p.batch ? clamp_len(p.seq_lens[tid], cap, bad) : 0;
+    long long mine = pack_tiles(block_tiles(L0));
+    for (int b = tid + kBThreads; b < p.batch; b += kBThreads)
+      mine += pack_tiles(block_tiles(clamp_len(p.seq_lens[b], cap, bad)));
+    if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
+    long long all = 0;
+    const long long incl = block_incl_scan<kBThreads, long long>(mine, scan, all);
+    const BlockCost cost = block_cost(all, p.readers);
+    const long long G = gridDim.x, g = blockIdx.x;
+    const long long X0 = g * cost.total / G, X1 = (g + 1) * cost.total / G;
+    if (X0 < X1) {
+      const int r0 = static_cast<int>(X0 / cost.per_reader), r1 = static_cast<int>((X1 - 1) / cost.per_reader);
+      for (int r = r0; r <= r1 && nseg <= kBMaxSeg; ++r) {
+        const long long rbase = r * cost.per_reader;
+        long long carry = 0;
+        for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kBThreads) {
+          const int b = c0 + tid;
+          bool again = false;
+          const int L = c0 == 0 ? L0 : (b < p.batch ? clamp_len(p.seq_lens[b], cap, again) : 0);
+          const int T = block_tiles(L);
+          const long long own = pack_tiles(T);
+          long long sum = all;
+          long long before = incl - own;
+          if (p.batch > kBThreads) before = block_incl_scan<kBThreads, long long>(own, scan, sum) - own + carry;
+          const long long base = rbase + cost_before(before);
+          const int lo = first_tile_at(X0, base, T), hi = first_tile_at(X1, base, T);
+          const int has = lo < hi ? 1 : 0;
+          int count = 0;
+          const int at = nseg + block_incl_scan<kBThreads>(has, iscan, count) - has;
+          if (has && at < kBMaxSeg) {
+            seg[at] = make_int4(b, r, lo, hi);
+            seg_len[at] = L;
+            atomicAdd(ctl + 2, hi - lo);
+          }
+          nseg += count;
+          carry += sum;
+        }
+      }
+      if (nseg > kBMaxSeg) {
+        if (tid == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
+        nseg = 0;
       }
     }
-  };
-  for (int t = warp; t < n; t += 8) {
-    const int blk = p.block_table[static_cast<size_t>(b) * p.max_pages + t / kBPage];
-    float kv[kPer], vv[kPer], sk = 0.f, sv = 0.f;
-    if (blk >= 0 && blk < p.num_blocks) {
-      const size_t ph = static_cast<size_t>(blk) * p.kv_heads + g;
-      load(p.k_cache + (ph * kBPage + t % kBPage) * kDim, kv);
-      load(p.v_cache + (ph * kBPage + t % kBPage) * kDim, vv);
-      const size_t si = (ph << (6 - p.log_scale)) + ((t % kBPage) >> p.log_scale);
-      sk = p.k_scale[si];
-      sv = p.v_scale[si];
-    } else {
-      if (lane == 0) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) kv[e] = vv[e] = 0.f;
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s += q[e] * kv[e];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.scale_log2 * sk;
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * al + w;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * al + w * sv * vv[e];
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = acc[e];
   __syncthreads();
-  float M = -INFINITY, S = 0.f;
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < 8; ++w) S += sm[w] == -INFINITY ? 0.f : sl[w] * exp2f(sm[w] - M);
-  for (int d = threadIdx.x; d < kDim; d += 256) {
-    float o = 0.f;
-    for (int w = 0; w < 8; ++w) o += sm[w] == -INFINITY ? 0.f : so[w][d] * exp2f(sm[w] - M);
-    o = n > 0 ? o / S : 0.f;
-    if (p.out_f32)
-      static_cast<float*>(p.out)[row * kDim + d] = o;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[row * kDim + d] = __float2bfloat16_rn(o);
+  if (p.early_metadata) grid_dep_wait();
+  grid_dep_launch();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
+  const int ntiles = nseg > 0 ? ctl[2] : 0;
+  // ring order of the tiles of K and V: K(0), K(1), V(0), K(2), V(1), ..., V(N - 1)
+  auto k_use = [&](int n) { return n == 0 ? 0 : 2 * n - 1; };
+  auto v_use = [&](int n) { return n == ntiles - 1 ? 2 * n + 1 : 2 * n + 2; };
+
+  if (warp == 0) {
+    // ---------------- producer: lane i < kBoxes loads box i of each tile (half i / 2, page i % 2)
+    if (lane < kBoxes && ntiles > 0) {
+      const int half = lane >> 1, pg = lane & 1;
+      const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
+      BlockTile it;
+      it.load(seg, seg_len, 0);
+      auto page_id = [&](const BlockTile& t) -> int {
+        return t.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(t.b) * p.max_pages + 2 * t.j + pg] : 0;
+      };
+      int id = page_id(it);
+      int z[2] = {0, 0}, rows[2] = {0, 0};   // (page, head) row of the pool and valid rows: this tile, the one before
+      bool keep[2] = {false, false};
+      bool ok = true;
+      int use = 0;
+      auto issue = [&](bool is_v, int w) {
+        const int slot = use % kGroups;
+        ok = wait_bar(bar(kEmpty + slot), ((use / kGroups) & 1) ^ 1, abort_flag);
+        if (!ok) return;
+        const uint32_t fb = bar(kFull + slot);
+        if (rows[w] <= 0) {
+          mbar_arrive(fb);
+        } else {
+          // the last page's rows land at the end of the box: rows before them are filled with zeros
+          mbar_arrive_expect_tx(fb, 8192);
+          tma_load_3d_hint(sbase + Lay::kOffRing + slot * Lay::kGroupBytes + (half * 2 + pg) * 8192,
+                           is_v ? &p.tm_v : &p.tm_k, fb, 128 * half, rows[w] - kBPage, z[w], keep[w] ? again : once);
+        }
+        ++use;
+      };
+      for (int n = 0; n <= ntiles && ok; ++n) {
+        if (n < ntiles) {
+          const int w = n & 1;
+          rows[w] = it.page_rows(pg);
+          z[w] = id * p.kv_heads + it.r / p.token_groups;
+          if (rows[w] > 0 && (id < 0 || id >= p.num_blocks)) {
+            z[w] = -1;   // outside the pool: the whole box reads as zeros
+            if (half == 0) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
+          }
+          keep[w] = it.r % p.token_groups != p.token_groups - 1;   // another unit reads the page next
+          issue(false, w);
+          if (it.next(seg, seg_len, nseg)) id = page_id(it);
+        }
+        if (n >= 1 && ok) issue(true, (n - 1) & 1);
+      }
+      if (!ok) {
+        atomicOr(p.status, MFA_DEV_TIMEOUT);
+        // let every copy already issued land before the CTA can exit
+        for (int u = max(0, use - kGroups); u < use; ++u)
+          wait_slow(bar(kFull + u % kGroups), (u / kGroups) & 1, nullptr, kDrainLimitNs);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: QK^T one tile ahead of PV
+    if (lane == 0 && ntiles > 0) {
+      constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, kNR);
+      constexpr uint32_t kIdescPV = idesc_e4m3(true, true, 128, 2 * kNR);
+      bool ok = true;
+      BlockTile tk, tv;
+      tk.load(seg, seg_len, 0);
+      tv.load(seg, seg_len, 0);
+      int k_first = tk.j, v_first = tv.j;   // first tile of the current segment
+      auto qk = [&](int n) {
+        const int use = k_use(n), slot = use % kGroups;
+        if (tk.j == k_first) ok = wait_bar(bar(kQReady), tk.s & 1, abort_flag);
+        if (ok) ok = wait_bar(bar(kFull + slot), (use / kGroups) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t d = tmem + Lay::kTmemS + kNR * (n & 1);
+        const uint32_t a0 = sbase + Lay::kOffRing + slot * Lay::kGroupBytes;
+        const uint32_t b0 = sbase + Lay::kOffQ;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ad = smem_desc(a0 + h * 16384 + 32 * kk, 16, 1024);
+            const uint32_t b = b0 + h * (2 * kNR * 128) + 32 * kk;
+            umma_f8_ss(d, ad, smem_desc(b, 16, 1024), kIdescQK, (h | kk) != 0);
+            umma_f8_ss(d, ad, smem_desc(b + kNR * 128, 16, 1024), kIdescQK, 1u);
+          }
+        umma_commit(bar(kEmpty + slot));
+        umma_commit(bar(kSFull + (n & 1)));
+        if (tk.j == tk.end - 1) umma_commit(bar(kQEmpty));
+        const int s = tk.s;
+        if (tk.next(seg, seg_len, nseg) && tk.s != s) k_first = tk.j;
+      };
+      auto pv = [&](int m) {
+        const int use = v_use(m), slot = use % kGroups;
+        const bool first = tv.j == v_first;
+        ok = wait_bar(bar(kPFull + m % kPBufs), (m / kPBufs) & 1, abort_flag);
+        if (ok && first && tv.s > 0) ok = wait_bar(bar(kOEmpty), (tv.s - 1) & 1, abort_flag);
+        if (ok) ok = wait_bar(bar(kFull + slot), (use / kGroups) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a0 = sbase + Lay::kOffRing + slot * Lay::kGroupBytes;
+        const uint32_t b0 = sbase + Lay::kOffP + (m % kPBufs) * 16384;
+        for (int pg = 0; pg < 2; ++pg) {
+          if (tv.page_rows(pg) <= 0) break;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              umma_f8_ss(tmem + Lay::kTmemO + 2 * kNR * h, smem_desc(a0 + (h * 2 + pg) * 8192 + 4096 * kk, 8192, 1024),
+                         smem_desc(b0 + pg * 8192 + 4096 * kk, 8192, 1024), kIdescPV, !(first && pg == 0 && kk == 0));
+        }
+        umma_commit(bar(kEmpty + slot));
+        umma_commit(bar(kPvDone + (m & 1)));
+        const int s = tv.s;
+        if (tv.next(seg, seg_len, nseg) && tv.s != s) v_first = tv.j;
+      };
+      for (int n = 0; n <= ntiles && ok; ++n) {
+        // a segment's first scores wait for its q, which is made after the last segment's
+        // weights: that segment's last PV goes first
+        const bool late = n >= 1 && n < ntiles && tk.j == k_first;
+        if (late) pv(n - 1);
+        if (ok && n < ntiles) qk(n);
+        if (ok && n >= 1 && !late) pv(n - 1);
+      }
+      if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
+      // every MMA must be complete before tensor memory is released
+      umma_commit(bar(kDrain));
+      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
+    }
+  } else {
+    // ---------------- softmax and epilogue: two warpgroups, each the whole tile (lane = token)
+    // for its kC rows
+    const int sw = warp - 2, wg = sw >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;          // token row of a tile; element of an O half
+    const int pg = row >> 6, ri = row & 63;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const int c0 = wg * kC;                       // this warpgroup's first row
+    float* my_red = red + wg * 128;               // [4 quarters][kC]
+    int* my_red_e = red_e + wg * 4;
+    const uint32_t vote_bar = 1 + wg;
+    const bool f32 = p.out_f32 != 0;
+
+    // sequences without tokens: zeros and -inf, in turn over the CTAs
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      bool dummy = false;
+      if (clamp_len(p.seq_lens[b], cap, dummy) != 0) continue;
+      const size_t n = static_cast<size_t>(p.tokens) * p.heads, at = static_cast<size_t>(b) * n;
+      const size_t chunks = n * kDim * (f32 ? 4 : 2) / 16;
+      uint4* o = static_cast<uint4*>(p.out) + at * kDim * (f32 ? 4 : 2) / 16;
+      for (size_t i = tid - 64; i < chunks; i += 32 * kBSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (size_t i = tid - 64; i < n; i += 32 * kBSoftmaxWarps) p.lse[at + i] = -INFINITY;
+    }
+
+    // A wait that gives up raises the CTA's abort flag; a warpgroup leaves its loops together,
+    // by a vote, so that its barriers stay in step.
+    bool aborted = false, stop = false;
+    // q of a segment, split into e4m3 hi + lo parts under one power of two a row (split_e4m3):
+    // 8 elements a lane, a row a warp (d = 256) or half a warp (d = 128)
+    auto convert_q = [&](int sidx) {
+      constexpr int kRowsAtOnce = 256 / kDim;
+      constexpr int kRounds = kNR / (kBSoftmaxWarps * kRowsAtOnce);
+      const int4 sg = seg[sidx];
+      const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
+      const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
+      const __nv_bfloat16* src =
+          p.q + ((static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group) * kDim;
+      const int e0 = (lane * 8) % kDim;            // first element of this lane
+      uint4 w[kRounds];
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int r = (i * kBSoftmaxWarps + sw) * kRowsAtOnce + lane * 8 / kDim;
+        w[i] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r] + e0)) : make_uint4(0, 0, 0, 0);
+      }
+      // (the previous segment's last scores are made: its q is read no more)
+      if (sidx > 0 && !aborted && !wait_warp(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int r = (i * kBSoftmaxWarps + sw) * kRowsAtOnce + lane * 8 / kDim;
+        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int o = kDim / 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        int sig = 0;   // the row's largest |q| goes to [64, 128)
+        if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          split_e4m3(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
+        const int byte = e0 % 128;
+        uint8_t* dst = smem + Lay::kOffQ + (e0 / 128) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        if (e0 == 0)
+          q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQReady));
+    };
+
+    // the scales of this thread's token: page ids two tiles ahead, scales one tile ahead
+    BlockTile ahead;
+    bool more = ntiles > 0;
+    auto page_of = [&](const BlockTile& t) -> int {
+      return t.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(t.b) * p.max_pages + 2 * t.j + pg] : -1;
+    };
+    auto load_scales = [&](const BlockTile& t, int id, float& sk, float& sv) {
+      const int pr = ri - (kBPage - t.page_rows(pg));   // page row of this box row
+      sk = sv = 0.f;
+      if (pr >= 0 && id >= 0 && id < p.num_blocks) {
+        const size_t at = ((static_cast<size_t>(id) * p.kv_heads + t.r / p.token_groups) << (6 - p.log_scale)) + (pr >> p.log_scale);
+        sk = __ldg(p.k_scale + at);
+        sv = __ldg(p.v_scale + at);
+      }
+    };
+    float sk_next = 0.f, sv_next = 0.f;
+    int id_next = -1;
+    if (more) {
+      ahead.load(seg, seg_len, 0);
+      load_scales(ahead, page_of(ahead), sk_next, sv_next);
+      more = ahead.next(seg, seg_len, nseg);
+      if (more) id_next = page_of(ahead);
+      convert_q(0);
+    }
+    int n = 0;
+    for (int s = 0; s < nseg && !stop; ++s) {
+      const int4 sg = seg[s];
+      const int L = seg_len[s];
+      const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
+      const int seen0 = L - (p.tokens - 1) + tg * p.unit_tokens;   // tokens that the unit's first row sees
+      uint64_t l2[kC / 2], nm2[kC / 2];   // row sums, minus the reference maximum: pairs of rows
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) {
+        l2[i] = 0;
+        nm2[i] = pack_f32x2(INFINITY, INFINITY);
+      }
+      int e_ref = kBEMin;   // reference exponent of the value scales
+      if (!aborted && !wait_warp(bar(kQReady), s & 1, abort_flag)) aborted = true;
+      const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
+      for (int j = sg.z; j < sg.w; ++j, ++n) {
+        const float a = p.scale_log2 * sk_next, sv = sv_next;
+        if (more) {
+          load_scales(ahead, id_next, sk_next, sv_next);
+          more = ahead.next(seg, seg_len, nseg);
+          if (more) id_next = page_of(ahead);
+        }
+        if (!aborted && !wait_warp(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
+        tc_fence_after();
+        const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));
+        const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;   // this lane's token
+        const bool masked = kBTile * (j + 1) > seen0;                      // (of the whole tile)
+        const uint64_t a2 = pack_f32x2(a, a);
+        const int ev = sv > 0.f ? static_cast<int>(__float_as_uint(sv) >> 23) - 127 : kBEMin;
+        uint64_t x2[kC / 2];
+        // scores relative to the reference, in powers of two; -inf for what a row does not see
+        auto relative = [&](bool from_zero) {
+          uint32_t sr[kC];
+          tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
+          tmem_ld_wait(sr);
+#pragma unroll
+          for (int i = 0; i < kC / 2; i += 2) {
+            const ulonglong2 w = w4[i / 2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t s2 = pack_f32x2(__uint_as_float(sr[2 * (i + k)]), __uint_as_float(sr[2 * (i + k) + 1]));
+              const uint64_t aw = mul_f32x2(a2, k ? w.y : w.x);
+              x2[i + k] = from_zero ? mul_f32x2(s2, aw) : fma_f32x2(s2, aw, nm2[i + k]);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) {
+              float lo, hi;
+              unpack_f32x2(x2[i], lo, hi);
+              lo = t < seen0 + row_tok[c0 + 2 * i] ? lo : -INFINITY;
+              hi = t < seen0 + row_tok[c0 + 2 * i + 1] ? hi : -INFINITY;
+              x2[i] = pack_f32x2(lo, hi);
+            }
+          }
+        };
+        relative(false);
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) {
+          float lo, hi;
+          unpack_f32x2(x2[i], lo, hi);
+          top = fmaxf(top, fmaxf(lo, hi));
+        }
+        bool o_ready = false;   // the previous tile's PV is known to be complete
+        if (named_bar_or(vote_bar, 128, top > kBThreshold || ev > e_ref || aborted)) {
+          // a score passes its row's reference by more than 2^3, or a value scale its own: new
+          // references, and the sums and O move to them
+          if (named_bar_or(vote_bar, 128, aborted || *abort_flag)) {
+            stop = true;
+            break;
+          }
+          relative(true);
+          float y[kC];
+#pragma unroll
+          for (int i = 0; i < kC / 2; ++i) unpack_f32x2(x2[i], y[2 * i], y[2 * i + 1]);
+          const float cmax = reduce_columns<kC, true>(y);
+          if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
+          const int emax = __reduce_max_sync(0xffffffffu, ev);
+          if (lane == 0) my_red_e[quarter] = emax;
+          named_bar_sync(vote_bar, 128);
+          int e_new = e_ref;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e_new = max(e_new, my_red_e[k]);
+          const bool begun = j > sg.z;   // O holds something
+          const float eshift = begun ? __uint_as_float(static_cast<uint32_t>(max(1, 127 + e_ref - e_new)) << 23) : 1.f;
+          e_ref = e_new;
+          float alpha[kC];
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            float m = my_red[i];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) m = fmaxf(m, my_red[k * kC + i]);
+            y[i] = m;
+          }
+#pragma unroll
+          for (int i = 0; i < kC / 2; ++i) {
+            float o0, o1, l0, l1;
+            unpack_f32x2(nm2[i], o0, o1);
+            unpack_f32x2(l2[i], l0, l1);
+            const float n0 = fminf(o0, -y[2 * i]), n1 = fminf(o1, -y[2 * i + 1]);   // minus the new references
+            alpha[2 * i] = n0 < INFINITY ? ex2_approx(n0 - o0) : 1.f;
+            alpha[2 * i + 1] = n1 < INFINITY ? ex2_approx(n1 - o1) : 1.f;
+            l2[i] = pack_f32x2(l0 * alpha[2 * i], l1 * alpha[2 * i + 1]);
+            nm2[i] = pack_f32x2(n0, n1);
+          }
+          if (begun) {
+            if (!wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
+            o_ready = true;
+            tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < 2 * kHalves; ++h) {   // halves x (hi, lo)
+              uint32_t o[kC];
+              const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + lane_base;
+              tmem_ld(at, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < kC; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (alpha[i] * eshift));
+              tmem_st(at, o);
+            }
+            tmem_st_wait();
+          }
+          relative(false);
+        }
+        // weights p = 2^x, their sums in fp32, and p s_v 2^(4 - E) as e4m3 hi + lo parts
+        const __half u = __float2half_rn(sv * __uint_as_float(static_cast<uint32_t>(127 + kBPvShift - e_ref) << 23));
+        const __half2 u2 = __half2half2(u);
+        uint32_t hi[kC / 4], lo[kC / 4];
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) {
+          float x0, x1;
+          unpack_f32x2(x2[i], x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          l2[i] = add_f32x2(l2[i], pack_f32x2(p0, p1));
+          const __half2 pu = __hmul2(__floats2half2_rn(p0, p1), u2);
+          uint16_t h8, l8;
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h8) : "r"(*reinterpret_cast<const uint32_t*>(&pu)));
+          uint32_t back;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h8));
+          const __half2 rest = __hsub2(pu, *reinterpret_cast<const __half2*>(&back));
+          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l8) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+          if (i % 2 == 0) {
+            hi[i / 2] = h8;
+            lo[i / 2] = l8;
+          } else {
+            hi[i / 2] |= static_cast<uint32_t>(h8) << 16;
+            lo[i / 2] |= static_cast<uint32_t>(l8) << 16;
+          }
+        }
+        // the P buffer is free once the PV that read it is complete
+        if (n >= kPBufs && !(kPBufs == 1 && o_ready) && !aborted)
+          if (!wait_warp(bar(kPvDone + ((n - kPBufs) & 1)), ((n - kPBufs) >> 1) & 1, abort_flag)) aborted = true;
+        {
+          uint8_t* dst = smem + Lay::kOffP + (n % kPBufs) * 16384 + row * 128;
+          const int sx = row & 7;
+          if constexpr (kC >= 16) {
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k) {
+              *reinterpret_cast<uint4*>(dst + (((c0 / 16 + k) ^ sx) << 4)) =
+                  make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+              *reinterpret_cast<uint4*>(dst + ((((kNR + c0) / 16 + k) ^ sx) << 4)) =
+                  make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+            }
+          } else {
+            *reinterpret_cast<uint2*>(dst + (sx << 4) + c0) = make_uint2(hi[0], hi[1]);          // chunk 0: rows 0..15
+            *reinterpret_cast<uint2*>(dst + ((1 ^ sx) << 4) + c0) = make_uint2(lo[0], lo[1]);    // chunk 1: lo parts
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + n % kPBufs));
+      }
+      if (stop) break;
+      if (s + 1 < nseg) convert_q(s + 1);
+
+      // ---------------- the segment's result
+      {
+        float l[kC], m[kC];
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) {
+          unpack_f32x2(l2[i], l[2 * i], l[2 * i + 1]);
+          unpack_f32x2(nm2[i], m[2 * i], m[2 * i + 1]);
+        }
+        const float lsum = reduce_columns<kC, false>(l);
+        named_bar_sync(vote_bar, 128);   // (the scratch may still be read from the last new reference)
+        if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = lsum;
+        if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
+        if (named_bar_or(vote_bar, 128, aborted)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const bool whole = sg.z == 0 && sg.w == block_tiles(L);
+        const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
+        const size_t slot = static_cast<size_t>(sg.y) * p.batch + sg.x + blockIdx.x;
+        const size_t first = (static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group;
+        float mine_l = 0.f, mine_m = 0.f;
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          l[i] = my_red[i] + my_red[kC + i] + my_red[2 * kC + i] + my_red[3 * kC + i];
+          if (row == i) {
+            mine_l = l[i];
+            mine_m = -m[i];
+          }
+        }
+        if (row < kC && c0 + row < valid) {
+          // (a row that sees nothing has no sum: -inf)
+          const float v = mine_l == 0.f ? -INFINITY : mine_m * 0.6931471805599453f + logf(mine_l);
+          if (!whole)
+            p.part_lse[slot * p.rows + c0 + row] = v;
+          else if (p.lse != nullptr)
+            p.lse[first + row_off[c0 + row] / kDim] = v;
+        }
+        const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref - kBPvShift) << 23);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) l[i] = l[i] == 0.f ? 0.f : back / l[i];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          uint32_t o[kC], o2[kC];
+          const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c0 + lane_base;
+          tmem_ld(at, o);
+          tmem_ld(at + kNR, o2);
+          tmem_ld_wait(o);
+          tmem_ld_wait(o2);
+          if (h == kHalves - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
+          }
+          const int col = 128 * h + row;
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            if (c0 + i < valid) {
+              const float v = (__uint_as_float(o[i]) + __uint_as_float(o2[i])) * l[i];
+              if (!whole)
+                p.part_o[(slot * p.rows + c0 + i) * kDim + col] = v;
+              else if (f32)
+                static_cast<float*>(p.out)[first * kDim + row_off[c0 + i] + col] = v;
+              else
+                static_cast<__nv_bfloat16*>(p.out)[first * kDim + row_off[c0 + i] + col] = __float2bfloat16_rn(v);
+            }
+          }
+        }
+      }
+    }
+    if (stop && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.status, MFA_DEV_TIMEOUT);
+    }
   }
-  if (threadIdx.x == 0 && p.lse != nullptr) p.lse[row] = n > 0 ? M * 0.6931471805599453f + logf(S) : -INFINITY;
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, Lay::kTmemCols);
+}
+
+// ------------------------------------------------------------------ combine kernel
+//
+// Units that CTA boundaries cut: out = sum_s e^(lse_s - lse) O_s over the parts, with
+// lse = ln sum_s e^lse_s.  A row's d / 4 threads hold 4 elements each; kSplit such groups share
+// one row's parts (few rows, many parts) or take a row each (kSplit = 1).  The parts go by in
+// rounds of four with a running maximum, loads of a round together.
+template <int kDim, bool kSplit>
+__global__ void __launch_bounds__(kBCombineThreads) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p,
+                                                                             const int num_ctas) {
+  constexpr int kLanes = kDim / 4, kTeams = kBCombineThreads / kLanes;
+  __shared__ long long scan[kBCombineThreads / 32];
+  __shared__ long long s_before;
+  __shared__ __align__(16) float so[kSplit ? kTeams : 1][kSplit ? kDim : 4];
+  __shared__ float sm[kTeams], sl[kTeams];
+  const int tid = threadIdx.x, team = tid / kLanes, el = tid % kLanes;
+  const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
+  // The decode kernel lets this one start once its own wait for what came before is over, so
+  // the lengths are final here; what the decode writes is read after this kernel's wait.
+  const int cap = p.max_pages * kBPage;
+  bool bad = false;
+  const int L = clamp_len(p.seq_lens[b], cap, bad);
+  if (L == 0) {
+    grid_dep_wait();
+    grid_dep_launch();
+    return;
+  }
+  long long carry = 0;
+  for (int c0 = 0; c0 < p.batch; c0 += kBCombineThreads) {
+    const int i = c0 + tid;
+    const long long own = i < p.batch ? pack_tiles(block_tiles(clamp_len(p.seq_lens[i], cap, bad))) : 0;
+    long long sum = 0;
+    const long long before = block_incl_scan<kBCombineThreads, long long>(own, scan, sum) - own + carry;
+    if (i == b) s_before = before;
+    carry += sum;
+  }
+  __syncthreads();
+  const BlockCost cost = block_cost(carry, p.readers);
+  const long long base = r * cost.per_reader + cost_before(s_before), G = num_ctas;
+  const int T = block_tiles(L);
+  // the CTA of the tile at cost X: the largest g with floor(g C / G) <= X
+  auto owner = [&](long long X) {
+    long long g = X * G / cost.total;
+    while (g + 1 < G && (g + 1) * cost.total / G <= X) ++g;
+    while (g > 0 && g * cost.total / G > X) --g;
+    return static_cast<int>(g);
+  };
+  const int g0 = owner(base), g1 = owner(base + kBCostTile * static_cast<long long>(T - 1));
+  grid_dep_wait();
+  grid_dep_launch();
+  if (g0 == g1) return;   // one CTA had the whole unit
+  const int tg = r % p.token_groups, kvh = r / p.token_groups;
+  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
+  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
+  const bool dense = cost.total >= kBCostTile * G;   // every CTA inside the unit holds a tile of it
+  constexpr int kRowStep = kSplit ? 1 : kTeams;
+  for (int row = blockIdx.y * kRowStep + (kSplit ? 0 : team); row < valid; row += gridDim.y * kRowStep) {
+    float M = -INFINITY, S = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kRound = 4;
+    const int step = kSplit ? kTeams : 1;
+    for (int ga = g0 + (kSplit ? team : 0); ga <= g1; ga += kRound * step) {
+      float v[kRound];
+      float4 o[kRound];
+#pragma unroll
+      for (int k = 0; k < kRound; ++k) {
+        const int gk = ga + k * step;
+        v[k] = -INFINITY;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (gk <= g1) {
+          // a CTA whose range lies between two tiles has no part of the unit
+          if (dense || first_tile_at(gk * cost.total / G, base, T) < first_tile_at((gk + 1) * cost.total / G, base, T)) {
+            const size_t at = (static_cast<size_t>(pos) + gk) * p.rows + row;
+            v[k] = p.part_lse[at];
+            o[k] = reinterpret_cast<const float4*>(p.part_o + at * kDim)[el];
+          }
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kRound; ++k) top = fmaxf(top, v[k]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float al = M == -INFINITY ? 0.f : expf(M - ref);
+      M = top;
+      S *= al;
+      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+#pragma unroll
+      for (int k = 0; k < kRound; ++k) {
+        const float w = v[k] == -INFINITY ? 0.f : expf(v[k] - ref);
+        S += w;
+        acc.x += w * o[k].x;
+        acc.y += w * o[k].y;
+        acc.z += w * o[k].z;
+        acc.w += w * o[k].w;
+      }
+    }
+    if constexpr (kSplit) {
+      *reinterpret_cast<float4*>(&so[team][4 * el]) = acc;
+      if (el == 0) {
+        sm[team] = M;
+        sl[team] = S;
+      }
+      __syncthreads();
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kTeams; ++k) top = fmaxf(top, sm[k]);
+      M = top;
+      S = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int k = 0; k < kTeams; ++k) {
+        const float w = sl[k] == 0.f ? 0.f : expf(sm[k] == -INFINITY ? 0.f : sm[k] - ref);
+        S += sl[k] * w;
+        const float4 o = *reinterpret_cast<const float4*>(&so[k][4 * el]);
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+      }
+      __syncthreads();
+    }
+    if (kSplit && team != 0) continue;
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const size_t at = first + static_cast<size_t>(row / p.group) * p.heads + row % p.group;
+    if (p.out_f32)
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kDim)[el] =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kDim)[el] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+    }
+    if (el == 0 && p.lse != nullptr) p.lse[at] = S == 0.f ? -INFINITY : M + logf(S);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+using BlockDecodeFn = void (*)(BlockDecodeParams);
+using BlockCombineFn = void (*)(BlockDecodeParams, int);
+
+// The instance of a problem: width and rows padded to 16, 32 or 64.
+static int block_instance(const mfa_problem* pr, const BlockShape& sh) {
+  return (pr->head_dim == 256 ? 3 : 0) + (sh.rows <= 16 ? 0 : sh.rows <= 32 ? 1 : 2);
+}
+static BlockDecodeFn block_kernel_of(int i) {
+  constexpr BlockDecodeFn k[6] = {mfa_block_decode_kernel<128, 16>, mfa_block_decode_kernel<128, 32>,
+                                  mfa_block_decode_kernel<128, 64>, mfa_block_decode_kernel<256, 16>,
+                                  mfa_block_decode_kernel<256, 32>, mfa_block_decode_kernel<256, 64>};
+  return k[i];
+}
+
+// cudaFuncSetAttribute for an instance's dynamic shared memory, once per device and instance.
+static mfa_status ensure_block_smem(int i) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> done[6][kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  if (cacheable && done[i][dev].load(std::memory_order_acquire)) return MFA_OK;
+  e = cudaFuncSetAttribute(block_kernel_of(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmem + 1024);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  if (cacheable) done[i][dev].store(true, std::memory_order_release);
+  return MFA_OK;
 }
 
 }  // namespace mfa
@@ -245,40 +1035,80 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   BlockDecodeParams p;
   std::memset(&p, 0, sizeof(p));
+  const void* pools[2] = {k_cache, v_cache};
+  CUtensorMap* maps[2] = {&p.tm_k, &p.tm_v};
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return cuda_fail_msg("cuTensorMapEncodeTiled is not available from the driver");
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t d = static_cast<cuuint64_t>(pr->head_dim);
+    const cuuint64_t dims[3] = {d, kBPage, static_cast<cuuint64_t>(pr->num_blocks) * pr->num_kv_heads};
+    const cuuint64_t strides[2] = {d, d * kBPage};
+    const cuuint32_t box[3] = {128, kBPage, 1}, es[3] = {1, 1, 1};
+    if (enc(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pools[i]), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cuda_fail_msg("cuTensorMapEncodeTiled rejected a tensor map");
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.out = out;
   p.lse = lse;
-  p.status = static_cast<unsigned int*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
+  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh.rows, pr->head_dim));
+  p.status = reinterpret_cast<unsigned int*>(ws);
   p.batch = pr->batch;
   p.tokens = pr->tokens_per_seq;
   p.heads = pr->num_q_heads;
   p.kv_heads = pr->num_kv_heads;
+  p.group = sh.group;
+  p.unit_tokens = sh.unit_tokens;
+  p.token_groups = sh.token_groups;
+  p.readers = sh.readers;
+  p.rows = sh.rows;
   p.log_scale = scale_tokens == 64 ? 6 : scale_tokens == 32 ? 5 : 4;
   p.max_pages = pr->max_pages_per_seq;
   p.num_blocks = pr->num_blocks;
   p.scale_log2 = static_cast<float>(static_cast<double>(pr->softmax_scale) * 1.4426950408889634);
   p.out_f32 = pr->out_dtype == MFA_OUT_FP32 ? 1 : 0;
+  p.early_metadata = (plan->flags & MFA_PLAN_EARLY_METADATA) ? 1 : 0;
   const bool check = (plan->flags & MFA_PLAN_CHECK) != 0;
   cudaError_t e = cudaSuccess;
   if (check && (e = cudaMemsetAsync(workspace, 0, 4, stream)) != cudaSuccess) return cuda_fail(e, "memset");
+  const int inst = block_instance(pr, sh);
+  const mfa_status sst = ensure_block_smem(inst);
+  if (sst != MFA_OK) return sst;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pr->batch) * pr->tokens_per_seq, static_cast<unsigned>(pr->num_q_heads), 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan->num_ctas), 1, 1);
+  cfg.blockDim = dim3(kBThreads, 1, 1);
+  cfg.dynamicSmemBytes = kBSmem + 1024;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = pr->head_dim == 256 ? cudaLaunchKernelEx(&cfg, mfa_block_decode_kernel<256>, p)
-                          : cudaLaunchKernelEx(&cfg, mfa_block_decode_kernel<128>, p);
+  e = cudaLaunchKernelEx(&cfg, block_kernel_of(inst), p);
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
+  if (plan->num_ctas > 1) {
+    const unsigned units = static_cast<unsigned>(pr->batch) * sh.readers;
+    const int teams = kBCombineThreads / (pr->head_dim / 4);
+    // about four CTAs an SM: with fewer rows than that a row is split over the CTA's teams
+    const bool split = static_cast<long long>(units) * sh.rows <= 4LL * plan->num_sms;
+    const int most = split ? sh.rows : (sh.rows + teams - 1) / teams;
+    const int want = static_cast<int>(std::max(1LL, (4LL * plan->num_sms + units - 1) / units));
+    cfg.gridDim = dim3(units, static_cast<unsigned>(std::min(most, want)), 1);
+    cfg.blockDim = dim3(kBCombineThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    const BlockCombineFn fn = pr->head_dim == 256
+                                  ? (split ? mfa_block_combine_kernel<256, true> : mfa_block_combine_kernel<256, false>)
+                                  : (split ? mfa_block_combine_kernel<128, true> : mfa_block_combine_kernel<128, false>);
+    e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(plan->num_ctas));
+    if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
+  }
   if (check) {
     uint32_t word = 0;
     if ((e = cudaMemcpyAsync(&word, workspace, 4, cudaMemcpyDeviceToHost, stream)) != cudaSuccess)

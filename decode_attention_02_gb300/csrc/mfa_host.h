@@ -1,6 +1,8 @@
 // Host-side helpers shared by the library's translation units (defined in mfa_decode.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -10,6 +12,11 @@ namespace mfa {
 
 // Records the text of a CUDA failure for mfa_last_cuda_error() and returns MFA_ERR_CUDA.
 mfa_status cuda_fail(cudaError_t e, const char* where);
+// The same for a failure with a text of its own (a static string).
+mfa_status cuda_fail_msg(const char* msg);
+
+// The driver's cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Shape, dtype and range checks of a problem description (MFA_OK, or the error to return).
 mfa_status check_problem(const mfa_problem* pr);

@@ -396,7 +396,9 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
 /*
  * Choose the split of the decode's work, as mfa_decode_plan does for the other caches (same
  * arguments; MFA_PLAN_NO_COMBINE is refused).  The plan is for mfa_block_decode_run alone.
- * plan->max_tiles_per_cta is the most 128-token tiles that a CTA can get and is not limited.
+ * The work is split as there, by cost: 4 a tile of 128 tokens and 6 a boundary between units
+ * (sequence, key/value head, and a group of the new tokens whose rows, tokens x query heads of
+ * the head, are at most 64).  plan->max_tiles_per_cta bounds a CTA's tiles and is not limited.
  */
 mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
@@ -418,7 +420,7 @@ mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_token
  * Slots past a sequence's length, the scales of blocks without a token and unused pages may
  * hold any bits.  A block id outside the pool reads as a page of zeros and sets
  * MFA_DEV_BAD_BLOCK; a length outside [0, max_pages*64] is clamped and sets MFA_DEV_BAD_LENGTH;
- * lengths that need more of a CTA than the plan allows leave outputs unwritten and set
+ * lengths that need more of a CTA than the plan allows leave the outputs unspecified and set
  * MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
  */
 mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_problem* problem, int32_t scale_tokens,

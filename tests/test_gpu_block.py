@@ -187,6 +187,18 @@ def test_bad_pages_read_as_zeros_and_bad_lengths_are_clamped():
     check(c, out, lse)
 
 
+def test_lengths_past_the_plan_are_refused_by_the_device():
+    """Planned for 3 short sequences on one CTA, run with lengths that need room for more units."""
+    n = 600
+    c = ref.Case([0] * (n - 3) + [3] * 3, heads=8, kv_heads=1, dim=128, columns=1, seed=1, poison=False)
+    dec = decoder(c, force_ctas=1)
+    d = device(c)
+    check(c, *dec(*d))
+    assert mfa.mfa_read_device_status(dec.workspace) == 0
+    dec(*d[:6], torch.full((n,), 5, dtype=torch.int32, device=DEV))
+    assert mfa.mfa_read_device_status(dec.workspace) == mfa.MFA_DEV_SCHEDULE
+
+
 def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
     c = ref.Case([700, 64, 1500], **GQA, tokens=2, seed=13)
     d, dec = device(c), decoder(c, lens=None)
