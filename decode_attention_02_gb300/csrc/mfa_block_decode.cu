@@ -32,18 +32,19 @@ constexpr int kBCostTile = 4;         // schedule: cost of a tile
 constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's range
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
-constexpr int kBThreads = 320;        // producer warp, MMA warp, eight softmax warps
+constexpr int kBThreads = 352;        // producer warp, MMA warp, eight softmax warps, scale warp
 constexpr int kBSoftmaxWarps = 8;
 constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
-constexpr int kBMisc = 8192;          // of it, behind the ring: segments, scratch, barriers (the last 256)
-// A row's reference maximum moves when a score passes it by more than 2^3.  A value scale s_v
-// is folded into its token's weights as s_v 2^(4 - E), E the segment's reference exponent
-// (s_v < 2^(E + 1) for all so far), so that weights stay below 2^3 * 2 * 2^4 = 256, inside
-// e4m3's 448, and ordinary ones lie near 1, where both e4m3 parts are normal numbers.
-constexpr float kBThreshold = 3.0f;
-constexpr int kBPvShift = 4;
-constexpr int kBEMin = -120;          // floor of E (2^(kBPvShift - E) stays a normal fp32 number)
+constexpr int kBMisc = 9216;          // of it, behind the ring: segments, scratch, barriers (the last 512)
+constexpr int kBMeta = 4;             // tiles whose scales are held in shared memory
+// Weights p = 2^x, x a score (in powers of two) relative to its row's reference.  A value scale
+// s_v is folded into its token's weights as s_v 2^-E, E the segment's reference exponent.  The
+// references move when max(x, 0) + log2(s_v) - E passes 7 for some token and row, so that what
+// is rounded to e4m3 stays below 2^8 (448 is its largest), and 2^x and s_v 2^-E inside f16.
+constexpr float kBThreshold = 7.0f;
+constexpr int kBMaxBelow = 8;         // a small s_v gives a score at most this much more room
+constexpr int kBEMin = -120;          // floor of E (2^-E stays a normal fp32 number)
 
 // The work of one problem: a unit is (sequence, key/value head, group of new tokens); its rows
 // are the group's new tokens x the query heads that read that head.
@@ -207,22 +208,25 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
   float* q_inv = reinterpret_cast<float*>(red_e + 8);                // [2 segments][64] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 128);                // [64] element offset of a row's output
   int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
-  long long* scan = reinterpret_cast<long long*>(row_tok + 64);      // [16]
+  float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
+  float* alpha = neg_ref + 64;                                       // [64] what old sums are multiplied by
+  float2* meta = reinterpret_cast<float2*>(alpha + 64);              // [kBMeta][2 pages][4 blocks] {K, V} scales
+  long long* scan = reinterpret_cast<long long*>(meta + 8 * kBMeta); // [16]
   int* iscan = reinterpret_cast<int*>(scan + 16);                    // [16]
   int* ctl = iscan + 16;                                             // tensor memory, abort flag, tiles of this CTA
   volatile int* abort_flag = ctl + 1;
-  const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 256;
+  const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   constexpr int kFull = 0, kEmpty = kGroups, kSFull = 2 * kGroups, kPFull = kSFull + 2, kPvDone = kPFull + 2,
                 kQReady = kPvDone + 2, kQEmpty = kQReady + 1, kOEmpty = kQEmpty + 1, kDrain = kOEmpty + 1,
-                kBars = kDrain + 1;
-  static_assert(kBars * 8 <= 256, "barrier area");
+                kMeta = kDrain + 1, kMetaEmpty = kMeta + kBMeta, kBars = kMetaEmpty + kBMeta;
+  static_assert(kBars * 8 <= 512, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == 0) {
     for (int i = lane; i < kBars; i += 32) {
       // arrivals a phase: one for each box of a slot; one for each softmax warp; else one commit
-      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty;
+      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty || i >= kMetaEmpty;
       mbar_init(bar(i), i < kEmpty ? kBoxes : by_warps ? kBSoftmaxWarps : 1);
     }
     if (lane == 0) {
@@ -359,6 +363,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           wait_slow(bar(kFull + u % kGroups), (u / kGroups) & 1, nullptr, kDrainLimitNs);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer: QK^T one tile ahead of PV
     if (lane == 0 && ntiles > 0) {
@@ -430,6 +435,57 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       umma_commit(bar(kDrain));
       wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
     }
+    __syncwarp();
+  } else if (warp == kBThreads / 32 - 1) {
+    // ---------------- scales: a tile's up to 2 x 4 block scales of K and of V, ahead of the softmax
+    // (lane = V? page, block); page ids two tiles ahead, scales one tile ahead
+    const int pg = (lane >> 2) & 1, blk = lane & 3;
+    const bool is_v = (lane & 8) != 0, mine = lane < 16 && blk < (kBPage >> p.log_scale);
+    const float* src = is_v ? p.v_scale : p.k_scale;
+    const float mul = is_v ? 1.f : p.scale_log2;
+    if (ntiles > 0) {
+      BlockTile it;
+      it.load(seg, seg_len, 0);
+      int kvh = it.r / p.token_groups;
+      auto page_id = [&]() -> int {
+        return mine && it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : -1;
+      };
+      auto scale_of = [&](int id) -> float {
+        if (id < 0 || id >= p.num_blocks) return 0.f;
+        return src[((static_cast<size_t>(id) * p.kv_heads + kvh) << (6 - p.log_scale)) + blk];
+      };
+      float value = scale_of(page_id());
+      int s = 0;
+      bool more = it.next(seg, seg_len, nseg);
+      int id = more ? page_id() : -1;
+      for (int n = 0; n < ntiles; ++n) {
+        float value_next = 0.f;
+        if (more) {
+          if (it.s != s) {
+            s = it.s;
+            kvh = it.r / p.token_groups;
+            // the next segment's q, for its conversion to find in L2
+            const char* q = reinterpret_cast<const char*>(
+                p.q + ((static_cast<size_t>(it.b) * p.tokens + (it.r % p.token_groups) * p.unit_tokens) * p.heads +
+                       static_cast<size_t>(kvh) * p.group) * kDim);
+            const int lines = p.group * kDim * 2 / 128;
+            for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 128));
+          }
+          value_next = scale_of(id);
+          more = it.next(seg, seg_len, nseg);
+          if (more) id = page_id();
+        }
+        if (!wait_warp(bar(kMetaEmpty + n % kBMeta), ((n / kBMeta) & 1) ^ 1, abort_flag)) {
+          if (lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
+          break;
+        }
+        if (mine) reinterpret_cast<float*>(meta + (n % kBMeta) * 8 + pg * 4 + blk)[is_v ? 1 : 0] = value * mul;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kMeta + n % kBMeta));
+        value = value_next;
+      }
+    }
+    __syncwarp();
   } else {
     // ---------------- softmax and epilogue: two warpgroups, each the whole tile (lane = token)
     // for its kC rows
@@ -507,157 +563,130 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       if (lane == 0) mbar_arrive(bar(kQReady));
     };
 
-    // the scales of this thread's token: page ids two tiles ahead, scales one tile ahead
-    BlockTile ahead;
-    bool more = ntiles > 0;
-    auto page_of = [&](const BlockTile& t) -> int {
-      return t.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(t.b) * p.max_pages + 2 * t.j + pg] : -1;
-    };
-    auto load_scales = [&](const BlockTile& t, int id, float& sk, float& sv) {
-      const int pr = ri - (kBPage - t.page_rows(pg));   // page row of this box row
-      sk = sv = 0.f;
-      if (pr >= 0 && id >= 0 && id < p.num_blocks) {
-        const size_t at = ((static_cast<size_t>(id) * p.kv_heads + t.r / p.token_groups) << (6 - p.log_scale)) + (pr >> p.log_scale);
-        sk = __ldg(p.k_scale + at);
-        sv = __ldg(p.v_scale + at);
-      }
-    };
-    float sk_next = 0.f, sv_next = 0.f;
-    int id_next = -1;
-    if (more) {
-      ahead.load(seg, seg_len, 0);
-      load_scales(ahead, page_of(ahead), sk_next, sv_next);
-      more = ahead.next(seg, seg_len, nseg);
-      if (more) id_next = page_of(ahead);
-      convert_q(0);
-    }
+    if (ntiles > 0) convert_q(0);
     int n = 0;
     for (int s = 0; s < nseg && !stop; ++s) {
       const int4 sg = seg[s];
       const int L = seg_len[s];
       const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
       const int seen0 = L - (p.tokens - 1) + tg * p.unit_tokens;   // tokens that the unit's first row sees
-      uint64_t l2[kC / 2], nm2[kC / 2];   // row sums, minus the reference maximum: pairs of rows
+      uint64_t l2[kC / 2];   // row sums over this lane's tokens: pairs of rows
 #pragma unroll
-      for (int i = 0; i < kC / 2; ++i) {
-        l2[i] = 0;
-        nm2[i] = pack_f32x2(INFINITY, INFINITY);
-      }
-      int e_ref = kBEMin;   // reference exponent of the value scales
+      for (int i = 0; i < kC / 2; ++i) l2[i] = 0;
+      if (row < kC) neg_ref[c0 + row] = INFINITY;
+      int e_ref = kBEMin;
       if (!aborted && !wait_warp(bar(kQReady), s & 1, abort_flag)) aborted = true;
+      named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
+      const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(neg_ref + c0);
       for (int j = sg.z; j < sg.w; ++j, ++n) {
-        const float a = p.scale_log2 * sk_next, sv = sv_next;
-        if (more) {
-          load_scales(ahead, id_next, sk_next, sv_next);
-          more = ahead.next(seg, seg_len, nseg);
-          if (more) id_next = page_of(ahead);
-        }
+        const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
+        const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
+        if (!aborted && !wait_warp(bar(kMeta + n % kBMeta), (n / kBMeta) & 1, abort_flag)) aborted = true;
+        const float2 sc = pr >= 0 ? meta[(n % kBMeta) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
+        const uint64_t a2 = pack_f32x2(sc.x, sc.x);
+        const int ev = sc.y > 0.f ? static_cast<int>(__float_as_uint(sc.y) >> 23) - 127 : kBEMin;
         if (!aborted && !wait_warp(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
-        const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));
-        const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;   // this lane's token
-        const bool masked = kBTile * (j + 1) > seen0;                      // (of the whole tile)
-        const uint64_t a2 = pack_f32x2(a, a);
-        const int ev = sv > 0.f ? static_cast<int>(__float_as_uint(sv) >> 23) - 127 : kBEMin;
         uint64_t x2[kC / 2];
-        // scores relative to the reference, in powers of two; -inf for what a row does not see
-        auto relative = [&](bool from_zero) {
-          uint32_t sr[kC];
-          tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
-          tmem_ld_wait(sr);
+        bool o_ready = false;   // the previous tile's PV is known to be complete
+        for (bool settled = false;; settled = true) {
+          // scores relative to the reference, in powers of two; -inf for what a row does not see
+          {
+            uint32_t sr[kC];
+            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
+            tmem_ld_wait(sr);
 #pragma unroll
-          for (int i = 0; i < kC / 2; i += 2) {
-            const ulonglong2 w = w4[i / 2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint64_t s2 = pack_f32x2(__uint_as_float(sr[2 * (i + k)]), __uint_as_float(sr[2 * (i + k) + 1]));
-              const uint64_t aw = mul_f32x2(a2, k ? w.y : w.x);
-              x2[i + k] = from_zero ? mul_f32x2(s2, aw) : fma_f32x2(s2, aw, nm2[i + k]);
+            for (int i = 0; i < kC / 2; i += 2) {
+              const ulonglong2 w = w4[i / 2], m = m4[i / 2];
+              x2[i] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), mul_f32x2(a2, w.x), m.x);
+              x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), m.y);
             }
           }
-          if (masked) {
+          if (kBTile * (j + 1) > seen0) {   // some row does not see some token of the tile
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i) {
               float lo, hi;
               unpack_f32x2(x2[i], lo, hi);
-              lo = t < seen0 + row_tok[c0 + 2 * i] ? lo : -INFINITY;
-              hi = t < seen0 + row_tok[c0 + 2 * i + 1] ? hi : -INFINITY;
-              x2[i] = pack_f32x2(lo, hi);
+              const int2 tok = *reinterpret_cast<const int2*>(row_tok + c0 + 2 * i);
+              x2[i] = pack_f32x2(t < seen0 + tok.x ? lo : -INFINITY, t < seen0 + tok.y ? hi : -INFINITY);
             }
           }
-        };
-        relative(false);
-        float top = -INFINITY;
+          if (settled) break;
+          float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kC / 2; ++i) {
-          float lo, hi;
-          unpack_f32x2(x2[i], lo, hi);
-          top = fmaxf(top, fmaxf(lo, hi));
-        }
-        bool o_ready = false;   // the previous tile's PV is known to be complete
-        if (named_bar_or(vote_bar, 128, top > kBThreshold || ev > e_ref || aborted)) {
-          // a score passes its row's reference by more than 2^3, or a value scale its own: new
-          // references, and the sums and O move to them
+          for (int i = 0; i < kC / 2; ++i) {
+            float lo, hi;
+            unpack_f32x2(x2[i], lo, hi);
+            top = fmaxf(top, fmaxf(lo, hi));
+          }
+          if (!named_bar_or(vote_bar, 128, fmaxf(top, 0.f) + static_cast<float>(max(ev - e_ref, -kBMaxBelow)) > kBThreshold || aborted)) break;
           if (named_bar_or(vote_bar, 128, aborted || *abort_flag)) {
             stop = true;
             break;
           }
-          relative(true);
-          float y[kC];
+          // ---- new references: each row's largest score so far, the largest value scale's
+          // exponent; the sums and O move to them.  Rare after a segment's first tile: eight rows
+          // at a time, so that the code stays small.
+#pragma unroll 1
+          for (int c = 0; c < kC; c += 8) {
+            uint32_t sr[8];
+            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + c + lane_base, sr);
+            tmem_ld_wait(sr);
+            float y[8];
 #pragma unroll
-          for (int i = 0; i < kC / 2; ++i) unpack_f32x2(x2[i], y[2 * i], y[2 * i + 1]);
-          const float cmax = reduce_columns<kC, true>(y);
-          if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
+            for (int i = 0; i < 8; ++i)
+              y[i] = t < seen0 + row_tok[c0 + c + i] ? __uint_as_float(sr[i]) * (sc.x * q_inv[(s & 1) * 64 + c0 + c + i]) : -INFINITY;
+            const float cmax = reduce_columns<8, true>(y);
+            if (lane % 4 == 0) my_red[quarter * kC + c + lane / 4] = cmax;
+          }
           const int emax = __reduce_max_sync(0xffffffffu, ev);
           if (lane == 0) my_red_e[quarter] = emax;
           named_bar_sync(vote_bar, 128);
+          if (row < kC) {
+            const float m = fmaxf(fmaxf(my_red[row], my_red[kC + row]), fmaxf(my_red[2 * kC + row], my_red[3 * kC + row]));
+            const float was = neg_ref[c0 + row], now = fminf(was, -m);
+            neg_ref[c0 + row] = now;
+            alpha[c0 + row] = now < INFINITY ? ex2_approx(now - was) : 1.f;
+          }
           int e_new = e_ref;
 #pragma unroll
           for (int k = 0; k < 4; ++k) e_new = max(e_new, my_red_e[k]);
-          const bool begun = j > sg.z;   // O holds something
-          const float eshift = begun ? __uint_as_float(static_cast<uint32_t>(max(1, 127 + e_ref - e_new)) << 23) : 1.f;
+          const float eshift = __uint_as_float(static_cast<uint32_t>(max(1, 127 + e_ref - e_new)) << 23);
           e_ref = e_new;
-          float alpha[kC];
+          named_bar_sync(vote_bar, 128);
 #pragma unroll
-          for (int i = 0; i < kC; ++i) {
-            float m = my_red[i];
-#pragma unroll
-            for (int k = 1; k < 4; ++k) m = fmaxf(m, my_red[k * kC + i]);
-            y[i] = m;
+          for (int i = 0; i < kC / 2; i += 2) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(alpha + c0 + 2 * i);
+            l2[i] = mul_f32x2(l2[i], f.x);
+            l2[i + 1] = mul_f32x2(l2[i + 1], f.y);
           }
-#pragma unroll
-          for (int i = 0; i < kC / 2; ++i) {
-            float o0, o1, l0, l1;
-            unpack_f32x2(nm2[i], o0, o1);
-            unpack_f32x2(l2[i], l0, l1);
-            const float n0 = fminf(o0, -y[2 * i]), n1 = fminf(o1, -y[2 * i + 1]);   // minus the new references
-            alpha[2 * i] = n0 < INFINITY ? ex2_approx(n0 - o0) : 1.f;
-            alpha[2 * i + 1] = n1 < INFINITY ? ex2_approx(n1 - o1) : 1.f;
-            l2[i] = pack_f32x2(l0 * alpha[2 * i], l1 * alpha[2 * i + 1]);
-            nm2[i] = pack_f32x2(n0, n1);
-          }
-          if (begun) {
-            if (!wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
+          if (j > sg.z) {   // O holds something
+            if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
             o_ready = true;
             tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < 2 * kHalves; ++h) {   // halves x (hi, lo)
-              uint32_t o[kC];
-              const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + lane_base;
-              tmem_ld(at, o);
-              tmem_ld_wait(o);
+            for (int h = 0; h < 2 * kHalves; ++h)   // halves x (hi, lo)
+#pragma unroll 1
+              for (int c = 0; c < kC; c += 8) {
+                uint32_t o[8];
+                const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + c + lane_base;
+                tmem_ld(at, o);
+                tmem_ld_wait(o);
 #pragma unroll
-              for (int i = 0; i < kC; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (alpha[i] * eshift));
-              tmem_st(at, o);
-            }
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (alpha[c0 + c + i] * eshift));
+                tmem_st(at, o);
+              }
             tmem_st_wait();
           }
-          relative(false);
         }
-        // weights p = 2^x, their sums in fp32, and p s_v 2^(4 - E) as e4m3 hi + lo parts
-        const __half u = __float2half_rn(sv * __uint_as_float(static_cast<uint32_t>(127 + kBPvShift - e_ref) << 23));
-        const __half2 u2 = __half2half2(u);
+        if (stop) break;
+        // weights p = 2^x, their sums in fp32; and P = p s_v 2^-E, rounded to f16 twice (2^-11 each)
+        // and split into e4m3 parts P = hi + lo / 16: each part keeps four bits, and the lo part's
+        // own accumulator lets it be 16 times larger, so that the smallest step is 2^-13 of the
+        // reference (ordinary weights are hundreds of steps)
+        const __half2 u2 = __half2half2(__float2half_rn(sc.y * __uint_as_float(static_cast<uint32_t>(127 - e_ref) << 23)));
+        const __half2 sixteen = __half2half2(__ushort_as_half(0x4C00));
         uint32_t hi[kC / 4], lo[kC / 4];
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) {
@@ -670,7 +699,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h8) : "r"(*reinterpret_cast<const uint32_t*>(&pu)));
           uint32_t back;
           asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h8));
-          const __half2 rest = __hsub2(pu, *reinterpret_cast<const __half2*>(&back));
+          const __half2 rest = __hmul2(__hsub2(pu, *reinterpret_cast<const __half2*>(&back)), sixteen);
           asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l8) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
           if (i % 2 == 0) {
             hi[i / 2] = h8;
@@ -702,19 +731,19 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull + n % kPBufs));
+        if (lane == 0) {
+          mbar_arrive(bar(kPFull + n % kPBufs));
+          mbar_arrive(bar(kMetaEmpty + n % kBMeta));
+        }
       }
       if (stop) break;
       if (s + 1 < nseg) convert_q(s + 1);
 
       // ---------------- the segment's result
       {
-        float l[kC], m[kC];
+        float l[kC];
 #pragma unroll
-        for (int i = 0; i < kC / 2; ++i) {
-          unpack_f32x2(l2[i], l[2 * i], l[2 * i + 1]);
-          unpack_f32x2(nm2[i], m[2 * i], m[2 * i + 1]);
-        }
+        for (int i = 0; i < kC / 2; ++i) unpack_f32x2(l2[i], l[2 * i], l[2 * i + 1]);
         const float lsum = reduce_columns<kC, false>(l);
         named_bar_sync(vote_bar, 128);   // (the scratch may still be read from the last new reference)
         if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = lsum;
@@ -728,26 +757,20 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
         const size_t slot = static_cast<size_t>(sg.y) * p.batch + sg.x + blockIdx.x;
         const size_t first = (static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group;
-        float mine_l = 0.f, mine_m = 0.f;
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
-          l[i] = my_red[i] + my_red[kC + i] + my_red[2 * kC + i] + my_red[3 * kC + i];
-          if (row == i) {
-            mine_l = l[i];
-            mine_m = -m[i];
+        const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
+        if (row < kC) {
+          // (a row that sees nothing has no sum: zeros and -inf)
+          const float sum = my_red[row] + my_red[kC + row] + my_red[2 * kC + row] + my_red[3 * kC + row];
+          alpha[c0 + row] = sum == 0.f ? 0.f : back / sum;
+          const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
+          if (c0 + row < valid) {
+            if (!whole)
+              p.part_lse[slot * p.rows + c0 + row] = v;
+            else if (p.lse != nullptr)
+              p.lse[first + row_off[c0 + row] / kDim] = v;
           }
         }
-        if (row < kC && c0 + row < valid) {
-          // (a row that sees nothing has no sum: -inf)
-          const float v = mine_l == 0.f ? -INFINITY : mine_m * 0.6931471805599453f + logf(mine_l);
-          if (!whole)
-            p.part_lse[slot * p.rows + c0 + row] = v;
-          else if (p.lse != nullptr)
-            p.lse[first + row_off[c0 + row] / kDim] = v;
-        }
-        const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref - kBPvShift) << 23);
-#pragma unroll
-        for (int i = 0; i < kC; ++i) l[i] = l[i] == 0.f ? 0.f : back / l[i];
+        named_bar_sync(vote_bar, 128);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           uint32_t o[kC], o2[kC];
@@ -765,7 +788,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
 #pragma unroll
           for (int i = 0; i < kC; ++i) {
             if (c0 + i < valid) {
-              const float v = (__uint_as_float(o[i]) + __uint_as_float(o2[i])) * l[i];
+              const float v = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * alpha[c0 + i];
               if (!whole)
                 p.part_o[(slot * p.rows + c0 + i) * kDim + col] = v;
               else if (f32)
