@@ -32,8 +32,9 @@ constexpr int kBCostTile = 4;         // schedule: cost of a tile
 constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's range
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
-constexpr int kBThreads = 352;        // producer warp, MMA warp, eight softmax warps, scale warp
+constexpr int kBThreads = 384;        // warps: producer, QK issuer, eight softmax, scales, PV issuer
 constexpr int kBSoftmaxWarps = 8;
+constexpr int kBScaleWarp = 10, kBPvWarp = 11;
 constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
 constexpr int kBMisc = 9216;          // of it, behind the ring: segments, scratch, barriers (the last 512)
@@ -81,18 +82,19 @@ struct BlockLayout {
   static constexpr int kHalves = kDim / 128;            // 128-byte swizzle rows of a cache row
   static constexpr int kC = kNR / 2;                    // rows a softmax warpgroup owns
   static constexpr int kBoxes = 2 * kHalves;            // TMA boxes [64 tokens x 128 B] of a tile of K or V
-  static constexpr int kGroupBytes = kBoxes * 8192;     // a ring slot: one tile of K or of V
+  static constexpr int kSlotBytes = 16384;              // a ring slot: one half of a tile's two pages
   static constexpr int kPBufs = (kDim == 256 && kNR == 64) ? 1 : 2;
   static constexpr int kOffQ = 0;                       // q: kHalves boxes of [kNR hi rows, kNR lo rows][128 B]
   static constexpr int kOffP = 2 * kNR * kDim;          // weights: [128 tokens][kNR hi, kNR lo], 128-byte rows
   static constexpr int kOffRing = kOffP + kPBufs * 16384;
-  static constexpr int kGroups = (kBSmem - kBMisc - kOffRing) / kGroupBytes;
-  static constexpr int kOffMisc = kOffRing + kGroups * kGroupBytes;
+  static constexpr int kSlots = (kBSmem - kBMisc - kOffRing) / kSlotBytes;
+  static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;   // K and V have rings of their own
+  static constexpr int kOffMisc = kOffRing + kSlots * kSlotBytes;
   static constexpr uint32_t kTmemS = 0;                 // S^T, two buffers of kNR columns
   static constexpr uint32_t kTmemO = 2 * kNR;           // O^T, for each half kNR hi and kNR lo columns
   static constexpr uint32_t kTmemUsed = 2 * kNR * (1 + kHalves);
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static_assert(kTmemUsed <= 512 && kGroups >= 4 && kOffP % 1024 == 0 && kOffRing % 1024 == 0, "layout");
+  static_assert(kTmemUsed <= 512 && kKSlots >= 2 * kHalves && kOffP % 1024 == 0 && kOffRing % 1024 == 0, "layout");
 };
 
 struct BlockDecodeParams {
@@ -191,12 +193,124 @@ struct BlockTile {
   __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
 };
 
+// This CTA's segments, by one warp: {sequence, reader, first tile, end tile} and lengths into
+// shared memory, their number and their tiles into counts[0] and counts[1].
+__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, int4* seg, int* seg_len, int* counts) {
+  constexpr int kPer = 4, kChunk = 32 * kPer;   // sequences of a lane, of a round
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  auto lengths = [&](int c0, int (&L)[kPer]) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int b = c0 + lane * kPer + k;
+      L[k] = b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0;
+    }
+  };
+  int L0[kPer];
+  lengths(0, L0);
+  long long all = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L0[k]));
+  for (int c0 = kChunk; c0 < p.batch; c0 += kChunk) {
+    int L[kPer];
+    lengths(c0, L);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L[k]));
+  }
+  if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  const BlockCost cost = block_cost(all, p.readers);
+  const long long G = gridDim.x, g = blockIdx.x;
+  long long X0, X1;
+  int r0, r1;
+  if (cost.total <= 0xFFFFFFFFll / G) {   // (32-bit divisions take a third of the time)
+    const uint32_t C = static_cast<uint32_t>(cost.total), Gu = gridDim.x, gu = blockIdx.x;
+    X0 = gu * C / Gu;
+    X1 = (gu + 1) * C / Gu;
+    const uint32_t per = max(static_cast<uint32_t>(cost.per_reader), 1u);
+    r0 = static_cast<uint32_t>(X0) / per;
+    r1 = static_cast<uint32_t>(X1 - 1) / per;
+  } else {
+    X0 = g * cost.total / G;
+    X1 = (g + 1) * cost.total / G;
+    r0 = static_cast<int>(X0 / cost.per_reader);
+    r1 = static_cast<int>((X1 - 1) / cost.per_reader);
+  }
+  int nseg = 0, tiles = 0;
+  if (X0 < X1) {
+    for (int r = r0; r <= r1 && nseg <= kBMaxSeg; ++r) {
+      const long long rbase = r * cost.per_reader;
+      long long carry = 0;
+      for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kChunk) {
+        int L[kPer], lo[kPer], hi[kPer];
+        if (c0 == 0) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) L[k] = L0[k];
+        } else {
+          lengths(c0, L);
+        }
+        long long own = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) own += pack_tiles(block_tiles(L[k]));
+        long long incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        long long before = carry + incl - own;
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const long long base = rbase + cost_before(before);
+          const int T = block_tiles(L[k]);
+          lo[k] = first_tile_at(X0, base, T);
+          hi[k] = first_tile_at(X1, base, T);
+          count += lo[k] < hi[k] ? 1 : 0;
+          before += pack_tiles(T);
+        }
+        int at = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += x;
+        }
+        const int found = __shfl_sync(0xffffffffu, at, 31);
+        at += nseg - count;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (lo[k] < hi[k]) {
+            if (at < kBMaxSeg) {
+              seg[at] = make_int4(c0 + lane * kPer + k, r, lo[k], hi[k]);
+              seg_len[at] = L[k];
+            }
+            tiles += hi[k] - lo[k];
+            ++at;
+          }
+        }
+        nseg += found;
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (nseg > kBMaxSeg) {
+      if (lane == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
+      nseg = tiles = 0;
+    }
+  }
+  if (lane == 0) {
+    counts[0] = nseg;
+    counts[1] = tiles;
+  }
+}
+
 // ------------------------------------------------------------------ decode kernel
 template <int kDim, int kNR>
 __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   using Lay = BlockLayout<kDim, kNR>;
-  constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes, kGroups = Lay::kGroups;
-  constexpr int kPBufs = Lay::kPBufs;
+  constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes;
+  constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kPBufs = Lay::kPBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -211,28 +325,26 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
   float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
   float* alpha = neg_ref + 64;                                       // [64] what old sums are multiplied by
   float2* meta = reinterpret_cast<float2*>(alpha + 64);              // [kBMeta][2 pages][4 blocks] {K, V} scales
-  long long* scan = reinterpret_cast<long long*>(meta + 8 * kBMeta); // [16]
-  int* iscan = reinterpret_cast<int*>(scan + 16);                    // [16]
-  int* ctl = iscan + 16;                                             // tensor memory, abort flag, tiles of this CTA
+  int* ctl = reinterpret_cast<int*>(meta + 8 * kBMeta);              // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
   const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  constexpr int kFull = 0, kEmpty = kGroups, kSFull = 2 * kGroups, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                kQReady = kPvDone + 2, kQEmpty = kQReady + 1, kOEmpty = kQEmpty + 1, kDrain = kOEmpty + 1,
-                kMeta = kDrain + 1, kMetaEmpty = kMeta + kBMeta, kBars = kMetaEmpty + kBMeta;
+  // slots: K's, then V's
+  constexpr int kFull = 0, kEmpty = Lay::kSlots, kSFull = 2 * Lay::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
+                kPvDone = kPFull + 2, kQReady = kPvDone + 2, kOEmpty = kQReady + 1, kQEmpty = kOEmpty + 1,
+                kDrain = kQEmpty + 1, kMeta = kDrain + 1, kMetaEmpty = kMeta + kBMeta, kBars = kMetaEmpty + kBMeta;
   static_assert(kBars * 8 <= 512, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cap = p.max_pages * kBPage;
 
   if (warp == 0) {
     for (int i = lane; i < kBars; i += 32) {
-      // arrivals a phase: one for each box of a slot; one for each softmax warp; else one commit
-      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty || i >= kMetaEmpty;
-      mbar_init(bar(i), i < kEmpty ? kBoxes : by_warps ? kBSoftmaxWarps : 1);
+      // arrivals a phase: one for each page of a slot; one for each softmax warp; one for each
+      // MMA issuer (drain); else one
+      const bool by_warps = (i >= kSEmpty && i < kPvDone) || i == kQReady || i == kOEmpty || i >= kMetaEmpty;
+      mbar_init(bar(i), i < kEmpty || i == kDrain ? 2 : by_warps ? kBSoftmaxWarps : 1);
     }
-    if (lane == 0) {
-      ctl[1] = 0;
-      ctl[2] = 0;
-    }
+    if (lane == 0) ctl[1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -244,191 +356,106 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     row_off[row] = (tok * p.heads + row % p.group) * kDim;
     row_tok[row] = tok;
   }
-  if (tid == 64) {
+  if (tid == 32 * kBPvWarp) {
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
   // nothing that the preceding kernel may write is read before this; with early metadata the
-  // lengths and the block table are (the caller says that it does not write them)
+  // lengths are (the caller says that it does not write them)
   if (!p.early_metadata) grid_dep_wait();
-
-  // ---------------- this CTA's segments
-  const int cap = p.max_pages * kBPage;
-  int nseg = 0;
-  {
-    bool bad = false;
-    const int L0 = tid < p.batch ? clamp_len(p.seq_lens[tid], cap, bad) : 0;
-    long long mine = pack_tiles(block_tiles(L0));
-    for (int b = tid + kBThreads; b < p.batch; b += kBThreads)
-      mine += pack_tiles(block_tiles(clamp_len(p.seq_lens[b], cap, bad)));
-    if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
-    long long all = 0;
-    const long long incl = block_incl_scan<kBThreads, long long>(mine, scan, all);
-    const BlockCost cost = block_cost(all, p.readers);
-    const long long G = gridDim.x, g = blockIdx.x;
-    const long long X0 = g * cost.total / G, X1 = (g + 1) * cost.total / G;
-    if (X0 < X1) {
-      const int r0 = static_cast<int>(X0 / cost.per_reader), r1 = static_cast<int>((X1 - 1) / cost.per_reader);
-      for (int r = r0; r <= r1 && nseg <= kBMaxSeg; ++r) {
-        const long long rbase = r * cost.per_reader;
-        long long carry = 0;
-        for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kBThreads) {
-          const int b = c0 + tid;
-          bool again = false;
-          const int L = c0 == 0 ? L0 : (b < p.batch ? clamp_len(p.seq_lens[b], cap, again) : 0);
-          const int T = block_tiles(L);
-          const long long own = pack_tiles(T);
-          long long sum = all;
-          long long before = incl - own;
-          if (p.batch > kBThreads) before = block_incl_scan<kBThreads, long long>(own, scan, sum) - own + carry;
-          const long long base = rbase + cost_before(before);
-          const int lo = first_tile_at(X0, base, T), hi = first_tile_at(X1, base, T);
-          const int has = lo < hi ? 1 : 0;
-          int count = 0;
-          const int at = nseg + block_incl_scan<kBThreads>(has, iscan, count) - has;
-          if (has && at < kBMaxSeg) {
-            seg[at] = make_int4(b, r, lo, hi);
-            seg_len[at] = L;
-            atomicAdd(ctl + 2, hi - lo);
-          }
-          nseg += count;
-          carry += sum;
-        }
-      }
-      if (nseg > kBMaxSeg) {
-        if (tid == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
-        nseg = 0;
-      }
-    }
-  }
+  if (warp == 0) block_segments(p, cap, seg, seg_len, ctl + 2);
   __syncthreads();
   if (p.early_metadata) grid_dep_wait();
   grid_dep_launch();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
-  const int ntiles = nseg > 0 ? ctl[2] : 0;
-  // ring order of the tiles of K and V: K(0), K(1), V(0), K(2), V(1), ..., V(N - 1)
-  auto k_use = [&](int n) { return n == 0 ? 0 : 2 * n - 1; };
-  auto v_use = [&](int n) { return n == ntiles - 1 ? 2 * n + 1 : 2 * n + 2; };
+  const int nseg = ctl[2], ntiles = ctl[3];
 
   if (warp == 0) {
-    // ---------------- producer: lane i < kBoxes loads box i of each tile (half i / 2, page i % 2)
-    if (lane < kBoxes && ntiles > 0) {
-      const int half = lane >> 1, pg = lane & 1;
+    // ---------------- producer: lane i loads box i of each tile of K (i < kBoxes) or of V (half
+    // i / 2, page i % 2), each on its own as its slots free
+    if (lane < 2 * kBoxes && ntiles > 0) {
+      const bool is_v = lane >= kBoxes;
+      const int half = (lane % kBoxes) >> 1, pg = lane & 1;
+      const int slots = is_v ? kVSlots : kKSlots, slot0 = is_v ? kKSlots : 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
       BlockTile it;
       it.load(seg, seg_len, 0);
-      auto page_id = [&](const BlockTile& t) -> int {
-        return t.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(t.b) * p.max_pages + 2 * t.j + pg] : 0;
+      auto page_id = [&]() -> int {
+        return it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : 0;
       };
-      int id = page_id(it);
-      int z[2] = {0, 0}, rows[2] = {0, 0};   // (page, head) row of the pool and valid rows: this tile, the one before
-      bool keep[2] = {false, false};
+      int id = page_id();
+      int slot = half, phase = 0;   // (half < slots)
       bool ok = true;
-      int use = 0;
-      auto issue = [&](bool is_v, int w) {
-        const int slot = use % kGroups;
-        ok = wait_bar(bar(kEmpty + slot), ((use / kGroups) & 1) ^ 1, abort_flag);
-        if (!ok) return;
-        const uint32_t fb = bar(kFull + slot);
-        if (rows[w] <= 0) {
+      int n = 0;
+      for (; n < ntiles; ++n) {
+        const int rows = it.page_rows(pg);
+        int z = id * p.kv_heads + it.r / p.token_groups;
+        if (rows > 0 && (id < 0 || id >= p.num_blocks)) {
+          z = -1;   // outside the pool: the whole box reads as zeros
+          if (lane < 2) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
+        }
+        const uint64_t pol = it.r % p.token_groups != p.token_groups - 1 ? again : once;   // (another unit reads it next)
+        if (it.next(seg, seg_len, nseg)) id = page_id();
+        ok = wait_bar(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
+        if (!ok) break;
+        const uint32_t fb = bar(kFull + slot0 + slot);
+        if (rows <= 0) {
           mbar_arrive(fb);
         } else {
           // the last page's rows land at the end of the box: rows before them are filled with zeros
           mbar_arrive_expect_tx(fb, 8192);
-          tma_load_3d_hint(sbase + Lay::kOffRing + slot * Lay::kGroupBytes + (half * 2 + pg) * 8192,
-                           is_v ? &p.tm_v : &p.tm_k, fb, 128 * half, rows[w] - kBPage, z[w], keep[w] ? again : once);
+          tma_load_3d_hint(sbase + Lay::kOffRing + (slot0 + slot) * Lay::kSlotBytes + pg * 8192, is_v ? &p.tm_v : &p.tm_k,
+                           fb, 128 * half, rows - kBPage, z, pol);
         }
-        ++use;
-      };
-      for (int n = 0; n <= ntiles && ok; ++n) {
-        if (n < ntiles) {
-          const int w = n & 1;
-          rows[w] = it.page_rows(pg);
-          z[w] = id * p.kv_heads + it.r / p.token_groups;
-          if (rows[w] > 0 && (id < 0 || id >= p.num_blocks)) {
-            z[w] = -1;   // outside the pool: the whole box reads as zeros
-            if (half == 0) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
-          }
-          keep[w] = it.r % p.token_groups != p.token_groups - 1;   // another unit reads the page next
-          issue(false, w);
-          if (it.next(seg, seg_len, nseg)) id = page_id(it);
+        slot += kHalves;
+        if (slot >= slots) {
+          slot -= slots;
+          phase ^= 1;
         }
-        if (n >= 1 && ok) issue(true, (n - 1) & 1);
       }
       if (!ok) {
         atomicOr(p.status, MFA_DEV_TIMEOUT);
         // let every copy already issued land before the CTA can exit
-        for (int u = max(0, use - kGroups); u < use; ++u)
-          wait_slow(bar(kFull + u % kGroups), (u / kGroups) & 1, nullptr, kDrainLimitNs);
+        for (int u = max(half, (n - kVSlots) * kHalves + half); u < n * kHalves + half; u += kHalves)
+          wait_slow(bar(kFull + slot0 + u % slots), (u / slots) & 1, nullptr, kDrainLimitNs);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer: QK^T one tile ahead of PV
+    // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts into one accumulator
     if (lane == 0 && ntiles > 0) {
       constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, kNR);
-      constexpr uint32_t kIdescPV = idesc_e4m3(true, true, 128, 2 * kNR);
       bool ok = true;
-      BlockTile tk, tv;
-      tk.load(seg, seg_len, 0);
-      tv.load(seg, seg_len, 0);
-      int k_first = tk.j, v_first = tv.j;   // first tile of the current segment
-      auto qk = [&](int n) {
-        const int use = k_use(n), slot = use % kGroups;
-        if (tk.j == k_first) ok = wait_bar(bar(kQReady), tk.s & 1, abort_flag);
-        if (ok) ok = wait_bar(bar(kFull + slot), (use / kGroups) & 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t d = tmem + Lay::kTmemS + kNR * (n & 1);
-        const uint32_t a0 = sbase + Lay::kOffRing + slot * Lay::kGroupBytes;
-        const uint32_t b0 = sbase + Lay::kOffQ;
+      int slot = 0, phase = 0, n = 0;
+      for (int s = 0; s < nseg && ok; ++s) {
+        const int count = seg[s].w - seg[s].z;
+        ok = wait_bar(bar(kQReady), s & 1, abort_flag);
+        for (int i = 0; i < count && ok; ++i, ++n) {
+          if (n >= 2) ok = wait_bar(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
+          const uint32_t d = tmem + Lay::kTmemS + kNR * (n & 1);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h)
+          for (int h = 0; h < kHalves; ++h) {
+            if (ok) ok = wait_bar(bar(kFull + slot), phase, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc(sbase + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
+            const uint64_t bd = smem_desc(sbase + Lay::kOffQ + h * (2 * kNR * 128), 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = smem_desc(a0 + h * 16384 + 32 * kk, 16, 1024);
-            const uint32_t b = b0 + h * (2 * kNR * 128) + 32 * kk;
-            umma_f8_ss(d, ad, smem_desc(b, 16, 1024), kIdescQK, (h | kk) != 0);
-            umma_f8_ss(d, ad, smem_desc(b + kNR * 128, 16, 1024), kIdescQK, 1u);
+            for (int kk = 0; kk < 4; ++kk) {   // 32 elements a step: 2 in the descriptors' 16-byte units
+              umma_f8_ss(d, ad + 2 * kk, bd + 2 * kk, kIdescQK, (h | kk) != 0);
+              umma_f8_ss(d, ad + 2 * kk, bd + 2 * kk + kNR * 8, kIdescQK, 1u);
+            }
+            umma_commit(bar(kEmpty + slot));
+            if (++slot == kKSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
           }
-        umma_commit(bar(kEmpty + slot));
-        umma_commit(bar(kSFull + (n & 1)));
-        if (tk.j == tk.end - 1) umma_commit(bar(kQEmpty));
-        const int s = tk.s;
-        if (tk.next(seg, seg_len, nseg) && tk.s != s) k_first = tk.j;
-      };
-      auto pv = [&](int m) {
-        const int use = v_use(m), slot = use % kGroups;
-        const bool first = tv.j == v_first;
-        ok = wait_bar(bar(kPFull + m % kPBufs), (m / kPBufs) & 1, abort_flag);
-        if (ok && first && tv.s > 0) ok = wait_bar(bar(kOEmpty), (tv.s - 1) & 1, abort_flag);
-        if (ok) ok = wait_bar(bar(kFull + slot), (use / kGroups) & 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t a0 = sbase + Lay::kOffRing + slot * Lay::kGroupBytes;
-        const uint32_t b0 = sbase + Lay::kOffP + (m % kPBufs) * 16384;
-        for (int pg = 0; pg < 2; ++pg) {
-          if (tv.page_rows(pg) <= 0) break;
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              umma_f8_ss(tmem + Lay::kTmemO + 2 * kNR * h, smem_desc(a0 + (h * 2 + pg) * 8192 + 4096 * kk, 8192, 1024),
-                         smem_desc(b0 + pg * 8192 + 4096 * kk, 8192, 1024), kIdescPV, !(first && pg == 0 && kk == 0));
+          if (!ok) break;
+          umma_commit(bar(kSFull + (n & 1)));
+          if (i == count - 1) umma_commit(bar(kQEmpty));
         }
-        umma_commit(bar(kEmpty + slot));
-        umma_commit(bar(kPvDone + (m & 1)));
-        const int s = tv.s;
-        if (tv.next(seg, seg_len, nseg) && tv.s != s) v_first = tv.j;
-      };
-      for (int n = 0; n <= ntiles && ok; ++n) {
-        // a segment's first scores wait for its q, which is made after the last segment's
-        // weights: that segment's last PV goes first
-        const bool late = n >= 1 && n < ntiles && tk.j == k_first;
-        if (late) pv(n - 1);
-        if (ok && n < ntiles) qk(n);
-        if (ok && n >= 1 && !late) pv(n - 1);
       }
       if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
       // every MMA must be complete before tensor memory is released
@@ -436,7 +463,46 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
     }
     __syncwarp();
-  } else if (warp == kBThreads / 32 - 1) {
+  } else if (warp == kBPvWarp) {
+    // ---------------- PV issuer: O^T += V^T P^T, the weights' hi and lo parts in columns of their own
+    if (lane == 0 && ntiles > 0) {
+      constexpr uint32_t kIdescPV = idesc_e4m3(true, true, 128, 2 * kNR);
+      bool ok = true;
+      int slot = 0, phase = 0, n = 0;
+      for (int s = 0; s < nseg && ok; ++s) {
+        const int4 sg = seg[s];
+        const int L = seg_len[s];
+        for (int j = sg.z; j < sg.w && ok; ++j, ++n) {
+          ok = wait_bar(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag);
+          if (ok && j == sg.z && s > 0) ok = wait_bar(bar(kOEmpty), (s - 1) & 1, abort_flag);
+          const bool both = L > kBTile * j + kBPage;   // the tile has its second page
+          const uint64_t bd = smem_desc(sbase + Lay::kOffP + (n % kPBufs) * 16384, 8192, 1024);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            if (ok) ok = wait_bar(bar(kFull + kKSlots + slot), phase, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = smem_desc(sbase + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
+            const uint32_t d = tmem + Lay::kTmemO + 2 * kNR * h;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
+              if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == sg.z && kk == 0));
+            umma_commit(bar(kEmpty + kKSlots + slot));
+            if (++slot == kVSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          umma_commit(bar(kPvDone + (n & 1)));
+        }
+      }
+      if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
+      umma_commit(bar(kDrain));
+      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == kBScaleWarp) {
     // ---------------- scales: a tile's up to 2 x 4 block scales of K and of V, ahead of the softmax
     // (lane = V? page, block); page ids two tiles ahead, scales one tile ahead
     const int pg = (lane >> 2) & 1, blk = lane & 3;
@@ -500,18 +566,6 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     const uint32_t vote_bar = 1 + wg;
     const bool f32 = p.out_f32 != 0;
 
-    // sequences without tokens: zeros and -inf, in turn over the CTAs
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-      bool dummy = false;
-      if (clamp_len(p.seq_lens[b], cap, dummy) != 0) continue;
-      const size_t n = static_cast<size_t>(p.tokens) * p.heads, at = static_cast<size_t>(b) * n;
-      const size_t chunks = n * kDim * (f32 ? 4 : 2) / 16;
-      uint4* o = static_cast<uint4*>(p.out) + at * kDim * (f32 ? 4 : 2) / 16;
-      for (size_t i = tid - 64; i < chunks; i += 32 * kBSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
-      if (p.lse != nullptr)
-        for (size_t i = tid - 64; i < n; i += 32 * kBSoftmaxWarps) p.lse[at + i] = -INFINITY;
-    }
-
     // A wait that gives up raises the CTA's abort flag; a warpgroup leaves its loops together,
     // by a vote, so that its barriers stay in step.
     bool aborted = false, stop = false;
@@ -570,15 +624,17 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       const int L = seg_len[s];
       const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
       const int seen0 = L - (p.tokens - 1) + tg * p.unit_tokens;   // tokens that the unit's first row sees
-      uint64_t l2[kC / 2];   // row sums over this lane's tokens: pairs of rows
+      uint64_t l2[kC / 2], nm2[kC / 2];   // row sums over this lane's tokens, minus the references: pairs of rows
 #pragma unroll
-      for (int i = 0; i < kC / 2; ++i) l2[i] = 0;
+      for (int i = 0; i < kC / 2; ++i) {
+        l2[i] = 0;
+        nm2[i] = pack_f32x2(INFINITY, INFINITY);
+      }
       if (row < kC) neg_ref[c0 + row] = INFINITY;
       int e_ref = kBEMin;
       if (!aborted && !wait_warp(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
-      const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(neg_ref + c0);
       for (int j = sg.z; j < sg.w; ++j, ++n) {
         const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
         const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
@@ -598,9 +654,9 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             tmem_ld_wait(sr);
 #pragma unroll
             for (int i = 0; i < kC / 2; i += 2) {
-              const ulonglong2 w = w4[i / 2], m = m4[i / 2];
-              x2[i] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), mul_f32x2(a2, w.x), m.x);
-              x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), m.y);
+              const ulonglong2 w = w4[i / 2];
+              x2[i] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), mul_f32x2(a2, w.x), nm2[i]);
+              x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), nm2[i + 1]);
             }
           }
           if (kBTile * (j + 1) > seen0) {   // some row does not see some token of the tile
@@ -626,19 +682,26 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             break;
           }
           // ---- new references: each row's largest score so far, the largest value scale's
-          // exponent; the sums and O move to them.  Rare after a segment's first tile: eight rows
-          // at a time, so that the code stays small.
-#pragma unroll 1
-          for (int c = 0; c < kC; c += 8) {
-            uint32_t sr[8];
-            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + c + lane_base, sr);
+          // exponent; the sums and O move to them.  Rare after a segment's first tile.
+          {
+            uint32_t sr[kC];
+            float y[kC];
+            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
             tmem_ld_wait(sr);
-            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y[i] = t < seen0 + row_tok[c0 + c + i] ? __uint_as_float(sr[i]) * (sc.x * q_inv[(s & 1) * 64 + c0 + c + i]) : -INFINITY;
-            const float cmax = reduce_columns<8, true>(y);
-            if (lane % 4 == 0) my_red[quarter * kC + c + lane / 4] = cmax;
+            for (int i = 0; i < kC; i += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + i);
+              y[i] = __uint_as_float(sr[i]) * (sc.x * w.x);
+              y[i + 1] = __uint_as_float(sr[i + 1]) * (sc.x * w.y);
+              y[i + 2] = __uint_as_float(sr[i + 2]) * (sc.x * w.z);
+              y[i + 3] = __uint_as_float(sr[i + 3]) * (sc.x * w.w);
+            }
+            if (kBTile * (j + 1) > seen0) {
+#pragma unroll
+              for (int i = 0; i < kC; ++i) y[i] = t < seen0 + row_tok[c0 + i] ? y[i] : -INFINITY;
+            }
+            const float cmax = reduce_columns<kC, true>(y);
+            if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
           }
           const int emax = __reduce_max_sync(0xffffffffu, ev);
           if (lane == 0) my_red_e[quarter] = emax;
@@ -660,27 +723,40 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(alpha + c0 + 2 * i);
             l2[i] = mul_f32x2(l2[i], f.x);
             l2[i + 1] = mul_f32x2(l2[i + 1], f.y);
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + 2 * i);
+            nm2[i] = m.x;
+            nm2[i + 1] = m.y;
           }
           if (j > sg.z) {   // O holds something
             if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
             o_ready = true;
             tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < 2 * kHalves; ++h)   // halves x (hi, lo)
-#pragma unroll 1
-              for (int c = 0; c < kC; c += 8) {
-                uint32_t o[8];
-                const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + c + lane_base;
-                tmem_ld(at, o);
-                tmem_ld_wait(o);
+            for (int h = 0; h < 2 * kHalves; ++h) {   // halves x (hi, lo)
+              uint32_t o[kC];
+              const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + lane_base;
+              tmem_ld(at, o);
+              tmem_ld_wait(o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (alpha[c0 + c + i] * eshift));
-                tmem_st(at, o);
+              for (int i = 0; i < kC; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
+                o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
+                o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
+                o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
               }
+              tmem_st(at, o);
+            }
             tmem_st_wait();
           }
         }
         if (stop) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kSEmpty + (n & 1)));
+          mbar_arrive(bar(kMetaEmpty + n % kBMeta));
+        }
         // weights p = 2^x, their sums in fp32; and P = p s_v 2^-E, rounded to f16 twice (2^-11 each)
         // and split into e4m3 parts P = hi + lo / 16: each part keeps four bits, and the lo part's
         // own accumulator lets it be 16 times larger, so that the smallest step is 2^-13 of the
@@ -731,10 +807,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         tc_fence_before();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kPFull + n % kPBufs));
-          mbar_arrive(bar(kMetaEmpty + n % kBMeta));
-        }
+        if (lane == 0) mbar_arrive(bar(kPFull + n % kPBufs));
       }
       if (stop) break;
       if (s + 1 < nseg) convert_q(s + 1);
@@ -771,7 +844,11 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           }
         }
         named_bar_sync(vote_bar, 128);
-#pragma unroll
+        // rows of a part, or of one new token, lie one after the other; else each has its place
+        const bool in_line = !whole || p.unit_tokens == 1;
+        float* dst32 = whole ? static_cast<float*>(p.out) + first * kDim : p.part_o + slot * p.rows * kDim;
+        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.out) + first * kDim;
+#pragma unroll 1
         for (int h = 0; h < kHalves; ++h) {
           uint32_t o[kC], o2[kC];
           const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c0 + lane_base;
@@ -784,21 +861,48 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
           }
-          const int col = 128 * h + row;
 #pragma unroll
-          for (int i = 0; i < kC; ++i) {
-            if (c0 + i < valid) {
-              const float v = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * alpha[c0 + i];
-              if (!whole)
-                p.part_o[(slot * p.rows + c0 + i) * kDim + col] = v;
-              else if (f32)
-                static_cast<float*>(p.out)[first * kDim + row_off[c0 + i] + col] = v;
+          for (int i = 0; i < kC; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * f.x);
+            o[i + 1] = __float_as_uint(fmaf(__uint_as_float(o2[i + 1]), 0.0625f, __uint_as_float(o[i + 1])) * f.y);
+            o[i + 2] = __float_as_uint(fmaf(__uint_as_float(o2[i + 2]), 0.0625f, __uint_as_float(o[i + 2])) * f.z);
+            o[i + 3] = __float_as_uint(fmaf(__uint_as_float(o2[i + 3]), 0.0625f, __uint_as_float(o[i + 3])) * f.w);
+          }
+          const int col = 128 * h + row;
+          if (in_line && (!whole || f32)) {
+            float* d = dst32 + c0 * kDim + col;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+              if (c0 + i < valid) d[i * kDim] = __uint_as_float(o[i]);
+          } else if (in_line) {
+            __nv_bfloat16* d = dst16 + c0 * kDim + col;
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+              if (c0 + i < valid) d[i * kDim] = __float2bfloat16_rn(__uint_as_float(o[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+              if (c0 + i >= valid) continue;
+              if (f32)
+                dst32[row_off[c0 + i] + col] = __uint_as_float(o[i]);
               else
-                static_cast<__nv_bfloat16*>(p.out)[first * kDim + row_off[c0 + i] + col] = __float2bfloat16_rn(v);
+                dst16[row_off[c0 + i] + col] = __float2bfloat16_rn(__uint_as_float(o[i]));
             }
           }
         }
       }
+    }
+    // sequences without tokens: zeros and -inf, in turn over the CTAs
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      bool dummy = false;
+      if (clamp_len(p.seq_lens[b], cap, dummy) != 0) continue;
+      const size_t n = static_cast<size_t>(p.tokens) * p.heads, at = static_cast<size_t>(b) * n;
+      const size_t chunks = n * kDim * (f32 ? 4 : 2) / 16;
+      uint4* o = static_cast<uint4*>(p.out) + at * kDim * (f32 ? 4 : 2) / 16;
+      for (size_t i = tid - 64; i < chunks; i += 32 * kBSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr)
+        for (size_t i = tid - 64; i < n; i += 32 * kBSoftmaxWarps) p.lse[at + i] = -INFINITY;
     }
     if (stop && lane == 0) {
       *abort_flag = 1;
