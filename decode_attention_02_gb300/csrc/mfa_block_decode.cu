@@ -30,6 +30,7 @@ constexpr int kBTile = 128;           // tokens of a tile (two pages)
 constexpr int kBRows = 64;            // query rows (new tokens x heads of one group) a unit holds at most
 constexpr int kBCostTile = 4;         // schedule: cost of a tile
 constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's range
+constexpr int kBSwitchTiles = 5;      // plan: tiles that a second unit in a CTA's range is worth (see the plan)
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
 constexpr int kBThreads = 384;        // warps: producer, QK issuer, eight softmax, scales, PV issuer
@@ -37,8 +38,7 @@ constexpr int kBSoftmaxWarps = 8;
 constexpr int kBScaleWarp = 10, kBPvWarp = 11;
 constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
-constexpr int kBMisc = 9216;          // of it, behind the ring: segments, scratch, barriers (the last 512)
-constexpr int kBMeta = 4;             // tiles whose scales are held in shared memory
+constexpr int kBMisc = 10240;         // of it, behind the ring: segments, scratch, barriers (the last 512)
 // Weights p = 2^x, x a score (in powers of two) relative to its row's reference.  A value scale
 // s_v is folded into its token's weights as s_v 2^-E, E the segment's reference exponent.  The
 // references move when max(x, 0) + log2(s_v) - E passes 7 for some token and row, so that what
@@ -55,6 +55,7 @@ struct BlockShape {
   int token_groups;  // units along the new tokens
   int readers;    // units of a sequence
   int rows;       // rows of a unit (its last token group may use fewer)
+  int rows8;      // and padded to 8, as partial results are laid out
 };
 
 static BlockShape block_shape(const mfa_problem* pr) {
@@ -64,6 +65,7 @@ static BlockShape block_shape(const mfa_problem* pr) {
   s.token_groups = (pr->tokens_per_seq + s.unit_tokens - 1) / s.unit_tokens;
   s.readers = s.token_groups * pr->num_kv_heads;
   s.rows = s.group * s.unit_tokens;
+  s.rows8 = (s.rows + 7) / 8 * 8;
   return s;
 }
 
@@ -106,11 +108,13 @@ struct BlockDecodeParams {
   const int32_t* seq_lens;
   void* out;
   float* lse;
-  float* part_o;             // [partials][rows][d]
-  float* part_lse;           // [partials][rows]
+  float* part_o;             // [partials][rows8 / 8][d][8 rows]: 32 bytes a thread of the epilogue
+  float* part_lse;           // [partials][rows8]
   unsigned int* status;
   int batch, tokens, heads, kv_heads;
-  int group, unit_tokens, token_groups, readers, rows;   // BlockShape
+  int group, unit_tokens, token_groups, readers, rows8;   // BlockShape
+  int num_partials;
+  int quantum;               // even split: most tiles of a part, or -1 for whole units; 0: split by cost
   int log_scale;             // log2(scale_tokens)
   int max_pages, num_blocks;
   float scale_log2;          // softmax_scale * log2(e)
@@ -125,6 +129,15 @@ struct BlockDecodeParams {
 // base, and the next unit's base is 4 T + c further (T tiles, c = kBCostUnit for the boundary;
 // nothing for an empty sequence).  CTA g of G owns the tiles whose cost lies in
 // [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.
+//
+// Even split (chosen by the plan where the units are fewer than the CTAs and lengths allow):
+// each unit of T tiles is cut into ceil(T / quantum) parts as equal as they come (or not at
+// all), part i of unit (b, r) being item r P + P_b + i (P parts of one reader of every
+// sequence, P_b of those before b), and CTA g takes items g, g + G, ...: one part each, none
+// with the end of one unit and the beginning of another.
+__device__ __forceinline__ int even_parts(int T, int quantum) {
+  return quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
+}
 struct BlockCost {
   long long per_reader;   // cost of one reader of every sequence
   long long total;        // C
@@ -174,130 +187,114 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
 struct BlockTile {
   int s, j, end;      // segment, tile of the sequence, end of the segment
   int b, r, L;        // sequence, reader, length
-  __device__ __forceinline__ void load(const int4* seg, const int* seg_len, int at) {
+  __device__ __forceinline__ void load(const int4* seg, const int2* seg_more, int at) {
     const int4 x = seg[at];
     s = at;
     b = x.x;
     r = x.y;
     j = x.z;
     end = x.w;
-    L = seg_len[at];
+    L = seg_more[at].x;
   }
   // the next tile; false past the last
-  __device__ __forceinline__ bool next(const int4* seg, const int* seg_len, int nseg) {
+  __device__ __forceinline__ bool next(const int4* seg, const int2* seg_more, int nseg) {
     if (++j < end) return true;
     if (s + 1 >= nseg) return false;
-    load(seg, seg_len, s + 1);
+    load(seg, seg_more, s + 1);
     return true;
   }
   __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
 };
 
-// This CTA's segments, by one warp: {sequence, reader, first tile, end tile} and lengths into
-// shared memory, their number and their tiles into counts[0] and counts[1].
-__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, int4* seg, int* seg_len, int* counts) {
-  constexpr int kPer = 4, kChunk = 32 * kPer;   // sequences of a lane, of a round
+// floor(a / b), a and b >= 0 (the 32-bit division is several times shorter)
+__device__ __noinline__ long long div_floor(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// This CTA's segments, by one warp: {sequence, reader, first tile, end tile}, lengths and slots of
+// the partial results (-1: a whole unit) into shared memory, their number and their tiles into
+// counts[0] and counts[1].  The loops stay rolled: what a CTA runs once costs as much for its
+// instructions' fetch as for their work.
+__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, int4* seg, int2* seg_more, int* counts) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
-  auto lengths = [&](int c0, int (&L)[kPer]) {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int b = c0 + lane * kPer + k;
-      L[k] = b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0;
-    }
-  };
-  int L0[kPer];
-  lengths(0, L0);
-  long long all = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L0[k]));
-  for (int c0 = kChunk; c0 < p.batch; c0 += kChunk) {
-    int L[kPer];
-    lengths(c0, L);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L[k]));
-  }
+  auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
+  const bool even = p.quantum != 0;
+  // what is summed along the sequences: tiles and non-empty sequences, or parts
+  auto weight = [&](int T) { return even ? static_cast<long long>(even_parts(T, p.quantum)) : pack_tiles(T); };
+  const int L0 = length(lane);
+  long long all = weight(block_tiles(L0));
+#pragma unroll 1
+  for (int b = lane + 32; b < p.batch; b += 32) all += weight(block_tiles(length(b)));
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   const BlockCost cost = block_cost(all, p.readers);
   const long long G = gridDim.x, g = blockIdx.x;
-  long long X0, X1;
-  int r0, r1;
-  if (cost.total <= 0xFFFFFFFFll / G) {   // (32-bit divisions take a third of the time)
-    const uint32_t C = static_cast<uint32_t>(cost.total), Gu = gridDim.x, gu = blockIdx.x;
-    X0 = gu * C / Gu;
-    X1 = (gu + 1) * C / Gu;
-    const uint32_t per = max(static_cast<uint32_t>(cost.per_reader), 1u);
-    r0 = static_cast<uint32_t>(X0) / per;
-    r1 = static_cast<uint32_t>(X1 - 1) / per;
-  } else {
-    X0 = g * cost.total / G;
-    X1 = (g + 1) * cost.total / G;
-    r0 = static_cast<int>(X0 / cost.per_reader);
-    r1 = static_cast<int>((X1 - 1) / cost.per_reader);
-  }
+  // [X0, X1): this CTA's costs, or items (one item a round of the grid); r0, r1: their readers
+  const long long span = even ? all * p.readers : cost.total, per = even ? all : cost.per_reader;
   int nseg = 0, tiles = 0;
-  if (X0 < X1) {
+  bool fits = !even || span <= p.num_partials;
+  long long round = 0;
+  do {
+    long long x = 0, y = 0;
+    if (lane < 2) {
+      x = even ? min(round + g + lane, span) : div_floor((g + lane) * span, G);
+      y = span > 0 ? div_floor(max(x - lane, 0ll), per) : 0;
+    }
+    const long long X0 = __shfl_sync(0xffffffffu, x, 0), X1 = __shfl_sync(0xffffffffu, x, 1);
+    const int r0 = __shfl_sync(0xffffffffu, static_cast<int>(y), 0), r1 = __shfl_sync(0xffffffffu, static_cast<int>(y), 1);
+    if (X0 >= X1) break;
+#pragma unroll 1
     for (int r = r0; r <= r1 && nseg <= kBMaxSeg; ++r) {
-      const long long rbase = r * cost.per_reader;
       long long carry = 0;
-      for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kChunk) {
-        int L[kPer], lo[kPer], hi[kPer];
-        if (c0 == 0) {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) L[k] = L0[k];
-        } else {
-          lengths(c0, L);
-        }
-        long long own = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) own += pack_tiles(block_tiles(L[k]));
+      const long long rbase = r * per;
+#pragma unroll 1
+      for (int c0 = 0; c0 < p.batch && rbase + (even ? carry : cost_before(carry)) < X1; c0 += 32) {
+        const int L = c0 == 0 ? L0 : length(c0 + lane);
+        const int T = block_tiles(L);
+        const long long own = weight(T);
         long long incl = own;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
         }
-        long long before = carry + incl - own;
-        int count = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
+        const long long before = carry + incl - own;
+        int lo, hi;
+        long long slot;
+        if (even) {
+          const long long i = X0 - rbase - before;   // the part, if it is this sequence's
+          const bool mine = i >= 0 && i < own;
+          lo = mine ? static_cast<int>(i * T / own) : 0;
+          hi = mine ? static_cast<int>((i + 1) * T / own) : 0;
+          slot = X0;
+        } else {
           const long long base = rbase + cost_before(before);
-          const int T = block_tiles(L[k]);
-          lo[k] = first_tile_at(X0, base, T);
-          hi[k] = first_tile_at(X1, base, T);
-          count += lo[k] < hi[k] ? 1 : 0;
-          before += pack_tiles(T);
+          lo = first_tile_at(X0, base, T);
+          hi = first_tile_at(X1, base, T);
+          slot = static_cast<long long>(r) * p.batch + c0 + lane + g;
         }
-        int at = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += x;
-        }
-        const int found = __shfl_sync(0xffffffffu, at, 31);
-        at += nseg - count;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (lo[k] < hi[k]) {
-            if (at < kBMaxSeg) {
-              seg[at] = make_int4(c0 + lane * kPer + k, r, lo[k], hi[k]);
-              seg_len[at] = L[k];
-            }
-            tiles += hi[k] - lo[k];
-            ++at;
+        const unsigned has = __ballot_sync(0xffffffffu, lo < hi);
+        const int at = nseg + __popc(has & ((1u << lane) - 1u));
+        if (lo < hi) {
+          if (at < kBMaxSeg) {
+            seg[at] = make_int4(c0 + lane, r, lo, hi);
+            seg_more[at] = make_int2(L, lo == 0 && hi == T ? -1 : static_cast<int>(slot));
           }
+          tiles += hi - lo;
         }
-        nseg += found;
+        nseg += __popc(has);
         carry += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
-    if (nseg > kBMaxSeg) {
-      if (lane == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
-      nseg = tiles = 0;
-    }
+    round += G;
+  } while (even && nseg <= kBMaxSeg);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  if (nseg > kBMaxSeg || !fits) {
+    if (lane == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
+    nseg = tiles = 0;
   }
   if (lane == 0) {
     counts[0] = nseg;
@@ -311,38 +308,40 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
   using Lay = BlockLayout<kDim, kNR>;
   constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes;
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kPBufs = Lay::kPBufs;
+  constexpr int kCh = kC < 16 ? kC : 16;   // rows at a time where the code is run seldom
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + Lay::kOffMisc;
   int4* seg = reinterpret_cast<int4*>(misc);                         // {sequence, reader, first tile, end tile}
-  int* seg_len = reinterpret_cast<int*>(misc + 16 * kBMaxSeg);
-  float* red = reinterpret_cast<float*>(misc + 20 * kBMaxSeg);       // [2 warpgroups][4 quarters][32]
+  int2* seg_more = reinterpret_cast<int2*>(misc + 16 * kBMaxSeg);    // {length, slot of the partial result or -1}
+  float* red = reinterpret_cast<float*>(misc + 24 * kBMaxSeg);       // [2 warpgroups][4 quarters][32]
   int* red_e = reinterpret_cast<int*>(red + 256);                    // [2][4]
   float* q_inv = reinterpret_cast<float*>(red_e + 8);                // [2 segments][64] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 128);                // [64] element offset of a row's output
   int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
   float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
   float* alpha = neg_ref + 64;                                       // [64] what old sums are multiplied by
-  float2* meta = reinterpret_cast<float2*>(alpha + 64);              // [kBMeta][2 pages][4 blocks] {K, V} scales
-  int* ctl = reinterpret_cast<int*>(meta + 8 * kBMeta);              // tensor memory, abort flag, segments, tiles
+  float2* meta = reinterpret_cast<float2*>(alpha + 64);              // [2 tiles][2 pages][4 blocks] {K, V} scales
+  int* ctl = reinterpret_cast<int*>(meta + 16);              // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
   const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // slots: K's, then V's
   constexpr int kFull = 0, kEmpty = Lay::kSlots, kSFull = 2 * Lay::kSlots, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2,
                 kPvDone = kPFull + 2, kQReady = kPvDone + 2, kOEmpty = kQReady + 1, kQEmpty = kOEmpty + 1,
-                kDrain = kQEmpty + 1, kMeta = kDrain + 1, kMetaEmpty = kMeta + kBMeta, kBars = kMetaEmpty + kBMeta;
+                kDrain = kQEmpty + 1, kBars = kDrain + 1;
   static_assert(kBars * 8 <= 512, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages * kBPage;
 
   if (warp == 0) {
     for (int i = lane; i < kBars; i += 32) {
-      // arrivals a phase: one for each page of a slot; one for each softmax warp; one for each
-      // MMA issuer (drain); else one
-      const bool by_warps = (i >= kSEmpty && i < kPvDone) || i == kQReady || i == kOEmpty || i >= kMetaEmpty;
-      mbar_init(bar(i), i < kEmpty || i == kDrain ? 2 : by_warps ? kBSoftmaxWarps : 1);
+      // arrivals a phase: one for each page of a slot; the QK issuer's and the scale warp's for a
+      // tile's scores; one for each softmax warp; one for each MMA issuer (drain); else one
+      const bool by_warps = (i >= kSEmpty && i < kPvDone) || i == kQReady || i == kOEmpty;
+      const bool by_two = i < kEmpty || i == kSFull || i == kSFull + 1 || i == kDrain;
+      mbar_init(bar(i), by_two ? 2 : by_warps ? kBSoftmaxWarps : 1);
     }
     if (lane == 0) ctl[1] = 0;
     fence_mbar_init();
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
   // nothing that the preceding kernel may write is read before this; with early metadata the
   // lengths are (the caller says that it does not write them)
   if (!p.early_metadata) grid_dep_wait();
-  if (warp == 0) block_segments(p, cap, seg, seg_len, ctl + 2);
+  if (warp == 0) block_segments(p, cap, seg, seg_more, ctl + 2);
   __syncthreads();
   if (p.early_metadata) grid_dep_wait();
   grid_dep_launch();
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       const int slots = is_v ? kVSlots : kKSlots, slot0 = is_v ? kKSlots : 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
       BlockTile it;
-      it.load(seg, seg_len, 0);
+      it.load(seg, seg_more, 0);
       auto page_id = [&]() -> int {
         return it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : 0;
       };
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           if (lane < 2) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
         }
         const uint64_t pol = it.r % p.token_groups != p.token_groups - 1 ? again : once;   // (another unit reads it next)
-        if (it.next(seg, seg_len, nseg)) id = page_id();
+        if (it.next(seg, seg_more, nseg)) id = page_id();
         ok = wait_bar(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
         if (!ok) break;
         const uint32_t fb = bar(kFull + slot0 + slot);
@@ -471,7 +470,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       int slot = 0, phase = 0, n = 0;
       for (int s = 0; s < nseg && ok; ++s) {
         const int4 sg = seg[s];
-        const int L = seg_len[s];
+        const int L = seg_more[s].x;
         for (int j = sg.z; j < sg.w && ok; ++j, ++n) {
           ok = wait_bar(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag);
           if (ok && j == sg.z && s > 0) ok = wait_bar(bar(kOEmpty), (s - 1) & 1, abort_flag);
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     const float mul = is_v ? 1.f : p.scale_log2;
     if (ntiles > 0) {
       BlockTile it;
-      it.load(seg, seg_len, 0);
+      it.load(seg, seg_more, 0);
       int kvh = it.r / p.token_groups;
       auto page_id = [&]() -> int {
         return mine && it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : -1;
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       };
       float value = scale_of(page_id());
       int s = 0;
-      bool more = it.next(seg, seg_len, nseg);
+      bool more = it.next(seg, seg_more, nseg);
       int id = more ? page_id() : -1;
       for (int n = 0; n < ntiles; ++n) {
         float value_next = 0.f;
@@ -538,16 +537,17 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 128));
           }
           value_next = scale_of(id);
-          more = it.next(seg, seg_len, nseg);
+          more = it.next(seg, seg_more, nseg);
           if (more) id = page_id();
         }
-        if (!wait_warp(bar(kMetaEmpty + n % kBMeta), ((n / kBMeta) & 1) ^ 1, abort_flag)) {
+        // the tile's scores and scales are read together: one barrier, one buffer each
+        if (n >= 2 && !wait_warp(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag)) {
           if (lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
           break;
         }
-        if (mine) reinterpret_cast<float*>(meta + (n % kBMeta) * 8 + pg * 4 + blk)[is_v ? 1 : 0] = value * mul;
+        if (mine) reinterpret_cast<float*>(meta + (n & 1) * 8 + pg * 4 + blk)[is_v ? 1 : 0] = value * mul;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kMeta + n % kBMeta));
+        if (lane == 0) mbar_arrive(bar(kSFull + (n & 1)));
         value = value_next;
       }
     }
@@ -566,51 +566,65 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     const uint32_t vote_bar = 1 + wg;
     const bool f32 = p.out_f32 != 0;
 
-    // A wait that gives up raises the CTA's abort flag; a warpgroup leaves its loops together,
-    // by a vote, so that its barriers stay in step.
+    // A wait that gives up raises the CTA's abort flag, and its warp waits no more; a warpgroup
+    // leaves together, by a vote at its segment's end, so that its barriers stay in step.
     bool aborted = false, stop = false;
     // q of a segment, split into e4m3 hi + lo parts under one power of two a row (split_e4m3):
-    // 8 elements a lane, a row a warp (d = 256) or half a warp (d = 128)
+    // eight lanes a row, four rows a warp at a time; lane i has the 8-element chunks i, i + 8, ...
     auto convert_q = [&](int sidx) {
-      constexpr int kRowsAtOnce = 256 / kDim;
-      constexpr int kRounds = kNR / (kBSoftmaxWarps * kRowsAtOnce);
+      constexpr int kRounds = (kNR + 4 * kBSoftmaxWarps - 1) / (4 * kBSoftmaxWarps), kChunks = kDim / 64;
       const int4 sg = seg[sidx];
       const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
       const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
       const __nv_bfloat16* src =
           p.q + ((static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group) * kDim;
-      const int e0 = (lane * 8) % kDim;            // first element of this lane
-      uint4 w[kRounds];
+      const int r0 = sw * 4 + (lane >> 3), i8 = lane & 7;
+      uint4 w[kRounds][kChunks];
 #pragma unroll
       for (int i = 0; i < kRounds; ++i) {
-        const int r = (i * kBSoftmaxWarps + sw) * kRowsAtOnce + lane * 8 / kDim;
-        w[i] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r] + e0)) : make_uint4(0, 0, 0, 0);
+        const int r = r0 + i * 4 * kBSoftmaxWarps;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+          w[i][k] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r]) + i8 + 8 * k) : make_uint4(0, 0, 0, 0);
       }
       // (the previous segment's last scores are made: its q is read no more)
       if (sidx > 0 && !aborted && !wait_warp(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < kRounds; ++i) {
-        const int r = (i * kBSoftmaxWarps + sw) * kRowsAtOnce + lane * 8 / kDim;
-        const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        const int r = r0 + i * 4 * kBSoftmaxWarps;
         float m = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+        for (int k = 0; k < kChunks; ++k) {
+          const uint32_t e[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
 #pragma unroll
-        for (int o = kDim / 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int x = 0; x < 4; ++x)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[x] << 16)), fabsf(__uint_as_float(e[x] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         int sig = 0;   // the row's largest |q| goes to [64, 128)
         if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
-        uint32_t hi[4], lo[4];
+        if (r < kNR) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          split_e4m3(__uint_as_float(e[k] << 16) * up, __uint_as_float(e[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
-        const int byte = e0 % 128;
-        uint8_t* dst = smem + Lay::kOffQ + (e0 / 128) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
-        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        if (e0 == 0)
-          q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
+          for (int k = 0; k < kChunks; ++k) {
+            const uint32_t e[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
+            const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
+            uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          }
+          if (i8 == 0) q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
+        }
+        // (a rolled loop over registers)
+#pragma unroll
+        for (int x = 0; x + 1 < kRounds; ++x)
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) w[x][k] = w[x + 1][k];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -621,7 +635,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     int n = 0;
     for (int s = 0; s < nseg && !stop; ++s) {
       const int4 sg = seg[s];
-      const int L = seg_len[s];
+      const int L = seg_more[s].x, slot = seg_more[s].y;
       const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
       const int seen0 = L - (p.tokens - 1) + tg * p.unit_tokens;   // tokens that the unit's first row sees
       uint64_t l2[kC / 2], nm2[kC / 2];   // row sums over this lane's tokens, minus the references: pairs of rows
@@ -638,17 +652,17 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       for (int j = sg.z; j < sg.w; ++j, ++n) {
         const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
         const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
-        if (!aborted && !wait_warp(bar(kMeta + n % kBMeta), (n / kBMeta) & 1, abort_flag)) aborted = true;
-        const float2 sc = pr >= 0 ? meta[(n % kBMeta) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
-        const uint64_t a2 = pack_f32x2(sc.x, sc.x);
-        const int ev = sc.y > 0.f ? static_cast<int>(__float_as_uint(sc.y) >> 23) - 127 : kBEMin;
         if (!aborted && !wait_warp(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
+        const float2 sc = pr >= 0 ? meta[(n & 1) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
+        const uint64_t a2 = pack_f32x2(sc.x, sc.x);
+        const int ev = sc.y > 0.f ? static_cast<int>(__float_as_uint(sc.y) >> 23) - 127 : kBEMin;
         uint64_t x2[kC / 2];
         bool o_ready = false;   // the previous tile's PV is known to be complete
-        for (bool settled = false;; settled = true) {
+        for (bool settled = false, first = j == sg.z;; settled = true) {
           // scores relative to the reference, in powers of two; -inf for what a row does not see
-          {
+          // (a segment's first tile has no reference yet)
+          if (settled || !first) {
             uint32_t sr[kC];
             tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
             tmem_ld_wait(sr);
@@ -659,7 +673,14 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
               x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), nm2[i + 1]);
             }
           }
-          if (kBTile * (j + 1) > seen0) {   // some row does not see some token of the tile
+          if (kBTile * (j + 1) <= seen0) {
+            // every row sees the whole tile
+          } else if (p.unit_tokens == 1) {
+            if (t >= seen0) {
+#pragma unroll
+              for (int i = 0; i < kC / 2; ++i) x2[i] = pack_f32x2(-INFINITY, -INFINITY);
+            }
+          } else {
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i) {
               float lo, hi;
@@ -669,28 +690,27 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             }
           }
           if (settled) break;
-          float top = -INFINITY;
+          if (!first) {
+            float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < kC / 2; ++i) {
-            float lo, hi;
-            unpack_f32x2(x2[i], lo, hi);
-            top = fmaxf(top, fmaxf(lo, hi));
-          }
-          if (!named_bar_or(vote_bar, 128, fmaxf(top, 0.f) + static_cast<float>(max(ev - e_ref, -kBMaxBelow)) > kBThreshold || aborted)) break;
-          if (named_bar_or(vote_bar, 128, aborted || *abort_flag)) {
-            stop = true;
-            break;
+            for (int i = 0; i < kC / 2; ++i) {
+              float lo, hi;
+              unpack_f32x2(x2[i], lo, hi);
+              top = fmaxf(top, fmaxf(lo, hi));
+            }
+            if (!named_bar_or(vote_bar, 128, top + static_cast<float>(max(ev - e_ref, -kBMaxBelow)) > kBThreshold)) break;
           }
           // ---- new references: each row's largest score so far, the largest value scale's
           // exponent; the sums and O move to them.  Rare after a segment's first tile.
-          {
-            uint32_t sr[kC];
-            float y[kC];
-            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
+#pragma unroll 1
+          for (int c = 0; c < kC; c += kCh) {
+            uint32_t sr[kCh];
+            float y[kCh];
+            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + c + lane_base, sr);
             tmem_ld_wait(sr);
 #pragma unroll
-            for (int i = 0; i < kC; i += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + i);
+            for (int i = 0; i < kCh; i += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + c + i);
               y[i] = __uint_as_float(sr[i]) * (sc.x * w.x);
               y[i + 1] = __uint_as_float(sr[i + 1]) * (sc.x * w.y);
               y[i + 2] = __uint_as_float(sr[i + 2]) * (sc.x * w.z);
@@ -698,10 +718,10 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             }
             if (kBTile * (j + 1) > seen0) {
 #pragma unroll
-              for (int i = 0; i < kC; ++i) y[i] = t < seen0 + row_tok[c0 + i] ? y[i] : -INFINITY;
+              for (int i = 0; i < kCh; ++i) y[i] = t < seen0 + row_tok[c0 + c + i] ? y[i] : -INFINITY;
             }
-            const float cmax = reduce_columns<kC, true>(y);
-            if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
+            const float cmax = reduce_columns<kCh, true>(y);
+            if (lane % (32 / kCh) == 0) my_red[quarter * kC + c + lane / (32 / kCh)] = cmax;
           }
           const int emax = __reduce_max_sync(0xffffffffu, ev);
           if (lane == 0) my_red_e[quarter] = emax;
@@ -733,30 +753,29 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             tc_fence_after();
 #pragma unroll 1
             for (int h = 0; h < 2 * kHalves; ++h) {   // halves x (hi, lo)
-              uint32_t o[kC];
-              const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + lane_base;
-              tmem_ld(at, o);
-              tmem_ld_wait(o);
+#pragma unroll 1
+              for (int c = 0; c < kC; c += kCh) {
+                uint32_t o[kCh];
+                const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + c + lane_base;
+                tmem_ld(at, o);
+                tmem_ld_wait(o);
 #pragma unroll
-              for (int i = 0; i < kC; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
-                o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
-                o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
-                o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
+                for (int i = 0; i < kCh; i += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + c + i);
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
+                  o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
+                  o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
+                  o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
+                }
+                tmem_st(at, o);
               }
-              tmem_st(at, o);
             }
             tmem_st_wait();
           }
         }
-        if (stop) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kSEmpty + (n & 1)));
-          mbar_arrive(bar(kMetaEmpty + n % kBMeta));
-        }
+        if (lane == 0) mbar_arrive(bar(kSEmpty + (n & 1)));
         // weights p = 2^x, their sums in fp32; and P = p s_v 2^-E, rounded to f16 twice (2^-11 each)
         // and split into e4m3 parts P = hi + lo / 16: each part keeps four bits, and the lo part's
         // own accumulator lets it be 16 times larger, so that the smallest step is 2^-13 of the
@@ -809,7 +828,6 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + n % kPBufs));
       }
-      if (stop) break;
       if (s + 1 < nseg) convert_q(s + 1);
 
       // ---------------- the segment's result
@@ -821,14 +839,13 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         named_bar_sync(vote_bar, 128);   // (the scratch may still be read from the last new reference)
         if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = lsum;
         if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
-        if (named_bar_or(vote_bar, 128, aborted)) {
+        if (named_bar_or(vote_bar, 128, aborted || *abort_flag)) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const bool whole = sg.z == 0 && sg.w == block_tiles(L);
+        const bool whole = slot < 0;
         const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-        const size_t slot = static_cast<size_t>(sg.y) * p.batch + sg.x + blockIdx.x;
         const size_t first = (static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group;
         const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
         if (row < kC) {
@@ -838,56 +855,49 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
           if (c0 + row < valid) {
             if (!whole)
-              p.part_lse[slot * p.rows + c0 + row] = v;
+              p.part_lse[static_cast<size_t>(slot) * p.rows8 + c0 + row] = v;
             else if (p.lse != nullptr)
               p.lse[first + row_off[c0 + row] / kDim] = v;
           }
         }
         named_bar_sync(vote_bar, 128);
-        // rows of a part, or of one new token, lie one after the other; else each has its place
-        const bool in_line = !whole || p.unit_tokens == 1;
-        float* dst32 = whole ? static_cast<float*>(p.out) + first * kDim : p.part_o + slot * p.rows * kDim;
-        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.out) + first * kDim;
+        // eight rows at a time.  A partial result keeps the accumulator's order, a thread's eight
+        // rows of one element side by side; bf16 outputs go out as pairs of elements, a lane and
+        // its neighbour exchanging a row each.
+        float* part = p.part_o + static_cast<size_t>(max(slot, 0)) * p.rows8 * kDim;
+        uint8_t* out = static_cast<uint8_t*>(p.out) + first * kDim * (f32 ? 4 : 2);
 #pragma unroll 1
-        for (int h = 0; h < kHalves; ++h) {
-          uint32_t o[kC], o2[kC];
-          const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c0 + lane_base;
+        for (int k = 0; k < kHalves * (kC / 8); ++k) {
+          const int h = k / (kC / 8), c = c0 + k % (kC / 8) * 8;
+          uint32_t o[8], o2[8];
+          const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c + lane_base;
           tmem_ld(at, o);
           tmem_ld(at + kNR, o2);
           tmem_ld_wait(o);
           tmem_ld_wait(o2);
-          if (h == kHalves - 1) {
+          if (k == kHalves * (kC / 8) - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
           }
-#pragma unroll
-          for (int i = 0; i < kC; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
-            o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * f.x);
-            o[i + 1] = __float_as_uint(fmaf(__uint_as_float(o2[i + 1]), 0.0625f, __uint_as_float(o[i + 1])) * f.y);
-            o[i + 2] = __float_as_uint(fmaf(__uint_as_float(o2[i + 2]), 0.0625f, __uint_as_float(o[i + 2])) * f.z);
-            o[i + 3] = __float_as_uint(fmaf(__uint_as_float(o2[i + 3]), 0.0625f, __uint_as_float(o[i + 3])) * f.w);
-          }
           const int col = 128 * h + row;
-          if (in_line && (!whole || f32)) {
-            float* d = dst32 + c0 * kDim + col;
+          float v[8];
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
-              if (c0 + i < valid) d[i * kDim] = __uint_as_float(o[i]);
-          } else if (in_line) {
-            __nv_bfloat16* d = dst16 + c0 * kDim + col;
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * alpha[c + i];
+          if (!whole) {
+            if (c < p.rows8) st_global_f32x8(part + (static_cast<size_t>(c >> 3) * kDim + col) * 8, v);
+          } else if (f32) {
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
-              if (c0 + i < valid) d[i * kDim] = __float2bfloat16_rn(__uint_as_float(o[i]));
+            for (int i = 0; i < 8; ++i)
+              if (c + i < valid) reinterpret_cast<float*>(out)[row_off[c + i] + col] = v[i];
           } else {
 #pragma unroll
-            for (int i = 0; i < kC; ++i) {
-              if (c0 + i >= valid) continue;
-              if (f32)
-                dst32[row_off[c0 + i] + col] = __uint_as_float(o[i]);
-              else
-                dst16[row_off[c0 + i] + col] = __float2bfloat16_rn(__uint_as_float(o[i]));
+            for (int i = 0; i < 8; i += 2) {
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+              const __nv_bfloat162 pair = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
+              const int r = c + i + (odd ? 1 : 0);
+              if (r < valid) *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(out) + row_off[r] + (col & ~1)) = pair;
             }
           }
         }
@@ -915,137 +925,161 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
 
 // ------------------------------------------------------------------ combine kernel
 //
-// Units that CTA boundaries cut: out = sum_s e^(lse_s - lse) O_s over the parts, with
-// lse = ln sum_s e^lse_s.  A row's d / 4 threads hold 4 elements each; kSplit such groups share
-// one row's parts (few rows, many parts) or take a row each (kSplit = 1).  The parts go by in
-// rounds of four with a running maximum, loads of a round together.
-template <int kDim, bool kSplit>
+// Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order.
+// A thread has eight rows of one element, as the parts hold them: one 32-byte load a part, four
+// parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or sixteen (d = 128); with many
+// parts a unit (kTeams = 4) it takes eight rows of 64 elements, its teams sharing the parts.
+template <int kDim, int kTeams>
 __global__ void __launch_bounds__(kBCombineThreads) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p,
                                                                              const int num_ctas) {
-  constexpr int kLanes = kDim / 4, kTeams = kBCombineThreads / kLanes;
+  constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
+  constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
   __shared__ long long scan[kBCombineThreads / 32];
   __shared__ long long s_before;
-  __shared__ __align__(16) float so[kSplit ? kTeams : 1][kSplit ? kDim : 4];
-  __shared__ float sm[kTeams], sl[kTeams];
-  const int tid = threadIdx.x, team = tid / kLanes, el = tid % kLanes;
+  __shared__ float s_lse[8 * kOcts];
+  __shared__ __align__(16) float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int team = tid / (kSlice * kOcts), oct = tid / kSlice % kOcts, el = blockIdx.z * kSlice + tid % kSlice;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
   // The decode kernel lets this one start once its own wait for what came before is over, so
   // the lengths are final here; what the decode writes is read after this kernel's wait.
   const int cap = p.max_pages * kBPage;
+  const bool even = p.quantum != 0;
   bool bad = false;
-  const int L = clamp_len(p.seq_lens[b], cap, bad);
-  if (L == 0) {
+  const int L = clamp_len(p.seq_lens[b], cap, bad), T = block_tiles(L);
+  if (L == 0 || (even && even_parts(T, p.quantum) == 1)) {   // nothing, or one part
     grid_dep_wait();
     grid_dep_launch();
     return;
   }
   long long carry = 0;
+#pragma unroll 1
   for (int c0 = 0; c0 < p.batch; c0 += kBCombineThreads) {
     const int i = c0 + tid;
-    const long long own = i < p.batch ? pack_tiles(block_tiles(clamp_len(p.seq_lens[i], cap, bad))) : 0;
+    const int Ti = i < p.batch ? block_tiles(clamp_len(p.seq_lens[i], cap, bad)) : 0;
+    const long long own = even ? even_parts(Ti, p.quantum) : pack_tiles(Ti);
     long long sum = 0;
     const long long before = block_incl_scan<kBCombineThreads, long long>(own, scan, sum) - own + carry;
     if (i == b) s_before = before;
     carry += sum;
   }
   __syncthreads();
-  const BlockCost cost = block_cost(carry, p.readers);
-  const long long base = r * cost.per_reader + cost_before(s_before), G = num_ctas;
-  const int T = block_tiles(L);
-  // the CTA of the tile at cost X: the largest g with floor(g C / G) <= X
-  auto owner = [&](long long X) {
-    long long g = X * G / cost.total;
-    while (g + 1 < G && (g + 1) * cost.total / G <= X) ++g;
-    while (g > 0 && g * cost.total / G > X) --g;
-    return static_cast<int>(g);
-  };
-  const int g0 = owner(base), g1 = owner(base + kBCostTile * static_cast<long long>(T - 1));
+  // the parts: slots first .. first + parts - 1
+  long long first_slot, base = 0, total = 0;
+  int parts, g0 = 0;
+  bool dense = true;
+  if (even) {
+    first_slot = r * carry + s_before;
+    parts = even_parts(T, p.quantum);
+  } else {
+    const BlockCost cost = block_cost(carry, p.readers);
+    total = cost.total;
+    base = r * cost.per_reader + cost_before(s_before);
+    // the CTA of the tile at cost X: the largest g with floor(g C / G) <= X
+    auto owner = [&](long long X) {
+      long long g = div_floor(X * num_ctas, total);
+      while (g + 1 < num_ctas && div_floor((g + 1) * total, num_ctas) <= X) ++g;
+      return static_cast<int>(g);
+    };
+    g0 = owner(base);
+    parts = owner(base + kBCostTile * static_cast<long long>(T - 1)) - g0 + 1;
+    first_slot = static_cast<long long>(pos) + g0;
+    dense = total >= kBCostTile * static_cast<long long>(num_ctas);   // every CTA inside the unit holds a tile of it
+  }
   grid_dep_wait();
   grid_dep_launch();
-  if (g0 == g1) return;   // one CTA had the whole unit
+  if (parts == 1 || first_slot + parts > p.num_partials) return;   // (past the plan: reported by the decode)
+  auto there = [&](int k) {   // (a CTA whose range lies between two tiles has no part)
+    return dense || first_tile_at(div_floor((g0 + k) * total, num_ctas), base, T) <
+                        first_tile_at(div_floor((g0 + k + 1) * total, num_ctas), base, T);
+  };
   const int tg = r % p.token_groups, kvh = r / p.token_groups;
   const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
   const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
-  const bool dense = cost.total >= kBCostTile * G;   // every CTA inside the unit holds a tile of it
-  constexpr int kRowStep = kSplit ? 1 : kTeams;
-  for (int row = blockIdx.y * kRowStep + (kSplit ? 0 : team); row < valid; row += gridDim.y * kRowStep) {
-    float M = -INFINITY, S = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int row0 = blockIdx.y * 8 * kOcts;   // this CTA's first row
+  // each row's lse: a warp a row
+#pragma unroll 1
+  for (int i = warp; i < 8 * kOcts; i += kBCombineThreads / 32) {
+    const int row = row0 + i;
+    float m = -INFINITY, l = 0.f;
+    if (row < valid) {
+      for (int k = lane; k < parts; k += 32)
+        if (there(k)) {
+          const float v = p.part_lse[(first_slot + k) * p.rows8 + row];
+          const float top = fmaxf(m, v);
+          l = v == -INFINITY ? l : l * (m == -INFINITY ? 0.f : expf(m - top)) + expf(v - top);
+          m = top;
+        }
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    l = l == 0.f ? 0.f : l * expf(m - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float v = l == 0.f ? -INFINITY : top + logf(l);
+    if (lane == 0) {
+      s_lse[i] = v;
+      if (row < valid && p.lse != nullptr && blockIdx.z == 0)
+        p.lse[first + static_cast<size_t>(row / p.group) * p.heads + row % p.group] = v;
+    }
+  }
+  __syncthreads();
+  float ref[8], acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    ref[i] = s_lse[8 * oct + i];
+    if (ref[i] == -INFINITY) ref[i] = 0.f;   // (a row that sees nothing: its parts weigh nothing)
+    acc[i] = 0.f;
+  }
+  if (row0 + 8 * oct < valid) {
+    const float* src = p.part_o + (static_cast<size_t>(row0 / 8 + oct) * kDim + el) * 8;
     constexpr int kRound = 4;
-    const int step = kSplit ? kTeams : 1;
-    for (int ga = g0 + (kSplit ? team : 0); ga <= g1; ga += kRound * step) {
-      float v[kRound];
-      float4 o[kRound];
+#pragma unroll 1
+    for (int k0 = team; k0 < parts; k0 += kRound * kTeams) {
+      float o[kRound][8], w[kRound][8];
 #pragma unroll
       for (int k = 0; k < kRound; ++k) {
-        const int gk = ga + k * step;
-        v[k] = -INFINITY;
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (gk <= g1) {
-          // a CTA whose range lies between two tiles has no part of the unit
-          if (dense || first_tile_at(gk * cost.total / G, base, T) < first_tile_at((gk + 1) * cost.total / G, base, T)) {
-            const size_t at = (static_cast<size_t>(pos) + gk) * p.rows + row;
-            v[k] = p.part_lse[at];
-            o[k] = reinterpret_cast<const float4*>(p.part_o + at * kDim)[el];
-          }
+        const int at = k0 + k * kTeams;
+        const bool have = at < parts && there(at);
+        const size_t slot = static_cast<size_t>(first_slot) + (have ? at : 0);
+        if (have) {
+          ld_global_f32x8(src + slot * p.rows8 * kDim, o[k]);
+          const float4* l4 = reinterpret_cast<const float4*>(p.part_lse + slot * p.rows8 + row0 + 8 * oct);
+          const float4 a = l4[0], c = l4[1];
+          w[k][0] = a.x, w[k][1] = a.y, w[k][2] = a.z, w[k][3] = a.w, w[k][4] = c.x, w[k][5] = c.y, w[k][6] = c.z, w[k][7] = c.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[k][i] = 0.f, w[k][i] = -INFINITY;
         }
       }
-      float top = M;
 #pragma unroll
-      for (int k = 0; k < kRound; ++k) top = fmaxf(top, v[k]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float al = M == -INFINITY ? 0.f : expf(M - ref);
-      M = top;
-      S *= al;
-      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+      for (int k = 0; k < kRound; ++k)
 #pragma unroll
-      for (int k = 0; k < kRound; ++k) {
-        const float w = v[k] == -INFINITY ? 0.f : expf(v[k] - ref);
-        S += w;
-        acc.x += w * o[k].x;
-        acc.y += w * o[k].y;
-        acc.z += w * o[k].z;
-        acc.w += w * o[k].w;
-      }
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(expf(w[k][i] - ref[i]), o[k][i], acc[i]);
     }
-    if constexpr (kSplit) {
-      *reinterpret_cast<float4*>(&so[team][4 * el]) = acc;
-      if (el == 0) {
-        sm[team] = M;
-        sl[team] = S;
-      }
-      __syncthreads();
-      float top = -INFINITY;
+  }
+  if constexpr (kTeams > 1) {
+    if (team > 0) {
 #pragma unroll
-      for (int k = 0; k < kTeams; ++k) top = fmaxf(top, sm[k]);
-      M = top;
-      S = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int k = 0; k < kTeams; ++k) {
-        const float w = sl[k] == 0.f ? 0.f : expf(sm[k] == -INFINITY ? 0.f : sm[k] - ref);
-        S += sl[k] * w;
-        const float4 o = *reinterpret_cast<const float4*>(&so[k][4 * el]);
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
-      }
-      __syncthreads();
+      for (int i = 0; i < 8; ++i) so[team - 1][tid % kSlice][i] = acc[i];
     }
-    if (kSplit && team != 0) continue;
-    const float inv = S == 0.f ? 0.f : 1.f / S;
-    const size_t at = first + static_cast<size_t>(row / p.group) * p.heads + row % p.group;
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int k = 0; k < kTeams - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += so[k][tid % kSlice][i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 8 * oct + i;
+    if (row >= valid) break;
+    const size_t at = (first + static_cast<size_t>(row / p.group) * p.heads + row % p.group) * kDim + el;
     if (p.out_f32)
-      reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kDim)[el] =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kDim)[el] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    }
-    if (el == 0 && p.lse != nullptr) p.lse[at] = S == 0.f ? -INFINITY : M + logf(S);
+      static_cast<float*>(p.out)[at] = acc[i];
+    else
+      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[i]);
   }
 }
 
@@ -1093,17 +1127,19 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   if (flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA)) return MFA_ERR_INVALID_ARG;
   const long long cap = static_cast<long long>(pr->max_pages_per_seq) * kBPage;
   const BlockShape sh = block_shape(pr);
-  long long tiles = 0, nonempty = 0;   // of one reader of each sequence
+  long long tiles = 0, nonempty = 0, longest = 0;   // tiles of one reader of each sequence
   if (host_seq_lens != nullptr) {
     for (int b = 0; b < pr->batch; ++b) {
       if (host_seq_lens[b] < 0 || host_seq_lens[b] > cap) return MFA_ERR_INVALID_ARG;
       tiles += (host_seq_lens[b] + kBTile - 1) / kBTile;
       nonempty += host_seq_lens[b] > 0;
+      longest = std::max<long long>(longest, (host_seq_lens[b] + kBTile - 1) / kBTile);
     }
   } else {
     if (max_seq_len < 0 || max_seq_len > cap) return MFA_ERR_INVALID_ARG;
     tiles = static_cast<long long>(pr->batch) * ((max_seq_len + kBTile - 1) / kBTile);
     nonempty = max_seq_len > 0 ? pr->batch : 0;
+    longest = (max_seq_len + kBTile - 1) / kBTile;
   }
   if (num_sms <= 0) {
     int dev = 0;
@@ -1120,20 +1156,48 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   const long long least = std::max(1ll, (C + share - 1) / share);
   long long G = force_ctas > 0 ? force_ctas : std::max(std::min<long long>(W, num_sms), least);
   if (G < least) return MFA_ERR_INVALID_ARG;
+  // Even split: the smallest quantum whose parts are no more than the CTAs, where every unit can
+  // have a CTA of its own.  It is taken where a CTA's part is not much longer than an equal
+  // share of the cost, since it spares the CTAs a second unit's beginning and end, worth about
+  // kBSwitchTiles tiles, and some or all of the combine.
+  int quantum = 0;
+  uint32_t mode = 0;
+  if (N > 0 && N <= G) {
+    auto parts_at = [&](long long q) {
+      long long parts = 0;
+      if (host_seq_lens != nullptr)
+        for (int b = 0; b < pr->batch; ++b) parts += ((host_seq_lens[b] + kBTile - 1) / kBTile + q - 1) / q;
+      else
+        parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
+      return parts * sh.readers;
+    };
+    long long lo = 1, hi = std::max(longest, 1ll);   // parts_at(hi) = N fits
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (parts_at(mid) <= G) hi = mid; else lo = mid + 1;
+    }
+    const long long share_tiles = (C + G * kBCostTile - 1) / (G * kBCostTile);
+    if (lo <= share_tiles + kBSwitchTiles) {
+      quantum = static_cast<int>(lo);
+      mode = lo >= longest ? MFA_PLAN_WHOLE_UNITS : MFA_PLAN_EVEN_SPLIT;
+      G = parts_at(lo);
+    }
+  }
   const long long partials = static_cast<long long>(pr->batch) * sh.readers + G - 1;
-  if (G > INT_MAX / 2 || partials > INT_MAX / 2 / sh.rows) return MFA_ERR_INVALID_ARG;
+  if (G > INT_MAX / 2 || partials > INT_MAX / 2 / sh.rows8 || W > INT_MAX) return MFA_ERR_INVALID_ARG;
   std::memset(plan, 0, sizeof(*plan));
   plan->num_ctas = static_cast<int32_t>(G);
   plan->tile_tokens = kBTile;
-  plan->max_tiles_per_cta = static_cast<int32_t>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
+  plan->max_tiles_per_cta = mode != 0 ? quantum
+                                      : static_cast<int32_t>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
   plan->num_partials = static_cast<int32_t>(partials);
   plan->batch = pr->batch;
   plan->tokens_per_seq = pr->tokens_per_seq;
   plan->kv_dtype = pr->kv_dtype;
-  plan->flags = flags;
+  plan->flags = flags | mode;
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
-  plan->workspace_bytes = block_workspace_bytes(partials, sh.rows, pr->head_dim);
+  plan->workspace_bytes = block_workspace_bytes(partials, sh.rows8, pr->head_dim);
   return MFA_OK;
 }
 
@@ -1147,9 +1211,10 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   if (plan == nullptr) return MFA_ERR_INVALID_ARG;
   const BlockShape sh = block_shape(pr);
   if (plan->batch != pr->batch || plan->kv_dtype != pr->kv_dtype || plan->tokens_per_seq != pr->tokens_per_seq ||
-      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA)) != 0 ||
+      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_WHOLE_UNITS)) != 0 ||
+      ((plan->flags & MFA_PLAN_EVEN_SPLIT) && plan->max_tiles_per_cta < 1) ||
       plan->num_partials != static_cast<long long>(pr->batch) * sh.readers + plan->num_ctas - 1 ||
-      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh.rows, pr->head_dim))
+      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh.rows8, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
@@ -1185,7 +1250,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.out = out;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
-  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh.rows, pr->head_dim));
+  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh.rows8, pr->head_dim));
   p.status = reinterpret_cast<unsigned int*>(ws);
   p.batch = pr->batch;
   p.tokens = pr->tokens_per_seq;
@@ -1195,7 +1260,9 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.unit_tokens = sh.unit_tokens;
   p.token_groups = sh.token_groups;
   p.readers = sh.readers;
-  p.rows = sh.rows;
+  p.rows8 = sh.rows8;
+  p.num_partials = plan->num_partials;
+  p.quantum = (plan->flags & MFA_PLAN_EVEN_SPLIT) ? plan->max_tiles_per_cta : (plan->flags & MFA_PLAN_WHOLE_UNITS) ? -1 : 0;
   p.log_scale = scale_tokens == 64 ? 6 : scale_tokens == 32 ? 5 : 4;
   p.max_pages = pr->max_pages_per_seq;
   p.num_blocks = pr->num_blocks;
@@ -1220,19 +1287,17 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, block_kernel_of(inst), p);
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
-  if (plan->num_ctas > 1) {
+  if (plan->num_ctas > 1 && p.quantum >= 0) {   // (whole units leave nothing to combine)
     const unsigned units = static_cast<unsigned>(pr->batch) * sh.readers;
-    const int teams = kBCombineThreads / (pr->head_dim / 4);
-    // about four CTAs an SM: with fewer rows than that a row is split over the CTA's teams
-    const bool split = static_cast<long long>(units) * sh.rows <= 4LL * plan->num_sms;
-    const int most = split ? sh.rows : (sh.rows + teams - 1) / teams;
-    const int want = static_cast<int>(std::max(1LL, (4LL * plan->num_sms + units - 1) / units));
-    cfg.gridDim = dim3(units, static_cast<unsigned>(std::min(most, want)), 1);
+    // many parts a unit: the CTAs of a row share them
+    const bool split = plan->num_ctas >= 8LL * units;
+    const int octs = split || pr->head_dim == 256 ? 1 : 2;
+    cfg.gridDim = dim3(units, static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 64 : 1);
     cfg.blockDim = dim3(kBCombineThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     const BlockCombineFn fn = pr->head_dim == 256
-                                  ? (split ? mfa_block_combine_kernel<256, true> : mfa_block_combine_kernel<256, false>)
-                                  : (split ? mfa_block_combine_kernel<128, true> : mfa_block_combine_kernel<128, false>);
+                                  ? (split ? mfa_block_combine_kernel<256, 4> : mfa_block_combine_kernel<256, 1>)
+                                  : (split ? mfa_block_combine_kernel<128, 4> : mfa_block_combine_kernel<128, 1>);
     e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(plan->num_ctas));
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }

@@ -95,6 +95,9 @@ typedef enum mfa_out_dtype {
  * once per decode step).  q, K, V, the new rows and all outputs are always ordered
  * after the preceding kernel. */
 #define MFA_PLAN_EARLY_METADATA 0x4u
+/* Set by mfa_block_decode_plan alone, in the plan: its way of splitting the work (see there). */
+#define MFA_PLAN_EVEN_SPLIT   0x100u
+#define MFA_PLAN_WHOLE_UNITS  0x200u
 
 typedef struct mfa_problem {
     int32_t batch;             /* B >= 0 sequences, one new query token each */
@@ -398,7 +401,9 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
  * arguments; MFA_PLAN_NO_COMBINE is refused).  The plan is for mfa_block_decode_run alone.
  * The work is split as there, by cost: 4 a tile of 128 tokens and 6 a boundary between units
  * (sequence, key/value head, and a group of the new tokens whose rows, tokens x query heads of
- * the head, are at most 64).  plan->max_tiles_per_cta bounds a CTA's tiles and is not limited.
+ * the head, are at most 64), or, where every unit can have a CTA, evenly: units whole
+ * (MFA_PLAN_WHOLE_UNITS) or in parts of at most max_tiles_per_cta tiles (MFA_PLAN_EVEN_SPLIT).
+ * force_ctas bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles and is not limited.
  */
 mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,

@@ -64,7 +64,7 @@ def test_problems_outside_the_cache_are_refused(lib, kw, block, code):
     (dict(), 64, 4),                                                       # 64 heads over one
     (dict(tokens_per_seq=3), 64, 12),                                      # each token a unit of its own
     (dict(num_kv_heads=4, head_dim=128, tokens_per_seq=4), 64, 16),        # 16 heads x 4 tokens in a unit
-    (dict(num_q_heads=40, num_kv_heads=8, head_dim=128), 5, 32),
+    (dict(num_q_heads=40, num_kv_heads=8, head_dim=128), 8, 32),           # 5 rows, padded to 8
     (dict(num_q_heads=24, num_kv_heads=1, tokens_per_seq=3), 48, 8),       # 2 + 1 tokens
 ])
 def test_plan_sizes(lib, kw, rows, units):
