@@ -33,12 +33,10 @@ constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's r
 constexpr int kBSwitchTiles = 5;      // plan: tiles that a second unit in a CTA's range is worth (see the plan)
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
-constexpr int kBThreads = 384;        // warps: producer, QK issuer, eight softmax, scales, PV issuer
-constexpr int kBSoftmaxWarps = 8;
-constexpr int kBScaleWarp = 10, kBPvWarp = 11;
+constexpr int kBScaleWarp = 2, kBPvWarp = 3, kBSoftmaxWarp0 = 4;   // warps: producer, QK issuer, scales, PV issuer, softmax
 constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
-constexpr int kBMisc = 10240;         // of it, behind the ring: segments, scratch, barriers (the last 512)
+constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scratch, barriers (the last 512)
 // Weights p = 2^x, x a score (in powers of two) relative to its row's reference.  A value scale
 // s_v is folded into its token's weights as s_v 2^-E, E the segment's reference exponent.  The
 // references move when max(x, 0) + log2(s_v) - E passes 7 for some token and row, so that what
@@ -69,12 +67,16 @@ static BlockShape block_shape(const mfa_problem* pr) {
   return s;
 }
 
-static uint64_t block_lse_offset(long long partials, int rows, int d) {
-  const uint64_t x = kBWsHeader + static_cast<uint64_t>(partials) * rows * d * 4;
+// Workspace: header; partial O; partial lse; and for each unit the slots of its first and last part.
+static uint64_t block_lse_offset(long long partials, const BlockShape& s, int d) {
+  const uint64_t x = kBWsHeader + static_cast<uint64_t>(partials) * s.rows8 * d * 4;
   return (x + 255) / 256 * 256;
 }
-static uint64_t block_workspace_bytes(long long partials, int rows, int d) {
-  return (block_lse_offset(partials, rows, d) + static_cast<uint64_t>(partials) * rows * 4 + 255) / 256 * 256;
+static uint64_t block_parts_offset(long long partials, const BlockShape& s, int d) {
+  return (block_lse_offset(partials, s, d) + static_cast<uint64_t>(partials) * s.rows8 * 4 + 255) / 256 * 256;
+}
+static uint64_t block_workspace_bytes(long long partials, const BlockShape& s, int batch, int d) {
+  return (block_parts_offset(partials, s, d) + static_cast<uint64_t>(batch) * s.readers * 8 + 255) / 256 * 256;
 }
 
 // Shared memory and tensor memory of an instance: kDim the head width, kNR the unit's rows
@@ -82,7 +84,10 @@ static uint64_t block_workspace_bytes(long long partials, int rows, int d) {
 template <int kDim, int kNR>
 struct BlockLayout {
   static constexpr int kHalves = kDim / 128;            // 128-byte swizzle rows of a cache row
-  static constexpr int kC = kNR / 2;                    // rows a softmax warpgroup owns
+  // softmax warpgroups: a tile's latency is what bounds them, so each owns no more than 16 rows
+  static constexpr int kWgs = kNR == 64 ? 4 : 2;
+  static constexpr int kC = kNR / kWgs;                 // rows a softmax warpgroup owns
+  static constexpr int kThreads = 32 * kBSoftmaxWarp0 + 128 * kWgs;
   static constexpr int kBoxes = 2 * kHalves;            // TMA boxes [64 tokens x 128 B] of a tile of K or V
   static constexpr int kSlotBytes = 16384;              // a ring slot: one half of a tile's two pages
   static constexpr int kPBufs = (kDim == 256 && kNR == 64) ? 1 : 2;
@@ -110,6 +115,7 @@ struct BlockDecodeParams {
   float* lse;
   float* part_o;             // [partials][rows8 / 8][d][8 rows]: 32 bytes a thread of the epilogue
   float* part_lse;           // [partials][rows8]
+  int2* parts;               // [units] slots of a unit's first and last part; -1: the output is written
   unsigned int* status;
   int batch, tokens, heads, kv_heads;
   int group, unit_tokens, token_groups, readers, rows8;   // BlockShape
@@ -136,7 +142,7 @@ struct BlockDecodeParams {
 // sequence, P_b of those before b), and CTA g takes items g, g + G, ...: one part each, none
 // with the end of one unit and the beginning of another.
 __device__ __forceinline__ int even_parts(int T, int quantum) {
-  return quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
+  return T <= quantum || quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
 }
 struct BlockCost {
   long long per_reader;   // cost of one reader of every sequence
@@ -162,6 +168,16 @@ __device__ __forceinline__ int first_tile_at(long long X, long long base, int T)
 }
 __device__ __forceinline__ int block_tiles(int L) { return (L + kBTile - 1) / kBTile; }
 
+// Bounded wait on an mbarrier phase; what runs when the phase is not over yet stays out of line.
+// False (after wait_bar's limit, or at once when the CTA is aborting): the caller carries on and
+// leaves at its next common exit.
+__device__ __noinline__ bool block_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return wait_bar(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool block_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || block_wait_slow(bar, parity, abort_flag);
+}
+
 // Reduce kC per-thread values over the 32 lanes: halving exchanges while values are left,
 // then whole exchanges of the last one.  Lane l ends with column l / (32 / kC).
 template <int kC, bool kMax>
@@ -183,114 +199,175 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
   return v[0];
 }
 
-// A role's place in its CTA's run of tiles.
-struct BlockTile {
-  int s, j, end;      // segment, tile of the sequence, end of the segment
-  int b, r, L;        // sequence, reader, length
-  __device__ __forceinline__ void load(const int4* seg, const int2* seg_more, int at) {
-    const int4 x = seg[at];
-    s = at;
-    b = x.x;
-    r = x.y;
-    j = x.z;
-    end = x.w;
-    L = seg_more[at].x;
-  }
-  // the next tile; false past the last
-  __device__ __forceinline__ bool next(const int4* seg, const int2* seg_more, int nseg) {
-    if (++j < end) return true;
-    if (s + 1 >= nseg) return false;
-    load(seg, seg_more, s + 1);
-    return true;
-  }
-  __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
-};
-
 // floor(a / b), a and b >= 0 (the 32-bit division is several times shorter)
 __device__ __noinline__ long long div_floor(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
 
-// This CTA's segments, by one warp: {sequence, reader, first tile, end tile}, lengths and slots of
-// the partial results (-1: a whole unit) into shared memory, their number and their tiles into
-// counts[0] and counts[1].  The loops stay rolled: what a CTA runs once costs as much for its
-// instructions' fetch as for their work.
-__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, int4* seg, int2* seg_more, int* counts) {
+// A segment: one unit's tiles of this CTA.
+struct __align__(16) BlockSegment {
+  int b, kvh, tg, L;       // sequence, key/value head, group of new tokens, length
+  int lo, hi;              // tiles
+  int slot;                // of the partial result; -1: the whole unit
+  int pos;                 // the unit's place in the schedule
+};
+
+// This CTA's segments, by one warp, into shared memory; their number and their tiles into counts[0]
+// and counts[1].  Lane l has four sequences of each 128, their lengths loaded together.  Rolled
+// loops where they can be: what a CTA runs once costs as much for its instructions' fetch as for
+// their work.
+__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
+  constexpr int kPer = 4, kChunk = 32 * kPer;
   const int lane = threadIdx.x & 31;
   bool bad = false;
-  auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
-  const bool even = p.quantum != 0;
-  // what is summed along the sequences: tiles and non-empty sequences, or parts
-  auto weight = [&](int T) { return even ? static_cast<long long>(even_parts(T, p.quantum)) : pack_tiles(T); };
-  const int L0 = length(lane);
-  long long all = weight(block_tiles(L0));
-#pragma unroll 1
-  for (int b = lane + 32; b < p.batch; b += 32) all += weight(block_tiles(length(b)));
-  if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const BlockCost cost = block_cost(all, p.readers);
-  const long long G = gridDim.x, g = blockIdx.x;
-  // [X0, X1): this CTA's costs, or items (one item a round of the grid); r0, r1: their readers
-  const long long span = even ? all * p.readers : cost.total, per = even ? all : cost.per_reader;
+  auto lengths = [&](int c0, int (&L)[kPer]) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int b = c0 + lane * kPer + k;
+      L[k] = b < p.batch ? p.seq_lens[b] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) L[k] = clamp_len(L[k], cap, bad);
+  };
+  auto add = [&](int at, int b, int r, int L, int lo, int hi, long long slot) {
+    if (at >= kBMaxSeg) return;
+    BlockSegment x;
+    x.b = b;
+    x.kvh = p.token_groups == 1 ? r : r / p.token_groups;
+    x.tg = r - x.kvh * p.token_groups;
+    x.L = L;
+    x.lo = lo;
+    x.hi = hi;
+    x.slot = lo == 0 && hi == block_tiles(L) ? -1 : static_cast<int>(slot);
+    x.pos = r * p.batch + b;
+    seg[at] = x;
+  };
+  const int G = gridDim.x, g = blockIdx.x;
+  int L[kPer];
+  lengths(0, L);
   int nseg = 0, tiles = 0;
-  bool fits = !even || span <= p.num_partials;
-  long long round = 0;
-  do {
+  bool fits = true;
+  if (p.quantum != 0) {
+    // even split: item g, g + G, ... of the units' parts
+    auto parts = [&](int x) { return even_parts(block_tiles(x), p.quantum); };
+    int all = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < p.batch; c0 += kChunk) {
+      if (c0 > 0) lengths(c0, L);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) all += parts(L[k]);
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    const long long items = static_cast<long long>(all) * p.readers;
+    fits = p.quantum < 0 || items <= p.num_partials;
+#pragma unroll 1
+    for (long long item = g; item < items && nseg <= kBMaxSeg; item += G) {
+      const int r = static_cast<int>(div_floor(item, all)), rem = static_cast<int>(item - static_cast<long long>(r) * all);
+      int carry = 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < p.batch && carry <= rem; c0 += kChunk) {
+        if (p.batch > kChunk) lengths(c0, L);
+        int own = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) own += parts(L[k]);
+        int incl = own;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        int i = rem - (carry + incl - own);   // the part, if it is one of this lane's sequences'
+        if (i >= 0 && i < own) {
+          int k = 0, len = L[0];
+#pragma unroll
+          for (int x = 0; x + 1 < kPer; ++x) {
+            const int n = parts(len);
+            if (k == x && i >= n) {
+              i -= n;
+              k = x + 1;
+              len = L[x + 1];
+            }
+          }
+          // part i of n: T / n tiles, the first T % n parts one more
+          const int T = block_tiles(len), n = parts(len), each = T / n, more = T - each * n;
+          const int lo = i * each + min(i, more), hi = lo + each + (i < more ? 1 : 0);
+          add(nseg, c0 + lane * kPer + k, r, len, lo, hi, item);
+          tiles += hi - lo;
+        }
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      ++nseg;
+    }
+  } else {
+    long long all = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < p.batch; c0 += kChunk) {
+      if (c0 > 0) lengths(c0, L);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L[k]));
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    const BlockCost cost = block_cost(all, p.readers);
+    // lane 0: the range's first cost, lane 1: its end; and the readers that hold them.  With less
+    // cost than a tile for each CTA the last CTAs have nothing: no CTA lies between two tiles.
+    const long long Ge = min(static_cast<long long>(G), max(cost.total / kBCostTile, 1ll));
     long long x = 0, y = 0;
     if (lane < 2) {
-      x = even ? min(round + g + lane, span) : div_floor((g + lane) * span, G);
-      y = span > 0 ? div_floor(max(x - lane, 0ll), per) : 0;
+      x = g + lane > Ge ? cost.total : div_floor((g + lane) * cost.total, Ge);
+      y = cost.total > 0 ? div_floor(max(x - lane, 0ll), cost.per_reader) : 0;
     }
     const long long X0 = __shfl_sync(0xffffffffu, x, 0), X1 = __shfl_sync(0xffffffffu, x, 1);
     const int r0 = __shfl_sync(0xffffffffu, static_cast<int>(y), 0), r1 = __shfl_sync(0xffffffffu, static_cast<int>(y), 1);
-    if (X0 >= X1) break;
 #pragma unroll 1
-    for (int r = r0; r <= r1 && nseg <= kBMaxSeg; ++r) {
+    for (int r = r0; X0 < X1 && r <= r1 && nseg <= kBMaxSeg; ++r) {
       long long carry = 0;
-      const long long rbase = r * per;
+      const long long rbase = r * cost.per_reader;
 #pragma unroll 1
-      for (int c0 = 0; c0 < p.batch && rbase + (even ? carry : cost_before(carry)) < X1; c0 += 32) {
-        const int L = c0 == 0 ? L0 : length(c0 + lane);
-        const int T = block_tiles(L);
-        const long long own = weight(T);
+      for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kChunk) {
+        if (p.batch > kChunk) lengths(c0, L);
+        long long own = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) own += pack_tiles(block_tiles(L[k]));
         long long incl = own;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += v;
         }
-        const long long before = carry + incl - own;
-        int lo, hi;
-        long long slot;
-        if (even) {
-          const long long i = X0 - rbase - before;   // the part, if it is this sequence's
-          const bool mine = i >= 0 && i < own;
-          lo = mine ? static_cast<int>(i * T / own) : 0;
-          hi = mine ? static_cast<int>((i + 1) * T / own) : 0;
-          slot = X0;
-        } else {
+        long long before = carry + incl - own;
+        int lo[kPer], hi[kPer], count = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
           const long long base = rbase + cost_before(before);
-          lo = first_tile_at(X0, base, T);
-          hi = first_tile_at(X1, base, T);
-          slot = static_cast<long long>(r) * p.batch + c0 + lane + g;
+          const int T = block_tiles(L[k]);
+          lo[k] = first_tile_at(X0, base, T);
+          hi[k] = first_tile_at(X1, base, T);
+          count += lo[k] < hi[k] ? 1 : 0;
+          before += pack_tiles(T);
         }
-        const unsigned has = __ballot_sync(0xffffffffu, lo < hi);
-        const int at = nseg + __popc(has & ((1u << lane) - 1u));
-        if (lo < hi) {
-          if (at < kBMaxSeg) {
-            seg[at] = make_int4(c0 + lane, r, lo, hi);
-            seg_more[at] = make_int2(L, lo == 0 && hi == T ? -1 : static_cast<int>(slot));
+        int at = count;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += v;
+        }
+        const int found = __shfl_sync(0xffffffffu, at, 31);
+        at += nseg - count;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (lo[k] < hi[k]) {
+            add(at++, c0 + lane * kPer + k, r, L[k], lo[k], hi[k], static_cast<long long>(r) * p.batch + c0 + lane * kPer + k + g);
+            tiles += hi[k] - lo[k];
           }
-          tiles += hi - lo;
         }
-        nseg += __popc(has);
+        nseg += found;
         carry += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    round += G;
-  } while (even && nseg <= kBMaxSeg);
+  }
+  if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   if (nseg > kBMaxSeg || !fits) {
     if (lane == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
@@ -302,22 +379,48 @@ __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int c
   }
 }
 
+// A role's place in its CTA's run of tiles.
+struct BlockTile {
+  int s, j, end;           // segment, tile of the sequence, end of the segment
+  int b, kvh, L;
+  bool again;              // another unit reads the tile's pages after this one
+  __device__ __forceinline__ void load(const BlockDecodeParams& p, const BlockSegment* seg, int at) {
+    const BlockSegment x = seg[at];
+    s = at;
+    b = x.b;
+    kvh = x.kvh;
+    L = x.L;
+    j = x.lo;
+    end = x.hi;
+    again = x.tg != p.token_groups - 1;
+  }
+  // the next tile; false past the last
+  __device__ __forceinline__ bool next(const BlockDecodeParams& p, const BlockSegment* seg, int nseg) {
+    if (++j < end) return true;
+    if (s + 1 >= nseg) return false;
+    load(p, seg, s + 1);
+    return true;
+  }
+  __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
+};
+
 // ------------------------------------------------------------------ decode kernel
 template <int kDim, int kNR>
-__global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+__global__ void __launch_bounds__(BlockLayout<kDim, kNR>::kThreads, 1)
+mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   using Lay = BlockLayout<kDim, kNR>;
   constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes;
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kPBufs = Lay::kPBufs;
-  constexpr int kCh = kC < 16 ? kC : 16;   // rows at a time where the code is run seldom
+  constexpr int kSoftmaxWarps = 4 * Lay::kWgs;
+  static_assert(kC == 8 || kC == 16 || kC == 32, "rows of a warpgroup");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + Lay::kOffMisc;
-  int4* seg = reinterpret_cast<int4*>(misc);                         // {sequence, reader, first tile, end tile}
-  int2* seg_more = reinterpret_cast<int2*>(misc + 16 * kBMaxSeg);    // {length, slot of the partial result or -1}
-  float* red = reinterpret_cast<float*>(misc + 24 * kBMaxSeg);       // [2 warpgroups][4 quarters][32]
-  int* red_e = reinterpret_cast<int*>(red + 256);                    // [2][4]
-  float* q_inv = reinterpret_cast<float*>(red_e + 8);                // [2 segments][64] what undoes a row's q scaling
+  BlockSegment* seg = reinterpret_cast<BlockSegment*>(misc);
+  float* red = reinterpret_cast<float*>(misc + sizeof(BlockSegment) * kBMaxSeg);   // [warpgroups][4 quarters][kC]
+  int* red_e = reinterpret_cast<int*>(red + 256);                    // [warpgroups][4]
+  float* q_inv = reinterpret_cast<float*>(red_e + 16);               // [2 segments][64] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 128);                // [64] element offset of a row's output
   int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
   float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
@@ -341,7 +444,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       // tile's scores; one for each softmax warp; one for each MMA issuer (drain); else one
       const bool by_warps = (i >= kSEmpty && i < kPvDone) || i == kQReady || i == kOEmpty;
       const bool by_two = i < kEmpty || i == kSFull || i == kSFull + 1 || i == kDrain;
-      mbar_init(bar(i), by_two ? 2 : by_warps ? kBSoftmaxWarps : 1);
+      mbar_init(bar(i), by_two ? 2 : by_warps ? kSoftmaxWarps : 1);
     }
     if (lane == 0) ctl[1] = 0;
     fence_mbar_init();
@@ -350,8 +453,8 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     tmem_alloc(smem_u32(ctl), Lay::kTmemCols);
     tmem_relinquish();
   }
-  if (tid >= 64 && tid < 64 + kNR) {
-    const int row = tid - 64, tok = row / p.group;
+  if (tid >= 32 * kBSoftmaxWarp0 && tid < 32 * kBSoftmaxWarp0 + kNR) {
+    const int row = tid - 32 * kBSoftmaxWarp0, tok = row / p.group;
     row_off[row] = (tok * p.heads + row % p.group) * kDim;
     row_tok[row] = tok;
   }
@@ -362,7 +465,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
   // nothing that the preceding kernel may write is read before this; with early metadata the
   // lengths are (the caller says that it does not write them)
   if (!p.early_metadata) grid_dep_wait();
-  if (warp == 0) block_segments(p, cap, seg, seg_more, ctl + 2);
+  if (warp == 0) block_segments(p, cap, seg, ctl + 2);
   __syncthreads();
   if (p.early_metadata) grid_dep_wait();
   grid_dep_launch();
@@ -379,7 +482,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       const int slots = is_v ? kVSlots : kKSlots, slot0 = is_v ? kKSlots : 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
       BlockTile it;
-      it.load(seg, seg_more, 0);
+      it.load(p, seg, 0);
       auto page_id = [&]() -> int {
         return it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : 0;
       };
@@ -387,16 +490,19 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       int slot = half, phase = 0;   // (half < slots)
       bool ok = true;
       int n = 0;
-      for (; n < ntiles; ++n) {
+      // V a round behind K: when every CTA fills its rings at once, the keys that all wait for
+      // come first
+      for (int round = is_v ? -1 : 0; n < ntiles; ++round) {
+        if (round < 0) continue;
         const int rows = it.page_rows(pg);
-        int z = id * p.kv_heads + it.r / p.token_groups;
+        int z = id * p.kv_heads + it.kvh;
         if (rows > 0 && (id < 0 || id >= p.num_blocks)) {
           z = -1;   // outside the pool: the whole box reads as zeros
           if (lane < 2) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
         }
-        const uint64_t pol = it.r % p.token_groups != p.token_groups - 1 ? again : once;   // (another unit reads it next)
-        if (it.next(seg, seg_more, nseg)) id = page_id();
-        ok = wait_bar(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
+        const uint64_t pol = it.again ? again : once;
+        if (it.next(p, seg, nseg)) id = page_id();
+        ok = block_wait(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
         if (!ok) break;
         const uint32_t fb = bar(kFull + slot0 + slot);
         if (rows <= 0) {
@@ -407,6 +513,7 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           tma_load_3d_hint(sbase + Lay::kOffRing + (slot0 + slot) * Lay::kSlotBytes + pg * 8192, is_v ? &p.tm_v : &p.tm_k,
                            fb, 128 * half, rows - kBPage, z, pol);
         }
+        ++n;
         slot += kHalves;
         if (slot >= slots) {
           slot -= slots;
@@ -428,14 +535,14 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
       for (int s = 0; s < nseg && ok; ++s) {
-        const int count = seg[s].w - seg[s].z;
-        ok = wait_bar(bar(kQReady), s & 1, abort_flag);
+        const int count = seg[s].hi - seg[s].lo;
+        ok = block_wait(bar(kQReady), s & 1, abort_flag);
         for (int i = 0; i < count && ok; ++i, ++n) {
-          if (n >= 2) ok = wait_bar(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
+          if (n >= 2) ok = block_wait(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
           const uint32_t d = tmem + Lay::kTmemS + kNR * (n & 1);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = wait_bar(bar(kFull + slot), phase, abort_flag);
+            if (ok) ok = block_wait(bar(kFull + slot), phase, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = smem_desc(sbase + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
@@ -469,23 +576,22 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
       for (int s = 0; s < nseg && ok; ++s) {
-        const int4 sg = seg[s];
-        const int L = seg_more[s].x;
-        for (int j = sg.z; j < sg.w && ok; ++j, ++n) {
-          ok = wait_bar(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag);
-          if (ok && j == sg.z && s > 0) ok = wait_bar(bar(kOEmpty), (s - 1) & 1, abort_flag);
+        const int lo = seg[s].lo, hi = seg[s].hi, L = seg[s].L;
+        for (int j = lo; j < hi && ok; ++j, ++n) {
+          ok = block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag);
+          if (ok && j == lo && s > 0) ok = block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag);
           const bool both = L > kBTile * j + kBPage;   // the tile has its second page
           const uint64_t bd = smem_desc(sbase + Lay::kOffP + (n % kPBufs) * 16384, 8192, 1024);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = wait_bar(bar(kFull + kKSlots + slot), phase, abort_flag);
+            if (ok) ok = block_wait(bar(kFull + kKSlots + slot), phase, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = smem_desc(sbase + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
             const uint32_t d = tmem + Lay::kTmemO + 2 * kNR * h;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
-              if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == sg.z && kk == 0));
+              if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == lo && kk == 0));
             umma_commit(bar(kEmpty + kKSlots + slot));
             if (++slot == kVSlots) {
               slot = 0;
@@ -510,38 +616,36 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     const float mul = is_v ? 1.f : p.scale_log2;
     if (ntiles > 0) {
       BlockTile it;
-      it.load(seg, seg_more, 0);
-      int kvh = it.r / p.token_groups;
+      it.load(p, seg, 0);
       auto page_id = [&]() -> int {
         return mine && it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : -1;
       };
       auto scale_of = [&](int id) -> float {
         if (id < 0 || id >= p.num_blocks) return 0.f;
-        return src[((static_cast<size_t>(id) * p.kv_heads + kvh) << (6 - p.log_scale)) + blk];
+        return src[((static_cast<size_t>(id) * p.kv_heads + it.kvh) << (6 - p.log_scale)) + blk];
       };
       float value = scale_of(page_id());
       int s = 0;
-      bool more = it.next(seg, seg_more, nseg);
+      bool more = it.next(p, seg, nseg);
       int id = more ? page_id() : -1;
       for (int n = 0; n < ntiles; ++n) {
         float value_next = 0.f;
         if (more) {
           if (it.s != s) {
             s = it.s;
-            kvh = it.r / p.token_groups;
             // the next segment's q, for its conversion to find in L2
             const char* q = reinterpret_cast<const char*>(
-                p.q + ((static_cast<size_t>(it.b) * p.tokens + (it.r % p.token_groups) * p.unit_tokens) * p.heads +
-                       static_cast<size_t>(kvh) * p.group) * kDim);
+                p.q + ((static_cast<size_t>(it.b) * p.tokens + seg[s].tg * p.unit_tokens) * p.heads +
+                       static_cast<size_t>(it.kvh) * p.group) * kDim);
             const int lines = p.group * kDim * 2 / 128;
             for (int i = lane; i < lines; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 128));
           }
           value_next = scale_of(id);
-          more = it.next(seg, seg_more, nseg);
+          more = it.next(p, seg, nseg);
           if (more) id = page_id();
         }
         // the tile's scores and scales are read together: one barrier, one buffer each
-        if (n >= 2 && !wait_warp(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag)) {
+        if (n >= 2 && !__all_sync(0xffffffffu, block_wait(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag))) {
           if (lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
           break;
         }
@@ -553,15 +657,15 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     }
     __syncwarp();
   } else {
-    // ---------------- softmax and epilogue: two warpgroups, each the whole tile (lane = token)
-    // for its kC rows
-    const int sw = warp - 2, wg = sw >> 2;
+    // ---------------- softmax and epilogue: each warpgroup has the whole tile (lane = token) for
+    // its kC rows
+    const int sw = warp - kBSoftmaxWarp0, wg = sw >> 2;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;          // token row of a tile; element of an O half
     const int pg = row >> 6, ri = row & 63;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const int c0 = wg * kC;                       // this warpgroup's first row
-    float* my_red = red + wg * 128;               // [4 quarters][kC]
+    float* my_red = red + wg * 4 * kC;            // [4 quarters][kC]
     int* my_red_e = red_e + wg * 4;
     const uint32_t vote_bar = 1 + wg;
     const bool f32 = p.out_f32 != 0;
@@ -572,59 +676,54 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     // q of a segment, split into e4m3 hi + lo parts under one power of two a row (split_e4m3):
     // eight lanes a row, four rows a warp at a time; lane i has the 8-element chunks i, i + 8, ...
     auto convert_q = [&](int sidx) {
-      constexpr int kRounds = (kNR + 4 * kBSoftmaxWarps - 1) / (4 * kBSoftmaxWarps), kChunks = kDim / 64;
-      const int4 sg = seg[sidx];
-      const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
-      const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-      const __nv_bfloat16* src =
-          p.q + ((static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group) * kDim;
+      constexpr int kChunks = kDim / 64, kRounds = (kNR + 4 * kSoftmaxWarps - 1) / (4 * kSoftmaxWarps);
+      const BlockSegment sg = seg[sidx];
+      const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
+      const __nv_bfloat16* src = p.q + ((static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads +
+                                        static_cast<size_t>(sg.kvh) * p.group) * kDim;
       const int r0 = sw * 4 + (lane >> 3), i8 = lane & 7;
-      uint4 w[kRounds][kChunks];
+      uint4 wr[kRounds][kChunks];
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int r = r0 + i * 4 * kBSoftmaxWarps;
+      for (int x = 0; x < kRounds; ++x) {
+        const int r = r0 + 4 * kSoftmaxWarps * x;
 #pragma unroll
         for (int k = 0; k < kChunks; ++k)
-          w[i][k] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r]) + i8 + 8 * k) : make_uint4(0, 0, 0, 0);
+          wr[x][k] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r]) + i8 + 8 * k) : make_uint4(0, 0, 0, 0);
       }
       // (the previous segment's last scores are made: its q is read no more)
-      if (sidx > 0 && !aborted && !wait_warp(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
-#pragma unroll 1
-      for (int i = 0; i < kRounds; ++i) {
-        const int r = r0 + i * 4 * kBSoftmaxWarps;
-        float m = 0.f;
+      if (sidx > 0 && !block_wait(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
+#pragma unroll
+      for (int x = 0; x < kRounds; ++x) {
+      const int r = r0 + 4 * kSoftmaxWarps * x;
+      const uint4(&w)[kChunks] = wr[x];
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t e[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[x] << 16)), fabsf(__uint_as_float(e[x] & 0xFFFF0000u))));
+      }
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      int sig = 0;   // the row's largest |q| goes to [64, 128)
+      if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
+      if (r < kNR) {
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-          const uint32_t e[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
+          const uint32_t e[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[x] << 16)), fabsf(__uint_as_float(e[x] & 0xFFFF0000u))));
+            split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
+          const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
+          uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
-#pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        int sig = 0;   // the row's largest |q| goes to [64, 128)
-        if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
-        if (r < kNR) {
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            const uint32_t e[4] = {w[0][k].x, w[0][k].y, w[0][k].z, w[0][k].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
-            const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
-            uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          }
-          if (i8 == 0) q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
-        }
-        // (a rolled loop over registers)
-#pragma unroll
-        for (int x = 0; x + 1 < kRounds; ++x)
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) w[x][k] = w[x + 1][k];
+        if (i8 == 0) q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
+      }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -634,10 +733,9 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
     if (ntiles > 0) convert_q(0);
     int n = 0;
     for (int s = 0; s < nseg && !stop; ++s) {
-      const int4 sg = seg[s];
-      const int L = seg_more[s].x, slot = seg_more[s].y;
-      const int tg = sg.y % p.token_groups, g = sg.y / p.token_groups;
-      const int seen0 = L - (p.tokens - 1) + tg * p.unit_tokens;   // tokens that the unit's first row sees
+      const BlockSegment sg = seg[s];
+      const int L = sg.L;
+      const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
       uint64_t l2[kC / 2], nm2[kC / 2];   // row sums over this lane's tokens, minus the references: pairs of rows
 #pragma unroll
       for (int i = 0; i < kC / 2; ++i) {
@@ -646,20 +744,20 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       }
       if (row < kC) neg_ref[c0 + row] = INFINITY;
       int e_ref = kBEMin;
-      if (!aborted && !wait_warp(bar(kQReady), s & 1, abort_flag)) aborted = true;
+      if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
-      for (int j = sg.z; j < sg.w; ++j, ++n) {
+      for (int j = sg.lo; j < sg.hi; ++j, ++n) {
         const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
         const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
-        if (!aborted && !wait_warp(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
+        if (!block_wait(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
         const float2 sc = pr >= 0 ? meta[(n & 1) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
         const uint64_t a2 = pack_f32x2(sc.x, sc.x);
         const int ev = sc.y > 0.f ? static_cast<int>(__float_as_uint(sc.y) >> 23) - 127 : kBEMin;
         uint64_t x2[kC / 2];
         bool o_ready = false;   // the previous tile's PV is known to be complete
-        for (bool settled = false, first = j == sg.z;; settled = true) {
+        for (bool settled = false, first = j == sg.lo;; settled = true) {
           // scores relative to the reference, in powers of two; -inf for what a row does not see
           // (a segment's first tile has no reference yet)
           if (settled || !first) {
@@ -702,15 +800,14 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           }
           // ---- new references: each row's largest score so far, the largest value scale's
           // exponent; the sums and O move to them.  Rare after a segment's first tile.
-#pragma unroll 1
-          for (int c = 0; c < kC; c += kCh) {
-            uint32_t sr[kCh];
-            float y[kCh];
-            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + c + lane_base, sr);
+          {
+            uint32_t sr[kC];
+            float y[kC];
+            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
             tmem_ld_wait(sr);
 #pragma unroll
-            for (int i = 0; i < kCh; i += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + c + i);
+            for (int i = 0; i < kC; i += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + i);
               y[i] = __uint_as_float(sr[i]) * (sc.x * w.x);
               y[i + 1] = __uint_as_float(sr[i + 1]) * (sc.x * w.y);
               y[i + 2] = __uint_as_float(sr[i + 2]) * (sc.x * w.z);
@@ -718,10 +815,10 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             }
             if (kBTile * (j + 1) > seen0) {
 #pragma unroll
-              for (int i = 0; i < kCh; ++i) y[i] = t < seen0 + row_tok[c0 + c + i] ? y[i] : -INFINITY;
+              for (int i = 0; i < kC; ++i) y[i] = t < seen0 + row_tok[c0 + i] ? y[i] : -INFINITY;
             }
-            const float cmax = reduce_columns<kCh, true>(y);
-            if (lane % (32 / kCh) == 0) my_red[quarter * kC + c + lane / (32 / kCh)] = cmax;
+            const float cmax = reduce_columns<kC, true>(y);
+            if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
           }
           const int emax = __reduce_max_sync(0xffffffffu, ev);
           if (lane == 0) my_red_e[quarter] = emax;
@@ -747,28 +844,25 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
             nm2[i] = m.x;
             nm2[i + 1] = m.y;
           }
-          if (j > sg.z) {   // O holds something
-            if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
+          if (j > sg.lo) {   // O holds something
+            if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
             o_ready = true;
             tc_fence_after();
 #pragma unroll 1
             for (int h = 0; h < 2 * kHalves; ++h) {   // halves x (hi, lo)
-#pragma unroll 1
-              for (int c = 0; c < kC; c += kCh) {
-                uint32_t o[kCh];
-                const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + c + lane_base;
-                tmem_ld(at, o);
-                tmem_ld_wait(o);
+              uint32_t o[kC];
+              const uint32_t at = tmem + Lay::kTmemO + kNR * h + c0 + lane_base;
+              tmem_ld(at, o);
+              tmem_ld_wait(o);
 #pragma unroll
-                for (int i = 0; i < kCh; i += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + c + i);
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
-                  o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
-                  o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
-                  o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
-                }
-                tmem_st(at, o);
+              for (int i = 0; i < kC; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
+                o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
+                o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
+                o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
               }
+              tmem_st(at, o);
             }
             tmem_st_wait();
           }
@@ -805,8 +899,8 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
           }
         }
         // the P buffer is free once the PV that read it is complete
-        if (n >= kPBufs && !(kPBufs == 1 && o_ready) && !aborted)
-          if (!wait_warp(bar(kPvDone + ((n - kPBufs) & 1)), ((n - kPBufs) >> 1) & 1, abort_flag)) aborted = true;
+        if (n >= kPBufs && !(kPBufs == 1 && o_ready))
+          if (!block_wait(bar(kPvDone + ((n - kPBufs) & 1)), ((n - kPBufs) >> 1) & 1, abort_flag)) aborted = true;
         {
           uint8_t* dst = smem + Lay::kOffP + (n % kPBufs) * 16384 + row * 128;
           const int sx = row & 7;
@@ -838,68 +932,80 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
         const float lsum = reduce_columns<kC, false>(l);
         named_bar_sync(vote_bar, 128);   // (the scratch may still be read from the last new reference)
         if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = lsum;
-        if (!aborted && !wait_warp(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
+        if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
         if (named_bar_or(vote_bar, 128, aborted || *abort_flag)) {
           stop = true;
           break;
         }
         tc_fence_after();
+        const int slot = sg.slot;
         const bool whole = slot < 0;
-        const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-        const size_t first = (static_cast<size_t>(sg.x) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(g) * p.group;
+        const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
+        const size_t first = (static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
         const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
-        if (row < kC) {
-          // (a row that sees nothing has no sum: zeros and -inf)
-          const float sum = my_red[row] + my_red[kC + row] + my_red[2 * kC + row] + my_red[3 * kC + row];
-          alpha[c0 + row] = sum == 0.f ? 0.f : back / sum;
-          const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
-          if (c0 + row < valid) {
-            if (!whole)
-              p.part_lse[static_cast<size_t>(slot) * p.rows8 + c0 + row] = v;
-            else if (p.lse != nullptr)
-              p.lse[first + row_off[c0 + row] / kDim] = v;
-          }
-        }
+        const int own = min(row, kC - 1);
+        const float sum = my_red[own] + my_red[kC + own] + my_red[2 * kC + own] + my_red[3 * kC + own];
+        if (row < kC) alpha[c0 + row] = sum == 0.f ? 0.f : __fdividef(back, sum);   // (a row that sees nothing: zeros)
         named_bar_sync(vote_bar, 128);
-        // eight rows at a time.  A partial result keeps the accumulator's order, a thread's eight
-        // rows of one element side by side; bf16 outputs go out as pairs of elements, a lane and
-        // its neighbour exchanging a row each.
+        // A partial result keeps the accumulator's order, a thread's eight rows of one element side
+        // by side; bf16 outputs go out as pairs of elements, a lane and its neighbour exchanging a
+        // row each.
         float* part = p.part_o + static_cast<size_t>(max(slot, 0)) * p.rows8 * kDim;
         uint8_t* out = static_cast<uint8_t*>(p.out) + first * kDim * (f32 ? 4 : 2);
 #pragma unroll 1
-        for (int k = 0; k < kHalves * (kC / 8); ++k) {
-          const int h = k / (kC / 8), c = c0 + k % (kC / 8) * 8;
-          uint32_t o[8], o2[8];
-          const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c + lane_base;
+        for (int h = 0; h < kHalves; ++h) {
+          uint32_t o[kC], o2[kC];
+          const uint32_t at = tmem + Lay::kTmemO + 2 * kNR * h + c0 + lane_base;
           tmem_ld(at, o);
           tmem_ld(at + kNR, o2);
           tmem_ld_wait(o);
           tmem_ld_wait(o2);
-          if (k == kHalves * (kC / 8) - 1) {
+          if (h == kHalves - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
           }
           const int col = 128 * h + row;
-          float v[8];
+          float v[kC];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * alpha[c + i];
+          for (int i = 0; i < kC; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
+            v[i] = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * f.x;
+            v[i + 1] = fmaf(__uint_as_float(o2[i + 1]), 0.0625f, __uint_as_float(o[i + 1])) * f.y;
+            v[i + 2] = fmaf(__uint_as_float(o2[i + 2]), 0.0625f, __uint_as_float(o[i + 2])) * f.z;
+            v[i + 3] = fmaf(__uint_as_float(o2[i + 3]), 0.0625f, __uint_as_float(o[i + 3])) * f.w;
+          }
           if (!whole) {
-            if (c < p.rows8) st_global_f32x8(part + (static_cast<size_t>(c >> 3) * kDim + col) * 8, v);
+#pragma unroll
+            for (int i = 0; i < kC; i += 8) {
+              const float v8[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
+              if (c0 + i < p.rows8) st_global_f32x8(part + (static_cast<size_t>((c0 + i) >> 3) * kDim + col) * 8, v8);
+            }
           } else if (f32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < valid) reinterpret_cast<float*>(out)[row_off[c + i] + col] = v[i];
+            for (int i = 0; i < kC; ++i)
+              if (c0 + i < valid) reinterpret_cast<float*>(out)[row_off[c0 + i] + col] = v[i];
           } else {
+            const bool odd = lane & 1;
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const bool odd = lane & 1;
+            for (int i = 0; i < kC; i += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
               const __nv_bfloat162 pair = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
-              const int r = c + i + (odd ? 1 : 0);
+              const int r = c0 + i + (odd ? 1 : 0);
               if (r < valid) *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(out) + row_off[r] + (col & ~1)) = pair;
             }
           }
+        }
+        if (row < kC && c0 + row < valid) {
+          const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
+          if (!whole)
+            p.part_lse[static_cast<size_t>(slot) * p.rows8 + c0 + row] = v;
+          else if (p.lse != nullptr)
+            p.lse[first + row_off[c0 + row] / kDim] = v;
+        }
+        if (sw == 0 && lane == 0) {   // for the combine
+          if (sg.lo == 0) p.parts[sg.pos].x = slot;
+          if (sg.hi == block_tiles(L)) p.parts[sg.pos].y = slot;
         }
       }
     }
@@ -910,9 +1016,10 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
       const size_t n = static_cast<size_t>(p.tokens) * p.heads, at = static_cast<size_t>(b) * n;
       const size_t chunks = n * kDim * (f32 ? 4 : 2) / 16;
       uint4* o = static_cast<uint4*>(p.out) + at * kDim * (f32 ? 4 : 2) / 16;
-      for (size_t i = tid - 64; i < chunks; i += 32 * kBSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
+      for (size_t i = tid - 32 * kBSoftmaxWarp0; i < chunks; i += 32 * kSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid - 32 * kBSoftmaxWarp0; i < p.readers; i += 32 * kSoftmaxWarps) p.parts[i * p.batch + b] = make_int2(-1, -1);
       if (p.lse != nullptr)
-        for (size_t i = tid - 64; i < n; i += 32 * kBSoftmaxWarps) p.lse[at + i] = -INFINITY;
+        for (size_t i = tid - 32 * kBSoftmaxWarp0; i < n; i += 32 * kSoftmaxWarps) p.lse[at + i] = -INFINITY;
     }
     if (stop && lane == 0) {
       *abort_flag = 1;
@@ -925,168 +1032,106 @@ __global__ void __launch_bounds__(kBThreads, 1) mfa_block_decode_kernel(const __
 
 // ------------------------------------------------------------------ combine kernel
 //
-// Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order.
-// A thread has eight rows of one element, as the parts hold them: one 32-byte load a part, four
-// parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or sixteen (d = 128); with many
-// parts a unit (kTeams = 4) it takes eight rows of 64 elements, its teams sharing the parts.
+// Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order,
+// with a running maximum.  A thread has eight rows of one element, as the parts hold them: one
+// 32-byte load a part, two parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or
+// sixteen (d = 128); with many parts a unit (kTeams = 8) it takes eight rows of 32 elements, its
+// teams sharing the parts.
 template <int kDim, int kTeams>
-__global__ void __launch_bounds__(kBCombineThreads) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p,
-                                                                             const int num_ctas) {
+__global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
   constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
-  __shared__ long long scan[kBCombineThreads / 32];
-  __shared__ long long s_before;
-  __shared__ float s_lse[8 * kOcts];
-  __shared__ __align__(16) float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
+  __shared__ float sm[kTeams > 1 ? kTeams - 1 : 1][8], sl[kTeams > 1 ? kTeams - 1 : 1][8];
+  const int tid = threadIdx.x;
   const int team = tid / (kSlice * kOcts), oct = tid / kSlice % kOcts, el = blockIdx.z * kSlice + tid % kSlice;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
-  // The decode kernel lets this one start once its own wait for what came before is over, so
-  // the lengths are final here; what the decode writes is read after this kernel's wait.
-  const int cap = p.max_pages * kBPage;
-  const bool even = p.quantum != 0;
-  bool bad = false;
-  const int L = clamp_len(p.seq_lens[b], cap, bad), T = block_tiles(L);
-  if (L == 0 || (even && even_parts(T, p.quantum) == 1)) {   // nothing, or one part
-    grid_dep_wait();
-    grid_dep_launch();
-    return;
-  }
-  long long carry = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < p.batch; c0 += kBCombineThreads) {
-    const int i = c0 + tid;
-    const int Ti = i < p.batch ? block_tiles(clamp_len(p.seq_lens[i], cap, bad)) : 0;
-    const long long own = even ? even_parts(Ti, p.quantum) : pack_tiles(Ti);
-    long long sum = 0;
-    const long long before = block_incl_scan<kBCombineThreads, long long>(own, scan, sum) - own + carry;
-    if (i == b) s_before = before;
-    carry += sum;
-  }
-  __syncthreads();
-  // the parts: slots first .. first + parts - 1
-  long long first_slot, base = 0, total = 0;
-  int parts, g0 = 0;
-  bool dense = true;
-  if (even) {
-    first_slot = r * carry + s_before;
-    parts = even_parts(T, p.quantum);
-  } else {
-    const BlockCost cost = block_cost(carry, p.readers);
-    total = cost.total;
-    base = r * cost.per_reader + cost_before(s_before);
-    // the CTA of the tile at cost X: the largest g with floor(g C / G) <= X
-    auto owner = [&](long long X) {
-      long long g = div_floor(X * num_ctas, total);
-      while (g + 1 < num_ctas && div_floor((g + 1) * total, num_ctas) <= X) ++g;
-      return static_cast<int>(g);
-    };
-    g0 = owner(base);
-    parts = owner(base + kBCostTile * static_cast<long long>(T - 1)) - g0 + 1;
-    first_slot = static_cast<long long>(pos) + g0;
-    dense = total >= kBCostTile * static_cast<long long>(num_ctas);   // every CTA inside the unit holds a tile of it
-  }
+  const int row0 = (blockIdx.y * kOcts + oct) * 8;   // this thread's first row
   grid_dep_wait();
   grid_dep_launch();
-  if (parts == 1 || first_slot + parts > p.num_partials) return;   // (past the plan: reported by the decode)
-  auto there = [&](int k) {   // (a CTA whose range lies between two tiles has no part)
-    return dense || first_tile_at(div_floor((g0 + k) * total, num_ctas), base, T) <
-                        first_tile_at(div_floor((g0 + k + 1) * total, num_ctas), base, T);
-  };
-  const int tg = r % p.token_groups, kvh = r / p.token_groups;
+  const int2 at = p.parts[pos];
+  // (the output is written already; or, past the plan, nothing is: the decode reports that)
+  if (at.x < 0 || at.y < at.x || at.y >= p.num_partials) return;
+  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
   const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
-  const int row0 = blockIdx.y * 8 * kOcts;   // this CTA's first row
-  // each row's lse: a warp a row
-#pragma unroll 1
-  for (int i = warp; i < 8 * kOcts; i += kBCombineThreads / 32) {
-    const int row = row0 + i;
-    float m = -INFINITY, l = 0.f;
-    if (row < valid) {
-      for (int k = lane; k < parts; k += 32)
-        if (there(k)) {
-          const float v = p.part_lse[(first_slot + k) * p.rows8 + row];
-          const float top = fmaxf(m, v);
-          l = v == -INFINITY ? l : l * (m == -INFINITY ? 0.f : expf(m - top)) + expf(v - top);
-          m = top;
-        }
-    }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    l = l == 0.f ? 0.f : l * expf(m - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float v = l == 0.f ? -INFINITY : top + logf(l);
-    if (lane == 0) {
-      s_lse[i] = v;
-      if (row < valid && p.lse != nullptr && blockIdx.z == 0)
-        p.lse[first + static_cast<size_t>(row / p.group) * p.heads + row % p.group] = v;
-    }
-  }
-  __syncthreads();
-  float ref[8], acc[8];
+  float M[8], S[8], acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    ref[i] = s_lse[8 * oct + i];
-    if (ref[i] == -INFINITY) ref[i] = 0.f;   // (a row that sees nothing: its parts weigh nothing)
-    acc[i] = 0.f;
+    M[i] = -INFINITY;
+    S[i] = acc[i] = 0.f;
   }
-  if (row0 + 8 * oct < valid) {
-    const float* src = p.part_o + (static_cast<size_t>(row0 / 8 + oct) * kDim + el) * 8;
-    constexpr int kRound = 4;
+  // one part (its lse l, its values o) into the running sums
+  auto take = [&](const float (&l)[8], const float (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float top = fmaxf(M[i], l[i]);
+      const float ref = top == -INFINITY ? 0.f : top;   // (nothing seen so far)
+      const float al = ex2_approx((M[i] - ref) * 1.4426950408889634f), w = ex2_approx((l[i] - ref) * 1.4426950408889634f);
+      S[i] = fmaf(S[i], al, w);
+      acc[i] = fmaf(acc[i], al, w * o[i]);
+      M[i] = top;
+    }
+  };
+  if (row0 < p.rows8) {
+    const float* src = p.part_o + (static_cast<size_t>(row0 / 8) * kDim + el) * 8;
 #pragma unroll 1
-    for (int k0 = team; k0 < parts; k0 += kRound * kTeams) {
-      float o[kRound][8], w[kRound][8];
-#pragma unroll
-      for (int k = 0; k < kRound; ++k) {
-        const int at = k0 + k * kTeams;
-        const bool have = at < parts && there(at);
-        const size_t slot = static_cast<size_t>(first_slot) + (have ? at : 0);
-        if (have) {
-          ld_global_f32x8(src + slot * p.rows8 * kDim, o[k]);
-          const float4* l4 = reinterpret_cast<const float4*>(p.part_lse + slot * p.rows8 + row0 + 8 * oct);
-          const float4 a = l4[0], c = l4[1];
-          w[k][0] = a.x, w[k][1] = a.y, w[k][2] = a.z, w[k][3] = a.w, w[k][4] = c.x, w[k][5] = c.y, w[k][6] = c.z, w[k][7] = c.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[k][i] = 0.f, w[k][i] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kRound; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(expf(w[k][i] - ref[i]), o[k][i], acc[i]);
+    for (int k = at.x + team; k <= at.y; k += 2 * kTeams) {
+      const bool two = k + kTeams <= at.y;
+      const size_t s0 = static_cast<size_t>(k) * p.rows8, s1 = static_cast<size_t>(two ? k + kTeams : k) * p.rows8;
+      float o0[8], o1[8], l0[8], l1[8];
+      ld_global_f32x8(src + s0 * kDim, o0);
+      ld_global_f32x8(src + s1 * kDim, o1);
+      ld_global_f32x8(p.part_lse + s0 + row0, l0);
+      ld_global_f32x8(p.part_lse + s1 + row0, l1);
+      take(l0, o0);
+      if (two) take(l1, o1);
     }
   }
   if constexpr (kTeams > 1) {
     if (team > 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) so[team - 1][tid % kSlice][i] = acc[i];
+      if (tid % kSlice == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sm[team - 1][i] = M[i];
+          sl[team - 1][i] = S[i];
+        }
+      }
     }
     __syncthreads();
     if (team > 0) return;
+#pragma unroll 1
+    for (int k = 0; k < kTeams - 1; ++k) {
 #pragma unroll
-    for (int k = 0; k < kTeams - 1; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += so[k][tid % kSlice][i];
+      for (int i = 0; i < 8; ++i) {
+        const float top = fmaxf(M[i], sm[k][i]), ref = top == -INFINITY ? 0.f : top;
+        const float al = ex2_approx((M[i] - ref) * 1.4426950408889634f), w = ex2_approx((sm[k][i] - ref) * 1.4426950408889634f);
+        S[i] = S[i] * al + sl[k][i] * w;
+        acc[i] = acc[i] * al + so[k][tid % kSlice][i] * w;
+        M[i] = top;
+      }
+    }
   }
+  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 8 * oct + i;
+    const int row = row0 + i;
     if (row >= valid) break;
-    const size_t at = (first + static_cast<size_t>(row / p.group) * p.heads + row % p.group) * kDim + el;
+    const size_t to = first + static_cast<size_t>(row / p.group) * p.heads + row % p.group;
+    const float v = S[i] == 0.f ? 0.f : acc[i] / S[i];
     if (p.out_f32)
-      static_cast<float*>(p.out)[at] = acc[i];
+      static_cast<float*>(p.out)[to * kDim + el] = v;
     else
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[i]);
+      static_cast<__nv_bfloat16*>(p.out)[to * kDim + el] = __float2bfloat16_rn(v);
+    if (el == 0 && p.lse != nullptr) p.lse[to] = S[i] == 0.f ? -INFINITY : M[i] + logf(S[i]);
   }
 }
 
 // ------------------------------------------------------------------ host side
 
 using BlockDecodeFn = void (*)(BlockDecodeParams);
-using BlockCombineFn = void (*)(BlockDecodeParams, int);
+using BlockCombineFn = void (*)(BlockDecodeParams);
 
 // The instance of a problem: width and rows padded to 16, 32 or 64.
 static int block_instance(const mfa_problem* pr, const BlockShape& sh) {
@@ -1097,6 +1142,11 @@ static BlockDecodeFn block_kernel_of(int i) {
                                   mfa_block_decode_kernel<128, 64>, mfa_block_decode_kernel<256, 16>,
                                   mfa_block_decode_kernel<256, 32>, mfa_block_decode_kernel<256, 64>};
   return k[i];
+}
+
+static int block_threads(int i) {
+  constexpr int t[3] = {BlockLayout<128, 16>::kThreads, BlockLayout<128, 32>::kThreads, BlockLayout<128, 64>::kThreads};
+  return t[i % 3];
 }
 
 // cudaFuncSetAttribute for an instance's dynamic shared memory, once per device and instance.
@@ -1197,7 +1247,7 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   plan->flags = flags | mode;
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
-  plan->workspace_bytes = block_workspace_bytes(partials, sh.rows8, pr->head_dim);
+  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->batch, pr->head_dim);
   return MFA_OK;
 }
 
@@ -1214,7 +1264,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
       plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_WHOLE_UNITS)) != 0 ||
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && plan->max_tiles_per_cta < 1) ||
       plan->num_partials != static_cast<long long>(pr->batch) * sh.readers + plan->num_ctas - 1 ||
-      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh.rows8, pr->head_dim))
+      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->batch, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
@@ -1250,7 +1300,8 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.out = out;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
-  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh.rows8, pr->head_dim));
+  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh, pr->head_dim));
+  p.parts = reinterpret_cast<int2*>(ws + block_parts_offset(plan->num_partials, sh, pr->head_dim));
   p.status = reinterpret_cast<unsigned int*>(ws);
   p.batch = pr->batch;
   p.tokens = pr->tokens_per_seq;
@@ -1277,7 +1328,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   if (sst != MFA_OK) return sst;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan->num_ctas), 1, 1);
-  cfg.blockDim = dim3(kBThreads, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(block_threads(inst)), 1, 1);
   cfg.dynamicSmemBytes = kBSmem + 1024;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1292,13 +1343,13 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
     // many parts a unit: the CTAs of a row share them
     const bool split = plan->num_ctas >= 8LL * units;
     const int octs = split || pr->head_dim == 256 ? 1 : 2;
-    cfg.gridDim = dim3(units, static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 64 : 1);
+    cfg.gridDim = dim3(units, static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 32 : 1);
     cfg.blockDim = dim3(kBCombineThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     const BlockCombineFn fn = pr->head_dim == 256
-                                  ? (split ? mfa_block_combine_kernel<256, 4> : mfa_block_combine_kernel<256, 1>)
-                                  : (split ? mfa_block_combine_kernel<128, 4> : mfa_block_combine_kernel<128, 1>);
-    e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(plan->num_ctas));
+                                  ? (split ? mfa_block_combine_kernel<256, 8> : mfa_block_combine_kernel<256, 1>)
+                                  : (split ? mfa_block_combine_kernel<128, 8> : mfa_block_combine_kernel<128, 1>);
+    e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }
   if (check) {
