@@ -67,16 +67,13 @@ static BlockShape block_shape(const mfa_problem* pr) {
   return s;
 }
 
-// Workspace: header; partial O; partial lse; and for each unit the slots of its first and last part.
+// Workspace: header; partial O; partial lse.
 static uint64_t block_lse_offset(long long partials, const BlockShape& s, int d) {
   const uint64_t x = kBWsHeader + static_cast<uint64_t>(partials) * s.rows8 * d * 4;
   return (x + 255) / 256 * 256;
 }
-static uint64_t block_parts_offset(long long partials, const BlockShape& s, int d) {
+static uint64_t block_workspace_bytes(long long partials, const BlockShape& s, int d) {
   return (block_lse_offset(partials, s, d) + static_cast<uint64_t>(partials) * s.rows8 * 4 + 255) / 256 * 256;
-}
-static uint64_t block_workspace_bytes(long long partials, const BlockShape& s, int batch, int d) {
-  return (block_parts_offset(partials, s, d) + static_cast<uint64_t>(batch) * s.readers * 8 + 255) / 256 * 256;
 }
 
 // Shared memory and tensor memory of an instance: kDim the head width, kNR the unit's rows
@@ -115,7 +112,6 @@ struct BlockDecodeParams {
   float* lse;
   float* part_o;             // [partials][rows8 / 8][d][8 rows]: 32 bytes a thread of the epilogue
   float* part_lse;           // [partials][rows8]
-  int2* parts;               // [units] slots of a unit's first and last part; -1: the output is written
   unsigned int* status;
   int batch, tokens, heads, kv_heads;
   int group, unit_tokens, token_groups, readers, rows8;   // BlockShape
@@ -137,9 +133,9 @@ struct BlockDecodeParams {
 // [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.
 //
 // Even split (chosen by the plan where the units are fewer than the CTAs and lengths allow):
-// each unit of T tiles is cut into ceil(T / quantum) parts as equal as they come (or not at
-// all), part i of unit (b, r) being item r P + P_b + i (P parts of one reader of every
-// sequence, P_b of those before b), and CTA g takes items g, g + G, ...: one part each, none
+// each unit of T tiles is cut into n = ceil(T / quantum) parts as equal as they come (or not at
+// all).  Part i of reader r of sequence b is item R P_b + r n + i (R readers, P_b parts of one
+// reader of each sequence before b), and CTA g takes items g, g + G, ...: one part each, none
 // with the end of one unit and the beginning of another.
 __device__ __forceinline__ int even_parts(int T, int quantum) {
   return T <= quantum || quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
@@ -210,170 +206,130 @@ struct __align__(16) BlockSegment {
   int b, kvh, tg, L;       // sequence, key/value head, group of new tokens, length
   int lo, hi;              // tiles
   int slot;                // of the partial result; -1: the whole unit
-  int pos;                 // the unit's place in the schedule
 };
 
-// This CTA's segments, by one warp, into shared memory; their number and their tiles into counts[0]
-// and counts[1].  Lane l has four sequences of each 128, their lengths loaded together.  Rolled
-// loops where they can be: what a CTA runs once costs as much for its instructions' fetch as for
-// their work.
-__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
-  constexpr int kPer = 4, kChunk = 32 * kPer;
+__device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSegment* seg, int at, int b, int r, int L, int lo,
+                                            int hi, long long slot) {
+  if (at >= kBMaxSeg) return;
+  BlockSegment x;
+  x.b = b;
+  x.kvh = p.token_groups == 1 ? r : r / p.token_groups;
+  x.tg = r - x.kvh * p.token_groups;
+  x.L = L;
+  x.lo = lo;
+  x.hi = hi;
+  x.slot = lo == 0 && hi == block_tiles(L) ? -1 : static_cast<int>(slot);
+  seg[at] = x;
+}
+
+// This CTA's segments, by one warp (a lane a sequence), into shared memory; their number and this
+// lane's tiles in (nseg, tiles).  The code is kept small and straight: what a CTA runs once costs
+// more for its instructions' fetch than for their work.
+__device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                              bool& bad, bool& fits) {
   const int lane = threadIdx.x & 31;
-  bool bad = false;
-  auto lengths = [&](int c0, int (&L)[kPer]) {
+  long long item = blockIdx.x, carry = 0;   // the item that is looked for; items of the sequences passed
+  int next = lane < p.batch ? p.seq_lens[lane] : 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < p.batch; c0 += 32) {
+    const int L = clamp_len(next, cap, bad);
+    next = c0 + 32 + lane < p.batch ? p.seq_lens[c0 + 32 + lane] : 0;
+    const int T = block_tiles(L), n = even_parts(T, p.quantum);
+    const long long own = static_cast<long long>(n) * p.readers;
+    long long incl = own;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int b = c0 + lane * kPer + k;
-      L[k] = b < p.batch ? p.seq_lens[b] : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) L[k] = clamp_len(L[k], cap, bad);
-  };
-  auto add = [&](int at, int b, int r, int L, int lo, int hi, long long slot) {
-    if (at >= kBMaxSeg) return;
-    BlockSegment x;
-    x.b = b;
-    x.kvh = p.token_groups == 1 ? r : r / p.token_groups;
-    x.tg = r - x.kvh * p.token_groups;
-    x.L = L;
-    x.lo = lo;
-    x.hi = hi;
-    x.slot = lo == 0 && hi == block_tiles(L) ? -1 : static_cast<int>(slot);
-    x.pos = r * p.batch + b;
-    seg[at] = x;
-  };
-  const int G = gridDim.x, g = blockIdx.x;
-  int L[kPer];
-  lengths(0, L);
-  int nseg = 0, tiles = 0;
-  bool fits = true;
-  if (p.quantum != 0) {
-    // even split: item g, g + G, ... of the units' parts
-    auto parts = [&](int x) { return even_parts(block_tiles(x), p.quantum); };
-    int all = 0;
+    const long long before = carry + incl - own;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
 #pragma unroll 1
-    for (int c0 = 0; c0 < p.batch; c0 += kChunk) {
-      if (c0 > 0) lengths(c0, L);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) all += parts(L[k]);
-    }
-    all = __reduce_add_sync(0xffffffffu, all);
-    const long long items = static_cast<long long>(all) * p.readers;
-    fits = p.quantum < 0 || items <= p.num_partials;
-#pragma unroll 1
-    for (long long item = g; item < items && nseg <= kBMaxSeg; item += G) {
-      const int r = static_cast<int>(div_floor(item, all)), rem = static_cast<int>(item - static_cast<long long>(r) * all);
-      int carry = 0;
-#pragma unroll 1
-      for (int c0 = 0; c0 < p.batch && carry <= rem; c0 += kChunk) {
-        if (p.batch > kChunk) lengths(c0, L);
-        int own = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) own += parts(L[k]);
-        int incl = own;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
+    while (item < carry && nseg <= kBMaxSeg) {
+      if (item >= before && item < before + own) {
+        int r = static_cast<int>(item - before), lo = 0, hi = T;
+        if (n > 1) {   // part i: T / n tiles, the first T % n parts one more
+          const int i = r % n, each = T / n, more = T - each * n;
+          r /= n;
+          lo = i * each + min(i, more);
+          hi = lo + each + (i < more ? 1 : 0);
+          fits = fits && item < p.num_partials;
         }
-        int i = rem - (carry + incl - own);   // the part, if it is one of this lane's sequences'
-        if (i >= 0 && i < own) {
-          int k = 0, len = L[0];
-#pragma unroll
-          for (int x = 0; x + 1 < kPer; ++x) {
-            const int n = parts(len);
-            if (k == x && i >= n) {
-              i -= n;
-              k = x + 1;
-              len = L[x + 1];
-            }
-          }
-          // part i of n: T / n tiles, the first T % n parts one more
-          const int T = block_tiles(len), n = parts(len), each = T / n, more = T - each * n;
-          const int lo = i * each + min(i, more), hi = lo + each + (i < more ? 1 : 0);
-          add(nseg, c0 + lane * kPer + k, r, len, lo, hi, item);
-          tiles += hi - lo;
-        }
-        carry += __shfl_sync(0xffffffffu, incl, 31);
+        add_segment(p, seg, nseg, c0 + lane, r, L, lo, hi, item);
+        tiles += hi - lo;
       }
       ++nseg;
-    }
-  } else {
-    long long all = 0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < p.batch; c0 += kChunk) {
-      if (c0 > 0) lengths(c0, L);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) all += pack_tiles(block_tiles(L[k]));
-    }
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    const BlockCost cost = block_cost(all, p.readers);
-    // lane 0: the range's first cost, lane 1: its end; and the readers that hold them.  With less
-    // cost than a tile for each CTA the last CTAs have nothing: no CTA lies between two tiles.
-    const long long Ge = min(static_cast<long long>(G), max(cost.total / kBCostTile, 1ll));
-    long long x = 0, y = 0;
-    if (lane < 2) {
-      x = g + lane > Ge ? cost.total : div_floor((g + lane) * cost.total, Ge);
-      y = cost.total > 0 ? div_floor(max(x - lane, 0ll), cost.per_reader) : 0;
-    }
-    const long long X0 = __shfl_sync(0xffffffffu, x, 0), X1 = __shfl_sync(0xffffffffu, x, 1);
-    const int r0 = __shfl_sync(0xffffffffu, static_cast<int>(y), 0), r1 = __shfl_sync(0xffffffffu, static_cast<int>(y), 1);
-#pragma unroll 1
-    for (int r = r0; X0 < X1 && r <= r1 && nseg <= kBMaxSeg; ++r) {
-      long long carry = 0;
-      const long long rbase = r * cost.per_reader;
-#pragma unroll 1
-      for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += kChunk) {
-        if (p.batch > kChunk) lengths(c0, L);
-        long long own = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) own += pack_tiles(block_tiles(L[k]));
-        long long incl = own;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        long long before = carry + incl - own;
-        int lo[kPer], hi[kPer], count = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const long long base = rbase + cost_before(before);
-          const int T = block_tiles(L[k]);
-          lo[k] = first_tile_at(X0, base, T);
-          hi[k] = first_tile_at(X1, base, T);
-          count += lo[k] < hi[k] ? 1 : 0;
-          before += pack_tiles(T);
-        }
-        int at = count;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += v;
-        }
-        const int found = __shfl_sync(0xffffffffu, at, 31);
-        at += nseg - count;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (lo[k] < hi[k]) {
-            add(at++, c0 + lane * kPer + k, r, L[k], lo[k], hi[k], static_cast<long long>(r) * p.batch + c0 + lane * kPer + k + g);
-            tiles += hi[k] - lo[k];
-          }
-        }
-        nseg += found;
-        carry += __shfl_sync(0xffffffffu, incl, 31);
-      }
+      item += gridDim.x;
     }
   }
+}
+
+__device__ __noinline__ void cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                           bool& bad) {
+  const int lane = threadIdx.x & 31;
+  auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
+  const int L0 = length(lane);
+  long long all = pack_tiles(block_tiles(L0));
+#pragma unroll 4
+  for (int b = lane + 32; b < p.batch; b += 32) all += pack_tiles(block_tiles(length(b)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  const BlockCost cost = block_cost(all, p.readers);
+  // lane 0: the range's first cost, lane 1: its end; and the readers that hold them.  With less
+  // cost than a tile for each CTA the last CTAs have nothing: no CTA lies between two tiles.
+  const long long G = min(static_cast<long long>(gridDim.x), max(cost.total / kBCostTile, 1ll)), g = blockIdx.x;
+  long long x = 0, y = 0;
+  if (lane < 2) {
+    x = g + lane > G ? cost.total : div_floor((g + lane) * cost.total, G);
+    y = cost.total > 0 ? div_floor(max(x - lane, 0ll), cost.per_reader) : 0;
+  }
+  const long long X0 = __shfl_sync(0xffffffffu, x, 0), X1 = __shfl_sync(0xffffffffu, x, 1);
+  const int r0 = __shfl_sync(0xffffffffu, static_cast<int>(y), 0), r1 = __shfl_sync(0xffffffffu, static_cast<int>(y), 1);
+#pragma unroll 1
+  for (int r = r0; X0 < X1 && r <= r1 && nseg <= kBMaxSeg; ++r) {
+    long long carry = 0;
+    const long long rbase = r * cost.per_reader;
+    int next = L0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += 32) {
+      const int L = next;
+      next = length(c0 + 32 + lane);
+      const int T = block_tiles(L);
+      const long long own = pack_tiles(T);
+      long long incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const long long base = rbase + cost_before(carry + incl - own);
+      const int lo = first_tile_at(X0, base, T), hi = first_tile_at(X1, base, T);
+      const unsigned has = __ballot_sync(0xffffffffu, lo < hi);
+      if (lo < hi) {
+        add_segment(p, seg, nseg + __popc(has & ((1u << lane) - 1u)), c0 + lane, r, L, lo, hi,
+                    static_cast<long long>(r) * p.batch + c0 + lane + g);
+        tiles += hi - lo;
+      }
+      nseg += __popc(has);
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+}
+
+__device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
+  int nseg = 0, tiles = 0;
+  bool bad = false, fits = true;
+  if (p.quantum != 0)
+    even_segments(p, cap, seg, nseg, tiles, bad, fits);
+  else
+    cost_segments(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
-  if (nseg > kBMaxSeg || !fits) {
-    if (lane == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
+  if (nseg > kBMaxSeg || !__all_sync(0xffffffffu, fits)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
     nseg = tiles = 0;
   }
-  if (lane == 0) {
+  if ((threadIdx.x & 31) == 0) {
     counts[0] = nseg;
     counts[1] = tiles;
   }
@@ -1003,10 +959,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           else if (p.lse != nullptr)
             p.lse[first + row_off[c0 + row] / kDim] = v;
         }
-        if (sw == 0 && lane == 0) {   // for the combine
-          if (sg.lo == 0) p.parts[sg.pos].x = slot;
-          if (sg.hi == block_tiles(L)) p.parts[sg.pos].y = slot;
-        }
       }
     }
     // sequences without tokens: zeros and -inf, in turn over the CTAs
@@ -1017,7 +969,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const size_t chunks = n * kDim * (f32 ? 4 : 2) / 16;
       uint4* o = static_cast<uint4*>(p.out) + at * kDim * (f32 ? 4 : 2) / 16;
       for (size_t i = tid - 32 * kBSoftmaxWarp0; i < chunks; i += 32 * kSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
-      for (int i = tid - 32 * kBSoftmaxWarp0; i < p.readers; i += 32 * kSoftmaxWarps) p.parts[i * p.batch + b] = make_int2(-1, -1);
       if (p.lse != nullptr)
         for (size_t i = tid - 32 * kBSoftmaxWarp0; i < n; i += 32 * kSoftmaxWarps) p.lse[at + i] = -INFINITY;
     }
@@ -1034,11 +985,12 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 //
 // Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order,
 // with a running maximum.  A thread has eight rows of one element, as the parts hold them: one
-// 32-byte load a part, two parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or
+// 32-byte load a part, four parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or
 // sixteen (d = 128); with many parts a unit (kTeams = 8) it takes eight rows of 32 elements, its
 // teams sharing the parts.
 template <int kDim, int kTeams>
-__global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+__global__ void __launch_bounds__(kBCombineThreads, 2) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p,
+                                                                                const int num_ctas) {
   constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
   constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
   __shared__ float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
@@ -1047,11 +999,47 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
   const int team = tid / (kSlice * kOcts), oct = tid / kSlice % kOcts, el = blockIdx.z * kSlice + tid % kSlice;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
   const int row0 = (blockIdx.y * kOcts + oct) * 8;   // this thread's first row
+  // The parts, slots at.x .. at.y.  The decode kernel lets this one start once its own wait for
+  // what came before is over, so the lengths are final; what the decode writes is read after this
+  // kernel's wait.
+  int2 at = make_int2(0, -1);
+  const int cap = p.max_pages * kBPage;
+  bool bad = false;
+  const int T = block_tiles(clamp_len(p.seq_lens[b], cap, bad));
+  if (p.quantum > 0) {
+    const int n = even_parts(T, p.quantum);
+    int before = 0;   // parts of the sequences before b, in every warp
+    for (int i = tid & 31; i < b; i += 32) before += even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), p.quantum);
+    before = __reduce_add_sync(0xffffffffu, before);
+    const long long first_part = static_cast<long long>(before) * p.readers + static_cast<long long>(r) * n;
+    if (n > 1 && first_part + n <= p.num_partials) at = make_int2(static_cast<int>(first_part), static_cast<int>(first_part) + n - 1);
+  } else if (T > 0) {
+    long long before = 0, all = 0;
+    for (int i = tid & 31; i < p.batch; i += 32) {
+      const long long own = pack_tiles(block_tiles(clamp_len(p.seq_lens[i], cap, bad)));
+      all += own;
+      before += i < b ? own : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    const BlockCost cost = block_cost(all, p.readers);
+    const long long G = min(static_cast<long long>(num_ctas), max(cost.total / kBCostTile, 1ll));
+    // the CTAs of the first and last tile: the largest g with floor(g C / G) <= the tile's cost
+    auto owner = [&](long long X) {
+      long long g = div_floor(X * G, cost.total);
+      while (g + 1 < G && div_floor((g + 1) * cost.total, G) <= X) ++g;
+      return static_cast<int>(g);
+    };
+    const long long base = r * cost.per_reader + cost_before(before);
+    const int g0 = owner(base), g1 = owner(base + kBCostTile * static_cast<long long>(T - 1));
+    if (g1 > g0 && pos + static_cast<long long>(g1) < p.num_partials) at = make_int2(pos + g0, pos + g1);
+  }
   grid_dep_wait();
   grid_dep_launch();
-  const int2 at = p.parts[pos];
-  // (the output is written already; or, past the plan, nothing is: the decode reports that)
-  if (at.x < 0 || at.y < at.x || at.y >= p.num_partials) return;
+  if (at.y < at.x) return;   // one part, the output itself; no tokens; or past the plan, as the decode reports
   const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
   const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
   float M[8], S[8], acc[8];
@@ -1074,17 +1062,20 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
   };
   if (row0 < p.rows8) {
     const float* src = p.part_o + (static_cast<size_t>(row0 / 8) * kDim + el) * 8;
+    const float* src_l = p.part_lse + row0;
+    constexpr int kRound = 4;
 #pragma unroll 1
-    for (int k = at.x + team; k <= at.y; k += 2 * kTeams) {
-      const bool two = k + kTeams <= at.y;
-      const size_t s0 = static_cast<size_t>(k) * p.rows8, s1 = static_cast<size_t>(two ? k + kTeams : k) * p.rows8;
-      float o0[8], o1[8], l0[8], l1[8];
-      ld_global_f32x8(src + s0 * kDim, o0);
-      ld_global_f32x8(src + s1 * kDim, o1);
-      ld_global_f32x8(p.part_lse + s0 + row0, l0);
-      ld_global_f32x8(p.part_lse + s1 + row0, l1);
-      take(l0, o0);
-      if (two) take(l1, o1);
+    for (int k = at.x + team; k <= at.y; k += kRound * kTeams) {
+      float o[kRound][8], l[kRound][8];
+#pragma unroll
+      for (int x = 0; x < kRound; ++x) {
+        const size_t slot = static_cast<size_t>(min(k + x * kTeams, at.y)) * p.rows8;   // (past the last: not taken)
+        ld_global_f32x8(src + slot * kDim, o[x]);
+        ld_global_f32x8(src_l + slot, l[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < kRound; ++x)
+        if (k + x * kTeams <= at.y) take(l[x], o[x]);
     }
   }
   if constexpr (kTeams > 1) {
@@ -1131,7 +1122,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
 // ------------------------------------------------------------------ host side
 
 using BlockDecodeFn = void (*)(BlockDecodeParams);
-using BlockCombineFn = void (*)(BlockDecodeParams);
+using BlockCombineFn = void (*)(BlockDecodeParams, int);
 
 // The instance of a problem: width and rows padded to 16, 32 or 64.
 static int block_instance(const mfa_problem* pr, const BlockShape& sh) {
@@ -1247,7 +1238,7 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   plan->flags = flags | mode;
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
-  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->batch, pr->head_dim);
+  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->head_dim);
   return MFA_OK;
 }
 
@@ -1264,7 +1255,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
       plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_WHOLE_UNITS)) != 0 ||
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && plan->max_tiles_per_cta < 1) ||
       plan->num_partials != static_cast<long long>(pr->batch) * sh.readers + plan->num_ctas - 1 ||
-      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->batch, pr->head_dim))
+      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
@@ -1301,7 +1292,6 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
   p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh, pr->head_dim));
-  p.parts = reinterpret_cast<int2*>(ws + block_parts_offset(plan->num_partials, sh, pr->head_dim));
   p.status = reinterpret_cast<unsigned int*>(ws);
   p.batch = pr->batch;
   p.tokens = pr->tokens_per_seq;
@@ -1349,7 +1339,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
     const BlockCombineFn fn = pr->head_dim == 256
                                   ? (split ? mfa_block_combine_kernel<256, 8> : mfa_block_combine_kernel<256, 1>)
                                   : (split ? mfa_block_combine_kernel<128, 8> : mfa_block_combine_kernel<128, 1>);
-    e = cudaLaunchKernelEx(&cfg, fn, p);
+    e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(plan->num_ctas));
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }
   if (check) {
