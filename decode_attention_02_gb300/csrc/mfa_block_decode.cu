@@ -29,7 +29,7 @@ constexpr int kBPage = 64;
 constexpr int kBTile = 128;           // tokens of a tile (two pages)
 constexpr int kBRows = 64;            // query rows (new tokens x heads of one group) a unit holds at most
 constexpr int kBCostTile = 4;         // schedule: cost of a tile
-constexpr int kBCostUnit = 6;         // and of a unit boundary inside a CTA's range
+constexpr int kBCostUnit = 16;        // and of a unit boundary inside a CTA's range
 constexpr int kBSwitchTiles = 5;      // plan: tiles that a second unit in a CTA's range is worth (see the plan)
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
@@ -67,13 +67,16 @@ static BlockShape block_shape(const mfa_problem* pr) {
   return s;
 }
 
-// Workspace: header; partial O; partial lse.
+// Workspace: header; partial O; partial lse; and for each unit the slots of its first and last part.
 static uint64_t block_lse_offset(long long partials, const BlockShape& s, int d) {
   const uint64_t x = kBWsHeader + static_cast<uint64_t>(partials) * s.rows8 * d * 4;
   return (x + 255) / 256 * 256;
 }
-static uint64_t block_workspace_bytes(long long partials, const BlockShape& s, int d) {
+static uint64_t block_parts_offset(long long partials, const BlockShape& s, int d) {
   return (block_lse_offset(partials, s, d) + static_cast<uint64_t>(partials) * s.rows8 * 4 + 255) / 256 * 256;
+}
+static uint64_t block_workspace_bytes(long long partials, const BlockShape& s, int batch, int d) {
+  return (block_parts_offset(partials, s, d) + static_cast<uint64_t>(batch) * s.readers * 8 + 255) / 256 * 256;
 }
 
 // Shared memory and tensor memory of an instance: kDim the head width, kNR the unit's rows
@@ -116,6 +119,8 @@ struct BlockDecodeParams {
   int batch, tokens, heads, kv_heads;
   int group, unit_tokens, token_groups, readers, rows8;   // BlockShape
   int num_partials;
+  int2* parts;               // split by cost: [units] slots of a unit's first and last part
+  int narrow;                // split by cost: G times the whole cost fits 32 bits
   int quantum;               // even split: most tiles of a part, or -1 for whole units; 0: split by cost
   int log_scale;             // log2(scale_tokens)
   int max_pages, num_blocks;
@@ -140,27 +145,10 @@ struct BlockDecodeParams {
 __device__ __forceinline__ int even_parts(int T, int quantum) {
   return T <= quantum || quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
 }
-struct BlockCost {
-  long long per_reader;   // cost of one reader of every sequence
-  long long total;        // C
-};
-__device__ __forceinline__ BlockCost block_cost(long long packed, int readers) {
-  const long long tiles = packed & 0xFFFFFFFFFll, n = packed >> 36;
-  BlockCost c;
-  c.per_reader = kBCostTile * tiles + kBCostUnit * n;
-  c.total = n > 0 ? c.per_reader * readers - kBCostUnit : 0;
-  return c;
-}
-// tiles in the low 36 bits, non-empty sequences above
-__device__ __forceinline__ long long pack_tiles(int tiles) {
-  return static_cast<long long>(tiles) | (static_cast<long long>(tiles > 0) << 36);
-}
-__device__ __forceinline__ long long cost_before(long long packed) {
-  return kBCostTile * (packed & 0xFFFFFFFFFll) + kBCostUnit * (packed >> 36);
-}
 // first of a unit's T tiles at cost >= X
-__device__ __forceinline__ int first_tile_at(long long X, long long base, int T) {
-  return X <= base ? 0 : static_cast<int>(min(static_cast<long long>(T), (X - base + kBCostTile - 1) / kBCostTile));
+template <typename I>
+__device__ __forceinline__ int first_tile_at(I X, I base, int T) {
+  return X <= base ? 0 : static_cast<int>(min(static_cast<I>(T), (X - base + kBCostTile - 1) / kBCostTile));
 }
 __device__ __forceinline__ int block_tiles(int L) { return (L + kBTile - 1) / kBTile; }
 
@@ -193,12 +181,6 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
 #pragma unroll
   for (; step >= 1; step /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], step));
   return v[0];
-}
-
-// floor(a / b), a and b >= 0 (the 32-bit division is several times shorter)
-__device__ __noinline__ long long div_floor(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
 }
 
 // A segment: one unit's tiles of this CTA.
@@ -264,50 +246,50 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
   }
 }
 
-__device__ __noinline__ void cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
-                                           bool& bad) {
+// I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).
+template <typename I>
+__device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                              bool& bad) {
   const int lane = threadIdx.x & 31;
   auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
+  auto cost = [](int T) { return T > 0 ? static_cast<I>(kBCostTile) * T + kBCostUnit : I{0}; };
   const int L0 = length(lane);
-  long long all = pack_tiles(block_tiles(L0));
-#pragma unroll 4
-  for (int b = lane + 32; b < p.batch; b += 32) all += pack_tiles(block_tiles(length(b)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const BlockCost cost = block_cost(all, p.readers);
-  // lane 0: the range's first cost, lane 1: its end; and the readers that hold them.  With less
-  // cost than a tile for each CTA the last CTAs have nothing: no CTA lies between two tiles.
-  const long long G = min(static_cast<long long>(gridDim.x), max(cost.total / kBCostTile, 1ll)), g = blockIdx.x;
-  long long x = 0, y = 0;
-  if (lane < 2) {
-    x = g + lane > G ? cost.total : div_floor((g + lane) * cost.total, G);
-    y = cost.total > 0 ? div_floor(max(x - lane, 0ll), cost.per_reader) : 0;
-  }
-  const long long X0 = __shfl_sync(0xffffffffu, x, 0), X1 = __shfl_sync(0xffffffffu, x, 1);
-  const int r0 = __shfl_sync(0xffffffffu, static_cast<int>(y), 0), r1 = __shfl_sync(0xffffffffu, static_cast<int>(y), 1);
+  I per = cost(block_tiles(L0));   // of one reader of every sequence
 #pragma unroll 1
-  for (int r = r0; X0 < X1 && r <= r1 && nseg <= kBMaxSeg; ++r) {
-    long long carry = 0;
-    const long long rbase = r * cost.per_reader;
+  for (int b = lane + 32; b < p.batch; b += 32) per += cost(block_tiles(length(b)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) per += __shfl_xor_sync(0xffffffffu, per, o);
+  if (per == 0) return;
+  // the whole cost; with less of it than a tile for each CTA the last CTAs have nothing, so that
+  // no CTA lies between two tiles
+  const I total = per * p.readers - kBCostUnit, G = min(static_cast<I>(gridDim.x), total / kBCostTile), g = blockIdx.x;
+  if (g >= G) return;
+  const I X0 = g * total / G, X1 = (g + 1) * total / G;
+  I rbase = X0 / per;   // the reader at X0, then its base
+  int r = static_cast<int>(rbase);
+  rbase *= per;
+#pragma unroll 1
+  for (; rbase < X1 && nseg <= kBMaxSeg; ++r, rbase += per) {
+    I carry = rbase;
     int next = L0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < p.batch && rbase + cost_before(carry) < X1; c0 += 32) {
+    for (int c0 = 0; c0 < p.batch && carry < X1; c0 += 32) {
       const int L = next;
       next = length(c0 + 32 + lane);
       const int T = block_tiles(L);
-      const long long own = pack_tiles(T);
-      long long incl = own;
+      const I own = cost(T);
+      I incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const I v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      const long long base = rbase + cost_before(carry + incl - own);
+      const I base = carry + incl - own;
       const int lo = first_tile_at(X0, base, T), hi = first_tile_at(X1, base, T);
       const unsigned has = __ballot_sync(0xffffffffu, lo < hi);
       if (lo < hi) {
         add_segment(p, seg, nseg + __popc(has & ((1u << lane) - 1u)), c0 + lane, r, L, lo, hi,
-                    static_cast<long long>(r) * p.batch + c0 + lane + g);
+                    static_cast<long long>(r) * p.batch + c0 + lane + blockIdx.x);
         tiles += hi - lo;
       }
       nseg += __popc(has);
@@ -315,14 +297,21 @@ __device__ __noinline__ void cost_segments(const BlockDecodeParams& p, int cap, 
     }
   }
 }
+// (the wide form, for problems of millions of tiles, out of the way of the usual one's code)
+__device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                                bool& bad) {
+  cost_segments<long long>(p, cap, seg, nseg, tiles, bad);
+}
 
 __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
   int nseg = 0, tiles = 0;
   bool bad = false, fits = true;
   if (p.quantum != 0)
     even_segments(p, cap, seg, nseg, tiles, bad, fits);
+  else if (p.narrow)
+    cost_segments<uint32_t>(p, cap, seg, nseg, tiles, bad);
   else
-    cost_segments(p, cap, seg, nseg, tiles, bad);
+    cost_segments_wide(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   if (nseg > kBMaxSeg || !__all_sync(0xffffffffu, fits)) {
@@ -570,6 +559,14 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     const bool is_v = (lane & 8) != 0, mine = lane < 16 && blk < (kBPage >> p.log_scale);
     const float* src = is_v ? p.v_scale : p.k_scale;
     const float mul = is_v ? 1.f : p.scale_log2;
+    if (p.quantum == 0) {   // where the combine finds a unit's parts
+      for (int i = lane; i < nseg; i += 32) {
+        const BlockSegment x = seg[i];
+        int2* at = p.parts + static_cast<size_t>(x.kvh * p.token_groups + x.tg) * p.batch + x.b;
+        if (x.lo == 0) at->x = x.slot;
+        if (x.hi == block_tiles(x.L)) at->y = x.slot;
+      }
+    }
     if (ntiles > 0) {
       BlockTile it;
       it.load(p, seg, 0);
@@ -985,12 +982,11 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 //
 // Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order,
 // with a running maximum.  A thread has eight rows of one element, as the parts hold them: one
-// 32-byte load a part, four parts in flight.  kTeams = 1: a CTA takes eight rows (d = 256) or
+// 32-byte load a part, two parts in flight (four with teams).  kTeams = 1: a CTA takes eight rows (d = 256) or
 // sixteen (d = 128); with many parts a unit (kTeams = 8) it takes eight rows of 32 elements, its
 // teams sharing the parts.
 template <int kDim, int kTeams>
-__global__ void __launch_bounds__(kBCombineThreads, 2) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p,
-                                                                                const int num_ctas) {
+__global__ void __launch_bounds__(kBCombineThreads, kTeams > 1 ? 2 : 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
   constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
   __shared__ float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
@@ -1013,33 +1009,12 @@ __global__ void __launch_bounds__(kBCombineThreads, 2) mfa_block_combine_kernel(
     before = __reduce_add_sync(0xffffffffu, before);
     const long long first_part = static_cast<long long>(before) * p.readers + static_cast<long long>(r) * n;
     if (n > 1 && first_part + n <= p.num_partials) at = make_int2(static_cast<int>(first_part), static_cast<int>(first_part) + n - 1);
-  } else if (T > 0) {
-    long long before = 0, all = 0;
-    for (int i = tid & 31; i < p.batch; i += 32) {
-      const long long own = pack_tiles(block_tiles(clamp_len(p.seq_lens[i], cap, bad)));
-      all += own;
-      before += i < b ? own : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    const BlockCost cost = block_cost(all, p.readers);
-    const long long G = min(static_cast<long long>(num_ctas), max(cost.total / kBCostTile, 1ll));
-    // the CTAs of the first and last tile: the largest g with floor(g C / G) <= the tile's cost
-    auto owner = [&](long long X) {
-      long long g = div_floor(X * G, cost.total);
-      while (g + 1 < G && div_floor((g + 1) * cost.total, G) <= X) ++g;
-      return static_cast<int>(g);
-    };
-    const long long base = r * cost.per_reader + cost_before(before);
-    const int g0 = owner(base), g1 = owner(base + kBCostTile * static_cast<long long>(T - 1));
-    if (g1 > g0 && pos + static_cast<long long>(g1) < p.num_partials) at = make_int2(pos + g0, pos + g1);
   }
   grid_dep_wait();
   grid_dep_launch();
-  if (at.y < at.x) return;   // one part, the output itself; no tokens; or past the plan, as the decode reports
+  if (p.quantum == 0 && T > 0) at = p.parts[pos];
+  // one part, the output itself; no tokens; or past the plan, as the decode reports
+  if (at.y <= at.x || at.x < 0 || at.y >= p.num_partials) return;
   const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
   const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
   float M[8], S[8], acc[8];
@@ -1063,7 +1038,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 2) mfa_block_combine_kernel(
   if (row0 < p.rows8) {
     const float* src = p.part_o + (static_cast<size_t>(row0 / 8) * kDim + el) * 8;
     const float* src_l = p.part_lse + row0;
-    constexpr int kRound = 4;
+    constexpr int kRound = kTeams > 1 ? 4 : 2;
 #pragma unroll 1
     for (int k = at.x + team; k <= at.y; k += kRound * kTeams) {
       float o[kRound][8], l[kRound][8];
@@ -1122,7 +1097,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 2) mfa_block_combine_kernel(
 // ------------------------------------------------------------------ host side
 
 using BlockDecodeFn = void (*)(BlockDecodeParams);
-using BlockCombineFn = void (*)(BlockDecodeParams, int);
+using BlockCombineFn = void (*)(BlockDecodeParams);
 
 // The instance of a problem: width and rows padded to 16, 32 or 64.
 static int block_instance(const mfa_problem* pr, const BlockShape& sh) {
@@ -1238,7 +1213,7 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   plan->flags = flags | mode;
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
-  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->head_dim);
+  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->batch, pr->head_dim);
   return MFA_OK;
 }
 
@@ -1255,7 +1230,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
       plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_WHOLE_UNITS)) != 0 ||
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && plan->max_tiles_per_cta < 1) ||
       plan->num_partials != static_cast<long long>(pr->batch) * sh.readers + plan->num_ctas - 1 ||
-      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->head_dim))
+      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->batch, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
@@ -1292,6 +1267,10 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
   p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh, pr->head_dim));
+  p.parts = reinterpret_cast<int2*>(ws + block_parts_offset(plan->num_partials, sh, pr->head_dim));
+  p.narrow = static_cast<double>(pr->batch) * sh.readers * plan->num_ctas *
+                     (kBCostTile * ((static_cast<double>(pr->max_pages_per_seq) * kBPage + kBTile - 1) / kBTile) + kBCostUnit) <
+                 4.0e9;
   p.status = reinterpret_cast<unsigned int*>(ws);
   p.batch = pr->batch;
   p.tokens = pr->tokens_per_seq;
@@ -1339,7 +1318,7 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
     const BlockCombineFn fn = pr->head_dim == 256
                                   ? (split ? mfa_block_combine_kernel<256, 8> : mfa_block_combine_kernel<256, 1>)
                                   : (split ? mfa_block_combine_kernel<128, 8> : mfa_block_combine_kernel<128, 1>);
-    e = cudaLaunchKernelEx(&cfg, fn, p, static_cast<int>(plan->num_ctas));
+    e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }
   if (check) {

@@ -399,7 +399,7 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
 /*
  * Choose the split of the decode's work, as mfa_decode_plan does for the other caches (same
  * arguments; MFA_PLAN_NO_COMBINE is refused).  The plan is for mfa_block_decode_run alone.
- * The work is split as there, by cost: 4 a tile of 128 tokens and 6 a boundary between units
+ * The work is split as there, by cost: 4 a tile of 128 tokens and 16 a boundary between units
  * (sequence, key/value head, and a group of the new tokens whose rows, tokens x query heads of
  * the head, are at most 64), or, where every unit can have a CTA, evenly: units whole
  * (MFA_PLAN_WHOLE_UNITS) or in parts of at most max_tiles_per_cta tiles (MFA_PLAN_EVEN_SPLIT).

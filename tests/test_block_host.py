@@ -73,7 +73,8 @@ def test_plan_sizes(lib, kw, rows, units):
     assert plan.total_tiles == 6 * units // 4 and plan.num_ctas == plan.total_tiles
     assert plan.num_partials == units + plan.num_ctas - 1
     o_end = (256 + plan.num_partials * rows * pr.head_dim * 4 + 255) // 256 * 256
-    assert plan.workspace_bytes == (o_end + plan.num_partials * rows * 4 + 255) // 256 * 256
+    lse_end = (o_end + plan.num_partials * rows * 4 + 255) // 256 * 256
+    assert plan.workspace_bytes == (lse_end + units * 8 + 255) // 256 * 256
 
 
 def test_plan_grids(lib):
