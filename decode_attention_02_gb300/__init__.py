@@ -459,30 +459,48 @@ class Decoder:
                             k_cache, v_cache, k_scale, v_scale, self.workspace, stream)
 
 
-def _is(x, name: str, dtype, shape, device) -> None:
-    """x must be a contiguous tensor of this dtype and shape on this device."""
-    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+def _fits(x, dtype, shape, index: int) -> bool:
+    """x is a contiguous tensor of this dtype and shape on CUDA device ``index``."""
+    return x.dtype is dtype and x.shape == shape and x.get_device() == index and x.is_contiguous()
+
+
+def _refuse(index: int, *wanted) -> None:
+    """Raise for the first (name, tensor, dtype, shape) that _fits does not hold for."""
+    for name, x, dtype, shape in wanted:
+        if not _fits(x, dtype, shape, index):
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                             f"{x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
 
 
 class _OnDevice:
-    """Makes a device current for a call on its tensors; used where another one is current."""
+    """The device that a handle's buffers live on; a call makes it current where another one is."""
 
     def __init__(self, device):
         import torch
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.device = torch.device("cuda") if device is None else torch.device(device)
         if self.device.type != "cuda":
             raise ValueError("expected a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._torch, self._index, self._lib = torch, self.device.index, load_library()
+        # the current stream's handle without a Stream object around it, where torch has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def _run(self, call, stream):
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            return call(_stream(stream))
-        with torch.cuda.device(self.device):
-            return call(_stream(stream))
+    def _call(self, function, where: str, args, stream) -> None:
+        """One library call on ``stream`` (None: the device's current stream)."""
+        index = self._index
+        if stream is None:
+            stream = self._current(index)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if self._torch.cuda.current_device() == index:
+            status = function(*args, stream)
+        else:
+            with self._torch.cuda.device(index):
+                status = function(*args, stream)
+        if status != MFA_OK:
+            raise MfaError(status, where)
 
 
 class BlockDecoder(_OnDevice):
@@ -498,8 +516,8 @@ class BlockDecoder(_OnDevice):
                  num_kv_heads: int = 1, head_dim: int = HEAD_DIM, scale_tokens: int = 64,
                  softmax_scale: Optional[float] = None, host_seq_lens=None, max_seq_len: int = 0, force_ctas: int = 0,
                  flags: int = 0, device=None, out_dtype: int = MFA_OUT_BF16, tokens_per_seq: int = 1):
-        import torch
         super().__init__(device)
+        torch = self._torch
         self.scale_tokens = int(scale_tokens)
         self.problem = make_problem(batch, max_pages_per_seq, num_blocks, MFA_KV_FP8_E4M3, softmax_scale,
                                     num_q_heads=num_q_heads, head_dim=head_dim, out_dtype=out_dtype,
@@ -510,41 +528,50 @@ class BlockDecoder(_OnDevice):
             self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
                                               force_ctas, flags)
             self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+        self._refs = (ctypes.byref(self.plan), ctypes.byref(self.problem))
         rows = batch * tokens_per_seq
-        self._q_shape = (rows, num_q_heads, head_dim)
-        self._cache_shape = (num_blocks, num_kv_heads, PAGE_SIZE, head_dim)
-        self._scale_shape = (num_blocks, num_kv_heads, PAGE_SIZE // self.scale_tokens)
-        self._table_shape = (batch, max_pages_per_seq)
+        self._q_shape = torch.Size((rows, num_q_heads, head_dim))
+        self._lse_shape = self._q_shape[:2]
+        self._cache_shape = torch.Size((num_blocks, num_kv_heads, PAGE_SIZE, head_dim))
+        self._scale_shape = torch.Size((num_blocks, num_kv_heads, PAGE_SIZE // self.scale_tokens))
+        self._table_shape = torch.Size((batch, max_pages_per_seq))
+        self._batch_shape = self._table_shape[:1]
+        self._row_shape = (num_kv_heads, head_dim)
+        self._types = (torch.bfloat16, torch.uint8, torch.float32, torch.int32)
         self._out_dtype = torch.float32 if out_dtype == MFA_OUT_FP32 else torch.bfloat16
 
-    def _check_cache(self, k_cache, v_cache, k_scale, v_scale, block_table):
-        import torch
-        _is(k_cache, "k_cache", torch.uint8, self._cache_shape, self.device)
-        _is(v_cache, "v_cache", torch.uint8, self._cache_shape, self.device)
-        _is(k_scale, "k_scale", torch.float32, self._scale_shape, self.device)
-        _is(v_scale, "v_scale", torch.float32, self._scale_shape, self.device)
-        _is(block_table, "block_table", torch.int32, self._table_shape, self.device)
+    def _cache_fits(self, k_cache, v_cache, k_scale, v_scale, block_table) -> bool:
+        _, u8, f32, i32 = self._types
+        i, codes, scales = self._index, self._cache_shape, self._scale_shape
+        return (_fits(k_cache, u8, codes, i) and _fits(v_cache, u8, codes, i) and _fits(k_scale, f32, scales, i) and
+                _fits(v_scale, f32, scales, i) and _fits(block_table, i32, self._table_shape, i))
+
+    def _cache_wants(self, k_cache, v_cache, k_scale, v_scale, block_table):
+        _, u8, f32, i32 = self._types
+        return (("k_cache", k_cache, u8, self._cache_shape), ("v_cache", v_cache, u8, self._cache_shape),
+                ("k_scale", k_scale, f32, self._scale_shape), ("v_scale", v_scale, f32, self._scale_shape),
+                ("block_table", block_table, i32, self._table_shape))
 
     def __call__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None, lse=None, stream=None):
         """One decode step: (out [batch * tokens, num_q_heads, head_dim], lse [.., num_q_heads])."""
-        import torch
-        _is(q, "q", torch.bfloat16, self._q_shape, self.device)
-        self._check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
-        _is(seq_lens, "seq_lens", torch.int32, self._table_shape[:1], self.device)
+        bf16, _, f32, i32 = self._types
+        i = self._index
+        if not (_fits(q, bf16, self._q_shape, i) and _fits(seq_lens, i32, self._batch_shape, i) and
+                self._cache_fits(k_cache, v_cache, k_scale, v_scale, block_table)):
+            _refuse(i, ("q", q, bf16, self._q_shape), ("seq_lens", seq_lens, i32, self._batch_shape),
+                    *self._cache_wants(k_cache, v_cache, k_scale, v_scale, block_table))
         if out is None:
-            out = torch.empty(self._q_shape, dtype=self._out_dtype, device=self.device)
-        else:
-            _is(out, "out", self._out_dtype, self._q_shape, self.device)
+            out = self._torch.empty(self._q_shape, dtype=self._out_dtype, device=self.device)
+        elif not _fits(out, self._out_dtype, self._q_shape, i):
+            _refuse(i, ("out", out, self._out_dtype, self._q_shape))
         if lse is None:
-            lse = torch.empty(self._q_shape[:2], dtype=torch.float32, device=self.device)
-        else:
-            _is(lse, "lse", torch.float32, self._q_shape[:2], self.device)
-        lib = load_library()
-        st = self._run(lambda s: lib.mfa_block_decode_run(
-            self.plan, self.problem, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes, s), stream)
-        _check(st, "mfa_block_decode_run")
+            lse = self._torch.empty(self._lse_shape, dtype=f32, device=self.device)
+        elif not _fits(lse, f32, self._lse_shape, i):
+            _refuse(i, ("lse", lse, f32, self._lse_shape))
+        self._call(self._lib.mfa_block_decode_run, "mfa_block_decode_run",
+                   (*self._refs, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                    k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream)
         return out, lse
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
@@ -553,23 +580,24 @@ class BlockDecoder(_OnDevice):
         being rows offsets[b] .. offsets[b + 1] - 1 (``offsets`` int32 [batch + 1], ``max_new`` their largest
         count), or ``tokens_per_seq`` each.  ``device_status``: the decoder's workspace by default, so that
         mfa_read_device_status(decoder.workspace) reports both steps."""
-        import torch
-        rows = int(k_new.shape[0])
-        shape = (rows,) + self._cache_shape[1:4:2]
-        _is(k_new, "k_new", torch.bfloat16, shape, self.device)
-        _is(v_new, "v_new", torch.bfloat16, shape, self.device)
-        self._check_cache(k_cache, v_cache, k_scale, v_scale, block_table)
-        _is(positions, "positions", torch.int32, self._table_shape[:1], self.device)
-        if offsets is not None:
-            _is(offsets, "offsets", torch.int32, (self._table_shape[0] + 1,), self.device)
-        status = self.workspace if device_status is None else device_status
-        lib = load_library()
-        st = self._run(lambda s: lib.mfa_block_kv_append(
-            self.problem, self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
-            None if offsets is None else offsets.data_ptr(), int(max_new), positions.data_ptr(),
-            block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            _ptr(status), s), stream)
-        _check(st, "mfa_block_kv_append")
+        bf16, _, _, i32 = self._types
+        i = self._index
+        rows = k_new.shape[0]
+        shape = (rows, *self._row_shape)
+        counts = (self._batch_shape[0] + 1,)
+        if not (_fits(k_new, bf16, shape, i) and _fits(v_new, bf16, shape, i) and
+                _fits(positions, i32, self._batch_shape, i) and (offsets is None or _fits(offsets, i32, counts, i)) and
+                self._cache_fits(k_cache, v_cache, k_scale, v_scale, block_table)):
+            _refuse(i, ("k_new", k_new, bf16, shape), ("v_new", v_new, bf16, shape),
+                    ("positions", positions, i32, self._batch_shape),
+                    *(() if offsets is None else (("offsets", offsets, i32, counts),)),
+                    *self._cache_wants(k_cache, v_cache, k_scale, v_scale, block_table))
+        status = self.workspace.data_ptr() if device_status is None else _ptr(device_status)
+        self._call(self._lib.mfa_block_kv_append, "mfa_block_kv_append",
+                   (self._refs[1], self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
+                    None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
+                    block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                    v_scale.data_ptr(), status), stream)
 
 
 class Rope(_OnDevice):
@@ -583,8 +611,8 @@ class Rope(_OnDevice):
 
     def __init__(self, head_dim: int, sections: Sequence[int], theta: float = 1e4, pairing: str = "half",
                  interleaved: bool = False, own_spectrum: bool = False, position_scale: float = 1.0, device=None):
-        import torch
         super().__init__(device)
+        torch = self._torch
         if pairing not in ("half", "adjacent"):
             raise ValueError(f"pairing: expected 'half' or 'adjacent', got {pairing!r}")
         if not 1 <= len(sections) <= MFA_ROPE_MAX_AXES:
@@ -597,40 +625,51 @@ class Rope(_OnDevice):
                                     (MFA_ROPE_OWN_SPECTRUM if own_spectrum else 0), float(theta), float(position_scale))
         table = mfa_rope_table(self.config)
         self.table = torch.frombuffer(bytearray(bytes(table)), dtype=torch.uint8).to(self.device)
+        self._config_ref = ctypes.byref(self.config)
+        self._dtypes = {torch.bfloat16: MFA_OUT_BF16, torch.float32: MFA_OUT_FP32}
 
     def _rows(self, x, out, name: str, rows: int, dtype) -> MfaRopeRows:
-        for t, what in ((x, name), (out, name + "_out")):
-            if t.dtype is not dtype or t.dim() != 3 or t.shape[0] != rows or t.shape[2] != self.head_dim or \
-                    t.shape != x.shape or t.device != self.device or \
-                    (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim))):
-                raise ValueError(f"{what}: expected {dtype} [{rows}, heads, {self.head_dim}] on {self.device} with "
-                                 f"each row's heads side by side, got {t.dtype} {tuple(t.shape)} strides {t.stride()} "
-                                 f"on {t.device}")
-        least = x.shape[1] * self.head_dim   # (a single row has no stride of its own)
-        return MfaRopeRows(x.data_ptr(), out.data_ptr(), max(x.stride(0), least) if rows < 2 else x.stride(0),
-                           max(out.stride(0), least) if rows < 2 else out.stride(0), x.shape[1])
+        """x and its output (x's shape; None: a new tensor) as the library takes them, and the output."""
+        shape, d = x.shape, self.head_dim
+        if len(shape) != 3 or shape[0] != rows or shape[2] != d or x.dtype is not dtype or x.get_device() != self._index:
+            raise ValueError(f"{name}: expected {dtype} [{rows}, heads, {d}] on {self.device}, got {x.dtype} "
+                             f"{tuple(shape)} on {x.device}")
+        line = shape[1] * d
+        strides = []
+        if out is None:
+            out = self._torch.empty(shape, dtype=dtype, device=self.device)
+        elif out is not x and (out.shape != shape or out.dtype is not dtype or out.get_device() != self._index):
+            raise ValueError(f"{name}_out: expected {dtype} {tuple(shape)} on {self.device}, got {out.dtype} "
+                             f"{tuple(out.shape)} on {out.device}")
+        for t in (x, out):
+            if t.is_contiguous():
+                strides.append(line)
+                continue
+            a, b, c = t.stride()
+            if c != 1 or (shape[1] > 1 and b != d):
+                raise ValueError(f"{name}: each row's heads must lie side by side, got strides {t.stride()}")
+            strides.append(a if rows > 1 else line)   # (a single row has no stride of its own)
+        return MfaRopeRows(x.data_ptr(), out.data_ptr(), *strides, shape[1]), out
 
     def __call__(self, q, k, positions, inverse: bool = False, q_out=None, k_out=None, stream=None):
         """Turned rows (q_out, k_out) of q and k, [rows, heads, head_dim] in bf16 or fp32 (either may be None; rows
         may be strided, as columns of one projection); positions int32 [axes, rows].  Pass q_out = q and k_out = k
         to turn in place.  ``inverse``: by the negative angles, which is the gradient of the forward call."""
-        import torch
         some = k if q is None else q
         if some is None:
             raise ValueError("expected q or k")
-        rows, dtype = int(some.shape[0]), some.dtype
-        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        rows, dtype = some.shape[0], some.dtype
+        kind = self._dtypes.get(dtype)
+        if kind is None:
             raise ValueError(f"expected bf16 or fp32 rows, got {dtype}")
-        _is(positions, "positions", torch.int32, (self.axes, rows), self.device)
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=self.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=self.device)
-        rq = None if q is None else self._rows(q, q_out, "q", rows, dtype)
-        rk = None if k is None else self._rows(k, k_out, "k", rows, dtype)
-        lib = load_library()
-        st = self._run(lambda s: lib.mfa_rope_run(
-            self.config, self.table.data_ptr(), positions.data_ptr(), rows,
-            MFA_OUT_BF16 if dtype is torch.bfloat16 else MFA_OUT_FP32, 1 if inverse else 0, rq, rk, s), stream)
-        _check(st, "mfa_rope_run")
+        if not _fits(positions, self._torch.int32, (self.axes, rows), self._index):
+            _refuse(self._index, ("positions", positions, self._torch.int32, (self.axes, rows)))
+        rq = rk = None
+        if q is not None:
+            rq, q_out = self._rows(q, q_out, "q", rows, dtype)
+        if k is not None:
+            rk, k_out = self._rows(k, k_out, "k", rows, dtype)
+        self._call(self._lib.mfa_rope_run, "mfa_rope_run",
+                   (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, 1 if inverse else 0,
+                    rq, rk), stream)
         return q_out, k_out
