@@ -11,10 +11,9 @@
 //
 // An item is one (block, head, K or V): its new rows are read once, into registers; their
 // maximum gives the scale; the codes are written.  Items share nothing, so the work is one
-// pass over the data with no atomics but error flags.
-//   - Prompts: one CTA of 256 threads an item, the rows of a whole block (up to 64 x 256
-//     elements) in 8 registers of 8 elements a thread, all loads in flight together.
-//   - Few rows a sequence (a decode step): one warp an item, up to 4 rows; 8 items a CTA.
+// pass over the data with no atomics but error flags.  A thread holds up to 8 chunks of 8
+// elements, all loads in flight together, and an item gets as many threads as that takes: a
+// warp for the row of a decode step or a block of 16 x 128, a whole CTA for one of 64 x 256.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,10 +31,8 @@ namespace mfa {
 
 constexpr int kBlkPage = 64;
 constexpr int kBlkThreads = 256;
-constexpr int kFewRows = 4;           // most new rows a block gets on the warp path
 constexpr int kChunks = 8;            // 8-element chunks a thread holds
 static_assert(kChunks * kBlkThreads * 8 >= 64 * 256, "a CTA holds a whole block of 64 rows of 256");
-static_assert(kChunks * 32 * 8 >= kFewRows * 256, "a warp holds the few rows");
 
 struct BlockAppendParams {
   const uint4* k_new;        // bf16 [num_new, G, d] as 8-element chunks
@@ -92,7 +89,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t codes, float r) {
   return out;
 }
 
-// kItemThreads = 256: an item a CTA; 32: an item a warp.
+// kItemThreads threads an item, 256 / kItemThreads items a CTA.
 template <int kItemThreads>
 __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __grid_constant__ BlockAppendParams p) {
   constexpr int kItems = kBlkThreads / kItemThreads;
@@ -103,7 +100,7 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   // item = ((sequence, touched block m), head, K or V)
   const long long items = static_cast<long long>(p.batch) * p.most_blocks * p.heads * 2;
   const long long item = static_cast<long long>(blockIdx.x) * kItems + threadIdx.x / kItemThreads;
-  if (item >= items) return;   // (the last CTA of the warp path: whole warps leave)
+  if (item >= items) return;   // (all of an item's threads leave together, here and below)
   const bool is_v = (item & 1) != 0;
   const long long bh = item >> 1;
   const int g = static_cast<int>(bh % p.heads);
@@ -135,6 +132,19 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   if (first >= t0 + n) return;
   const int lo = max(t0, first), hi = min(t0 + n, first + bt);  // new tokens [lo, hi) of the block
   const int blk = p.block_table[static_cast<size_t>(b) * p.max_pages + first / kBlkPage];
+  // the new rows, in registers; the loads go out before the page id is looked at
+  const uint4* src = (is_v ? p.v_new : p.k_new);
+  const int chunks = (hi - lo) << p.log_chunks;
+  uint4 x[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = it + i * kItemThreads;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < chunks) {
+      const size_t r = static_cast<size_t>(r0 + (lo - t0) + (c >> p.log_chunks)) * p.heads + g;
+      x[i] = __ldg(src + (r << p.log_chunks) + (c & ((1 << p.log_chunks) - 1)));
+    }
+  }
   if (blk < 0 || blk >= p.num_blocks) {
     if (reporter) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
     return;
@@ -145,10 +155,6 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   const bool begun = lo > first;
   const float s_old = begun ? *scale : 0.f;
 
-  // the new rows, in registers
-  const uint4* src = (is_v ? p.v_new : p.k_new);
-  const int chunks = (hi - lo) << p.log_chunks;
-  uint4 x[kChunks];
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
@@ -159,24 +165,23 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
     }
   }
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    if (it + i * kItemThreads < chunks) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  for (int i = 0; i < kChunks; ++i) {   // (zeros past the rows)
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float u = fabsf(bf16_bits_lo(w[k])), v = fabsf(bf16_bits_hi(w[k]));
-        a = fmaxf(a, u < INFINITY ? u : 0.f);   // (false for NaN too)
-        a = fmaxf(a, v < INFINITY ? v : 0.f);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float u = fabsf(bf16_bits_lo(w[k])), v = fabsf(bf16_bits_hi(w[k]));
+      a = fmaxf(a, u < INFINITY ? u : 0.f);   // (false for NaN too)
+      a = fmaxf(a, v < INFINITY ? v : 0.f);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   if constexpr (kItemThreads > 32) {
+    const int it_item = threadIdx.x / kItemThreads;
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = a;
-    __syncthreads();   // (and every thread has read s_old)
+    named_bar_sync(1 + it_item, kItemThreads);   // (and every thread of the item has read s_old)
 #pragma unroll
-    for (int w = 0; w < kItemThreads / 32; ++w) a = fmaxf(a, wmax[w]);
+    for (int w = 0; w < kItemThreads / 32; ++w) a = fmaxf(a, wmax[it_item * (kItemThreads / 32) + w]);
   }
   const float need = pow2_scale(a);
   const float s = begun ? fmaxf(s_old, need) : need;
@@ -253,9 +258,11 @@ extern "C" mfa_status mfa_block_kv_append(const mfa_problem* pr, int32_t scale_t
   const long long most =
       std::min<long long>((static_cast<long long>(most_rows) + scale_tokens - 2) / scale_tokens + 1,
                           static_cast<long long>(pr->max_pages_per_seq) * (kBlkPage / scale_tokens));
-  const bool few = most_rows <= kFewRows;
   const long long items = pr->batch * most * pr->num_kv_heads * 2;
-  const long long ctas = few ? (items + 7) / 8 : items;
+  // threads an item: kChunks chunks each of the rows that a block can get
+  const int need = std::min(most_rows, static_cast<int>(scale_tokens)) * (pr->head_dim / 8) / kChunks;
+  const int threads = need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
+  const long long ctas = (items * threads + kBlkThreads - 1) / kBlkThreads;
   if (ctas > INT_MAX) return MFA_ERR_INVALID_ARG;
   BlockAppendParams p;
   p.k_new = static_cast<const uint4*>(k_new);
@@ -287,8 +294,11 @@ extern "C" mfa_status mfa_block_kv_append(const mfa_problem* pr, int32_t scale_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, mfa_block_append_kernel<32>, p)
-                            : cudaLaunchKernelEx(&cfg, mfa_block_append_kernel<256>, p);
+  void (*const fn)(BlockAppendParams) = threads == 32    ? mfa_block_append_kernel<32>
+                                        : threads == 64  ? mfa_block_append_kernel<64>
+                                        : threads == 128 ? mfa_block_append_kernel<128>
+                                                         : mfa_block_append_kernel<256>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
   if (e != cudaSuccess) return cuda_fail(e, "block append launch");
   return MFA_OK;
 }

@@ -28,7 +28,9 @@
 namespace mfa {
 
 constexpr int kRopeMaxDim = 512;
-constexpr int kRopeHeads = 4;        // heads a thread turns, all loaded before the first is used
+// heads a thread turns, all loaded before the first is used
+template <typename T>
+constexpr int kRopeHeads = sizeof(T) == 2 ? 4 : 2;
 constexpr int kRopeMaxThreads = 512;
 
 struct RopeSide {
@@ -47,42 +49,50 @@ struct RopeParams {
   int inverse;
 };
 
-// kVec elements, widened to fp32
+// kVec elements as they lie in memory (widened when they are used: a thread holds its heads'
+// loads in half the registers)
 template <typename T, int kVec>
 struct RopeVec {
-  float v[kVec];
+  static constexpr int kWords = kVec == 8 ? kVec * sizeof(T) / 4 : kVec;
+  uint32_t w[kWords];   // kVec = 1: one element in the low bits
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kVec == 8 && sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (kVec == 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(e[i] << 16);
-        v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
       }
-    } else if constexpr (kVec == 8) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (sizeof(T) == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = static_cast<float>(p[i]);
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kVec == 8 && sizeof(T) == 2) {
-      uint32_t e[4];
+  __device__ __forceinline__ void store_raw(T* p) const {
+    if constexpr (kVec == 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        e[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
-    } else if constexpr (kVec == 8) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
     } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) p[i] = static_cast<T>(v[i]);
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  // the pair of values i, i + 1 (kVec = 1: lo alone)
+  __device__ __forceinline__ void set(int i, float lo, float hi) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(lo);
+      if constexpr (kVec > 1) w[i + 1] = __float_as_uint(hi);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
 };
@@ -109,11 +119,12 @@ __global__ void __launch_bounds__(kRopeMaxThreads) mfa_rope_kernel(const __grid_
     a0 = 2 * p.pairs + (u - p.turned_units) * kVec;
     b0 = a0;
   }
-  RopeVec<T, kVec> a[kRopeHeads], b[kRopeHeads];
+  constexpr int kN = kRopeHeads<T>;
+  RopeVec<T, kVec> a[kN], b[kN];
   const int heads = p.q.heads + p.k.heads;
-  const int h0 = blockIdx.y * (blockDim.y * kRopeHeads) + threadIdx.y;
+  const int h0 = blockIdx.y * (blockDim.y * kN) + threadIdx.y;
 #pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const int h = h0 + i * blockDim.y;
     if (h < heads) {
       const bool is_q = h < p.q.heads;
@@ -151,34 +162,37 @@ __global__ void __launch_bounds__(kRopeMaxThreads) mfa_rope_kernel(const __grid_
     }
   }
 #pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
+  for (int i = 0; i < kN; ++i) {
     const int h = h0 + i * blockDim.y;
     if (h >= heads) continue;
     const bool is_q = h < p.q.heads;
     T* dst = static_cast<T*>(is_q ? p.q.out : p.k.out) + row * (is_q ? p.q.out_stride : p.k.out_stride) +
              static_cast<long long>(is_q ? h : h - p.q.heads) * p.head_dim;
     if (!turned) {
-      a[i].store(dst + a0);
+      a[i].store_raw(dst + a0);
       continue;
     }
-    if constexpr (kTwo) {
+    RopeVec<T, kVec> u, v;
+    if constexpr (kVec == 1) {
+      const float x = a[i].get(0), y = b[i].get(0);
+      u.set(0, x * c[0] - y * s[0], 0.f);
+      v.set(0, y * c[0] + x * s[0], 0.f);
+    } else if constexpr (kTwo) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float x = a[i].v[j], y = b[i].v[j];
-        a[i].v[j] = x * c[j] - y * s[j];
-        b[i].v[j] = y * c[j] + x * s[j];
+      for (int j = 0; j < kVec; j += 2) {
+        const float x0 = a[i].get(j), y0 = b[i].get(j), x1 = a[i].get(j + 1), y1 = b[i].get(j + 1);
+        u.set(j, x0 * c[j] - y0 * s[j], x1 * c[j + 1] - y1 * s[j + 1]);
+        v.set(j, y0 * c[j] + x0 * s[j], y1 * c[j + 1] + x1 * s[j + 1]);
       }
-      a[i].store(dst + a0);
-      b[i].store(dst + b0);
     } else {
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const float x = a[i].v[2 * j], y = a[i].v[2 * j + 1];
-        a[i].v[2 * j] = x * c[j] - y * s[j];
-        a[i].v[2 * j + 1] = y * c[j] + x * s[j];
+        const float x = a[i].get(2 * j), y = a[i].get(2 * j + 1);
+        u.set(2 * j, x * c[j] - y * s[j], y * c[j] + x * s[j]);
       }
-      a[i].store(dst + a0);
     }
+    u.store_raw(dst + a0);
+    if constexpr (kTwo) v.store_raw(dst + b0);
   }
 }
 
@@ -302,10 +316,11 @@ extern "C" mfa_status mfa_rope_run(const mfa_rope_config* c, const mfa_rope_pair
   const bool in_place = (p.q.heads == 0 || p.q.in == p.q.out) && (p.k.heads == 0 || p.k.in == p.k.out);
   p.units = p.turned_units + (in_place ? 0 : (c->head_dim - c->rotary_dim) / vec);
   p.inverse = inverse;
-  // threads: a head's units by as many heads as a CTA can take, each thread kRopeHeads of them
+  // threads: a head's units by as many heads as a CTA can take, each thread some of them
   const int most = std::max(1, kRopeMaxThreads / p.units);
-  const int ny = static_cast<int>(std::min<long long>(most, (heads + kRopeHeads - 1) / kRopeHeads));
-  const long long gy = (heads + static_cast<long long>(ny) * kRopeHeads - 1) / (static_cast<long long>(ny) * kRopeHeads);
+  const int each = dtype == MFA_OUT_BF16 ? kRopeHeads<__nv_bfloat16> : kRopeHeads<float>;
+  const int ny = static_cast<int>(std::min<long long>(most, (heads + each - 1) / each));
+  const long long gy = (heads + static_cast<long long>(ny) * each - 1) / (static_cast<long long>(ny) * each);
   if (gy > 65535) return MFA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_rows), static_cast<unsigned>(gy), 1);
