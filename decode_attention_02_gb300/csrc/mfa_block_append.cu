@@ -65,15 +65,37 @@ __device__ __forceinline__ float pow2_scale(float a) {
 // Eight bf16 values to eight e4m3 codes of x / s.  Where s is a power of two with a normal
 // reciprocal the product with it is the quotient, exactly (a quotient below the normal range
 // rounds to a zero code either way).
-__device__ __forceinline__ uint2 encode_chunk(uint4 x, float s, float inv, bool exact_inv) {
+template <bool kProduct>
+__device__ __forceinline__ uint2 encode_chunk(uint4 x, float s) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float lo = bf16_bits_lo(w[i]), hi = bf16_bits_hi(w[i]);
-    c[i] = exact_inv ? e4m3x2_rn_sat(lo * inv, hi * inv) : e4m3x2_rn_sat(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+    c[i] = kProduct ? e4m3x2_rn_sat(lo * s, hi * s) : e4m3x2_rn_sat(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+// (a scale of another kind is met where a begun block keeps the one it had: out of the way)
+__device__ __noinline__ uint2 encode_chunk_by_division(uint4 x, float s) { return encode_chunk<false>(x, s); }
+
+// The largest |x| of a chunk's bf16 values as bit patterns, pairwise: magnitudes order as integers,
+// infinities and NaN above all finite ones.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint4 x) {
+  m = __vmaxu2(m, x.x & 0x7FFF7FFFu);
+  m = __vmaxu2(m, x.y & 0x7FFF7FFFu);
+  m = __vmaxu2(m, x.z & 0x7FFF7FFFu);
+  return __vmaxu2(m, x.w & 0x7FFF7FFFu);
+}
+// The same with what is not finite left out (as zeros).
+__device__ __noinline__ uint4 finite_only(uint4 x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Four e4m3 codes times r, rounded back to e4m3 (e4m3 values are exact in f16).
@@ -91,7 +113,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t codes, float r) {
 
 // kItemThreads threads an item, 256 / kItemThreads items a CTA.
 template <int kItemThreads>
-__global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __grid_constant__ BlockAppendParams p) {
+__global__ void __launch_bounds__(kBlkThreads, 5) mfa_block_append_kernel(const __grid_constant__ BlockAppendParams p) {
   constexpr int kItems = kBlkThreads / kItemThreads;
   __shared__ float wmax[kBlkThreads / 32];
   grid_dep_wait();
@@ -133,18 +155,15 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   const int lo = max(t0, first), hi = min(t0 + n, first + bt);  // new tokens [lo, hi) of the block
   const int blk = p.block_table[static_cast<size_t>(b) * p.max_pages + first / kBlkPage];
   // the new rows, in registers; the loads go out before the page id is looked at
-  const uint4* src = (is_v ? p.v_new : p.k_new);
+  // (a row's chunks divide the item's threads: a thread's chunks lie a fixed step apart)
   const int chunks = (hi - lo) << p.log_chunks;
+  const uint4* src = (is_v ? p.v_new : p.k_new) +
+                     ((static_cast<size_t>(r0 + (lo - t0) + (it >> p.log_chunks)) * p.heads + g) << p.log_chunks) +
+                     (it & ((1 << p.log_chunks) - 1));
+  const int step = kItemThreads * p.heads;
   uint4 x[kChunks];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = it + i * kItemThreads;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < chunks) {
-      const size_t r = static_cast<size_t>(r0 + (lo - t0) + (c >> p.log_chunks)) * p.heads + g;
-      x[i] = __ldg(src + (r << p.log_chunks) + (c & ((1 << p.log_chunks) - 1)));
-    }
-  }
+  for (int i = 0; i < kChunks; ++i) x[i] = it + i * kItemThreads < chunks ? __ldg(src + i * step) : make_uint4(0u, 0u, 0u, 0u);
   if (blk < 0 || blk >= p.num_blocks) {
     if (reporter) atomicOr(p.status, MFA_DEV_BAD_BLOCK);
     return;
@@ -155,25 +174,15 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   const bool begun = lo > first;
   const float s_old = begun ? *scale : 0.f;
 
-  float a = 0.f;
+  uint32_t bits = 0;   // (zeros past the rows)
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = it + i * kItemThreads;
-    if (c < chunks) {
-      const size_t r = static_cast<size_t>(r0 + (lo - t0) + (c >> p.log_chunks)) * p.heads + g;
-      x[i] = __ldg(src + (r << p.log_chunks) + (c & ((1 << p.log_chunks) - 1)));
-    }
+  for (int i = 0; i < kChunks; ++i) bits = max_bits(bits, x[i]);
+  if (max(bits & 0xFFFFu, bits >> 16) >= 0x7F80u) {   // infinities or NaN: they do not count
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) bits = max_bits(bits, finite_only(x[i]));
   }
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {   // (zeros past the rows)
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float u = fabsf(bf16_bits_lo(w[k])), v = fabsf(bf16_bits_hi(w[k]));
-      a = fmaxf(a, u < INFINITY ? u : 0.f);   // (false for NaN too)
-      a = fmaxf(a, v < INFINITY ? v : 0.f);
-    }
-  }
+  float a = __uint_as_float(max(bits & 0xFFFFu, bits >> 16) << 16);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   if constexpr (kItemThreads > 32) {
@@ -191,10 +200,9 @@ __global__ void __launch_bounds__(kBlkThreads) mfa_block_append_kernel(const __g
   uint2* dst = reinterpret_cast<uint2*>(rows);
   const int at = ((lo % kBlkPage) << p.log_chunks);       // first new row's chunk in the page
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = it + i * kItemThreads;
-    if (c < chunks) dst[at + c] = encode_chunk(x[i], s, inv, exact_inv);
-  }
+  for (int i = 0; i < kChunks; ++i)
+    if (it + i * kItemThreads < chunks)
+      dst[at + it + i * kItemThreads] = exact_inv ? encode_chunk<true>(x[i], inv) : encode_chunk_by_division(x[i], s);
   if (begun && s > s_old) {
     const float r = __fdiv_rn(s_old, s);
     const int from = (first % kBlkPage) << p.log_chunks;
