@@ -43,6 +43,8 @@ MFA_DEV_RANGE = 0x10
 MFA_PLAN_CHECK = 0x1
 MFA_PLAN_NO_COMBINE = 0x2
 MFA_PLAN_EARLY_METADATA = 0x4
+MFA_PLAN_EVEN_SPLIT = 0x100      # set by mfa_block_decode_plan alone
+MFA_PLAN_UNIT_CLUSTERS = 0x200   # likewise
 
 MFA_ROPE_HALF = 0
 MFA_ROPE_ADJACENT = 1

@@ -30,7 +30,6 @@ constexpr int kBTile = 128;           // tokens of a tile (two pages)
 constexpr int kBRows = 64;            // query rows (new tokens x heads of one group) a unit holds at most
 constexpr int kBCostTile = 4;         // schedule: cost of a tile
 constexpr int kBCostUnit = 16;        // and of a unit boundary inside a CTA's range
-constexpr int kBSwitchTiles = 5;      // plan: tiles that a second unit in a CTA's range is worth (see the plan)
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
 constexpr int kBScaleWarp = 2, kBPvWarp = 3, kBSoftmaxWarp0 = 4;   // warps: producer, QK issuer, scales, PV issuer, softmax
@@ -121,7 +120,8 @@ struct BlockDecodeParams {
   int num_partials;
   int2* parts;               // split by cost: [units] slots of a unit's first and last part
   int narrow;                // split by cost: G times the whole cost fits 32 bits
-  int quantum;               // even split: most tiles of a part, or -1 for whole units; 0: split by cost
+  int quantum;               // even split: most tiles of a part; else 0
+  int cluster;               // CTAs of a unit, one cluster; 0: split evenly or by cost
   int log_scale;             // log2(scale_tokens)
   int max_pages, num_blocks;
   float scale_log2;          // softmax_scale * log2(e)
@@ -137,13 +137,15 @@ struct BlockDecodeParams {
 // nothing for an empty sequence).  CTA g of G owns the tiles whose cost lies in
 // [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.
 //
-// Even split (chosen by the plan where the units are fewer than the CTAs and lengths allow):
-// each unit of T tiles is cut into n = ceil(T / quantum) parts as equal as they come (or not at
-// all).  Part i of reader r of sequence b is item R P_b + r n + i (R readers, P_b parts of one
-// reader of each sequence before b), and CTA g takes items g, g + G, ...: one part each, none
-// with the end of one unit and the beginning of another.
+// Two other ways, for few units:
+// Clusters: every unit (b, r) has c CTAs of its own, CTA c (r B + b) + i taking part i, tiles
+// [floor(i T / c), floor((i + 1) T / c)); c > 1: the CTAs are a cluster and exchange their results.
+// Even split: a unit of T tiles is cut into n = ceil(T / quantum) parts as equal as they come.
+// Part i of reader r of sequence b is item R P_b + r n + i (R readers, P_b parts of one reader of
+// each sequence before b), and CTA g takes items g, g + G, ...: one part each, none with the end
+// of one unit and the beginning of another.
 __device__ __forceinline__ int even_parts(int T, int quantum) {
-  return T <= quantum || quantum < 0 ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
+  return T <= quantum ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
 }
 // first of a unit's T tiles at cost >= X
 template <typename I>
@@ -187,7 +189,7 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
 struct __align__(16) BlockSegment {
   int b, kvh, tg, L;       // sequence, key/value head, group of new tokens, length
   int lo, hi;              // tiles
-  int slot;                // of the partial result; -1: the whole unit
+  int slot;                // of the partial result; -1: the whole unit; -2: a part, for the cluster's exchange
 };
 
 __device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSegment* seg, int at, int b, int r, int L, int lo,
@@ -303,10 +305,30 @@ __device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int 
   cost_segments<long long>(p, cap, seg, nseg, tiles, bad);
 }
 
+__device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float (&a)[4], float scale) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a[0] * scale, a[1] * scale), hi = __floats2bfloat162_rn(a[2] * scale, a[3] * scale);
+  *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+__device__ __forceinline__ void unit_segment(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                             bool& bad) {
+  if ((threadIdx.x & 31) != 0) return;
+  const unsigned c = p.cluster, unit = c == 1 ? blockIdx.x : blockIdx.x / c, i = blockIdx.x - unit * c;
+  const int r = unit / p.batch, b = unit - r * p.batch;
+  const int L = clamp_len(p.seq_lens[b], cap, bad);
+  const unsigned T = block_tiles(L);
+  const int lo = c == 1 ? 0 : i * T / c, hi = c == 1 ? T : (i + 1) * T / c;
+  add_segment(p, seg, 0, b, r, L, lo, hi, -2);   // (without tiles too: the exchange wants the unit)
+  nseg = lo < hi ? 1 : 0;
+  tiles = hi - lo;
+}
+
 __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
   int nseg = 0, tiles = 0;
   bool bad = false, fits = true;
-  if (p.quantum != 0)
+  if (p.cluster > 0)
+    unit_segment(p, cap, seg, nseg, tiles, bad);
+  else if (p.quantum > 0)
     even_segments(p, cap, seg, nseg, tiles, bad, fits);
   else if (p.narrow)
     cost_segments<uint32_t>(p, cap, seg, nseg, tiles, bad);
@@ -559,7 +581,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     const bool is_v = (lane & 8) != 0, mine = lane < 16 && blk < (kBPage >> p.log_scale);
     const float* src = is_v ? p.v_scale : p.k_scale;
     const float mul = is_v ? 1.f : p.scale_log2;
-    if (p.quantum == 0) {   // where the combine finds a unit's parts
+    if (p.quantum == 0 && p.cluster == 0) {   // where the combine finds a unit's parts
       for (int i = lane; i < nseg; i += 32) {
         const BlockSegment x = seg[i];
         int2* at = p.parts + static_cast<size_t>(x.kvh * p.token_groups + x.tg) * p.batch + x.b;
@@ -892,7 +914,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         }
         tc_fence_after();
         const int slot = sg.slot;
-        const bool whole = slot < 0;
+        const bool whole = slot == -1;
         const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
         const size_t first = (static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
         const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
@@ -904,6 +926,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         // by side; bf16 outputs go out as pairs of elements, a lane and its neighbour exchanging a
         // row each.
         float* part = p.part_o + static_cast<size_t>(max(slot, 0)) * p.rows8 * kDim;
+        float* ring = reinterpret_cast<float*>(smem + Lay::kOffRing);   // (free: this was the CTA's only segment, if slot is -2)
         uint8_t* out = static_cast<uint8_t*>(p.out) + first * kDim * (f32 ? 4 : 2);
 #pragma unroll 1
         for (int h = 0; h < kHalves; ++h) {
@@ -928,7 +951,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             v[i + 2] = fmaf(__uint_as_float(o2[i + 2]), 0.0625f, __uint_as_float(o[i + 2])) * f.z;
             v[i + 3] = fmaf(__uint_as_float(o2[i + 3]), 0.0625f, __uint_as_float(o[i + 3])) * f.w;
           }
-          if (!whole) {
+          if (slot == -2) {
+#pragma unroll
+            for (int i = 0; i < kC; ++i) ring[(c0 + i) * kDim + col] = v[i];
+          } else if (!whole) {
 #pragma unroll
             for (int i = 0; i < kC; i += 8) {
               const float v8[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
@@ -951,7 +977,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         }
         if (row < kC && c0 + row < valid) {
           const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
-          if (!whole)
+          if (slot == -2)
+            ring[kNR * kDim + c0 + row] = v;
+          else if (!whole)
             p.part_lse[static_cast<size_t>(slot) * p.rows8 + c0 + row] = v;
           else if (p.lse != nullptr)
             p.lse[first + row_off[c0 + row] / kDim] = v;
@@ -975,26 +1003,81 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     }
   }
   __syncthreads();
+  if (p.cluster > 1) {
+    // ---------------- the cluster's exchange: CTA i takes rows i, i + c, ... of the unit and adds up
+    // the parts, in order, as they lie in the CTAs' rings.  (Every CTA comes here, whatever its roles
+    // have met, and both barriers are the hardware's.)
+    const unsigned c = p.cluster, rank = blockIdx.x % c;
+    const BlockSegment sg = seg[0];
+    const unsigned T = block_tiles(sg.L);
+    const unsigned parts = __ballot_sync(0xffffffffu, lane < c && lane * T / c < (lane + 1) * T / c);   // those with tiles
+    static_assert(Lay::kSlots * Lay::kSlotBytes >= kNR * kDim * 4 + kNR * 4, "room for a part");
+    cluster_sync();
+    if (T > 1 && warp >= kBSoftmaxWarp0) {
+      const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
+      const size_t first = (static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
+      constexpr int kQuads = kDim / 4;
+      const int t = tid - 32 * kBSoftmaxWarp0, el = t % kQuads * 4;
+      uint32_t from[8];
+#pragma unroll
+      for (unsigned k = 0; k < 8; ++k) from[k] = cluster_map(sbase + Lay::kOffRing, min(k, c - 1));
+#pragma unroll 1
+      for (int row = t / kQuads * c + rank; row < valid; row += 32 * kSoftmaxWarps / kQuads * c) {
+        float l[8], o[8][4], top = -INFINITY, sum = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          l[k] = -INFINITY;
+          if (parts >> k & 1) {
+            l[k] = ld_cluster_f32(from[k] + (kNR * kDim + row) * 4);
+            ld_cluster_f32x4(from[k] + (row * kDim + el) * 4, o[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, l[k]);
+        const float ref = top == -INFINITY ? 0.f : top;   // (a row that sees nothing)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (parts >> k & 1) {
+            const float w = ex2_approx((l[k] - ref) * 1.4426950408889634f);
+            sum += w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = fmaf(w, o[k][i], a[i]);
+          }
+        const float back = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t to = first + (p.unit_tokens == 1 ? row : row / p.group * p.heads + row % p.group);
+        if (p.out_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to * kDim + el) =
+              make_float4(a[0] * back, a[1] * back, a[2] * back, a[3] * back);
+        else
+          store_bf16x4(static_cast<__nv_bfloat16*>(p.out) + to * kDim + el, a, back);
+        if (el == 0 && p.lse != nullptr) p.lse[to] = sum == 0.f ? -INFINITY : top + logf(sum);
+      }
+    }
+    cluster_sync();   // (the rings may be read until here)
+  }
   if (warp == 1) tmem_dealloc(tmem, Lay::kTmemCols);
 }
 
 // ------------------------------------------------------------------ combine kernel
 //
-// Units in parts: out = sum_s e^(lse_s - lse) O_s with lse = ln sum_s e^lse_s, in the parts' order,
-// with a running maximum.  A thread has eight rows of one element, as the parts hold them: one
-// 32-byte load a part, two parts in flight (four with teams).  kTeams = 1: a CTA takes eight rows (d = 256) or
+// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s, in the
+// parts' order.  First a warp a row makes the weights, then a thread has eight rows of one element, as
+// the parts hold them: one 32-byte load a part.  kTeams = 1: a CTA takes eight rows (d = 256) or
 // sixteen (d = 128); with many parts a unit (kTeams = 8) it takes eight rows of 32 elements, its
 // teams sharing the parts.
+constexpr int kBHeld = 5;               // a lane's parts whose lse stays in a register
+constexpr int kBChunk = 32 * kBHeld;    // parts whose weights are held at a time
+
 template <int kDim, int kTeams>
-__global__ void __launch_bounds__(kBCombineThreads, kTeams > 1 ? 2 : 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+__global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
   constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
   __shared__ float so[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? kSlice : 1][9];   // (odd pitch: no bank conflicts)
-  __shared__ float sm[kTeams > 1 ? kTeams - 1 : 1][8], sl[kTeams > 1 ? kTeams - 1 : 1][8];
-  const int tid = threadIdx.x;
+  __shared__ __align__(16) float sw[kBChunk][8 * kOcts];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int team = tid / (kSlice * kOcts), oct = tid / kSlice % kOcts, el = blockIdx.z * kSlice + tid % kSlice;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
-  const int row0 = (blockIdx.y * kOcts + oct) * 8;   // this thread's first row
+  const int row0 = blockIdx.y * kOcts * 8;   // the CTA's first row
   // The parts, slots at.x .. at.y.  The decode kernel lets this one start once its own wait for
   // what came before is over, so the lengths are final; what the decode writes is read after this
   // kernel's wait.
@@ -1005,92 +1088,125 @@ __global__ void __launch_bounds__(kBCombineThreads, kTeams > 1 ? 2 : 3) mfa_bloc
   if (p.quantum > 0) {
     const int n = even_parts(T, p.quantum);
     int before = 0;   // parts of the sequences before b, in every warp
-    for (int i = tid & 31; i < b; i += 32) before += even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), p.quantum);
+    for (int i = lane; i < b; i += 32) before += even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), p.quantum);
     before = __reduce_add_sync(0xffffffffu, before);
     const long long first_part = static_cast<long long>(before) * p.readers + static_cast<long long>(r) * n;
     if (n > 1 && first_part + n <= p.num_partials) at = make_int2(static_cast<int>(first_part), static_cast<int>(first_part) + n - 1);
   }
+  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
+  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
+  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
   grid_dep_wait();
   grid_dep_launch();
   if (p.quantum == 0 && T > 0) at = p.parts[pos];
   // one part, the output itself; no tokens; or past the plan, as the decode reports
   if (at.y <= at.x || at.x < 0 || at.y >= p.num_partials) return;
-  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
-  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-  float M[8], S[8], acc[8];
+  // the first parts' values come while the weights are made
+  constexpr int kRound = kTeams > 1 ? 4 : 2;
+  const bool rows = row0 + 8 * oct < p.rows8;
+  const float* src = p.part_o + (static_cast<size_t>(row0 / 8 + (rows ? oct : 0)) * kDim + el) * 8;
+  const size_t pitch = static_cast<size_t>(p.rows8) * kDim;
+  float o[kRound][8];
+  auto fetch = [&](int k) {   // parts k, k + kTeams, ... of at.x .. (past the last: weight 0 or not taken)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    M[i] = -INFINITY;
-    S[i] = acc[i] = 0.f;
-  }
-  // one part (its lse l, its values o) into the running sums
-  auto take = [&](const float (&l)[8], const float (&o)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float top = fmaxf(M[i], l[i]);
-      const float ref = top == -INFINITY ? 0.f : top;   // (nothing seen so far)
-      const float al = ex2_approx((M[i] - ref) * 1.4426950408889634f), w = ex2_approx((l[i] - ref) * 1.4426950408889634f);
-      S[i] = fmaf(S[i], al, w);
-      acc[i] = fmaf(acc[i], al, w * o[i]);
-      M[i] = top;
-    }
+    for (int x = 0; x < kRound; ++x) ld_global_f32x8(src + static_cast<size_t>(min(at.x + k + x * kTeams, at.y)) * pitch, o[x]);
   };
-  if (row0 < p.rows8) {
-    const float* src = p.part_o + (static_cast<size_t>(row0 / 8) * kDim + el) * 8;
-    const float* src_l = p.part_lse + row0;
-    constexpr int kRound = kTeams > 1 ? 4 : 2;
+  fetch(team);
+  // a warp's rows: the largest lse and the sum of what is over it; a lane has every 32nd part
+  float held[kOcts][kBHeld], top[kOcts], back[kOcts];
+#pragma unroll
+  for (int x = 0; x < kOcts; ++x) {
+    const int row = row0 + warp + 8 * x;
+    const float* lse = p.part_lse + min(row, p.rows8 - 1);
+    auto of = [&](int k) { return lse[static_cast<size_t>(k) * p.rows8]; };
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kBHeld; ++j) {
+      const int k = at.x + lane + 32 * j;
+      held[x][j] = k <= at.y && row < valid ? of(k) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < kBHeld; ++j) m = fmaxf(m, held[x][j]);
 #pragma unroll 1
-    for (int k = at.x + team; k <= at.y; k += kRound * kTeams) {
-      float o[kRound][8], l[kRound][8];
+    for (int k = at.x + kBChunk + lane; k <= at.y; k += 32) m = fmaxf(m, of(k));
+#pragma unroll 1
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    top[x] = m == -INFINITY ? 0.f : m;   // (a row that sees nothing)
+#pragma unroll
+    for (int j = 0; j < kBHeld; ++j) {
+      held[x][j] = ex2_approx((held[x][j] - top[x]) * 1.4426950408889634f);
+      s += held[x][j];
+    }
+#pragma unroll 1
+    for (int k = at.x + kBChunk + lane; k <= at.y; k += 32) s += ex2_approx((of(k) - top[x]) * 1.4426950408889634f);
+#pragma unroll 1
+    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0 && blockIdx.z == 0 && p.lse != nullptr && row < valid)
+      p.lse[first + (p.unit_tokens == 1 ? row : row / p.group * p.heads + row % p.group)] = s == 0.f ? -INFINITY : m + logf(s);
+    back[x] = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+    for (int j = 0; j < kBHeld; ++j) sw[lane + 32 * j][warp + 8 * x] = held[x][j] * back[x];
+  }
+  __syncthreads();
+  float acc[8] = {};
+#pragma unroll 1
+  for (int k0 = 0;;) {
+    const int n = min(kBChunk, at.y + 1 - at.x - k0);
+#pragma unroll 1
+    for (int k = team; k < n;) {
 #pragma unroll
       for (int x = 0; x < kRound; ++x) {
-        const size_t slot = static_cast<size_t>(min(k + x * kTeams, at.y)) * p.rows8;   // (past the last: not taken)
-        ld_global_f32x8(src + slot * kDim, o[x]);
-        ld_global_f32x8(src_l + slot, l[x]);
+        if (k + x * kTeams >= n) break;
+        const float4* w = reinterpret_cast<const float4*>(&sw[k + x * kTeams][8 * oct]);
+        const float4 w0 = w[0], w1 = w[1];
+        acc[0] = fmaf(w0.x, o[x][0], acc[0]);
+        acc[1] = fmaf(w0.y, o[x][1], acc[1]);
+        acc[2] = fmaf(w0.z, o[x][2], acc[2]);
+        acc[3] = fmaf(w0.w, o[x][3], acc[3]);
+        acc[4] = fmaf(w1.x, o[x][4], acc[4]);
+        acc[5] = fmaf(w1.y, o[x][5], acc[5]);
+        acc[6] = fmaf(w1.z, o[x][6], acc[6]);
+        acc[7] = fmaf(w1.w, o[x][7], acc[7]);
       }
-#pragma unroll
-      for (int x = 0; x < kRound; ++x)
-        if (k + x * kTeams <= at.y) take(l[x], o[x]);
+      k += kRound * kTeams;
+      if (k < n) fetch(k0 + k);
     }
+    k0 += kBChunk;
+    if (at.x + k0 > at.y) break;
+    fetch(k0 + team);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kOcts; ++x) {
+      const int row = row0 + warp + 8 * x;
+#pragma unroll 1
+      for (int k = lane; k < min(kBChunk, at.y + 1 - at.x - k0); k += 32)
+        sw[k][warp + 8 * x] = row >= valid ? 0.f
+                              : ex2_approx((p.part_lse[static_cast<size_t>(at.x + k0 + k) * p.rows8 + row] - top[x]) * 1.4426950408889634f) * back[x];
+    }
+    __syncthreads();
   }
   if constexpr (kTeams > 1) {
     if (team > 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) so[team - 1][tid % kSlice][i] = acc[i];
-      if (tid % kSlice == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sm[team - 1][i] = M[i];
-          sl[team - 1][i] = S[i];
-        }
-      }
     }
     __syncthreads();
     if (team > 0) return;
 #pragma unroll 1
     for (int k = 0; k < kTeams - 1; ++k) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float top = fmaxf(M[i], sm[k][i]), ref = top == -INFINITY ? 0.f : top;
-        const float al = ex2_approx((M[i] - ref) * 1.4426950408889634f), w = ex2_approx((sm[k][i] - ref) * 1.4426950408889634f);
-        S[i] = S[i] * al + sl[k][i] * w;
-        acc[i] = acc[i] * al + so[k][tid % kSlice][i] * w;
-        M[i] = top;
-      }
+      for (int i = 0; i < 8; ++i) acc[i] += so[k][tid % kSlice][i];
     }
   }
-  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = row0 + i;
+    const int row = row0 + 8 * oct + i;
     if (row >= valid) break;
-    const size_t to = first + static_cast<size_t>(row / p.group) * p.heads + row % p.group;
-    const float v = S[i] == 0.f ? 0.f : acc[i] / S[i];
+    const size_t to = (first + (p.unit_tokens == 1 ? row : row / p.group * p.heads + row % p.group)) * kDim + el;
     if (p.out_f32)
-      static_cast<float*>(p.out)[to * kDim + el] = v;
+      static_cast<float*>(p.out)[to] = acc[i];
     else
-      static_cast<__nv_bfloat16*>(p.out)[to * kDim + el] = __float2bfloat16_rn(v);
-    if (el == 0 && p.lse != nullptr) p.lse[to] = S[i] == 0.f ? -INFINITY : M[i] + logf(S[i]);
+      static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(acc[i]);
   }
 }
 
@@ -1164,48 +1280,66 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
     e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
   }
-  const long long W = tiles * sh.readers, N = nonempty * sh.readers;
+  const long long W = tiles * sh.readers, N = nonempty * sh.readers, units = static_cast<long long>(pr->batch) * sh.readers;
   const long long C = kBCostTile * W + kBCostUnit * std::max(N - 1, 0ll);
-  // a CTA's share of at most ceil(C / G) holds that over (tile + boundary) whole units and two
-  // parts of units
+  const long long most = force_ctas > 0 ? force_ctas : num_sms;
+  // Split by cost.  A CTA's share of at most ceil(C / G) holds that over (tile + boundary) whole
+  // units and two parts of units.
   const long long share = static_cast<long long>(kBMaxSeg - 2) * (kBCostTile + kBCostUnit);
   const long long least = std::max(1ll, (C + share - 1) / share);
-  long long G = force_ctas > 0 ? force_ctas : std::max(std::min<long long>(W, num_sms), least);
-  if (G < least) return MFA_ERR_INVALID_ARG;
-  // Even split: the smallest quantum whose parts are no more than the CTAs, where every unit can
-  // have a CTA of its own.  It is taken where a CTA's part is not much longer than an equal
-  // share of the cost, since it spares the CTAs a second unit's beginning and end, worth about
-  // kBSwitchTiles tiles, and some or all of the combine.
-  int quantum = 0;
+  long long G = std::max(1ll, std::max(std::min(W, most), force_ctas > 0 ? 0ll : least));
+  if (force_ctas > 0) G = force_ctas;
+  // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs):
+  const long long tile = pr->head_dim == 128 && sh.rows <= 32 ? 1400 : 2600;   // a tile
+  constexpr long long kExchange = 3000;   // a cluster's exchange
+  constexpr long long kCombine = 11000;   // the combine kernel, launch and all
+  constexpr long long kSwitch = 9000;     // a second unit's beginning and end in a CTA's range
+  long long best = (C + G * kBCostTile - 1) / (G * kBCostTile) * tile + (G > 1 ? kCombine + kSwitch : 0);
   uint32_t mode = 0;
-  if (N > 0 && N <= G) {
-    auto parts_at = [&](long long q) {
-      long long parts = 0;
-      if (host_seq_lens != nullptr)
-        for (int b = 0; b < pr->batch; ++b) parts += ((host_seq_lens[b] + kBTile - 1) / kBTile + q - 1) / q;
-      else
-        parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
-      return parts * sh.readers;
-    };
-    long long lo = 1, hi = std::max(longest, 1ll);   // parts_at(hi) = N fits
-    while (lo < hi) {
-      const long long mid = (lo + hi) / 2;
-      if (parts_at(mid) <= G) hi = mid; else lo = mid + 1;
+  int per_cta = static_cast<int>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
+  const bool by_cost = G >= least;
+  if (!by_cost) best = LLONG_MAX;
+  if (N > 0) {
+    // Clusters: 152 SMs hold 76, 46, 36, 28, 23 and 15 clusters of 2, 3, 4, 5, 6 and 8 such CTAs
+    for (const int c : {1, 2, 3, 4, 5, 6, 8}) {
+      const long long room = c == 1 || force_ctas > 0 ? most : c < 8 ? most * 9 / 10 : most * 3 / 4;
+      const long long q = (longest + c - 1) / c, cost = q * tile + (c > 1 ? kExchange : 0);
+      if (units * c > room || (c > 1 && q == (longest + c - 2) / (c - 1)) || cost >= best) continue;
+      best = cost;
+      mode = MFA_PLAN_UNIT_CLUSTERS;
+      per_cta = static_cast<int>(std::max(q, 1ll));
+      G = units * c;
     }
-    const long long share_tiles = (C + G * kBCostTile - 1) / (G * kBCostTile);
-    if (lo <= share_tiles + kBSwitchTiles) {
-      quantum = static_cast<int>(lo);
-      mode = lo >= longest ? MFA_PLAN_WHOLE_UNITS : MFA_PLAN_EVEN_SPLIT;
-      G = parts_at(lo);
+    // Even split: the smallest quantum whose parts are no more than the CTAs
+    if (N <= most) {
+      auto parts_at = [&](long long q) {
+        long long parts = 0;
+        if (host_seq_lens != nullptr)
+          for (int b = 0; b < pr->batch; ++b) parts += ((host_seq_lens[b] + kBTile - 1) / kBTile + q - 1) / q;
+        else
+          parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
+        return parts * sh.readers;
+      };
+      long long lo = 1, hi = std::max(longest, 1ll);   // parts_at(hi) = N fits
+      while (lo < hi) {
+        const long long mid = (lo + hi) / 2;
+        if (parts_at(mid) <= most) hi = mid; else lo = mid + 1;
+      }
+      if (lo * tile + kCombine < best) {
+        best = lo * tile + kCombine;
+        mode = MFA_PLAN_EVEN_SPLIT;
+        per_cta = static_cast<int>(lo);
+        G = parts_at(lo);
+      }
     }
   }
-  const long long partials = static_cast<long long>(pr->batch) * sh.readers + G - 1;
+  if (mode == 0 && !by_cost) return MFA_ERR_INVALID_ARG;   // (a forced grid of too few CTAs)
+  const long long partials = units + G - 1;   // (in every mode: a plan for another problem shows)
   if (G > INT_MAX / 2 || partials > INT_MAX / 2 / sh.rows8 || W > INT_MAX) return MFA_ERR_INVALID_ARG;
   std::memset(plan, 0, sizeof(*plan));
   plan->num_ctas = static_cast<int32_t>(G);
   plan->tile_tokens = kBTile;
-  plan->max_tiles_per_cta = mode != 0 ? quantum
-                                      : static_cast<int32_t>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
+  plan->max_tiles_per_cta = per_cta;
   plan->num_partials = static_cast<int32_t>(partials);
   plan->batch = pr->batch;
   plan->tokens_per_seq = pr->tokens_per_seq;
@@ -1226,10 +1360,13 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   if (st != MFA_OK) return st;
   if (plan == nullptr) return MFA_ERR_INVALID_ARG;
   const BlockShape sh = block_shape(pr);
+  const long long units = static_cast<long long>(pr->batch) * sh.readers;
+  const bool clusters = (plan->flags & MFA_PLAN_UNIT_CLUSTERS) != 0;
   if (plan->batch != pr->batch || plan->kv_dtype != pr->kv_dtype || plan->tokens_per_seq != pr->tokens_per_seq ||
-      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_WHOLE_UNITS)) != 0 ||
-      ((plan->flags & MFA_PLAN_EVEN_SPLIT) && plan->max_tiles_per_cta < 1) ||
-      plan->num_partials != static_cast<long long>(pr->batch) * sh.readers + plan->num_ctas - 1 ||
+      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) != 0 ||
+      ((plan->flags & MFA_PLAN_EVEN_SPLIT) && (clusters || plan->max_tiles_per_cta < 1)) ||
+      (clusters && (units == 0 || plan->num_ctas % units != 0 || plan->num_ctas / units > 8)) ||
+      plan->num_partials != units + plan->num_ctas - 1 ||
       plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->batch, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
@@ -1282,7 +1419,8 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.readers = sh.readers;
   p.rows8 = sh.rows8;
   p.num_partials = plan->num_partials;
-  p.quantum = (plan->flags & MFA_PLAN_EVEN_SPLIT) ? plan->max_tiles_per_cta : (plan->flags & MFA_PLAN_WHOLE_UNITS) ? -1 : 0;
+  p.quantum = (plan->flags & MFA_PLAN_EVEN_SPLIT) ? plan->max_tiles_per_cta : 0;
+  p.cluster = clusters ? static_cast<int>(plan->num_ctas / units) : 0;
   p.log_scale = scale_tokens == 64 ? 6 : scale_tokens == 32 ? 5 : 4;
   p.max_pages = pr->max_pages_per_seq;
   p.num_blocks = pr->num_blocks;
@@ -1300,19 +1438,22 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   cfg.blockDim = dim3(static_cast<unsigned>(block_threads(inst)), 1, 1);
   cfg.dynamicSmemBytes = kBSmem + 1024;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(std::max(p.cluster, 1));
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, block_kernel_of(inst), p);
+  cfg.numAttrs = 1;
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
-  if (plan->num_ctas > 1 && p.quantum >= 0) {   // (whole units leave nothing to combine)
-    const unsigned units = static_cast<unsigned>(pr->batch) * sh.readers;
+  if (plan->num_ctas > 1 && !clusters) {
     // many parts a unit: the CTAs of a row share them
-    const bool split = plan->num_ctas >= 8LL * units;
+    const bool split = plan->num_ctas >= 8 * units;
     const int octs = split || pr->head_dim == 256 ? 1 : 2;
-    cfg.gridDim = dim3(units, static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 32 : 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 32 : 1);
     cfg.blockDim = dim3(kBCombineThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     const BlockCombineFn fn = pr->head_dim == 256

@@ -96,8 +96,8 @@ typedef enum mfa_out_dtype {
  * after the preceding kernel. */
 #define MFA_PLAN_EARLY_METADATA 0x4u
 /* Set by mfa_block_decode_plan alone, in the plan: its way of splitting the work (see there). */
-#define MFA_PLAN_EVEN_SPLIT   0x100u
-#define MFA_PLAN_WHOLE_UNITS  0x200u
+#define MFA_PLAN_EVEN_SPLIT    0x100u
+#define MFA_PLAN_UNIT_CLUSTERS 0x200u
 
 typedef struct mfa_problem {
     int32_t batch;             /* B >= 0 sequences, one new query token each */
@@ -399,11 +399,13 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
 /*
  * Choose the split of the decode's work, as mfa_decode_plan does for the other caches (same
  * arguments; MFA_PLAN_NO_COMBINE is refused).  The plan is for mfa_block_decode_run alone.
- * The work is split as there, by cost: 4 a tile of 128 tokens and 16 a boundary between units
- * (sequence, key/value head, and a group of the new tokens whose rows, tokens x query heads of
- * the head, are at most 64), or, where every unit can have a CTA, evenly: units whole
- * (MFA_PLAN_WHOLE_UNITS) or in parts of at most max_tiles_per_cta tiles (MFA_PLAN_EVEN_SPLIT).
- * force_ctas bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles and is not limited.
+ * The work is units: a sequence, a key/value head, and a group of the new tokens whose rows
+ * (tokens x query heads of the head) are at most 64.  They are laid end to end and split by cost,
+ * as there (4 a tile of 128 tokens, 16 a boundary between units); or, where the plan finds that
+ * faster, every unit has num_ctas / units CTAs of its own (MFA_PLAN_UNIT_CLUSTERS; several are a
+ * thread-block cluster, no partial results pass through the workspace), or the units are cut
+ * into parts of at most max_tiles_per_cta tiles, one a CTA (MFA_PLAN_EVEN_SPLIT).  force_ctas
+ * bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles for the lengths planned with.
  */
 mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,

@@ -70,7 +70,9 @@ def test_problems_outside_the_cache_are_refused(lib, kw, block, code):
 def test_plan_sizes(lib, kw, rows, units):
     pr = problem(**kw)
     plan = mfa.mfa_block_decode_plan(pr, 32, [0, 1, 128, 512], num_sms=152)
-    assert plan.total_tiles == 6 * units // 4 and plan.num_ctas == plan.total_tiles
+    assert plan.total_tiles == 6 * units // 4
+    # the longest sequence's four tiles each on a CTA of a cluster
+    assert plan.flags == mfa.MFA_PLAN_UNIT_CLUSTERS and plan.num_ctas == 4 * units
     assert plan.num_partials == units + plan.num_ctas - 1
     o_end = (256 + plan.num_partials * rows * pr.head_dim * 4 + 255) // 256 * 256
     lse_end = (o_end + plan.num_partials * rows * 4 + 255) // 256 * 256

@@ -68,6 +68,39 @@ def test_decode_split_over_any_grid(shape, tokens, ctas):
     check(c, out, lse)
 
 
+WAYS = {"cost": 0, "even": mfa.MFA_PLAN_EVEN_SPLIT, "clusters": mfa.MFA_PLAN_UNIT_CLUSTERS}
+
+
+@pytest.mark.parametrize("way, lens, shape, kw, ctas", [
+    ("clusters", [900, 1, 0, 200], MFA, dict(), 4),                  # whole units
+    ("clusters", [900, 1, 0, 200], MFA, dict(tokens=3), 12),
+    ("clusters", [1300, 100], GQA, dict(), 16),                      # two CTAs a unit, of 11 tiles
+    ("clusters", [1300, 100], TWELVE, dict(tokens=2), 12),           # three: two groups of rows
+    ("clusters", [700, 257], MFA, dict(), 10),
+    ("clusters", [700, 129], GQA, dict(tokens=2), 48),               # six CTAs to six tiles
+    ("clusters", [700, 129, 2000], FIVE, dict(), 24 * 4),
+    ("clusters", [5000, 3], SINGLE, dict(), 48),                     # one group of rows, eight CTAs
+    ("even", [9000, 100, 3000], MFA, dict(), 0),
+    ("even", [9000, 100, 0, 3000], GQA, dict(tokens=2), 0),
+    ("even", [20000], SINGLE, dict(), 0),
+    ("even", [30000], MFA, dict(), 240),                             # more parts than weights held at a time
+    ("even", [30000] + [1] * 40, MFA, dict(), 280),
+    ("even", [30000] + [1] * 60, GQA, dict(), 1200),
+    ("cost", [700] * 200, SINGLE, dict(), 0),
+    ("cost", [100, 3000, 700, 0, 1], GQA, dict(), 7),
+])
+def test_every_way_to_split(way, lens, shape, kw, ctas):
+    """Also with device lengths other than those of the plan, as far as it has room for them."""
+    c = ref.Case(lens, **shape, **kw, scale_tokens=32, seed=len(lens) + ctas)
+    dec = decoder(c, force_ctas=ctas, flags=mfa.MFA_PLAN_CHECK, out_dtype=mfa.MFA_OUT_FP32)
+    assert dec.plan.flags & ~mfa.MFA_PLAN_CHECK == WAYS[way]
+    d = device(c)
+    check(c, *dec(*d))
+    c.seq_lens = torch.tensor([max(n // 2, 1) for n in reversed(sorted(lens))][::-1], dtype=torch.int32)
+    c.seq_lens = torch.minimum(c.seq_lens, torch.tensor(lens, dtype=torch.int32))
+    check(c, *dec(*d[:6], c.seq_lens.to(DEV)))
+
+
 @pytest.mark.parametrize("kw", [dict(spread=12.0), dict(spread=6.0, pow2=False), dict(q_spread=10.0), dict(pow2=False)])
 @pytest.mark.parametrize("shape", [MFA, GQA])
 def test_decode_of_scales_and_heads_far_apart(shape, kw):
