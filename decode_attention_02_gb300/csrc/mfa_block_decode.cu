@@ -100,6 +100,7 @@ struct BlockLayout {
   static constexpr uint32_t kTmemO = 2 * kNR;           // O^T, for each half kNR hi and kNR lo columns
   static constexpr uint32_t kTmemUsed = 2 * kNR * (1 + kHalves);
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kSlots * kSlotBytes >= (kDim + 1) * kNR * 4, "a part fits the rings");
   static_assert(kTmemUsed <= 512 && kKSlots >= 2 * kHalves && kOffP % 1024 == 0 && kOffRing % 1024 == 0, "layout");
 };
 
@@ -1011,7 +1012,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     const BlockSegment sg = seg[0];
     const unsigned T = block_tiles(sg.L);
     const unsigned parts = __ballot_sync(0xffffffffu, lane < c && lane * T / c < (lane + 1) * T / c);   // those with tiles
-    static_assert(Lay::kSlots * Lay::kSlotBytes >= kNR * kDim * 4 + kNR * 4, "room for a part");
     cluster_sync();
     if (T > 1 && warp >= kBSoftmaxWarp0) {
       const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
@@ -1053,7 +1053,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         if (el == 0 && p.lse != nullptr) p.lse[to] = sum == 0.f ? -INFINITY : top + logf(sum);
       }
     }
-    cluster_sync();   // (the rings may be read until here)
+    cluster_sync_relaxed();   // (the rings may be read until here)
   }
   if (warp == 1) tmem_dealloc(tmem, Lay::kTmemCols);
 }
