@@ -712,17 +712,13 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const BlockSegment sg = seg[s];
       const int L = sg.L;
       const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
-      uint64_t l2[kC / 2], nm2[kC / 2];   // row sums over this lane's tokens, minus the references: pairs of rows
-#pragma unroll
-      for (int i = 0; i < kC / 2; ++i) {
-        l2[i] = 0;
-        nm2[i] = pack_f32x2(INFINITY, INFINITY);
-      }
+      uint64_t l2[kC / 2] = {};   // row sums over this lane's tokens, pairs of rows
       if (row < kC) neg_ref[c0 + row] = INFINITY;
       int e_ref = kBEMin;
       if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
+      const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(neg_ref + c0);
       for (int j = sg.lo; j < sg.hi; ++j, ++n) {
         const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
         const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
@@ -742,9 +738,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             tmem_ld_wait(sr);
 #pragma unroll
             for (int i = 0; i < kC / 2; i += 2) {
-              const ulonglong2 w = w4[i / 2];
-              x2[i] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), mul_f32x2(a2, w.x), nm2[i]);
-              x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), nm2[i + 1]);
+              const ulonglong2 w = w4[i / 2], m = m4[i / 2];
+              x2[i] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), mul_f32x2(a2, w.x), m.x);
+              x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), m.y);
             }
           }
           if (kBTile * (j + 1) <= seen0) {
@@ -816,9 +812,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(alpha + c0 + 2 * i);
             l2[i] = mul_f32x2(l2[i], f.x);
             l2[i + 1] = mul_f32x2(l2[i + 1], f.y);
-            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_ref + c0 + 2 * i);
-            nm2[i] = m.x;
-            nm2[i + 1] = m.y;
           }
           if (j > sg.lo) {   // O holds something
             if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
