@@ -97,8 +97,8 @@ struct BlockLayout {
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;   // K and V have rings of their own
   static constexpr int kOffMisc = kOffRing + kSlots * kSlotBytes;
   static constexpr uint32_t kTmemS = 0;                 // S^T, two buffers of kNR columns
-  static constexpr uint32_t kTmemO = 2 * kNR;           // O^T, for each half kNR hi and kNR lo columns
-  static constexpr uint32_t kTmemUsed = 2 * kNR * (1 + kHalves);
+  static constexpr uint32_t kTmemO = 4 * kNR;           // O^T, for each half kNR hi and kNR lo columns
+  static constexpr uint32_t kTmemUsed = 2 * kNR * (2 + kHalves);
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static_assert(kSlots * kSlotBytes >= (kDim + 1) * kNR * 4, "a part fits the rings");
   static_assert(kTmemUsed <= 512 && kKSlots >= 2 * kHalves && kOffP % 1024 == 0 && kOffRing % 1024 == 0, "layout");
@@ -163,6 +163,26 @@ __device__ __noinline__ bool block_wait_slow(uint32_t bar, uint32_t parity, vola
 }
 __device__ __forceinline__ bool block_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_try_wait(bar, parity) || block_wait_slow(bar, parity, abort_flag);
+}
+
+// Four e4m3 codes of two pairs of halves, and back.
+__device__ __forceinline__ uint32_t cvt_e4m3x4(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void cvt_f16x4(uint32_t codes, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "mov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(codes));
 }
 
 // Reduce kC per-thread values over the 32 lanes: halving exchanges while values are left,
@@ -497,9 +517,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts into one accumulator
+    // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts in columns of their own (one
+    // MMA for both reads K once)
     if (lane == 0 && ntiles > 0) {
-      constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, kNR);
+      constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, 2 * kNR);
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
       for (int s = 0; s < nseg && ok; ++s) {
@@ -507,7 +528,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         ok = block_wait(bar(kQReady), s & 1, abort_flag);
         for (int i = 0; i < count && ok; ++i, ++n) {
           if (n >= 2) ok = block_wait(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
-          const uint32_t d = tmem + Lay::kTmemS + kNR * (n & 1);
+          const uint32_t d = tmem + Lay::kTmemS + 2 * kNR * (n & 1);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
             if (ok) ok = block_wait(bar(kFull + slot), phase, abort_flag);
@@ -516,10 +537,8 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             const uint64_t ad = smem_desc(sbase + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
             const uint64_t bd = smem_desc(sbase + Lay::kOffQ + h * (2 * kNR * 128), 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {   // 32 elements a step: 2 in the descriptors' 16-byte units
+            for (int kk = 0; kk < 4; ++kk)   // 32 elements a step: 2 in the descriptors' 16-byte units
               umma_f8_ss(d, ad + 2 * kk, bd + 2 * kk, kIdescQK, (h | kk) != 0);
-              umma_f8_ss(d, ad + 2 * kk, bd + 2 * kk + kNR * 8, kIdescQK, 1u);
-            }
             umma_commit(bar(kEmpty + slot));
             if (++slot == kKSlots) {
               slot = 0;
@@ -706,6 +725,24 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       if (lane == 0) mbar_arrive(bar(kQReady));
     };
 
+    // a tile's scores for this lane's token: q's hi parts' and lo parts' sums
+    auto load_scores = [&](uint32_t (&sr)[kC], int buffer) {
+      uint32_t lo[kC];
+      const uint32_t at = tmem + Lay::kTmemS + 2 * kNR * buffer + c0 + lane_base;
+      tmem_ld(at, sr);
+      tmem_ld(at + kNR, lo);
+      tmem_ld_wait(sr);
+      tmem_ld_wait(lo);
+#pragma unroll
+      for (int i = 0; i < kC; i += 2) {
+        float a, b;
+        unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
+                               pack_f32x2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))), a, b);
+        sr[i] = __float_as_uint(a);
+        sr[i + 1] = __float_as_uint(b);
+      }
+    };
+
     if (ntiles > 0) convert_q(0);
     int n = 0;
     for (int s = 0; s < nseg && !stop; ++s) {
@@ -734,8 +771,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           // (a segment's first tile has no reference yet)
           if (settled || !first) {
             uint32_t sr[kC];
-            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
-            tmem_ld_wait(sr);
+            load_scores(sr, n & 1);
 #pragma unroll
             for (int i = 0; i < kC / 2; i += 2) {
               const ulonglong2 w = w4[i / 2], m = m4[i / 2];
@@ -775,8 +811,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           {
             uint32_t sr[kC];
             float y[kC];
-            tmem_ld(tmem + Lay::kTmemS + kNR * (n & 1) + c0 + lane_base, sr);
-            tmem_ld_wait(sr);
+            load_scores(sr, n & 1);
 #pragma unroll
             for (int i = 0; i < kC; i += 4) {
               const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + i);
@@ -847,25 +882,25 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         const __half2 sixteen = __half2half2(__ushort_as_half(0x4C00));
         uint32_t hi[kC / 4], lo[kC / 4];
 #pragma unroll
-        for (int i = 0; i < kC / 2; ++i) {
-          float x0, x1;
-          unpack_f32x2(x2[i], x0, x1);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          l2[i] = add_f32x2(l2[i], pack_f32x2(p0, p1));
-          const __half2 pu = __hmul2(__floats2half2_rn(p0, p1), u2);
-          uint16_t h8, l8;
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h8) : "r"(*reinterpret_cast<const uint32_t*>(&pu)));
-          uint32_t back;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h8));
-          const __half2 rest = __hmul2(__hsub2(pu, *reinterpret_cast<const __half2*>(&back)), sixteen);
-          asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l8) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
-          if (i % 2 == 0) {
-            hi[i / 2] = h8;
-            lo[i / 2] = l8;
-          } else {
-            hi[i / 2] |= static_cast<uint32_t>(h8) << 16;
-            lo[i / 2] |= static_cast<uint32_t>(l8) << 16;
+        for (int i = 0; i < kC / 4; ++i) {
+          uint32_t pu[2], back[2], rest[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float x0, x1;
+            unpack_f32x2(x2[2 * i + k], x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            l2[2 * i + k] = add_f32x2(l2[2 * i + k], pack_f32x2(p0, p1));
+            const __half2 v = __hmul2(__floats2half2_rn(p0, p1), u2);
+            pu[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
+          hi[i] = cvt_e4m3x4(pu[0], pu[1]);
+          cvt_f16x4(hi[i], back[0], back[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&pu[k]), *reinterpret_cast<const __half2*>(&back[k])), sixteen);
+            rest[k] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          lo[i] = cvt_e4m3x4(rest[0], rest[1]);
         }
         // the P buffer is free once the PV that read it is complete
         if (n >= kPBufs && !(kPBufs == 1 && o_ready))
