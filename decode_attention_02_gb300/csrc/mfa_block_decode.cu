@@ -1320,9 +1320,11 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs):
   const long long tile = pr->head_dim == 128 && sh.rows <= 32 ? 1400 : 2600;   // a tile
   constexpr long long kExchange = 3000;   // a cluster's exchange
-  constexpr long long kCombine = 11000;   // the combine kernel, launch and all
-  constexpr long long kSwitch = 9000;     // a second unit's beginning and end in a CTA's range
-  long long best = (C + G * kBCostTile - 1) / (G * kBCostTile) * tile + (G > 1 ? kCombine + kSwitch : 0);
+  constexpr long long kSwitch = 18000;    // a second unit's beginning and end in a CTA's range
+  auto combine = [&](long long ctas) {    // the combine kernel, launch and all
+    return (pr->head_dim == 256 ? 1500 : 3000) + 25 * ctas;
+  };
+  long long best = (C + G * kBCostTile - 1) / (G * kBCostTile) * tile + (G > 1 ? combine(G) + kSwitch : 0);
   uint32_t mode = 0;
   int per_cta = static_cast<int>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
   const bool by_cost = G >= least;
@@ -1353,8 +1355,7 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
         const long long mid = (lo + hi) / 2;
         if (parts_at(mid) <= most) hi = mid; else lo = mid + 1;
       }
-      if (lo * tile + kCombine < best) {
-        best = lo * tile + kCombine;
+      if (lo * tile + combine(parts_at(lo)) < best) {
         mode = MFA_PLAN_EVEN_SPLIT;
         per_cta = static_cast<int>(lo);
         G = parts_at(lo);
@@ -1478,15 +1479,27 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   cfg.numAttrs = 1;
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
   if (plan->num_ctas > 1 && !clusters) {
-    // many parts a unit: the CTAs of a row share them
-    const bool split = plan->num_ctas >= 8 * units;
-    const int octs = split || pr->head_dim == 256 ? 1 : 2;
-    cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((sh.rows8 + 8 * octs - 1) / (8 * octs)), split ? pr->head_dim / 32 : 1);
+    // Teams that share a unit's parts, and then its elements' slices in CTAs of their own, while the
+    // parts and the grid's size pay for them.  Measured at 152 SMs (graph, us; d = 256, 64 rows), 1 / 2 / 4 / 8 teams:
+    // 1 unit of 32 parts 16.1 / 12.5 / 11.6 / 11.1, 8 of 16 16.8 / 15.9 / 14.7 / 16.8, 24 of 6
+    // 21.9 / 20.5 / 23.3 / 28.9, 48 of 3 28.6 / 31.0 / 36.2 / 46.3.
+    const long long octs = sh.rows8 / 8;
+    auto grid_of = [&](int teams) { return units * octs * (pr->head_dim / std::min(pr->head_dim, kBCombineThreads / teams)); };
+    int teams = 1;
+    if (grid_of(2) <= 512) teams = 2;
+    for (const int t : {4, 8})
+      if (plan->num_ctas >= 4 * t * units && grid_of(t) <= 256) teams = t;
+    const int slice = std::min(pr->head_dim, kBCombineThreads / teams), rows = 8 * (kBCombineThreads / (teams * slice));
+    cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((sh.rows8 + rows - 1) / rows),
+                       static_cast<unsigned>(pr->head_dim / slice));
     cfg.blockDim = dim3(kBCombineThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    const BlockCombineFn fn = pr->head_dim == 256
-                                  ? (split ? mfa_block_combine_kernel<256, 8> : mfa_block_combine_kernel<256, 1>)
-                                  : (split ? mfa_block_combine_kernel<128, 8> : mfa_block_combine_kernel<128, 1>);
+    const BlockCombineFn wide[] = {mfa_block_combine_kernel<256, 1>, mfa_block_combine_kernel<256, 2>,
+                                   mfa_block_combine_kernel<256, 4>, mfa_block_combine_kernel<256, 8>};
+    const BlockCombineFn narrow[] = {mfa_block_combine_kernel<128, 1>, mfa_block_combine_kernel<128, 2>,
+                                     mfa_block_combine_kernel<128, 4>, mfa_block_combine_kernel<128, 8>};
+    const int at = teams == 8 ? 3 : teams / 2;
+    const BlockCombineFn fn = pr->head_dim == 256 ? wide[at] : narrow[at];
     e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }

@@ -71,8 +71,9 @@ def test_plan_sizes(lib, kw, rows, units):
     pr = problem(**kw)
     plan = mfa.mfa_block_decode_plan(pr, 32, [0, 1, 128, 512], num_sms=152)
     assert plan.total_tiles == 6 * units // 4
-    # the longest sequence's four tiles each on a CTA of a cluster
-    assert plan.flags == mfa.MFA_PLAN_UNIT_CLUSTERS and plan.num_ctas == 4 * units
+    # a tile a CTA, or the longest sequence's four tiles on the four CTAs of a cluster
+    ctas = {mfa.MFA_PLAN_EVEN_SPLIT: plan.total_tiles, mfa.MFA_PLAN_UNIT_CLUSTERS: 4 * units}
+    assert plan.num_ctas == ctas[plan.flags]
     assert plan.num_partials == units + plan.num_ctas - 1
     o_end = (256 + plan.num_partials * rows * pr.head_dim * 4 + 255) // 256 * 256
     lse_end = (o_end + plan.num_partials * rows * 4 + 255) // 256 * 256

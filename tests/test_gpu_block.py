@@ -72,14 +72,22 @@ WAYS = {"cost": 0, "even": mfa.MFA_PLAN_EVEN_SPLIT, "clusters": mfa.MFA_PLAN_UNI
 
 
 @pytest.mark.parametrize("way, lens, shape, kw, ctas", [
-    ("clusters", [900, 1, 0, 200], MFA, dict(), 4),                  # whole units
-    ("clusters", [900, 1, 0, 200], MFA, dict(tokens=3), 12),
-    ("clusters", [1300, 100], GQA, dict(), 16),                      # two CTAs a unit, of 11 tiles
-    ("clusters", [1300, 100], TWELVE, dict(tokens=2), 12),           # three: two groups of rows
-    ("clusters", [700, 257], MFA, dict(), 10),
+    ("clusters", [300] * 130, MFA, dict(), 0),                       # whole units
+    ("clusters", [700] * 16, GQA, dict(tokens=2), 0),                # two CTAs a unit
+    ("clusters", [700, 129], GQA, dict(tokens=2), 24),               # three; a sequence of two tiles on them
+    ("clusters", [1024] * 20, MFA, dict(), 0),                       # four
+    ("clusters", [700, 1300], FIVE, dict(), 80),
     ("clusters", [700, 129], GQA, dict(tokens=2), 48),               # six CTAs to six tiles
-    ("clusters", [700, 129, 2000], FIVE, dict(), 24 * 4),
-    ("clusters", [5000, 3], SINGLE, dict(), 48),                     # one group of rows, eight CTAs
+    ("clusters", [1100] * 8, TWELVE, dict(tokens=3), 112),           # six: five groups of rows
+    ("clusters", [900] * 10, MFA, dict(), 0),                        # eight
+    ("clusters", [5000, 4990], SINGLE, dict(), 48),                  # eight for one group of rows
+    ("even", [900, 1, 0, 200], MFA, dict(), 4),
+    ("even", [900, 1, 0, 200], MFA, dict(tokens=3), 12),
+    ("even", [1300, 100], GQA, dict(), 16),
+    ("even", [1300, 100], TWELVE, dict(tokens=2), 12),
+    ("even", [700, 257], MFA, dict(), 10),
+    ("even", [700, 129, 2000], FIVE, dict(), 24 * 4),
+    ("even", [5000, 3], SINGLE, dict(), 48),
     ("even", [9000, 100, 3000], MFA, dict(), 0),
     ("even", [9000, 100, 0, 3000], GQA, dict(tokens=2), 0),
     ("even", [20000], SINGLE, dict(), 0),
