@@ -489,6 +489,14 @@ class _OnDevice:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._current = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+    def _keep(self, stream, *tensors) -> None:
+        """Memory of the current stream's that a call on ``stream`` uses: not given out again before that is done."""
+        cuda = self._torch.cuda
+        if isinstance(stream, int):
+            stream = cuda.ExternalStream(stream, device=self.device)
+        for x in tensors:
+            x.record_stream(stream)
+
     def _call(self, function, where: str, args, stream) -> None:
         """One library call on ``stream`` (None: the device's current stream)."""
         index = self._index
@@ -511,7 +519,9 @@ class BlockDecoder(_OnDevice):
     The cache: ``k_cache``, ``v_cache`` uint8 [num_blocks, num_kv_heads, 64, head_dim] (e4m3
     codes), ``k_scale``, ``v_scale`` fp32 [num_blocks, num_kv_heads, 64 // scale_tokens];
     ``block_table`` int32 [batch, max_pages_per_seq].  Device buffers come from PyTorch's
-    allocator.  Calls that may overlap on the GPU need a decoder (a workspace) each.
+    allocator.  Calls that may overlap on the GPU need a decoder (a workspace) each.  A call runs on
+    ``stream`` (a torch stream or its handle; None: the current one), and so must what made its
+    inputs, or be waited for by it.
     """
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, num_q_heads: int = NUM_Q_HEADS,
@@ -530,6 +540,8 @@ class BlockDecoder(_OnDevice):
             self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
                                               force_ctas, flags)
             self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
         self._refs = (ctypes.byref(self.plan), ctypes.byref(self.problem))
         rows = batch * tokens_per_seq
         self._q_shape = torch.Size((rows, num_q_heads, head_dim))
@@ -574,6 +586,8 @@ class BlockDecoder(_OnDevice):
                    (*self._refs, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                     k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                     lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream)
+        if stream is not None:
+            self._keep(stream, out, lse, self.workspace)
         return out, lse
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
@@ -600,6 +614,8 @@ class BlockDecoder(_OnDevice):
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
                     block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), status), stream)
+        if stream is not None:
+            self._keep(stream, self.workspace)
 
 
 class Rope(_OnDevice):
@@ -674,4 +690,6 @@ class Rope(_OnDevice):
         self._call(self._lib.mfa_rope_run, "mfa_rope_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, 1 if inverse else 0,
                     rq, rk), stream)
+        if stream is not None:
+            self._keep(stream, self.table, *(x for x in (q_out, k_out) if x is not None))
         return q_out, k_out

@@ -5,6 +5,29 @@
 //     s_t = softmax_scale * sk_t * dot(q, k_t),  out = sum_t e^(s_t) sv_t v_t / sum_t e^(s_t),
 //     lse = ln sum_t e^(s_t),
 // k_t and v_t being the e4m3 codes' values and sk_t, sv_t their blocks' scales.
+//
+// A unit is a sequence, a key/value head and as many new tokens as fit 64 rows (tokens x the head's
+// query heads); a tile is 128 tokens.  Both contractions run on the codes as they lie in the cache:
+//   S^T [128 tokens x rows] = K Q^T, q split into e4m3 hi + lo parts under one power of two a row
+//     (exact, but for elements under 2^-9 of the row's largest, which err by 2^-16 of it), in
+//     columns of their own; a token's key scale multiplies its fp32 scores;
+//   O^T [128 of d x rows] += V^T P^T, the weights (with the token's value scale) split likewise.
+// Tokens as the MMAs' M = 128 keep the tensor core full however few the rows, and let a softmax
+// thread own a token, so that a token's scales are its own two registers.  Sums, references and
+// accumulators are fp32.
+//
+// Warps: a producer (TMA boxes of one page into rings of 16 KB slots, K's and V's apart, so that a
+// tile's keys never wait behind another's values), the issuers of the two MMAs, one that fetches
+// block scales a tile ahead, and 2 or 4 warpgroups of softmax, each with all tokens and a share of
+// the rows.  The running maximum is a reference that moves only when a score passes it by 2^7
+// (then O is rescaled in tensor memory), so that an ordinary tile costs one vote.
+//
+// What bounds it: for one new token a sequence the cache's bytes (512 a token at d = 256);
+// 64 rows, 128 sequences of 4096, one CTA each: 49.2 us, 5.6 TB/s, 83% of the copy rate; of the
+// rest some 5 us are the beginning (lengths, q, the first tile's way through five stages) and 2 us
+// the end.  Short batches are bound by that chain (one sequence of 512: 10.5 us).  Several tokens'
+// units of a sequence read the same pages (from L2), and there shared memory is the bound: a tile of
+// 64 rows moves 208 KB through it, 1625 clocks at its 128 bytes a clock, and takes 2300.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,7 +52,9 @@ constexpr int kBPage = 64;
 constexpr int kBTile = 128;           // tokens of a tile (two pages)
 constexpr int kBRows = 64;            // query rows (new tokens x heads of one group) a unit holds at most
 constexpr int kBCostTile = 4;         // schedule: cost of a tile
-constexpr int kBCostUnit = 16;        // and of a unit boundary inside a CTA's range
+// and of a unit boundary inside a CTA's range: the pipeline drains and fills again (61 ragged
+// sequences, two new tokens: 67.8 us at a cost of 6, 65.0 at 12, 64.2 at 16)
+constexpr int kBCostUnit = 16;
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
 constexpr uint64_t kBWsHeader = 256;
 constexpr int kBScaleWarp = 2, kBPvWarp = 3, kBSoftmaxWarp0 = 4;   // warps: producer, QK issuer, scales, PV issuer, softmax
@@ -84,6 +109,8 @@ template <int kDim, int kNR>
 struct BlockLayout {
   static constexpr int kHalves = kDim / 128;            // 128-byte swizzle rows of a cache row
   // softmax warpgroups: a tile's latency is what bounds them, so each owns no more than 16 rows
+  // (64 rows, four warpgroups / two: 32 sequences of 4096 29.2 / 31.1 us, 61 ragged ones with two
+  // new tokens 68.8 / 79.7 us, as the kernel stood when both were built)
   static constexpr int kWgs = kNR == 64 ? 4 : 2;
   static constexpr int kC = kNR / kWgs;                 // rows a softmax warpgroup owns
   static constexpr int kThreads = 32 * kBSoftmaxWarp0 + 128 * kWgs;
@@ -96,7 +123,7 @@ struct BlockLayout {
   static constexpr int kSlots = (kBSmem - kBMisc - kOffRing) / kSlotBytes;
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;   // K and V have rings of their own
   static constexpr int kOffMisc = kOffRing + kSlots * kSlotBytes;
-  static constexpr uint32_t kTmemS = 0;                 // S^T, two buffers of kNR columns
+  static constexpr uint32_t kTmemS = 0;                 // S^T, two buffers of kNR hi and kNR lo columns
   static constexpr uint32_t kTmemO = 4 * kNR;           // O^T, for each half kNR hi and kNR lo columns
   static constexpr uint32_t kTmemUsed = 2 * kNR * (2 + kHalves);
   static constexpr uint32_t kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
@@ -228,8 +255,8 @@ __device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSeg
 }
 
 // This CTA's segments, by one warp (a lane a sequence), into shared memory; their number and this
-// lane's tiles in (nseg, tiles).  The code is kept small and straight: what a CTA runs once costs
-// more for its instructions' fetch than for their work.
+// lane's tiles in (nseg, tiles).  Every CTA runs it before its first load, so it is kept short (61
+// sequences by cost: 2.3 us, evenly 1.0, one unit a cluster 0.8).
 __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                               bool& bad, bool& fits) {
   const int lane = threadIdx.x & 31;
@@ -517,8 +544,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts in columns of their own (one
-    // MMA for both reads K once)
+    // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts in columns of their own: one
+    // MMA for both reads K from shared memory once (as two MMAs into the same columns, four long
+    // sequences 41.3 us against 40.5, two new tokens 58.1 against 57.0)
     if (lane == 0 && ntiles > 0) {
       constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, 2 * kNR);
       bool ok = true;
@@ -1033,7 +1061,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   }
   __syncthreads();
   if (p.cluster > 1) {
-    // ---------------- the cluster's exchange: CTA i takes rows i, i + c, ... of the unit and adds up
+    // ---------------- the cluster's exchange, in place of partial results in the workspace and a
+    // second kernel (32 sequences of 4096, four CTAs each: 22.0 us against 25.4): CTA i takes rows
+    // i, i + c, ... of the unit and adds up
     // the parts, in order, as they lie in the CTAs' rings.  (Every CTA comes here, whatever its roles
     // have met, and both barriers are the hardware's.)
     const unsigned c = p.cluster, rank = blockIdx.x % c;
@@ -1088,11 +1118,13 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 
 // ------------------------------------------------------------------ combine kernel
 //
-// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s, in the
-// parts' order.  First a warp a row makes the weights, then a thread has eight rows of one element, as
-// the parts hold them: one 32-byte load a part.  kTeams = 1: a CTA takes eight rows (d = 256) or
-// sixteen (d = 128); with many parts a unit (kTeams = 8) it takes eight rows of 32 elements, its
-// teams sharing the parts.
+// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s.  First a
+// warp a row makes the weights, while the first parts' values are on their way; then a thread has
+// eight rows of one element, as the parts hold them: one 32-byte load and eight multiply-adds a part.
+// kTeams teams of threads share the parts, in a fixed order, each CTA with 256 / kTeams elements of
+// eight rows (kTeams = 1, d = 128: all elements of sixteen).  Latency bounds it: four dependent
+// steps after the decode kernel's end, 2 to 5 us; with a running maximum in every thread instead of
+// weights made once a row it took 64.2 us for the two-token batch against 60.5.
 constexpr int kBHeld = 5;               // a lane's parts whose lse stays in a register
 constexpr int kBChunk = 32 * kBHeld;    // parts whose weights are held at a time
 
@@ -1317,12 +1349,16 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   const long long least = std::max(1ll, (C + share - 1) / share);
   long long G = std::max(1ll, std::max(std::min(W, most), force_ctas > 0 ? 0ll : least));
   if (force_ctas > 0) G = force_ctas;
-  // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs):
+  // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs).  us for
+  // equal sequences of 64 rows and 4096 tokens, clusters / even / by cost: 1 of them 14.7 / 11.1 /
+  // 11.6, 8 16.5 / 14.8 / 15.9, 32 22.3 / 25.4 / 26.5, 48 32.7 / 29.0 / 30.8, 128 49.4 / 53.6 / 59.1;
+  // for 16 rows of 128 x 4 heads: 1 8.9 / 8.2 / 9.4, 8 12.1 / 13.7 / 14.5, 12 17.1 / 16.6 / 17.9,
+  // 32 26.7 / 27.8 / 31.0; 61 ragged ones with two new tokens 84 / 78 / 57.
   const long long tile = pr->head_dim == 128 && sh.rows <= 32 ? 1400 : 2600;   // a tile
   constexpr long long kExchange = 3000;   // a cluster's exchange
   constexpr long long kSwitch = 18000;    // a second unit's beginning and end in a CTA's range
   auto combine = [&](long long ctas) {    // the combine kernel, launch and all
-    return (pr->head_dim == 256 ? 1500 : 3000) + 25 * ctas;
+    return (pr->head_dim == 256 && sh.rows > 32 ? 1500 : 3000) + 25 * ctas;
   };
   long long best = (C + G * kBCostTile - 1) / (G * kBCostTile) * tile + (G > 1 ? combine(G) + kSwitch : 0);
   uint32_t mode = 0;

@@ -13,6 +13,11 @@
 // thread owns one place in a head (8 elements of a pair's first half and 8 of its second) and
 // keeps its 8 cosines and sines in registers over its heads.  The loads of all its heads go
 // out before the angles are computed.
+//
+// Measured: 8191 rows of 64 + 1 heads of 256 (545 MB) 79 us, 6.9 TB/s, the copy rate; 4097 rows of
+// 64 + 4 heads of 128, 96 of them turned, adjacent pairs (143 MB) 24.5 us, 5.8 TB/s; a decode step's
+// 128 rows 2.6 us, of which the copy would take 1.3.  (Loads widened to fp32 as they came took twice
+// the registers and 212 us for the first of these.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -388,7 +388,7 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
  * block_table[b][t / 64], slot s = t % 64 and scale s / scale_tokens of that page and head.
  * The calls take an mfa_problem with kv_dtype MFA_KV_FP8_E4M3 and these shapes:
  *   head_dim d    : 128 or 256;
- *   num_kv_heads  : G >= 1, a divisor of num_q_heads, with at most 64 query heads for each;
+ *   num_kv_heads  : G in 1..65536, a divisor of num_q_heads, with at most 64 query heads for each;
  *                   query head h reads key/value head h / (num_q_heads / G);
  *   kv_shared     : 0;   tokens_per_seq : T in 1..4;   page_size : 64;
  *   scale_tokens  : 16, 32 or 64 tokens a scale (an argument of each call).
@@ -405,7 +405,8 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
  * faster, every unit has num_ctas / units CTAs of its own (MFA_PLAN_UNIT_CLUSTERS; several are a
  * thread-block cluster, no partial results pass through the workspace), or the units are cut
  * into parts of at most max_tiles_per_cta tiles, one a CTA (MFA_PLAN_EVEN_SPLIT).  force_ctas
- * bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles for the lengths planned with.
+ * bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles for the lengths planned with;
+ * num_partials is units + num_ctas - 1 however the work is split.
  */
 mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
@@ -429,6 +430,9 @@ mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_token
  * MFA_DEV_BAD_BLOCK; a length outside [0, max_pages*64] is clamped and sets MFA_DEV_BAD_LENGTH;
  * lengths that need more of a CTA than the plan allows leave the outputs unspecified and set
  * MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
+ * A NaN code among the keys makes the rows that see its token NaN, one among the values their
+ * element; a NaN among the values of a sequence's T newest tokens may also reach, in its head and
+ * element, the rows of new tokens before it.
  */
 mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_problem* problem, int32_t scale_tokens,
                                 const void* q, const void* k_cache, const void* v_cache,

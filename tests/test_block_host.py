@@ -37,6 +37,7 @@ def problem(**kw):
     (dict(), 128, mfa.MFA_ERR_UNSUPPORTED),
     (dict(), 0, mfa.MFA_ERR_INVALID_ARG),
     (dict(num_q_heads=128), 64, mfa.MFA_ERR_UNSUPPORTED),          # 128 query heads a key head
+    (dict(num_q_heads=65537, num_kv_heads=65537, head_dim=128), 64, mfa.MFA_ERR_UNSUPPORTED),
     (dict(num_q_heads=10, num_kv_heads=4), 64, mfa.MFA_ERR_INVALID_ARG),
     (dict(num_kv_heads=0), 64, mfa.MFA_ERR_INVALID_ARG),
     (dict(num_q_heads=0), 64, mfa.MFA_ERR_INVALID_ARG),

@@ -78,7 +78,7 @@ WAYS = {"cost": 0, "even": mfa.MFA_PLAN_EVEN_SPLIT, "clusters": mfa.MFA_PLAN_UNI
     ("clusters", [1024] * 20, MFA, dict(), 0),                       # four
     ("clusters", [700, 1300], FIVE, dict(), 80),
     ("clusters", [700, 129], GQA, dict(tokens=2), 48),               # six CTAs to six tiles
-    ("clusters", [1100] * 8, TWELVE, dict(tokens=3), 112),           # six: five groups of rows
+    ("clusters", [1100] * 8, TWELVE, dict(tokens=3), 112),           # five: five groups of rows
     ("clusters", [900] * 10, MFA, dict(), 0),                        # eight
     ("clusters", [5000, 4990], SINGLE, dict(), 48),                  # eight for one group of rows
     ("even", [900, 1, 0, 200], MFA, dict(), 4),
@@ -260,6 +260,51 @@ def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
         again, again_lse = dec(*d)
         torch.cuda.synchronize()
         assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+def test_outputs_of_a_call_on_another_stream_stay_until_it_is_done():
+    c = ref.Case([500], **GQA, seed=3)
+    d, dec, side = device(c), decoder(c), torch.cuda.Stream()
+    dec(*d, stream=side)   # (loads what is loaded at a first call)
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        out, lse = dec(*d, stream=stream)
+        used, like = {out.data_ptr(), lse.data_ptr()}, (torch.empty(0, dtype=out.dtype), out.shape, lse.shape)
+        del out, lse
+        new = [torch.empty(like[1], dtype=like[0].dtype, device=DEV), torch.empty(like[2], device=DEV)]
+        assert not side.query() and not used & {x.data_ptr() for x in new}
+    torch.cuda.synchronize()
+    check(c, *dec(*d))
+
+
+def test_the_first_call_may_be_on_another_stream():
+    """The workspace is ready when the decoder is."""
+    c = ref.Case([3000, 40], **MFA, seed=4)
+    d, side = device(c), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)   # what the current stream still has to do when the workspace is made
+    dec = decoder(c, out_dtype=mfa.MFA_OUT_FP32)
+    out, lse = dec(*d, stream=side)
+    torch.cuda.synchronize()
+    check(c, out, lse)
+    assert mfa.mfa_read_device_status(dec.workspace) == 0
+
+
+def test_a_nan_among_the_newest_values_stays_in_its_element_and_head():
+    c = ref.Case([70, 200], **GQA, tokens=2, seed=5)
+    d, dec = device(c), decoder(c, out_dtype=mfa.MFA_OUT_FP32)
+    want, want_lse = dec(*d)
+    page, slot, head, element = int(c.block_table[0, 1]), 69 % 64, 2, 17
+    d[2][page, head, slot, element] = 0x7F
+    out, lse = dec(*d)
+    torch.cuda.synchronize()
+    group = GQA["heads"] // GQA["kv_heads"]
+    assert torch.isnan(out[1, head * group:(head + 1) * group, element]).all()
+    out[0:2, head * group:(head + 1) * group, element] = 0   # (the token before it may be reached too)
+    want[0:2, head * group:(head + 1) * group, element] = 0
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
 def test_two_decoders_at_once():

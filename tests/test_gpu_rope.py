@@ -120,6 +120,21 @@ def test_rope_gradient():
         assert abs(slope - float(grad[r, h, j])) <= 2.0 ** -16
 
 
+def test_outputs_of_a_call_on_another_stream_stay_until_it_is_done():
+    rope, side = mfa.Rope(128, [64]), torch.cuda.Stream()
+    q = torch.randn(64, 8, 128, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    rope(q, None, pos, stream=side)   # (loads what is loaded at a first call)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    out, _ = rope(q, None, pos, stream=side)
+    used = out.data_ptr()
+    del out
+    assert not side.query() and torch.empty_like(q).data_ptr() != used
+    torch.cuda.synchronize()
+
+
 def test_rope_repeats_on_any_stream_and_in_a_graph():
     rope = mfa.Rope(256, (64, 32, 32))
     q, pos = inputs(33, 64, 256, 3, 7, torch.bfloat16, 1 << 18)
