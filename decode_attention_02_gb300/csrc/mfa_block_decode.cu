@@ -358,6 +358,7 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float (&a)
   *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// A unit's CTAs: only its own sequence's length is read.
 __device__ __forceinline__ void unit_segment(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                              bool& bad) {
   if ((threadIdx.x & 31) != 0) return;
@@ -717,36 +718,36 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       if (sidx > 0 && !block_wait(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
 #pragma unroll
       for (int x = 0; x < kRounds; ++x) {
-      const int r = r0 + 4 * kSoftmaxWarps * x;
-      const uint4(&w)[kChunks] = wr[x];
-      float m = 0.f;
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const uint32_t e[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[x] << 16)), fabsf(__uint_as_float(e[x] & 0xFFFF0000u))));
-      }
-#pragma unroll
-      for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int sig = 0;   // the row's largest |q| goes to [64, 128)
-      if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
-      if (r < kNR) {
+        const int r = r0 + 4 * kSoftmaxWarps * x;
+        const uint4(&w)[kChunks] = wr[x];
+        float m = 0.f;
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
           const uint32_t e[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
-          const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
-          uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[x] << 16)), fabsf(__uint_as_float(e[x] & 0xFFFF0000u))));
         }
-        if (i8 == 0) q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
-      }
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        int sig = 0;   // the row's largest |q| goes to [64, 128)
+        if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
+        if (r < kNR) {
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            const uint32_t e[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
+            const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
+            uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(dst + kNR * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          }
+          if (i8 == 0) q_inv[(sidx & 1) * 64 + r] = m < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - sig) << 23) : NAN;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
