@@ -131,7 +131,7 @@ def test_outputs_of_a_call_on_another_stream_stay_until_it_is_done():
     out, _ = rope(q, None, pos, stream=side)
     used = out.data_ptr()
     del out
-    assert not side.query() and torch.empty_like(q).data_ptr() != used
+    assert torch.empty_like(q).data_ptr() != used or side.query()   # (its memory is free once it is done)
     torch.cuda.synchronize()
 
 
