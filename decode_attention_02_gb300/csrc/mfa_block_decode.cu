@@ -428,7 +428,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kHalves = Lay::kHalves, kC = Lay::kC, kBoxes = Lay::kBoxes;
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kPBufs = Lay::kPBufs;
   constexpr int kSoftmaxWarps = 4 * Lay::kWgs;
-  static_assert(kC == 8 || kC == 16 || kC == 32, "rows of a warpgroup");
+  static_assert(kC == 8 || kC == 16, "rows of a warpgroup");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);

@@ -148,6 +148,18 @@ def test_decode_of_many_short_sequences():
         check(c, out, lse)
 
 
+def test_a_table_so_wide_that_costs_pass_32_bits():
+    c = ref.Case([700, 0, 129, 1, 1300], **GQA, seed=8)
+    q, k, v, ks, vs, table, lens = device(c)
+    wide = torch.zeros((5, 15_000_000), dtype=torch.int32, device=DEV)
+    wide[:, :c.columns] = table
+    dec = mfa.BlockDecoder(5, wide.shape[1], c.pages, num_q_heads=c.heads, num_kv_heads=c.kv_heads, head_dim=c.dim,
+                           scale_tokens=c.scale_tokens, host_seq_lens=c.seq_lens.tolist(), force_ctas=7,
+                           flags=mfa.MFA_PLAN_CHECK, out_dtype=mfa.MFA_OUT_FP32)
+    assert dec.plan.flags == mfa.MFA_PLAN_CHECK   # by cost
+    check(c, *dec(q, k, v, ks, vs, wide, lens))
+
+
 def test_bf16_output_is_the_rounded_fp32_output():
     c = ref.Case([200, 1000], **GQA, seed=2)
     d = device(c)
