@@ -61,13 +61,14 @@ constexpr int kBScaleWarp = 2, kBPvWarp = 3, kBSoftmaxWarp0 = 4;   // warps: pro
 constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
 constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scratch, barriers (the last 512)
-// Weights p = 2^x, x a score (in powers of two) relative to its row's reference.  A value scale
-// s_v is folded into its token's weights as s_v 2^-E, E the segment's reference exponent.  The
-// references move when max(x, 0) + log2(s_v) - E passes 7 for some token and row, so that what
-// is rounded to e4m3 stays below 2^8 (448 is its largest), and 2^x and s_v 2^-E inside f16.
+// Weights: p = 2^x, x a score in powers of two relative to its row's reference, goes into the row's
+// sum as it is; P = p s_v, s_v the token's value scale, is what is rounded.  The reference is the
+// largest x + e that the row has seen, e the exponent of s_v, so that rounding is relative to the
+// row's own largest P whatever scales there are elsewhere; it moves when x + e passes 7, so that P
+// stays below 2^8 (448 is e4m3's largest).  e counts as no less than -100, which keeps the sums in
+// range (an empty block's scale is 2^-126; its P is next to nothing either way).
 constexpr float kBThreshold = 7.0f;
-constexpr int kBMaxBelow = 8;         // a small s_v gives a score at most this much more room
-constexpr int kBEMin = -120;          // floor of E (2^-E stays a normal fp32 number)
+constexpr int kBEMin = -100, kBEMax = 126;
 
 // The work of one problem: a unit is (sequence, key/value head, group of new tokens); its rows
 // are the group's new tokens x the query heads that read that head.
@@ -435,8 +436,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   uint8_t* misc = smem + Lay::kOffMisc;
   BlockSegment* seg = reinterpret_cast<BlockSegment*>(misc);
   float* red = reinterpret_cast<float*>(misc + sizeof(BlockSegment) * kBMaxSeg);   // [warpgroups][4 quarters][kC]
-  int* red_e = reinterpret_cast<int*>(red + 256);                    // [warpgroups][4]
-  float* q_inv = reinterpret_cast<float*>(red_e + 16);               // [2 segments][64] what undoes a row's q scaling
+  float* q_inv = red + 256;                                                       // [2 segments][64] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 128);                // [64] element offset of a row's output
   int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
   float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
@@ -690,7 +690,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const int c0 = wg * kC;                       // this warpgroup's first row
     float* my_red = red + wg * 4 * kC;            // [4 quarters][kC]
-    int* my_red_e = red_e + wg * 4;
     const uint32_t vote_bar = 1 + wg;
     const bool f32 = p.out_f32 != 0;
 
@@ -780,7 +779,6 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
       uint64_t l2[kC / 2] = {};   // row sums over this lane's tokens, pairs of rows
       if (row < kC) neg_ref[c0 + row] = INFINITY;
-      int e_ref = kBEMin;
       if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
@@ -792,7 +790,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         tc_fence_after();
         const float2 sc = pr >= 0 ? meta[(n & 1) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
         const uint64_t a2 = pack_f32x2(sc.x, sc.x);
-        const int ev = sc.y > 0.f ? static_cast<int>(__float_as_uint(sc.y) >> 23) - 127 : kBEMin;
+        const float e = static_cast<float>(min(max(static_cast<int>(__float_as_uint(sc.y) >> 23) - 127, kBEMin), kBEMax));
         uint64_t x2[kC / 2];
         bool o_ready = false;   // the previous tile's PV is known to be complete
         for (bool settled = false, first = j == sg.lo;; settled = true) {
@@ -826,17 +824,17 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           }
           if (settled) break;
           if (!first) {
-            float top = 0.f;
+            float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i) {
               float lo, hi;
               unpack_f32x2(x2[i], lo, hi);
               top = fmaxf(top, fmaxf(lo, hi));
             }
-            if (!named_bar_or(vote_bar, 128, top + static_cast<float>(max(ev - e_ref, -kBMaxBelow)) > kBThreshold)) break;
+            if (!named_bar_or(vote_bar, 128, top + e > kBThreshold)) break;
           }
-          // ---- new references: each row's largest score so far, the largest value scale's
-          // exponent; the sums and O move to them.  Rare after a segment's first tile.
+          // ---- new references: each row's largest x + e so far, rounded down; the sums and O move to
+          // them (by powers of two, exactly).  Rare after a segment's first tile.
           {
             uint32_t sr[kC];
             float y[kC];
@@ -844,10 +842,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 #pragma unroll
             for (int i = 0; i < kC; i += 4) {
               const float4 w = *reinterpret_cast<const float4*>(q_inv + (s & 1) * 64 + c0 + i);
-              y[i] = __uint_as_float(sr[i]) * (sc.x * w.x);
-              y[i + 1] = __uint_as_float(sr[i + 1]) * (sc.x * w.y);
-              y[i + 2] = __uint_as_float(sr[i + 2]) * (sc.x * w.z);
-              y[i + 3] = __uint_as_float(sr[i + 3]) * (sc.x * w.w);
+              y[i] = fmaf(__uint_as_float(sr[i]), sc.x * w.x, e);
+              y[i + 1] = fmaf(__uint_as_float(sr[i + 1]), sc.x * w.y, e);
+              y[i + 2] = fmaf(__uint_as_float(sr[i + 2]), sc.x * w.z, e);
+              y[i + 3] = fmaf(__uint_as_float(sr[i + 3]), sc.x * w.w, e);
             }
             if (kBTile * (j + 1) > seen0) {
 #pragma unroll
@@ -856,20 +854,13 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             const float cmax = reduce_columns<kC, true>(y);
             if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
           }
-          const int emax = __reduce_max_sync(0xffffffffu, ev);
-          if (lane == 0) my_red_e[quarter] = emax;
           named_bar_sync(vote_bar, 128);
           if (row < kC) {
             const float m = fmaxf(fmaxf(my_red[row], my_red[kC + row]), fmaxf(my_red[2 * kC + row], my_red[3 * kC + row]));
-            const float was = neg_ref[c0 + row], now = fminf(was, -m);
+            const float was = neg_ref[c0 + row], now = fminf(was, -floorf(m));
             neg_ref[c0 + row] = now;
             alpha[c0 + row] = now < INFINITY ? ex2_approx(now - was) : 1.f;
           }
-          int e_new = e_ref;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) e_new = max(e_new, my_red_e[k]);
-          const float eshift = __uint_as_float(static_cast<uint32_t>(max(1, 127 + e_ref - e_new)) << 23);
-          e_ref = e_new;
           named_bar_sync(vote_bar, 128);
 #pragma unroll
           for (int i = 0; i < kC / 2; i += 2) {
@@ -890,10 +881,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 #pragma unroll
               for (int i = 0; i < kC; i += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * (f.x * eshift));
-                o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * (f.y * eshift));
-                o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * (f.z * eshift));
-                o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * (f.w * eshift));
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * f.x);
+                o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * f.y);
+                o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * f.z);
+                o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * f.w);
               }
               tmem_st(at, o);
             }
@@ -903,11 +894,11 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSEmpty + (n & 1)));
-        // weights p = 2^x, their sums in fp32; and P = p s_v 2^-E, rounded to f16 twice (2^-11 each)
-        // and split into e4m3 parts P = hi + lo / 16: each part keeps four bits, and the lo part's
-        // own accumulator lets it be 16 times larger, so that the smallest step is 2^-13 of the
-        // reference (ordinary weights are hundreds of steps)
-        const __half2 u2 = __half2half2(__float2half_rn(sc.y * __uint_as_float(static_cast<uint32_t>(127 - e_ref) << 23)));
+        // p = 2^x and its sums in fp32; P = p s_v rounded to f16 (2^-12) and split into e4m3 parts
+        // P = hi + lo / 16: each part keeps four bits, and the lo part's own accumulator lets it be 16
+        // times larger, so that the smallest step is 2^-13 where the row's largest P is 1 or more
+        // (ordinary weights are hundreds of steps)
+        const uint64_t v2 = pack_f32x2(sc.y, sc.y);
         const __half2 sixteen = __half2half2(__ushort_as_half(0x4C00));
         uint32_t hi[kC / 4], lo[kC / 4];
 #pragma unroll
@@ -919,7 +910,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             unpack_f32x2(x2[2 * i + k], x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             l2[2 * i + k] = add_f32x2(l2[2 * i + k], pack_f32x2(p0, p1));
-            const __half2 v = __hmul2(__floats2half2_rn(p0, p1), u2);
+            float w0, w1;
+            unpack_f32x2(mul_f32x2(pack_f32x2(p0, p1), v2), w0, w1);
+            const __half2 v = __floats2half2_rn(w0, w1);
             pu[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
           hi[i] = cvt_e4m3x4(pu[0], pu[1]);
@@ -975,10 +968,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         const bool whole = slot == -1;
         const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
         const size_t first = (static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
-        const float back = __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
         const int own = min(row, kC - 1);
         const float sum = my_red[own] + my_red[kC + own] + my_red[2 * kC + own] + my_red[3 * kC + own];
-        if (row < kC) alpha[c0 + row] = sum == 0.f ? 0.f : __fdividef(back, sum);   // (a row that sees nothing: zeros)
+        if (row < kC) alpha[c0 + row] = sum == 0.f ? 0.f : 1.f / sum;   // (a row that sees nothing: zeros)
         named_bar_sync(vote_bar, 128);
         // A partial result keeps the accumulator's order, a thread's eight rows of one element side
         // by side; bf16 outputs go out as pairs of elements, a lane and its neighbour exchanging a

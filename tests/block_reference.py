@@ -61,9 +61,11 @@ def decode(case, softmax_scale=None):
       (where an element is under 2^-9 of it); the products are exact and their sum, the scale's
       product and the subtraction of the reference are in fp32: (dim + 4) 2^-23 sum |q k|.
       A score off by e changes a weight and the sum of weights by at most e^(2 e) - 1.
-    - weights: rounded to f16, twice (2^-10), then split into two e4m3 parts: 2^-8 of the weight,
-      or the half step 2^-10 of e4m3's smallest numbers where the weight times 16 (relative to
-      the largest weight, and to the largest value scale) is small, and never more than itself.
+    - weights: rounded to f16 (2^-11), then split into two e4m3 parts: 2^-8 of what is left (a part is
+      off by 2^-4 of itself), or the half step 2^-10 of e4m3's smallest numbers where 16 times that
+      (relative to the row's largest weight times its value scale, at least) is small, and never
+      more than itself.  The two add up: where the half step is the larger, the f16 rounding of the
+      weight comes on top of it.
     - fp32 sums: 2^-18.
     """
     B, T, H, G, d = len(case.seq_lens), case.tokens, case.heads, case.kv_heads, case.dim
@@ -96,8 +98,8 @@ def decode(case, softmax_scale=None):
                 e = (scale * small @ k[g, :n].abs().T + (d + 4) * 2.0 ** -23 * scale * q.abs() @ k[g, :n].abs().T).amax(-1, keepdim=True)
                 e = e + 2.0 ** -22 * s.abs().amax(-1, keepdim=True)
                 shift = torch.expm1(2 * e)
-                step = 2.0 ** -14 * sv[g, :n].amax() / sv[g, :n] / l     # e4m3's half step, as a weight
-                dw = torch.minimum(torch.maximum((2.0 ** -8 + 2.0 ** -10) * w, step), w + 2.0 ** -10 * w)
+                step = 2.0 ** -14 * (p * sv[g, :n]).amax(-1, keepdim=True) / sv[g, :n] / l     # e4m3's half step, as a weight
+                dw = torch.minimum(torch.maximum(2.0 ** -8 * w, step), w) + 2.0 ** -10 * w
                 tol[b * T + i, hs] = (dw + (shift + 2.0 ** -18) * w) @ v[g, :n].abs() + 1e-30
                 lse_tol[b * T + i, hs] = (e + 2.0 ** -18 + 2.0 ** -23 * lse[b * T + i, hs, None].abs()).squeeze(-1)
     return out, lse, tol, lse_tol

@@ -120,6 +120,33 @@ def test_decode_of_scales_and_heads_far_apart(shape, kw):
     check(c, out, lse)
 
 
+@pytest.mark.parametrize("shape, tokens, lens", [(MFA, 2, [33, 200]), (GQA, 3, [34, 129, 66]), (TWELVE, 4, [35, 65]), (FIVE, 1, [300])])
+@pytest.mark.parametrize("rise", [20, -20, 60])
+def test_a_value_scale_far_from_the_others_costs_no_other_token_its_precision(shape, tokens, lens, rise):
+    """The last block's scale 2^rise times what it was: the new tokens that see none of it, and the weights of the
+    tokens before it, keep theirs."""
+    c = ref.Case(lens, **shape, tokens=tokens, scale_tokens=32, seed=rise + 100, poison=False)
+    for b, L in enumerate(lens):
+        page, block = int(c.block_table[b, (L - 1) // 64]), (L - 1) % 64 // 32
+        c.v_scale[page, :, block] *= 2.0 ** rise
+    out, lse = decoder(c, flags=mfa.MFA_PLAN_CHECK, out_dtype=mfa.MFA_OUT_FP32)(*device(c))
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("shape", [MFA, GQA])
+def test_blocks_of_zero_values_stay_in_the_sums(shape):
+    """As the append leaves them: zero codes under the smallest scale; in front, between others and alone."""
+    c = ref.Case([512, 700, 128, 40], **shape, scale_tokens=32, seed=9, poison=False)
+    for b, blocks in enumerate(([0, 1, 2, 3, 4, 5, 6], [3, 4, 9, 20], [0, 1, 2, 3], [1])):
+        for k in blocks:
+            page, at = int(c.block_table[b, k // 2]), k % 2
+            c.v_cache[page, :, 32 * at:32 * at + 32] = 0
+            c.v_scale[page, :, at] = 2.0 ** -126
+    for ctas in (2, 0):
+        out, lse = decoder(c, force_ctas=ctas, flags=mfa.MFA_PLAN_CHECK, out_dtype=mfa.MFA_OUT_FP32)(*device(c))
+        check(c, out, lse)
+
+
 def test_decode_of_peaked_and_growing_scores():
     """Scores that climb along the sequence (the reference of the weights moves often) and one token that
     outweighs all others."""
