@@ -19,8 +19,8 @@
 // Warps: a producer (TMA boxes of one page into rings of 16 KB slots, K's and V's apart, so that a
 // tile's keys never wait behind another's values), the issuers of the two MMAs, one that fetches
 // block scales a tile ahead, and 2 or 4 warpgroups of softmax, each with all tokens and a share of
-// the rows.  The running maximum is a reference that moves only when a score passes it by 2^7
-// (then O is rescaled in tensor memory), so that an ordinary tile costs one vote.
+// the rows.  The running maximum is a reference that moves only when weights leave a range around
+// it (then O is rescaled in tensor memory), so that an ordinary tile costs one vote.
 //
 // What bounds it: for one new token a sequence the cache's bytes (512 a token at d = 256);
 // 64 rows, 128 sequences of 4096, one CTA each: 49.2 us, 5.6 TB/s, 83% of the copy rate; of the
@@ -64,11 +64,30 @@ constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scrat
 // Weights: p = 2^x, x a score in powers of two relative to its row's reference, goes into the row's
 // sum as it is; P = p s_v, s_v the token's value scale, is what is rounded.  The reference is the
 // largest x + e that the row has seen, e the exponent of s_v, so that rounding is relative to the
-// row's own largest P whatever scales there are elsewhere; it moves when x + e passes 7, so that P
-// stays below 2^8 (448 is e4m3's largest).  e counts as no less than -100, which keeps the sums in
-// range (an empty block's scale is 2^-126; its P is next to nothing either way).
-constexpr float kBThreshold = 7.0f;
-constexpr int kBEMin = -100, kBEMax = 126;
+// row's own largest P whatever scales there are elsewhere.  Two parts, the second 32 times larger,
+// resolve P to 2^-14 from 2^8 down (448 is e4m3's largest, and the first part leaves up to 8), and a
+// P under 2^-15 is lost; so the reference follows what a row is made of.  It lies 1 under the tile's
+// largest x + e (in powers of two, as all here), or 6 where few tokens outweigh what is about them,
+// as first tokens do (a quarter of the tile 6 above the others, or 7 above one of them):
+//   it rises when x + e passes 7 over it, and then for the warpgroup's other rows too where that is a
+//   rise (rows that rise by themselves only come to a third more moves);
+//   it falls, to 24 below its highest at most, when a tile's largest x + e is 4 under it (without
+//   that, 32768 tokens behind one of 0.8 of the weight came out as 0.1 of their sum).
+// Falls are looked for in the tile after a move for the sake of few tokens, and every 64 tiles.
+// Measured on 8000 tokens of normal scores behind one to three of next to no value that stand 5 to 11
+// nats above (relative error of the output row, at most): 0.005; 0.013 with a fall at 6 under, 0.015
+// with 8 in place of 7, 0.009 without the 1 of room, 0.04 with no such rules.
+// A move costs its CTA some microseconds, most of it code that is not at hand: 32 / 128 sequences of
+// 4096 take 23.9 / 53.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62 with 6 of room for
+// all rows; and 22.3 / 49.5 when P was held to 2^-14 of a row's largest and nothing fell.
+// Scales are taken 2^-24 times smaller, the results as many times larger: p = 2^(x - reference)
+// and its sums then stay in fp32's range for scales from 2^-50 (smaller ones count as that: an
+// empty block's is 2^-126, and its P next to nothing either way) to the largest.
+constexpr float kBThreshold = 7.0f, kBLow = -4.0f, kBDepth = 24.0f, kBRoom = 1.0f, kBRoomFew = 6.0f;
+constexpr int kBLookEvery = 64;
+constexpr float kBScaleDown = 0x1p-24f, kBScaleUp = 0x1p24f;
+constexpr int kBEMin = -50 - 24, kBEMax = 127 - 24;
+constexpr float kBPart = 32.0f;   // the second part's factor
 
 // The work of one problem: a unit is (sequence, key/value head, group of new tokens); its rows
 // are the group's new tokens x the query heads that read that head.
@@ -213,12 +232,11 @@ __device__ __forceinline__ void cvt_f16x4(uint32_t codes, uint32_t& a, uint32_t&
       : "r"(codes));
 }
 
-// Reduce kC per-thread values over the 32 lanes: halving exchanges while values are left,
+// Sum kC per-thread values over the 32 lanes: halving exchanges while values are left,
 // then whole exchanges of the last one.  Lane l ends with column l / (32 / kC).
-template <int kC, bool kMax>
+template <int kC>
 __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
   const int lane = threadIdx.x & 31;
-  auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
   int step = 16;
 #pragma unroll
   for (int n = kC / 2; n >= 1; n /= 2, step /= 2) {
@@ -226,11 +244,11 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kC]) {
     for (int i = 0; i < n; ++i) {
       const bool hi = lane & step;
       const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, step));
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, step);
     }
   }
 #pragma unroll
-  for (; step >= 1; step /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], step));
+  for (; step >= 1; step /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], step);
   return v[0];
 }
 
@@ -441,7 +459,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   int* row_tok = row_off + 64;                                       // [64] new token of a row within the unit
   float* neg_ref = reinterpret_cast<float*>(row_tok + 64);           // [64] minus the rows' reference maxima
   float* alpha = neg_ref + 64;                                       // [64] what old sums are multiplied by
-  float2* meta = reinterpret_cast<float2*>(alpha + 64);              // [2 tiles][2 pages][4 blocks] {K, V} scales
+  float* top_neg = alpha + 64;                                       // [64] minus the highest references so far
+  int* look = reinterpret_cast<int*>(top_neg + 64);                  // [64] at a warpgroup's first row: its next tile to look at
+  float2* meta = reinterpret_cast<float2*>(look + 64);               // [2 tiles][2 pages][4 blocks] {K, V} scales
   int* ctl = reinterpret_cast<int*>(meta + 16);              // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
   const uint32_t bars = sbase + Lay::kOffMisc + kBMisc - 512;
@@ -629,7 +649,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     const int pg = (lane >> 2) & 1, blk = lane & 3;
     const bool is_v = (lane & 8) != 0, mine = lane < 16 && blk < (kBPage >> p.log_scale);
     const float* src = is_v ? p.v_scale : p.k_scale;
-    const float mul = is_v ? 1.f : p.scale_log2;
+    const float mul = is_v ? kBScaleDown : p.scale_log2;
     if (p.quantum == 0 && p.cluster == 0) {   // where the combine finds a unit's parts
       for (int i = lane; i < nseg; i += 32) {
         const BlockSegment x = seg[i];
@@ -778,7 +798,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const int L = sg.L;
       const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
       uint64_t l2[kC / 2] = {};   // row sums over this lane's tokens, pairs of rows
-      if (row < kC) neg_ref[c0 + row] = INFINITY;
+      if (row < kC) neg_ref[c0 + row] = top_neg[c0 + row] = INFINITY;
       if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
@@ -831,10 +851,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               unpack_f32x2(x2[i], lo, hi);
               top = fmaxf(top, fmaxf(lo, hi));
             }
-            if (!named_bar_or(vote_bar, 128, top + e > kBThreshold)) break;
+            if (!named_bar_or(vote_bar, 128, look[c0] == n || top + e > kBThreshold)) break;
           }
-          // ---- new references: each row's largest x + e so far, rounded down; the sums and O move to
-          // them (by powers of two, exactly).  Rare after a segment's first tile.
+          // ---- new references, from each row's largest x + e in this tile; the sums and O move to
+          // them (by powers of two, exactly).  Rare after a segment's first two tiles.
           {
             uint32_t sr[kC];
             float y[kC];
@@ -851,15 +871,29 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 #pragma unroll
               for (int i = 0; i < kC; ++i) y[i] = t < seen0 + row_tok[c0 + i] ? y[i] : -INFINITY;
             }
-            const float cmax = reduce_columns<kC, true>(y);
-            if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = cmax;
+#pragma unroll
+            for (int i = 0; i < kC; ++i) y[i] = warp_max(y[i]);
+            if (lane == 0) {
+#pragma unroll
+              for (int i = 0; i < kC; i += 4)
+                *reinterpret_cast<float4*>(my_red + quarter * kC + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+            if (row == 0) look[c0] = n + kBLookEvery;
           }
           named_bar_sync(vote_bar, 128);
           if (row < kC) {
-            const float m = fmaxf(fmaxf(my_red[row], my_red[kC + row]), fmaxf(my_red[2 * kC + row], my_red[3 * kC + row]));
-            const float was = neg_ref[c0 + row], now = fminf(was, -floorf(m));
+            const float a = my_red[row], b = my_red[kC + row], c = my_red[2 * kC + row], d = my_red[3 * kC + row];
+            const float ab = fmaxf(a, b), cd = fmaxf(c, d), m = fmaxf(ab, cd);
+            const float second = fmaxf(fminf(ab, cd), ab > cd ? fminf(a, b) : fminf(c, d)), least = fminf(fminf(a, b), fminf(c, d));
+            const bool few = m - fminf(second, least + 1.f) > 6.f;
+            const float was = neg_ref[c0 + row], top = top_neg[c0 + row], to = kBRoom - floorf(m);
+            // (as it was where the row sees nothing of the tile, or m is NaN)
+            float now = fminf(was, to) + (few && m + was > kBThreshold ? kBRoomFew - kBRoom : 0.f);
+            if (m + was < kBLow && m > -INFINITY) now = fminf(to + (few ? kBRoomFew - kBRoom : 0.f), top + kBDepth);
             neg_ref[c0 + row] = now;
+            top_neg[c0 + row] = fminf(top, now);
             alpha[c0 + row] = now < INFINITY ? ex2_approx(now - was) : 1.f;
+            if (few && least + now < kBLow) look[c0] = n + 1;
           }
           named_bar_sync(vote_bar, 128);
 #pragma unroll
@@ -895,11 +929,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSEmpty + (n & 1)));
         // p = 2^x and its sums in fp32; P = p s_v rounded to f16 (2^-12) and split into e4m3 parts
-        // P = hi + lo / 16: each part keeps four bits, and the lo part's own accumulator lets it be 16
-        // times larger, so that the smallest step is 2^-13 where the row's largest P is 1 or more
-        // (ordinary weights are hundreds of steps)
+        // P = hi + lo / 32: each part keeps four bits, and the lo part's own accumulator lets it be 32
+        // times larger (see kBThreshold)
         const uint64_t v2 = pack_f32x2(sc.y, sc.y);
-        const __half2 sixteen = __half2half2(__ushort_as_half(0x4C00));
+        const __half2 part = __half2half2(__float2half_rn(kBPart));
         uint32_t hi[kC / 4], lo[kC / 4];
 #pragma unroll
         for (int i = 0; i < kC / 4; ++i) {
@@ -919,7 +952,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           cvt_f16x4(hi[i], back[0], back[1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&pu[k]), *reinterpret_cast<const __half2*>(&back[k])), sixteen);
+            const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&pu[k]), *reinterpret_cast<const __half2*>(&back[k])), part);
             rest[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
           lo[i] = cvt_e4m3x4(rest[0], rest[1]);
@@ -955,7 +988,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         float l[kC];
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) unpack_f32x2(l2[i], l[2 * i], l[2 * i + 1]);
-        const float lsum = reduce_columns<kC, false>(l);
+        const float lsum = reduce_columns<kC>(l);
         named_bar_sync(vote_bar, 128);   // (the scratch may still be read from the last new reference)
         if (lane % (32 / kC) == 0) my_red[quarter * kC + lane / (32 / kC)] = lsum;
         if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
@@ -970,7 +1003,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         const size_t first = (static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
         const int own = min(row, kC - 1);
         const float sum = my_red[own] + my_red[kC + own] + my_red[2 * kC + own] + my_red[3 * kC + own];
-        if (row < kC) alpha[c0 + row] = sum == 0.f ? 0.f : 1.f / sum;   // (a row that sees nothing: zeros)
+        if (row < kC) alpha[c0 + row] = sum == 0.f ? 0.f : kBScaleUp / sum;   // (a row that sees nothing: zeros)
         named_bar_sync(vote_bar, 128);
         // A partial result keeps the accumulator's order, a thread's eight rows of one element side
         // by side; bf16 outputs go out as pairs of elements, a lane and its neighbour exchanging a
@@ -996,10 +1029,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 #pragma unroll
           for (int i = 0; i < kC; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + i);
-            v[i] = fmaf(__uint_as_float(o2[i]), 0.0625f, __uint_as_float(o[i])) * f.x;
-            v[i + 1] = fmaf(__uint_as_float(o2[i + 1]), 0.0625f, __uint_as_float(o[i + 1])) * f.y;
-            v[i + 2] = fmaf(__uint_as_float(o2[i + 2]), 0.0625f, __uint_as_float(o[i + 2])) * f.z;
-            v[i + 3] = fmaf(__uint_as_float(o2[i + 3]), 0.0625f, __uint_as_float(o[i + 3])) * f.w;
+            v[i] = fmaf(__uint_as_float(o2[i]), 1.f / kBPart, __uint_as_float(o[i])) * f.x;
+            v[i + 1] = fmaf(__uint_as_float(o2[i + 1]), 1.f / kBPart, __uint_as_float(o[i + 1])) * f.y;
+            v[i + 2] = fmaf(__uint_as_float(o2[i + 2]), 1.f / kBPart, __uint_as_float(o[i + 2])) * f.z;
+            v[i + 3] = fmaf(__uint_as_float(o2[i + 3]), 1.f / kBPart, __uint_as_float(o[i + 3])) * f.w;
           }
           if (slot == -2) {
 #pragma unroll
@@ -1026,7 +1059,11 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           }
         }
         if (row < kC && c0 + row < valid) {
-          const float v = sum == 0.f ? -INFINITY : logf(sum) - neg_ref[c0 + row] * 0.6931471805599453f;
+          // (the sum's exponent joins the reference first: their logarithms alone would cancel)
+          const int k = min(static_cast<int>(__float_as_uint(sum) >> 23), 253) - 127;
+          const float v = sum == 0.f ? -INFINITY
+                                     : fmaf(static_cast<float>(k) - neg_ref[c0 + row], 0.6931471805599453f,
+                                            logf(sum * __uint_as_float(static_cast<uint32_t>(127 - k) << 23)));
           if (slot == -2)
             ring[kNR * kDim + c0 + row] = v;
           else if (!whole)

@@ -339,6 +339,12 @@ __device__ __forceinline__ void ld_cluster_f32x4(uint32_t addr, float (&v)[4]) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
 }
 
+// The largest of the 32 lanes' values (NaN left out), in every lane.
+__device__ __forceinline__ float warp_max(float v) {
+  asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
+  return v;
+}
+
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;

@@ -430,8 +430,10 @@ mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_token
  * MFA_DEV_BAD_BLOCK; a length outside [0, max_pages*64] is clamped and sets MFA_DEV_BAD_LENGTH;
  * lengths that need more of a CTA than the plan allows leave the outputs unspecified and set
  * MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
- * Sums are fp32; a weight times its value scale is held to 2^-8 of itself, or to 2^-14 of the
- * row's largest where that is more.
+ * Sums and lse are fp32.  A weight times its value scale is rounded to 8 significant bits (with
+ * fp32 outputs too), the smallest of a row more coarsely: to 2^-16 of the largest about them, which
+ * is followed along the sequence, so that thousands of small weights behind a far larger one keep
+ * theirs.  Value scales under 2^-50 count as 2^-50 there.
  * A NaN code among the keys makes the rows that see its token NaN, one among the values their
  * element; a NaN among the values of a sequence's T newest tokens may also reach, in its head and
  * element, the rows of new tokens before it.
