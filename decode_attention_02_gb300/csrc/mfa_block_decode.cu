@@ -191,9 +191,29 @@ struct BlockDecodeParams {
 // Even split: a unit of T tiles is cut into n = ceil(T / quantum) parts as equal as they come.
 // Part i of reader r of sequence b is item R P_b + r n + i (R readers, P_b parts of one reader of
 // each sequence before b), and CTA g takes items g, g + G, ...: one part each, none with the end
-// of one unit and the beginning of another.
+// of one unit and the beginning of another.  Where lengths have grown past those of the plan the
+// parts may be more than the workspace's slots: then every CTA takes the same larger quantum
+// (wider_quantum), and some CTAs two items.
 __device__ __forceinline__ int even_parts(int T, int quantum) {
   return T <= quantum ? (T > 0 ? 1 : 0) : (T + quantum - 1) / quantum;
+}
+// A quantum with which the units' parts are no more than the slots: with W tiles in N units
+// (all readers), sum ceil(T / q) <= W / q + N, and W / q <= slots - N.  (One warp; out of the way.)
+__device__ __noinline__ int wider_quantum(const BlockDecodeParams& p, int cap) {
+  long long tiles = 0, units = 0;
+  bool bad = false;
+  for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
+    const int T = (clamp_len(p.seq_lens[b], cap, bad) + kBTile - 1) / kBTile;
+    tiles += T;
+    units += T > 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+  }
+  const long long spare = p.num_partials - units * p.readers;   // (>= 0: a slot a unit is there)
+  return spare < 1 ? INT_MAX : static_cast<int>(min((tiles * p.readers + spare - 1) / spare, static_cast<long long>(INT_MAX)));
 }
 // first of a unit's T tiles at cost >= X
 template <typename I>
@@ -277,41 +297,47 @@ __device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSeg
 // lane's tiles in (nseg, tiles).  Every CTA runs it before its first load, so it is kept short (61
 // sequences by cost: 2.3 us, evenly 1.0, one unit a cluster 0.8).
 __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
-                                              bool& bad, bool& fits) {
+                                              bool& bad) {
   const int lane = threadIdx.x & 31;
-  long long item = blockIdx.x, carry = 0;   // the item that is looked for; items of the sequences passed
-  int next = lane < p.batch ? p.seq_lens[lane] : 0;
+  int quantum = p.quantum;
 #pragma unroll 1
-  for (int c0 = 0; c0 < p.batch; c0 += 32) {
-    const int L = clamp_len(next, cap, bad);
-    next = c0 + 32 + lane < p.batch ? p.seq_lens[c0 + 32 + lane] : 0;
-    const int T = block_tiles(L), n = even_parts(T, p.quantum);
-    const long long own = static_cast<long long>(n) * p.readers;
-    long long incl = own;
+  while (true) {
+    long long item = blockIdx.x, carry = 0;   // the item that is looked for; items of the sequences passed
+    int next = lane < p.batch ? p.seq_lens[lane] : 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < p.batch; c0 += 32) {
+      const int L = clamp_len(next, cap, bad);
+      next = c0 + 32 + lane < p.batch ? p.seq_lens[c0 + 32 + lane] : 0;
+      const int T = block_tiles(L), n = even_parts(T, quantum);
+      const long long own = static_cast<long long>(n) * p.readers;
+      long long incl = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const long long before = carry + incl - own;
-    carry += __shfl_sync(0xffffffffu, incl, 31);
-#pragma unroll 1
-    while (item < carry && nseg <= kBMaxSeg) {
-      if (item >= before && item < before + own) {
-        int r = static_cast<int>(item - before), lo = 0, hi = T;
-        if (n > 1) {   // part i: T / n tiles, the first T % n parts one more
-          const int i = r % n, each = T / n, more = T - each * n;
-          r /= n;
-          lo = i * each + min(i, more);
-          hi = lo + each + (i < more ? 1 : 0);
-          fits = fits && item < p.num_partials;
-        }
-        add_segment(p, seg, nseg, c0 + lane, r, L, lo, hi, item);
-        tiles += hi - lo;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-      ++nseg;
-      item += gridDim.x;
+      const long long before = carry + incl - own;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll 1
+      while (item < carry && nseg <= kBMaxSeg) {
+        if (item >= before && item < before + own) {
+          int r = static_cast<int>(item - before), lo = 0, hi = T;
+          if (n > 1) {   // part i: T / n tiles, the first T % n parts one more
+            const int i = r % n, each = T / n, more = T - each * n;
+            r /= n;
+            lo = i * each + min(i, more);
+            hi = lo + each + (i < more ? 1 : 0);
+          }
+          add_segment(p, seg, nseg, c0 + lane, r, L, lo, hi, item);
+          tiles += hi - lo;
+        }
+        ++nseg;
+        item += gridDim.x;
+      }
     }
+    if (carry <= p.num_partials) return;
+    quantum = wider_quantum(p, cap);
+    nseg = tiles = 0;
   }
 }
 
@@ -393,18 +419,18 @@ __device__ __forceinline__ void unit_segment(const BlockDecodeParams& p, int cap
 
 __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
   int nseg = 0, tiles = 0;
-  bool bad = false, fits = true;
+  bool bad = false;
   if (p.cluster > 0)
     unit_segment(p, cap, seg, nseg, tiles, bad);
   else if (p.quantum > 0)
-    even_segments(p, cap, seg, nseg, tiles, bad, fits);
+    even_segments(p, cap, seg, nseg, tiles, bad);
   else if (p.narrow)
     cost_segments<uint32_t>(p, cap, seg, nseg, tiles, bad);
   else
     cost_segments_wide(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
-  if (nseg > kBMaxSeg || !__all_sync(0xffffffffu, fits)) {
+  if (nseg > kBMaxSeg) {
     if ((threadIdx.x & 31) == 0) atomicOr(p.status, MFA_DEV_SCHEDULE);
     nseg = tiles = 0;
   }
@@ -1176,12 +1202,26 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
   bool bad = false;
   const int T = block_tiles(clamp_len(p.seq_lens[b], cap, bad));
   if (p.quantum > 0) {
-    const int n = even_parts(T, p.quantum);
-    int before = 0;   // parts of the sequences before b, in every warp
-    for (int i = lane; i < b; i += 32) before += even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), p.quantum);
-    before = __reduce_add_sync(0xffffffffu, before);
-    const long long first_part = static_cast<long long>(before) * p.readers + static_cast<long long>(r) * n;
-    if (n > 1 && first_part + n <= p.num_partials) at = make_int2(static_cast<int>(first_part), static_cast<int>(first_part) + n - 1);
+    int quantum = p.quantum;
+#pragma unroll 1
+    while (true) {
+      int before = 0;        // parts of the sequences before b, in every warp
+      long long all = 0;     // and of all
+#pragma unroll 1
+      for (int i = lane; i < p.batch; i += 32) {
+        const int n = even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), quantum);
+        all += n;
+        before += i < b ? n : 0;
+      }
+      const long long low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(all & 0xFFFFF));
+      all = low + (static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(all >> 20))) << 20);
+      if (all * p.readers <= p.num_partials) {
+        const int n = even_parts(T, quantum), first_part = __reduce_add_sync(0xffffffffu, before) * p.readers + r * n;
+        if (n > 1) at = make_int2(first_part, first_part + n - 1);
+        break;
+      }
+      quantum = wider_quantum(p, cap);
+    }
   }
   const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
   const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);

@@ -407,6 +407,8 @@ mfa_status mfa_decode_append_run(const mfa_plan* plan, const mfa_problem* proble
  * into parts of at most max_tiles_per_cta tiles, one a CTA (MFA_PLAN_EVEN_SPLIT).  force_ctas
  * bounds the grid.  plan->max_tiles_per_cta bounds a CTA's tiles for the lengths planned with;
  * num_partials is units + num_ctas - 1 however the work is split.
+ * A plan runs other lengths than its own too, longer ones included (a decode loop's, step by step);
+ * far from those planned with it is only no longer the fastest split.
  */
 mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
@@ -428,8 +430,8 @@ mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_token
  * Slots past a sequence's length, the scales of blocks without a token and unused pages may
  * hold any bits.  A block id outside the pool reads as a page of zeros and sets
  * MFA_DEV_BAD_BLOCK; a length outside [0, max_pages*64] is clamped and sets MFA_DEV_BAD_LENGTH;
- * lengths that need more of a CTA than the plan allows leave the outputs unspecified and set
- * MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
+ * lengths with which one CTA of the plan would meet more than 256 units leave the outputs
+ * unspecified and set MFA_DEV_SCHEDULE (lengths up to the planned ones never do).
  * Sums and lse are fp32.  A weight times its value scale is rounded to 8 significant bits (with
  * fp32 outputs too), the smallest of a row more coarsely: to 2^-16 of the largest about them, which
  * is followed along the sequence, so that thousands of small weights behind a far larger one keep
