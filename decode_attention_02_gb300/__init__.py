@@ -553,6 +553,8 @@ class BlockDecoder(_OnDevice):
         self._row_shape = (num_kv_heads, head_dim)
         self._types = (torch.bfloat16, torch.uint8, torch.float32, torch.int32)
         self._out_dtype = torch.float32 if out_dtype == MFA_OUT_FP32 else torch.bfloat16
+        # appends whose status a checked decode has yet to report (it clears the word for its own)
+        self._checked, self._unreported = bool(flags & MFA_PLAN_CHECK), False
 
     def _cache_fits(self, k_cache, v_cache, k_scale, v_scale, block_table) -> bool:
         _, u8, f32, i32 = self._types
@@ -567,7 +569,8 @@ class BlockDecoder(_OnDevice):
                 ("block_table", block_table, i32, self._table_shape))
 
     def __call__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None, lse=None, stream=None):
-        """One decode step: (out [batch * tokens, num_q_heads, head_dim], lse [.., num_q_heads])."""
+        """One decode step: (out [batch * tokens, num_q_heads, head_dim], lse [.., num_q_heads]).  With
+        MFA_PLAN_CHECK it reports what appends since the last one could not place, too."""
         bf16, _, f32, i32 = self._types
         i = self._index
         if not (_fits(q, bf16, self._q_shape, i) and _fits(seq_lens, i32, self._batch_shape, i) and
@@ -582,13 +585,37 @@ class BlockDecoder(_OnDevice):
             lse = self._torch.empty(self._lse_shape, dtype=f32, device=self.device)
         elif not _fits(lse, f32, self._lse_shape, i):
             _refuse(i, ("lse", lse, f32, self._lse_shape))
+        before = self._take_status(stream) if self._unreported else 0
+        try:
+            self._decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, stream)
+        finally:
+            if before:
+                self._leave_status(before, stream)
+        if before:
+            raise MfaError(MFA_ERR_DEVICE_CHECK, "mfa_block_kv_append")
+        return out, lse
+
+    def _take_status(self, stream) -> int:
+        """The status word's bits, which the checked decode about to run clears."""
+        self._unreported = False
+        word = ctypes.c_uint32(0)
+        self._call(self._lib.mfa_read_device_status, "mfa_read_device_status",
+                   (self.workspace.data_ptr(), ctypes.byref(word), 0), stream)
+        return word.value
+
+    def _leave_status(self, bits: int, stream) -> None:
+        """Put bits back beside the checked decode's own (which has synchronised), for mfa_read_device_status."""
+        self.workspace[:4].bitwise_or_(self._torch.tensor(list(bits.to_bytes(4, "little")), dtype=self._torch.uint8,
+                                                          device=self.device))
+        self._torch.cuda.current_stream(self._index).synchronize()
+
+    def _decode(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, stream) -> None:
         self._call(self._lib.mfa_block_decode_run, "mfa_block_decode_run",
                    (*self._refs, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                     k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                     lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream)
         if stream is not None:
             self._keep(stream, out, lse, self.workspace)
-        return out, lse
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
                max_new: int = 0, device_status=None, stream=None):
@@ -609,6 +636,8 @@ class BlockDecoder(_OnDevice):
                     *(() if offsets is None else (("offsets", offsets, i32, counts),)),
                     *self._cache_wants(k_cache, v_cache, k_scale, v_scale, block_table))
         status = self.workspace.data_ptr() if device_status is None else _ptr(device_status)
+        if self._checked and device_status is None:
+            self._unreported = True
         self._call(self._lib.mfa_block_kv_append, "mfa_block_kv_append",
                    (self._refs[1], self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),

@@ -52,3 +52,39 @@ def test_a_decode_loop_on_the_plan_of_its_first_step(shape, batch):
         c.seq_lens = torch.full((batch,), n, dtype=torch.int32)
         out, lse = dec(*d[:6], c.seq_lens.to(DEV), out=torch.full(c.q.shape, float("nan"), device=DEV))
         check(c, out, lse)
+
+
+def test_a_checked_decode_reports_what_an_append_could_not_place():
+    """The decode clears the status word for its own bits; those of an append before it are not lost."""
+    c = ref.Case([64, 20], **GQA, scale_tokens=32, columns=2, seed=3, poison=False)
+    dec = decoder(c, lens=None, flags=mfa.MFA_PLAN_CHECK)
+    d = device(c)
+    new = torch.ones((2, 4, 128), dtype=torch.bfloat16, device=DEV)
+
+    def append(positions, table=None, **kw):
+        dec.append(new, new, torch.tensor(positions, dtype=torch.int32, device=DEV), d[5] if table is None else table, *d[1:5],
+                   **kw)
+
+    bad = d[5].clone()
+    bad[0, 1] = c.pages
+    for table, positions, bits in ((bad, [64, 20], mfa.MFA_DEV_BAD_BLOCK), (None, [128, 20], mfa.MFA_DEV_BAD_LENGTH)):
+        append(positions, table)
+        with pytest.raises(mfa.MfaError) as e:
+            dec(*d)
+        assert e.value.status == mfa.MFA_ERR_DEVICE_CHECK
+        assert mfa.mfa_read_device_status(dec.workspace) == bits
+        dec(*d)
+        append([63, 20])
+        dec(*d)                                              # an append with nothing to report
+    # both steps at once, on another stream
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    append([64, 20], bad, stream=side)
+    with pytest.raises(mfa.MfaError):
+        dec(*d[:6], torch.tensor([129, 20], dtype=torch.int32, device=DEV), stream=side)
+    assert mfa.mfa_read_device_status(dec.workspace) == mfa.MFA_DEV_BAD_BLOCK | mfa.MFA_DEV_BAD_LENGTH
+    # a word of the caller's own is the caller's to read
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    append([64, 20], bad, device_status=word)
+    dec(*d)
+    assert int(word) == mfa.MFA_DEV_BAD_BLOCK
