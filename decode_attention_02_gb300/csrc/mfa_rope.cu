@@ -2,10 +2,11 @@
 //
 // Pair i of a head turns by the angle position[axis(i)] * frequency(i):
 //     a' = a cos - b sin,   b' = b cos + a sin.
-// Angles: the table holds each frequency as a 64-bit fraction of a turn, and position times
-// fraction modulo 2^64 is the angle modulo one turn, exact to 2^-53 of a turn at any 32-bit
-// position, in two integer multiplies; sincospif of its top 32 bits gives cos and sin to fp32.
-// (A product in fp32 is off by 2^-24 of the whole angle, 0.008 rad at position 131072.)
+// Angles: the table holds each frequency as a 64-bit fraction of a turn, rounded to nearest, and
+// position times fraction modulo 2^64 is the angle modulo one turn in two integer multiplies, off by
+// 2^-34 of a turn at most at any 32-bit position; sincospif of its top 32 bits (2^-32 of a turn)
+// gives cos and sin to fp32.  (A product in fp32 is off by 2^-24 of the whole angle, 0.008 rad at
+// position 131072; a table made in doubles by 2^-20 of a turn at 2^31, stretched 16 times.)
 //
 // Every element is read once and written once, with some 3 operations for each: HBM-bound for
 // a prompt, launch-bound for a decode step.  A CTA turns all heads of one row, so that the
@@ -263,6 +264,58 @@ static void (*rope_kernel(bool wide, bool half))(RopeParams) {
   return half ? mfa_rope_kernel<T, 1, true> : mfa_rope_kernel<T, 1, false>;
 }
 
+// ------------------------------------------------------------------ frequencies, on the host
+//
+// Sums of two doubles, hi + lo with |lo| at most half a step of hi: some 100 bits, by error-free sums and
+// products (Dekker's; the products by fma).
+struct Twofold {
+  double hi, lo;
+};
+static Twofold two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+static Twofold add(Twofold a, Twofold b) {
+  const Twofold s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+static Twofold mul(Twofold a, Twofold b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+static Twofold ratio(double a, double b) {   // of two whole numbers
+  const double q = a / b;
+  return two_sum(q, std::fma(-q, b, a) / b);
+}
+constexpr Twofold kLn2 = {0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56};
+constexpr Twofold kInv2Pi = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
+
+// e^x, |x| < 745: x = k ln 2 + 512 r, e^r - 1 by its series, then nine times s -> 2 s + s^2.
+static Twofold exp_of(Twofold x) {
+  const double k = std::nearbyint(x.hi / kLn2.hi);
+  Twofold r = add(x, mul({-k, 0.0}, kLn2));
+  r = {std::ldexp(r.hi, -9), std::ldexp(r.lo, -9)};
+  Twofold s = ratio(1.0, 10.0);   // s = r (1 + r / 2 (1 + r / 3 (...))), |r| < 7e-4
+  s = mul(s, r);
+  for (int n = 9; n >= 1; --n) s = mul(mul(add(s, {1.0, 0.0}), r), ratio(1.0, n));
+  for (int n = 0; n < 9; ++n) s = add({2.0 * s.hi, 2.0 * s.lo}, mul(s, s));
+  s = add(s, {1.0, 0.0});
+  return {std::ldexp(s.hi, static_cast<int>(k)), std::ldexp(s.lo, static_cast<int>(k))};
+}
+// ln x, x >= 1: of its fraction m in [1/2, 1) a double's logarithm y and one Newton step, y + (m e^-y - 1).
+static Twofold log_of(double x) {
+  int e;
+  const double m = std::frexp(x, &e), y = std::log(m);
+  const Twofold step = add(mul({m, 0.0}, exp_of({-y, 0.0})), {-1.0, 0.0});
+  return add(mul({static_cast<double>(e), 0.0}, kLn2), add({y, 0.0}, step));
+}
+// t turns (t >= 0) in units of 2^-64, to nearest, modulo 2^64.
+static uint64_t turn_fraction(Twofold t) {
+  const double hi = std::ldexp(t.hi, 64), whole = std::floor(hi);
+  const double rest = std::nearbyint((hi - whole) + std::ldexp(t.lo, 64));   // (|lo| < 2^13 there)
+  return static_cast<uint64_t>(std::fmod(whole, 18446744073709551616.0)) + static_cast<uint64_t>(static_cast<int64_t>(rest));
+}
+
 }  // namespace mfa
 
 using namespace mfa;
@@ -272,19 +325,16 @@ extern "C" mfa_status mfa_rope_table(const mfa_rope_config* c, mfa_rope_pair* ta
   if (st != MFA_OK) return st;
   if (table == nullptr) return MFA_ERR_INVALID_ARG;
   const int pairs = c->rotary_dim / 2;
+  const Twofold log_theta = log_of(c->theta);
   int used[MFA_ROPE_MAX_AXES] = {0, 0, 0, 0};
   int axis = 0;
   for (int i = 0; i < pairs; ++i) {
     // the next pair's axis: the current run's, or the next in turn, skipping those that are full
     while (used[axis] == c->sections[axis]) axis = (axis + 1) % c->num_axes;
-    const double power = (c->flags & MFA_ROPE_OWN_SPECTRUM)
-                             ? static_cast<double>(used[axis]) / c->sections[axis]
-                             : 2.0 * i / c->rotary_dim;
-    const double turns = std::pow(c->theta, -power) * c->position_scale * 0.15915494309189535;   // 1 / (2 pi)
-    const double part = turns - std::floor(turns);
-    // 2^64 * part, exact up to the double's own rounding; part < 1, and 2^64 itself is one turn
-    const double scaled = std::ldexp(part, 64);
-    table[i].turns = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+    const Twofold power = (c->flags & MFA_ROPE_OWN_SPECTRUM) ? ratio(used[axis], c->sections[axis])
+                                                             : ratio(2.0 * i, c->rotary_dim);
+    const Twofold frequency = exp_of(mul(mul(power, log_theta), {-1.0, 0.0}));
+    table[i].turns = turn_fraction(mul(mul(frequency, kInv2Pi), {c->position_scale, 0.0}));
     table[i].axis = axis;
     table[i].reserved = 0;
     ++used[axis];

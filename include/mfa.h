@@ -526,9 +526,9 @@ typedef struct mfa_rope_pair {
 
 /*
  * Fill `table` (host, rotary_dim / 2 entries).  Host only.  The caller copies it to the device
- * once and keeps it.  Angles are 64-bit fractions of a turn, so that a position of any size has
- * the angle of its exact product with the frequency (fp32 products are off by 0.01 rad at
- * position 131072).
+ * once and keeps it.  Frequencies are 64-bit fractions of a turn, rounded to nearest, so that any
+ * position has the angle of its exact product with the frequency to 2^-31 of a turn (fp32 products
+ * are off by 0.01 rad at position 131072).
  */
 mfa_status mfa_rope_table(const mfa_rope_config* config, mfa_rope_pair* table);
 
