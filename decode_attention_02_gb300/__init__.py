@@ -488,27 +488,35 @@ class _OnDevice:
         # the current stream's handle without a Stream object around it, where torch has that
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._current = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self._home = self._current(self._index)   # the stream that the handle's own buffers are allocated on
 
-    def _keep(self, stream, *tensors) -> None:
-        """Memory of the current stream's that a call on ``stream`` uses: not given out again before that is done."""
+    def _keep(self, stream, tensors) -> None:
+        """Memory that a call on ``stream`` uses: not given out again before that is done."""
         cuda = self._torch.cuda
-        if isinstance(stream, int):
-            stream = cuda.ExternalStream(stream, device=self.device)
+        if isinstance(stream, int):   # (0 and 1 both name the default stream)
+            stream = cuda.ExternalStream(stream, device=self.device) if stream > 1 else cuda.default_stream(self.device)
         for x in tensors:
-            x.record_stream(stream)
+            if x is not None:
+                x.record_stream(stream)
 
-    def _call(self, function, where: str, args, stream) -> None:
-        """One library call on ``stream`` (None: the device's current stream)."""
+    def _call(self, function, where: str, args, stream, own=(), used=()) -> None:
+        """One library call on ``stream`` (None: the device's current stream), with the handle's ``own`` tensors
+        and the call's: those stay until it is done, on whichever stream they were allocated.  (On the current
+        stream the call's tensors do without that, as for any call of torch's.)"""
         index = self._index
         if stream is None:
-            stream = self._current(index)
-        elif not isinstance(stream, int):
-            stream = stream.cuda_stream
+            handle = self._current(index)
+        else:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
         if self._torch.cuda.current_device() == index:
-            status = function(*args, stream)
+            status = function(*args, handle)
         else:
             with self._torch.cuda.device(index):
-                status = function(*args, stream)
+                status = function(*args, handle)
+        if stream is not None:
+            self._keep(stream, (*own, *used))
+        elif handle != self._home:
+            self._keep(self._torch.cuda.current_stream(index), own)
         if status != MFA_OK:
             raise MfaError(status, where)
 
@@ -521,7 +529,9 @@ class BlockDecoder(_OnDevice):
     ``block_table`` int32 [batch, max_pages_per_seq].  Device buffers come from PyTorch's
     allocator.  Calls that may overlap on the GPU need a decoder (a workspace) each.  A call runs on
     ``stream`` (a torch stream or its handle; None: the current one), and so must what made its
-    inputs, or be waited for by it.
+    inputs, or be waited for by it.  What it uses stays allocated until it is done: the decoder's
+    workspace always, the tensors of a call with ``stream`` too.  A captured call's decoder and
+    tensors have to outlive the graph.
     """
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, num_q_heads: int = NUM_Q_HEADS,
@@ -613,9 +623,8 @@ class BlockDecoder(_OnDevice):
         self._call(self._lib.mfa_block_decode_run, "mfa_block_decode_run",
                    (*self._refs, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                     k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream)
-        if stream is not None:
-            self._keep(stream, out, lse, self.workspace)
+                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
+                   (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse))
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
                max_new: int = 0, device_status=None, stream=None):
@@ -642,9 +651,8 @@ class BlockDecoder(_OnDevice):
                    (self._refs[1], self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
                     block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                    v_scale.data_ptr(), status), stream)
-        if stream is not None:
-            self._keep(stream, self.workspace)
+                    v_scale.data_ptr(), status), stream, (self.workspace,),
+                   (k_new, v_new, offsets, positions, block_table, k_cache, v_cache, k_scale, v_scale))
 
 
 class Rope(_OnDevice):
@@ -718,7 +726,5 @@ class Rope(_OnDevice):
             rk, k_out = self._rows(k, k_out, "k", rows, dtype)
         self._call(self._lib.mfa_rope_run, "mfa_rope_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, 1 if inverse else 0,
-                    rq, rk), stream)
-        if stream is not None:
-            self._keep(stream, self.table, *(x for x in (q_out, k_out) if x is not None))
+                    rq, rk), stream, (self.table,), (q, k, positions, q_out, k_out))
         return q_out, k_out
