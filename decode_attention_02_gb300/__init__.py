@@ -630,8 +630,8 @@ class BlockDecoder(_OnDevice):
                max_new: int = 0, device_status=None, stream=None):
         """Quantise new rows into the cache: bf16 ``k_new``, ``v_new`` [rows, num_kv_heads, head_dim], sequence b's
         being rows offsets[b] .. offsets[b + 1] - 1 (``offsets`` int32 [batch + 1], ``max_new`` their largest
-        count), or ``tokens_per_seq`` each.  ``device_status``: the decoder's workspace by default, so that
-        mfa_read_device_status(decoder.workspace) reports both steps."""
+        count), or ``tokens_per_seq`` each.  ``device_status``: a tensor of 4 bytes or more, or an address; the
+        decoder's workspace by default, so that mfa_read_device_status(decoder.workspace) reports both steps."""
         bf16, _, _, i32 = self._types
         i = self._index
         rows = k_new.shape[0]
@@ -644,15 +644,23 @@ class BlockDecoder(_OnDevice):
                     ("positions", positions, i32, self._batch_shape),
                     *(() if offsets is None else (("offsets", offsets, i32, counts),)),
                     *self._cache_wants(k_cache, v_cache, k_scale, v_scale, block_table))
-        status = self.workspace.data_ptr() if device_status is None else _ptr(device_status)
-        if self._checked and device_status is None:
+        if device_status is None:
+            status = self.workspace.data_ptr()
+        elif isinstance(device_status, int):
+            status, device_status = device_status, None
+        else:
+            status = device_status.data_ptr()
+            if device_status.get_device() != i or _nbytes(device_status) < 4 or not device_status.is_contiguous():
+                raise ValueError(f"device_status: expected at least 4 contiguous bytes on {self.device}, got "
+                                 f"{device_status.dtype} {tuple(device_status.shape)} on {device_status.device}")
+        if self._checked and status == self.workspace.data_ptr():
             self._unreported = True
         self._call(self._lib.mfa_block_kv_append, "mfa_block_kv_append",
                    (self._refs[1], self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
                     block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), status), stream, (self.workspace,),
-                   (k_new, v_new, offsets, positions, block_table, k_cache, v_cache, k_scale, v_scale))
+                   (k_new, v_new, offsets, positions, block_table, k_cache, v_cache, k_scale, v_scale, device_status))
 
 
 class Rope(_OnDevice):

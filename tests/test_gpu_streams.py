@@ -98,3 +98,20 @@ def test_the_default_stream_by_its_handle():
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     check(c, out, lse)
+
+
+def test_a_status_word_that_four_bytes_do_not_fit_is_refused():
+    c = ref.Case([300, 30], **GQA, seed=5)
+    d, dec = device(c), decoder(c)
+    new = torch.ones((2, 4, 128), dtype=torch.bfloat16, device=DEV)
+    positions = torch.tensor([300, 30], dtype=torch.int32, device=DEV)
+    for bad in (torch.zeros(3, dtype=torch.uint8, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV),
+                torch.zeros(1, dtype=torch.int32), torch.zeros((4, 4), dtype=torch.uint8, device=DEV)[:, 0]):
+        with pytest.raises(ValueError):
+            dec.append(new, new, positions, d[5], *d[1:5], device_status=bad)
+    with pytest.raises(mfa.MfaError):
+        dec.append(new, new, positions, d[5], *d[1:5], device_status=torch.zeros(9, dtype=torch.uint8, device=DEV)[1:])
+    good = torch.zeros(4, dtype=torch.uint8, device=DEV)
+    for word in (good, good.data_ptr()):
+        dec.append(new, new, positions + 10 ** 6, d[5], *d[1:5], device_status=word)
+    assert int(good.view(torch.int32)) == mfa.MFA_DEV_BAD_LENGTH
