@@ -1167,7 +1167,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         if (el == 0 && p.lse != nullptr) p.lse[to] = sum == 0.f ? -INFINITY : top + logf(sum);
       }
     }
-    cluster_sync_relaxed();   // (the rings may be read until here)
+    cluster_sync();   // (the rings may be read until here: a CTA's reads come before its arrival)
   }
   if (warp == 1) tmem_dealloc(tmem, Lay::kTmemCols);
 }

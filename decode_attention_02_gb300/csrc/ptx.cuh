@@ -320,10 +320,6 @@ __device__ __forceinline__ void ld_global_f32x8(const float* p, float (&v)[8]) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The same where nothing that was written matters: reads whose values have been used are over.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
-}
 // The address of this CTA's shared-memory location `saddr` in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
