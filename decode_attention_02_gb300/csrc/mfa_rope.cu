@@ -222,28 +222,32 @@ static mfa_status check_rope(const mfa_rope_config* c) {
   return MFA_OK;
 }
 
+// Whether two sets of rows share memory: `rows` rows of `len` elements each, `stride` apart.  Ranges that
+// overlap are apart as columns of one wider row (q and k of one projection): equal strides, and the two
+// column ranges apart.  (Different strides count as sharing.)
+static bool share(const void* a, int64_t a_stride, int64_t a_len, const void* b, int64_t b_stride, int64_t b_len, int rows,
+                  int esz) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + ((rows - 1) * a_stride + a_len) * esz, b1 = b0 + ((rows - 1) * b_stride + b_len) * esz;
+  if (a0 >= b1 || b0 >= a1) return false;
+  if (rows == 1 || a_stride != b_stride) return true;
+  const uintptr_t stride = static_cast<uintptr_t>(a_stride) * esz;
+  const uintptr_t apart = (b0 >= a0 ? b0 - a0 : stride - (a0 - b0) % stride) % stride;   // b's columns past a's
+  return apart < static_cast<uintptr_t>(a_len) * esz || stride - apart < static_cast<uintptr_t>(b_len) * esz;
+}
+
 static mfa_status check_side(const mfa_rope_rows* s, const mfa_rope_config* c, int rows, int esz) {
   if (s == nullptr || s->heads == 0) return MFA_OK;
   if (s->heads < 0 || s->heads > INT_MAX / 4 / kRopeMaxDim) return MFA_ERR_INVALID_ARG;
   if (rows == 0) return MFA_OK;
   if (s->in == nullptr || s->out == nullptr || !aligned(s->in, esz) || !aligned(s->out, esz)) return MFA_ERR_INVALID_ARG;
   const int64_t least = static_cast<int64_t>(s->heads) * c->head_dim;
-  constexpr int64_t kMost = int64_t{1} << 40;   // rows * stride * size stays far inside 64 bits
-  if (s->in_stride < least || s->out_stride < least || s->in_stride > kMost || s->out_stride > kMost)
+  const int64_t most = (int64_t{1} << 58) / rows;   // rows * stride * size stays inside 64 bits
+  if (s->in_stride < least || s->out_stride < least || s->in_stride > most || s->out_stride > most)
     return MFA_ERR_INVALID_ARG;
   // in place means the same rows; anything between would be read after it is written
   if (s->in == s->out) return s->in_stride == s->out_stride ? MFA_OK : MFA_ERR_INVALID_ARG;
-  const uintptr_t i0 = reinterpret_cast<uintptr_t>(s->in), o0 = reinterpret_cast<uintptr_t>(s->out);
-  const uintptr_t i1 = i0 + ((rows - 1) * s->in_stride + least) * esz, o1 = o0 + ((rows - 1) * s->out_stride + least) * esz;
-  if (i0 < o1 && o0 < i1) {
-    // overlapping ranges are fine only as columns of one wider row (q and k of one projection):
-    // equal strides, and the two column ranges apart
-    if (s->in_stride != s->out_stride) return MFA_ERR_INVALID_ARG;
-    const uintptr_t stride = static_cast<uintptr_t>(s->in_stride) * esz, len = static_cast<uintptr_t>(least) * esz;
-    const uintptr_t apart = (o0 > i0 ? o0 - i0 : stride - (i0 - o0) % stride) % stride;
-    if (apart < len || stride - apart < len) return MFA_ERR_INVALID_ARG;
-  }
-  return MFA_OK;
+  return share(s->in, s->in_stride, least, s->out, s->out_stride, least, rows, esz) ? MFA_ERR_INVALID_ARG : MFA_OK;
 }
 
 // The wide path needs 16-byte aligned vectors of 8 elements everywhere.
@@ -357,6 +361,13 @@ extern "C" mfa_status mfa_rope_run(const mfa_rope_config* c, const mfa_rope_pair
   p.k = side_of(k);
   const long long heads = static_cast<long long>(p.q.heads) + p.k.heads;
   if (num_rows == 0 || heads == 0) return MFA_OK;
+  if (p.q.heads > 0 && p.k.heads > 0) {   // what one side writes is neither read nor written by the other
+    const int64_t nq = static_cast<int64_t>(p.q.heads) * c->head_dim, nk = static_cast<int64_t>(p.k.heads) * c->head_dim;
+    if (share(p.q.out, p.q.out_stride, nq, p.k.in, p.k.in_stride, nk, num_rows, esz) ||
+        share(p.q.out, p.q.out_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz) ||
+        share(p.q.in, p.q.in_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz))
+      return MFA_ERR_INVALID_ARG;
+  }
   if (table == nullptr || positions == nullptr || !aligned(table, 16) || !aligned(positions, 4)) return MFA_ERR_INVALID_ARG;
   const bool half = c->pairing == MFA_ROPE_HALF;
   const bool wide = c->head_dim % 8 == 0 && c->rotary_dim % (half ? 16 : 8) == 0 && wide_side(q) && wide_side(k);

@@ -551,7 +551,8 @@ typedef struct mfa_rope_rows {
  *   inverse   : 1 turns by the negative angles: the gradient of the call with 0, or its undoing.
  *   q, k      : the rows; either may be NULL or have no heads.  All-16-byte-aligned rows with
  *               head_dim and the pairs in multiples of 8 elements take the wide path, all
- *               others one pair at a time.  q's rows and k's must not overlap.
+ *               others one pair at a time.  What one writes must not be read or written for the other
+ *               (MFA_ERR_INVALID_ARG; columns of one wider row do not overlap).
  */
 mfa_status mfa_rope_run(const mfa_rope_config* config, const mfa_rope_pair* table,
                         const int32_t* positions, int32_t num_rows, int32_t dtype, int32_t inverse,
