@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kBlkThreads, 5) mfa_block_append_kernel(const 
     named_bar_sync(1 + it_item, kItemThreads);   // (and every thread of the item has read s_old)
 #pragma unroll
     for (int w = 0; w < kItemThreads / 32; ++w) a = fmaxf(a, wmax[it_item * (kItemThreads / 32) + w]);
+  } else {
+    __syncwarp();   // (every lane has read s_old before the first writes it anew)
   }
   const float need = pow2_scale(a);
   const float s = begun ? fmaxf(s_old, need) : need;
