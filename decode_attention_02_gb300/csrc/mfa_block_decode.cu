@@ -912,10 +912,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             const float ab = fmaxf(a, b), cd = fmaxf(c, d), m = fmaxf(ab, cd);
             const float second = fmaxf(fminf(ab, cd), ab > cd ? fminf(a, b) : fminf(c, d)), least = fminf(fminf(a, b), fminf(c, d));
             const bool few = m - fminf(second, least + 1.f) > 6.f;
-            const float was = neg_ref[c0 + row], top = top_neg[c0 + row], to = kBRoom - floorf(m);
-            // (as it was where the row sees nothing of the tile, or m is NaN)
-            float now = fminf(was, to) + (few && m + was > kBThreshold ? kBRoomFew - kBRoom : 0.f);
-            if (m + was < kBLow && m > -INFINITY) now = fminf(to + (few ? kBRoomFew - kBRoom : 0.f), top + kBDepth);
+            const float was = neg_ref[c0 + row], top = top_neg[c0 + row], to = (few ? kBRoomFew : kBRoom) - floorf(m);
+            float now = fminf(was, to);   // (as it was where the row sees nothing of the tile, or m is NaN)
+            if (m + was < kBLow && m > -INFINITY) now = fminf(to, top + kBDepth);
             neg_ref[c0 + row] = now;
             top_neg[c0 + row] = fminf(top, now);
             alpha[c0 + row] = now < INFINITY ? ex2_approx(now - was) : 1.f;

@@ -82,6 +82,15 @@ def test_a_few_tokens_of_small_value_however_far_above(nats, at):
     check_norms(c, out, 2.0 ** -7)
 
 
+@pytest.mark.parametrize("at", [[8060, 8070], [500, 600, 700], [0, 130, 1024]])
+def test_tokens_of_small_value_in_neighbouring_tiles(at):
+    """Each tile's other tokens keep their share: 4 % of the row's norm a tile, where they were lost."""
+    c = sinks([15000], dict(heads=32, kv_heads=1, dim=256), 1, 11.2, at, 0.3, 0.0, 0.0, seed=3)
+    for ctas in (1, 2):
+        out, _ = decoder(c, force_ctas=ctas, flags=mfa.MFA_PLAN_CHECK, out_dtype=mfa.MFA_OUT_FP32)(*device(c))
+        check_norms(c, out, 2.0 ** -7)
+
+
 @pytest.mark.parametrize("length", [4096, 65536])
 @pytest.mark.parametrize("nats", [7.0, 9.9, 12.0, 14.1, 16.0, 20.0])
 @pytest.mark.parametrize("at", [0, 1001])
