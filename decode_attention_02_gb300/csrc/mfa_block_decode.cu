@@ -23,11 +23,13 @@
 // it (then O is rescaled in tensor memory), so that an ordinary tile costs one vote.
 //
 // What bounds it: for one new token a sequence the cache's bytes (512 a token at d = 256);
-// 64 rows, 128 sequences of 4096, one CTA each: 49.2 us, 5.6 TB/s, 83% of the copy rate; of the
-// rest some 5 us are the beginning (lengths, q, the first tile's way through five stages) and 2 us
-// the end.  Short batches are bound by that chain (one sequence of 512: 10.5 us).  Several tokens'
-// units of a sequence read the same pages (from L2), and there shared memory is the bound: a tile of
-// 64 rows moves 208 KB through it, 1625 clocks at its 128 bytes a clock, and takes 2300.
+// 64 rows, 128 sequences of 4096, one CTA each: 52.2 us, 5.3 TB/s, 78% of the copy rate; of the
+// rest some 5 us are the beginning (lengths, q, the first tile's way through five stages), 2 us the
+// end and 3 us moves of references.  Short batches are bound by that chain (one sequence of 512:
+// 10.6 us).  Several tokens' units of a sequence read the same pages (from L2), and nothing alone
+// bounds them: a tile of 64 rows takes some 2300 clocks, of which its 208 KB are 1625 of shared
+// memory at 128 bytes a clock, and whole captures show shared memory's pipe and the tensor cores at
+// a third, issue slots at a half.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,13 +64,14 @@ constexpr int kBCombineThreads = 256;
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
 constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scratch, barriers (the last 512)
 // Weights: p = 2^x, x a score in powers of two relative to its row's reference, goes into the row's
-// sum as it is; P = p s_v, s_v the token's value scale, is what is rounded.  The reference is the
-// largest x + e that the row has seen, e the exponent of s_v, so that rounding is relative to the
-// row's own largest P whatever scales there are elsewhere.  Two parts, the second 32 times larger,
-// resolve P to 2^-14 from 2^8 down (448 is e4m3's largest, and the first part leaves up to 8), and a
-// P under 2^-15 is lost; so the reference follows what a row is made of.  It lies 1 under the tile's
-// largest x + e (in powers of two, as all here), or 6 where few tokens outweigh what is about them,
-// as first tokens do (a quarter of the tile 6 above the others, or 7 above one of them):
+// sum as it is; P = p s_v, s_v the token's value scale, is what is rounded.  The reference
+// is set by x + e, e the exponent of s_v, so that rounding is relative to the row's own P whatever
+// scales there are elsewhere.  Two parts, the second 32 times larger, resolve P to 2^-14 from 2^8
+// down (448 is e4m3's largest, and the first part leaves up to 8), and a P under 2^-15 is lost; so
+// the reference follows what a row is made of.  It lies 1 under a tile's largest x + e (in powers of
+// two, as all here), or 6 where few tokens outweigh what is about them, as first tokens do (a
+// quarter's largest 6 above those of the others, or 7 above that of one; what stands 2^21 under them
+// in their own tile is lost):
 //   it rises when x + e passes 7 over it, and then for the warpgroup's other rows too where that is a
 //   rise (rows that rise by themselves only come to a third more moves);
 //   it falls, to 24 below its highest at most, when a tile's largest x + e is 4 under it (without
@@ -78,7 +81,7 @@ constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scrat
 // nats above (relative error of the output row, at most): 0.005; 0.013 with a fall at 6 under, 0.015
 // with 8 in place of 7, 0.009 without the 1 of room, 0.04 with no such rules.
 // A move costs its CTA some microseconds, most of it code that is not at hand: 32 / 128 sequences of
-// 4096 take 23.9 / 53.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62 with 6 of room for
+// 4096 take 23.7 / 52.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62 with 6 of room for
 // all rows; and 22.3 / 49.5 when P was held to 2^-14 of a row's largest and nothing fell.
 // Scales are taken 2^-24 times smaller, the results as many times larger: p = 2^(x - reference)
 // and its sums then stay in fp32's range for scales from 2^-50 (smaller ones count as that: an
@@ -880,7 +883,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             if (!named_bar_or(vote_bar, 128, look[c0] == n || top + e > kBThreshold)) break;
           }
           // ---- new references, from each row's largest x + e in this tile; the sums and O move to
-          // them (by powers of two, exactly).  Rare after a segment's first two tiles.
+          // them (by powers of two).  Rare after a segment's first two tiles.
           {
             uint32_t sr[kC];
             float y[kC];
@@ -1117,7 +1120,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   __syncthreads();
   if (p.cluster > 1) {
     // ---------------- the cluster's exchange, in place of partial results in the workspace and a
-    // second kernel (32 sequences of 4096, four CTAs each: 22.0 us against 25.4): CTA i takes rows
+    // second kernel (32 sequences of 4096, four CTAs each: 23.7 us against 26.8): CTA i takes rows
     // i, i + c, ... of the unit and adds up
     // the parts, in order, as they lie in the CTAs' rings.  (Every CTA comes here, whatever its roles
     // have met, and both barriers are the hardware's.)
@@ -1418,11 +1421,11 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   const long long least = std::max(1ll, (C + share - 1) / share);
   long long G = std::max(1ll, std::max(std::min(W, most), force_ctas > 0 ? 0ll : least));
   if (force_ctas > 0) G = force_ctas;
-  // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs).  us for
-  // equal sequences of 64 rows and 4096 tokens, clusters / even / by cost: 1 of them 14.7 / 11.1 /
-  // 11.6, 8 16.5 / 14.8 / 15.9, 32 22.3 / 25.4 / 26.5, 48 32.7 / 29.0 / 30.8, 128 49.4 / 53.6 / 59.1;
-  // for 16 rows of 128 x 4 heads: 1 8.9 / 8.2 / 9.4, 8 12.1 / 13.7 / 14.5, 12 17.1 / 16.6 / 17.9,
-  // 32 26.7 / 27.8 / 31.0; 61 ragged ones with two new tokens 84 / 78 / 57.
+  // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs; other counts
+  // of SMs take them over).  us for equal sequences of 64 rows and 4096 tokens, clusters / even / by
+  // cost: 1 of them 16.5 / 11.3 / 11.8, 8 16.9 / 15.2 / 16.0, 32 23.7 / 26.8 / 27.8, 48 34.2 / 30.3 /
+  // 31.4, 128 52.2 / 57.2 / 61.2; for 16 rows of 128 x 4 heads: 1 9.2 / 8.4 / 9.4, 8 12.5 / 14.0 /
+  // 14.8, 12 17.7 / 17.1 / 18.2, 32 26.8 / 28.2 / 30.6; 61 ragged ones with two new tokens 90 / 86 / 63.
   const long long tile = pr->head_dim == 128 && sh.rows <= 32 ? 1400 : 2600;   // a tile
   constexpr long long kExchange = 3000;   // a cluster's exchange
   constexpr long long kSwitch = 18000;    // a second unit's beginning and end in a CTA's range
@@ -1585,9 +1588,12 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
   if (plan->num_ctas > 1 && !clusters) {
     // Teams that share a unit's parts, and then its elements' slices in CTAs of their own, while the
-    // parts and the grid's size pay for them.  Measured at 152 SMs (graph, us; d = 256, 64 rows), 1 / 2 / 4 / 8 teams:
-    // 1 unit of 32 parts 16.1 / 12.5 / 11.6 / 11.1, 8 of 16 16.8 / 15.9 / 14.7 / 16.8, 24 of 6
-    // 21.9 / 20.5 / 23.3 / 28.9, 48 of 3 28.6 / 31.0 / 36.2 / 46.3.
+    // parts and the grid's size pay for them.  Measured at 152 SMs (graph, us), 1 / 2 / 4 / 8 teams;
+    // d = 256, 64 rows: 1 unit of 32 parts 16.0 / 12.7 / 11.8 / 11.3, 8 of 16 15.2 / 14.2 / 13.2 / 15.2,
+    // 24 of 6 14.4 / 13.0 / 15.9 / 21.4, 48 of 3 14.2 / 16.4 / 21.9 / 32.0; d = 128, 64 rows: the same
+    // 15.9 / 11.3 / 10.5 / 9.9, 14.9 / 12.0 / 11.6 / 11.5, 14.2 / 11.5 / 11.5 / 14.5, 14.2 / 12.0 / 15.1 /
+    // 20.7; d = 128, 16 rows: 4 of 32 15.1 / 9.6 / 8.5 / 8.4, 8 of 16 11.7 / 8.5 / 8.2 / 8.7, 24 of 6
+    // 11.6 / 9.2 / 9.1 / 9.2, 48 of 3 11.3 / 8.9 / 9.1 / 9.6.
     const long long octs = sh.rows8 / 8;
     auto grid_of = [&](int teams) { return units * octs * (pr->head_dim / std::min(pr->head_dim, kBCombineThreads / teams)); };
     int teams = 1;
