@@ -73,16 +73,16 @@ constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scrat
 // quarter's largest 6 above those of the others, or 7 above that of one; what stands 2^21 under them
 // in their own tile is lost):
 //   it rises when x + e passes 7 over it, and then for the warpgroup's other rows too where that is a
-//   rise (rows that rise by themselves only come to a third more moves);
+//   rise (rows that rise by themselves only come to half as many moves again);
 //   it falls, to 24 below its highest at most, when a tile's largest x + e is 4 under it (without
 //   that, 32768 tokens behind one of 0.8 of the weight came out as 0.1 of their sum).
 // Falls are looked for in the tile after a move for the sake of few tokens, and every 64 tiles.
 // Measured on 8000 tokens of normal scores behind one to three of next to no value that stand 5 to 11
 // nats above (relative error of the output row, at most): 0.005; 0.013 with a fall at 6 under, 0.015
 // with 8 in place of 7, 0.009 without the 1 of room, 0.04 with no such rules.
-// A move costs its CTA some microseconds, most of it code that is not at hand: 32 / 128 sequences of
-// 4096 take 23.7 / 52.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62 with 6 of room for
-// all rows; and 22.3 / 49.5 when P was held to 2^-14 of a row's largest and nothing fell.
+// 32 / 128 sequences of 4096 take 23.7 / 52.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62
+// with 6 of room for all rows; and 22.3 / 49.5 when P was held to 2^-14 of a row's largest and nothing
+// fell.  (With as many moves as then the longer code of a move alone came to 2 us at 128 sequences.)
 // Scales are taken 2^-24 times smaller, the results as many times larger: p = 2^(x - reference)
 // and its sums then stay in fp32's range for scales from 2^-50 (smaller ones count as that: an
 // empty block's is 2^-126, and its P next to nothing either way) to the largest.
