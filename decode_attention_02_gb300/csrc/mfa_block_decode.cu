@@ -23,10 +23,10 @@
 // it (then O is rescaled in tensor memory), so that an ordinary tile costs one vote.
 //
 // What bounds it: for one new token a sequence the cache's bytes (512 a token at d = 256);
-// 64 rows, 128 sequences of 4096, one CTA each: 52.2 us, 5.3 TB/s, 78% of the copy rate; of the
+// 64 rows, 128 sequences of 4096, one CTA each: 51.3 us, 5.4 TB/s, 79% of the copy rate; of the
 // rest some 5 us are the beginning (lengths, q, the first tile's way through five stages), 2 us the
-// end and 3 us moves of references.  Short batches are bound by that chain (one sequence of 512:
-// 10.6 us).  Several tokens' units of a sequence read the same pages (from L2), and nothing alone
+// end and 2 us moves of references.  Short batches are bound by that chain (one sequence of 512:
+// 10.8 us).  Several tokens' units of a sequence read the same pages (from L2), and nothing alone
 // bounds them: a tile of 64 rows takes some 2300 clocks, of which its 208 KB are 1625 of shared
 // memory at 128 bytes a clock, and whole captures show shared memory's pipe and the tensor cores at
 // a third, issue slots at a half.
@@ -68,26 +68,26 @@ constexpr int kBMisc = 12288;         // of it, behind the ring: segments, scrat
 // is set by x + e, e the exponent of s_v, so that rounding is relative to the row's own P whatever
 // scales there are elsewhere.  Two parts, the second 32 times larger, resolve P to 2^-14 from 2^8
 // down (448 is e4m3's largest, and the first part leaves up to 8), and a P under 2^-15 is lost; so
-// the reference follows what a row is made of.  It lies 1 under a tile's largest x + e (in powers of
-// two, as all here), or 6 where few tokens outweigh what is about them, as first tokens do (a
-// quarter's largest 6 above those of the others, or 7 above that of one; what stands 2^21 under them
-// in their own tile is lost):
+// the reference follows what a row is made of.  It is set under a tile's largest x + e (in powers of
+// two, as all here): 1 under it, or as far, up to 6, as brings the other tokens up where few outweigh
+// them, as first tokens do (a quarter of the tile outweighs the others by 4 and more, or one of them by
+// 7 and more):
 //   it rises when x + e passes 7 over it, and then for the warpgroup's other rows too where that is a
 //   rise (rows that rise by themselves only come to half as many moves again);
-//   it falls, to 24 below its highest at most, when a tile's largest x + e is 4 under it (without
-//   that, 32768 tokens behind one of 0.8 of the weight came out as 0.1 of their sum).
-// Falls are looked for in the tile after a move for the sake of few tokens, and every 64 tiles.
+//   it falls, to 24 below its highest at most, in a tile that is looked at and whose largest x + e is 4
+//   under it (without that, 32768 tokens behind one of 0.8 of the weight came out as 0.1 of their sum).
+// A tile is looked at where the one before holds few tokens 11 over the others, or the eighth after it
+// if that happens again and again, and 32 tiles after the last look.
 // Measured on 8000 tokens of normal scores behind one to three of next to no value that stand 5 to 11
-// nats above (relative error of the output row, at most): 0.005; 0.013 with a fall at 6 under, 0.015
-// with 8 in place of 7, 0.009 without the 1 of room, 0.04 with no such rules.
-// 32 / 128 sequences of 4096 take 23.7 / 52.2 us, 23.1 / 51.1 with the cheapest of those choices, 26 / 62
-// with 6 of room for all rows; and 22.3 / 49.5 when P was held to 2^-14 of a row's largest and nothing
-// fell.  (With as many moves as then the longer code of a move alone came to 2 us at 128 sequences.)
+// nats above: the output row is off by 0.005 at most, by 0.4 to 0.6 with a reference that only rises.
+// Every move costs its CTA a microsecond or two.  128 sequences of 4096 with the queries as they are /
+// 2 / 3 times as large (deviations of the scores up to 2, 4, 6): 51.1 / 64.7 / 76.8 us, 49.3 / 52.6 /
+// 55.5 with a reference that only rises; 62 for the first with 6 of room for all rows.
 // Scales are taken 2^-24 times smaller, the results as many times larger: p = 2^(x - reference)
 // and its sums then stay in fp32's range for scales from 2^-50 (smaller ones count as that: an
 // empty block's is 2^-126, and its P next to nothing either way) to the largest.
-constexpr float kBThreshold = 7.0f, kBLow = -4.0f, kBDepth = 24.0f, kBRoom = 1.0f, kBRoomFew = 6.0f;
-constexpr int kBLookEvery = 64;
+constexpr float kBThreshold = 7.0f, kBLow = -4.0f, kBDepth = 24.0f, kBRoom = 1.0f, kBRoomFew = 6.0f, kBOver = 11.0f, kBNear = 4.0f;
+constexpr int kBLookEvery = 32;
 constexpr float kBScaleDown = 0x1p-24f, kBScaleUp = 0x1p24f;
 constexpr int kBEMin = -50 - 24, kBEMax = 127 - 24;
 constexpr float kBPart = 32.0f;   // the second part's factor
@@ -828,6 +828,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
       uint64_t l2[kC / 2] = {};   // row sums over this lane's tokens, pairs of rows
       if (row < kC) neg_ref[c0 + row] = top_neg[c0 + row] = INFINITY;
+      if (row == 0) look[c0] = n;
       if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
       named_bar_sync(vote_bar, 128);
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
@@ -907,21 +908,23 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               for (int i = 0; i < kC; i += 4)
                 *reinterpret_cast<float4*>(my_red + quarter * kC + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
             }
-            if (row == 0) look[c0] = n + kBLookEvery;
           }
           named_bar_sync(vote_bar, 128);
           if (row < kC) {
             const float a = my_red[row], b = my_red[kC + row], c = my_red[2 * kC + row], d = my_red[3 * kC + row];
             const float ab = fmaxf(a, b), cd = fmaxf(c, d), m = fmaxf(ab, cd);
             const float second = fmaxf(fminf(ab, cd), ab > cd ? fminf(a, b) : fminf(c, d)), least = fminf(fminf(a, b), fminf(c, d));
-            const bool few = m - fminf(second, least + 1.f) > 6.f;
-            const float was = neg_ref[c0 + row], top = top_neg[c0 + row], to = (few ? kBRoomFew : kBRoom) - floorf(m);
+            const float over = m - fminf(second, least + 3.f);   // how far few tokens outweigh the others
+            const float was = neg_ref[c0 + row], top = top_neg[c0 + row];
+            const float to = fminf(fmaxf(floorf(over) - 2.f, kBRoom), kBRoomFew) - floorf(m);
+            const int at = look[c0];
             float now = fminf(was, to);   // (as it was where the row sees nothing of the tile, or m is NaN)
-            if (m + was < kBLow && m > -INFINITY) now = fminf(to, top + kBDepth);
+            if (at == n && m + was < kBLow && m > -INFINITY) now = fminf(to, top + kBDepth);
+            const bool soon = __any_sync((1u << kC) - 1, over >= kBOver && m + was > kBNear);
+            if (row == 0 && (soon || at == n)) look[c0] = n + (!soon ? kBLookEvery : at - n <= kBLookEvery - 7 ? 1 : 8);   // (8: the last look is near)
             neg_ref[c0 + row] = now;
             top_neg[c0 + row] = fminf(top, now);
             alpha[c0 + row] = now < INFINITY ? ex2_approx(now - was) : 1.f;
-            if (few && least + now < kBLow) look[c0] = n + 1;
           }
           named_bar_sync(vote_bar, 128);
 #pragma unroll
@@ -1120,7 +1123,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   __syncthreads();
   if (p.cluster > 1) {
     // ---------------- the cluster's exchange, in place of partial results in the workspace and a
-    // second kernel (32 sequences of 4096, four CTAs each: 23.7 us against 26.8): CTA i takes rows
+    // second kernel (32 sequences of 4096, four CTAs each: 23.3 us against 26.4): CTA i takes rows
     // i, i + c, ... of the unit and adds up
     // the parts, in order, as they lie in the CTAs' rings.  (Every CTA comes here, whatever its roles
     // have met, and both barriers are the hardware's.)
@@ -1423,9 +1426,9 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   if (force_ctas > 0) G = force_ctas;
   // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs; other counts
   // of SMs take them over).  us for equal sequences of 64 rows and 4096 tokens, clusters / even / by
-  // cost: 1 of them 16.5 / 11.3 / 11.8, 8 16.9 / 15.2 / 16.0, 32 23.7 / 26.8 / 27.8, 48 34.2 / 30.3 /
-  // 31.4, 128 52.2 / 57.2 / 61.2; for 16 rows of 128 x 4 heads: 1 9.2 / 8.4 / 9.4, 8 12.5 / 14.0 /
-  // 14.8, 12 17.7 / 17.1 / 18.2, 32 26.8 / 28.2 / 30.6; 61 ragged ones with two new tokens 90 / 86 / 63.
+  // cost: 1 of them 16.3 / 11.5 / 12.0, 8 17.1 / 15.4 / 16.3, 32 23.2 / 26.4 / 27.6, 48 33.7 / 30.1 /
+  // 31.6, 128 51.3 / 55.8 / 60.9; for 16 rows of 128 x 4 heads: 1 9.3 / 8.4 / 9.4, 8 12.7 / 14.2 /
+  // 14.9, 12 17.5 / 17.0 / 18.3, 32 26.9 / 28.5 / 30.9; 61 ragged ones with two new tokens 90 / 85 / 63.
   const long long tile = pr->head_dim == 128 && sh.rows <= 32 ? 1400 : 2600;   // a tile
   constexpr long long kExchange = 3000;   // a cluster's exchange
   constexpr long long kSwitch = 18000;    // a second unit's beginning and end in a CTA's range
