@@ -45,6 +45,7 @@ MFA_PLAN_NO_COMBINE = 0x2
 MFA_PLAN_EARLY_METADATA = 0x4
 MFA_PLAN_EVEN_SPLIT = 0x100      # set by mfa_block_decode_plan alone
 MFA_PLAN_UNIT_CLUSTERS = 0x200   # likewise
+MFA_PLAN_WINDOW = 0x400          # set by mfa_window_decode_plan alone
 
 MFA_ROPE_HALF = 0
 MFA_ROPE_ADJACENT = 1
@@ -61,7 +62,7 @@ EXPORTED_SYMBOLS = ("mfa_decode_plan", "mfa_decode_run", "mfa_combine", "mfa_rea
                     "mfa_status_string", "mfa_abi_version", "mfa_last_cuda_error",
                     "mfa_decode_run_static_workspace", "mfa_kv_append", "mfa_decode_run_host",
                     "mfa_decode_append_run", "mfa_block_decode_plan", "mfa_block_decode_run", "mfa_block_kv_append",
-                    "mfa_rope_table", "mfa_rope_run")
+                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_rope_table", "mfa_rope_run")
 
 # Size of the library's own scratch array used by mfa_decode_run_static_workspace.
 MFA_STATIC_WORKSPACE_BYTES = 24 * 1024 * 1024
@@ -83,6 +84,10 @@ class MfaPlan(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("num_sms", ctypes.c_int32),
                 ("total_tiles", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64),
                 ("tokens_per_seq", ctypes.c_int32)]
+
+
+class MfaWindow(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 class MfaRopeConfig(ctypes.Structure):
@@ -155,6 +160,13 @@ def load_library(path: str = LIB_PATH):
     lib.mfa_block_decode_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, P,
                                          P, P, P, P, P, P, P, ctypes.c_uint64, P]
     lib.mfa_block_decode_run.restype = ctypes.c_int
+    lib.mfa_window_decode_plan.argtypes = [ctypes.POINTER(MfaProblem), ctypes.c_int32, ctypes.POINTER(MfaWindow), P,
+                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_uint32,
+                                           ctypes.POINTER(MfaPlan)]
+    lib.mfa_window_decode_plan.restype = ctypes.c_int
+    lib.mfa_window_decode_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), ctypes.c_int32,
+                                          ctypes.POINTER(MfaWindow), P, P, P, P, P, P, P, P, P, P, ctypes.c_uint64, P]
+    lib.mfa_window_decode_run.restype = ctypes.c_int
     lib.mfa_block_kv_append.argtypes = [ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, ctypes.c_int32, P,
                                         ctypes.c_int32, P, P, P, P, P, P, P, P]
     lib.mfa_block_kv_append.restype = ctypes.c_int
@@ -328,17 +340,22 @@ def mfa_kv_append(problem: MfaProblem, k_new, v_new, positions, block_table, k_c
     _check(st, "mfa_kv_append")
 
 
+def _host_lengths(problem: MfaProblem, host_seq_lens: Optional[Sequence[int]]):
+    """The lengths as the library takes them, one for each sequence (None: none)."""
+    if host_seq_lens is None:
+        return None
+    vals = [int(v) for v in host_seq_lens]
+    if len(vals) != problem.batch:
+        raise ValueError(f"host_seq_lens holds {len(vals)} lengths, the batch is {problem.batch}")
+    return (ctypes.c_int32 * max(1, len(vals)))(*vals)
+
+
 def mfa_block_decode_plan(problem: MfaProblem, scale_tokens: int, host_seq_lens: Optional[Sequence[int]] = None,
                           max_seq_len: int = 0, num_sms: int = 0, force_ctas: int = 0, flags: int = 0) -> MfaPlan:
     """Split the work of mfa_block_decode_run (host only); see include/mfa.h."""
     lib = load_library()
     plan = MfaPlan()
-    lens_arr = None
-    if host_seq_lens is not None:
-        vals = [int(v) for v in host_seq_lens]
-        if len(vals) != problem.batch:
-            raise ValueError(f"host_seq_lens holds {len(vals)} lengths, the batch is {problem.batch}")
-        lens_arr = (ctypes.c_int32 * max(1, len(vals)))(*vals)
+    lens_arr = _host_lengths(problem, host_seq_lens)
     st = lib.mfa_block_decode_plan(ctypes.byref(problem), int(scale_tokens), lens_arr, int(max_seq_len), int(num_sms),
                                    int(force_ctas), int(flags), ctypes.byref(plan))
     _check(st, "mfa_block_decode_plan")
@@ -356,6 +373,33 @@ def mfa_block_decode_run(plan: MfaPlan, problem: MfaProblem, scale_tokens: int, 
                                   _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
                                   _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream(stream))
     _check(st, "mfa_block_decode_run")
+
+
+def mfa_window_decode_plan(problem: MfaProblem, scale_tokens: int, window: MfaWindow,
+                           host_seq_lens: Optional[Sequence[int]] = None, max_seq_len: int = 0, num_sms: int = 0,
+                           force_ctas: int = 0, flags: int = 0) -> MfaPlan:
+    """Split the work of mfa_window_decode_run (host only); see include/mfa.h."""
+    lib = load_library()
+    plan = MfaPlan()
+    lens_arr = _host_lengths(problem, host_seq_lens)
+    st = lib.mfa_window_decode_plan(ctypes.byref(problem), int(scale_tokens), ctypes.byref(window), lens_arr,
+                                    int(max_seq_len), int(num_sms), int(force_ctas), int(flags), ctypes.byref(plan))
+    _check(st, "mfa_window_decode_plan")
+    return plan
+
+
+def mfa_window_decode_run(plan: MfaPlan, problem: MfaProblem, scale_tokens: int, window: MfaWindow, q, k_cache, v_cache,
+                          k_scale, v_scale, block_table, seq_lens, out, lse, workspace, stream=None,
+                          workspace_bytes: Optional[int] = None) -> None:
+    """One decode step over the window and the first tokens of a block-scaled 8-bit cache (see include/mfa.h)."""
+    lib = load_library()
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    st = lib.mfa_window_decode_run(ctypes.byref(plan), ctypes.byref(problem), scale_tokens, ctypes.byref(window), _ptr(q),
+                                   _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                                   _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+                                   _stream(stream))
+    _check(st, "mfa_window_decode_run")
 
 
 def mfa_block_kv_append(problem: MfaProblem, scale_tokens: int, k_new, v_new, num_new: int, new_offsets, max_new: int,
@@ -532,27 +576,44 @@ class BlockDecoder(_OnDevice):
     inputs, or be waited for by it.  What it uses stays allocated until it is done: the decoder's
     workspace always, the tensors of a call with ``stream`` too.  A captured call's decoder and
     tensors have to outlive the graph.
+
+    ``window``: a new token sees only itself, the ``window - 1`` tokens before it and the sequence's first
+    ``sinks`` tokens; the pages between are not read.  (None: all tokens before it.)
     """
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, num_q_heads: int = NUM_Q_HEADS,
                  num_kv_heads: int = 1, head_dim: int = HEAD_DIM, scale_tokens: int = 64,
                  softmax_scale: Optional[float] = None, host_seq_lens=None, max_seq_len: int = 0, force_ctas: int = 0,
-                 flags: int = 0, device=None, out_dtype: int = MFA_OUT_BF16, tokens_per_seq: int = 1):
+                 flags: int = 0, device=None, out_dtype: int = MFA_OUT_BF16, tokens_per_seq: int = 1,
+                 window: Optional[int] = None, sinks: int = 0):
         super().__init__(device)
         torch = self._torch
         self.scale_tokens = int(scale_tokens)
+        if window is None and sinks:
+            raise ValueError("sinks: first tokens stay visible beside a window, and there is none")
+        self.window = None if window is None else MfaWindow(int(window), int(sinks))
         self.problem = make_problem(batch, max_pages_per_seq, num_blocks, MFA_KV_FP8_E4M3, softmax_scale,
                                     num_q_heads=num_q_heads, head_dim=head_dim, out_dtype=out_dtype,
                                     tokens_per_seq=tokens_per_seq, num_kv_heads=num_kv_heads)
         if host_seq_lens is None and max_seq_len == 0:
             max_seq_len = max_pages_per_seq * PAGE_SIZE
         with torch.cuda.device(self.device):
-            self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
-                                              force_ctas, flags)
+            if self.window is None:
+                self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
+                                                  force_ctas, flags)
+            else:
+                self.plan = mfa_window_decode_plan(self.problem, self.scale_tokens, self.window, host_seq_lens, max_seq_len,
+                                                   0, force_ctas, flags)
             self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
         self._refs = (ctypes.byref(self.plan), ctypes.byref(self.problem))
+        # the library's decode and its arguments up to q
+        if self.window is None:
+            self._run = (self._lib.mfa_block_decode_run, "mfa_block_decode_run", (*self._refs, self.scale_tokens))
+        else:
+            self._run = (self._lib.mfa_window_decode_run, "mfa_window_decode_run",
+                         (*self._refs, self.scale_tokens, ctypes.byref(self.window)))
         rows = batch * tokens_per_seq
         self._q_shape = torch.Size((rows, num_q_heads, head_dim))
         self._lse_shape = self._q_shape[:2]
@@ -620,10 +681,11 @@ class BlockDecoder(_OnDevice):
         self._torch.cuda.current_stream(self._index).synchronize()
 
     def _decode(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, stream) -> None:
-        self._call(self._lib.mfa_block_decode_run, "mfa_block_decode_run",
-                   (*self._refs, self.scale_tokens, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                    k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
+        function, where, head = self._run
+        self._call(function, where,
+                   (*head, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                    block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                    self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
                    (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse))
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,

@@ -175,10 +175,48 @@ struct BlockDecodeParams {
   int cluster;               // CTAs of a unit, one cluster; 0: split evenly or by cost
   int log_scale;             // log2(scale_tokens)
   int max_pages, num_blocks;
+  int window, sinks;         // windowed instances: the tokens that a new token sees (0: all)
   float scale_log2;          // softmax_scale * log2(e)
   int out_f32;
   int early_metadata;
 };
+
+// ------------------------------------------------------------------ windows
+//
+// With a window, new token i of a sequence's T, at position p = L - T + i, sees the tokens t <= p with
+// t < sinks or t > p - window.  The pages between the sinks' and the first that the window of new token 0
+// touches are left out, and the rest laid end to end: a sequence of L' = L - 64 skip tokens, on which
+// everything else works as on any other, but for where a page lies and what a row sees:
+//   page v is the sequence's page v, or v + skip from the sinks' pages on;
+//   row i sees t' < L' - T + 1 + i with t' < sinks or t' >= low + i (both also where nothing is left out:
+//   every t' in a sink's page behind the sinks is under low).
+// A page's rows under the window's first token are not loaded, nor those behind the last sink, so that
+// whatever they hold reaches nothing: the box starts at the first row that anyone sees and is filled with
+// zeros behind the page, as the last page's box is before it.  Where a box cannot leave out what no one
+// sees (the window starts in the last page, or in the last of the sinks'), the PV issuer's warp zeroes
+// those rows of the values.
+struct BlockView {
+  int L, skip, low, sink_pages;
+};
+__host__ __device__ __forceinline__ BlockView block_view(int L, int tokens, int window, int sinks) {
+  BlockView v;
+  v.low = L - tokens - window + 1;   // new token 0's first token of its window (window <= the table's tokens)
+  v.sink_pages = (sinks + kBPage - 1) / kBPage;
+  v.skip = v.low > 0 ? v.low / kBPage - v.sink_pages : 0;
+  if (v.skip < 0) v.skip = 0;
+  v.L = L - kBPage * v.skip;
+  v.low -= kBPage * v.skip;
+  return v;
+}
+// The tokens that a sequence of L has to go over.
+__device__ __forceinline__ int block_length(const BlockDecodeParams& p, int L) {
+  return p.window > 0 ? block_view(L, p.tokens, p.window, p.sinks).L : L;
+}
+template <bool kWindow>
+__device__ __forceinline__ int view_length(const BlockDecodeParams& p, int L) {
+  if constexpr (kWindow) return block_view(L, p.tokens, p.window, p.sinks).L;
+  return L;
+}
 
 // ------------------------------------------------------------------ schedule
 //
@@ -206,7 +244,7 @@ __device__ __noinline__ int wider_quantum(const BlockDecodeParams& p, int cap) {
   long long tiles = 0, units = 0;
   bool bad = false;
   for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
-    const int T = (clamp_len(p.seq_lens[b], cap, bad) + kBTile - 1) / kBTile;
+    const int T = (block_length(p, clamp_len(p.seq_lens[b], cap, bad)) + kBTile - 1) / kBTile;
     tiles += T;
     units += T > 0;
   }
@@ -282,6 +320,7 @@ struct __align__(16) BlockSegment {
   int slot;                // of the partial result; -1: the whole unit; -2: a part, for the cluster's exchange
 };
 
+template <bool kWindow>
 __device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSegment* seg, int at, int b, int r, int L, int lo,
                                             int hi, long long slot) {
   if (at >= kBMaxSeg) return;
@@ -292,13 +331,14 @@ __device__ __forceinline__ void add_segment(const BlockDecodeParams& p, BlockSeg
   x.L = L;
   x.lo = lo;
   x.hi = hi;
-  x.slot = lo == 0 && hi == block_tiles(L) ? -1 : static_cast<int>(slot);
+  x.slot = lo == 0 && hi == block_tiles(view_length<kWindow>(p, L)) ? -1 : static_cast<int>(slot);
   seg[at] = x;
 }
 
 // This CTA's segments, by one warp (a lane a sequence), into shared memory; their number and this
 // lane's tiles in (nseg, tiles).  Every CTA runs it before its first load, so it is kept short (61
 // sequences by cost: 2.3 us, evenly 1.0, one unit a cluster 0.8).
+template <bool kWindow>
 __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                               bool& bad) {
   const int lane = threadIdx.x & 31;
@@ -311,7 +351,7 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
     for (int c0 = 0; c0 < p.batch; c0 += 32) {
       const int L = clamp_len(next, cap, bad);
       next = c0 + 32 + lane < p.batch ? p.seq_lens[c0 + 32 + lane] : 0;
-      const int T = block_tiles(L), n = even_parts(T, quantum);
+      const int T = block_tiles(view_length<kWindow>(p, L)), n = even_parts(T, quantum);
       const long long own = static_cast<long long>(n) * p.readers;
       long long incl = own;
 #pragma unroll
@@ -331,7 +371,7 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
             lo = i * each + min(i, more);
             hi = lo + each + (i < more ? 1 : 0);
           }
-          add_segment(p, seg, nseg, c0 + lane, r, L, lo, hi, item);
+          add_segment<kWindow>(p, seg, nseg, c0 + lane, r, L, lo, hi, item);
           tiles += hi - lo;
         }
         ++nseg;
@@ -345,16 +385,16 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
 }
 
 // I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).
-template <typename I>
+template <typename I, bool kWindow>
 __device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                               bool& bad) {
   const int lane = threadIdx.x & 31;
   auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
   auto cost = [](int T) { return T > 0 ? static_cast<I>(kBCostTile) * T + kBCostUnit : I{0}; };
   const int L0 = length(lane);
-  I per = cost(block_tiles(L0));   // of one reader of every sequence
+  I per = cost(block_tiles(view_length<kWindow>(p, L0)));   // of one reader of every sequence
 #pragma unroll 1
-  for (int b = lane + 32; b < p.batch; b += 32) per += cost(block_tiles(length(b)));
+  for (int b = lane + 32; b < p.batch; b += 32) per += cost(block_tiles(view_length<kWindow>(p, length(b))));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) per += __shfl_xor_sync(0xffffffffu, per, o);
   if (per == 0) return;
@@ -374,7 +414,7 @@ __device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int ca
     for (int c0 = 0; c0 < p.batch && carry < X1; c0 += 32) {
       const int L = next;
       next = length(c0 + 32 + lane);
-      const int T = block_tiles(L);
+      const int T = block_tiles(view_length<kWindow>(p, L));
       const I own = cost(T);
       I incl = own;
 #pragma unroll
@@ -386,7 +426,7 @@ __device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int ca
       const int lo = first_tile_at(X0, base, T), hi = first_tile_at(X1, base, T);
       const unsigned has = __ballot_sync(0xffffffffu, lo < hi);
       if (lo < hi) {
-        add_segment(p, seg, nseg + __popc(has & ((1u << lane) - 1u)), c0 + lane, r, L, lo, hi,
+        add_segment<kWindow>(p, seg, nseg + __popc(has & ((1u << lane) - 1u)), c0 + lane, r, L, lo, hi,
                     static_cast<long long>(r) * p.batch + c0 + lane + blockIdx.x);
         tiles += hi - lo;
       }
@@ -396,9 +436,10 @@ __device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int ca
   }
 }
 // (the wide form, for problems of millions of tiles, out of the way of the usual one's code)
+template <bool kWindow>
 __device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                                 bool& bad) {
-  cost_segments<long long>(p, cap, seg, nseg, tiles, bad);
+  cost_segments<long long, kWindow>(p, cap, seg, nseg, tiles, bad);
 }
 
 __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float (&a)[4], float scale) {
@@ -407,30 +448,32 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float (&a)
 }
 
 // A unit's CTAs: only its own sequence's length is read.
+template <bool kWindow>
 __device__ __forceinline__ void unit_segment(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                              bool& bad) {
   if ((threadIdx.x & 31) != 0) return;
   const unsigned c = p.cluster, unit = c == 1 ? blockIdx.x : blockIdx.x / c, i = blockIdx.x - unit * c;
   const int r = unit / p.batch, b = unit - r * p.batch;
   const int L = clamp_len(p.seq_lens[b], cap, bad);
-  const unsigned T = block_tiles(L);
+  const unsigned T = block_tiles(view_length<kWindow>(p, L));
   const int lo = c == 1 ? 0 : i * T / c, hi = c == 1 ? T : (i + 1) * T / c;
-  add_segment(p, seg, 0, b, r, L, lo, hi, -2);   // (without tiles too: the exchange wants the unit)
+  add_segment<kWindow>(p, seg, 0, b, r, L, lo, hi, -2);   // (without tiles too: the exchange wants the unit)
   nseg = lo < hi ? 1 : 0;
   tiles = hi - lo;
 }
 
+template <bool kWindow>
 __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int* counts) {
   int nseg = 0, tiles = 0;
   bool bad = false;
   if (p.cluster > 0)
-    unit_segment(p, cap, seg, nseg, tiles, bad);
+    unit_segment<kWindow>(p, cap, seg, nseg, tiles, bad);
   else if (p.quantum > 0)
-    even_segments(p, cap, seg, nseg, tiles, bad);
+    even_segments<kWindow>(p, cap, seg, nseg, tiles, bad);
   else if (p.narrow)
-    cost_segments<uint32_t>(p, cap, seg, nseg, tiles, bad);
+    cost_segments<uint32_t, kWindow>(p, cap, seg, nseg, tiles, bad);
   else
-    cost_segments_wide(p, cap, seg, nseg, tiles, bad);
+    cost_segments_wide<kWindow>(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   if (nseg > kBMaxSeg) {
@@ -443,17 +486,51 @@ __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int c
   }
 }
 
+// The rows of page v of a sequence that any new token sees: [from, to), none where to <= 0; page row
+// `first` lies in the box's row 0.
+struct BlockRows {
+  int from, to, first;
+};
+template <bool kWindow>
+__device__ __forceinline__ BlockRows view_rows(const BlockView& w, int sinks, int v) {
+  BlockRows r = {0, min(kBPage, w.L - kBPage * v), 0};
+  if constexpr (kWindow) {
+    if (w.low >= kBPage * w.sink_pages) {   // the window starts behind the sinks' pages
+      if (v == w.sink_pages - 1) r.to = min(r.to, sinks - kBPage * v);
+      if (v == w.low / kBPage) r.from = w.low % kBPage;
+    }
+  }
+  r.first = kWindow && r.from > 0 && r.to == kBPage ? r.from : r.to - kBPage;
+  return r;
+}
+
+// The rows of page v's box that are loaded and that no new token sees: [x, y), box rows.
+__device__ __forceinline__ int2 view_gap(const BlockView& w, int sinks, int v) {
+  const BlockRows r = view_rows<true>(w, sinks, v);
+  int from = 0, to = 0;
+  if (r.first < 0 && r.from > 0)
+    to = r.from;
+  else if (w.low < kBPage * w.sink_pages && v == w.sink_pages - 1)
+    from = sinks - kBPage * v, to = min(w.low - kBPage * v, r.to);
+  return make_int2(from - r.first, to - r.first);
+}
+
 // A role's place in its CTA's run of tiles.
+template <bool kWindow>
 struct BlockTile {
   int s, j, end;           // segment, tile of the sequence, end of the segment
-  int b, kvh, L;
+  int b, kvh;
+  BlockView w;
   bool again;              // another unit reads the tile's pages after this one
   __device__ __forceinline__ void load(const BlockDecodeParams& p, const BlockSegment* seg, int at) {
     const BlockSegment x = seg[at];
     s = at;
     b = x.b;
     kvh = x.kvh;
-    L = x.L;
+    if constexpr (kWindow)
+      w = block_view(x.L, p.tokens, p.window, p.sinks);
+    else
+      w.L = x.L;
     j = x.lo;
     end = x.hi;
     again = x.tg != p.token_groups - 1;
@@ -465,11 +542,16 @@ struct BlockTile {
     load(p, seg, s + 1);
     return true;
   }
-  __device__ __forceinline__ int page_rows(int pg) const { return min(kBPage, L - kBTile * j - kBPage * pg); }
+  // the tile's page pg in the sequence's table, and its rows
+  __device__ __forceinline__ int page(int pg) const {
+    const int v = 2 * j + pg;
+    return kWindow && v >= w.sink_pages ? v + w.skip : v;
+  }
+  __device__ __forceinline__ BlockRows rows(const BlockDecodeParams& p, int pg) const { return view_rows<kWindow>(w, p.sinks, 2 * j + pg); }
 };
 
 // ------------------------------------------------------------------ decode kernel
-template <int kDim, int kNR>
+template <int kDim, int kNR, bool kWindow>
 __global__ void __launch_bounds__(BlockLayout<kDim, kNR>::kThreads, 1)
 mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   using Lay = BlockLayout<kDim, kNR>;
@@ -530,7 +612,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   // nothing that the preceding kernel may write is read before this; with early metadata the
   // lengths are (the caller says that it does not write them)
   if (!p.early_metadata) grid_dep_wait();
-  if (warp == 0) block_segments(p, cap, seg, ctl + 2);
+  if (warp == 0) block_segments<kWindow>(p, cap, seg, ctl + 2);
   __syncthreads();
   if (p.early_metadata) grid_dep_wait();
   grid_dep_launch();
@@ -546,10 +628,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const int half = (lane % kBoxes) >> 1, pg = lane & 1;
       const int slots = is_v ? kVSlots : kKSlots, slot0 = is_v ? kKSlots : 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_last();
-      BlockTile it;
+      BlockTile<kWindow> it;
       it.load(p, seg, 0);
       auto page_id = [&]() -> int {
-        return it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : 0;
+        return it.rows(p, pg).to > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + it.page(pg)] : 0;
       };
       int id = page_id();
       int slot = half, phase = 0;   // (half < slots)
@@ -559,7 +641,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       // come first
       for (int round = is_v ? -1 : 0; n < ntiles; ++round) {
         if (round < 0) continue;
-        const int rows = it.page_rows(pg);
+        const int rows = it.rows(p, pg).to, first = it.rows(p, pg).first;
         int z = id * p.kv_heads + it.kvh;
         if (rows > 0 && (id < 0 || id >= p.num_blocks)) {
           z = -1;   // outside the pool: the whole box reads as zeros
@@ -573,10 +655,11 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         if (rows <= 0) {
           mbar_arrive(fb);
         } else {
-          // the last page's rows land at the end of the box: rows before them are filled with zeros
+          // the last page's rows land at the end of the box: rows before them are filled with zeros (a
+          // window's first page's at its beginning)
           mbar_arrive_expect_tx(fb, 8192);
           tma_load_3d_hint(sbase + Lay::kOffRing + (slot0 + slot) * Lay::kSlotBytes + pg * 8192, is_v ? &p.tm_v : &p.tm_k,
-                           fb, 128 * half, rows - kBPage, z, pol);
+                           fb, 128 * half, first, z, pol);
         }
         ++n;
         slot += kHalves;
@@ -636,40 +719,65 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     __syncwarp();
   } else if (warp == kBPvWarp) {
     // ---------------- PV issuer: O^T += V^T P^T, the weights' hi and lo parts in columns of their own
-    if (lane == 0 && ntiles > 0) {
+    // (with a window the whole warp comes along: it zeroes values that no new token sees)
+    if ((kWindow || lane == 0) && ntiles > 0) {
       constexpr uint32_t kIdescPV = idesc_e4m3(true, true, 128, 2 * kNR);
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
+      auto all = [](bool x) { return kWindow ? __all_sync(0xffffffffu, x) != 0 : x; };
       for (int s = 0; s < nseg && ok; ++s) {
-        const int lo = seg[s].lo, hi = seg[s].hi, L = seg[s].L;
+        const int lo = seg[s].lo, hi = seg[s].hi;
+        BlockView w;
+        if constexpr (kWindow)
+          w = block_view(seg[s].L, p.tokens, p.window, p.sinks);
+        else
+          w.L = seg[s].L;
         for (int j = lo; j < hi && ok; ++j, ++n) {
-          ok = block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag);
-          if (ok && j == lo && s > 0) ok = block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag);
-          const bool both = L > kBTile * j + kBPage;   // the tile has its second page
+          ok = all(block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag));
+          if (ok && j == lo && s > 0) ok = all(block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag));
+          const bool both = w.L > kBTile * j + kBPage;   // the tile has its second page
           const uint64_t bd = smem_desc(sbase + Lay::kOffP + (n % kPBufs) * 16384, 8192, 1024);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = block_wait(bar(kFull + kKSlots + slot), phase, abort_flag);
+            if (ok) ok = all(block_wait(bar(kFull + kKSlots + slot), phase, abort_flag));
             if (!ok) break;
+            if constexpr (kWindow) {
+              bool any = false;
+#pragma unroll 1
+              for (int pg = 0; pg < (both ? 2 : 1); ++pg) {
+                const int2 gap = view_gap(w, p.sinks, 2 * j + pg);
+                uint8_t* box = smem + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes + pg * 8192;
+                for (int r = gap.x + (lane >> 3); r < gap.y; r += 4) *reinterpret_cast<uint4*>(box + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                any |= gap.x < gap.y;
+              }
+              if (any) {
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
             tc_fence_after();
             const uint64_t ad = smem_desc(sbase + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
             const uint32_t d = tmem + Lay::kTmemO + 2 * kNR * h;
+            if (!kWindow || lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
-              if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == lo && kk == 0));
-            umma_commit(bar(kEmpty + kKSlots + slot));
+              for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
+                if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == lo && kk == 0));
+              umma_commit(bar(kEmpty + kKSlots + slot));
+            }
             if (++slot == kVSlots) {
               slot = 0;
               phase ^= 1;
             }
           }
           if (!ok) break;
-          umma_commit(bar(kPvDone + (n & 1)));
+          if (!kWindow || lane == 0) umma_commit(bar(kPvDone + (n & 1)));
         }
       }
-      if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
-      umma_commit(bar(kDrain));
-      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
+      if (!kWindow || lane == 0) {
+        if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
+        umma_commit(bar(kDrain));
+        wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
+      }
     }
     __syncwarp();
   } else if (warp == kBScaleWarp) {
@@ -684,14 +792,14 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
         const BlockSegment x = seg[i];
         int2* at = p.parts + static_cast<size_t>(x.kvh * p.token_groups + x.tg) * p.batch + x.b;
         if (x.lo == 0) at->x = x.slot;
-        if (x.hi == block_tiles(x.L)) at->y = x.slot;
+        if (x.hi == block_tiles(view_length<kWindow>(p, x.L))) at->y = x.slot;
       }
     }
     if (ntiles > 0) {
-      BlockTile it;
+      BlockTile<kWindow> it;
       it.load(p, seg, 0);
       auto page_id = [&]() -> int {
-        return mine && it.page_rows(pg) > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + 2 * it.j + pg] : -1;
+        return mine && it.rows(p, pg).to > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + it.page(pg)] : -1;
       };
       auto scale_of = [&](int id) -> float {
         if (id < 0 || id >= p.num_blocks) return 0.f;
@@ -824,8 +932,18 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     int n = 0;
     for (int s = 0; s < nseg && !stop; ++s) {
       const BlockSegment sg = seg[s];
-      const int L = sg.L;
-      const int seen0 = L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
+      BlockView w;
+      if constexpr (kWindow)
+        w = block_view(sg.L, p.tokens, p.window, p.sinks);
+      else
+        w.L = sg.L;
+      const int seen0 = w.L - (p.tokens - 1) + sg.tg * p.unit_tokens;   // tokens that the unit's first row sees
+      const int low0 = kWindow ? w.low + sg.tg * p.unit_tokens : 0;     // (of the window: from here on)
+      // whether a row of the unit's new token x sees token t
+      auto sees = [&](int t, int x) {
+        if constexpr (kWindow) return t < seen0 + x && (t >= low0 + x || t < p.sinks);
+        return t < seen0 + x;
+      };
       uint64_t l2[kC / 2] = {};   // row sums over this lane's tokens, pairs of rows
       if (row < kC) neg_ref[c0 + row] = top_neg[c0 + row] = INFINITY;
       if (row == 0) look[c0] = n;
@@ -834,11 +952,14 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
       const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(neg_ref + c0);
       for (int j = sg.lo; j < sg.hi; ++j, ++n) {
-        const int pr = ri - (kBPage - min(kBPage, L - kBTile * j - kBPage * pg));   // page row of this lane's box row
-        const int t = pr >= 0 ? kBTile * j + kBPage * pg + pr : INT_MAX;            // and its token
+        const BlockRows rows = view_rows<kWindow>(w, p.sinks, 2 * j + pg);
+        const int pr = ri + rows.first;                                  // page row of this lane's box row
+        int t = pr >= rows.from ? kBTile * j + kBPage * pg + pr : INT_MAX;   // and its token, if any row sees it
+        if (kWindow && (pr >= rows.to || (t < w.low && t >= p.sinks))) t = INT_MAX;
+        const bool held = t != INT_MAX;
         if (!block_wait(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
-        const float2 sc = pr >= 0 ? meta[(n & 1) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
+        const float2 sc = held ? meta[(n & 1) * 8 + pg * 4 + (pr >> p.log_scale)] : make_float2(0.f, 0.f);
         const uint64_t a2 = pack_f32x2(sc.x, sc.x);
         const float e = static_cast<float>(min(max(static_cast<int>(__float_as_uint(sc.y) >> 23) - 127, kBEMin), kBEMax));
         uint64_t x2[kC / 2];
@@ -856,10 +977,10 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), m.y);
             }
           }
-          if (kBTile * (j + 1) <= seen0) {
+          if (kBTile * (j + 1) <= seen0 && (!kWindow || kBTile * j >= low0 + p.unit_tokens - 1 || kBTile * (j + 1) <= p.sinks)) {
             // every row sees the whole tile
           } else if (p.unit_tokens == 1) {
-            if (t >= seen0) {
+            if (!sees(t, 0)) {
 #pragma unroll
               for (int i = 0; i < kC / 2; ++i) x2[i] = pack_f32x2(-INFINITY, -INFINITY);
             }
@@ -869,7 +990,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               float lo, hi;
               unpack_f32x2(x2[i], lo, hi);
               const int2 tok = *reinterpret_cast<const int2*>(row_tok + c0 + 2 * i);
-              x2[i] = pack_f32x2(t < seen0 + tok.x ? lo : -INFINITY, t < seen0 + tok.y ? hi : -INFINITY);
+              x2[i] = pack_f32x2(sees(t, tok.x) ? lo : -INFINITY, sees(t, tok.y) ? hi : -INFINITY);
             }
           }
           if (settled) break;
@@ -897,9 +1018,9 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               y[i + 2] = fmaf(__uint_as_float(sr[i + 2]), sc.x * w.z, e);
               y[i + 3] = fmaf(__uint_as_float(sr[i + 3]), sc.x * w.w, e);
             }
-            if (kBTile * (j + 1) > seen0) {
+            if (kWindow || kBTile * (j + 1) > seen0) {
 #pragma unroll
-              for (int i = 0; i < kC; ++i) y[i] = t < seen0 + row_tok[c0 + i] ? y[i] : -INFINITY;
+              for (int i = 0; i < kC; ++i) y[i] = sees(t, row_tok[c0 + i]) ? y[i] : -INFINITY;
             }
 #pragma unroll
             for (int i = 0; i < kC; ++i) y[i] = warp_max(y[i]);
@@ -1129,7 +1250,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     // have met, and both barriers are the hardware's.)
     const unsigned c = p.cluster, rank = blockIdx.x % c;
     const BlockSegment sg = seg[0];
-    const unsigned T = block_tiles(sg.L);
+    const unsigned T = block_tiles(view_length<kWindow>(p, sg.L));
     const unsigned parts = __ballot_sync(0xffffffffu, lane < c && lane * T / c < (lane + 1) * T / c);   // those with tiles
     cluster_sync();
     if (T > 1 && warp >= kBSoftmaxWarp0) {
@@ -1205,7 +1326,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
   int2 at = make_int2(0, -1);
   const int cap = p.max_pages * kBPage;
   bool bad = false;
-  const int T = block_tiles(clamp_len(p.seq_lens[b], cap, bad));
+  const int T = block_tiles(block_length(p, clamp_len(p.seq_lens[b], cap, bad)));
   if (p.quantum > 0) {
     int quantum = p.quantum;
 #pragma unroll 1
@@ -1214,7 +1335,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
       long long all = 0;     // and of all
 #pragma unroll 1
       for (int i = lane; i < p.batch; i += 32) {
-        const int n = even_parts(block_tiles(clamp_len(p.seq_lens[i], cap, bad)), quantum);
+        const int n = even_parts(block_tiles(block_length(p, clamp_len(p.seq_lens[i], cap, bad))), quantum);
         all += n;
         before += i < b ? n : 0;
       }
@@ -1351,13 +1472,16 @@ using BlockDecodeFn = void (*)(BlockDecodeParams);
 using BlockCombineFn = void (*)(BlockDecodeParams);
 
 // The instance of a problem: width and rows padded to 16, 32 or 64.
-static int block_instance(const mfa_problem* pr, const BlockShape& sh) {
-  return (pr->head_dim == 256 ? 3 : 0) + (sh.rows <= 16 ? 0 : sh.rows <= 32 ? 1 : 2);
+static int block_instance(const mfa_problem* pr, const BlockShape& sh, bool window) {
+  return (window ? 6 : 0) + (pr->head_dim == 256 ? 3 : 0) + (sh.rows <= 16 ? 0 : sh.rows <= 32 ? 1 : 2);
 }
+constexpr int kBInstances = 12;
 static BlockDecodeFn block_kernel_of(int i) {
-  constexpr BlockDecodeFn k[6] = {mfa_block_decode_kernel<128, 16>, mfa_block_decode_kernel<128, 32>,
-                                  mfa_block_decode_kernel<128, 64>, mfa_block_decode_kernel<256, 16>,
-                                  mfa_block_decode_kernel<256, 32>, mfa_block_decode_kernel<256, 64>};
+  constexpr BlockDecodeFn k[kBInstances] = {
+      mfa_block_decode_kernel<128, 16, false>, mfa_block_decode_kernel<128, 32, false>, mfa_block_decode_kernel<128, 64, false>,
+      mfa_block_decode_kernel<256, 16, false>, mfa_block_decode_kernel<256, 32, false>, mfa_block_decode_kernel<256, 64, false>,
+      mfa_block_decode_kernel<128, 16, true>,  mfa_block_decode_kernel<128, 32, true>,  mfa_block_decode_kernel<128, 64, true>,
+      mfa_block_decode_kernel<256, 16, true>,  mfa_block_decode_kernel<256, 32, true>,  mfa_block_decode_kernel<256, 64, true>};
   return k[i];
 }
 
@@ -1369,7 +1493,7 @@ static int block_threads(int i) {
 // cudaFuncSetAttribute for an instance's dynamic shared memory, once per device and instance.
 static mfa_status ensure_block_smem(int i) {
   constexpr int kMaxDevices = 64;
-  static std::atomic<bool> done[6][kMaxDevices];
+  static std::atomic<bool> done[kBInstances][kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -1381,32 +1505,42 @@ static mfa_status ensure_block_smem(int i) {
   return MFA_OK;
 }
 
-}  // namespace mfa
+// A window, its sizes cut to the table's tokens (which changes nothing that a token sees).
+static mfa_status check_window(const mfa_problem* pr, const mfa_window* window, mfa_window* cut) {
+  if (window == nullptr || window->tokens < 1 || window->sinks < 0) return MFA_ERR_INVALID_ARG;
+  const int cap = pr->max_pages_per_seq * kBPage;
+  *cut = {std::min(window->tokens, cap), std::min(window->sinks, cap)};
+  return MFA_OK;
+}
 
-using namespace mfa;
-
-extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale_tokens, const int32_t* host_seq_lens,
-                                            int32_t max_seq_len, int32_t num_sms, int32_t force_ctas, uint32_t flags,
-                                            mfa_plan* plan) {
-  const mfa_status st = check_block_problem(pr, scale_tokens);
-  if (st != MFA_OK) return st;
+static mfa_status block_plan(const mfa_problem* pr, const mfa_window* window, const int32_t* host_seq_lens, int32_t max_seq_len,
+                             int32_t num_sms, int32_t force_ctas, uint32_t flags, mfa_plan* plan) {
   if (plan == nullptr || force_ctas < 0) return MFA_ERR_INVALID_ARG;
   if (flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA)) return MFA_ERR_INVALID_ARG;
   const long long cap = static_cast<long long>(pr->max_pages_per_seq) * kBPage;
   const BlockShape sh = block_shape(pr);
   long long tiles = 0, nonempty = 0, longest = 0;   // tiles of one reader of each sequence
+  auto tiles_of = [&](int L) -> long long {
+    if (window != nullptr) L = block_view(L, pr->tokens_per_seq, window->tokens, window->sinks).L;
+    return (L + kBTile - 1) / kBTile;
+  };
   if (host_seq_lens != nullptr) {
     for (int b = 0; b < pr->batch; ++b) {
       if (host_seq_lens[b] < 0 || host_seq_lens[b] > cap) return MFA_ERR_INVALID_ARG;
-      tiles += (host_seq_lens[b] + kBTile - 1) / kBTile;
+      tiles += tiles_of(host_seq_lens[b]);
       nonempty += host_seq_lens[b] > 0;
-      longest = std::max<long long>(longest, (host_seq_lens[b] + kBTile - 1) / kBTile);
+      longest = std::max(longest, tiles_of(host_seq_lens[b]));
     }
   } else {
     if (max_seq_len < 0 || max_seq_len > cap) return MFA_ERR_INVALID_ARG;
-    tiles = static_cast<long long>(pr->batch) * ((max_seq_len + kBTile - 1) / kBTile);
-    nonempty = max_seq_len > 0 ? pr->batch : 0;
     longest = (max_seq_len + kBTile - 1) / kBTile;
+    if (window != nullptr) {   // the sinks' pages, the window and up to a page before it
+      const long long most = (window->sinks + kBPage - 1) / kBPage * kBPage + static_cast<long long>(window->tokens) +
+                             pr->tokens_per_seq - 1 + kBPage - 1;
+      longest = std::min(longest, (most + kBTile - 1) / kBTile);
+    }
+    tiles = pr->batch * longest;
+    nonempty = max_seq_len > 0 ? pr->batch : 0;
   }
   if (num_sms <= 0) {
     int dev = 0;
@@ -1456,7 +1590,7 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
       auto parts_at = [&](long long q) {
         long long parts = 0;
         if (host_seq_lens != nullptr)
-          for (int b = 0; b < pr->batch; ++b) parts += ((host_seq_lens[b] + kBTile - 1) / kBTile + q - 1) / q;
+          for (int b = 0; b < pr->batch; ++b) parts += (tiles_of(host_seq_lens[b]) + q - 1) / q;
         else
           parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
         return parts * sh.readers;
@@ -1484,26 +1618,24 @@ extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale
   plan->batch = pr->batch;
   plan->tokens_per_seq = pr->tokens_per_seq;
   plan->kv_dtype = pr->kv_dtype;
-  plan->flags = flags | mode;
+  plan->flags = flags | mode | (window != nullptr ? MFA_PLAN_WINDOW : 0);
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
   plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->batch, pr->head_dim);
   return MFA_OK;
 }
 
-extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_problem* pr, int32_t scale_tokens,
-                                           const void* q, const void* k_cache, const void* v_cache,
-                                           const float* k_scale, const float* v_scale, const int32_t* block_table,
-                                           const int32_t* seq_lens, void* out, float* lse, void* workspace,
-                                           uint64_t workspace_bytes, void* stream_ptr) {
-  const mfa_status st = check_block_problem(pr, scale_tokens);
-  if (st != MFA_OK) return st;
+static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t scale_tokens, const mfa_window* window,
+                            const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                            void* workspace, uint64_t workspace_bytes, void* stream_ptr) {
   if (plan == nullptr) return MFA_ERR_INVALID_ARG;
   const BlockShape sh = block_shape(pr);
   const long long units = static_cast<long long>(pr->batch) * sh.readers;
   const bool clusters = (plan->flags & MFA_PLAN_UNIT_CLUSTERS) != 0;
   if (plan->batch != pr->batch || plan->kv_dtype != pr->kv_dtype || plan->tokens_per_seq != pr->tokens_per_seq ||
-      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) != 0 ||
+      plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) !=
+                                (window != nullptr ? MFA_PLAN_WINDOW : 0) ||
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && (clusters || plan->max_tiles_per_cta < 1)) ||
       (clusters && (units == 0 || plan->num_ctas % units != 0 || plan->num_ctas / units > 8)) ||
       plan->num_partials != units + plan->num_ctas - 1 ||
@@ -1564,13 +1696,15 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
   p.log_scale = scale_tokens == 64 ? 6 : scale_tokens == 32 ? 5 : 4;
   p.max_pages = pr->max_pages_per_seq;
   p.num_blocks = pr->num_blocks;
+  p.window = window != nullptr ? window->tokens : 0;
+  p.sinks = window != nullptr ? window->sinks : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(pr->softmax_scale) * 1.4426950408889634);
   p.out_f32 = pr->out_dtype == MFA_OUT_FP32 ? 1 : 0;
   p.early_metadata = (plan->flags & MFA_PLAN_EARLY_METADATA) ? 1 : 0;
   const bool check = (plan->flags & MFA_PLAN_CHECK) != 0;
   cudaError_t e = cudaSuccess;
   if (check && (e = cudaMemsetAsync(workspace, 0, 4, stream)) != cudaSuccess) return cuda_fail(e, "memset");
-  const int inst = block_instance(pr, sh);
+  const int inst = block_instance(pr, sh, window != nullptr);
   const mfa_status sst = ensure_block_smem(inst);
   if (sst != MFA_OK) return sst;
   cudaLaunchConfig_t cfg = {};
@@ -1625,4 +1759,46 @@ extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_probl
     if (word != 0) return MFA_ERR_DEVICE_CHECK;
   }
   return MFA_OK;
+}
+
+}  // namespace mfa
+
+using namespace mfa;
+
+extern "C" mfa_status mfa_block_decode_plan(const mfa_problem* pr, int32_t scale_tokens, const int32_t* host_seq_lens,
+                                            int32_t max_seq_len, int32_t num_sms, int32_t force_ctas, uint32_t flags,
+                                            mfa_plan* plan) {
+  const mfa_status st = check_block_problem(pr, scale_tokens);
+  return st != MFA_OK ? st : block_plan(pr, nullptr, host_seq_lens, max_seq_len, num_sms, force_ctas, flags, plan);
+}
+
+extern "C" mfa_status mfa_block_decode_run(const mfa_plan* plan, const mfa_problem* pr, int32_t scale_tokens,
+                                           const void* q, const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                           const int32_t* seq_lens, void* out, float* lse, void* workspace,
+                                           uint64_t workspace_bytes, void* stream) {
+  const mfa_status st = check_block_problem(pr, scale_tokens);
+  return st != MFA_OK ? st : block_run(plan, pr, scale_tokens, nullptr, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                       seq_lens, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" mfa_status mfa_window_decode_plan(const mfa_problem* pr, int32_t scale_tokens, const mfa_window* window,
+                                             const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
+                                             int32_t force_ctas, uint32_t flags, mfa_plan* plan) {
+  mfa_window cut;
+  mfa_status st = check_block_problem(pr, scale_tokens);
+  if (st == MFA_OK) st = check_window(pr, window, &cut);
+  return st != MFA_OK ? st : block_plan(pr, &cut, host_seq_lens, max_seq_len, num_sms, force_ctas, flags, plan);
+}
+
+extern "C" mfa_status mfa_window_decode_run(const mfa_plan* plan, const mfa_problem* pr, int32_t scale_tokens,
+                                            const mfa_window* window, const void* q, const void* k_cache,
+                                            const void* v_cache, const float* k_scale, const float* v_scale,
+                                            const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                                            void* workspace, uint64_t workspace_bytes, void* stream) {
+  mfa_window cut;
+  mfa_status st = check_block_problem(pr, scale_tokens);
+  if (st == MFA_OK) st = check_window(pr, window, &cut);
+  return st != MFA_OK ? st : block_run(plan, pr, scale_tokens, &cut, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                       seq_lens, out, lse, workspace, workspace_bytes, stream);
 }

@@ -98,6 +98,8 @@ typedef enum mfa_out_dtype {
 /* Set by mfa_block_decode_plan alone, in the plan: its way of splitting the work (see there). */
 #define MFA_PLAN_EVEN_SPLIT    0x100u
 #define MFA_PLAN_UNIT_CLUSTERS 0x200u
+/* Set by mfa_window_decode_plan alone, in the plan: a plan of a windowed decode. */
+#define MFA_PLAN_WINDOW        0x400u
 
 typedef struct mfa_problem {
     int32_t batch;             /* B >= 0 sequences, one new query token each */
@@ -482,6 +484,34 @@ mfa_status mfa_block_kv_append(const mfa_problem* problem, int32_t scale_tokens,
                                const int32_t* positions, const int32_t* block_table,
                                void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                                uint32_t* device_status, void* stream);
+
+/*
+ * A sliding window with first tokens that stay visible: new token i of sequence b, at position
+ * p = L_b - T + i, sees the cached tokens t <= p with t > p - tokens or t < sinks.
+ */
+typedef struct mfa_window {
+    int32_t tokens;            /* >= 1: the new token itself and the tokens - 1 before it */
+    int32_t sinks;             /* >= 0: the sequence's first tokens that stay visible */
+} mfa_window;
+
+/*
+ * mfa_block_decode_plan and mfa_block_decode_run with a window.  Only the pages that hold a token
+ * which a new token of the sequence sees are read, and only their table entries (those of other
+ * pages may hold anything): about tokens + sinks tokens a sequence, however long it is, which is
+ * also what the plan splits.  Otherwise everything there holds; a plan is for the calls with the
+ * window it was made for, and runs any lengths up to the table's.
+ * Tokens that no new token sees may hold any bits.  With T > 1, a NaN among the values of a token
+ * that some of a sequence's new tokens see may reach the rows of the others, in its head and element.
+ */
+mfa_status mfa_window_decode_plan(const mfa_problem* problem, int32_t scale_tokens, const mfa_window* window,
+                                  const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
+                                  int32_t force_ctas, uint32_t flags, mfa_plan* plan);
+mfa_status mfa_window_decode_run(const mfa_plan* plan, const mfa_problem* problem, int32_t scale_tokens,
+                                 const mfa_window* window, const void* q, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens,
+                                 void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                                 void* stream);
 
 /*
  * ------------------------------------------------------------------ rotary positions
