@@ -197,6 +197,7 @@ struct BlockDecodeParams {
 // those rows of the values.
 struct BlockView {
   int L, skip, low, sink_pages;
+  int plain;   // from this page on only the end of L cuts a page's rows
 };
 __host__ __device__ __forceinline__ BlockView block_view(int L, int tokens, int window, int sinks) {
   BlockView v;
@@ -206,6 +207,7 @@ __host__ __device__ __forceinline__ BlockView block_view(int L, int tokens, int 
   if (v.skip < 0) v.skip = 0;
   v.L = L - kBPage * v.skip;
   v.low -= kBPage * v.skip;
+  v.plain = v.low > 0 && v.low / kBPage >= v.sink_pages ? v.low / kBPage + 1 : v.sink_pages;
   return v;
 }
 // The tokens that a sequence of L has to go over.
@@ -495,7 +497,7 @@ template <bool kWindow>
 __device__ __forceinline__ BlockRows view_rows(const BlockView& w, int sinks, int v) {
   BlockRows r = {0, min(kBPage, w.L - kBPage * v), 0};
   if constexpr (kWindow) {
-    if (w.low >= kBPage * w.sink_pages) {   // the window starts behind the sinks' pages
+    if (v < w.plain && w.low >= kBPage * w.sink_pages) {   // the window starts behind the sinks' pages
       if (v == w.sink_pages - 1) r.to = min(r.to, sinks - kBPage * v);
       if (v == w.low / kBPage) r.from = w.low % kBPage;
     }
@@ -504,15 +506,20 @@ __device__ __forceinline__ BlockRows view_rows(const BlockView& w, int sinks, in
   return r;
 }
 
-// The rows of page v's box that are loaded and that no new token sees: [x, y), box rows.
-__device__ __forceinline__ int2 view_gap(const BlockView& w, int sinks, int v) {
+// The page, of one sequence, whose box has rows that are loaded and that no new token sees: box rows
+// [from, to) of page v; v < 0 where there is none.
+struct BlockGap {
+  int v, from, to;
+};
+__device__ __forceinline__ BlockGap view_gap(const BlockView& w, int sinks) {
+  const int v = w.low >= kBPage * w.sink_pages ? w.low / kBPage : w.sink_pages - 1;
   const BlockRows r = view_rows<true>(w, sinks, v);
   int from = 0, to = 0;
-  if (r.first < 0 && r.from > 0)
-    to = r.from;
-  else if (w.low < kBPage * w.sink_pages && v == w.sink_pages - 1)
+  if (w.low >= kBPage * w.sink_pages)
+    to = r.first < 0 ? r.from : 0;   // (the box starts at the window's first token where it can)
+  else
     from = sinks - kBPage * v, to = min(w.low - kBPage * v, r.to);
-  return make_int2(from - r.first, to - r.first);
+  return {from < to ? v : -1, from - r.first, to - r.first};
 }
 
 // A role's place in its CTA's run of tiles.
@@ -728,10 +735,13 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       for (int s = 0; s < nseg && ok; ++s) {
         const int lo = seg[s].lo, hi = seg[s].hi;
         BlockView w;
-        if constexpr (kWindow)
+        BlockGap gap = {-1, 0, 0};
+        if constexpr (kWindow) {
           w = block_view(seg[s].L, p.tokens, p.window, p.sinks);
-        else
+          gap = view_gap(w, p.sinks);
+        } else {
           w.L = seg[s].L;
+        }
         for (int j = lo; j < hi && ok; ++j, ++n) {
           ok = all(block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag));
           if (ok && j == lo && s > 0) ok = all(block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag));
@@ -741,19 +751,11 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
           for (int h = 0; h < kHalves; ++h) {
             if (ok) ok = all(block_wait(bar(kFull + kKSlots + slot), phase, abort_flag));
             if (!ok) break;
-            if constexpr (kWindow) {
-              bool any = false;
-#pragma unroll 1
-              for (int pg = 0; pg < (both ? 2 : 1); ++pg) {
-                const int2 gap = view_gap(w, p.sinks, 2 * j + pg);
-                uint8_t* box = smem + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes + pg * 8192;
-                for (int r = gap.x + (lane >> 3); r < gap.y; r += 4) *reinterpret_cast<uint4*>(box + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                any |= gap.x < gap.y;
-              }
-              if (any) {
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
+            if (kWindow && gap.v >> 1 == j) {
+              uint8_t* box = smem + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes + (gap.v & 1) * 8192;
+              for (int r = gap.from + (lane >> 3); r < gap.to; r += 4) *reinterpret_cast<uint4*>(box + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
             tc_fence_after();
             const uint64_t ad = smem_desc(sbase + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
@@ -952,10 +954,15 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
       const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(q_inv + (s & 1) * 64 + c0);
       const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(neg_ref + c0);
       for (int j = sg.lo; j < sg.hi; ++j, ++n) {
-        const BlockRows rows = view_rows<kWindow>(w, p.sinks, 2 * j + pg);
-        const int pr = ri + rows.first;                                  // page row of this lane's box row
-        int t = pr >= rows.from ? kBTile * j + kBPage * pg + pr : INT_MAX;   // and its token, if any row sees it
-        if (kWindow && (pr >= rows.to || (t < w.low && t >= p.sinks))) t = INT_MAX;
+        // every row sees the whole tile
+        const bool inside = kBTile * (j + 1) <= seen0 && (!kWindow || kBTile * j >= low0 + p.unit_tokens - 1 || kBTile * (j + 1) <= p.sinks);
+        int pr = ri, t = kBTile * j + row;   // page row of this lane's box row, and its token, if any row sees it
+        if (!kWindow || !inside) {
+          const BlockRows rows = view_rows<kWindow>(w, p.sinks, 2 * j + pg);
+          pr += rows.first;
+          t = pr >= rows.from ? kBTile * j + kBPage * pg + pr : INT_MAX;
+          if (kWindow && (pr >= rows.to || (t < w.low && t >= p.sinks))) t = INT_MAX;
+        }
         const bool held = t != INT_MAX;
         if (!block_wait(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
@@ -977,8 +984,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               x2[i + 1] = fma_f32x2(pack_f32x2(__uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])), mul_f32x2(a2, w.y), m.y);
             }
           }
-          if (kBTile * (j + 1) <= seen0 && (!kWindow || kBTile * j >= low0 + p.unit_tokens - 1 || kBTile * (j + 1) <= p.sinks)) {
-            // every row sees the whole tile
+          if (inside) {
           } else if (p.unit_tokens == 1) {
             if (!sees(t, 0)) {
 #pragma unroll
@@ -1018,7 +1024,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               y[i + 2] = fmaf(__uint_as_float(sr[i + 2]), sc.x * w.z, e);
               y[i + 3] = fmaf(__uint_as_float(sr[i + 3]), sc.x * w.w, e);
             }
-            if (kWindow || kBTile * (j + 1) > seen0) {
+            if (!inside) {
 #pragma unroll
               for (int i = 0; i < kC; ++i) y[i] = sees(t, row_tok[c0 + i]) ? y[i] : -INFINITY;
             }
