@@ -52,6 +52,7 @@ MFA_ROPE_ADJACENT = 1
 MFA_ROPE_MAX_AXES = 4
 MFA_ROPE_INTERLEAVED = 0x1
 MFA_ROPE_OWN_SPECTRUM = 0x2
+MFA_NORM_ROPE_GRAD_PARTS = 512
 
 NUM_Q_HEADS = 64
 HEAD_DIM = 256
@@ -62,7 +63,8 @@ EXPORTED_SYMBOLS = ("mfa_decode_plan", "mfa_decode_run", "mfa_combine", "mfa_rea
                     "mfa_status_string", "mfa_abi_version", "mfa_last_cuda_error",
                     "mfa_decode_run_static_workspace", "mfa_kv_append", "mfa_decode_run_host",
                     "mfa_decode_append_run", "mfa_block_decode_plan", "mfa_block_decode_run", "mfa_block_kv_append",
-                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_rope_table", "mfa_rope_run")
+                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_rope_table", "mfa_rope_run",
+                    "mfa_norm_rope_run", "mfa_norm_rope_grad_run")
 
 # Size of the library's own scratch array used by mfa_decode_run_static_workspace.
 MFA_STATIC_WORKSPACE_BYTES = 24 * 1024 * 1024
@@ -103,6 +105,16 @@ class MfaRopePair(ctypes.Structure):
 class MfaRopeRows(ctypes.Structure):
     _fields_ = [("data_in", ctypes.c_void_p), ("data_out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
                 ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class MfaNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class MfaNormGradRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64), ("heads", ctypes.c_int32)]
 
 
 class MfaError(RuntimeError):
@@ -175,6 +187,13 @@ def load_library(path: str = LIB_PATH):
     lib.mfa_rope_run.argtypes = [ctypes.POINTER(MfaRopeConfig), P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                  ctypes.POINTER(MfaRopeRows), ctypes.POINTER(MfaRopeRows), P]
     lib.mfa_rope_run.restype = ctypes.c_int
+    lib.mfa_norm_rope_run.argtypes = [ctypes.POINTER(MfaRopeConfig), P, P, ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.POINTER(MfaNorm), ctypes.POINTER(MfaRopeRows), ctypes.POINTER(MfaRopeRows), P]
+    lib.mfa_norm_rope_run.restype = ctypes.c_int
+    lib.mfa_norm_rope_grad_run.argtypes = [ctypes.POINTER(MfaRopeConfig), P, P, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.POINTER(MfaNorm), ctypes.POINTER(MfaNormGradRows),
+                                           ctypes.POINTER(MfaNormGradRows), P, P, P, ctypes.c_uint64, P]
+    lib.mfa_norm_rope_grad_run.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -429,6 +448,30 @@ def mfa_rope_run(config: MfaRopeConfig, table, positions, num_rows: int, dtype: 
                           None if q is None else ctypes.byref(q), None if k is None else ctypes.byref(k),
                           _stream(stream))
     _check(st, "mfa_rope_run")
+
+
+def mfa_norm_rope_run(config: MfaRopeConfig, table, positions, num_rows: int, dtype: int, norm: MfaNorm,
+                      q: Optional[MfaRopeRows], k: Optional[MfaRopeRows], stream=None) -> None:
+    """Norm each head's rows, weigh and turn them (see include/mfa.h)."""
+    lib = load_library()
+    st = lib.mfa_norm_rope_run(ctypes.byref(config), _ptr(table), _ptr(positions), num_rows, dtype, ctypes.byref(norm),
+                               None if q is None else ctypes.byref(q), None if k is None else ctypes.byref(k),
+                               _stream(stream))
+    _check(st, "mfa_norm_rope_run")
+
+
+def mfa_norm_rope_grad_run(config: MfaRopeConfig, table, positions, num_rows: int, dtype: int, norm: MfaNorm,
+                           q: Optional[MfaNormGradRows], k: Optional[MfaNormGradRows], q_weight_grad, k_weight_grad,
+                           workspace, stream=None, workspace_bytes: Optional[int] = None) -> None:
+    """The gradient of mfa_norm_rope_run (see include/mfa.h)."""
+    lib = load_library()
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else _nbytes(workspace)
+    st = lib.mfa_norm_rope_grad_run(ctypes.byref(config), _ptr(table), _ptr(positions), num_rows, dtype, ctypes.byref(norm),
+                                    None if q is None else ctypes.byref(q), None if k is None else ctypes.byref(k),
+                                    _ptr(q_weight_grad), _ptr(k_weight_grad), _ptr(workspace), int(workspace_bytes),
+                                    _stream(stream))
+    _check(st, "mfa_norm_rope_grad_run")
 
 
 def mfa_read_device_status(workspace, clear: bool = True, stream=None) -> int:
@@ -753,6 +796,15 @@ class Rope(_OnDevice):
         self._config_ref = ctypes.byref(self.config)
         self._dtypes = {torch.bfloat16: MFA_OUT_BF16, torch.float32: MFA_OUT_FP32}
 
+    def _row_stride(self, t, name: str, line: int) -> int:
+        """Elements from one row of t to the next; a row's heads lie side by side, `line` elements of them."""
+        if t.is_contiguous():
+            return line
+        a, b, c = t.stride()
+        if c != 1 or (t.shape[1] > 1 and b != self.head_dim):
+            raise ValueError(f"{name}: each row's heads must lie side by side, got strides {t.stride()}")
+        return a if t.shape[0] > 1 else line   # (a single row has no stride of its own)
+
     def _rows(self, x, out, name: str, rows: int, dtype) -> MfaRopeRows:
         """x and its output (x's shape; None: a new tensor) as the library takes them, and the output."""
         shape, d = x.shape, self.head_dim
@@ -760,21 +812,13 @@ class Rope(_OnDevice):
             raise ValueError(f"{name}: expected {dtype} [{rows}, heads, {d}] on {self.device}, got {x.dtype} "
                              f"{tuple(shape)} on {x.device}")
         line = shape[1] * d
-        strides = []
         if out is None:
             out = self._torch.empty(shape, dtype=dtype, device=self.device)
         elif out is not x and (out.shape != shape or out.dtype is not dtype or out.get_device() != self._index):
             raise ValueError(f"{name}_out: expected {dtype} {tuple(shape)} on {self.device}, got {out.dtype} "
                              f"{tuple(out.shape)} on {out.device}")
-        for t in (x, out):
-            if t.is_contiguous():
-                strides.append(line)
-                continue
-            a, b, c = t.stride()
-            if c != 1 or (shape[1] > 1 and b != d):
-                raise ValueError(f"{name}: each row's heads must lie side by side, got strides {t.stride()}")
-            strides.append(a if rows > 1 else line)   # (a single row has no stride of its own)
-        return MfaRopeRows(x.data_ptr(), out.data_ptr(), *strides, shape[1]), out
+        return MfaRopeRows(x.data_ptr(), out.data_ptr(), self._row_stride(x, name, line), self._row_stride(out, name, line),
+                           shape[1]), out
 
     def __call__(self, q, k, positions, inverse: bool = False, q_out=None, k_out=None, stream=None):
         """Turned rows (q_out, k_out) of q and k, [rows, heads, head_dim] in bf16 or fp32 (either may be None; rows
@@ -798,3 +842,90 @@ class Rope(_OnDevice):
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, 1 if inverse else 0,
                     rq, rk), stream, (self.table,), (q, k, positions, q_out, k_out))
         return q_out, k_out
+
+
+class NormRope(Rope):
+    """Norms of query and key heads with their rotary positions in one pass, and the gradient.
+
+    y = turn(x (mean x^2 + eps)^(-1/2) w) for each head x, with one weight for each element of a query
+    head and one for each of a key head.  The other arguments are those of Rope.
+    """
+
+    def __init__(self, head_dim: int, sections: Sequence[int], eps: float = 1e-6, theta: float = 1e4, pairing: str = "half",
+                 interleaved: bool = False, own_spectrum: bool = False, position_scale: float = 1.0, device=None):
+        super().__init__(head_dim, sections, theta, pairing, interleaved, own_spectrum, position_scale, device)
+        self.eps = float(eps)
+        self._weight_shape = self._torch.Size((self.head_dim,))
+
+    def _start(self, q, k, q_weight, k_weight, positions):
+        """(rows, row type, its code, MfaNorm) of a call's arguments."""
+        some = k if q is None else q
+        if some is None:
+            raise ValueError("expected q or k")
+        rows, dtype = some.shape[0], some.dtype
+        kind = self._dtypes.get(dtype)
+        if kind is None:
+            raise ValueError(f"expected bf16 or fp32 rows, got {dtype}")
+        if not _fits(positions, self._torch.int32, (self.axes, rows), self._index):
+            _refuse(self._index, ("positions", positions, self._torch.int32, (self.axes, rows)))
+        weight_type = None
+        for name, x, w in (("q_weight", q, q_weight), ("k_weight", k, k_weight)):
+            if x is None:
+                continue
+            if w is None:
+                raise ValueError(f"{name}: expected a weight for each element of a head")
+            weight_type = weight_type or w.dtype
+            if weight_type not in self._dtypes or not _fits(w, weight_type, self._weight_shape, self._index):
+                raise ValueError(f"{name}: expected contiguous bf16 or fp32 weights (of one type) of shape "
+                                 f"({self.head_dim},) on {self.device}, got {w.dtype} {tuple(w.shape)} on {w.device}")
+        norm = MfaNorm(None if q is None else q_weight.data_ptr(), None if k is None else k_weight.data_ptr(),
+                       self._dtypes[weight_type], self.eps)
+        return rows, dtype, kind, norm
+
+    def __call__(self, q, k, q_weight, k_weight, positions, q_out=None, k_out=None, stream=None):
+        """Normed, weighed and turned rows (q_out, k_out) of q and k, [rows, heads, head_dim] in bf16 or fp32 (either
+        may be None; rows may be strided, as columns of one projection); weights [head_dim] in bf16 or fp32;
+        positions int32 [axes, rows].  Pass q_out = q and k_out = k to do it in place."""
+        rows, dtype, kind, norm = self._start(q, k, q_weight, k_weight, positions)
+        rq = rk = None
+        if q is not None:
+            rq, q_out = self._rows(q, q_out, "q", rows, dtype)
+        if k is not None:
+            rk, k_out = self._rows(k, k_out, "k", rows, dtype)
+        self._call(self._lib.mfa_norm_rope_run, "mfa_norm_rope_run",
+                   (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, norm, rq, rk), stream,
+                   (self.table,), (q, k, q_weight, k_weight, positions, q_out, k_out))
+        return q_out, k_out
+
+    def _grad_rows(self, x, dy, dx, name: str, rows: int, dtype):
+        """x, dy and dx (x's shape; None: a new tensor) as the library takes them, and dx."""
+        if dy is None:
+            raise ValueError(f"d{name}: expected the gradient of {name}'s output")
+        if dy.shape != x.shape or dy.dtype is not dtype or dy.get_device() != self._index:
+            raise ValueError(f"d{name}: expected {dtype} {tuple(x.shape)} on {self.device}, got {dy.dtype} {tuple(dy.shape)} "
+                             f"on {dy.device}")
+        r, dx = self._rows(x, dx, name, rows, dtype)
+        line = x.shape[1] * self.head_dim
+        return MfaNormGradRows(r.data_in, dy.data_ptr(), r.data_out, r.in_stride, self._row_stride(dy, "d" + name, line),
+                               r.out_stride, r.heads), dx
+
+    def grad(self, dq, dk, q, k, q_weight, k_weight, positions, q_grad=None, k_grad=None, stream=None):
+        """The gradient of a call: (q_grad, k_grad, q_weight_grad, k_weight_grad) from dq and dk, the gradients of
+        its q_out and k_out, and the call's own arguments.  The weights' gradients are fp32; q_grad and k_grad may be
+        given (dq and dk, or q and k, themselves too)."""
+        torch = self._torch
+        rows, dtype, kind, norm = self._start(q, k, q_weight, k_weight, positions)
+        rq = rk = wq = wk = None
+        if q is not None:
+            rq, q_grad = self._grad_rows(q, dq, q_grad, "q", rows, dtype)
+            wq = torch.empty(self._weight_shape, dtype=torch.float32, device=self.device)
+        if k is not None:
+            rk, k_grad = self._grad_rows(k, dk, k_grad, "k", rows, dtype)
+            wk = torch.empty(self._weight_shape, dtype=torch.float32, device=self.device)
+        size = 8 * self.head_dim * min(rows, MFA_NORM_ROPE_GRAD_PARTS)
+        scratch = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self._call(self._lib.mfa_norm_rope_grad_run, "mfa_norm_rope_grad_run",
+                   (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, norm, rq, rk,
+                    None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), scratch.data_ptr(), size),
+                   stream, (self.table,), (dq, dk, q, k, q_weight, k_weight, positions, q_grad, k_grad, wq, wk, scratch))
+        return q_grad, k_grad, wq, wk

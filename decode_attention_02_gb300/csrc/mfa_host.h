@@ -28,6 +28,13 @@ int problem_shape(const mfa_problem* pr);
 // Shape, dtype and range checks of a problem over a block-scaled cache (MFA_OK, or the error).
 mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens);
 
+// Shape and range checks of a rope's description (MFA_OK, or the error).
+mfa_status check_rope(const mfa_rope_config* c);
+
+// Whether two sets of rows share memory: `rows` rows of `len` elements of esz bytes each, `stride` apart.
+bool rows_share(const void* a, int64_t a_stride, int64_t a_len, const void* b, int64_t b_stride, int64_t b_len, int rows,
+                int esz);
+
 // True when p is a multiple of a bytes.
 bool aligned(const void* p, uintptr_t a);
 

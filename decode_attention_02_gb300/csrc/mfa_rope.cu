@@ -30,11 +30,11 @@
 
 #include "mfa.h"
 #include "mfa_host.h"
+#include "mfa_rope.cuh"
 #include "ptx.cuh"
 
 namespace mfa {
 
-constexpr int kRopeMaxDim = 512;
 // heads a thread turns, all loaded before the first is used
 template <typename T>
 constexpr int kRopeHeads = sizeof(T) == 2 ? 4 : 2;
@@ -54,54 +54,6 @@ struct RopeParams {
   int rows, axes, pairs, head_dim;
   int turned_units, units;   // a head's units: turned ones first, then (out of place) copied ones
   int inverse;
-};
-
-// kVec elements as they lie in memory (widened when they are used: a thread holds its heads'
-// loads in half the registers)
-template <typename T, int kVec>
-struct RopeVec {
-  static constexpr int kWords = kVec == 8 ? kVec * sizeof(T) / 4 : kVec;
-  uint32_t w[kWords];   // kVec = 1: one element in the low bits
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kVec == 8) {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
-        w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
-      }
-    } else if constexpr (sizeof(T) == 2) {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
-  }
-  __device__ __forceinline__ void store_raw(T* p) const {
-    if constexpr (kVec == 8) {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4)
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    } else if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
-    } else {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
-    }
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (sizeof(T) == 4)
-      return __uint_as_float(w[i]);
-    else
-      return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-  }
-  // the pair of values i, i + 1 (kVec = 1: lo alone)
-  __device__ __forceinline__ void set(int i, float lo, float hi) {
-    if constexpr (sizeof(T) == 4) {
-      w[i] = __float_as_uint(lo);
-      if constexpr (kVec > 1) w[i + 1] = __float_as_uint(hi);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-      w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
 };
 
 // kVec = 8: a unit is 8 elements of the first half and the 8 of the second that pair with them
@@ -147,14 +99,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads) mfa_rope_kernel(const __grid_
     for (int x = 0; x < MFA_ROPE_MAX_AXES; ++x)
       pos[x] = x < p.axes ? p.positions[static_cast<long long>(x) * p.rows + row] : 0;
     for (int i = threadIdx.y * blockDim.x + u; i < p.pairs; i += blockDim.x * blockDim.y) {
-      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(p.table + i);
-      const int axis = static_cast<int>(e.y & 3u);
-      const int32_t at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-      const uint64_t turn = e.x * static_cast<uint64_t>(static_cast<int64_t>(at));
-      // the top 32 bits as a signed fraction in [-1/2, 1/2) turns; 2^-31 of it is half turns
-      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
       float s, c;
-      sincospif(half_turns, &s, &c);
+      rope_angle(p.table, i, pos, s, c);
       cs[0][i] = c;
       cs[1][i] = p.inverse ? -s : s;
     }
@@ -203,7 +149,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads) mfa_rope_kernel(const __grid_
   }
 }
 
-static mfa_status check_rope(const mfa_rope_config* c) {
+mfa_status check_rope(const mfa_rope_config* c) {
   if (c == nullptr) return MFA_ERR_INVALID_ARG;
   if (c->head_dim < 1 || c->rotary_dim < 2 || (c->rotary_dim & 1) || c->rotary_dim > c->head_dim)
     return MFA_ERR_INVALID_ARG;
@@ -226,8 +172,8 @@ static mfa_status check_rope(const mfa_rope_config* c) {
 // Whether two sets of rows share memory: `rows` rows of `len` elements each, `stride` apart.  Ranges that
 // overlap are apart as columns of one wider row (q and k of one projection): equal strides, and the two
 // column ranges apart.  (Different strides count as sharing.)
-static bool share(const void* a, int64_t a_stride, int64_t a_len, const void* b, int64_t b_stride, int64_t b_len, int rows,
-                  int esz) {
+bool rows_share(const void* a, int64_t a_stride, int64_t a_len, const void* b, int64_t b_stride, int64_t b_len, int rows,
+                int esz) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   const uintptr_t a1 = a0 + ((rows - 1) * a_stride + a_len) * esz, b1 = b0 + ((rows - 1) * b_stride + b_len) * esz;
   if (a0 >= b1 || b0 >= a1) return false;
@@ -248,7 +194,7 @@ static mfa_status check_side(const mfa_rope_rows* s, const mfa_rope_config* c, i
     return MFA_ERR_INVALID_ARG;
   // in place means the same rows; anything between would be read after it is written
   if (s->in == s->out) return s->in_stride == s->out_stride ? MFA_OK : MFA_ERR_INVALID_ARG;
-  return share(s->in, s->in_stride, least, s->out, s->out_stride, least, rows, esz) ? MFA_ERR_INVALID_ARG : MFA_OK;
+  return rows_share(s->in, s->in_stride, least, s->out, s->out_stride, least, rows, esz) ? MFA_ERR_INVALID_ARG : MFA_OK;
 }
 
 // The wide path needs 16-byte aligned vectors of 8 elements everywhere.
@@ -364,9 +310,9 @@ extern "C" mfa_status mfa_rope_run(const mfa_rope_config* c, const mfa_rope_pair
   if (num_rows == 0 || heads == 0) return MFA_OK;
   if (p.q.heads > 0 && p.k.heads > 0) {   // what one side writes is neither read nor written by the other
     const int64_t nq = static_cast<int64_t>(p.q.heads) * c->head_dim, nk = static_cast<int64_t>(p.k.heads) * c->head_dim;
-    if (share(p.q.out, p.q.out_stride, nq, p.k.in, p.k.in_stride, nk, num_rows, esz) ||
-        share(p.q.out, p.q.out_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz) ||
-        share(p.q.in, p.q.in_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz))
+    if (rows_share(p.q.out, p.q.out_stride, nq, p.k.in, p.k.in_stride, nk, num_rows, esz) ||
+        rows_share(p.q.out, p.q.out_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz) ||
+        rows_share(p.q.in, p.q.in_stride, nq, p.k.out, p.k.out_stride, nk, num_rows, esz))
       return MFA_ERR_INVALID_ARG;
   }
   if (table == nullptr || positions == nullptr || !aligned(table, 16) || !aligned(positions, 4)) return MFA_ERR_INVALID_ARG;

@@ -588,6 +588,62 @@ mfa_status mfa_rope_run(const mfa_rope_config* config, const mfa_rope_pair* tabl
                         const int32_t* positions, int32_t num_rows, int32_t dtype, int32_t inverse,
                         const mfa_rope_rows* q, const mfa_rope_rows* k, void* stream);
 
+/*
+ * ------------------------------------------------------------------ normed rotary rows
+ *
+ * Each head of the queries and of the new keys divided by its root mean square, times a weight for
+ * each element (one set for all query heads, one for all key heads), and turned by its row's positions,
+ * in one pass: for a head x of head_dim elements,
+ *     r = (sum x^2 / head_dim + eps)^(-1/2),   y = turn(x r w),
+ * the sum over the whole head, elements past rotary_dim too.  fp32 arithmetic, one rounding.  A head whose
+ * sum of squares leaves fp32's range, or that holds an infinity or NaN, gives unspecified results of its own.
+ */
+typedef struct mfa_norm {
+    const void* q_weight;      /* device [head_dim], aligned to the element; NULL without query heads */
+    const void* k_weight;      /* the same for the keys */
+    int32_t weight_dtype;      /* MFA_OUT_BF16 or MFA_OUT_FP32, of both */
+    float eps;                 /* finite, > 0 */
+} mfa_norm;
+
+/*
+ * Enqueue the norm and rotation of num_rows rows of q and of k (one launch).  Arguments and conditions as
+ * for mfa_rope_run (in place too); the wide path takes heads of up to 32 units as well: a unit is 16
+ * elements of whole pairs under half pairing, else 8 elements.
+ */
+mfa_status mfa_norm_rope_run(const mfa_rope_config* config, const mfa_rope_pair* table, const int32_t* positions,
+                             int32_t num_rows, int32_t dtype, const mfa_norm* norm, const mfa_rope_rows* q,
+                             const mfa_rope_rows* k, void* stream);
+
+/* The rows of the gradient: as mfa_rope_rows, for three sets of rows. */
+typedef struct mfa_norm_grad_rows {
+    const void* x;             /* what the forward call read */
+    const void* dy;            /* the gradient of what it wrote */
+    void* dx;                  /* = x or = dy (with that one's stride), or no overlap with either */
+    int64_t x_stride, dy_stride, dx_stride;
+    int32_t heads;
+} mfa_norm_grad_rows;
+
+/* Bytes of workspace of mfa_norm_rope_grad_run. */
+#define MFA_NORM_ROPE_GRAD_PARTS 512
+#define MFA_NORM_ROPE_GRAD_BYTES(num_rows, head_dim)                                                        \
+    (8ull * (uint64_t)(head_dim) *                                                                          \
+     (uint64_t)((num_rows) < MFA_NORM_ROPE_GRAD_PARTS ? (num_rows) : MFA_NORM_ROPE_GRAD_PARTS))
+
+/*
+ * Enqueue the gradient of mfa_norm_rope_run (two launches): with g = dy turned back and h = x r,
+ *     dx = r (g w - h sum(g w h) / head_dim),   dw = sum over the rows and a side's heads of g h.
+ *   config .. norm : as given to the forward call, whose r is computed again from x.
+ *   q_weight_grad, k_weight_grad : device fp32 [head_dim], written (zeros without rows or heads), or
+ *               NULL.  Summed in fp32 in an order that depends on the sizes and the device alone: the same call
+ *               gives the same bits.
+ *   workspace : device, 16-byte aligned, >= MFA_NORM_ROPE_GRAD_BYTES(num_rows, head_dim) bytes; scratch.
+ *               Two calls that may overlap on the GPU need one each.
+ */
+mfa_status mfa_norm_rope_grad_run(const mfa_rope_config* config, const mfa_rope_pair* table,
+                                  const int32_t* positions, int32_t num_rows, int32_t dtype, const mfa_norm* norm,
+                                  const mfa_norm_grad_rows* q, const mfa_norm_grad_rows* k, float* q_weight_grad,
+                                  float* k_weight_grad, void* workspace, uint64_t workspace_bytes, void* stream);
+
 /* MFA_ABI_VERSION of the loaded library. */
 int32_t mfa_abi_version(void);
 
