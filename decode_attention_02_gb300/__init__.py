@@ -922,7 +922,7 @@ class NormRope(Rope):
         if k is not None:
             rk, k_grad = self._grad_rows(k, dk, k_grad, "k", rows, dtype)
             wk = torch.empty(self._weight_shape, dtype=torch.float32, device=self.device)
-        size = 8 * self.head_dim * min(rows, MFA_NORM_ROPE_GRAD_PARTS)
+        size = 8 * self.head_dim * MFA_NORM_ROPE_GRAD_PARTS
         scratch = torch.empty(size, dtype=torch.uint8, device=self.device)
         self._call(self._lib.mfa_norm_rope_grad_run, "mfa_norm_rope_grad_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, norm, rq, rk,

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -28,7 +29,7 @@
 
 namespace mfa {
 
-constexpr int kNormThreads = 512;        // of a CTA, at most
+constexpr int kNormThreads = 288;        // of a CTA that have heads, at most; with a warp of angles two CTAs on an SM
 constexpr int kNormAnyThreads = 256;     // of a CTA of the path for any shape
 constexpr int kNormAnyEach = kRopeMaxDim / 32;   // its elements a lane
 
@@ -73,24 +74,27 @@ __device__ __forceinline__ float norm_weight(const NormParams& p, const NormSide
   return p.w_f32 ? norm_load<float>(s.w, i) : norm_load<__nv_bfloat16>(s.w, i);
 }
 
-// Angles of row `row`, one pair a thread, into cs.
-__device__ __forceinline__ void row_angles(const NormParams& p, long long row, int tid, int threads, float (&cs)[2][kRopeMaxDim / 2]) {
+// Angles of row `row`, one pair a thread, into cs, pair i at place(i).
+template <typename Place>
+__device__ __forceinline__ void row_angles(const NormParams& p, long long row, int tid, int threads, float (&cs)[2][kRopeMaxDim / 2],
+                                           Place place) {
   int32_t pos[MFA_ROPE_MAX_AXES];
 #pragma unroll
   for (int x = 0; x < MFA_ROPE_MAX_AXES; ++x) pos[x] = x < p.axes ? p.positions[static_cast<long long>(x) * p.rows + row] : 0;
   for (int i = tid; i < p.pairs; i += threads) {
     float s, c;
     rope_angle(p.table, i, pos, s, c);
-    cs[0][i] = c;
-    cs[1][i] = s;
+    cs[0][place(i)] = c;
+    cs[1][place(i)] = s;
   }
 }
 
 // Sums of N values over a head's group of 2^log_lanes lanes.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], unsigned mask, int lanes) {
-#pragma unroll 1
-  for (int o = lanes / 2; o > 0; o /= 2) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    if (o >= lanes) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(mask, v[i], o);
   }
@@ -108,243 +112,318 @@ struct NormPlace {
     active = u < p.units;
     turned = u < p.turned_units;
     on_q = slot < p.q.slots;
-    h0 = on_q ? slot : slot - p.q.slots;
-    step = on_q ? p.q.slots : p.k.slots;
+    active = active && slot < p.q.slots + p.k.slots;
+    const int slots = on_q ? p.q.slots : p.k.slots;
+    h0 = (on_q ? slot : slot - p.q.slots) + blockIdx.y * slots;
+    step = slots * gridDim.y;
     mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & ~(lanes - 1));
     a0 = turned ? 8 * u : 2 * p.pairs + 8 * (u - p.turned_units);
     b0 = kHalf && turned ? a0 + p.pairs : a0;
   }
 };
 
-// ------------------------------------------------------------------ forward
-template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kNormThreads) mfa_norm_rope_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kN = sizeof(T) == 2 ? 4 : 2;   // heads a thread has at a time
-  constexpr int kPairs = kHalf ? 8 : 4;
-  __shared__ __align__(16) float cs[2][kRopeMaxDim / 2];
-  grid_dep_wait();
-  grid_dep_launch();
-  const NormPlace<kHalf> at(p);
-  const NormSide& side = at.on_q ? p.q : p.k;
-  const long long row = blockIdx.x;
-  const T* src = static_cast<const T*>(side.x) + row * side.x_stride;
-  T* dst = static_cast<T*>(side.out) + row * side.out_stride;
-  RopeVec<T, 8> a[kN], b[kN];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int hi = h + i * at.step;
-      if (hi < side.heads && at.active) {
-        a[i].load(src + static_cast<long long>(hi) * p.head_dim + at.a0);
-        if (kHalf && at.turned) b[i].load(src + static_cast<long long>(hi) * p.head_dim + at.b0);
-      }
-    }
-  };
-  load(at.h0);
-  // weights times cosines and sines: y = r (a ac - b bs), r (b bc + a as)
-  float ac[kPairs], as[kPairs], bc[kPairs], bs[kPairs];
-  if (at.active) {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      ac[i] = norm_weight(p, side, at.a0 + (kHalf ? i : 2 * i));
-      bc[i] = norm_weight(p, side, kHalf ? at.b0 + i : at.a0 + 2 * i + 1);
-    }
-  }
-  row_angles(p, row, threadIdx.x, blockDim.x, cs);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const float c = at.turned ? cs[0][kPairs * at.u + i] : 1.f, s = at.turned ? cs[1][kPairs * at.u + i] : 0.f;
-    as[i] = ac[i] * s;
-    ac[i] *= c;
-    bs[i] = bc[i] * s;
-    bc[i] *= c;
-  }
-#pragma unroll 1
-  for (int h = at.h0; h < side.heads; h += kN * at.step) {
-    if (h != at.h0) load(h);
-    float sum[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      sum[i] = 0.f;
-      if (h + i * at.step < side.heads && at.active) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[i] = fmaf(a[i].get(j), a[i].get(j), sum[i]);
-        if (kHalf && at.turned) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum[i] = fmaf(b[i].get(j), b[i].get(j), sum[i]);
-        }
-      }
-    }
-    group_sum<kN>(sum, at.mask, 1 << p.log_lanes);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int hi = h + i * at.step;
-      if (hi >= side.heads || !at.active) continue;
-      const float r = rsqrtf(fmaf(sum[i], p.inv_dim, p.eps));
-      T* to = dst + static_cast<long long>(hi) * p.head_dim;
-      RopeVec<T, 8> y, z;
-      if constexpr (kHalf) {
-        if (at.turned) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float a0 = a[i].get(j), b0 = b[i].get(j), a1 = a[i].get(j + 1), b1 = b[i].get(j + 1);
-            y.set(j, r * (a0 * ac[j] - b0 * bs[j]), r * (a1 * ac[j + 1] - b1 * bs[j + 1]));
-            z.set(j, r * (b0 * bc[j] + a0 * as[j]), r * (b1 * bc[j + 1] + a1 * as[j + 1]));
-          }
-          z.store_raw(to + at.b0);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) y.set(j, r * (a[i].get(j) * ac[j]), r * (a[i].get(j + 1) * ac[j + 1]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x0 = a[i].get(2 * j), x1 = a[i].get(2 * j + 1);
-          y.set(2 * j, r * (x0 * ac[j] - x1 * bs[j]), r * (x1 * bc[j] + x0 * as[j]));
-        }
-      }
-      y.store_raw(to + at.a0);
-    }
-  }
+__device__ __forceinline__ uint64_t swap_f32x2(uint64_t v) {
+  float lo, hi;
+  unpack_f32x2(v, lo, hi);
+  return pack_f32x2(hi, lo);
+}
+__device__ __forceinline__ uint64_t neg_f32x2(uint64_t v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float sum_f32x2(uint64_t v) {
+  float lo, hi;
+  unpack_f32x2(v, lo, hi);
+  return lo + hi;
+}
+// ------------------------------------------------------------------ forward and gradient
+//
+// A CTA takes rows blockIdx.x, + gridDim.x, ... (with few rows, of each the share blockIdx.y of its heads).  Each thread copies its elements of the next kDepth heads,
+// of this row and those after it, into shared memory of its own ahead of their use, without registers and
+// without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
+// In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows; each
+// CTA leaves one partial sum a side and element, and a second kernel adds those in a fixed order.
+template <typename T, bool kHalf, bool kGrad>
+struct NormRing {
+  static constexpr int kVectors = sizeof(T) / 2;                      // 16-byte vectors of 8 elements
+  static constexpr int kParts = (kHalf ? 2 : 1) * (kGrad ? 2 : 1);    // x's first and second halves, dy's
+  // rows from one meeting to the next (prompt of 8191 rows 86 us at 1, 93 at 4; its gradient 203 and 155)
+  static constexpr int kAngleRows = kGrad ? 4 : 1;
+  static constexpr int kDepth = 16 / (kVectors * (kGrad ? 4 : 2));    // heads ahead: up to 256 bytes a thread
+  static constexpr int kVectorBytes = kNormThreads * 16;              // all threads' vector of one part
+  static constexpr int kPartBytes = kVectors * kVectorBytes, kStageBytes = kParts * kPartBytes, kBytes = kDepth * kStageBytes;
+};
+
+// Eight floats of a lane, two conflict-free vectors `pitch` floats apart, packed in pairs.
+__device__ __forceinline__ void load_pairs(const float* from, int pitch, uint64_t (&v)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(from), b = *reinterpret_cast<const ulonglong2*>(from + pitch);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
-// ------------------------------------------------------------------ gradient
-//
-// CTAs loop over rows, so that the sums of the weights' gradient stay in registers; each CTA leaves one
-// partial sum a side and element, and a second kernel adds those in a fixed order.
-template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kNormThreads) mfa_norm_rope_grad_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kN = sizeof(T) == 2 ? 2 : 1;
-  constexpr int kPairs = kHalf ? 8 : 4;
-  __shared__ __align__(16) float cs[2][2][kRopeMaxDim / 2];
-  extern __shared__ float red[];   // [slots][head_dim]
+// The same, read again where it is used again (values kept over a head's sums are registers that spill).
+__device__ __forceinline__ void load_pairs_again(const float* from, int pitch, uint64_t (&v)[4]) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(smem_u32(from)));
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2]), "=l"(v[3]) : "r"(smem_u32(from + pitch)));
+}
+
+template <typename T, bool kHalf, bool kGrad>
+__global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(const __grid_constant__ NormParams p) {
+  using Ring = NormRing<T, kHalf, kGrad>;
+  constexpr int kDepth = Ring::kDepth, kParts = Ring::kParts, kVectors = Ring::kVectors, kAngleRows = Ring::kAngleRows;
+  // a lane's four floats lie beside its neighbour's
+  __shared__ __align__(16) float cs[2][kAngleRows][2][kRopeMaxDim / 2];
+  __shared__ __align__(16) float sw[2][2][kRopeMaxDim / 2];   // [side][first half, second half][2 x 4 floats of a lane]
+  extern __shared__ __align__(16) uint8_t ring[];             // stages; at the end the CTA's sums
   grid_dep_wait();
+  if constexpr (!kGrad) grid_dep_launch();
   const NormPlace<kHalf> at(p);
-  const NormSide& side = at.on_q ? p.q : p.k;
-  float wa[8], wb[8], da[8] = {}, db[8] = {};   // weights and their gradients' sums, of a lane's elements
+  const int threads = blockDim.x, tid = threadIdx.x, lanes = 1 << p.log_lanes;
+  const int step = at.step, d = p.head_dim;
+  // (the last warp has angles in place of heads; what is left of a warp behind the slots has nothing)
+  const bool angles = tid >= threads - 32;
+  int heads = at.on_q ? p.q.heads : p.k.heads;
+  if (angles || tid >= (p.q.slots + p.k.slots) << p.log_lanes || at.h0 >= heads) heads = 0;
+  const bool two = kHalf && at.turned;
+
+  // The head that is copied next; each thread goes over (row, head) by itself.
+  const int head_step = step * d;
+  long long in_row = blockIdx.x;
+  int in_head = at.h0;
+  const T* in_x;
+  const T* in_dy;
+  auto start = [&](long long row) {   // the row's first head of this thread
+    const T* x = static_cast<const T*>(at.on_q ? p.q.x : p.k.x);
+    in_x = x + row * (at.on_q ? p.q.x_stride : p.k.x_stride) + static_cast<long long>(at.h0) * d + at.a0;
+    if constexpr (kGrad) {
+      const T* dy = static_cast<const T*>(at.on_q ? p.q.dy : p.k.dy);
+      in_dy = dy + row * (at.on_q ? p.q.dy_stride : p.k.dy_stride) + static_cast<long long>(at.h0) * d + at.a0;
+    }
+  };
+  const uint32_t mine = smem_u32(ring) + tid * 16;
+  uint32_t in_at = mine;
+  const int second = at.b0 - at.a0;
+  auto copy = [&]() {
+    if (in_row < p.rows && heads > 0 && at.active) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    wa[j] = at.active ? norm_weight(p, side, at.a0 + j) : 0.f;
-    wb[j] = kHalf && at.turned ? norm_weight(p, side, at.b0 + j) : 0.f;
-  }
-  int buffer = 0;
+      for (int v = 0; v < kVectors; ++v) {
+        cp_async_16(in_at + v * Ring::kVectorBytes, in_x + 8 / kVectors * v);
+        if constexpr (kGrad) cp_async_16(in_at + kParts / 2 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + 8 / kVectors * v);
+        if (two) {
+          cp_async_16(in_at + Ring::kPartBytes + v * Ring::kVectorBytes, in_x + second + 8 / kVectors * v);
+          if constexpr (kGrad) cp_async_16(in_at + 3 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + second + 8 / kVectors * v);
+        }
+      }
+    }
+    cp_async_commit();
+    in_at = in_at == mine + (kDepth - 1) * Ring::kStageBytes ? mine : in_at + Ring::kStageBytes;
+    in_head += step;
+    in_x += head_step;
+    if constexpr (kGrad) in_dy += head_step;
+    if (in_head >= heads) {
+      in_head = at.h0;
+      in_row += gridDim.x;
+      start(in_row);
+    }
+  };
+  const uint8_t* out_at = ring + tid * 16;   // the stage that is used next
+  const uint8_t* const out_end = out_at + Ring::kBytes;
+  auto fetch_again = [&](int part) {   // as load_pairs_again
+    RopeVec<T, 8> r;
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.w[4 * v]), "=r"(r.w[4 * v + 1]), "=r"(r.w[4 * v + 2]), "=r"(r.w[4 * v + 3])
+                   : "r"(smem_u32(out_at) + part * Ring::kPartBytes + v * Ring::kVectorBytes));
+    return r;
+  };
+  auto fetch = [&](int part) {
+    RopeVec<T, 8> r;
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v) {
+      const uint4 x = *reinterpret_cast<const uint4*>(out_at + part * Ring::kPartBytes + v * Ring::kVectorBytes);
+      r.w[4 * v] = x.x, r.w[4 * v + 1] = x.y, r.w[4 * v + 2] = x.z, r.w[4 * v + 3] = x.w;
+    }
+    return r;
+  };
+  if (heads > 0) {
+    start(in_row);
 #pragma unroll 1
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
-    const T* xs = static_cast<const T*>(side.x) + row * side.x_stride;
-    const T* dys = static_cast<const T*>(side.dy) + row * side.dy_stride;
-    T* dst = static_cast<T*>(side.out) + row * side.out_stride;
-    RopeVec<T, 8> a[kN], b[kN], ga[kN], gb[kN];
-    auto load = [&](int h) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const long long hi = h + i * at.step;
-        if (hi < side.heads && at.active) {
-          a[i].load(xs + hi * p.head_dim + at.a0);
-          ga[i].load(dys + hi * p.head_dim + at.a0);
-          if (kHalf && at.turned) {
-            b[i].load(xs + hi * p.head_dim + at.b0);
-            gb[i].load(dys + hi * p.head_dim + at.b0);
-          }
-        }
-      }
-    };
-    load(at.h0);
-    row_angles(p, row, threadIdx.x, blockDim.x, cs[buffer]);
-    __syncthreads();   // (the other buffer's readers are behind this barrier before it is written again)
-    float c[kPairs], s[kPairs];
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      c[i] = at.turned ? cs[buffer][0][kPairs * at.u + i] : 1.f;
-      s[i] = at.turned ? cs[buffer][1][kPairs * at.u + i] : 0.f;
-    }
+    for (int i = 0; i < kDepth; ++i) copy();
+  }
+  for (int i = tid; i < 32 * lanes; i += threads) {   // side, half, vector, lane, element
+    const int lane = i >> 2, vector = lane >> p.log_lanes;   // (vector: side, half, first or second four elements)
+    const int on_k = vector >> 2, half = vector >> 1 & 1, u = lane & (lanes - 1), e = (vector & 1) * 4 + (i & 3);
+    const NormSide& side = on_k ? p.k : p.q;
+    const bool turned = u < p.turned_units;
+    const bool there = side.heads > 0 && u < p.units && (half == 0 || (kHalf && turned));
+    sw[on_k][half][(e / 4 * lanes + u) * 4 + (e & 3)] =
+        there ? norm_weight(p, side, (turned ? 8 * u : 2 * p.pairs + 8 * (u - p.turned_units)) + half * p.pairs + e) : 0.f;
+  }
+  // half pairing: a lane's eight pairs in two vectors; adjacent: its four in one
+  auto place = [&](int i) { return kHalf ? ((i >> 2 & 1) * lanes + (i >> 3)) * 4 + (i & 3) : i; };
+  const long long chunk = static_cast<long long>(kAngleRows) * gridDim.x;
+  auto make_angles = [&](long long row, int buffer, int from, int by) {
 #pragma unroll 1
-    for (int h = at.h0; h < side.heads; h += kN * at.step) {
-      if (h != at.h0) load(h);
-      // g of a lane's elements: dy turned back
-      auto turn_back = [&](int i, float (&g)[8], float (&k)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (kHalf) {
-            const float x = ga[i].get(j), y = at.turned ? gb[i].get(j) : 0.f;
-            g[j] = x * c[j] + y * s[j];
-            k[j] = y * c[j] - x * s[j];
-          } else {
-            const float x = ga[i].get(j & ~1), y = ga[i].get(j | 1);
-            g[j] = (j & 1) ? y * c[j / 2] - x * s[j / 2] : x * c[j / 2] + y * s[j / 2];
-          }
-        }
-      };
-      float sum[2 * kN];   // sum x^2, sum u x
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        sum[2 * i] = sum[2 * i + 1] = 0.f;
-        if (h + i * at.step < side.heads && at.active) {
-          float g[8], k[8];
-          turn_back(i, g, k);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sum[2 * i] = fmaf(a[i].get(j), a[i].get(j), sum[2 * i]);
-            sum[2 * i + 1] = fmaf(g[j] * wa[j], a[i].get(j), sum[2 * i + 1]);
-          }
-          if (kHalf && at.turned) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              sum[2 * i] = fmaf(b[i].get(j), b[i].get(j), sum[2 * i]);
-              sum[2 * i + 1] = fmaf(k[j] * wb[j], b[i].get(j), sum[2 * i + 1]);
-            }
-          }
-        }
-      }
-      group_sum<2 * kN>(sum, at.mask, 1 << p.log_lanes);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const long long hi = h + i * at.step;
-        if (hi >= side.heads || !at.active) continue;
-        const float r = rsqrtf(fmaf(sum[2 * i], p.inv_dim, p.eps));
-        const float m = r * r * sum[2 * i + 1] * p.inv_dim;   // dx = r (u - x m)
-        float g[8], k[8];
-        turn_back(i, g, k);
-        T* to = dst + hi * p.head_dim;
-        RopeVec<T, 8> y;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float x0 = a[i].get(j), x1 = a[i].get(j + 1);
-          y.set(j, r * (g[j] * wa[j] - x0 * m), r * (g[j + 1] * wa[j + 1] - x1 * m));
-          da[j] = fmaf(g[j], x0 * r, da[j]);
-          da[j + 1] = fmaf(g[j + 1], x1 * r, da[j + 1]);
-        }
-        y.store_raw(to + at.a0);
-        if (kHalf && at.turned) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float x0 = b[i].get(j), x1 = b[i].get(j + 1);
-            y.set(j, r * (k[j] * wb[j] - x0 * m), r * (k[j + 1] * wb[j + 1] - x1 * m));
-            db[j] = fmaf(k[j], x0 * r, db[j]);
-            db[j + 1] = fmaf(k[j + 1], x1 * r, db[j + 1]);
-          }
-          y.store_raw(to + at.b0);
-        }
-      }
-    }
-  }
-  grid_dep_launch();
-  // the CTA's sums: over the slots of a side, in order
-  float* mine = red + (threadIdx.x >> p.log_lanes) * p.head_dim;
-  if (at.active) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mine[at.a0 + j] = da[j];
-      if (kHalf && at.turned) mine[at.b0 + j] = db[j];
-    }
-  }
+    for (int i = 0; i < kAngleRows && row < p.rows; ++i, row += gridDim.x) row_angles(p, row, from, by, cs[buffer][i], place);
+  };
+  make_angles(blockIdx.x, 0, tid, threads);
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * p.head_dim; e += blockDim.x) {
-    const bool on_k = e >= p.head_dim;
-    const int from = on_k ? p.q.slots : 0, to = on_k ? p.q.slots + p.k.slots : p.q.slots;
-    float v = 0.f;
-    for (int x = from; x < to; ++x) v += red[x * p.head_dim + (on_k ? e - p.head_dim : e)];
-    p.partial[static_cast<size_t>(blockIdx.x) * 2 * p.head_dim + e] = v;
+  const float* my_wa = &sw[at.on_q ? 0 : 1][0][4 * at.u];
+  const float* my_wb = &sw[at.on_q ? 0 : 1][1][4 * at.u];
+  uint64_t da[4] = {}, db[4] = {};   // the weights' gradient, of this thread's elements
+  int buffer = 0;
+  if (angles) {   // rows ahead, so that their loads' way is nobody's wait
+#pragma unroll 1
+    for (long long row = blockIdx.x; row < p.rows; row += chunk, buffer ^= 1) {
+      make_angles(row + chunk, buffer ^ 1, tid & 31, 32);
+      __syncthreads();
+    }
+  }
+  int in_chunk = 0;
+#pragma unroll 1
+  for (long long row = blockIdx.x; row < p.rows && !angles; row += gridDim.x) {
+    T* to = static_cast<T*>(at.on_q ? p.q.out : p.k.out) + row * (at.on_q ? p.q.out_stride : p.k.out_stride) +
+            static_cast<long long>(at.h0) * d + at.a0;
+    // Half pairing: c and s of the thread's eight pairs; adjacent: of its four, as (c, c) and (-s, s).
+    uint64_t c[4], s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = pack_f32x2(1.f, 1.f);
+      s[j] = 0;
+    }
+    if (at.turned) {
+      if constexpr (kHalf) {
+        load_pairs(&cs[buffer][in_chunk][0][4 * at.u], 4 * lanes, c);
+        load_pairs(&cs[buffer][in_chunk][1][4 * at.u], 4 * lanes, s);
+      } else {
+        const float4 x = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][0][4 * at.u]);
+        const float4 y = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][1][4 * at.u]);
+        c[0] = pack_f32x2(x.x, x.x), c[1] = pack_f32x2(x.y, x.y), c[2] = pack_f32x2(x.z, x.z), c[3] = pack_f32x2(x.w, x.w);
+        s[0] = pack_f32x2(-y.x, y.x), s[1] = pack_f32x2(-y.y, y.y), s[2] = pack_f32x2(-y.z, y.z), s[3] = pack_f32x2(-y.w, y.w);
+      }
+    }
+    // Forward: c and s times the weights.  Half pairing: y = r (a ac + b bs), r (b bc + a as), with bs negated;
+    // adjacent: y = r ((x0, x1) ac + (x1, x0) bs).
+    uint64_t ac[4], as[4], bc[4], bs[4];
+    if constexpr (!kGrad) {
+      load_pairs(my_wa, 4 * lanes, ac);
+      if constexpr (kHalf) load_pairs(my_wb, 4 * lanes, bc);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (kHalf) {
+          as[j] = mul_f32x2(ac[j], s[j]);
+          bs[j] = neg_f32x2(mul_f32x2(bc[j], s[j]));
+          bc[j] = mul_f32x2(bc[j], c[j]);
+        } else {
+          bs[j] = mul_f32x2(swap_f32x2(ac[j]), s[j]);
+        }
+        ac[j] = mul_f32x2(ac[j], c[j]);
+      }
+    }
+#pragma unroll 1
+    for (int h = at.h0; h < heads; h += step, to += head_step) {
+      cp_async_wait<kDepth - 1>();
+      const RopeVec<T, 8> a = fetch(0);
+      RopeVec<T, 8> b = {};
+      if (two) b = fetch(1);
+      uint64_t sq = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sq = fma_f32x2(a.pair(2 * j), a.pair(2 * j), sq);
+        if constexpr (kHalf) sq = fma_f32x2(b.pair(2 * j), b.pair(2 * j), sq);
+      }
+      RopeVec<T, 8> y, z;
+      if constexpr (!kGrad) {
+        float sum[1] = {at.active ? sum_f32x2(sq) : 0.f};
+        group_sum<1>(sum, at.mask, lanes);
+        const float r = rsqrtf(fmaf(sum[0], p.inv_dim, p.eps));
+        const uint64_t r2 = pack_f32x2(r, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t u = mul_f32x2(a.pair(2 * j), r2);
+          if constexpr (kHalf) {
+            const uint64_t v = mul_f32x2(b.pair(2 * j), r2);
+            y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(v, bs[j])));
+            z.set_pair(2 * j, fma_f32x2(v, bc[j], mul_f32x2(u, as[j])));
+          } else {
+            y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(swap_f32x2(u), bs[j])));
+          }
+        }
+      } else {
+        // g: dy turned back; sums of x^2 and, with u = g w, of u x
+        uint64_t g[4], k[4], wa[4], wb[4], ux = 0;
+        const RopeVec<T, 8> ga = fetch(kParts / 2);
+        RopeVec<T, 8> gb = {};
+        if (two) gb = fetch(kParts / 2 + 1);
+        load_pairs(my_wa, 4 * lanes, wa);
+        if constexpr (kHalf) load_pairs(my_wb, 4 * lanes, wb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t x = ga.pair(2 * j);
+          if constexpr (kHalf) {
+            const uint64_t v = gb.pair(2 * j);
+            g[j] = fma_f32x2(x, c[j], mul_f32x2(v, s[j]));
+            k[j] = fma_f32x2(v, c[j], neg_f32x2(mul_f32x2(x, s[j])));
+            ux = fma_f32x2(mul_f32x2(k[j], wb[j]), b.pair(2 * j), ux);
+          } else {
+            g[j] = fma_f32x2(x, c[j], neg_f32x2(mul_f32x2(swap_f32x2(x), s[j])));
+          }
+          ux = fma_f32x2(mul_f32x2(g[j], wa[j]), a.pair(2 * j), ux);
+        }
+        float sum[2] = {at.active ? sum_f32x2(sq) : 0.f, at.active ? sum_f32x2(ux) : 0.f};
+        group_sum<2>(sum, at.mask, lanes);
+        const float r = rsqrtf(fmaf(sum[0], p.inv_dim, p.eps));
+        const float m = r * (r * (r * (sum[1] * p.inv_dim)));   // dx = r u - x m
+        const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(-m, -m);
+        const RopeVec<T, 8> a = fetch_again(0);
+        RopeVec<T, 8> b = {};
+        if (two) b = fetch_again(1);
+        load_pairs_again(my_wa, 4 * lanes, wa);
+        if constexpr (kHalf) load_pairs_again(my_wb, 4 * lanes, wb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t x = a.pair(2 * j), gr = mul_f32x2(g[j], r2);
+          y.set_pair(2 * j, fma_f32x2(gr, wa[j], mul_f32x2(x, m2)));
+          da[j] = fma_f32x2(gr, x, da[j]);
+          if constexpr (kHalf) {
+            const uint64_t v = b.pair(2 * j), kr = mul_f32x2(k[j], r2);
+            z.set_pair(2 * j, fma_f32x2(kr, wb[j], mul_f32x2(v, m2)));
+            db[j] = fma_f32x2(kr, v, db[j]);
+          }
+        }
+      }
+      if (at.active) {
+        y.store_raw(to);
+        if (two) z.store_raw(to + second);
+      }
+      copy();   // into the stage that was read
+      out_at = out_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : out_at + Ring::kStageBytes;
+    }
+    if (++in_chunk == kAngleRows || row + gridDim.x >= p.rows) {
+      __syncthreads();   // the next rows' angles are there, and these rows' may be written over
+      in_chunk = 0;
+      buffer ^= 1;
+    }
+  }
+  if constexpr (kGrad) {
+    grid_dep_launch();
+    cp_async_wait<0>();   // (copies past the last row are empty)
+    // the CTA's sums: over the slots of a side, in order
+    float* red = reinterpret_cast<float*>(ring);
+    float* own = red + (tid >> p.log_lanes) * d + at.a0;
+    __syncthreads();
+    if (at.active) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<uint64_t*>(own + 2 * j) = da[j];
+        if (two) *reinterpret_cast<uint64_t*>(own + second + 2 * j) = db[j];
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < 2 * d; e += threads) {
+      const bool on_k = e >= d;
+      const int from = on_k ? p.q.slots : 0, to = on_k ? p.q.slots + p.k.slots : p.q.slots;
+      float v = 0.f;
+      for (int x = from; x < to; ++x) v += red[x * d + (on_k ? e - d : e)];
+      p.partial[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * d + e] = v;
+    }
   }
 }
 
@@ -386,7 +465,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(cons
   int buffer = 0;
 #pragma unroll 1
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
-    row_angles(p, row, threadIdx.x, blockDim.x, cs[buffer]);
+    row_angles(p, row, threadIdx.x, blockDim.x, cs[buffer], [](int i) { return i; });
     __syncthreads();
     const T* xs = static_cast<const T*>(side.x) + row * side.x_stride;
     const T* dys = static_cast<const T*>(side.dy) + row * side.dy_stride;
@@ -496,6 +575,25 @@ static void norm_slots(NormParams& p, int room, int each) {
   p.k.slots = nk;
 }
 
+// The wide path's kernel, and its shared memory in cfg.
+template <typename T, bool kHalf>
+static void (*wide_norm(bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
+  cfg.dynamicSmemBytes = grad ? NormRing<T, kHalf, true>::kBytes : NormRing<T, kHalf, false>::kBytes;
+  return grad ? mfa_norm_rope_kernel<T, kHalf, true> : mfa_norm_rope_kernel<T, kHalf, false>;
+}
+
+// cudaFuncSetAttribute for a wide kernel's dynamic shared memory, once per device and kernel.
+static mfa_status ensure_norm_smem(int i, const void* fn, int dev) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> done[8][kMaxDevices];
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  if (cacheable && done[i][dev].load(std::memory_order_acquire)) return MFA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormThreads * 256);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  if (cacheable) done[i][dev].store(true, std::memory_order_release);
+  return MFA_OK;
+}
+
 static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* table, const int32_t* positions, int32_t num_rows,
                               int32_t dtype, const mfa_norm* norm, NormSide q, NormSide k, bool grad, float* const (&dw)[2],
                               void* workspace, uint64_t workspace_bytes, void* stream) {
@@ -527,7 +625,7 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
   if (grad) {
     if ((dw[0] && !aligned(dw[0], 4)) || (dw[1] && !aligned(dw[1], 4)) || (dw[0] && dw[0] == dw[1])) return MFA_ERR_INVALID_ARG;
     if (run && (workspace == nullptr || !aligned(workspace, 16))) return MFA_ERR_INVALID_ARG;
-    if (run && workspace_bytes < MFA_NORM_ROPE_GRAD_BYTES(num_rows, c->head_dim)) return MFA_ERR_WORKSPACE;
+    if (run && workspace_bytes < MFA_NORM_ROPE_GRAD_BYTES(c->head_dim)) return MFA_ERR_WORKSPACE;
   }
   if (!run && !(grad && (dw[0] || dw[1]))) return MFA_OK;
   const bool half = c->pairing == MFA_ROPE_HALF;
@@ -562,35 +660,31 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
   cudaError_t e = cudaSuccess;
   const bool bf16 = dtype == MFA_OUT_BF16;
   if (run) {
-    int ctas = num_rows;
-    if (grad) {
-      int dev = 0, sms = 0;
-      if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-      if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-        return cuda_fail(e, "cudaDeviceGetAttribute");
-      ctas = std::min({num_rows, 2 * sms, MFA_NORM_ROPE_GRAD_PARTS});
-    }
-    p.parts = grad ? ctas : 0;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+      return cuda_fail(e, "cudaDeviceGetAttribute");
+    const int ctas = std::min({num_rows, 2 * sms, MFA_NORM_ROPE_GRAD_PARTS});
+    int shares = 1;
     void (*fn)(NormParams);
     if (wide) {
       norm_slots(p, kNormThreads >> p.log_lanes, bf16 ? 4 : 2);
-      cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) << p.log_lanes), 1, 1);
-      if (grad) {
-        if (bf16) fn = half ? mfa_norm_rope_grad_kernel<__nv_bfloat16, true> : mfa_norm_rope_grad_kernel<__nv_bfloat16, false>;
-        else fn = half ? mfa_norm_rope_grad_kernel<float, true> : mfa_norm_rope_grad_kernel<float, false>;
-      } else {
-        if (bf16) fn = half ? mfa_norm_rope_kernel<__nv_bfloat16, true> : mfa_norm_rope_kernel<__nv_bfloat16, false>;
-        else fn = half ? mfa_norm_rope_kernel<float, true> : mfa_norm_rope_kernel<float, false>;
-      }
+      // few rows: a row's heads shared by CTAs, as far as there is room and each slot has a head
+      const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1, p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
+      shares = std::max(1, std::min({rounds, std::min(2 * sms, MFA_NORM_ROPE_GRAD_PARTS) / ctas, 65535}));
+      cfg.blockDim = dim3(static_cast<unsigned>((((p.q.slots + p.k.slots) << p.log_lanes) + 31) / 32 * 32 + 32), 1, 1);
+      if (bf16) fn = half ? wide_norm<__nv_bfloat16, true>(grad, cfg) : wide_norm<__nv_bfloat16, false>(grad, cfg);
+      else fn = half ? wide_norm<float, true>(grad, cfg) : wide_norm<float, false>(grad, cfg);
+      if ((st = ensure_norm_smem((bf16 ? 0 : 4) + (half ? 2 : 0) + grad, reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
     } else {
       norm_slots(p, kNormAnyThreads / 32, 1);
       cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) * 32), 1, 1);
       if (grad) fn = bf16 ? mfa_norm_rope_any_kernel<__nv_bfloat16, true> : mfa_norm_rope_any_kernel<float, true>;
       else fn = bf16 ? mfa_norm_rope_any_kernel<__nv_bfloat16, false> : mfa_norm_rope_any_kernel<float, false>;
+      if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * 4;   // (8 warps x 512 at most)
     }
-    // a slot's sums of the weights' gradient: at most 512 threads x 16 elements, or 8 warps x 512
-    if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * 4;
+    p.parts = grad ? ctas * shares : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(shares), 1);
     if ((e = cudaLaunchKernelEx(&cfg, fn, p)) != cudaSuccess) return cuda_fail(e, "norm rope launch");
   }
   if (grad && (dw[0] || dw[1])) {

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "mfa.h"
+#include "ptx.cuh"
 
 namespace mfa {
 
@@ -45,6 +46,13 @@ struct RopeVec {
       return __uint_as_float(w[i]);
     else
       return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  // values i and i + 1 (i even, kVec > 1), packed
+  __device__ __forceinline__ uint64_t pair(int i) const { return pack_f32x2(get(i), get(i + 1)); }
+  __device__ __forceinline__ void set_pair(int i, uint64_t v) {
+    float lo, hi;
+    unpack_f32x2(v, lo, hi);
+    set(i, lo, hi);
   }
   // the pair of values i, i + 1 (kVec = 1: lo alone)
   __device__ __forceinline__ void set(int i, float lo, float hi) {

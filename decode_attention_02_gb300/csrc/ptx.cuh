@@ -314,6 +314,17 @@ __device__ __forceinline__ void ld_global_f32x8(const float* p, float (&v)[8]) {
                : "l"(p));
 }
 
+// ---------------------------------------------------------------- 16-byte copies of a thread's own
+__device__ __forceinline__ void cp_async_16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but this thread's last kGroups groups are there.
+template <int kGroups>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kGroups) : "memory");
+}
+
 // ---------------------------------------------------------------- thread-block clusters
 // All threads of the cluster's CTAs; what was written before (the other CTAs' shared memory too) is
 // seen after.

@@ -625,9 +625,7 @@ typedef struct mfa_norm_grad_rows {
 
 /* Bytes of workspace of mfa_norm_rope_grad_run. */
 #define MFA_NORM_ROPE_GRAD_PARTS 512
-#define MFA_NORM_ROPE_GRAD_BYTES(num_rows, head_dim)                                                        \
-    (8ull * (uint64_t)(head_dim) *                                                                          \
-     (uint64_t)((num_rows) < MFA_NORM_ROPE_GRAD_PARTS ? (num_rows) : MFA_NORM_ROPE_GRAD_PARTS))
+#define MFA_NORM_ROPE_GRAD_BYTES(head_dim) (8ull * (uint64_t)(head_dim) * MFA_NORM_ROPE_GRAD_PARTS)
 
 /*
  * Enqueue the gradient of mfa_norm_rope_run (two launches): with g = dy turned back and h = x r,
@@ -636,7 +634,7 @@ typedef struct mfa_norm_grad_rows {
  *   q_weight_grad, k_weight_grad : device fp32 [head_dim], written (zeros without rows or heads), or
  *               NULL.  Summed in fp32 in an order that depends on the sizes and the device alone: the same call
  *               gives the same bits.
- *   workspace : device, 16-byte aligned, >= MFA_NORM_ROPE_GRAD_BYTES(num_rows, head_dim) bytes; scratch.
+ *   workspace : device, 16-byte aligned, >= MFA_NORM_ROPE_GRAD_BYTES(head_dim) bytes; scratch.
  *               Two calls that may overlap on the GPU need one each.
  */
 mfa_status mfa_norm_rope_grad_run(const mfa_rope_config* config, const mfa_rope_pair* table,

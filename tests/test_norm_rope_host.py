@@ -55,7 +55,7 @@ def run(lib, c=None, q=None, k=None, norm=None, rows=8, dtype=0, table=0x1000, p
 
 
 def grad(lib, c=None, q=None, k=None, norm=None, rows=8, dtype=0, table=0x1000, positions=0x2000, dwq=0x8000, dwk=0x9000, ws=0xA000,
-         size=8 * 128 * 8):
+         size=8 * 128 * 512):
     n = dict(q_weight=0x3000, k_weight=0x4000, weight_dtype=0, eps=1e-6) | (norm or {})
     return lib.mfa_norm_rope_grad_run(c or config(), P(table), P(positions), rows, dtype, mfa.MfaNorm(*n.values()),
                                       mfa.MfaNormGradRows(*(GRAD | (q or {})).values()),
@@ -92,6 +92,6 @@ def test_refusals_of_the_gradient(lib, kw):
 
 def test_other_refusals(lib):
     assert run(lib, c=config(head_dim=513, rotary_dim=128)) == UNSUPPORTED
-    assert grad(lib, size=8 * 128 * 8 - 1) == WORKSPACE
+    assert grad(lib, size=8 * 128 * 512 - 1) == WORKSPACE
     assert lib.mfa_norm_rope_run(config(), P(0x1000), P(0x2000), 8, 0, None, mfa.MfaRopeRows(*ROWS.values()), None, None) == INVALID
     assert run(lib, rows=0, table=None, positions=None, norm=dict(q_weight=None, k_weight=None)) == mfa.MFA_OK   # nothing to do
