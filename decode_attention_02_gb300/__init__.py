@@ -46,6 +46,7 @@ MFA_PLAN_EARLY_METADATA = 0x4
 MFA_PLAN_EVEN_SPLIT = 0x100      # set by mfa_block_decode_plan alone
 MFA_PLAN_UNIT_CLUSTERS = 0x200   # likewise
 MFA_PLAN_WINDOW = 0x400          # set by mfa_window_decode_plan alone
+MFA_PLAN_TREE = 0x800            # set by mfa_tree_decode_plan alone
 
 MFA_ROPE_HALF = 0
 MFA_ROPE_ADJACENT = 1
@@ -53,6 +54,8 @@ MFA_ROPE_MAX_AXES = 4
 MFA_ROPE_INTERLEAVED = 0x1
 MFA_ROPE_OWN_SPECTRUM = 0x2
 MFA_NORM_ROPE_GRAD_PARTS = 512
+
+MFA_TREE_MAX_NODES = 64
 
 NUM_Q_HEADS = 64
 HEAD_DIM = 256
@@ -63,7 +66,7 @@ EXPORTED_SYMBOLS = ("mfa_decode_plan", "mfa_decode_run", "mfa_combine", "mfa_rea
                     "mfa_status_string", "mfa_abi_version", "mfa_last_cuda_error",
                     "mfa_decode_run_static_workspace", "mfa_kv_append", "mfa_decode_run_host",
                     "mfa_decode_append_run", "mfa_block_decode_plan", "mfa_block_decode_run", "mfa_block_kv_append",
-                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_rope_table", "mfa_rope_run",
+                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_tree_decode_plan", "mfa_tree_decode_run", "mfa_rope_table", "mfa_rope_run",
                     "mfa_norm_rope_run", "mfa_norm_rope_grad_run")
 
 # Size of the library's own scratch array used by mfa_decode_run_static_workspace.
@@ -179,6 +182,11 @@ def load_library(path: str = LIB_PATH):
     lib.mfa_window_decode_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), ctypes.c_int32,
                                           ctypes.POINTER(MfaWindow), P, P, P, P, P, P, P, P, P, P, ctypes.c_uint64, P]
     lib.mfa_window_decode_run.restype = ctypes.c_int
+    lib.mfa_tree_decode_plan.argtypes = lib.mfa_block_decode_plan.argtypes
+    lib.mfa_tree_decode_plan.restype = ctypes.c_int
+    lib.mfa_tree_decode_run.argtypes = [ctypes.POINTER(MfaPlan), ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, P, P, P,
+                                        P, P, P, P, P, P, ctypes.c_uint64, P]
+    lib.mfa_tree_decode_run.restype = ctypes.c_int
     lib.mfa_block_kv_append.argtypes = [ctypes.POINTER(MfaProblem), ctypes.c_int32, P, P, ctypes.c_int32, P,
                                         ctypes.c_int32, P, P, P, P, P, P, P, P]
     lib.mfa_block_kv_append.restype = ctypes.c_int
@@ -421,6 +429,31 @@ def mfa_window_decode_run(plan: MfaPlan, problem: MfaProblem, scale_tokens: int,
     _check(st, "mfa_window_decode_run")
 
 
+def mfa_tree_decode_plan(problem: MfaProblem, scale_tokens: int, host_seq_lens: Optional[Sequence[int]] = None,
+                         max_seq_len: int = 0, num_sms: int = 0, force_ctas: int = 0, flags: int = 0) -> MfaPlan:
+    """Split the work of mfa_tree_decode_run (host only); see include/mfa.h."""
+    lib = load_library()
+    plan = MfaPlan()
+    lens_arr = _host_lengths(problem, host_seq_lens)
+    st = lib.mfa_tree_decode_plan(ctypes.byref(problem), int(scale_tokens), lens_arr, int(max_seq_len), int(num_sms),
+                                  int(force_ctas), int(flags), ctypes.byref(plan))
+    _check(st, "mfa_tree_decode_plan")
+    return plan
+
+
+def mfa_tree_decode_run(plan: MfaPlan, problem: MfaProblem, scale_tokens: int, q, k_cache, v_cache, k_scale, v_scale,
+                        block_table, seq_lens, tree, out, lse, workspace, stream=None,
+                        workspace_bytes: Optional[int] = None) -> None:
+    """Attention of a tree of drafted tokens over a block-scaled 8-bit cache (see include/mfa.h)."""
+    lib = load_library()
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    st = lib.mfa_tree_decode_run(ctypes.byref(plan), ctypes.byref(problem), scale_tokens, _ptr(q), _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(tree),
+                                 _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check(st, "mfa_tree_decode_run")
+
+
 def mfa_block_kv_append(problem: MfaProblem, scale_tokens: int, k_new, v_new, num_new: int, new_offsets, max_new: int,
                         positions, block_table, k_cache, v_cache, k_scale, v_scale, device_status=None,
                         stream=None) -> None:
@@ -641,22 +674,13 @@ class BlockDecoder(_OnDevice):
         if host_seq_lens is None and max_seq_len == 0:
             max_seq_len = max_pages_per_seq * PAGE_SIZE
         with torch.cuda.device(self.device):
-            if self.window is None:
-                self.plan = mfa_block_decode_plan(self.problem, self.scale_tokens, host_seq_lens, max_seq_len, 0,
-                                                  force_ctas, flags)
-            else:
-                self.plan = mfa_window_decode_plan(self.problem, self.scale_tokens, self.window, host_seq_lens, max_seq_len,
-                                                   0, force_ctas, flags)
+            self.plan = self._split(host_seq_lens, max_seq_len, 0, force_ctas, flags)
             self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
         self._refs = (ctypes.byref(self.plan), ctypes.byref(self.problem))
-        # the library's decode and its arguments up to q
-        if self.window is None:
-            self._run = (self._lib.mfa_block_decode_run, "mfa_block_decode_run", (*self._refs, self.scale_tokens))
-        else:
-            self._run = (self._lib.mfa_window_decode_run, "mfa_window_decode_run",
-                         (*self._refs, self.scale_tokens, ctypes.byref(self.window)))
+        self._run = self._decode_call()
+        self._append_ref = self._refs[1]
         rows = batch * tokens_per_seq
         self._q_shape = torch.Size((rows, num_q_heads, head_dim))
         self._lse_shape = self._q_shape[:2]
@@ -669,6 +693,19 @@ class BlockDecoder(_OnDevice):
         self._out_dtype = torch.float32 if out_dtype == MFA_OUT_FP32 else torch.bfloat16
         # appends whose status a checked decode has yet to report (it clears the word for its own)
         self._checked, self._unreported = bool(flags & MFA_PLAN_CHECK), False
+
+    def _split(self, *args) -> MfaPlan:
+        """The plan of this decoder's calls."""
+        if self.window is None:
+            return mfa_block_decode_plan(self.problem, self.scale_tokens, *args)
+        return mfa_window_decode_plan(self.problem, self.scale_tokens, self.window, *args)
+
+    def _decode_call(self):
+        """The library's decode, its name, and its arguments up to q."""
+        if self.window is None:
+            return self._lib.mfa_block_decode_run, "mfa_block_decode_run", (*self._refs, self.scale_tokens)
+        return (self._lib.mfa_window_decode_run, "mfa_window_decode_run",
+                (*self._refs, self.scale_tokens, ctypes.byref(self.window)))
 
     def _cache_fits(self, k_cache, v_cache, k_scale, v_scale, block_table) -> bool:
         _, u8, f32, i32 = self._types
@@ -685,6 +722,10 @@ class BlockDecoder(_OnDevice):
     def __call__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None, lse=None, stream=None):
         """One decode step: (out [batch * tokens, num_q_heads, head_dim], lse [.., num_q_heads]).  With
         MFA_PLAN_CHECK it reports what appends since the last one could not place, too."""
+        return self._step(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, (), out, lse, stream)
+
+    def _step(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, more, out, lse, stream):
+        """A decode step; ``more``: the (checked) tensors of the library's call between seq_lens and out."""
         bf16, _, f32, i32 = self._types
         i = self._index
         if not (_fits(q, bf16, self._q_shape, i) and _fits(seq_lens, i32, self._batch_shape, i) and
@@ -701,7 +742,7 @@ class BlockDecoder(_OnDevice):
             _refuse(i, ("lse", lse, f32, self._lse_shape))
         before = self._take_status(stream) if self._unreported else 0
         try:
-            self._decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, stream)
+            self._decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, more, out, lse, stream)
         finally:
             if before:
                 self._leave_status(before, stream)
@@ -723,13 +764,13 @@ class BlockDecoder(_OnDevice):
                                                           device=self.device))
         self._torch.cuda.current_stream(self._index).synchronize()
 
-    def _decode(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, stream) -> None:
+    def _decode(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, more, out, lse, stream) -> None:
         function, where, head = self._run
         self._call(function, where,
                    (*head, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                    block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                    self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
-                   (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse))
+                    block_table.data_ptr(), seq_lens.data_ptr(), *[x.data_ptr() for x in more], out.data_ptr(),
+                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
+                   (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *more, out, lse))
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
                max_new: int = 0, device_status=None, stream=None):
@@ -761,11 +802,64 @@ class BlockDecoder(_OnDevice):
         if self._checked and status == self.workspace.data_ptr():
             self._unreported = True
         self._call(self._lib.mfa_block_kv_append, "mfa_block_kv_append",
-                   (self._refs[1], self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
+                   (self._append_ref, self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
                     block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), status), stream, (self.workspace,),
                    (k_new, v_new, offsets, positions, block_table, k_cache, v_cache, k_scale, v_scale, device_status))
+
+
+class TreeDecoder(BlockDecoder):
+    """Attention of trees of drafted tokens over a block-scaled 8-bit cache, and the append of their rows.
+
+    Each sequence's last ``tree_tokens`` cached tokens (1 to 64) are the nodes of a tree: node i sees the tokens
+    before the tree, and node j where bit j of its mask is set.  The other arguments, the cache and the rules of
+    streams and workspaces are those of BlockDecoder.  A shorter tree takes its nodes first and masks that leave
+    out the rest.  Once some nodes are accepted, ``append`` their rows again from the tree's first position, and
+    the cache goes on behind them.
+    """
+
+    def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, tree_tokens: int, num_q_heads: int = NUM_Q_HEADS,
+                 num_kv_heads: int = 1, head_dim: int = HEAD_DIM, scale_tokens: int = 64,
+                 softmax_scale: Optional[float] = None, host_seq_lens=None, max_seq_len: int = 0, force_ctas: int = 0,
+                 flags: int = 0, device=None, out_dtype: int = MFA_OUT_BF16):
+        super().__init__(batch, max_pages_per_seq, num_blocks, num_q_heads, num_kv_heads, head_dim, scale_tokens,
+                         softmax_scale, host_seq_lens, max_seq_len, force_ctas, flags, device, out_dtype, tree_tokens)
+        torch = self._torch
+        # appends: rows of any number a sequence (offsets), by default the tree's
+        self._append_problem = make_problem(batch, max_pages_per_seq, num_blocks, MFA_KV_FP8_E4M3, softmax_scale,
+                                            num_q_heads=num_q_heads, head_dim=head_dim, num_kv_heads=num_kv_heads)
+        self._append_ref = ctypes.byref(self._append_problem)
+        self._tree_type, self._tree_shape = torch.int64, torch.Size((batch, tree_tokens))
+        with torch.cuda.device(self.device):
+            self._offsets = torch.arange(0, (batch + 1) * tree_tokens, tree_tokens, dtype=torch.int32, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
+
+    def _split(self, *args) -> MfaPlan:
+        return mfa_tree_decode_plan(self.problem, self.scale_tokens, *args)
+
+    def _decode_call(self):
+        return self._lib.mfa_tree_decode_run, "mfa_tree_decode_run", (*self._refs, self.scale_tokens)
+
+    def __call__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, tree, out=None, lse=None, stream=None):
+        """One step: (out [batch * tree_tokens, num_q_heads, head_dim], lse [.., num_q_heads]); ``tree`` int64
+        [batch, tree_tokens], the masks (bit 63 is the sign).  seq_lens count the trees' tokens."""
+        if not _fits(tree, self._tree_type, self._tree_shape, self._index):
+            _refuse(self._index, ("tree", tree, self._tree_type, self._tree_shape))
+        return self._step(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, (tree,), out, lse, stream)
+
+    def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
+               max_new: int = 0, device_status=None, stream=None):
+        """As BlockDecoder.append; without ``offsets`` each sequence's rows are its tree's."""
+        if offsets is None:
+            offsets, max_new = self._offsets, self._tree_shape[1]
+            if k_new.shape[0] != self._tree_shape.numel():
+                raise ValueError(f"k_new: expected {self._tree_shape.numel()} rows, {max_new} a sequence, got {k_new.shape[0]}")
+        super().append(k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets, max_new,
+                       device_status, stream)
+        if stream is not None and offsets is self._offsets:
+            self._keep(stream, (offsets,))
 
 
 class Rope(_OnDevice):

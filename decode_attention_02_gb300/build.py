@@ -10,8 +10,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmfa.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in
-           ("mfa_decode.cu", "mfa_kv_append.cu", "mfa_block_decode.cu", "mfa_block_append.cu", "mfa_rope.cu",
-            "mfa_norm_rope.cu")]
+           ("mfa_decode.cu", "mfa_kv_append.cu", "mfa_block_decode.cu", "mfa_tree_decode.cu", "mfa_block_append.cu",
+            "mfa_rope.cu", "mfa_norm_rope.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -220,10 +220,10 @@ __global__ void __launch_bounds__(kBlkThreads, 5) mfa_block_append_kernel(const 
   if (it == 0 && !(begun && s == s_old)) *scale = s;
 }
 
-mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens) {
+mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens, int most_tokens) {
   if (pr == nullptr) return MFA_ERR_INVALID_ARG;
   if (pr->batch < 0 || pr->max_pages_per_seq < 1 || pr->num_blocks < 1) return MFA_ERR_INVALID_ARG;
-  if (pr->tokens_per_seq < 1 || pr->tokens_per_seq > 4) return MFA_ERR_INVALID_ARG;
+  if (pr->tokens_per_seq < 1 || pr->tokens_per_seq > most_tokens) return MFA_ERR_INVALID_ARG;
   if (pr->num_q_heads < 1 || pr->num_kv_heads < 1 || pr->head_dim < 1 || pr->page_size < 1 || scale_tokens < 1)
     return MFA_ERR_INVALID_ARG;
   if (pr->kv_dtype != MFA_KV_BF16 && pr->kv_dtype != MFA_KV_FP8_E4M3 && pr->kv_dtype != MFA_KV_MXFP4)

@@ -25,8 +25,9 @@ mfa_status check_problem(const mfa_problem* pr);
 // 2 shared latent.
 int problem_shape(const mfa_problem* pr);
 
-// Shape, dtype and range checks of a problem over a block-scaled cache (MFA_OK, or the error).
-mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens);
+// Shape, dtype and range checks of a problem over a block-scaled cache with 1 to most_tokens new tokens a
+// sequence (MFA_OK, or the error).
+mfa_status check_block_problem(const mfa_problem* pr, int scale_tokens, int most_tokens = 4);
 
 // Shape and range checks of a rope's description (MFA_OK, or the error).
 mfa_status check_rope(const mfa_rope_config* c);

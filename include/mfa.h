@@ -100,6 +100,8 @@ typedef enum mfa_out_dtype {
 #define MFA_PLAN_UNIT_CLUSTERS 0x200u
 /* Set by mfa_window_decode_plan alone, in the plan: a plan of a windowed decode. */
 #define MFA_PLAN_WINDOW        0x400u
+/* Set by mfa_tree_decode_plan alone, in the plan: a plan of a decode of drafted trees. */
+#define MFA_PLAN_TREE          0x800u
 
 typedef struct mfa_problem {
     int32_t batch;             /* B >= 0 sequences, one new query token each */
@@ -512,6 +514,43 @@ mfa_status mfa_window_decode_run(const mfa_plan* plan, const mfa_problem* proble
                                  const int32_t* block_table, const int32_t* seq_lens,
                                  void* out, float* lse, void* workspace, uint64_t workspace_bytes,
                                  void* stream);
+
+/*
+ * ------------------------------------------------------------------ trees of drafted tokens
+ *
+ * A decode step over the block-scaled cache that verifies a tree of drafted tokens (speculative
+ * decoding): the T = problem->tokens_per_seq nodes of sequence b, 1 to MFA_TREE_MAX_NODES, are the last
+ * T of its L_b cached tokens (appended as any others, node j at position L_b - T + j whatever its depth),
+ * and node i sees the tokens 0 .. L_b - T - 1 before the tree, and node j where bit j of tree[b][i]
+ * is set: usually its ancestors and itself.  Any mask is taken (bits from T on count for nothing; a
+ * node whose mask is 0 sees what is before the tree); in a sequence of fewer than T tokens the nodes at
+ * negative positions are not there.  A row that sees nothing gets out = 0 and lse = -inf.
+ */
+#define MFA_TREE_MAX_NODES 64
+
+/* As mfa_block_decode_plan; the work is split by cost, in units of at most 128 rows.  The plan is for
+ * mfa_tree_decode_run alone. */
+mfa_status mfa_tree_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
+                                const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
+                                int32_t force_ctas, uint32_t flags, mfa_plan* plan);
+
+/*
+ * As mfa_block_decode_run, with
+ *   q, out, lse  : [B, T, num_q_heads, d] and [B, T, num_q_heads];
+ *   tree         : device uint64 [B, T], 8-byte aligned.
+ * Sums and lse are fp32.  A weight times its value scale is rounded to 7 significant bits, where it is under
+ * 2^-12 of its row's largest of the 128 tokens about it more coarsely, and 2^-23 of that is the
+ * smallest that counts.  Value scales under 2^-50 count as 2^-50 there.
+ * A NaN code among the keys makes the rows that see its token NaN.  One among the values of a token
+ * before the tree makes its element NaN; among those of the tree's T tokens it may also reach, in its
+ * head and element, the rows that do not see it.
+ */
+mfa_status mfa_tree_decode_run(const mfa_plan* plan, const mfa_problem* problem, int32_t scale_tokens,
+                               const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale,
+                               const int32_t* block_table, const int32_t* seq_lens, const uint64_t* tree,
+                               void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                               void* stream);
 
 /*
  * ------------------------------------------------------------------ rotary positions

@@ -36,7 +36,7 @@ def decode(case, seen, out_rows, weight_bound, softmax_scale=None):
     ``seen(b, L)``: bool [out_rows, L].  The bound counts, per output element: scores and sums as the
     decode of whole sequences has them (q in two e4m3 parts: 2^-16 of its row's largest where an element is
     under 2^-9 of it; fp32 products and sums: (dim + 4) 2^-23 sum |q k|), and the rounding of a weight:
-    ``weight_bound(w, p sv's largest, p, sv, l)``.  fp32 sums: 2^-18.
+    ``weight_bound(w, p, sv, l, the tokens)``.  fp32 sums: 2^-18.
     """
     B, T, H, G, d = len(case.seq_lens), out_rows, case.heads, case.kv_heads, case.dim
     scale = d ** -0.5 if softmax_scale is None else softmax_scale
@@ -67,16 +67,32 @@ def decode(case, seen, out_rows, weight_bound, softmax_scale=None):
                 small = (q.abs() < qmax * 2.0 ** -8) * qmax * 2.0 ** -16
                 e = (scale * small @ kk.abs().T + (d + 4) * 2.0 ** -23 * scale * q.abs() @ kk.abs().T).amax(-1, keepdim=True)
                 e = e + 2.0 ** -22 * s.abs().amax(-1, keepdim=True)
-                dw = weight_bound(w, (p * ss).amax(-1, keepdim=True), p, ss, l)
+                dw = weight_bound(w, p, ss, l, see.nonzero().flatten())
                 tol[b * T + i, hs] = (dw + (torch.expm1(2 * e) + 2.0 ** -18) * w) @ vv.abs() + 1e-30
                 lse_tol[b * T + i, hs] = (e + 2.0 ** -18 + 2.0 ** -23 * lse[b * T + i, hs, None].abs()).squeeze(-1)
     return out, lse, tol, lse_tol
 
 
-def two_e4m3(w, top, p, sv, l):
+def two_e4m3(w, p, sv, l, t):
     """A weight rounded to f16 (2^-11) and split into two e4m3 parts: 2^-8 of it, or the half step of e4m3's smallest
     numbers, 2^-14 of the row's largest weight times value scale, and never more than itself; and 2^-10 for the f16."""
+    top = (p * sv).amax(-1, keepdim=True)
     return torch.minimum(torch.maximum(2.0 ** -8 * w, 2.0 ** -14 * top / sv / l), w) + 2.0 ** -10 * w
+
+
+def e4m3_and_e5m2(w, p, sv, l, t):
+    """A weight times its value scale, P, rounded to f16 (2^-11) and split into an e4m3 part and an e5m2 one of what is
+    left, where the largest P of its 128 tokens is 2^-2 at least: 2^-7 of itself (2^-4 by 2^-3); under 2^-6, where the
+    first part's half step is 2^-10, 2^-3 of that or of itself; 2^-17, the second part's smallest half step, or itself.
+    (References reach 24 under the highest, whose P is 2^8.75 at most: 2^-40 of the row's largest beside it.)"""
+    P = p * sv
+    top = torch.zeros_like(P)
+    for j in t.div(128, rounding_mode="floor").unique():
+        at = t.div(128, rounding_mode="floor") == j
+        top[:, at] = P[:, at].amax(-1, keepdim=True)
+    top = torch.maximum(top, P.amax(-1, keepdim=True) * 2.0 ** -27)
+    split = torch.maximum(2.0 ** -7 * P, torch.minimum(2.0 ** -3 * P, 2.0 ** -11 * top)) + torch.minimum(P, 2.0 ** -15 * top)
+    return split / sv / l + 2.0 ** -10 * w
 
 
 def check(out, lse, expect):
