@@ -455,5 +455,7 @@ using BlockDecodeFn = void (*)(BlockDecodeParams);
 // The kernel of drafted trees for a head width, and its threads (defined in mfa_tree_decode.cu).
 BlockDecodeFn tree_kernel(int head_dim);
 int tree_threads();
+// Enqueues the merge of the units' parts that the kernel left (cfg: stream and attributes).
+cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int head_dim, cudaLaunchConfig_t cfg);
 
 }  // namespace mfa

@@ -1172,7 +1172,48 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
   int per_cta = static_cast<int>(std::min<long long>((C + G - 1) / G / kBCostTile + 1, std::max(W, 1ll)));
   const bool by_cost = G >= least;
   if (!by_cost) best = LLONG_MAX;
-  if (N > 0 && !kind.is_tree) {
+  // Even split: the smallest quantum whose parts are no more than the CTAs (N <= most)
+  auto even_quantum = [&](long long* parts_out) {
+    auto parts_at = [&](long long q) {
+      long long parts = 0;
+      if (host_seq_lens != nullptr)
+        for (int b = 0; b < pr->batch; ++b) parts += (tiles_of(host_seq_lens[b]) + q - 1) / q;
+      else
+        parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
+      return parts * sh.readers;
+    };
+    long long lo = 1, hi = std::max(longest, 1ll);   // parts_at(hi) = N fits
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (parts_at(mid) <= most) hi = mid; else lo = mid + 1;
+    }
+    *parts_out = parts_at(lo);
+    return lo;
+  };
+  if (N > 0 && kind.is_tree) {
+    // The same for a tree's units, but without clusters: whole units, a CTA each and as many CTAs as units (in
+    // turn where they are more than the SMs), or cut evenly, or by cost.  In clocks, as measured.
+    const long long tree_tile = pr->head_dim == 256 ? 2700 : 1950, begin = 10000;   // a tile; a unit's beginning and end
+    auto tree_combine = [&](long long ctas) { return 8000 + ctas * (pr->head_dim == 256 ? 90 : 45); };
+    const long long unit = longest * tree_tile + begin, all = (W * tree_tile + N * begin) / most;
+    best = by_cost ? W * tree_tile / G + begin * (1 + (N + G - 1) / G) + (G > 1 ? tree_combine(G) : 0) : LLONG_MAX;
+    const long long whole = std::min((N + most - 1) / most * unit, all + unit);
+    if (whole <= best && (N <= most || force_ctas == 0)) {
+      best = whole;
+      mode = MFA_PLAN_UNIT_CLUSTERS;
+      per_cta = static_cast<int>(std::max(longest, 1ll));
+      G = units;
+    }
+    if (N <= most) {
+      long long parts = 0;
+      const long long q = even_quantum(&parts);
+      if (q * tree_tile + begin + tree_combine(parts) < best) {
+        mode = MFA_PLAN_EVEN_SPLIT;
+        per_cta = static_cast<int>(q);
+        G = parts;
+      }
+    }
+  } else if (N > 0) {
     // Clusters: 152 SMs hold 76, 46, 36, 28, 23 and 15 clusters of 2, 3, 4, 5, 6 and 8 such CTAs
     for (const int c : {1, 2, 3, 4, 5, 6, 8}) {
       const long long room = c == 1 || force_ctas > 0 ? most : c < 8 ? most * 9 / 10 : most * 3 / 4;
@@ -1183,25 +1224,13 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
       per_cta = static_cast<int>(std::max(q, 1ll));
       G = units * c;
     }
-    // Even split: the smallest quantum whose parts are no more than the CTAs
     if (N <= most) {
-      auto parts_at = [&](long long q) {
-        long long parts = 0;
-        if (host_seq_lens != nullptr)
-          for (int b = 0; b < pr->batch; ++b) parts += (tiles_of(host_seq_lens[b]) + q - 1) / q;
-        else
-          parts = static_cast<long long>(pr->batch) * ((longest + q - 1) / q);
-        return parts * sh.readers;
-      };
-      long long lo = 1, hi = std::max(longest, 1ll);   // parts_at(hi) = N fits
-      while (lo < hi) {
-        const long long mid = (lo + hi) / 2;
-        if (parts_at(mid) <= most) hi = mid; else lo = mid + 1;
-      }
-      if (lo * tile + combine(parts_at(lo)) < best) {
+      long long parts = 0;
+      const long long q = even_quantum(&parts);
+      if (q * tile + combine(parts) < best) {
         mode = MFA_PLAN_EVEN_SPLIT;
-        per_cta = static_cast<int>(lo);
-        G = parts_at(lo);
+        per_cta = static_cast<int>(q);
+        G = parts;
       }
     }
   }
@@ -1235,7 +1264,7 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
   if (plan->batch != pr->batch || plan->kv_dtype != pr->kv_dtype || plan->tokens_per_seq != pr->tokens_per_seq ||
       plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) !=
                                 kind.flag() ||
-      (kind.is_tree && (plan->flags & (MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) != 0) ||
+      (kind.is_tree && clusters && plan->num_ctas != units) ||
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && (clusters || plan->max_tiles_per_cta < 1)) ||
       (clusters && (units == 0 || plan->num_ctas % units != 0 || plan->num_ctas / units > 8)) ||
       plan->num_partials != units + plan->num_ctas - 1 ||
@@ -1324,7 +1353,11 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
   e = cudaLaunchKernelEx(&cfg, block_kernel_of(inst), p);
   cfg.numAttrs = 1;
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
-  if (plan->num_ctas > 1 && !clusters) {
+  if (plan->num_ctas > 1 && !clusters && kind.is_tree && plan->num_ctas <= 8 * units) {
+    // a unit's few parts (many parts of few units: by teams, below)
+    e = launch_tree_combine(p, static_cast<int>(units), pr->head_dim, cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "tree combine launch");
+  } else if (plan->num_ctas > 1 && !clusters) {
     // Teams that share a unit's parts, and then its elements' slices in CTAs of their own, while the
     // parts and the grid's size pay for them.  Measured at 152 SMs (graph, us), 1 / 2 / 4 / 8 teams;
     // d = 256, 64 rows: 1 unit of 32 parts 16.0 / 12.7 / 11.8 / 11.3, 8 of 16 15.2 / 14.2 / 13.2 / 15.2,

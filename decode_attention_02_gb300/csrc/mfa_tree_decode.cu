@@ -17,8 +17,8 @@
 //
 // P: hi keeps four bits and lo three of what is left: off by 2^-7 of itself at most, where it is at least
 // 2^-6; hi's subnormals and lo's go on to 2^-17.  A row's reference R, P = 2^(x + e - R) with x its score and
-// e its value scale's logarithm, is set so that a tile's largest P is 2^6.  It rises when one would pass 2^8.75
-// (448 is e4m3's largest), and falls when a tile's largest is under 2^-2 (to 24 under its highest at most),
+// e its value scale's logarithm, is set so that a tile's largest P is 2^2.  It rises when one would pass 2^8.75
+// (448 is e4m3's largest), and falls when a tile's largest is under 2^-3 (to 24 under its highest at most),
 // so that what follows a far larger token keeps its precision; sums and O are fp32 and move by powers of two.
 //
 // What bounds it: a tile's products are 128 x 128 x d for S and as many for O, each twice (hi and lo), 2048
@@ -44,13 +44,12 @@ namespace mfa {
 
 constexpr int kTRows = kTreeRows;      // rows of a unit
 constexpr int kTWgs = 2;               // softmax warpgroups, a page of a tile each
-constexpr int kTSoftmaxWarp0 = 4;      // warps: producer, MMA issuer, scales, one without work, softmax
+constexpr int kTSoftmaxWarp0 = 4;      // warps: producer, QK issuer, scales, PV issuer, softmax
 constexpr int kTSoftmaxWarps = 4 * kTWgs;
 constexpr int kTThreads = 32 * (kTSoftmaxWarp0 + kTSoftmaxWarps);
-constexpr int kTSlotBytes = 16384;     // a ring slot: one 128-wide half of a tile's two pages
 // shared memory behind the rings: segments, scratch, barriers (the last 512 bytes)
 constexpr int kTMisc = 14336;
-constexpr float kTTop = 6.f, kTMost = 8.75f, kTLeast = -2.f, kTDepth = 24.f;   // exponents of P, see above
+constexpr float kTTop = 4.f, kTMost = 8.75f, kTLeast = -2.f, kTDepth = 24.f;   // exponents of P, see above
 constexpr float kTScaleDown = 0x1p-24f, kTScaleUp = 0x1p24f;   // value scales are taken smaller: p = 2^(x - R) stays in range
 constexpr float kTEMin = -50.f - 24.f;   // and their logarithms at least this (smaller scales count as 2^-50)
 
@@ -58,15 +57,23 @@ template <int kDim>
 struct TreeLayout {
   static constexpr int kHalves = kDim / 128;
   static constexpr int kBoxes = 2 * kHalves;            // TMA boxes [64 tokens x 128 B] of a tile of K or V
+  static constexpr int kSlotBytes = kBoxes * 8192;      // a ring slot: a tile's keys or values, by 128-wide halves
   static constexpr int kOffQ = 0;                       // q: kHalves boxes of [128 hi rows, 128 lo rows][128 B]
   static constexpr int kOffRing = 2 * kTRows * kDim;
-  static constexpr int kSlots = (kBSmem - kTMisc - kOffRing) / kTSlotBytes;
+  static constexpr int kSlots = (kBSmem - kTMisc - kOffRing) / kSlotBytes;
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;   // K and V have rings of their own
-  static constexpr int kOffMisc = kOffRing + kSlots * kTSlotBytes;
+  static constexpr int kOffMisc = kOffRing + kSlots * kSlotBytes;
   static constexpr uint32_t kTmemS = 0;                 // two buffers of 128 columns; then P, 64 columns a page: hi, lo
   static constexpr uint32_t kTmemO = 256;               // kDim columns
-  static_assert(kKSlots >= 2 * kHalves && kOffRing % 1024 == 0, "layout");
+  static_assert(kKSlots >= 2 && kOffRing % 1024 == 0, "layout");
 };
+
+// A value that is one for the warp, told to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// A converged warp's bounded wait (see block_wait).
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, block_wait(bar, parity, abort_flag)) != 0;
+}
 
 // The nodes that a row sees of the 64 tokens from t0 on, as bits; `prefix` tokens come before the tree.
 __device__ __forceinline__ uint64_t tree_bits(uint64_t mask, int t0, int prefix, int L) {
@@ -97,18 +104,19 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // slots: K's, then V's
   constexpr int kFull = 0, kEmpty = Lay::kSlots, kSFull = 2 * Lay::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                kQReady = kPvDone + 2, kOEmpty = kQReady + 1, kQEmpty = kOEmpty + 1, kDrain = kQEmpty + 1, kBars = kDrain + 1;
+                kQReady = kPvDone + 2, kOEmpty = kQReady + 1, kQEmpty = kOEmpty + 1, kDrain = kQEmpty + 1, kScoresTurn = kDrain + 1,
+                kWeightsTurn = kScoresTurn + 2, kBars = kWeightsTurn + 1;
   static_assert(kBars * 8 <= 512, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages * kBPage;
 
   if (warp == 0) {
     for (int i = lane; i < kBars; i += 32) {
-      // arrivals a phase: one for each page of a slot; the issuer's and the scale warp's for a tile's
-      // scores; one for each softmax warp; else one
+      // arrivals a phase: one for each box of a slot; the issuer's and the scale warp's for a tile's
+      // scores; one for each softmax warp; one for each MMA issuer (drain); else one
       const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty;
-      const bool by_two = i < kEmpty || i == kSFull || i == kSFull + 1;
-      mbar_init(bar(i), by_two ? 2 : by_warps ? kTSoftmaxWarps : 1);
+      const bool by_two = i == kSFull || i == kSFull + 1 || i == kDrain;
+      mbar_init(bar(i), i < kEmpty ? kBoxes : by_two ? 2 : by_warps ? kTSoftmaxWarps : 1);
     }
     if (lane == 0) ctl[1] = 0;
     fence_mbar_init();
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         return it.rows(p, pg).to > 0 ? p.block_table[static_cast<size_t>(it.b) * p.max_pages + it.page(pg)] : 0;
       };
       int id = page_id();
-      int slot = half, phase = 0;   // (half < slots)
+      int slot = 0, phase = 0;
       bool ok = true;
       int n = 0;
       for (; n < ntiles;) {
@@ -170,111 +178,139 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           mbar_arrive(fb);
         } else {   // (the rows past the sequence's end come along: scores and weights leave them out, and the issuer zeroes V's)
           mbar_arrive_expect_tx(fb, 8192);
-          tma_load_3d_hint(sbase + Lay::kOffRing + (slot0 + slot) * kTSlotBytes + pg * 8192, is_v ? &p.tm_v : &p.tm_k, fb,
+          tma_load_3d_hint(sbase + Lay::kOffRing + (slot0 + slot) * Lay::kSlotBytes + (2 * half + pg) * 8192, is_v ? &p.tm_v : &p.tm_k, fb,
                            128 * half, 0, z, pol);
         }
         ++n;
-        slot += kHalves;
-        if (slot >= slots) {
-          slot -= slots;
+        if (++slot == slots) {
+          slot = 0;
           phase ^= 1;
         }
       }
       if (!ok) {
         atomicOr(p.status, MFA_DEV_TIMEOUT);
         // let every copy already issued land before the CTA can exit
-        for (int u = max(half, (n - kVSlots) * kHalves + half); u < n * kHalves + half; u += kHalves)
+        for (int u = max(0, n - slots); u < n; ++u)
           wait_slow(bar(kFull + slot0 + u % slots), (u / slots) & 1, nullptr, kDrainLimitNs);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer, the whole warp: lane 0 issues, all of them zero the values past a sequence's
-    // end.  One thread issues both products, so that they run in the order S(n + 1), P V(n), and S(n + 2)
-    // overwrites P(n) once it is used.
+    // ---------------- QK issuer: S(n) = Q K(n)^T
     if (ntiles > 0) {
       constexpr uint32_t kIdescQK = idesc_e4m3(false, false, kTRows, kBTile);
-      constexpr uint32_t kIdescHi = idesc_e4m3(false, true, kTRows, 128), kIdescLo = kIdescHi | (1u << 7);   // (A: e5m2)
+      const uint32_t lead = elect_lane(), base = uniform(sbase), tm = uniform(tmem);
+      const int segments = uniform(nseg);
       bool ok = true;
-      int kslot = 0, kphase = 0, vslot = 0, vphase = 0, n = 0;
-      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-      auto issue_scores = [&](int m, bool last) {
-        const uint32_t d = tmem + Lay::kTmemS + kBTile * (m & 1);
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          if (ok) ok = all(block_wait(bar(kFull + kslot), kphase, abort_flag));
-          if (!ok) return;
+      int slot = 0, phase = 0, n = 0;
+#pragma unroll 1
+      for (int s = 0; s < segments && ok; ++s) {
+        const int count = uniform(seg[s].hi - seg[s].lo);
+        ok = wait_all(bar(kQReady), s & 1, abort_flag);
+#pragma unroll 1
+        for (int i = 0; i < count && ok; ++i, ++n) {
+          ok = wait_all(bar(kFull + slot), phase, abort_flag);
+          const uint32_t d = tm + Lay::kTmemS + kBTile * (n & 1);
+          uint64_t bd = smem_desc(base + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
+          uint64_t ad = smem_desc(base + Lay::kOffQ, 16, 1024);
+          // the product that reads the weights where these scores go is issued
+          if (ok && n >= 2) ok = wait_all(bar(kScoresTurn + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t bd = smem_desc(sbase + Lay::kOffRing + kslot * kTSlotBytes, 16, 1024);
-            const uint64_t ad = smem_desc(sbase + Lay::kOffQ + h * (2 * kTRows * 128), 16, 1024);
+          uint32_t more = 0;
+#pragma unroll 1
+          for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)   // hi, lo: 16 KB on, 1024 of the descriptors' units
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)   // 32 elements a step: 2 units
-                umma_f8_ss(d, ad + 1024 * x + 2 * kk, bd + 2 * kk, kIdescQK, (h | x | kk) != 0);
-            umma_commit(bar(kEmpty + kslot));
+            for (int kk = 0; kk < 4; ++kk) {   // 32 elements a step: 2 of the descriptors' 16-byte units
+              umma_f8_ss_by(lead, d, ad + 2 * kk, bd + 2 * kk, kIdescQK, more);
+              more = 1;
+              umma_f8_ss_by(lead, d, ad + 1024 + 2 * kk, bd + 2 * kk, kIdescQK, 1);   // lo: 16 KB on
+            }
+            ad += 2048;
+            bd += 1024;
           }
-          if (++kslot == kKSlots) {
-            kslot = 0;
-            kphase ^= 1;
+          if (i > 0 && lead) mbar_arrive(bar(kWeightsTurn));
+          __syncwarp();
+          umma_commit_by(lead, bar(kSFull + (n & 1)));
+          umma_commit_by(lead, bar(kEmpty + slot));
+          if (i == count - 1) umma_commit_by(lead, bar(kQEmpty));
+          if (++slot == kKSlots) {
+            slot = 0;
+            phase ^= 1;
           }
         }
-        if (lane == 0) {
-          umma_commit(bar(kSFull + (m & 1)));
-          if (last) umma_commit(bar(kQEmpty));
-        }
-      };
-      for (int s = 0; s < nseg && ok; ++s) {
-        const int lo = seg[s].lo, hi = seg[s].hi, L = seg[s].L;
-        ok = all(block_wait(bar(kQReady), s & 1, abort_flag));
-        if (ok) issue_scores(n, lo + 1 == hi);
+      }
+      if (!ok && lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
+      // every MMA must be complete before tensor memory is released
+      umma_commit_by(lead, bar(kDrain));
+      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---------------- PV issuer: O += P(n) V(n)
+    if (ntiles > 0) {
+      constexpr uint32_t kIdescHi = idesc_e4m3(false, true, kTRows, 128), kIdescLo = kIdescHi | (1u << 7);   // (A: e5m2)
+      const uint32_t lead = elect_lane(), base = uniform(sbase), tm = uniform(tmem);
+      const int segments = uniform(nseg);
+      bool ok = true;
+      int slot = 0, phase = 0, n = 0, turn = 0;
+#pragma unroll 1
+      for (int s = 0; s < segments && ok; ++s) {
+        const int lo = uniform(seg[s].lo), hi = uniform(seg[s].hi), L = uniform(seg[s].L);
+#pragma unroll 1
         for (int j = lo; j < hi && ok; ++j, ++n) {
-          if (j + 1 < hi) issue_scores(n + 1, j + 2 == hi);
-          if (ok) ok = all(block_wait(bar(kPFull + (n & 1)), (n >> 1) & 1, abort_flag));
-          if (ok && j == lo && s > 0) ok = all(block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag));
+          ok = wait_all(bar(kFull + kKSlots + slot), phase, abort_flag);
+          const int box = Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes;
           const int rest = L - kBTile * j;            // tokens of the tile
           const bool both = rest > kBPage;            // it has its second page
-          const uint32_t ap = tmem + Lay::kTmemS + kBTile * (n & 1);
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = all(block_wait(bar(kFull + kKSlots + vslot), vphase, abort_flag));
-            if (!ok) break;
-            const int box = Lay::kOffRing + (kKSlots + vslot) * kTSlotBytes;
-            if (rest < kBTile && rest % kBPage != 0) {   // whatever lies past the end of the last page
-              uint8_t* at = smem + box + (both ? 8192 : 0);
+          if (ok && rest < kBTile && rest % kBPage != 0) {   // whatever lies past the end of the last page: zeros
+#pragma unroll 1
+            for (int h = 0; h < kHalves; ++h) {
+              uint8_t* at = smem + box + h * 16384 + (both ? 8192 : 0);
               for (int r = rest % kBPage + (lane >> 3); r < kBPage; r += 4)
                 *reinterpret_cast<uint4*>(at + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
             }
-            tc_fence_after();
-            if (lane == 0) {
-              const uint64_t bd = smem_desc(sbase + box, 8192, 1024);
-              const uint32_t d = tmem + Lay::kTmemO + 128 * h;
-#pragma unroll
-              for (int x = 0; x < 2; ++x)   // hi, lo
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)   // 32 tokens a step: 4096 bytes of V, two steps a page; 8 columns of P
-                  if (kk < 2 || both)
-                    umma_f8_ts(d, ap + 64 * (kk >> 1) + 8 * (kk & 1) + 16 * x, bd + 256 * kk, x == 0 ? kIdescHi : kIdescLo,
-                               !(j == lo && x == 0 && kk == 0));
-              umma_commit(bar(kEmpty + kKSlots + vslot));
-            }
-            if (++vslot == kVSlots) {
-              vslot = 0;
-              vphase ^= 1;
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          if (ok && lane == 0) umma_commit(bar(kPvDone + (n & 1)));
+          const uint32_t ap = tm + Lay::kTmemS + kBTile * (n & 1);
+          uint64_t bd = smem_desc(base + box, 8192, 1024);
+          if (ok && j == lo && s > 0) ok = wait_all(bar(kOEmpty), (s - 1) & 1, abort_flag);
+          if (ok) ok = wait_all(bar(kPFull + (n & 1)), (n >> 1) & 1, abort_flag);
+          // the next tile's scores go first: the softmax waits for them
+          if (ok && j + 1 < hi) ok = wait_all(bar(kWeightsTurn), turn++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < kHalves; ++h) {
+            const uint32_t d = tm + Lay::kTmemO + 128 * h;
+            // 32 tokens a step: 8 columns of P, 4096 bytes of V, two steps a page
+            umma_f8_ts_by(lead, d, ap, bd, kIdescHi, j != lo);
+            umma_f8_ts_by(lead, d, ap + 16, bd, kIdescLo, 1);
+            umma_f8_ts_by(lead, d, ap + 8, bd + 256, kIdescHi, 1);
+            umma_f8_ts_by(lead, d, ap + 24, bd + 256, kIdescLo, 1);
+            if (both) {
+              umma_f8_ts_by(lead, d, ap + 64, bd + 512, kIdescHi, 1);
+              umma_f8_ts_by(lead, d, ap + 80, bd + 512, kIdescLo, 1);
+              umma_f8_ts_by(lead, d, ap + 72, bd + 768, kIdescHi, 1);
+              umma_f8_ts_by(lead, d, ap + 88, bd + 768, kIdescLo, 1);
+            }
+            bd += 1024;
+          }
+          tc_fence_before();
+          if (lead) mbar_arrive(bar(kScoresTurn + (n & 1)));
+          __syncwarp();
+          umma_commit_by(lead, bar(kPvDone + (n & 1)));
+          umma_commit_by(lead, bar(kEmpty + kKSlots + slot));
+          if (++slot == kVSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      if (lane == 0) {
-        if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
-        // every MMA must be complete before tensor memory is released
-        umma_commit(bar(kDrain));
-        wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
-      }
+      if (!ok && lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
+      umma_commit_by(lead, bar(kDrain));
+      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -284,7 +320,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     const bool is_v = (lane & 8) != 0, mine = lane < 16 && blk < (kBPage >> p.log_scale);
     const float* src = is_v ? p.v_scale : p.k_scale;
     const float mul = is_v ? kTScaleDown : p.scale_log2;
-    for (int i = lane; i < nseg; i += 32) {   // where the combine finds a unit's parts
+    for (int i = lane; i < nseg && p.cluster == 0; i += 32) {   // where the combine finds a unit's parts
       const BlockSegment x = seg[i];
       int2* at = p.parts + static_cast<size_t>(x.kvh * p.token_groups + x.tg) * p.batch + x.b;
       if (x.lo == 0) at->x = x.slot;
@@ -339,7 +375,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       }
     }
     __syncwarp();
-  } else if (warp >= kTSoftmaxWarp0) {
+  } else {
     // ---------------- softmax and epilogue: warpgroup wg has page wg of each tile, a thread one row
     const int sw = warp - kTSoftmaxWarp0, wg = sw >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
@@ -352,7 +388,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     // q of a segment, split into e4m3 hi + lo parts under one power of two a row (split_e4m3):
     // eight lanes a row, four rows a warp at a time; lane i has the 8-element chunks i, i + 8, ...
     auto convert_q = [&](int sidx) {
-      constexpr int kChunks = kDim / 64, kRounds = kTRows / (4 * kTSoftmaxWarps), kAtOnce = 2;
+      constexpr int kChunks = kDim / 64, kRounds = kTRows / (4 * kTSoftmaxWarps), kAtOnce = 4;
       const BlockSegment sg = seg[sidx];
       const int valid = p.group * min(p.unit_tokens, p.tokens - sg.tg * p.unit_tokens);
       const __nv_bfloat16* src = p.q + ((static_cast<size_t>(sg.b) * p.tokens + sg.tg * p.unit_tokens) * p.heads +
@@ -450,9 +486,12 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         float m = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          float x = -INFINITY;
+          const uint32_t(&r)[32] = sr[g >> 1];
+          const int c = 16 * (g & 1);
+          float x = __uint_as_float(r[c + 15]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x = fmaxf(x, __uint_as_float(sr[g >> 1][16 * (g & 1) + i]));
+          for (int i = 0; i < 14; i += 2) x = max3(x, __uint_as_float(r[c + i]), __uint_as_float(r[c + i + 1]));
+          x = fmaxf(x, __uint_as_float(r[c + 14]));
           m = fmaxf(m, fmaf(x, a[g], e[g]));
         }
         // the row's largest x + e, of both pages
@@ -617,6 +656,85 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ combine kernel
+//
+// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s.  A thread has eight rows of
+// one element, as the parts hold them (32 bytes), and makes their weights itself: most units have no parts or
+// two or three, and a CTA that has nothing to do is gone after one load.  (With a warp a row for the weights
+// and few large CTAs an SM, as the decode's units of 64 rows in many parts want it, 192 units over 152 CTAs took
+// 18 us.)
+template <int kDim>
+__global__ void __launch_bounds__(256, 4) mfa_tree_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+  constexpr int kOcts = 256 / kDim, kAhead = 3;   // octs of rows of a CTA; parts that are loaded together
+  const int el = threadIdx.x % kDim, oct = blockIdx.y * kOcts + threadIdx.x / kDim;
+  const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
+  bool bad = false;
+  const int L = clamp_len(p.seq_lens[b], p.max_pages * kBPage, bad);   // (final: the decode kernel has waited for what came before)
+  grid_dep_wait();
+  grid_dep_launch();
+  if (L == 0 || oct * 8 >= p.rows8) return;
+  const int2 at = p.parts[pos];
+  if (at.y <= at.x || at.x < 0 || at.y >= p.num_partials) return;   // one part, the output itself; or past the plan, as reported
+  const float* part = p.part_o + (static_cast<size_t>(oct) * kDim + el) * 8;
+  const float* lse = p.part_lse + oct * 8;
+  const size_t pitch = static_cast<size_t>(p.rows8) * kDim;
+  float o[kAhead][8], l[kAhead][8], acc[8] = {}, sum[8] = {}, top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = -INFINITY;
+#pragma unroll 1
+  for (int k = at.x; k <= at.y; k += kAhead) {
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const size_t slot = min(k + x, at.y);
+      ld_global_f32x8(lse + slot * p.rows8, l[x]);
+      ld_global_f32x8(part + slot * pitch, o[x]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float m = top[i];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (k + x > at.y) l[x][i] = -INFINITY;
+        m = fmaxf(m, l[x][i]);
+      }
+      const float ref = m == -INFINITY ? 0.f : m;   // (a row that sees nothing of these parts)
+      const float back = ex2_approx((top[i] - ref) * 1.4426950408889634f);
+      top[i] = m;
+      sum[i] *= back;
+      acc[i] *= back;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const float w = ex2_approx((l[x][i] - ref) * 1.4426950408889634f);
+        sum[i] += w;
+        acc[i] = fmaf(w, o[x][i], acc[i]);
+      }
+    }
+  }
+  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
+  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
+  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = oct * 8 + i;
+    if (row >= valid) break;
+    const size_t to = first + row / p.group * p.heads + row % p.group;
+    const float v = sum[i] == 0.f ? 0.f : acc[i] / sum[i];
+    if (p.out_f32)
+      static_cast<float*>(p.out)[to * kDim + el] = v;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[to * kDim + el] = __float2bfloat16_rn(v);
+    if (el == 0 && p.lse != nullptr) p.lse[to] = sum[i] == 0.f ? -INFINITY : top[i] + logf(sum[i]);
+  }
+}
+
+cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int head_dim, cudaLaunchConfig_t cfg) {
+  const int octs = 256 / head_dim;
+  cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((p.rows8 / 8 + octs - 1) / octs), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, head_dim == 256 ? mfa_tree_combine_kernel<256> : mfa_tree_combine_kernel<128>, p);
 }
 
 BlockDecodeFn tree_kernel(int head_dim) { return head_dim == 256 ? mfa_tree_decode_kernel<256> : mfa_tree_decode_kernel<128>; }

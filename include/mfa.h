@@ -528,8 +528,9 @@ mfa_status mfa_window_decode_run(const mfa_plan* plan, const mfa_problem* proble
  */
 #define MFA_TREE_MAX_NODES 64
 
-/* As mfa_block_decode_plan; the work is split by cost, in units of at most 128 rows.  The plan is for
- * mfa_tree_decode_run alone. */
+/* As mfa_block_decode_plan, in units of at most 128 rows: whole units (MFA_PLAN_UNIT_CLUSTERS, num_ctas = units,
+ * of one CTA each; more than the SMs run in turn), cut evenly (MFA_PLAN_EVEN_SPLIT), or by cost.  The plan is
+ * for mfa_tree_decode_run alone. */
 mfa_status mfa_tree_decode_plan(const mfa_problem* problem, int32_t scale_tokens,
                                 const int32_t* host_seq_lens, int32_t max_seq_len, int32_t num_sms,
                                 int32_t force_ctas, uint32_t flags, mfa_plan* plan);
@@ -538,9 +539,10 @@ mfa_status mfa_tree_decode_plan(const mfa_problem* problem, int32_t scale_tokens
  * As mfa_block_decode_run, with
  *   q, out, lse  : [B, T, num_q_heads, d] and [B, T, num_q_heads];
  *   tree         : device uint64 [B, T], 8-byte aligned.
- * Sums and lse are fp32.  A weight times its value scale is rounded to 7 significant bits, where it is under
- * 2^-12 of its row's largest of the 128 tokens about it more coarsely, and 2^-23 of that is the
- * smallest that counts.  Value scales under 2^-50 count as 2^-50 there.
+ * Sums and lse are fp32.  A weight times its value scale is rounded to 7 significant bits (with fp32 outputs
+ * too); one under 2^-3 of its row's largest of the 128 tokens about it may be rounded more coarsely, at
+ * worst to 2^-3 of itself, 2^-10 of that largest at most, and 2^-14 of it is the smallest that is sure to
+ * count.  Value scales under 2^-50 count as 2^-50 there.
  * A NaN code among the keys makes the rows that see its token NaN.  One among the values of a token
  * before the tree makes its element NaN; among those of the tree's T tokens it may also reach, in its
  * head and element, the rows that do not see it.

@@ -82,7 +82,7 @@ def two_e4m3(w, p, sv, l, t):
 
 def e4m3_and_e5m2(w, p, sv, l, t):
     """A weight times its value scale, P, rounded to f16 (2^-11) and split into an e4m3 part and an e5m2 one of what is
-    left, where the largest P of its 128 tokens is 2^-2 at least: 2^-7 of itself (2^-4 by 2^-3); under 2^-6, where the
+    left, where the largest P of its 128 tokens is 2^-3 at least: 2^-7 of itself (2^-4 by 2^-3); under 2^-6, where the
     first part's half step is 2^-10, 2^-3 of that or of itself; 2^-17, the second part's smallest half step, or itself.
     (References reach 24 under the highest, whose P is 2^8.75 at most: 2^-40 of the row's largest beside it.)"""
     P = p * sv
@@ -91,7 +91,7 @@ def e4m3_and_e5m2(w, p, sv, l, t):
         at = t.div(128, rounding_mode="floor") == j
         top[:, at] = P[:, at].amax(-1, keepdim=True)
     top = torch.maximum(top, P.amax(-1, keepdim=True) * 2.0 ** -27)
-    split = torch.maximum(2.0 ** -7 * P, torch.minimum(2.0 ** -3 * P, 2.0 ** -11 * top)) + torch.minimum(P, 2.0 ** -15 * top)
+    split = torch.maximum(2.0 ** -7 * P, torch.minimum(2.0 ** -3 * P, 2.0 ** -10 * top)) + torch.minimum(P, 2.0 ** -14 * top)
     return split / sv / l + 2.0 ** -10 * w
 
 
