@@ -70,7 +70,7 @@ struct BlockDecodeParams {
   const int32_t* seq_lens;
   void* out;
   float* lse;
-  float* part_o;             // [partials][rows8 / 8][d][8 rows]: 32 bytes a thread of the epilogue
+  float* part_o;             // [partials][rows8 / 8][d][8 rows]: 32 bytes a thread of the epilogue (trees: [partials][rows8][d])
   float* part_lse;           // [partials][rows8]
   unsigned int* status;
   int batch, tokens, heads, kv_heads;
@@ -455,7 +455,7 @@ using BlockDecodeFn = void (*)(BlockDecodeParams);
 // The kernel of drafted trees for a head width, and its threads (defined in mfa_tree_decode.cu).
 BlockDecodeFn tree_kernel(int head_dim);
 int tree_threads();
-// Enqueues the merge of the units' parts that the kernel left (cfg: stream and attributes).
-cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int head_dim, cudaLaunchConfig_t cfg);
+// Enqueues the merge of the units' parts that the kernel's CTAs left (cfg: stream and attributes).
+cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int ctas, int head_dim, cudaLaunchConfig_t cfg);
 
 }  // namespace mfa

@@ -1353,9 +1353,8 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
   e = cudaLaunchKernelEx(&cfg, block_kernel_of(inst), p);
   cfg.numAttrs = 1;
   if (e != cudaSuccess) return cuda_fail(e, "block decode launch");
-  if (plan->num_ctas > 1 && !clusters && kind.is_tree && plan->num_ctas <= 8 * units) {
-    // a unit's few parts (many parts of few units: by teams, below)
-    e = launch_tree_combine(p, static_cast<int>(units), pr->head_dim, cfg);
+  if (plan->num_ctas > 1 && !clusters && kind.is_tree) {
+    e = launch_tree_combine(p, static_cast<int>(units), plan->num_ctas, pr->head_dim, cfg);
     if (e != cudaSuccess) return cuda_fail(e, "tree combine launch");
   } else if (plan->num_ctas > 1 && !clusters) {
     // Teams that share a unit's parts, and then its elements' slices in CTAs of their own, while the

@@ -600,27 +600,25 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * back;
-          if (!whole) {
-            if (row < p.rows8) {
+          if (row >= valid) {
+          } else if (!whole) {   // (parts: rows as they are in the outputs)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) part[(static_cast<size_t>(row >> 3) * kDim + col + i) * 8 + (row & 7)] = v[i];
-            }
-          } else if (row < valid) {
-            if (f32) {
+            for (int i = 0; i < 32; i += 8)
+              st_global_f32x8(part + static_cast<size_t>(row) * kDim + col + i, reinterpret_cast<const float(&)[8]>(v[i]));
+          } else if (f32) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(out + (col + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(out + (col + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-                  w[k] = *reinterpret_cast<const uint32_t*>(&x);
-                }
-                *reinterpret_cast<uint4*>(out + (col + i) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&x);
               }
+              *reinterpret_cast<uint4*>(out + (col + i) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
@@ -660,81 +658,106 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
 
 // ------------------------------------------------------------------ combine kernel
 //
-// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s.  A thread has eight rows of
-// one element, as the parts hold them (32 bytes), and makes their weights itself: most units have no parts or
-// two or three, and a CTA that has nothing to do is gone after one load.  (With a warp a row for the weights
-// and few large CTAs an SM, as the decode's units of 64 rows in many parts want it, 192 units over 152 CTAs took
-// 18 us.)
-template <int kDim>
-__global__ void __launch_bounds__(256, 4) mfa_tree_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
-  constexpr int kOcts = 256 / kDim, kAhead = 3;   // octs of rows of a CTA; parts that are loaded together
-  const int el = threadIdx.x % kDim, oct = blockIdx.y * kOcts + threadIdx.x / kDim;
+// Units in parts: out = sum_s w_s O_s with w_s = e^(lse_s - lse), lse = ln sum_s e^lse_s.  A thread has eight elements
+// of a row (32 bytes of a part), so that a part's weight is one for them, and goes over the parts with a running
+// maximum.  kTeams warps share a row's parts, in a fixed order, where they are many; where units have two or
+// three parts, or none, CTAs are short and an SM holds many.
+template <int kDim, int kTeams>
+__global__ void __launch_bounds__(256, 6) mfa_tree_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+  constexpr int kLanes = kDim / 8, kRows = 32 / kLanes * (8 / kTeams);   // lanes of a row, rows of a CTA
+  constexpr int kAhead = 2;                                             // parts that are loaded together
+  __shared__ float other[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? 32 : 1][11];   // (odd pitch: no bank conflicts)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp % kTeams;
+  const int row = blockIdx.y * kRows + warp / kTeams * (32 / kLanes) + lane / kLanes, el = lane % kLanes * 8;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
+  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
+  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
   bool bad = false;
   const int L = clamp_len(p.seq_lens[b], p.max_pages * kBPage, bad);   // (final: the decode kernel has waited for what came before)
   grid_dep_wait();
   grid_dep_launch();
-  if (L == 0 || oct * 8 >= p.rows8) return;
+  if (L == 0) return;
   const int2 at = p.parts[pos];
   if (at.y <= at.x || at.x < 0 || at.y >= p.num_partials) return;   // one part, the output itself; or past the plan, as reported
-  const float* part = p.part_o + (static_cast<size_t>(oct) * kDim + el) * 8;
-  const float* lse = p.part_lse + oct * 8;
+  const int here = min(row, valid - 1);
+  const float* part = p.part_o + static_cast<size_t>(here) * kDim + el;
+  const float* lse = p.part_lse + here;
   const size_t pitch = static_cast<size_t>(p.rows8) * kDim;
-  float o[kAhead][8], l[kAhead][8], acc[8] = {}, sum[8] = {}, top[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top[i] = -INFINITY;
+  float acc[8] = {}, sum = 0.f, top = -INFINITY;
+  auto add = [&](float l) {   // (sums and accumulators move to the larger maximum)
+    const float m = fmaxf(top, l), ref = m == -INFINITY ? 0.f : m;   // (a row that sees nothing of these parts)
+    const float back = ex2_approx((top - ref) * 1.4426950408889634f), w = ex2_approx((l - ref) * 1.4426950408889634f);
+    top = m;
+    return make_float2(back, w);
+  };
 #pragma unroll 1
-  for (int k = at.x; k <= at.y; k += kAhead) {
+  for (int k = at.x + team; k <= at.y; k += kAhead * kTeams) {
+    float o[kAhead][8], l[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const size_t slot = min(k + x, at.y);
-      ld_global_f32x8(lse + slot * p.rows8, l[x]);
+      const size_t slot = min(k + x * kTeams, at.y);
+      l[x] = lse[slot * p.rows8];
       ld_global_f32x8(part + slot * pitch, o[x]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m = top[i];
+    for (int x = 0; x < kAhead; ++x) {
+      const float2 f = add(k + x * kTeams <= at.y ? l[x] : -INFINITY);
+      sum = fmaf(sum, f.x, f.y);
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        if (k + x > at.y) l[x][i] = -INFINITY;
-        m = fmaxf(m, l[x][i]);
-      }
-      const float ref = m == -INFINITY ? 0.f : m;   // (a row that sees nothing of these parts)
-      const float back = ex2_approx((top[i] - ref) * 1.4426950408889634f);
-      top[i] = m;
-      sum[i] *= back;
-      acc[i] *= back;
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const float w = ex2_approx((l[x][i] - ref) * 1.4426950408889634f);
-        sum[i] += w;
-        acc[i] = fmaf(w, o[x][i], acc[i]);
-      }
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(acc[i], f.x, f.y * o[x][i]);
     }
   }
-  const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
-  const int valid = p.group * min(p.unit_tokens, p.tokens - tg * p.unit_tokens);
-  const size_t first = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens) * p.heads + static_cast<size_t>(kvh) * p.group;
+  if constexpr (kTeams > 1) {
+    if (team > 0) {
+      float* mine = other[team - 1][lane];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = oct * 8 + i;
-    if (row >= valid) break;
-    const size_t to = first + row / p.group * p.heads + row % p.group;
-    const float v = sum[i] == 0.f ? 0.f : acc[i] / sum[i];
-    if (p.out_f32)
-      static_cast<float*>(p.out)[to * kDim + el] = v;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[to * kDim + el] = __float2bfloat16_rn(v);
-    if (el == 0 && p.lse != nullptr) p.lse[to] = sum[i] == 0.f ? -INFINITY : top[i] + logf(sum[i]);
+      for (int i = 0; i < 8; ++i) mine[i] = acc[i];
+      mine[8] = sum;
+      mine[9] = top;
+    }
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll 1
+    for (int x = 0; x < kTeams - 1; ++x) {
+      const float* theirs = other[x][lane];
+      const float2 f = add(theirs[9]);
+      sum = fmaf(sum, f.x, f.y * theirs[8]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(acc[i], f.x, f.y * theirs[i]);
+    }
   }
+  if (row >= valid) return;
+  const size_t to = (static_cast<size_t>(b) * p.tokens + tg * p.unit_tokens + row / p.group) * p.heads + static_cast<size_t>(kvh) * p.group +
+                    row % p.group;
+  const float back = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] *= back;
+  if (p.out_f32) {
+    float* o = static_cast<float*>(p.out) + to * kDim + el;
+    *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to * kDim + el) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (el == 0 && p.lse != nullptr) p.lse[to] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
-cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int head_dim, cudaLaunchConfig_t cfg) {
-  const int octs = 256 / head_dim;
-  cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((p.rows8 / 8 + octs - 1) / octs), 1);
+cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int ctas, int head_dim, cudaLaunchConfig_t cfg) {
+  const bool many = ctas > 8 * units;   // parts of a unit
+  const int rows = 256 / head_dim * (many ? 1 : 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((p.rows8 + rows - 1) / rows), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, head_dim == 256 ? mfa_tree_combine_kernel<256> : mfa_tree_combine_kernel<128>, p);
+  BlockDecodeFn fn;
+  if (head_dim == 256) fn = many ? mfa_tree_combine_kernel<256, 8> : mfa_tree_combine_kernel<256, 1>;
+  else fn = many ? mfa_tree_combine_kernel<128, 8> : mfa_tree_combine_kernel<128, 1>;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 BlockDecodeFn tree_kernel(int head_dim) { return head_dim == 256 ? mfa_tree_decode_kernel<256> : mfa_tree_decode_kernel<128>; }
