@@ -44,11 +44,15 @@ namespace mfa {
 
 constexpr int kTRows = kTreeRows;      // rows of a unit
 constexpr int kTWgs = 2;               // softmax warpgroups, a page of a tile each
-constexpr int kTSoftmaxWarp0 = 4;      // warps: producer, QK issuer, scales, PV issuer, softmax
+constexpr int kTSoftmaxWarp0 = 4;      // warps: producer, QK issuer, scales, PV issuer, softmax, O's
 constexpr int kTSoftmaxWarps = 4 * kTWgs;
-constexpr int kTThreads = 32 * (kTSoftmaxWarp0 + kTSoftmaxWarps);
+constexpr int kTOutWarp0 = kTSoftmaxWarp0 + kTSoftmaxWarps;   // four warps that keep O
+constexpr int kTThreads = 32 * (kTOutWarp0 + 4);
+// registers a thread, of 128 at launch: the first four warps, softmax (two times four), O's
+constexpr int kTRegsRoles = 80, kTRegsSoftmax = 168, kTRegsOut = 96;
+static_assert(kTRegsRoles + kTWgs * kTRegsSoftmax + kTRegsOut <= 512, "registers");
 // shared memory behind the rings: segments, scratch, barriers (the last 512 bytes)
-constexpr int kTMisc = 14336;
+constexpr int kTMisc = 17408;
 constexpr float kTTop = 4.f, kTMost = 8.75f, kTLeast = -2.f, kTDepth = 24.f;   // exponents of P, see above
 constexpr float kTScaleDown = 0x1p-24f, kTScaleUp = 0x1p24f;   // value scales are taken smaller: p = 2^(x - R) stays in range
 constexpr float kTEMin = -50.f - 24.f;   // and their logarithms at least this (smaller scales count as 2^-50)
@@ -70,9 +74,9 @@ struct TreeLayout {
 
 // A value that is one for the warp, told to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-// A converged warp's bounded wait (see block_wait).
+// A converged warp's bounded wait (see wait_bar; inline, as calls and register budgets do not go together).
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, block_wait(bar, parity, abort_flag)) != 0;
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
 }
 
 // The nodes that a row sees of the 64 tokens from t0 on, as bits; `prefix` tokens come before the tree.
@@ -93,19 +97,23 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + Lay::kOffMisc;
   BlockSegment* seg = reinterpret_cast<BlockSegment*>(misc);
-  float* red = reinterpret_cast<float*>(misc + sizeof(BlockSegment) * kBMaxSeg);   // [2 tiles, sums][warpgroups][128 rows]
-  float* q_inv = red + 3 * kTWgs * kTRows;                          // [2 segments][128] what undoes a row's q scaling
+  float* red = reinterpret_cast<float*>(misc + sizeof(BlockSegment) * kBMaxSeg);   // [2 tiles][warpgroups][128 rows]
+  float* alpha = red + 2 * kTWgs * kTRows;                          // [2 tiles][128] what O is multiplied by
+  float* fin = alpha + 2 * kTRows;                                  // [2 segments][sums of the warpgroups, reference][128]
+  float* q_inv = fin + 2 * (kTWgs + 1) * kTRows;                         // [2 segments][128] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 2 * kTRows);        // [128] element offset of a row's output
-  float4* meta = reinterpret_cast<float4*>(row_off + kTRows);       // [2 tiles][2 pages][4 blocks] {K, V scales, log2 of V's}
+  int* moved = row_off + kTRows;                                    // [2 tiles][4 quarters of the rows] whether it is
+  float4* meta = reinterpret_cast<float4*>(moved + 8);       // [2 tiles][2 pages][4 blocks] {K, V scales, log2 of V's}
   int* ctl = reinterpret_cast<int*>(meta + 16);                     // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
-  static_assert(sizeof(BlockSegment) * kBMaxSeg + (3 * kTWgs * kTRows + 3 * kTRows) * 4 + 16 * 16 + 16 + 512 <= kTMisc, "misc");
+  static_assert(sizeof(BlockSegment) * kBMaxSeg + (2 * kTWgs + 2 + 2 * (kTWgs + 1) + 3) * kTRows * 4 + 8 * 4 + 16 * 16 + 16 + 512 <= kTMisc, "misc");
   const uint32_t bars = sbase + Lay::kOffMisc + kTMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // slots: K's, then V's
   constexpr int kFull = 0, kEmpty = Lay::kSlots, kSFull = 2 * Lay::kSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
                 kQReady = kPvDone + 2, kOEmpty = kQReady + 1, kQEmpty = kOEmpty + 1, kDrain = kQEmpty + 1, kScoresTurn = kDrain + 1,
-                kWeightsTurn = kScoresTurn + 2, kBars = kWeightsTurn + 1;
+                kWeightsTurn = kScoresTurn + 2, kMoved = kWeightsTurn + 1, kOReady = kMoved + 8, kFinal = kOReady + 2,
+                kFinEmpty = kFinal + 2, kBars = kFinEmpty + 2;
   static_assert(kBars * 8 <= 512, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages * kBPage;
@@ -114,9 +122,10 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     for (int i = lane; i < kBars; i += 32) {
       // arrivals a phase: one for each box of a slot; the issuer's and the scale warp's for a tile's
       // scores; one for each softmax warp; one for each MMA issuer (drain); else one
-      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kOEmpty;
+      const bool by_warps = i == kPFull || i == kPFull + 1 || i == kQReady || i == kFinal || i == kFinal + 1;
+      const bool by_four = i == kOEmpty || i == kOReady || i == kOReady + 1 || i == kFinEmpty || i == kFinEmpty + 1;   // O's warps
       const bool by_two = i == kSFull || i == kSFull + 1 || i == kDrain;
-      mbar_init(bar(i), i < kEmpty ? kBoxes : by_two ? 2 : by_warps ? kTSoftmaxWarps : 1);
+      mbar_init(bar(i), i < kEmpty ? kBoxes : by_two ? 2 : by_four ? 4 : by_warps ? kTSoftmaxWarps : 1);
     }
     if (lane == 0) ctl[1] = 0;
     fence_mbar_init();
@@ -145,7 +154,9 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
   const int nseg = ctl[2], ntiles = ctl[3];
 
+  // (each role's budget begins its branch and so covers all of its code)
   if (warp == 0) {
+    reg_dealloc<kTRegsRoles>();
     // ---------------- producer: lane i loads box i of each tile of K (i < kBoxes) or of V (half
     // i / 2, page i % 2), each on its own as its slots free
     if (lane < 2 * kBoxes && ntiles > 0) {
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         }
         const uint64_t pol = it.again ? again : once;
         if (it.next(p, seg, nseg)) id = page_id();
-        ok = block_wait(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
+        ok = wait_bar(bar(kEmpty + slot0 + slot), phase ^ 1, abort_flag);
         if (!ok) break;
         const uint32_t fb = bar(kFull + slot0 + slot);
         if (rows <= 0) {
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     }
     __syncwarp();
   } else if (warp == 1) {
+    reg_dealloc<kTRegsRoles>();
     // ---------------- QK issuer: S(n) = Q K(n)^T
     if (ntiles > 0) {
       constexpr uint32_t kIdescQK = idesc_e4m3(false, false, kTRows, kBTile);
@@ -247,6 +259,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     }
     __syncwarp();
   } else if (warp == 3) {
+    reg_dealloc<kTRegsRoles>();
     // ---------------- PV issuer: O += P(n) V(n)
     if (ntiles > 0) {
       constexpr uint32_t kIdescHi = idesc_e4m3(false, true, kTRows, 128), kIdescLo = kIdescHi | (1u << 7);   // (A: e5m2)
@@ -277,6 +290,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           uint64_t bd = smem_desc(base + box, 8192, 1024);
           if (ok && j == lo && s > 0) ok = wait_all(bar(kOEmpty), (s - 1) & 1, abort_flag);
           if (ok) ok = wait_all(bar(kPFull + (n & 1)), (n >> 1) & 1, abort_flag);
+          if (ok) ok = wait_all(bar(kOReady + (n & 1)), (n >> 1) & 1, abort_flag);
           // the next tile's scores go first: the softmax waits for them
           if (ok && j + 1 < hi) ok = wait_all(bar(kWeightsTurn), turn++ & 1, abort_flag);
           if (!ok) break;
@@ -314,6 +328,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
     }
     __syncwarp();
   } else if (warp == 2) {
+    reg_dealloc<kTRegsRoles>();
     // ---------------- scales: a tile's up to 2 x 4 block scales of K and of V, ahead of the softmax
     // (lane = V? page, block); page ids two tiles ahead, scales one tile ahead
     const int pg = (lane >> 2) & 1, blk = lane & 3;
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           if (more) id = page_id();
         }
         // the softmax has read the tile before last's when its weights are there
-        if (n >= 2 && !__all_sync(0xffffffffu, block_wait(bar(kPFull + (n & 1)), ((n >> 1) - 1) & 1, abort_flag))) {
+        if (n >= 2 && !__all_sync(0xffffffffu, wait_bar(bar(kPFull + (n & 1)), ((n >> 1) - 1) & 1, abort_flag))) {
           if (lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
           break;
         }
@@ -375,8 +390,9 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       }
     }
     __syncwarp();
-  } else {
-    // ---------------- softmax and epilogue: warpgroup wg has page wg of each tile, a thread one row
+  } else if (warp < kTOutWarp0) {
+    reg_alloc<kTRegsSoftmax>();
+    // ---------------- softmax: warpgroup wg has page wg of each tile, a thread one row
     const int sw = warp - kTSoftmaxWarp0, wg = sw >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -405,7 +421,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
             wr[x][k] = r < valid ? __ldg(reinterpret_cast<const uint4*>(src + row_off[r]) + i8 + 8 * k) : make_uint4(0, 0, 0, 0);
         }
         // (the previous segment's last scores are made: its q is read no more)
-        if (x0 == 0 && sidx > 0 && !block_wait(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
+        if (x0 == 0 && sidx > 0 && !wait_bar(bar(kQEmpty), (sidx - 1) & 1, abort_flag)) aborted = true;
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
           const int r = r0 + 4 * kTSoftmaxWarps * (x0 + x);
@@ -451,12 +467,12 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       const int node0 = sg.tg * p.unit_tokens;
       const int valid = p.group * min(p.unit_tokens, p.tokens - node0);
       const uint64_t mask = row < valid ? __ldg(p.tree + static_cast<size_t>(sg.b) * p.tokens + node0 + row / p.group) : 0;
-      if (!block_wait(bar(kQReady), s & 1, abort_flag)) aborted = true;
+      if (!wait_bar(bar(kQReady), s & 1, abort_flag)) aborted = true;
       const float inv = q_inv[(s & 1) * kTRows + row];
       float ref = 0.f, top = -INFINITY, most = -INFINITY;   // the reference, its highest, and what x + e may reach
       uint64_t l2 = 0;                                      // the row's sum over this page's tokens, in two parts
       for (int j = sg.lo; j < sg.hi; ++j, ++n) {
-        if (!block_wait(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
+        if (!wait_bar(bar(kSFull + (n & 1)), (n >> 1) & 1, abort_flag)) aborted = true;
         tc_fence_after();
         uint32_t sr[2][32];
         const uint32_t at = tmem + Lay::kTmemS + kBTile * (n & 1) + 64 * wg + lane_base;
@@ -501,34 +517,27 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         m = fmaxf(m, mine[(wg ^ 1) * kTRows + row]);
         const bool rise = m > most;
         const bool fall = m < ref + kTLeast && m > -INFINITY && most > -INFINITY && fmaxf(m - kTTop, top - kTDepth) < ref - 1.f;
-        if (__any_sync(0xffffffffu, rise || fall)) {
-          // ---- new references: the sums and O move to them.  (Rare after a segment's first two tiles.)
+        const bool moves = __any_sync(0xffffffffu, rise || fall);
+        float factor = 1.f;
+        if (moves) {   // new references: the sums move to them here, O by its warps
           float to = ref;
           if (fall) to = fmaxf(m - kTTop, top - kTDepth);
           if (m > ref + kTTop + 1.f || rise) to = m - kTTop;
           if (!(m > -INFINITY && m < INFINITY)) to = ref;
           const bool set = most > -INFINITY;
-          const float alpha = set ? ex2_approx(ref - to) : 1.f;
+          factor = set ? ex2_approx(ref - to) : 1.f;
           ref = to;
           if (set || (m > -INFINITY && m < INFINITY)) {
             most = ref + kTMost;
             top = fmaxf(top, ref);
           }
-          l2 = mul_f32x2(l2, pack_f32x2(alpha, alpha));
-          if (j > sg.lo) {   // O holds something: each of the two warps has half of its columns
-            if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kDim / 2; c += 32) {
-              uint32_t o[32];
-              const uint32_t oat = tmem + Lay::kTmemO + wg * (kDim / 2) + c + lane_base;
-              tmem_ld32(oat, o);
-              tmem_ld_wait(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(oat, o);
-            }
-          }
+          l2 = mul_f32x2(l2, pack_f32x2(factor, factor));
+        }
+        if (wg == 0) {
+          if (moves) alpha[(n & 1) * kTRows + row] = factor;
+          if (lane == 0) moved[(n & 1) * 4 + quarter] = moves && j > sg.lo;   // (before a segment's second tile O holds nothing)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kMoved + 4 * (n & 1) + quarter));
         }
         // p = 2^(x - R) and its sum in fp32; P = p sv rounded to f16 (2^-11) and split
         const uint64_t nref = pack_f32x2(-ref, -ref);
@@ -566,74 +575,18 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + (n & 1)));
       }
-      if (s + 1 < nseg) convert_q(s + 1);
-
-      // ---------------- the segment's result
-      {
+      {   // what the segment's result takes beside O
+        if (s >= 2 && !wait_bar(bar(kFinEmpty + (s & 1)), ((s >> 1) - 1) & 1, abort_flag)) aborted = true;
         float l0, l1;
         unpack_f32x2(l2, l0, l1);
-        float* mine = red + 2 * (kTWgs * kTRows);
-        mine[wg * kTRows + row] = l0 + l1;
-        if (!block_wait(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag)) aborted = true;
-        if (named_bar_or(1 + 4, 32 * kTSoftmaxWarps, aborted || *abort_flag)) {
-          stop = true;
-          break;
-        }
-        tc_fence_after();
-        const float sum = mine[row] + mine[kTRows + row];
-        const float back = sum == 0.f ? 0.f : kTScaleUp / sum;   // (a row that sees nothing: zeros)
-        const bool whole = sg.slot == -1;
-        const size_t first = (static_cast<size_t>(sg.b) * p.tokens + node0) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
-        float* part = p.part_o + static_cast<size_t>(max(sg.slot, 0)) * p.rows8 * kDim;
-        uint8_t* out = static_cast<uint8_t*>(p.out) + (first * kDim + row_off[row]) * (f32 ? 4 : 2);
-#pragma unroll 1
-        for (int c = 0; c < kDim / 2; c += 32) {
-          const int col = wg * (kDim / 2) + c;
-          uint32_t o[32];
-          tmem_ld32(tmem + Lay::kTmemO + col + lane_base, o);
-          tmem_ld_wait(o);
-          if (c + 32 == kDim / 2) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
-          }
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * back;
-          if (row >= valid) {
-          } else if (!whole) {   // (parts: rows as they are in the outputs)
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              st_global_f32x8(part + static_cast<size_t>(row) * kDim + col + i, reinterpret_cast<const float(&)[8]>(v[i]));
-          } else if (f32) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(out + (col + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&x);
-              }
-              *reinterpret_cast<uint4*>(out + (col + i) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        if (wg == 0 && row < valid) {
-          // (the sum's exponent joins the reference first: their logarithms alone would cancel)
-          const int k = min(static_cast<int>(__float_as_uint(sum) >> 23), 253) - 127;
-          const float v = sum == 0.f ? -INFINITY
-                                     : fmaf(static_cast<float>(k) + ref, 0.6931471805599453f,
-                                            logf(sum * __uint_as_float(static_cast<uint32_t>(127 - k) << 23)));
-          if (!whole)
-            p.part_lse[static_cast<size_t>(sg.slot) * p.rows8 + row] = v;
-          else if (p.lse != nullptr)
-            p.lse[first + row_off[row] / kDim] = v;
-        }
+        float* mine = fin + (s & 1) * ((kTWgs + 1) * kTRows) + row;
+        mine[wg * kTRows] = l0 + l1;
+        if (wg == 0) mine[kTWgs * kTRows] = ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kFinal + (s & 1)));
       }
+      if (s + 1 < nseg) convert_q(s + 1);
+      if (named_bar_or(1 + 4, 32 * kTSoftmaxWarps, aborted || *abort_flag)) stop = true;
     }
     // sequences without tokens: zeros and -inf, in turn over the CTAs
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -650,6 +603,103 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       *abort_flag = 1;
       atomicOr(p.status, MFA_DEV_TIMEOUT);
     }
+  } else {
+    reg_dealloc<kTRegsOut>();
+    // ---------------- O: a warp has 32 rows.  References that move: O moves with them between two products, while the
+    // softmax goes on (by the softmax's own threads, in between, such a tile took half as long again).  A segment's
+    // result: written while the next one's q is converted.
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t at = tmem + Lay::kTmemO + (static_cast<uint32_t>(quarter * 32) << 16);
+    const bool f32 = p.out_f32 != 0;
+    bool ok = true;
+    int n = 0;
+#pragma unroll 1
+    for (int s = 0; s < nseg && ok; ++s) {
+      const BlockSegment sg = seg[s];
+#pragma unroll 1
+      for (int j = sg.lo; j < sg.hi && ok; ++j, ++n) {
+        ok = wait_all(bar(kMoved + 4 * (n & 1) + quarter), (n >> 1) & 1, abort_flag);
+        if (ok && moved[(n & 1) * 4 + quarter]) {
+          const float f = alpha[(n & 1) * kTRows + row];
+          ok = wait_all(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kDim && ok; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(at + c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(at + c, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kOReady + (n & 1)));
+      }
+      if (ok) ok = wait_all(bar(kFinal + (s & 1)), (s >> 1) & 1, abort_flag);
+      if (!ok) break;
+      const float* mine = fin + (s & 1) * ((kTWgs + 1) * kTRows) + row;
+      const float sum = mine[0] + mine[kTRows], ref = mine[kTWgs * kTRows];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kFinEmpty + (s & 1)));
+      ok = wait_all(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int node0 = sg.tg * p.unit_tokens, valid = p.group * min(p.unit_tokens, p.tokens - node0);
+      const float back = sum == 0.f ? 0.f : kTScaleUp / sum;   // (a row that sees nothing: zeros)
+      const bool whole = sg.slot == -1;
+      const size_t first = (static_cast<size_t>(sg.b) * p.tokens + node0) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
+      float* part = p.part_o + (static_cast<size_t>(max(sg.slot, 0)) * p.rows8 + row) * kDim;
+      uint8_t* out = static_cast<uint8_t*>(p.out) + (first * kDim + row_off[row]) * (f32 ? 4 : 2);
+#pragma unroll 1
+      for (int c = 0; c < kDim; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(at + c, o);
+        tmem_ld_wait(o);
+        if (c + 32 == kDim) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * back;
+        if (row >= valid) {
+        } else if (!whole) {   // (parts: rows as they are in the outputs)
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) st_global_f32x8(part + c + i, reinterpret_cast<const float(&)[8]>(v[i]));
+        } else if (f32) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+              w[k] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(out + (c + i) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (row < valid) {
+        // (the sum's exponent joins the reference first: their logarithms alone would cancel)
+        const int k = min(static_cast<int>(__float_as_uint(sum) >> 23), 253) - 127;
+        const float v = sum == 0.f ? -INFINITY
+                                   : fmaf(static_cast<float>(k) + ref, 0.6931471805599453f,
+                                          logf(sum * __uint_as_float(static_cast<uint32_t>(127 - k) << 23)));
+        if (!whole)
+          p.part_lse[static_cast<size_t>(sg.slot) * p.rows8 + row] = v;
+        else if (p.lse != nullptr)
+          p.lse[first + row_off[row] / kDim] = v;
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, MFA_DEV_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
