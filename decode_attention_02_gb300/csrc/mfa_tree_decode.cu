@@ -53,6 +53,7 @@ constexpr int kTRegsRoles = 80, kTRegsSoftmax = 168, kTRegsOut = 96;
 static_assert(kTRegsRoles + kTWgs * kTRegsSoftmax + kTRegsOut <= 512, "registers");
 // shared memory behind the rings: segments, scratch, barriers (the last 512 bytes)
 constexpr int kTMisc = 17408;
+constexpr int kTurnStep = 2;
 constexpr float kTTop = 4.f, kTMost = 8.75f, kTLeast = -2.f, kTDepth = 24.f;   // exponents of P, see above
 constexpr float kTScaleDown = 0x1p-24f, kTScaleUp = 0x1p24f;   // value scales are taken smaller: p = 2^(x - R) stays in range
 constexpr float kTEMin = -50.f - 24.f;   // and their logarithms at least this (smaller scales count as 2^-50)
@@ -74,6 +75,28 @@ struct TreeLayout {
 
 // A value that is one for the warp, told to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// Of four neighbouring lanes, each with four quarters of kWords words: lane l ends with quarter l of all four, in the
+// lanes' order.
+template <int kWords>
+__device__ __forceinline__ void exchange_quarters(uint32_t (&v)[4 * kWords]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int step = 1; step <= 2; step *= 2) {
+    const bool hi = lane & step;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q & step) continue;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {   // quarters q and q + step: keep one, send the other
+        uint32_t& a = v[q * kWords + i];
+        uint32_t& b = v[(q + step) * kWords + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? a : b, step);
+        a = hi ? got : a;
+        b = hi ? b : got;
+      }
+    }
+  }
+}
 // A converged warp's bounded wait (see wait_bar; inline, as calls and register budgets do not go together).
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag)) != 0;
@@ -234,6 +257,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {   // 32 elements a step: 2 of the descriptors' 16-byte units
+              // (the other issuer's turn begins while the last steps, which share nothing with its product, wait their own)
+              if (kk == kTurnStep && h == kHalves - 1 && i > 0 && lead) mbar_arrive(bar(kWeightsTurn));
               umma_f8_ss_by(lead, d, ad + 2 * kk, bd + 2 * kk, kIdescQK, more);
               more = 1;
               umma_f8_ss_by(lead, d, ad + 1024 + 2 * kk, bd + 2 * kk, kIdescQK, 1);   // lo: 16 KB on
@@ -241,8 +266,6 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
             ad += 2048;
             bd += 1024;
           }
-          if (i > 0 && lead) mbar_arrive(bar(kWeightsTurn));
-          __syncwarp();
           umma_commit_by(lead, bar(kSFull + (n & 1)));
           umma_commit_by(lead, bar(kEmpty + slot));
           if (i == count - 1) umma_commit_by(lead, bar(kQEmpty));
@@ -651,8 +674,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       const float back = sum == 0.f ? 0.f : kTScaleUp / sum;   // (a row that sees nothing: zeros)
       const bool whole = sg.slot == -1;
       const size_t first = (static_cast<size_t>(sg.b) * p.tokens + node0) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
-      float* part = p.part_o + (static_cast<size_t>(max(sg.slot, 0)) * p.rows8 + row) * kDim;
-      uint8_t* out = static_cast<uint8_t*>(p.out) + (first * kDim + row_off[row]) * (f32 ? 4 : 2);
+      float* part = p.part_o + static_cast<size_t>(max(sg.slot, 0)) * p.rows8 * kDim;
+      uint8_t* out = static_cast<uint8_t*>(p.out) + first * kDim * (f32 ? 4 : 2);
 #pragma unroll 1
       for (int c = 0; c < kDim; c += 32) {
         uint32_t o[32];
@@ -663,27 +686,35 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kOEmpty));   // the next segment may accumulate
         }
-        float v[32];
+        // Four lanes exchange quarters of their rows, so that each writes its quarter of all four rows and a store
+        // touches eight lines in place of 32.
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * back;
-        if (row >= valid) {
-        } else if (!whole) {   // (parts: rows as they are in the outputs)
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back);
+        if (whole && !f32) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) st_global_f32x8(part + c + i, reinterpret_cast<const float(&)[8]>(v[i]));
-        } else if (f32) {
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+            w[k] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          exchange_quarters<4>(w);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(out + (c + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else {
+          for (int i = 0; i < 4; ++i) {
+            const int r = row - (lane & 3) + i;
+            if (r < valid)
+              *reinterpret_cast<uint4*>(out + row_off[r] * 2 + c * 2 + (lane & 3) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        } else {   // (parts: rows as they are in the outputs)
+          exchange_quarters<8>(o);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-              w[k] = *reinterpret_cast<const uint32_t*>(&x);
+          for (int i = 0; i < 4; ++i) {
+            const int r = row - (lane & 3) + i;
+            float* to = whole ? reinterpret_cast<float*>(out) + row_off[r] : part + static_cast<size_t>(r) * kDim;
+            if (r < valid) {
+              const uint4 x = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]), y = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
+              *reinterpret_cast<uint4*>(to + c + (lane & 3) * 8) = x;
+              *reinterpret_cast<uint4*>(to + c + (lane & 3) * 8 + 4) = y;
             }
-            *reinterpret_cast<uint4*>(out + (c + i) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
