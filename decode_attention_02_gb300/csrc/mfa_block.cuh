@@ -183,6 +183,9 @@ __device__ __forceinline__ bool block_wait(uint32_t bar, uint32_t parity, volati
   return mbar_try_wait(bar, parity) || block_wait_slow(bar, parity, abort_flag);
 }
 
+// A value that is one for the warp, told to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Four e4m3 codes of two pairs of halves, and back; four e5m2 codes.
 __device__ __forceinline__ uint32_t cvt_e4m3x4(uint32_t a, uint32_t b) {
   uint32_t r;

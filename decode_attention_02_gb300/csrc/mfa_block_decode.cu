@@ -137,6 +137,29 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float (&a)
   *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// How an MMA warp issues: one lane alone (kWarp false), or the converged warp by one of its lanes.
+template <bool kWarp>
+struct BlockIssuer {
+  uint32_t lead = 1;
+  __device__ __forceinline__ BlockIssuer() {
+    if constexpr (kWarp) lead = elect_lane();
+  }
+  __device__ __forceinline__ int one(int x) const { return kWarp ? uniform(x) : x; }   // a value that is one for the warp
+  __device__ __forceinline__ bool all(bool x) const { return kWarp ? __all_sync(0xffffffffu, x) != 0 : x; }
+  __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) const {
+    if constexpr (kWarp)
+      umma_f8_ss_by(lead, d, a, b, idesc, accumulate);
+    else
+      umma_f8_ss(d, a, b, idesc, accumulate);
+  }
+  __device__ __forceinline__ void commit(uint32_t bar) const {
+    if constexpr (kWarp)
+      umma_commit_by(lead, bar);
+    else
+      umma_commit(bar);
+  }
+};
+
 // ------------------------------------------------------------------ decode kernel
 template <int kDim, int kNR, bool kWindow>
 __global__ void __launch_bounds__(BlockLayout<kDim, kNR>::kThreads, 1)
@@ -267,40 +290,44 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     // ---------------- QK issuer: S^T(n) = K(n) Q^T, q's hi and lo parts in columns of their own: one
     // MMA for both reads K from shared memory once (as two MMAs into the same columns, four long
     // sequences 41.3 us against 40.5, two new tokens 58.1 against 57.0)
-    if (lane == 0 && ntiles > 0) {
+    // (Windowed instances issue by a converged warp, whose descriptors stay in uniform registers.)
+    if ((kWindow || lane == 0) && ntiles > 0) {
       constexpr uint32_t kIdescQK = idesc_e4m3(false, false, 128, 2 * kNR);
+      const BlockIssuer<kWindow> by;
+      const uint32_t base = by.one(sbase), tm = by.one(tmem);
+      const int segments = by.one(nseg);
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
-      for (int s = 0; s < nseg && ok; ++s) {
-        const int count = seg[s].hi - seg[s].lo;
-        ok = block_wait(bar(kQReady), s & 1, abort_flag);
+      for (int s = 0; s < segments && ok; ++s) {
+        const int count = by.one(seg[s].hi - seg[s].lo);
+        ok = by.all(block_wait(bar(kQReady), s & 1, abort_flag));
         for (int i = 0; i < count && ok; ++i, ++n) {
-          if (n >= 2) ok = block_wait(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
-          const uint32_t d = tmem + Lay::kTmemS + 2 * kNR * (n & 1);
+          if (n >= 2) ok = by.all(block_wait(bar(kSEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag));
+          const uint32_t d = tm + Lay::kTmemS + 2 * kNR * (n & 1);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = block_wait(bar(kFull + slot), phase, abort_flag);
+            if (ok) ok = by.all(block_wait(bar(kFull + slot), phase, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const uint64_t ad = smem_desc(sbase + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
-            const uint64_t bd = smem_desc(sbase + Lay::kOffQ + h * (2 * kNR * 128), 16, 1024);
+            const uint64_t ad = smem_desc(base + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
+            const uint64_t bd = smem_desc(base + Lay::kOffQ + h * (2 * kNR * 128), 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 32 elements a step: 2 in the descriptors' 16-byte units
-              umma_f8_ss(d, ad + 2 * kk, bd + 2 * kk, kIdescQK, (h | kk) != 0);
-            umma_commit(bar(kEmpty + slot));
+              by.mma(d, ad + 2 * kk, bd + 2 * kk, kIdescQK, (h | kk) != 0);
+            by.commit(bar(kEmpty + slot));
             if (++slot == kKSlots) {
               slot = 0;
               phase ^= 1;
             }
           }
           if (!ok) break;
-          umma_commit(bar(kSFull + (n & 1)));
-          if (i == count - 1) umma_commit(bar(kQEmpty));
+          by.commit(bar(kSFull + (n & 1)));
+          if (i == count - 1) by.commit(bar(kQEmpty));
         }
       }
       if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
       // every MMA must be complete before tensor memory is released
-      umma_commit(bar(kDrain));
+      by.commit(bar(kDrain));
       wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
     }
     __syncwarp();
@@ -309,27 +336,29 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     // (with a window the whole warp comes along: it zeroes values that no new token sees)
     if ((kWindow || lane == 0) && ntiles > 0) {
       constexpr uint32_t kIdescPV = idesc_e4m3(true, true, 128, 2 * kNR);
+      const BlockIssuer<kWindow> by;
+      const uint32_t base = by.one(sbase), tm = by.one(tmem);
+      const int segments = by.one(nseg);
       bool ok = true;
       int slot = 0, phase = 0, n = 0;
-      auto all = [](bool x) { return kWindow ? __all_sync(0xffffffffu, x) != 0 : x; };
-      for (int s = 0; s < nseg && ok; ++s) {
-        const int lo = seg[s].lo, hi = seg[s].hi;
+      for (int s = 0; s < segments && ok; ++s) {
+        const int lo = by.one(seg[s].lo), hi = by.one(seg[s].hi);
         BlockView w;
         BlockGap gap = {-1, 0, 0};
         if constexpr (kWindow) {
-          w = block_view(seg[s].L, p.tokens, p.window, p.sinks);
+          w = block_view(by.one(seg[s].L), p.tokens, p.window, p.sinks);
           gap = view_gap(w, p.sinks);
         } else {
           w.L = seg[s].L;
         }
         for (int j = lo; j < hi && ok; ++j, ++n) {
-          ok = all(block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag));
-          if (ok && j == lo && s > 0) ok = all(block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag));
+          ok = by.all(block_wait(bar(kPFull + n % kPBufs), (n / kPBufs) & 1, abort_flag));
+          if (ok && j == lo && s > 0) ok = by.all(block_wait(bar(kOEmpty), (s - 1) & 1, abort_flag));
           const bool both = w.L > kBTile * j + kBPage;   // the tile has its second page
-          const uint64_t bd = smem_desc(sbase + Lay::kOffP + (n % kPBufs) * 16384, 8192, 1024);
+          const uint64_t bd = smem_desc(base + Lay::kOffP + (n % kPBufs) * 16384, 8192, 1024);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (ok) ok = all(block_wait(bar(kFull + kKSlots + slot), phase, abort_flag));
+            if (ok) ok = by.all(block_wait(bar(kFull + kKSlots + slot), phase, abort_flag));
             if (!ok) break;
             if (kWindow && gap.v >> 1 == j) {
               uint8_t* box = smem + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes + (gap.v & 1) * 8192;
@@ -338,28 +367,24 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
               __syncwarp();
             }
             tc_fence_after();
-            const uint64_t ad = smem_desc(sbase + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
-            const uint32_t d = tmem + Lay::kTmemO + 2 * kNR * h;
-            if (!kWindow || lane == 0) {
+            const uint64_t ad = smem_desc(base + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes, 8192, 1024);
+            const uint32_t d = tm + Lay::kTmemO + 2 * kNR * h;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
-                if (kk < 2 || both) umma_f8_ss(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == lo && kk == 0));
-              umma_commit(bar(kEmpty + kKSlots + slot));
-            }
+            for (int kk = 0; kk < 4; ++kk)     // 32 tokens a step: 4096 bytes, two steps a page
+              if (kk < 2 || both) by.mma(d, ad + 256 * kk, bd + 256 * kk, kIdescPV, !(j == lo && kk == 0));
+            by.commit(bar(kEmpty + kKSlots + slot));
             if (++slot == kVSlots) {
               slot = 0;
               phase ^= 1;
             }
           }
           if (!ok) break;
-          if (!kWindow || lane == 0) umma_commit(bar(kPvDone + (n & 1)));
+          by.commit(bar(kPvDone + (n & 1)));
         }
       }
-      if (!kWindow || lane == 0) {
-        if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
-        umma_commit(bar(kDrain));
-        wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
-      }
+      if (!ok) atomicOr(p.status, MFA_DEV_TIMEOUT);
+      by.commit(bar(kDrain));
+      wait_slow(bar(kDrain), 0, nullptr, kDrainLimitNs);
     }
     __syncwarp();
   } else if (warp == kBScaleWarp) {

@@ -73,8 +73,6 @@ struct TreeLayout {
   static_assert(kKSlots >= 2 && kOffRing % 1024 == 0, "layout");
 };
 
-// A value that is one for the warp, told to the compiler.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // Of four neighbouring lanes, each with four quarters of kWords words: lane l ends with quarter l of all four, in the
 // lanes' order.
 template <int kWords>
