@@ -1133,6 +1133,8 @@ struct BlockKind {
   const uint64_t* tree;
   uint32_t flag() const { return window != nullptr ? MFA_PLAN_WINDOW : is_tree ? MFA_PLAN_TREE : 0; }
   int rows() const { return is_tree ? kTreeRows : kBRows; }
+  // partial results that the workspace has room for (a tree's whole units leave none)
+  long long slots(long long partials, uint32_t flags) const { return is_tree && (flags & MFA_PLAN_UNIT_CLUSTERS) ? 0 : partials; }
 };
 
 static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const int32_t* host_seq_lens, int32_t max_seq_len,
@@ -1273,7 +1275,7 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
   plan->flags = flags | mode | kind.flag();
   plan->num_sms = num_sms;
   plan->total_tiles = static_cast<uint64_t>(W);
-  plan->workspace_bytes = block_workspace_bytes(partials, sh, pr->batch, pr->head_dim);
+  plan->workspace_bytes = block_workspace_bytes(kind.slots(partials, mode), sh, pr->batch, pr->head_dim);
   return MFA_OK;
 }
 
@@ -1286,6 +1288,7 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
   const BlockShape sh = block_shape(pr, kind.rows());
   const long long units = static_cast<long long>(pr->batch) * sh.readers;
   const bool clusters = (plan->flags & MFA_PLAN_UNIT_CLUSTERS) != 0;
+  const long long slots = kind.slots(plan->num_partials, plan->flags);
   if (plan->batch != pr->batch || plan->kv_dtype != pr->kv_dtype || plan->tokens_per_seq != pr->tokens_per_seq ||
       plan->num_ctas < 1 || (plan->flags & ~(MFA_PLAN_CHECK | MFA_PLAN_EARLY_METADATA | MFA_PLAN_EVEN_SPLIT | MFA_PLAN_UNIT_CLUSTERS)) !=
                                 kind.flag() ||
@@ -1293,7 +1296,7 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
       ((plan->flags & MFA_PLAN_EVEN_SPLIT) && (clusters || plan->max_tiles_per_cta < 1)) ||
       (clusters && (units == 0 || plan->num_ctas % units != 0 || plan->num_ctas / units > 8)) ||
       plan->num_partials != units + plan->num_ctas - 1 ||
-      plan->workspace_bytes != block_workspace_bytes(plan->num_partials, sh, pr->batch, pr->head_dim))
+      plan->workspace_bytes != block_workspace_bytes(slots, sh, pr->batch, pr->head_dim))
     return MFA_ERR_INVALID_ARG;
   if (pr->batch == 0) return MFA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
@@ -1329,8 +1332,8 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
   p.out = out;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws + kBWsHeader);
-  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(plan->num_partials, sh, pr->head_dim));
-  p.parts = reinterpret_cast<int2*>(ws + block_parts_offset(plan->num_partials, sh, pr->head_dim));
+  p.part_lse = reinterpret_cast<float*>(ws + block_lse_offset(slots, sh, pr->head_dim));
+  p.parts = reinterpret_cast<int2*>(ws + block_parts_offset(slots, sh, pr->head_dim));
   p.narrow = static_cast<double>(pr->batch) * sh.readers * plan->num_ctas *
                      (kBCostTile * ((static_cast<double>(pr->max_pages_per_seq) * kBPage + kBTile - 1) / kBTile) + kBCostUnit) <
                  4.0e9;

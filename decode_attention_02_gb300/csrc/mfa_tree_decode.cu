@@ -21,10 +21,19 @@
 // (448 is e4m3's largest), and falls when a tile's largest is under 2^-3 (to 24 under its highest at most),
 // so that what follows a far larger token keeps its precision; sums and O are fp32 and move by powers of two.
 //
+// Warps: a producer (TMA boxes of a page, K's and V's rings apart), the issuers of the two MMAs, which take
+// turns (the next tile's scores go before a tile's weights, so that the softmax has them in time), one that fetches
+// block scales, eight of softmax, and four that keep O: they move it when references do and write the results
+// while the softmax begins the next unit.
+//
 // What bounds it: a tile's products are 128 x 128 x d for S and as many for O, each twice (hi and lo), 2048
 // clocks of the tensor cores at d = 256; operands from shared memory are 192 KB of it and the tile's TMA
-// writes 64 KB, 2048 clocks at 128 bytes a clock.  The cache's bytes bound it where all rows of a key head
-// are one unit.
+// writes 64 KB, 2048 clocks at 128 bytes a clock.  The first tiles take 2200 clocks; under that load the card's
+// power brings its clock from 1.94 GHz to 1.4.  At d = 128 the softmax bounds it, 1900 clocks a tile, most of them
+// the conversions to eight bits and the maxima, which share one pipe.  A unit's beginning and end take 8 us beside
+// its tiles, a boundary inside a CTA's range 4 to 5, parts and their combine 5.  Eight trees of 32 nodes over 4096
+// tokens, 64 heads of 256 over one: 57.4 us (1.2 PFLOP/s of the products' 1.9 in bf16); seven ragged ones of 61
+// nodes 92.2 us; 48 of 8 nodes, 64 heads of 128 over four: 65.7 us (214 MB); one of 8 over 2048 tokens 18.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       const int L = sg.L, prefix = L - p.tokens;   // tokens before the tree (all nodes see them)
       const int node0 = sg.tg * p.unit_tokens;
       const int valid = p.group * min(p.unit_tokens, p.tokens - node0);
-      const uint64_t mask = row < valid ? __ldg(p.tree + static_cast<size_t>(sg.b) * p.tokens + node0 + row / p.group) : 0;
+      const uint64_t mask = row < valid ? p.tree[static_cast<size_t>(sg.b) * p.tokens + node0 + row / p.group] : 0;
       if (!wait_bar(bar(kQReady), s & 1, abort_flag)) aborted = true;
       const float inv = q_inv[(s & 1) * kTRows + row];
       float ref = 0.f, top = -INFINITY, most = -INFINITY;   // the reference, its highest, and what x + e may reach
@@ -745,7 +754,7 @@ template <int kDim, int kTeams>
 __global__ void __launch_bounds__(256, 6) mfa_tree_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kLanes = kDim / 8, kRows = 32 / kLanes * (8 / kTeams);   // lanes of a row, rows of a CTA
   constexpr int kAhead = 2;                                             // parts that are loaded together
-  __shared__ float other[kTeams > 1 ? kTeams - 1 : 1][kTeams > 1 ? 32 : 1][11];   // (odd pitch: no bank conflicts)
+  __shared__ float other[kTeams > 1 ? 8 : 1][kTeams > 1 ? 32 : 1][11];   // of the warps (odd pitch: no bank conflicts)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp % kTeams;
   const int row = blockIdx.y * kRows + warp / kTeams * (32 / kLanes) + lane / kLanes, el = lane % kLanes * 8;
   const int pos = blockIdx.x, b = pos % p.batch, r = pos / p.batch;
@@ -788,7 +797,7 @@ __global__ void __launch_bounds__(256, 6) mfa_tree_combine_kernel(const __grid_c
   }
   if constexpr (kTeams > 1) {
     if (team > 0) {
-      float* mine = other[team - 1][lane];
+      float* mine = other[warp][lane];
 #pragma unroll
       for (int i = 0; i < 8; ++i) mine[i] = acc[i];
       mine[8] = sum;
@@ -797,8 +806,8 @@ __global__ void __launch_bounds__(256, 6) mfa_tree_combine_kernel(const __grid_c
     __syncthreads();
     if (team > 0) return;
 #pragma unroll 1
-    for (int x = 0; x < kTeams - 1; ++x) {
-      const float* theirs = other[x][lane];
+    for (int x = 1; x < kTeams; ++x) {
+      const float* theirs = other[warp + x][lane];
       const float2 f = add(theirs[9]);
       sum = fmaf(sum, f.x, f.y * theirs[8]);
 #pragma unroll
@@ -828,14 +837,13 @@ __global__ void __launch_bounds__(256, 6) mfa_tree_combine_kernel(const __grid_c
 }
 
 cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int ctas, int head_dim, cudaLaunchConfig_t cfg) {
-  const bool many = ctas > 8 * units;   // parts of a unit
-  const int rows = 256 / head_dim * (many ? 1 : 8);
+  const int teams = ctas > 32 * units ? 8 : ctas > 4 * units ? 4 : 1, rows = 256 / head_dim * (8 / teams);   // by a unit's parts
   cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>((p.rows8 + rows - 1) / rows), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   BlockDecodeFn fn;
-  if (head_dim == 256) fn = many ? mfa_tree_combine_kernel<256, 8> : mfa_tree_combine_kernel<256, 1>;
-  else fn = many ? mfa_tree_combine_kernel<128, 8> : mfa_tree_combine_kernel<128, 1>;
+  if (head_dim == 256) fn = teams == 8 ? mfa_tree_combine_kernel<256, 8> : teams == 4 ? mfa_tree_combine_kernel<256, 4> : mfa_tree_combine_kernel<256, 1>;
+  else fn = teams == 8 ? mfa_tree_combine_kernel<128, 8> : teams == 4 ? mfa_tree_combine_kernel<128, 4> : mfa_tree_combine_kernel<128, 1>;
   return cudaLaunchKernelEx(&cfg, fn, p);
 }
 

@@ -74,3 +74,11 @@ def test_bad_pointers_are_refused(lib):
 def test_units_of_at_most_128_rows(lib, heads, kv_heads, tokens, units):
     pr = problem(batch=1, num_q_heads=heads, num_kv_heads=kv_heads, head_dim=128, tokens_per_seq=tokens)
     assert mfa.mfa_tree_decode_plan(pr, 64, [1000], num_sms=8).total_tiles == 8 * units
+
+
+def test_whole_units_need_no_room_for_parts(lib):
+    pr = problem(batch=60, tokens_per_seq=64)
+    plan = mfa.mfa_tree_decode_plan(pr, 64, [1000] * 60, num_sms=152)
+    assert plan.flags & mfa.MFA_PLAN_UNIT_CLUSTERS and plan.num_ctas == 60 * 32 and plan.workspace_bytes < 1 << 16
+    few = problem(batch=2, tokens_per_seq=64)
+    assert not mfa.mfa_tree_decode_plan(few, 64, [4000] * 2, num_sms=152).flags & mfa.MFA_PLAN_UNIT_CLUSTERS
