@@ -169,6 +169,8 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kKSlots = Lay::kKSlots, kVSlots = Lay::kVSlots, kPBufs = Lay::kPBufs;
   constexpr int kSoftmaxWarps = 4 * Lay::kWgs;
   static_assert(kC == 8 || kC == 16, "rows of a warpgroup");
+  // q's lo parts have columns of their own: windowed instances take them larger, so that small elements are exact
+  constexpr int kLoFactor = kWindow ? 16 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -503,7 +505,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              split_e4m3(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
+              split_e4m3<kLoFactor>(__uint_as_float(e[x] << 16) * up, __uint_as_float(e[x] & 0xFFFF0000u) * up, hi[x], lo[x]);
             const int byte = 8 * (i8 + 8 * k) % 128;   // chunk of a half's 128-byte row
             uint8_t* dst = smem + Lay::kOffQ + (k / 2) * (2 * kNR * 128) + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
@@ -528,8 +530,12 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 #pragma unroll
       for (int i = 0; i < kC; i += 2) {
         float a, b;
-        unpack_f32x2(add_f32x2(pack_f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])),
-                               pack_f32x2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))), a, b);
+        const uint64_t h2 = pack_f32x2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+        const uint64_t l2 = pack_f32x2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]));
+        if constexpr (kLoFactor == 1)
+          unpack_f32x2(add_f32x2(h2, l2), a, b);
+        else
+          unpack_f32x2(fma_f32x2(l2, pack_f32x2(1.f / kLoFactor, 1.f / kLoFactor), h2), a, b);
         sr[i] = __float_as_uint(a);
         sr[i + 1] = __float_as_uint(b);
       }

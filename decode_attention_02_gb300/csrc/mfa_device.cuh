@@ -140,12 +140,15 @@ __device__ __forceinline__ uint32_t pack_e4m3_sat(float lo, float hi) {
 // the 7 magnitude bits at bit 20 of an fp32 word times 2^120, gives the same bits, but the
 // conversion measured faster end to end -- finishing a segment's q split earlier moves the
 // CTAs' load streams into a worse phase.)
+// kLoFactor, a power of two up to 16: lo that many times larger, and elements down to 2^-9 / kLoFactor of the
+// largest exact (|x - hi| <= 4).
+template <int kLoFactor = 1>
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_e4m3_sat(x0, x1);
   uint32_t back;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(static_cast<uint16_t>(hi)));
-  lo = pack_e4m3_sat(x0 - __half2float(__ushort_as_half(static_cast<unsigned short>(back))),
-                     x1 - __half2float(__ushort_as_half(static_cast<unsigned short>(back >> 16))));
+  lo = pack_e4m3_sat((x0 - __half2float(__ushort_as_half(static_cast<unsigned short>(back)))) * kLoFactor,
+                     (x1 - __half2float(__ushort_as_half(static_cast<unsigned short>(back >> 16)))) * kLoFactor);
 }
 
 }  // namespace mfa

@@ -62,9 +62,13 @@ constexpr int kTRegsRoles = 80, kTRegsSoftmax = 168, kTRegsOut = 96;
 static_assert(kTRegsRoles + kTWgs * kTRegsSoftmax + kTRegsOut <= 512, "registers");
 // shared memory behind the rings: segments, scratch, barriers (the last 512 bytes)
 constexpr int kTMisc = 17408;
+constexpr int kTFin = (kTWgs + 1) * kTRows + 4;   // floats of a segment's sums, references and scale
 constexpr int kTurnStep = 2;
 constexpr float kTTop = 4.f, kTMost = 8.75f, kTLeast = -2.f, kTDepth = 24.f;   // exponents of P, see above
-constexpr float kTScaleDown = 0x1p-24f, kTScaleUp = 0x1p24f;   // value scales are taken smaller: p = 2^(x - R) stays in range
+// Value scales are taken 2^-24 times smaller, so that p = 2^(x - R) stays in range for scales up to 2^127; and then, where
+// a segment's first scale is small, up to 2^24 times larger again, so that x - R is a number of few digits before its
+// point (with a first scale of 2^-6 and the factor alone: 2^-19 off in every exponent).
+constexpr float kTScaleDown = 0x1p-24f, kTScaleUp = 0x1p24f;
 constexpr float kTEMin = -50.f - 24.f;   // and their logarithms at least this (smaller scales count as 2^-50)
 
 template <int kDim>
@@ -129,14 +133,14 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   BlockSegment* seg = reinterpret_cast<BlockSegment*>(misc);
   float* red = reinterpret_cast<float*>(misc + sizeof(BlockSegment) * kBMaxSeg);   // [2 tiles][warpgroups][128 rows]
   float* alpha = red + 2 * kTWgs * kTRows;                          // [2 tiles][128] what O is multiplied by
-  float* fin = alpha + 2 * kTRows;                                  // [2 segments][sums of the warpgroups, reference][128]
-  float* q_inv = fin + 2 * (kTWgs + 1) * kTRows;                         // [2 segments][128] what undoes a row's q scaling
+  float* fin = alpha + 2 * kTRows;                                  // [2 segments][sums of the warpgroups, reference][128], scale
+  float* q_inv = fin + 2 * kTFin;                         // [2 segments][128] what undoes a row's q scaling
   int* row_off = reinterpret_cast<int*>(q_inv + 2 * kTRows);        // [128] element offset of a row's output
   int* moved = row_off + kTRows;                                    // [2 tiles][4 quarters of the rows] whether it is
   float4* meta = reinterpret_cast<float4*>(moved + 8);       // [2 tiles][2 pages][4 blocks] {K, V scales, log2 of V's}
   int* ctl = reinterpret_cast<int*>(meta + 16);                     // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
-  static_assert(sizeof(BlockSegment) * kBMaxSeg + (2 * kTWgs + 2 + 2 * (kTWgs + 1) + 3) * kTRows * 4 + 8 * 4 + 16 * 16 + 16 + 512 <= kTMisc, "misc");
+  static_assert(sizeof(BlockSegment) * kBMaxSeg + (2 * kTWgs + 2 + 3) * kTRows * 4 + 2 * kTFin * 4 + 8 * 4 + 16 * 16 + 16 + 512 <= kTMisc, "misc");
   const uint32_t bars = sbase + Lay::kOffMisc + kTMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // slots: K's, then V's
@@ -466,8 +470,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           }
 #pragma unroll
           for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          int sig = 0;   // the row's largest |q| goes to [64, 128)
-          if (m > 0.f) sig = min(126, max(-126, 6 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
+          int sig = 0;   // the row's largest |q| goes to [128, 256): what is under 2^-10 of it errs by 2^-17 of it
+          if (m > 0.f) sig = min(126, max(-126, 7 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
           const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
@@ -499,6 +503,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       const uint64_t mask = row < valid ? p.tree[static_cast<size_t>(sg.b) * p.tokens + node0 + row / p.group] : 0;
       if (!wait_bar(bar(kQReady), s & 1, abort_flag)) aborted = true;
       const float inv = q_inv[(s & 1) * kTRows + row];
+      float shift = 0.f, up = 1.f;   // see kTScaleDown
       float ref = 0.f, top = -INFINITY, most = -INFINITY;   // the reference, its highest, and what x + e may reach
       uint64_t l2 = 0;                                      // the row's sum over this page's tokens, in two parts
       for (int j = sg.lo; j < sg.hi; ++j, ++n) {
@@ -508,13 +513,17 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         const uint32_t at = tmem + Lay::kTmemS + kBTile * (n & 1) + 64 * wg + lane_base;
         tmem_ld32(at, sr[0]);
         tmem_ld32(at + 32, sr[1]);
+        if (j == sg.lo) {
+          shift = fminf(fmaxf(-rintf(meta[(n & 1) * 8].z), 0.f), 24.f);
+          up = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(shift)) << 23);
+        }
         float a[4], sv[4], e[4];   // by 16 tokens: key scale with the row's, value scale and its exponent
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float4 sc = meta[(n & 1) * 8 + wg * 4 + ((16 * g) >> p.log_scale)];
           a[g] = sc.x * inv;
-          sv[g] = sc.y;
-          e[g] = sc.z;
+          sv[g] = sc.y * up;
+          e[g] = sc.z + shift;
         }
         tmem_ld_wait(sr[0]);
         tmem_ld_wait(sr[1]);
@@ -609,9 +618,12 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
         if (s >= 2 && !wait_bar(bar(kFinEmpty + (s & 1)), ((s >> 1) - 1) & 1, abort_flag)) aborted = true;
         float l0, l1;
         unpack_f32x2(l2, l0, l1);
-        float* mine = fin + (s & 1) * ((kTWgs + 1) * kTRows) + row;
+        float* mine = fin + (s & 1) * kTFin + row;
         mine[wg * kTRows] = l0 + l1;
-        if (wg == 0) mine[kTWgs * kTRows] = ref;
+        if (wg == 0) {
+          mine[kTWgs * kTRows] = ref;
+          if (row == 0) mine[(kTWgs + 1) * kTRows] = kTScaleUp / up;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kFinal + (s & 1)));
       }
@@ -670,15 +682,15 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
       }
       if (ok) ok = wait_all(bar(kFinal + (s & 1)), (s >> 1) & 1, abort_flag);
       if (!ok) break;
-      const float* mine = fin + (s & 1) * ((kTWgs + 1) * kTRows) + row;
-      const float sum = mine[0] + mine[kTRows], ref = mine[kTWgs * kTRows];
+      const float* mine = fin + (s & 1) * kTFin;
+      const float sum = mine[row] + mine[kTRows + row], ref = mine[kTWgs * kTRows + row], unit = mine[(kTWgs + 1) * kTRows];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kFinEmpty + (s & 1)));
       ok = wait_all(bar(kPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const int node0 = sg.tg * p.unit_tokens, valid = p.group * min(p.unit_tokens, p.tokens - node0);
-      const float back = sum == 0.f ? 0.f : kTScaleUp / sum;   // (a row that sees nothing: zeros)
+      const float back = sum == 0.f ? 0.f : unit / sum;   // (a row that sees nothing: zeros)
       const bool whole = sg.slot == -1;
       const size_t first = (static_cast<size_t>(sg.b) * p.tokens + node0) * p.heads + static_cast<size_t>(sg.kvh) * p.group;
       float* part = p.part_o + static_cast<size_t>(max(sg.slot, 0)) * p.rows8 * kDim;

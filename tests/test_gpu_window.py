@@ -100,7 +100,10 @@ def test_a_window_over_the_whole_sequence_is_the_decode_without():
     kw = dict(num_q_heads=64, head_dim=256, scale_tokens=16, host_seq_lens=c.seq_lens.tolist())
     a = mfa.BlockDecoder(4, c.columns, c.pages, **kw)(*d)
     b = mfa.BlockDecoder(4, c.columns, c.pages, window=1300, **kw)(*d)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    want = ref.decode(c)
+    for got in (a, b):   # (not the same bits: small elements of q are more exact with a window)
+        seen.check(*got, want)
+    assert torch.equal(want[0], expect(c, 1300, 0)[0])
 
 
 def test_long_contexts_and_bad_pages():
