@@ -11,8 +11,18 @@
 // the registers of a group of up to 32 lanes (a lane: 8 elements of a pair's first half and the 8 of
 // its second, as they lie in memory), so that its sums are a few shuffles and nothing is read twice.
 // A CTA turns all heads of a row: the row's angles are computed once and shared.  A group keeps to one
-// side, q or k, so that a lane's weights stay in its registers, multiplied with the angles' cosines and
-// sines in the forward pass.  All sums are fp32; outputs are rounded once.
+// side, q or k, and multiplies its weights with the angles' cosines and sines once a row in the forward
+// pass.  All sums are fp32; outputs are rounded once.
+//
+// Measured, bf16 unless said (the bytes at the copy rate of 6.7 TB/s in brackets):
+//   8191 rows of 65 heads of 256, three axes: 88 us, 6.2 TB/s (82); 128 such rows 8.2 us, launch and one
+//   chain of loads: positions and angles, the elements, two sums;
+//   its gradient 157 us, 5.2 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 31 us (16).
+// What bounds the gradient: issue slots as much as memory, some 13 instructions an element beside the loads.
+// The steps that carried it, the prompt / its gradient: plain loads, one CTA on an SM 188 / 272; arithmetic
+// in pairs, two CTAs 108 / 240; copies ahead into shared memory, free of bank conflicts, 105 / 203; angles
+// by a warp of their own 88 / -; values read from shared memory again in place of kept, and the CTA's
+// meetings one in four rows, - / 157.  Asking L2 for the next rows gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

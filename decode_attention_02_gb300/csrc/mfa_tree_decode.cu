@@ -17,8 +17,8 @@
 //
 // P: hi keeps four bits and lo three of what is left: off by 2^-7 of itself at most, where it is at least
 // 2^-6; hi's subnormals and lo's go on to 2^-17.  A row's reference R, P = 2^(x + e - R) with x its score and
-// e its value scale's logarithm, is set so that a tile's largest P is 2^2.  It rises when one would pass 2^8.75
-// (448 is e4m3's largest), and falls when a tile's largest is under 2^-3 (to 24 under its highest at most),
+// e its value scale's logarithm, is set so that a tile's largest P is 2^4.  It rises when one would pass 2^8.75
+// (448 is e4m3's largest), and falls when a tile's largest is under 2^-2 (to 24 under its highest at most),
 // so that what follows a far larger token keeps its precision; sums and O are fp32 and move by powers of two.
 //
 // Warps: a producer (TMA boxes of a page, K's and V's rings apart), the issuers of the two MMAs, which take
