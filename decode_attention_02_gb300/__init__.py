@@ -610,11 +610,27 @@ class _OnDevice:
         self._current = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         self._home = self._current(self._index)   # the stream that the handle's own buffers are allocated on
 
-    def _keep(self, stream, tensors) -> None:
-        """Memory that a call on ``stream`` uses: not given out again before that is done."""
+    def _stream(self, stream):
+        """A torch stream of a stream or its handle."""
         cuda = self._torch.cuda
         if isinstance(stream, int):   # (0 and 1 both name the default stream)
-            stream = cuda.ExternalStream(stream, device=self.device) if stream > 1 else cuda.default_stream(self.device)
+            return cuda.ExternalStream(stream, device=self.device) if stream > 1 else cuda.default_stream(self.device)
+        return stream
+
+    def _new(self, shape, dtype, stream):
+        """Memory that a call on ``stream`` writes.  (Of that stream's: what the current stream has freed may still be
+        written by its work.  The caller may use and drop it on the current stream.)"""
+        torch = self._torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self._stream(stream)):
+            x = torch.empty(shape, dtype=dtype, device=self.device)
+        x.record_stream(torch.cuda.current_stream(self._index))
+        return x
+
+    def _keep(self, stream, tensors) -> None:
+        """Memory that a call on ``stream`` uses: not given out again before that is done."""
+        stream = self._stream(stream)
         for x in tensors:
             if x is not None:
                 x.record_stream(stream)
@@ -679,6 +695,7 @@ class BlockDecoder(_OnDevice):
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
         self._refs = (ctypes.byref(self.plan), ctypes.byref(self.problem))
+        self._own = (self.workspace,)   # buffers that calls use
         self._run = self._decode_call()
         self._append_ref = self._refs[1]
         rows = batch * tokens_per_seq
@@ -733,11 +750,11 @@ class BlockDecoder(_OnDevice):
             _refuse(i, ("q", q, bf16, self._q_shape), ("seq_lens", seq_lens, i32, self._batch_shape),
                     *self._cache_wants(k_cache, v_cache, k_scale, v_scale, block_table))
         if out is None:
-            out = self._torch.empty(self._q_shape, dtype=self._out_dtype, device=self.device)
+            out = self._new(self._q_shape, self._out_dtype, stream)
         elif not _fits(out, self._out_dtype, self._q_shape, i):
             _refuse(i, ("out", out, self._out_dtype, self._q_shape))
         if lse is None:
-            lse = self._torch.empty(self._lse_shape, dtype=f32, device=self.device)
+            lse = self._new(self._lse_shape, f32, stream)
         elif not _fits(lse, f32, self._lse_shape, i):
             _refuse(i, ("lse", lse, f32, self._lse_shape))
         before = self._take_status(stream) if self._unreported else 0
@@ -769,7 +786,7 @@ class BlockDecoder(_OnDevice):
         self._call(function, where,
                    (*head, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                     block_table.data_ptr(), seq_lens.data_ptr(), *[x.data_ptr() for x in more], out.data_ptr(),
-                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream, (self.workspace,),
+                    lse.data_ptr(), self.workspace.data_ptr(), self.plan.workspace_bytes), stream, self._own,
                    (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *more, out, lse))
 
     def append(self, k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets=None,
@@ -805,7 +822,7 @@ class BlockDecoder(_OnDevice):
                    (self._append_ref, self.scale_tokens, k_new.data_ptr(), v_new.data_ptr(), rows,
                     None if offsets is None else offsets.data_ptr(), max_new, positions.data_ptr(),
                     block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                    v_scale.data_ptr(), status), stream, (self.workspace,),
+                    v_scale.data_ptr(), status), stream, self._own,
                    (k_new, v_new, offsets, positions, block_table, k_cache, v_cache, k_scale, v_scale, device_status))
 
 
@@ -835,6 +852,7 @@ class TreeDecoder(BlockDecoder):
             self._offsets = torch.arange(0, (batch + 1) * tree_tokens, tree_tokens, dtype=torch.int32, device=self.device)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()   # (the first call may be on another stream)
+        self._own = (self.workspace, self._offsets)
 
     def _split(self, *args) -> MfaPlan:
         return mfa_tree_decode_plan(self.problem, self.scale_tokens, *args)
@@ -858,8 +876,6 @@ class TreeDecoder(BlockDecoder):
                 raise ValueError(f"k_new: expected {self._tree_shape.numel()} rows, {max_new} a sequence, got {k_new.shape[0]}")
         super().append(k_new, v_new, positions, block_table, k_cache, v_cache, k_scale, v_scale, offsets, max_new,
                        device_status, stream)
-        if stream is not None and offsets is self._offsets:
-            self._keep(stream, (offsets,))
 
 
 class Rope(_OnDevice):
@@ -899,7 +915,7 @@ class Rope(_OnDevice):
             raise ValueError(f"{name}: each row's heads must lie side by side, got strides {t.stride()}")
         return a if t.shape[0] > 1 else line   # (a single row has no stride of its own)
 
-    def _rows(self, x, out, name: str, rows: int, dtype) -> MfaRopeRows:
+    def _rows(self, x, out, name: str, rows: int, dtype, stream):
         """x and its output (x's shape; None: a new tensor) as the library takes them, and the output."""
         shape, d = x.shape, self.head_dim
         if len(shape) != 3 or shape[0] != rows or shape[2] != d or x.dtype is not dtype or x.get_device() != self._index:
@@ -907,7 +923,7 @@ class Rope(_OnDevice):
                              f"{tuple(shape)} on {x.device}")
         line = shape[1] * d
         if out is None:
-            out = self._torch.empty(shape, dtype=dtype, device=self.device)
+            out = self._new(shape, dtype, stream)
         elif out is not x and (out.shape != shape or out.dtype is not dtype or out.get_device() != self._index):
             raise ValueError(f"{name}_out: expected {dtype} {tuple(shape)} on {self.device}, got {out.dtype} "
                              f"{tuple(out.shape)} on {out.device}")
@@ -929,9 +945,9 @@ class Rope(_OnDevice):
             _refuse(self._index, ("positions", positions, self._torch.int32, (self.axes, rows)))
         rq = rk = None
         if q is not None:
-            rq, q_out = self._rows(q, q_out, "q", rows, dtype)
+            rq, q_out = self._rows(q, q_out, "q", rows, dtype, stream)
         if k is not None:
-            rk, k_out = self._rows(k, k_out, "k", rows, dtype)
+            rk, k_out = self._rows(k, k_out, "k", rows, dtype, stream)
         self._call(self._lib.mfa_rope_run, "mfa_rope_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, 1 if inverse else 0,
                     rq, rk), stream, (self.table,), (q, k, positions, q_out, k_out))
@@ -983,22 +999,22 @@ class NormRope(Rope):
         rows, dtype, kind, norm = self._start(q, k, q_weight, k_weight, positions)
         rq = rk = None
         if q is not None:
-            rq, q_out = self._rows(q, q_out, "q", rows, dtype)
+            rq, q_out = self._rows(q, q_out, "q", rows, dtype, stream)
         if k is not None:
-            rk, k_out = self._rows(k, k_out, "k", rows, dtype)
+            rk, k_out = self._rows(k, k_out, "k", rows, dtype, stream)
         self._call(self._lib.mfa_norm_rope_run, "mfa_norm_rope_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, norm, rq, rk), stream,
                    (self.table,), (q, k, q_weight, k_weight, positions, q_out, k_out))
         return q_out, k_out
 
-    def _grad_rows(self, x, dy, dx, name: str, rows: int, dtype):
+    def _grad_rows(self, x, dy, dx, name: str, rows: int, dtype, stream):
         """x, dy and dx (x's shape; None: a new tensor) as the library takes them, and dx."""
         if dy is None:
             raise ValueError(f"d{name}: expected the gradient of {name}'s output")
         if dy.shape != x.shape or dy.dtype is not dtype or dy.get_device() != self._index:
             raise ValueError(f"d{name}: expected {dtype} {tuple(x.shape)} on {self.device}, got {dy.dtype} {tuple(dy.shape)} "
                              f"on {dy.device}")
-        r, dx = self._rows(x, dx, name, rows, dtype)
+        r, dx = self._rows(x, dx, name, rows, dtype, stream)
         line = x.shape[1] * self.head_dim
         return MfaNormGradRows(r.data_in, dy.data_ptr(), r.data_out, r.in_stride, self._row_stride(dy, "d" + name, line),
                                r.out_stride, r.heads), dx
@@ -1011,13 +1027,13 @@ class NormRope(Rope):
         rows, dtype, kind, norm = self._start(q, k, q_weight, k_weight, positions)
         rq = rk = wq = wk = None
         if q is not None:
-            rq, q_grad = self._grad_rows(q, dq, q_grad, "q", rows, dtype)
-            wq = torch.empty(self._weight_shape, dtype=torch.float32, device=self.device)
+            rq, q_grad = self._grad_rows(q, dq, q_grad, "q", rows, dtype, stream)
+            wq = self._new(self._weight_shape, torch.float32, stream)
         if k is not None:
-            rk, k_grad = self._grad_rows(k, dk, k_grad, "k", rows, dtype)
-            wk = torch.empty(self._weight_shape, dtype=torch.float32, device=self.device)
+            rk, k_grad = self._grad_rows(k, dk, k_grad, "k", rows, dtype, stream)
+            wk = self._new(self._weight_shape, torch.float32, stream)
         size = 8 * self.head_dim * MFA_NORM_ROPE_GRAD_PARTS
-        scratch = torch.empty(size, dtype=torch.uint8, device=self.device)
+        scratch = self._new(size, torch.uint8, stream)
         self._call(self._lib.mfa_norm_rope_grad_run, "mfa_norm_rope_grad_run",
                    (self._config_ref, self.table.data_ptr(), positions.data_ptr(), rows, kind, norm, rq, rk,
                     None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), scratch.data_ptr(), size),
