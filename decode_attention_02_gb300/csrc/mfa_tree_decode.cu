@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           for (int i = 0; i < 4; ++i) {
             const int r = row - (lane & 3) + i;
             if (r < valid)
-              *reinterpret_cast<uint4*>(out + row_off[r] * 2 + c * 2 + (lane & 3) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(row_off[r]) * 2 + c * 2 + (lane & 3) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
         } else {   // (parts: rows as they are in the outputs)
           exchange_quarters<8>(o);
