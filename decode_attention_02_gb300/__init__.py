@@ -683,7 +683,8 @@ class BlockDecoder(_OnDevice):
         self.scale_tokens = int(scale_tokens)
         if window is None and sinks:
             raise ValueError("sinks: first tokens stay visible beside a window, and there is none")
-        self.window = None if window is None else MfaWindow(int(window), int(sinks))
+        # (the library takes 32 bits, and cuts both to the table's tokens)
+        self.window = None if window is None else MfaWindow(*(max(-1, min(int(x), 2 ** 31 - 1)) for x in (window, sinks)))
         self.problem = make_problem(batch, max_pages_per_seq, num_blocks, MFA_KV_FP8_E4M3, softmax_scale,
                                     num_q_heads=num_q_heads, head_dim=head_dim, out_dtype=out_dtype,
                                     tokens_per_seq=tokens_per_seq, num_kv_heads=num_kv_heads)

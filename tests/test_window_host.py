@@ -105,3 +105,21 @@ def test_sinks_without_a_window_are_refused(monkeypatch):
     monkeypatch.setattr(mfa._OnDevice, "__init__", lambda self, device: setattr(self, "_torch", torch))
     with pytest.raises(ValueError, match="sinks"):
         mfa.BlockDecoder(1, 1, 1, sinks=4)
+
+
+@pytest.mark.parametrize("window, sinks, taken", [(2 ** 32 + 1, 2 ** 33 + 2, (2 ** 31 - 1, 2 ** 31 - 1)),
+                                                  (-2 ** 32 + 5, -2 ** 32 + 1, (-1, -1)), (7, 3, (7, 3))])
+def test_windows_past_32_bits_stay_what_they_mean(monkeypatch, window, sinks, taken):
+    """As large as the library takes (the whole sequence), or refused by it; not what is left of them in 32 bits."""
+    class Stop(Exception):
+        pass
+
+    def stop(*args, **kw):
+        raise Stop
+
+    monkeypatch.setattr(mfa._OnDevice, "__init__", lambda self, device: setattr(self, "_torch", torch))
+    monkeypatch.setattr(mfa, "make_problem", stop)
+    dec = mfa.BlockDecoder.__new__(mfa.BlockDecoder)
+    with pytest.raises(Stop):
+        dec.__init__(1, 1, 1, window=window, sinks=sinks)
+    assert (dec.window.tokens, dec.window.sinks) == taken
