@@ -41,7 +41,6 @@ namespace mfa {
 
 constexpr int kNormThreads = 288;        // of a CTA that have heads, at most; with a warp of angles two CTAs on an SM
 constexpr int kNormAnyThreads = 256;     // of a CTA of the path for any shape
-constexpr int kNormAnyEach = kRopeMaxDim / 32;   // its elements a lane
 
 struct NormSide {
   const void* x;
@@ -57,6 +56,7 @@ struct NormParams {
   const mfa_rope_pair* table;
   const int32_t* positions;
   int rows, axes, pairs, head_dim;
+  int angles;           // pairs, and those that do not turn of the last adjacent ones' unit
   int turned_units, units, log_lanes;   // wide path: a head's units, lanes of its group
   int half;                             // pairing, for any shape
   int w_f32;
@@ -91,9 +91,9 @@ __device__ __forceinline__ void row_angles(const NormParams& p, long long row, i
   int32_t pos[MFA_ROPE_MAX_AXES];
 #pragma unroll
   for (int x = 0; x < MFA_ROPE_MAX_AXES; ++x) pos[x] = x < p.axes ? p.positions[static_cast<long long>(x) * p.rows + row] : 0;
-  for (int i = tid; i < p.pairs; i += threads) {
-    float s, c;
-    rope_angle(p.table, i, pos, s, c);
+  for (int i = tid; i < p.angles; i += threads) {
+    float s = 0.f, c = 1.f;
+    if (i < p.pairs) rope_angle(p.table, i, pos, s, c);
     cs[0][place(i)] = c;
     cs[1][place(i)] = s;
   }
@@ -127,8 +127,12 @@ struct NormPlace {
     h0 = (on_q ? slot : slot - p.q.slots) + blockIdx.y * slots;
     step = slots * gridDim.y;
     mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & ~(lanes - 1));
-    a0 = turned ? 8 * u : 2 * p.pairs + 8 * (u - p.turned_units);
+    a0 = start(p, u);
     b0 = kHalf && turned ? a0 + p.pairs : a0;
+  }
+  // the first element of unit x
+  static __device__ __forceinline__ int start(const NormParams& p, int x) {
+    return kHalf && x >= p.turned_units ? 2 * p.pairs + 8 * (x - p.turned_units) : 8 * x;
   }
 };
 
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
     const bool turned = u < p.turned_units;
     const bool there = side.heads > 0 && u < p.units && (half == 0 || (kHalf && turned));
     sw[on_k][half][(e / 4 * lanes + u) * 4 + (e & 3)] =
-        there ? norm_weight(p, side, (turned ? 8 * u : 2 * p.pairs + 8 * (u - p.turned_units)) + half * p.pairs + e) : 0.f;
+        there ? norm_weight(p, side, at.start(p, u) + half * p.pairs + e) : 0.f;
   }
   // half pairing: a lane's eight pairs in two vectors; adjacent: its four in one
   auto place = [&](int i) { return kHalf ? ((i >> 2 & 1) * lanes + (i >> 3)) * 4 + (i & 3) : i; };
@@ -443,9 +447,14 @@ __global__ void __launch_bounds__(256) mfa_norm_rope_weights_kernel(const __grid
   grid_dep_wait();
   grid_dep_launch();
   const int el = blockIdx.x * 8 + (threadIdx.x & 7), part = threadIdx.x >> 3;
-  float v = 0.f;
-  if (el < 2 * p.head_dim)
-    for (int i = part; i < p.parts; i += 32) v += p.partial[static_cast<size_t>(i) * 2 * p.head_dim + el];
+  float of[MFA_NORM_ROPE_GRAD_PARTS / 32], v = 0.f;   // (all loads on their way at once)
+#pragma unroll
+  for (int k = 0; k < MFA_NORM_ROPE_GRAD_PARTS / 32; ++k) {
+    const int i = part + 32 * k;
+    of[k] = el < 2 * p.head_dim && i < p.parts ? p.partial[static_cast<size_t>(i) * 2 * p.head_dim + el] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < MFA_NORM_ROPE_GRAD_PARTS / 32; ++k) v += of[k];
   red[part][threadIdx.x & 7] = v;
   __syncthreads();
   if (part != 0 || el >= 2 * p.head_dim) return;
@@ -458,10 +467,11 @@ __global__ void __launch_bounds__(256) mfa_norm_rope_weights_kernel(const __grid
 
 // ------------------------------------------------------------------ any shape
 //
-// Heads of odd sizes, unaligned rows: a warp a head, a lane its every 32nd element and that element's
-// partner in the pair.
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(const __grid_constant__ NormParams p) {
+// Heads of odd sizes, half pairing of pairs that are no eights, unaligned rows: a warp a head, a lane its every 32nd
+// element and that element's partner in the pair.  Bound by its loads' latency: 2000 rows of 26 heads of 256, 100
+// elements turned, half pairing: gradient 74 us of 12 (with registers for heads of 512, one CTA on an SM, 184).
+template <typename T, bool kGrad, int kEach>
+__global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_rope_any_kernel(const __grid_constant__ NormParams p) {
   __shared__ __align__(16) float cs[2][2][kRopeMaxDim / 2];
   extern __shared__ float red[];   // gradient: [warps][head_dim]
   grid_dep_wait();
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(cons
   const NormSide& side = on_q ? p.q : p.k;
   const int h0 = on_q ? warp : warp - p.q.slots, step = side.slots;
   const int r2 = 2 * p.pairs;
-  float dw[kNormAnyEach] = {};
+  float dw[kEach] = {};
   int buffer = 0;
 #pragma unroll 1
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
@@ -483,9 +493,9 @@ __global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(cons
 #pragma unroll 1
     for (long long h = h0; h < side.heads; h += step) {
       const T* x = xs + h * p.head_dim;
-      float own[kNormAnyEach], out[kNormAnyEach], sum[2] = {0.f, 0.f};
+      float own[kEach], out[kEach], sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kNormAnyEach; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         const int e = lane + 32 * i;
         own[i] = out[i] = 0.f;
         if (e >= p.head_dim) continue;
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(cons
       const float r = rsqrtf(fmaf(sum[0], p.inv_dim, p.eps)), m = r * r * sum[1] * p.inv_dim;
       T* to = dst + h * p.head_dim;
 #pragma unroll
-      for (int i = 0; i < kNormAnyEach; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         const int e = lane + 32 * i;
         if (e >= p.head_dim) continue;
         if constexpr (kGrad) {
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) mfa_norm_rope_any_kernel(cons
   if constexpr (kGrad) {
     grid_dep_launch();
 #pragma unroll
-    for (int i = 0; i < kNormAnyEach; ++i) {
+    for (int i = 0; i < kEach; ++i) {
       const int e = lane + 32 * i;
       if (e < p.head_dim) red[warp * p.head_dim + e] = dw[i];
     }
@@ -568,11 +578,12 @@ static bool wide_norm_side(const NormSide& s, bool grad) {
                           (!grad || (aligned(s.dy, 16) && s.dy_stride % 8 == 0)));
 }
 
-// Groups of lanes (or warps) for the sides' heads: as many as heads of `each` a time fill, or, of what a CTA
-// has room for, a share by their heads.
-static void norm_slots(NormParams& p, int room, int each) {
+// Groups of lanes (or warps) for the sides' heads: one each, or, of what a CTA has room for, a share by their heads.
+// (Fewer, with four heads each, leave CTAs of 17 groups of 8 lanes: 8191 rows of 68 heads of 128 66 us against 55, their
+// gradient 121 against 96.)
+static void norm_slots(NormParams& p, int room) {
   const int hq = p.q.heads, hk = p.k.heads;
-  int nq = (hq + each - 1) / each, nk = (hk + each - 1) / each;
+  int nq = hq, nk = hk;
   if (nq + nk > room) {
     nk = hk == 0 ? 0 : std::max(1, static_cast<int>(static_cast<long long>(room) * hk / (hq + hk)));
     nk = hq == 0 ? room : std::min(nk, room - 1);
@@ -590,6 +601,13 @@ template <typename T, bool kHalf>
 static void (*wide_norm(bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
   cfg.dynamicSmemBytes = grad ? NormRing<T, kHalf, true>::kBytes : NormRing<T, kHalf, false>::kBytes;
   return grad ? mfa_norm_rope_kernel<T, kHalf, true> : mfa_norm_rope_kernel<T, kHalf, false>;
+}
+
+// The kernel for any shape: a lane's elements of a head (up to 256: fewer registers, three CTAs on an SM).
+template <typename T>
+static void (*any_norm(bool grad, int head_dim))(NormParams) {
+  if (head_dim <= 256) return grad ? mfa_norm_rope_any_kernel<T, true, 8> : mfa_norm_rope_any_kernel<T, false, 8>;
+  return grad ? mfa_norm_rope_any_kernel<T, true, 16> : mfa_norm_rope_any_kernel<T, false, 16>;
 }
 
 // cudaFuncSetAttribute for a wide kernel's dynamic shared memory, once per device and kernel.
@@ -655,11 +673,14 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
   p.partial = static_cast<float*>(workspace);
   p.dw[0] = dw[0];
   p.dw[1] = dw[1];
-  p.turned_units = (half ? p.pairs : c->rotary_dim) / 8;
-  p.units = p.turned_units + (c->head_dim - c->rotary_dim) / 8;
+  p.turned_units = half ? p.pairs / 8 : (c->rotary_dim + 7) / 8;
+  p.units = half ? p.turned_units + (c->head_dim - c->rotary_dim) / 8 : c->head_dim / 8;
   while ((1 << p.log_lanes) < p.units) ++p.log_lanes;
-  const bool wide = c->head_dim % 8 == 0 && c->rotary_dim % (half ? 16 : 8) == 0 && p.log_lanes <= 5 && wide_norm_side(q, grad) &&
+  // (adjacent pairs: what is left of the last unit turns by nothing; 52000 heads of 256 with 100 elements turned, their
+  // gradient: 25 us, 111 on the other path)
+  const bool wide = c->head_dim % 8 == 0 && (!half || c->rotary_dim % 16 == 0) && p.log_lanes <= 5 && wide_norm_side(q, grad) &&
                     wide_norm_side(k, grad);
+  p.angles = wide && !half ? 4 * p.turned_units : p.pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -674,11 +695,11 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return cuda_fail(e, "cudaDeviceGetAttribute");
-    const int ctas = std::min({num_rows, 2 * sms, MFA_NORM_ROPE_GRAD_PARTS});
+    int ctas = std::min({num_rows, 2 * sms, MFA_NORM_ROPE_GRAD_PARTS});
     int shares = 1;
     void (*fn)(NormParams);
     if (wide) {
-      norm_slots(p, kNormThreads >> p.log_lanes, bf16 ? 4 : 2);
+      norm_slots(p, kNormThreads >> p.log_lanes);
       // few rows: a row's heads shared by CTAs, as far as there is room and each slot has a head
       const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1, p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
       shares = std::max(1, std::min({rounds, std::min(2 * sms, MFA_NORM_ROPE_GRAD_PARTS) / ctas, 65535}));
@@ -687,10 +708,10 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
       else fn = half ? wide_norm<float, true>(grad, cfg) : wide_norm<float, false>(grad, cfg);
       if ((st = ensure_norm_smem((bf16 ? 0 : 4) + (half ? 2 : 0) + grad, reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
     } else {
-      norm_slots(p, kNormAnyThreads / 32, 1);
+      norm_slots(p, kNormAnyThreads / 32);
       cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) * 32), 1, 1);
-      if (grad) fn = bf16 ? mfa_norm_rope_any_kernel<__nv_bfloat16, true> : mfa_norm_rope_any_kernel<float, true>;
-      else fn = bf16 ? mfa_norm_rope_any_kernel<__nv_bfloat16, false> : mfa_norm_rope_any_kernel<float, false>;
+      fn = bf16 ? any_norm<__nv_bfloat16>(grad, p.head_dim) : any_norm<float>(grad, p.head_dim);
+      ctas = std::min(num_rows, grad ? std::min(3 * sms, MFA_NORM_ROPE_GRAD_PARTS) : 6 * sms);
       if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * 4;   // (8 warps x 512 at most)
     }
     p.parts = grad ? ctas * shares : 0;

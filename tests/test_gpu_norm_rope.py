@@ -58,6 +58,26 @@ def test_forward_and_gradient(dim, sections, heads, pairing, dtype, weight_type)
                 assert grads[2 + i].dtype is torch.float32
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+@pytest.mark.parametrize("dim, sections, heads", [(256, (50,), (24, 2)), (128, (1,), (64, 4)), (64, (13, 10), (5, 3)), (256, (127,), (3, 1)),
+                                                  (512, (255,), (2, 1)), (8, (3,), (40, 2)), (72, (30, 5), (9, 9)), (256, (2, 3, 4, 5), (1, 0))])
+def test_pairs_that_are_no_eights(dim, sections, heads, pairing, dtype):
+    """(Adjacent ones: a vector of eight elements holds turned pairs and others.)"""
+    for rows in (3, 500):
+        x, dy, w, pos = inputs(rows, heads, dim, len(sections), rows, dtype)
+        op = mfa.NormRope(dim, sections, eps=EPS, pairing=pairing)
+        d, dd = ([t.to(DEV) if n else None for t, n in zip(y, heads)] for y in (x, dy))
+        ww = [t.to(DEV) for t in w]
+        out = op(*d, *ww, pos.to(DEV))
+        grads = op.grad(*dd, *d, *ww, pos.to(DEV))
+        for i in range(2 if heads[1] else 1):
+            rounded(out[i], *norm.forward(x[i], w[i], pos, sections, EPS, theta=1e4, pairing=pairing))
+            dx, tol, dw, dw_tol = norm.gradient(x[i], dy[i], w[i], pos, sections, EPS, theta=1e4, pairing=pairing)
+            rounded(grads[i], dx, tol)
+            rounded(grads[2 + i], dw, dw_tol)
+
+
 @pytest.mark.parametrize("dim, sections, heads", [(256, (128,), (64, 1)), (128, (24, 24), (40, 8)), (33, (3, 5), (3, 2))])
 def test_many_rows(dim, sections, heads):
     """More rows than CTAs: their sums go on over rows.  The gradient twice gives the same bits."""
