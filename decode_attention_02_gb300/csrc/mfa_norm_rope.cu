@@ -8,8 +8,8 @@
 //
 // Every element is read once (in the gradient x and dy) and written once, with some ten operations for each:
 // HBM-bound for a prompt or a training batch, launch-bound for a decode step.  A head's elements lie in
-// the registers of a group of up to 32 lanes (a lane: 8 elements of a pair's first half and the 8 of
-// its second, as they lie in memory), so that its sums are a few shuffles and nothing is read twice.
+// the registers of a group of up to 32 lanes (a lane: 8 elements, under half pairing with their 8 partners, in
+// vectors of 16 bytes), so that its sums are a few shuffles and nothing is read twice.
 // A CTA turns all heads of a row: the row's angles are computed once and shared.  A group keeps to one
 // side, q or k, and multiplies its weights with the angles' cosines and sines once a row in the forward
 // pass.  All sums are fp32; outputs are rounded once.
@@ -17,12 +17,15 @@
 // Measured, bf16 unless said (the bytes at the copy rate of 6.7 TB/s in brackets):
 //   8191 rows of 65 heads of 256, three axes: 88 us, 6.2 TB/s (82); 128 such rows 8.2 us, launch and one
 //   chain of loads: positions and angles, the elements, two sums;
-//   its gradient 157 us, 5.2 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 31 us (16).
+//   its gradient 156 us, 5.2 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 23 us (16),
+//   4000 rows of 65 of 256 in fp32 91 us forward (80), 132 the gradient (120).
 // What bounds the gradient: issue slots as much as memory, some 13 instructions an element beside the loads.
 // The steps that carried it, the prompt / its gradient: plain loads, one CTA on an SM 188 / 272; arithmetic
 // in pairs, two CTAs 108 / 240; copies ahead into shared memory, free of bank conflicts, 105 / 203; angles
 // by a warp of their own 88 / -; values read from shared memory again in place of kept, and the CTA's
-// meetings one in four rows, - / 157.  Asking L2 for the next rows gained nothing.
+// meetings one in four rows, - / 156.  Asking L2 for the next rows gained nothing; three CTAs on an SM (fewer registers
+// and copies ahead) 120 for the prompt.  fp32, a lane's two vectors side by side, so that each copy takes half of every
+// sector: 115 and 193 for the 4000 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,8 +59,8 @@ struct NormParams {
   const mfa_rope_pair* table;
   const int32_t* positions;
   int rows, axes, pairs, head_dim;
-  int angles;           // pairs, and those that do not turn of the last adjacent ones' unit
-  int turned_units, units, log_lanes;   // wide path: a head's units, lanes of its group
+  int angles;           // pairs, and on the wide path what does not turn beside them
+  int turned_vectors, units, log_lanes;   // wide path: vectors with partners (half pairing), a head's units, lanes of its group
   int half;                             // pairing, for any shape
   int w_f32;
   float eps, inv_dim;
@@ -110,29 +113,36 @@ __device__ __forceinline__ void group_sum(float (&v)[N], unsigned mask, int lane
   }
 }
 
-// A thread's place: its group's slot on one side, its unit of the head.
-template <bool kHalf>
+// A thread's place: its group's slot on one side, its unit of the head: one vector of 16 bytes, or two that lie as far
+// apart as the units' vectors reach (fp32), so that neighbouring lanes' vectors are neighbours in memory; and under half
+// pairing the partners of the vectors that turn.
+template <typename T, bool kHalf>
 struct NormPlace {
-  int u, a0, b0, h0, step;
-  bool on_q, active, turned;
+  static constexpr int kVectors = sizeof(T) / 2, kVec = 8 / kVectors;   // vectors of a unit, elements of one
+  int u, a0, h0, step;
+  int from[kVectors];   // elements from the first vector
+  bool two[kVectors];   // it has a partner
+  bool on_q, active;
   unsigned mask;
   __device__ __forceinline__ NormPlace(const NormParams& p) {
     const int lanes = 1 << p.log_lanes, slot = threadIdx.x >> p.log_lanes, lane = threadIdx.x & 31;
     u = threadIdx.x & (lanes - 1);
-    active = u < p.units;
-    turned = u < p.turned_units;
     on_q = slot < p.q.slots;
-    active = active && slot < p.q.slots + p.k.slots;
+    active = u < p.units && slot < p.q.slots + p.k.slots;
     const int slots = on_q ? p.q.slots : p.k.slots;
     h0 = (on_q ? slot : slot - p.q.slots) + blockIdx.y * slots;
     step = slots * gridDim.y;
     mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & ~(lanes - 1));
     a0 = start(p, u);
-    b0 = kHalf && turned ? a0 + p.pairs : a0;
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v) {
+      from[v] = start(p, u + v * p.units) - a0;
+      two[v] = kHalf && active && u + v * p.units < p.turned_vectors;
+    }
   }
-  // the first element of unit x
+  // the first element of vector x
   static __device__ __forceinline__ int start(const NormParams& p, int x) {
-    return kHalf && x >= p.turned_units ? 2 * p.pairs + 8 * (x - p.turned_units) : 8 * x;
+    return kHalf && x >= p.turned_vectors ? 2 * p.pairs + kVec * (x - p.turned_vectors) : kVec * x;
   }
 };
 
@@ -187,14 +197,14 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
   extern __shared__ __align__(16) uint8_t ring[];             // stages; at the end the CTA's sums
   grid_dep_wait();
   if constexpr (!kGrad) grid_dep_launch();
-  const NormPlace<kHalf> at(p);
+  const NormPlace<T, kHalf> at(p);
   const int threads = blockDim.x, tid = threadIdx.x, lanes = 1 << p.log_lanes;
   const int step = at.step, d = p.head_dim;
   // (the last warp has angles in place of heads; what is left of a warp behind the slots has nothing)
   const bool angles = tid >= threads - 32;
   int heads = at.on_q ? p.q.heads : p.k.heads;
   if (angles || tid >= (p.q.slots + p.k.slots) << p.log_lanes || at.h0 >= heads) heads = 0;
-  const bool two = kHalf && at.turned;
+  const bool two = kHalf && (at.two[0] || at.two[kVectors - 1]);
 
   // The head that is copied next; each thread goes over (row, head) by itself.
   const int head_step = step * d;
@@ -212,16 +222,16 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
   };
   const uint32_t mine = smem_u32(ring) + tid * 16;
   uint32_t in_at = mine;
-  const int second = at.b0 - at.a0;
+  const int second = p.pairs;   // from a vector to its partner
   auto copy = [&]() {
     if (in_row < p.rows && heads > 0 && at.active) {
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        cp_async_16(in_at + v * Ring::kVectorBytes, in_x + 8 / kVectors * v);
-        if constexpr (kGrad) cp_async_16(in_at + kParts / 2 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + 8 / kVectors * v);
-        if (two) {
-          cp_async_16(in_at + Ring::kPartBytes + v * Ring::kVectorBytes, in_x + second + 8 / kVectors * v);
-          if constexpr (kGrad) cp_async_16(in_at + 3 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + second + 8 / kVectors * v);
+        cp_async_16(in_at + v * Ring::kVectorBytes, in_x + at.from[v]);
+        if constexpr (kGrad) cp_async_16(in_at + kParts / 2 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + at.from[v]);
+        if (at.two[v]) {
+          cp_async_16(in_at + Ring::kPartBytes + v * Ring::kVectorBytes, in_x + second + at.from[v]);
+          if constexpr (kGrad) cp_async_16(in_at + 3 * Ring::kPartBytes + v * Ring::kVectorBytes, in_dy + second + at.from[v]);
         }
       }
     }
@@ -238,19 +248,23 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
   };
   const uint8_t* out_at = ring + tid * 16;   // the stage that is used next
   const uint8_t* const out_end = out_at + Ring::kBytes;
+  auto partner = [&](int part, int v) { return !(kHalf && part % 2 == 1) || at.two[v]; };
   auto fetch_again = [&](int part) {   // as load_pairs_again
-    RopeVec<T, 8> r;
+    RopeVec<T, 8> r = {};
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v)
+    for (int v = 0; v < kVectors; ++v) {
+      if (!partner(part, v)) continue;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(r.w[4 * v]), "=r"(r.w[4 * v + 1]), "=r"(r.w[4 * v + 2]), "=r"(r.w[4 * v + 3])
                    : "r"(smem_u32(out_at) + part * Ring::kPartBytes + v * Ring::kVectorBytes));
+    }
     return r;
   };
   auto fetch = [&](int part) {
-    RopeVec<T, 8> r;
+    RopeVec<T, 8> r = {};
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) {
+      if (!partner(part, v)) continue;
       const uint4 x = *reinterpret_cast<const uint4*>(out_at + part * Ring::kPartBytes + v * Ring::kVectorBytes);
       r.w[4 * v] = x.x, r.w[4 * v + 1] = x.y, r.w[4 * v + 2] = x.z, r.w[4 * v + 3] = x.w;
     }
@@ -265,13 +279,18 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
     const int lane = i >> 2, vector = lane >> p.log_lanes;   // (vector: side, half, first or second four elements)
     const int on_k = vector >> 2, half = vector >> 1 & 1, u = lane & (lanes - 1), e = (vector & 1) * 4 + (i & 3);
     const NormSide& side = on_k ? p.k : p.q;
-    const bool turned = u < p.turned_units;
-    const bool there = side.heads > 0 && u < p.units && (half == 0 || (kHalf && turned));
+    const int x = kVectors == 2 ? u + (vector & 1) * p.units : u;
+    const bool there = side.heads > 0 && u < p.units && (half == 0 || (kHalf && x < p.turned_vectors));
     sw[on_k][half][(e / 4 * lanes + u) * 4 + (e & 3)] =
-        there ? norm_weight(p, side, at.start(p, u) + half * p.pairs + e) : 0.f;
+        there ? norm_weight(p, side, at.start(p, x) + half * p.pairs + (kVectors == 2 ? i & 3 : e)) : 0.f;
   }
-  // half pairing: a lane's eight pairs in two vectors; adjacent: its four in one
-  auto place = [&](int i) { return kHalf ? ((i >> 2 & 1) * lanes + (i >> 3)) * 4 + (i & 3) : i; };
+  // half pairing: a lane's eight pairs in two groups of four; adjacent: its four together
+  auto place = [&](int i) {
+    const int x = i / (kHalf ? at.kVec : at.kVec / 2);   // the pair's vector
+    const int v = kVectors == 2 && x >= p.units, u = x - v * p.units;
+    if constexpr (kHalf) return kVectors == 2 ? (v * lanes + u) * 4 + (i & 3) : ((i >> 2 & 1) * lanes + u) * 4 + (i & 3);
+    return kVectors == 2 ? 4 * u + 2 * v + (i & 1) : i;
+  };
   const long long chunk = static_cast<long long>(kAngleRows) * gridDim.x;
   auto make_angles = [&](long long row, int buffer, int from, int by) {
 #pragma unroll 1
@@ -297,21 +316,14 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
             static_cast<long long>(at.h0) * d + at.a0;
     // Half pairing: c and s of the thread's eight pairs; adjacent: of its four, as (c, c) and (-s, s).
     uint64_t c[4], s[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c[j] = pack_f32x2(1.f, 1.f);
-      s[j] = 0;
-    }
-    if (at.turned) {
-      if constexpr (kHalf) {
-        load_pairs(&cs[buffer][in_chunk][0][4 * at.u], 4 * lanes, c);
-        load_pairs(&cs[buffer][in_chunk][1][4 * at.u], 4 * lanes, s);
-      } else {
-        const float4 x = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][0][4 * at.u]);
-        const float4 y = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][1][4 * at.u]);
-        c[0] = pack_f32x2(x.x, x.x), c[1] = pack_f32x2(x.y, x.y), c[2] = pack_f32x2(x.z, x.z), c[3] = pack_f32x2(x.w, x.w);
-        s[0] = pack_f32x2(-y.x, y.x), s[1] = pack_f32x2(-y.y, y.y), s[2] = pack_f32x2(-y.z, y.z), s[3] = pack_f32x2(-y.w, y.w);
-      }
+    if constexpr (kHalf) {
+      load_pairs(&cs[buffer][in_chunk][0][4 * at.u], 4 * lanes, c);
+      load_pairs(&cs[buffer][in_chunk][1][4 * at.u], 4 * lanes, s);
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][0][4 * at.u]);
+      const float4 y = *reinterpret_cast<const float4*>(&cs[buffer][in_chunk][1][4 * at.u]);
+      c[0] = pack_f32x2(x.x, x.x), c[1] = pack_f32x2(x.y, x.y), c[2] = pack_f32x2(x.z, x.z), c[3] = pack_f32x2(x.w, x.w);
+      s[0] = pack_f32x2(-y.x, y.x), s[1] = pack_f32x2(-y.y, y.y), s[2] = pack_f32x2(-y.z, y.z), s[3] = pack_f32x2(-y.w, y.w);
     }
     // Forward: c and s times the weights.  Half pairing: y = r (a ac + b bs), r (b bc + a as), with bs negated;
     // adjacent: y = r ((x0, x1) ac + (x1, x0) bs).
@@ -404,8 +416,11 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
         }
       }
       if (at.active) {
-        y.store_raw(to);
-        if (two) z.store_raw(to + second);
+#pragma unroll
+        for (int v = 0; v < kVectors; ++v) {
+          *reinterpret_cast<uint4*>(to + at.from[v]) = make_uint4(y.w[4 * v], y.w[4 * v + 1], y.w[4 * v + 2], y.w[4 * v + 3]);
+          if (at.two[v]) *reinterpret_cast<uint4*>(to + second + at.from[v]) = make_uint4(z.w[4 * v], z.w[4 * v + 1], z.w[4 * v + 2], z.w[4 * v + 3]);
+        }
       }
       copy();   // into the stage that was read
       out_at = out_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : out_at + Ring::kStageBytes;
@@ -426,8 +441,10 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
     if (at.active) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        *reinterpret_cast<uint64_t*>(own + 2 * j) = da[j];
-        if (two) *reinterpret_cast<uint64_t*>(own + second + 2 * j) = db[j];
+        const int v = kVectors == 2 ? j / 2 : 0;
+        float* to = own + at.from[v] + (kVectors == 2 ? 2 * (j & 1) : 2 * j);
+        *reinterpret_cast<uint64_t*>(to) = da[j];
+        if (at.two[v]) *reinterpret_cast<uint64_t*>(to + second) = db[j];
       }
     }
     __syncthreads();
@@ -673,14 +690,14 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
   p.partial = static_cast<float*>(workspace);
   p.dw[0] = dw[0];
   p.dw[1] = dw[1];
-  p.turned_units = half ? p.pairs / 8 : (c->rotary_dim + 7) / 8;
-  p.units = half ? p.turned_units + (c->head_dim - c->rotary_dim) / 8 : c->head_dim / 8;
+  p.turned_vectors = half ? p.pairs / (16 / esz) : 0;
+  p.units = (c->head_dim - (half ? p.pairs : 0)) / 8;
   while ((1 << p.log_lanes) < p.units) ++p.log_lanes;
   // (adjacent pairs: what is left of the last unit turns by nothing; 52000 heads of 256 with 100 elements turned, their
   // gradient: 25 us, 111 on the other path)
   const bool wide = c->head_dim % 8 == 0 && (!half || c->rotary_dim % 16 == 0) && p.log_lanes <= 5 && wide_norm_side(q, grad) &&
                     wide_norm_side(k, grad);
-  p.angles = wide && !half ? 4 * p.turned_units : p.pairs;
+  p.angles = wide ? (half ? 8 : 4) * p.units : p.pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
