@@ -43,6 +43,11 @@
 namespace mfa {
 
 constexpr int kNormThreads = 288;        // of a CTA that have heads, at most; with a warp of angles two CTAs on an SM
+// Wide path: where an element's partner in its pair lies.  In the same vector; in a vector of its own, which the same lane
+// has; or anywhere in the head (half pairing of pairs that are no eights), read from the copies of the group's lanes, element by
+// element, and with half as many elements a lane (65 heads of 256, fp32, gradient of 2000 rows: 70 us of 60, 288 on the
+// path for any shape).
+enum NormPairs { kPairsNext, kPairsVectors, kPairsFar };
 constexpr int kNormAnyThreads = 256;     // of a CTA of the path for any shape
 
 struct NormSide {
@@ -87,8 +92,9 @@ __device__ __forceinline__ float norm_weight(const NormParams& p, const NormSide
   return p.w_f32 ? norm_load<float>(s.w, i) : norm_load<__nv_bfloat16>(s.w, i);
 }
 
-// Angles of row `row`, one pair a thread, into cs, pair i at place(i).
-template <typename Place>
+// Angles of row `row`, one pair a thread, into cs, pair i at place(i); kFar: one element a thread, its sine with the sign
+// that its partner has in it.
+template <bool kFar, typename Place>
 __device__ __forceinline__ void row_angles(const NormParams& p, long long row, int tid, int threads, float (&cs)[2][kRopeMaxDim / 2],
                                            Place place) {
   int32_t pos[MFA_ROPE_MAX_AXES];
@@ -96,9 +102,11 @@ __device__ __forceinline__ void row_angles(const NormParams& p, long long row, i
   for (int x = 0; x < MFA_ROPE_MAX_AXES; ++x) pos[x] = x < p.axes ? p.positions[static_cast<long long>(x) * p.rows + row] : 0;
   for (int i = tid; i < p.angles; i += threads) {
     float s = 0.f, c = 1.f;
-    if (i < p.pairs) rope_angle(p.table, i, pos, s, c);
+    const bool second = kFar && i >= p.pairs;
+    const int pair = second ? i - p.pairs : i;
+    if (pair < p.pairs) rope_angle(p.table, pair, pos, s, c);
     cs[0][place(i)] = c;
-    cs[1][place(i)] = s;
+    cs[1][place(i)] = kFar && !second ? -s : s;
   }
 }
 
@@ -164,8 +172,9 @@ __device__ __forceinline__ float sum_f32x2(uint64_t v) {
 // without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
 // In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows; each
 // CTA leaves one partial sum a side and element, and a second kernel adds those in a fixed order.
-template <typename T, bool kHalf, bool kGrad>
+template <typename T, NormPairs kPairs, bool kGrad>
 struct NormRing {
+  static constexpr bool kHalf = kPairs == kPairsVectors;
   static constexpr int kVectors = sizeof(T) / 2;                      // 16-byte vectors of 8 elements
   static constexpr int kParts = (kHalf ? 2 : 1) * (kGrad ? 2 : 1);    // x's first and second halves, dy's
   // rows from one meeting to the next (prompt of 8191 rows 86 us at 1, 93 at 4; its gradient 203 and 155)
@@ -187,9 +196,10 @@ __device__ __forceinline__ void load_pairs_again(const float* from, int pitch, u
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2]), "=l"(v[3]) : "r"(smem_u32(from + pitch)));
 }
 
-template <typename T, bool kHalf, bool kGrad>
+template <typename T, NormPairs kPairs, bool kGrad>
 __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(const __grid_constant__ NormParams p) {
-  using Ring = NormRing<T, kHalf, kGrad>;
+  using Ring = NormRing<T, kPairs, kGrad>;
+  constexpr bool kHalf = kPairs == kPairsVectors, kFar = kPairs == kPairsFar;
   constexpr int kDepth = Ring::kDepth, kParts = Ring::kParts, kVectors = Ring::kVectors, kAngleRows = Ring::kAngleRows;
   // a lane's four floats lie beside its neighbour's
   __shared__ __align__(16) float cs[2][kAngleRows][2][kRopeMaxDim / 2];
@@ -270,6 +280,29 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
     }
     return r;
   };
+  int far[8];   // of each element's partner, bytes from the group's first lane's
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = kFar ? at.a0 + (kVectors == 2 && i >= 4 ? at.from[kVectors - 1] : 0) + (kVectors == 2 ? i & 3 : i) : 0;
+    const int x = e < p.pairs ? e + p.pairs : e < 2 * p.pairs ? e - p.pairs : e;
+    const int v = kVectors == 2 && x / 4 >= p.units;
+    far[i] = kVectors == 1 ? 2 * x : 4 * x - v * 16 * p.units + v * Ring::kVectorBytes;
+  }
+  auto fetch_far = [&](int part) {
+    const uint8_t* base = out_at - 16 * at.u + part * Ring::kPartBytes;
+    RopeVec<T, 8> r;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if constexpr (kVectors == 1) {
+        r.w[i / 2] = *reinterpret_cast<const uint16_t*>(base + far[i]) |
+                     static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(base + far[i + 1])) << 16;
+      } else {
+        r.w[i] = *reinterpret_cast<const uint32_t*>(base + far[i]);
+        r.w[i + 1] = *reinterpret_cast<const uint32_t*>(base + far[i + 1]);
+      }
+    }
+    return r;
+  };
   if (heads > 0) {
     start(in_row);
 #pragma unroll 1
@@ -280,21 +313,22 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
     const int on_k = vector >> 2, half = vector >> 1 & 1, u = lane & (lanes - 1), e = (vector & 1) * 4 + (i & 3);
     const NormSide& side = on_k ? p.k : p.q;
     const int x = kVectors == 2 ? u + (vector & 1) * p.units : u;
-    const bool there = side.heads > 0 && u < p.units && (half == 0 || (kHalf && x < p.turned_vectors));
-    sw[on_k][half][(e / 4 * lanes + u) * 4 + (e & 3)] =
-        there ? norm_weight(p, side, at.start(p, x) + half * p.pairs + (kVectors == 2 ? i & 3 : e)) : 0.f;
+    const bool there = side.heads > 0 && u < p.units && (half == 0 || kFar || (kHalf && x < p.turned_vectors));
+    int el = at.start(p, x) + (kVectors == 2 ? i & 3 : e);
+    if (half) el = kFar && el >= p.pairs ? (el < 2 * p.pairs ? el - p.pairs : el) : el + p.pairs;   // the partner's
+    sw[on_k][half][(e / 4 * lanes + u) * 4 + (e & 3)] = there ? norm_weight(p, side, el) : 0.f;
   }
-  // half pairing: a lane's eight pairs in two groups of four; adjacent: its four together
+  // half pairing: a lane's eight pairs (or elements) in two groups of four; adjacent: its four together
   auto place = [&](int i) {
-    const int x = i / (kHalf ? at.kVec : at.kVec / 2);   // the pair's vector
+    const int x = i / (kPairs != kPairsNext ? at.kVec : at.kVec / 2);   // the pair's vector
     const int v = kVectors == 2 && x >= p.units, u = x - v * p.units;
-    if constexpr (kHalf) return kVectors == 2 ? (v * lanes + u) * 4 + (i & 3) : ((i >> 2 & 1) * lanes + u) * 4 + (i & 3);
+    if constexpr (kPairs != kPairsNext) return kVectors == 2 ? (v * lanes + u) * 4 + (i & 3) : ((i >> 2 & 1) * lanes + u) * 4 + (i & 3);
     return kVectors == 2 ? 4 * u + 2 * v + (i & 1) : i;
   };
   const long long chunk = static_cast<long long>(kAngleRows) * gridDim.x;
   auto make_angles = [&](long long row, int buffer, int from, int by) {
 #pragma unroll 1
-    for (int i = 0; i < kAngleRows && row < p.rows; ++i, row += gridDim.x) row_angles(p, row, from, by, cs[buffer][i], place);
+    for (int i = 0; i < kAngleRows && row < p.rows; ++i, row += gridDim.x) row_angles<kFar>(p, row, from, by, cs[buffer][i], place);
   };
   make_angles(blockIdx.x, 0, tid, threads);
   __syncthreads();
@@ -314,9 +348,9 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
   for (long long row = blockIdx.x; row < p.rows && !angles; row += gridDim.x) {
     T* to = static_cast<T*>(at.on_q ? p.q.out : p.k.out) + row * (at.on_q ? p.q.out_stride : p.k.out_stride) +
             static_cast<long long>(at.h0) * d + at.a0;
-    // Half pairing: c and s of the thread's eight pairs; adjacent: of its four, as (c, c) and (-s, s).
+    // Half pairing: c and s of the thread's eight pairs (or elements, s with its sign); adjacent: of its four, as (c, c) and (-s, s).
     uint64_t c[4], s[4];
-    if constexpr (kHalf) {
+    if constexpr (kPairs != kPairsNext) {
       load_pairs(&cs[buffer][in_chunk][0][4 * at.u], 4 * lanes, c);
       load_pairs(&cs[buffer][in_chunk][1][4 * at.u], 4 * lanes, s);
     } else {
@@ -326,14 +360,16 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
       s[0] = pack_f32x2(-y.x, y.x), s[1] = pack_f32x2(-y.y, y.y), s[2] = pack_f32x2(-y.z, y.z), s[3] = pack_f32x2(-y.w, y.w);
     }
     // Forward: c and s times the weights.  Half pairing: y = r (a ac + b bs), r (b bc + a as), with bs negated;
-    // adjacent: y = r ((x0, x1) ac + (x1, x0) bs).
+    // else: y = r ((x0, x1) ac + (x0's partner, x1's) bs).
     uint64_t ac[4], as[4], bc[4], bs[4];
     if constexpr (!kGrad) {
       load_pairs(my_wa, 4 * lanes, ac);
-      if constexpr (kHalf) load_pairs(my_wb, 4 * lanes, bc);
+      if constexpr (kPairs != kPairsNext) load_pairs(my_wb, 4 * lanes, bc);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kHalf) {
+        if constexpr (kFar) {
+          bs[j] = mul_f32x2(bc[j], s[j]);
+        } else if constexpr (kHalf) {
           as[j] = mul_f32x2(ac[j], s[j]);
           bs[j] = neg_f32x2(mul_f32x2(bc[j], s[j]));
           bc[j] = mul_f32x2(bc[j], c[j]);
@@ -346,9 +382,11 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
 #pragma unroll 1
     for (int h = at.h0; h < heads; h += step, to += head_step) {
       cp_async_wait<kDepth - 1>();
+      if constexpr (kFar) __syncwarp(at.mask);   // the group's copies
       const RopeVec<T, 8> a = fetch(0);
       RopeVec<T, 8> b = {};
       if (two) b = fetch(1);
+      if constexpr (kFar && !kGrad) b = fetch_far(0);
       uint64_t sq = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -369,7 +407,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
             y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(v, bs[j])));
             z.set_pair(2 * j, fma_f32x2(v, bc[j], mul_f32x2(u, as[j])));
           } else {
-            y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(swap_f32x2(u), bs[j])));
+            y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(kFar ? mul_f32x2(b.pair(2 * j), r2) : swap_f32x2(u), bs[j])));
           }
         }
       } else {
@@ -378,6 +416,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
         const RopeVec<T, 8> ga = fetch(kParts / 2);
         RopeVec<T, 8> gb = {};
         if (two) gb = fetch(kParts / 2 + 1);
+        if constexpr (kFar) gb = fetch_far(kParts / 2);
         load_pairs(my_wa, 4 * lanes, wa);
         if constexpr (kHalf) load_pairs(my_wb, 4 * lanes, wb);
 #pragma unroll
@@ -389,7 +428,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
             k[j] = fma_f32x2(v, c[j], neg_f32x2(mul_f32x2(x, s[j])));
             ux = fma_f32x2(mul_f32x2(k[j], wb[j]), b.pair(2 * j), ux);
           } else {
-            g[j] = fma_f32x2(x, c[j], neg_f32x2(mul_f32x2(swap_f32x2(x), s[j])));
+            g[j] = fma_f32x2(x, c[j], neg_f32x2(mul_f32x2(kFar ? gb.pair(2 * j) : swap_f32x2(x), s[j])));
           }
           ux = fma_f32x2(mul_f32x2(g[j], wa[j]), a.pair(2 * j), ux);
         }
@@ -422,6 +461,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
           if (at.two[v]) *reinterpret_cast<uint4*>(to + second + at.from[v]) = make_uint4(z.w[4 * v], z.w[4 * v + 1], z.w[4 * v + 2], z.w[4 * v + 3]);
         }
       }
+      if constexpr (kFar) __syncwarp(at.mask);   // (read by all)
       copy();   // into the stage that was read
       out_at = out_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : out_at + Ring::kStageBytes;
     }
@@ -484,9 +524,9 @@ __global__ void __launch_bounds__(256) mfa_norm_rope_weights_kernel(const __grid
 
 // ------------------------------------------------------------------ any shape
 //
-// Heads of odd sizes, half pairing of pairs that are no eights, unaligned rows: a warp a head, a lane its every 32nd
-// element and that element's partner in the pair.  Bound by its loads' latency: 2000 rows of 26 heads of 256, 100
-// elements turned, half pairing: gradient 74 us of 12 (with registers for heads of 512, one CTA on an SM, 184).
+// Heads of odd sizes or too many units, unaligned rows: a warp a head, a lane its every 32nd element and that element's
+// partner in the pair.  Bound by its loads' latency: 2000 rows of 26 heads of 256, 100 elements turned, half pairing,
+// gradient: 72 us (184 with registers for heads of 512, one CTA on an SM; 31 on the wide path).
 template <typename T, bool kGrad, int kEach>
 __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_rope_any_kernel(const __grid_constant__ NormParams p) {
   __shared__ __align__(16) float cs[2][2][kRopeMaxDim / 2];
@@ -502,7 +542,7 @@ __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_
   int buffer = 0;
 #pragma unroll 1
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
-    row_angles(p, row, threadIdx.x, blockDim.x, cs[buffer], [](int i) { return i; });
+    row_angles<false>(p, row, threadIdx.x, blockDim.x, cs[buffer], [](int i) { return i; });
     __syncthreads();
     const T* xs = static_cast<const T*>(side.x) + row * side.x_stride;
     const T* dys = static_cast<const T*>(side.dy) + row * side.dy_stride;
@@ -614,10 +654,16 @@ static void norm_slots(NormParams& p, int room) {
 }
 
 // The wide path's kernel, and its shared memory in cfg.
-template <typename T, bool kHalf>
+template <typename T, NormPairs kPairs>
 static void (*wide_norm(bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
-  cfg.dynamicSmemBytes = grad ? NormRing<T, kHalf, true>::kBytes : NormRing<T, kHalf, false>::kBytes;
-  return grad ? mfa_norm_rope_kernel<T, kHalf, true> : mfa_norm_rope_kernel<T, kHalf, false>;
+  cfg.dynamicSmemBytes = grad ? NormRing<T, kPairs, true>::kBytes : NormRing<T, kPairs, false>::kBytes;
+  return grad ? mfa_norm_rope_kernel<T, kPairs, true> : mfa_norm_rope_kernel<T, kPairs, false>;
+}
+template <typename T>
+static void (*wide_norm(NormPairs pairs, bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
+  return pairs == kPairsNext      ? wide_norm<T, kPairsNext>(grad, cfg)
+         : pairs == kPairsVectors ? wide_norm<T, kPairsVectors>(grad, cfg)
+                                  : wide_norm<T, kPairsFar>(grad, cfg);
 }
 
 // The kernel for any shape: a lane's elements of a head (up to 256: fewer registers, three CTAs on an SM).
@@ -630,7 +676,7 @@ static void (*any_norm(bool grad, int head_dim))(NormParams) {
 // cudaFuncSetAttribute for a wide kernel's dynamic shared memory, once per device and kernel.
 static mfa_status ensure_norm_smem(int i, const void* fn, int dev) {
   constexpr int kMaxDevices = 64;
-  static std::atomic<bool> done[8][kMaxDevices];
+  static std::atomic<bool> done[12][kMaxDevices];
   const bool cacheable = dev >= 0 && dev < kMaxDevices;
   if (cacheable && done[i][dev].load(std::memory_order_acquire)) return MFA_OK;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormThreads * 256);
@@ -690,13 +736,12 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
   p.partial = static_cast<float*>(workspace);
   p.dw[0] = dw[0];
   p.dw[1] = dw[1];
-  p.turned_vectors = half ? p.pairs / (16 / esz) : 0;
-  p.units = (c->head_dim - (half ? p.pairs : 0)) / 8;
+  const NormPairs pairs = !half ? kPairsNext : c->rotary_dim % 16 == 0 ? kPairsVectors : kPairsFar;
+  p.turned_vectors = pairs == kPairsVectors ? p.pairs / (16 / esz) : 0;
+  p.units = (c->head_dim - (pairs == kPairsVectors ? p.pairs : 0)) / 8;
   while ((1 << p.log_lanes) < p.units) ++p.log_lanes;
-  // (adjacent pairs: what is left of the last unit turns by nothing; 52000 heads of 256 with 100 elements turned, their
-  // gradient: 25 us, 111 on the other path)
-  const bool wide = c->head_dim % 8 == 0 && (!half || c->rotary_dim % 16 == 0) && p.log_lanes <= 5 && wide_norm_side(q, grad) &&
-                    wide_norm_side(k, grad);
+  // (what is left of the last turned vector turns by nothing)
+  const bool wide = c->head_dim % 8 == 0 && p.log_lanes <= 5 && wide_norm_side(q, grad) && wide_norm_side(k, grad);
   p.angles = wide ? (half ? 8 : 4) * p.units : p.pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -721,9 +766,8 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
       const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1, p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
       shares = std::max(1, std::min({rounds, std::min(2 * sms, MFA_NORM_ROPE_GRAD_PARTS) / ctas, 65535}));
       cfg.blockDim = dim3(static_cast<unsigned>((((p.q.slots + p.k.slots) << p.log_lanes) + 31) / 32 * 32 + 32), 1, 1);
-      if (bf16) fn = half ? wide_norm<__nv_bfloat16, true>(grad, cfg) : wide_norm<__nv_bfloat16, false>(grad, cfg);
-      else fn = half ? wide_norm<float, true>(grad, cfg) : wide_norm<float, false>(grad, cfg);
-      if ((st = ensure_norm_smem((bf16 ? 0 : 4) + (half ? 2 : 0) + grad, reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
+      fn = bf16 ? wide_norm<__nv_bfloat16>(pairs, grad, cfg) : wide_norm<float>(pairs, grad, cfg);
+      if ((st = ensure_norm_smem((bf16 ? 0 : 6) + 2 * pairs + grad, reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
     } else {
       norm_slots(p, kNormAnyThreads / 32);
       cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) * 32), 1, 1);

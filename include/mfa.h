@@ -648,8 +648,8 @@ typedef struct mfa_norm {
 
 /*
  * Enqueue the norm and rotation of num_rows rows of q and of k (one launch).  Arguments and conditions as
- * for mfa_rope_run (in place too); the wide path takes any number of adjacent pairs, and heads of up to
- * 32 units: a unit is 16 elements of whole pairs under half pairing, else 8 elements.
+ * for mfa_rope_run (in place too), but that the wide path takes any number of pairs, and heads of up to 32
+ * units: a unit is 16 elements of whole pairs where half pairing's pairs are a multiple of 8, else 8 elements.
  */
 mfa_status mfa_norm_rope_run(const mfa_rope_config* config, const mfa_rope_pair* table, const int32_t* positions,
                              int32_t num_rows, int32_t dtype, const mfa_norm* norm, const mfa_rope_rows* q,

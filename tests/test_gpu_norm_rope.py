@@ -156,6 +156,13 @@ def test_in_place_and_strided(dim, sections, pairing):
         assert torch.equal(q, plain[0]) and torch.equal(k, plain[1]) and untouched()
 
 
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+@pytest.mark.parametrize("dim, sections", [(256, (50,)), (128, (3, 2)), (248, (100, 23)), (64, (31,))])
+def test_in_place_with_pairs_that_are_no_eights(dim, sections, pairing):
+    """(Half pairing: lanes read what other lanes of the head have copied.)"""
+    test_in_place_and_strided(dim, sections, pairing)
+
+
 def test_gradient_against_differences():
     """<dx, v> + <dw, vw> against a central difference of the call itself, in fp32: outputs off by 2^-18 of about 4 each,
     n of them at random signs, over 2 h; and h^2 / 6 of a third derivative of at most 8 sum |dy| |v|^3."""
