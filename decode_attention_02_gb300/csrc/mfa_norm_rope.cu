@@ -379,8 +379,53 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
         ac[j] = mul_f32x2(ac[j], c[j]);
       }
     }
+    // Lanes with 8 bf16 elements of a head: two heads at a time, so that one's waits are the other's work (8191 rows of 68 heads
+    // of 128, adjacent, 53 us in place of 63; with 16 elements 57 in place of 55).
+    constexpr bool kTwo = !kGrad && !kHalf && kVectors == 1;
+    if constexpr (kTwo) {
 #pragma unroll 1
-    for (int h = at.h0; h < heads; h += step, to += head_step) {
+      for (int h = at.h0; h < heads; h += 2 * step, to += 2 * head_step) {
+        cp_async_wait<kDepth - 2>();
+        if constexpr (kFar) __syncwarp(at.mask);   // the group's copies
+        const bool second_head = h + step < heads;
+        const uint8_t* const first_at = out_at;
+        RopeVec<T, 8> a[2], b[2];
+        float sum[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {   // (a second head that is not there: the next row's, and nothing is written)
+          if (k == 1) out_at = out_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : out_at + Ring::kStageBytes;
+          a[k] = fetch(0);
+          if constexpr (kFar) b[k] = fetch_far(0);
+          uint64_t sq = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sq = fma_f32x2(a[k].pair(2 * j), a[k].pair(2 * j), sq);
+          sum[k] = at.active ? sum_f32x2(sq) : 0.f;
+        }
+        group_sum<2>(sum, at.mask, lanes);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float r = rsqrtf(fmaf(sum[k], p.inv_dim, p.eps));
+          const uint64_t r2 = pack_f32x2(r, r);
+          RopeVec<T, 8> y;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t u = mul_f32x2(a[k].pair(2 * j), r2);
+            y.set_pair(2 * j, fma_f32x2(u, ac[j], mul_f32x2(kFar ? mul_f32x2(b[k].pair(2 * j), r2) : swap_f32x2(u), bs[j])));
+          }
+          if (at.active && (k == 0 || second_head)) y.store_raw(to + k * head_step);
+        }
+        if constexpr (kFar) __syncwarp(at.mask);   // (read by all)
+        copy();   // into the stages that were read
+        if (second_head) {
+          copy();
+          out_at = out_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : out_at + Ring::kStageBytes;
+        } else {
+          out_at = first_at + Ring::kStageBytes == out_end ? out_end - Ring::kBytes : first_at + Ring::kStageBytes;
+        }
+      }
+    }
+#pragma unroll 1
+    for (int h = at.h0; !kTwo && h < heads; h += step, to += head_step) {
       cp_async_wait<kDepth - 1>();
       if constexpr (kFar) __syncwarp(at.mask);   // the group's copies
       const RopeVec<T, 8> a = fetch(0);
