@@ -29,11 +29,14 @@
 // What bounds it: a tile's products are 128 x 128 x d for S and as many for O, each twice (hi and lo), 2048
 // clocks of the tensor cores at d = 256; operands from shared memory are 192 KB of it and the tile's TMA
 // writes 64 KB, 2048 clocks at 128 bytes a clock.  The first tiles take 2200 clocks; under that load the card's
-// power brings its clock from 1.94 GHz to 1.4.  At d = 128 the softmax bounds it, 1900 clocks a tile, most of them
-// the conversions to eight bits and the maxima, which share one pipe.  A unit's beginning and end take 8 us beside
-// its tiles, a boundary inside a CTA's range 4 to 5, parts and their combine 5.  Eight trees of 32 nodes over 4096
+// power brings its clock from 1.94 GHz to 1.4.  At d = 128 a tile takes 2000 to 2600 clocks: the
+// softmax's chain (scores, maxima, their exchange, exponentials, two conversions to eight bits, stores) in two warps a
+// scheduler, which issue in half of the clocks; the tensor cores are active for 1024.  A unit's beginning and end take 8 us
+// beside its tiles, a boundary inside a CTA's range 4 to 5, parts and their combine 5.  Eight trees of 32 nodes over 4096
 // tokens, 64 heads of 256 over one: 57.4 us (1.2 PFLOP/s of the products' 1.9 in bf16); seven ragged ones of 61
-// nodes 92.2 us; 48 of 8 nodes, 64 heads of 128 over four: 65.7 us (214 MB); one of 8 over 2048 tokens 18.4 us.
+// nodes 90.6 us; 48 of 8 nodes, 64 heads of 128 over four: 65.3 us (214 MB); one of 8 over 2048 tokens 18.5 us.
+// Measured for the 48, and slower: sixteen softmax warps, with half the registers, 79.2 us against 77.9 at the time;
+// warpgroups that take the tiles in turn, each with an accumulator of its own, 88; P and V as f16, V by the warps that keep O, 77.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
