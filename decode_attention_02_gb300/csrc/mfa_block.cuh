@@ -24,6 +24,7 @@ constexpr int kBCostTile = 4;         // schedule: cost of a tile
 // sequences, two new tokens: 67.8 us at a cost of 6, 65.0 at 12, 64.2 at 16)
 constexpr int kBCostUnit = 16;
 constexpr int kBMaxSeg = 256;         // units that one CTA can meet
+constexpr int kBMaxShare = (kBMaxSeg - 2) * (kBCostTile + kBCostUnit);   // a range of this cost holds no more, whatever the lengths
 constexpr uint64_t kBWsHeader = 256;
 constexpr int kTreeRows = 128;        // query rows of a unit of a tree's kernel
 constexpr int kBSmem = 227 * 1024 - 1024;   // dynamic shared memory after its alignment
@@ -141,7 +142,9 @@ __device__ __forceinline__ int view_length(const BlockDecodeParams& p, int L) {
 // group; unit (b, r) at position r B + b): tile k of a unit sits at cost 4 k past the unit's
 // base, and the next unit's base is 4 T + c further (T tiles, c = kBCostUnit for the boundary;
 // nothing for an empty sequence).  CTA g of G owns the tiles whose cost lies in
-// [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.
+// [floor(g C / G), floor((g + 1) C / G)), C the whole cost: equal shares for any length mix.  Where lengths
+// have grown so far past the plan's that such a range could hold more units than a CTA can meet, all CTAs
+// take a higher c (grown_boundary).
 //
 // Two other ways, for few units:
 // Clusters: every unit (b, r) has c CTAs of its own, CTA c (r B + b) + i taking part i, tiles
@@ -294,24 +297,27 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
   }
 }
 
-// I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).
-template <typename I, bool kWindow>
-__device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
-                                              bool& bad) {
+// I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).  kGrown: with a
+// boundary's cost of `boundary`; else of kBCostUnit, and false where a CTA's range could then hold too many units.
+template <typename I, bool kWindow, bool kGrown>
+__device__ __forceinline__ bool cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
+                                              bool& bad, I boundary) {
   const int lane = threadIdx.x & 31;
   auto length = [&](int b) { return b < p.batch ? clamp_len(p.seq_lens[b], cap, bad) : 0; };
-  auto cost = [](int T) { return T > 0 ? static_cast<I>(kBCostTile) * T + kBCostUnit : I{0}; };
+  auto cost = [boundary](int T) { return T > 0 ? static_cast<I>(kBCostTile) * T + boundary : I{0}; };
   const int L0 = length(lane);
   I per = cost(block_tiles(view_length<kWindow>(p, L0)));   // of one reader of every sequence
 #pragma unroll 1
   for (int b = lane + 32; b < p.batch; b += 32) per += cost(block_tiles(view_length<kWindow>(p, length(b))));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) per += __shfl_xor_sync(0xffffffffu, per, o);
-  if (per == 0) return;
+  if (per == 0) return true;
   // the whole cost; with less of it than a tile for each CTA the last CTAs have nothing, so that
   // no CTA lies between two tiles
-  const I total = per * p.readers - kBCostUnit, G = min(static_cast<I>(gridDim.x), total / kBCostTile), g = blockIdx.x;
-  if (g >= G) return;
+  const I total = per * p.readers - boundary;
+  if (!kGrown && (total - 1) / kBMaxShare >= gridDim.x) return false;
+  const I G = min(static_cast<I>(gridDim.x), total / kBCostTile), g = blockIdx.x;
+  if (g >= G) return true;
   const I X0 = g * total / G, X1 = (g + 1) * total / G;
   I rbase = X0 / per;   // the reader at X0, then its base
   int r = static_cast<int>(rbase);
@@ -344,12 +350,38 @@ __device__ __forceinline__ void cost_segments(const BlockDecodeParams& p, int ca
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
+  return true;
 }
-// (the wide form, for problems of millions of tiles, out of the way of the usual one's code)
+// A boundary's cost c with which no CTA's range holds more than kBMaxSeg units: units begin at least 4 + c apart, so a
+// range of X holds ceil(X / (4 + c)) + 1 at most, and with W tiles in N units X <= (4 W + c (N - 1)) / G + 1.  There is
+// one where N - 1 <= (kBMaxSeg - 2) G, which a plan sees to unless its grid is forced.
+template <bool kWindow>
+__device__ __noinline__ long long grown_boundary(const BlockDecodeParams& p, int cap) {
+  long long tiles = 0, units = 0;
+  bool bad = false;
+  for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
+    const int T = block_tiles(view_length<kWindow>(p, clamp_len(p.seq_lens[b], cap, bad)));
+    tiles += T;
+    units += T > 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+  }
+  tiles *= p.readers;
+  units *= p.readers;
+  const long long G = gridDim.x, spare = (kBMaxSeg - 1) * G - (units - 1);
+  if (units <= kBMaxSeg || spare < 1) return kBCostUnit;   // (few units; too few CTAs for so many)
+  const long long over = kBCostTile * (tiles - (kBMaxSeg - 1) * G);
+  return max((over + spare - 1) / spare, static_cast<long long>(kBCostUnit));
+}
+// The wide form, for problems of millions of tiles and lengths far past the plan's, out of the way of the usual one's code.
 template <bool kWindow>
 __device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                                 bool& bad) {
-  cost_segments<long long, kWindow>(p, cap, seg, nseg, tiles, bad);
+  if (!cost_segments<long long, kWindow, false>(p, cap, seg, nseg, tiles, bad, kBCostUnit))
+    cost_segments<long long, kWindow, true>(p, cap, seg, nseg, tiles, bad, grown_boundary<kWindow>(p, cap));
 }
 
 // A unit's CTAs: only its own sequence's length is read.
@@ -375,9 +407,7 @@ __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int c
     unit_segment<kWindow>(p, cap, seg, nseg, tiles, bad);
   else if (p.quantum > 0)
     even_segments<kWindow>(p, cap, seg, nseg, tiles, bad);
-  else if (p.narrow)
-    cost_segments<uint32_t, kWindow>(p, cap, seg, nseg, tiles, bad);
-  else
+  else if (!p.narrow || !cost_segments<uint32_t, kWindow, false>(p, cap, seg, nseg, tiles, bad, kBCostUnit))
     cost_segments_wide<kWindow>(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);

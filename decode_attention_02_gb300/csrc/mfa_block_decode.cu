@@ -1184,10 +1184,12 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
   const long long C = kBCostTile * W + kBCostUnit * std::max(N - 1, 0ll);
   const long long most = force_ctas > 0 ? force_ctas : num_sms;
   // Split by cost.  A CTA's share of at most ceil(C / G) holds that over (tile + boundary) whole
-  // units and two parts of units.
-  const long long share = static_cast<long long>(kBMaxSeg - 2) * (kBCostTile + kBCostUnit);
-  const long long least = std::max(1ll, (C + share - 1) / share);
-  long long G = std::max(1ll, std::max(std::min(W, most), force_ctas > 0 ? 0ll : least));
+  // units and two parts of units.  And, as lengths grow past the plan's (from none, too), a CTA's units,
+  // whichever they are then, have to fit it.
+  long long least = std::max(1ll, (C + kBMaxShare - 1) / kBMaxShare);
+  if (force_ctas == 0) least = std::max(least, (units - 1 + kBMaxSeg - 3) / (kBMaxSeg - 2));
+  // (of no tokens: one CTA, or where it cannot meet all units one for each, as far as they go)
+  long long G = std::max(1ll, std::max(std::min(N > 0 || least == 1 ? W : units, most), force_ctas > 0 ? 0ll : least));
   if (force_ctas > 0) G = force_ctas;
   // The way that takes the fewest clocks by these measured figures (bf16 outputs, 152 SMs; other counts
   // of SMs take them over).  us for equal sequences of 64 rows and 4096 tokens, clusters / even / by
@@ -1223,7 +1225,13 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
     *parts_out = parts_at(lo);
     return lo;
   };
-  if (N > 0 && kind.is_tree) {
+  // (lengths past the plan's: CTAs take the slots' items in turn, as many as fit)
+  auto in_turn = [&](long long parts) { return force_ctas > 0 || units + parts - 1 <= kBMaxSeg * parts; };
+  if (kind.is_tree && N == 0 && units > 0 && force_ctas == 0) {
+    mode = MFA_PLAN_UNIT_CLUSTERS;
+    per_cta = 1;
+    G = units;
+  } else if (N > 0 && kind.is_tree) {
     // The same for a tree's units, but without clusters: whole units, a CTA each and as many CTAs as units (in
     // turn where they are more than the SMs), or cut evenly, or by cost.  In clocks, as measured.
     const long long tree_tile = pr->head_dim == 256 ? 2700 : 1950, begin = 10000;   // a tile; a unit's beginning and end
@@ -1240,7 +1248,7 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
     if (N <= most) {
       long long parts = 0;
       const long long q = even_quantum(&parts);
-      if (q * tree_tile + begin + tree_combine(parts) < best) {
+      if (q * tree_tile + begin + tree_combine(parts) < best && in_turn(parts)) {
         mode = MFA_PLAN_EVEN_SPLIT;
         per_cta = static_cast<int>(q);
         G = parts;
@@ -1260,7 +1268,7 @@ static mfa_status block_plan(const mfa_problem* pr, const BlockKind& kind, const
     if (N <= most) {
       long long parts = 0;
       const long long q = even_quantum(&parts);
-      if (q * tile + combine(parts) < best) {
+      if (q * tile + combine(parts) < best && in_turn(parts)) {
         mode = MFA_PLAN_EVEN_SPLIT;
         per_cta = static_cast<int>(q);
         G = parts;
