@@ -49,6 +49,12 @@ constexpr int kNormThreads = 288;        // of a CTA that have heads, at most; w
 // path for any shape).
 enum NormPairs { kPairsNext, kPairsVectors, kPairsFar };
 constexpr int kNormAnyThreads = 256;     // of a CTA of the path for any shape
+// The weights' gradient: where a thread's fp32 sum would have more terms than this, it is added to one in 64 bits and begins
+// anew after so many, or after those of 36 rows, if they are more.  (One sum over all of a thread's rows is off by up to 2^-24
+// a term: 2^21 equal rows, 6900 terms, by 9e-5 of itself.  65536 rows of 65 heads of 256 take 1136 us with, 1130 without; other
+// widths and types 2 to 4% more.)
+constexpr int kNormTerms = 256;
+constexpr int kNormGradRows = 4;         // rows of a CTA from one meeting to the next, in the gradient on the wide path
 
 struct NormSide {
   const void* x;
@@ -72,6 +78,7 @@ struct NormParams {
   float* partial;                       // gradient: [CTAs][q, k][head_dim]
   float* dw[2];                         // gradient of the weights
   int parts;                            // CTAs that leave partial sums
+  int fold;                             // rows (wide path: meetings) that a thread's sum goes over; 0: all
 };
 
 template <typename T>
@@ -170,7 +177,7 @@ __device__ __forceinline__ float sum_f32x2(uint64_t v) {
 // A CTA takes rows blockIdx.x, + gridDim.x, ... (with few rows, of each the share blockIdx.y of its heads).  Each thread copies its elements of the next kDepth heads,
 // of this row and those after it, into shared memory of its own ahead of their use, without registers and
 // without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
-// In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows; each
+// In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows (kNormTerms); each
 // CTA leaves one partial sum a side and element, and a second kernel adds those in a fixed order.
 template <typename T, NormPairs kPairs, bool kGrad>
 struct NormRing {
@@ -178,7 +185,7 @@ struct NormRing {
   static constexpr int kVectors = sizeof(T) / 2;                      // 16-byte vectors of 8 elements
   static constexpr int kParts = (kHalf ? 2 : 1) * (kGrad ? 2 : 1);    // x's first and second halves, dy's
   // rows from one meeting to the next (prompt of 8191 rows 86 us at 1, 93 at 4; its gradient 203 and 155)
-  static constexpr int kAngleRows = kGrad ? 4 : 1;
+  static constexpr int kAngleRows = kGrad ? kNormGradRows : 1;
   static constexpr int kDepth = 16 / (kVectors * (kGrad ? 4 : 2));    // heads ahead: up to 256 bytes a thread
   static constexpr int kVectorBytes = kNormThreads * 16;              // all threads' vector of one part
   static constexpr int kPartBytes = kVectors * kVectorBytes, kStageBytes = kParts * kPartBytes, kBytes = kDepth * kStageBytes;
@@ -196,7 +203,8 @@ __device__ __forceinline__ void load_pairs_again(const float* from, int pitch, u
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2]), "=l"(v[3]) : "r"(smem_u32(from + pitch)));
 }
 
-template <typename T, NormPairs kPairs, bool kGrad>
+// kFold: the gradient with sums of many terms (instances of their own: their code costs the others registers).
+template <typename T, NormPairs kPairs, bool kGrad, bool kFold>
 __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(const __grid_constant__ NormParams p) {
   using Ring = NormRing<T, kPairs, kGrad>;
   constexpr bool kHalf = kPairs == kPairsVectors, kFar = kPairs == kPairsFar;
@@ -335,6 +343,37 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
   const float* my_wa = &sw[at.on_q ? 0 : 1][0][4 * at.u];
   const float* my_wb = &sw[at.on_q ? 0 : 1][1][4 * at.u];
   uint64_t da[4] = {}, db[4] = {};   // the weights' gradient, of this thread's elements
+  // Where they are many: the CTA's sums of both sides, in 64 bits, behind the ring.  A warp's threads add theirs to them, its
+  // groups in turn, and begin anew; one warp between two meetings.
+  double* const sums = reinterpret_cast<double*>(ring + Ring::kBytes);
+  if constexpr (kFold) {
+    for (int e = tid; e < 2 * d; e += threads) sums[e] = 0.;   // (before the first meeting)
+  }
+  auto fold = [&]() {
+    double* const own = sums + (at.on_q ? 0 : d) + at.a0;
+    const int here = (tid >> p.log_lanes) & ((32 >> p.log_lanes) - 1);
+#pragma unroll 1
+    for (int g = 0; g < 32 >> p.log_lanes; ++g) {
+      if (g == here && at.active) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int v = kVectors == 2 ? j / 2 : 0;
+          double* const to = own + at.from[v] + (kVectors == 2 ? 2 * (j & 1) : 2 * j);
+          float lo, hi;
+          unpack_f32x2(da[j], lo, hi);
+          to[0] += lo, to[1] += hi;
+          if (at.two[v]) {
+            unpack_f32x2(db[j], lo, hi);
+            to[second] += lo, to[second + 1] += hi;
+          }
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) da[j] = db[j] = 0;
+  };
+  [[maybe_unused]] int turn = 0;   // the warp that folds next
   int buffer = 0;
   if (angles) {   // rows ahead, so that their loads' way is nobody's wait
 #pragma unroll 1
@@ -514,6 +553,10 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
       __syncthreads();   // the next rows' angles are there, and these rows' may be written over
       in_chunk = 0;
       buffer ^= 1;
+      if constexpr (kFold) {
+        if (turn == tid >> 5) fold();
+        if (++turn == p.fold) turn = 0;
+      }
     }
   }
   if constexpr (kGrad) {
@@ -538,6 +581,7 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
       const int from = on_k ? p.q.slots : 0, to = on_k ? p.q.slots + p.k.slots : p.q.slots;
       float v = 0.f;
       for (int x = from; x < to; ++x) v += red[x * d + (on_k ? e - d : e)];
+      if constexpr (kFold) v = static_cast<float>(sums[e] + v);
       p.partial[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * d + e] = v;
     }
   }
@@ -572,10 +616,11 @@ __global__ void __launch_bounds__(256) mfa_norm_rope_weights_kernel(const __grid
 // Heads of odd sizes or too many units, unaligned rows: a warp a head, a lane its every 32nd element and that element's
 // partner in the pair.  Bound by its loads' latency: 2000 rows of 26 heads of 256, 100 elements turned, half pairing,
 // gradient: 72 us (184 with registers for heads of 512, one CTA on an SM; 31 on the wide path).
-template <typename T, bool kGrad, int kEach>
+template <typename T, bool kGrad, bool kFold, int kEach>
 __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_rope_any_kernel(const __grid_constant__ NormParams p) {
   __shared__ __align__(16) float cs[2][2][kRopeMaxDim / 2];
-  extern __shared__ float red[];   // gradient: [warps][head_dim]
+  extern __shared__ __align__(16) uint8_t any_smem[];   // gradient: [warps][head_dim], with sums of many terms in 64 bits before it
+  float* const red = reinterpret_cast<float*>(any_smem) + (kFold ? 2 * (p.q.slots + p.k.slots) * p.head_dim : 0);
   grid_dep_wait();
   if constexpr (!kGrad) grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -584,6 +629,17 @@ __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_
   const int h0 = on_q ? warp : warp - p.q.slots, step = side.slots;
   const int r2 = 2 * p.pairs;
   float dw[kEach] = {};
+  // where a thread's sums are many: the sum of them, in 64 bits, as on the wide path
+  double* const sums = reinterpret_cast<double*>(any_smem) + warp * p.head_dim + lane;
+  auto fold = [&](bool first) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (lane + 32 * i < p.head_dim) sums[32 * i] = first ? 0. : sums[32 * i] + dw[i];
+      dw[i] = 0.f;
+    }
+  };
+  if constexpr (kFold) fold(true);
+  [[maybe_unused]] int to_fold = p.fold;
   int buffer = 0;
 #pragma unroll 1
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
@@ -636,13 +692,19 @@ __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_
         }
       }
     }
+    if constexpr (kFold) {
+      if (--to_fold == 0) {
+        fold(false);
+        to_fold = p.fold;
+      }
+    }
   }
   if constexpr (kGrad) {
     grid_dep_launch();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int e = lane + 32 * i;
-      if (e < p.head_dim) red[warp * p.head_dim + e] = dw[i];
+      if (e < p.head_dim) red[warp * p.head_dim + e] = kFold ? static_cast<float>(sums[32 * i] + dw[i]) : dw[i];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * p.head_dim; e += blockDim.x) {
@@ -700,31 +762,39 @@ static void norm_slots(NormParams& p, int room) {
 
 // The wide path's kernel, and its shared memory in cfg.
 template <typename T, NormPairs kPairs>
-static void (*wide_norm(bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
+static void (*wide_norm(const NormParams& p, bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
   cfg.dynamicSmemBytes = grad ? NormRing<T, kPairs, true>::kBytes : NormRing<T, kPairs, false>::kBytes;
-  return grad ? mfa_norm_rope_kernel<T, kPairs, true> : mfa_norm_rope_kernel<T, kPairs, false>;
+  if (p.fold > 0) cfg.dynamicSmemBytes += 16 * static_cast<size_t>(p.head_dim);
+  return p.fold > 0 ? mfa_norm_rope_kernel<T, kPairs, true, true>
+         : grad     ? mfa_norm_rope_kernel<T, kPairs, true, false>
+                    : mfa_norm_rope_kernel<T, kPairs, false, false>;
 }
 template <typename T>
-static void (*wide_norm(NormPairs pairs, bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
-  return pairs == kPairsNext      ? wide_norm<T, kPairsNext>(grad, cfg)
-         : pairs == kPairsVectors ? wide_norm<T, kPairsVectors>(grad, cfg)
-                                  : wide_norm<T, kPairsFar>(grad, cfg);
+static void (*wide_norm(NormPairs pairs, const NormParams& p, bool grad, cudaLaunchConfig_t& cfg))(NormParams) {
+  return pairs == kPairsNext      ? wide_norm<T, kPairsNext>(p, grad, cfg)
+         : pairs == kPairsVectors ? wide_norm<T, kPairsVectors>(p, grad, cfg)
+                                  : wide_norm<T, kPairsFar>(p, grad, cfg);
 }
 
 // The kernel for any shape: a lane's elements of a head (up to 256: fewer registers, three CTAs on an SM).
+template <typename T, int kEach>
+static void (*any_norm(bool grad, bool fold))(NormParams) {
+  return fold   ? mfa_norm_rope_any_kernel<T, true, true, kEach>
+         : grad ? mfa_norm_rope_any_kernel<T, true, false, kEach>
+                : mfa_norm_rope_any_kernel<T, false, false, kEach>;
+}
 template <typename T>
-static void (*any_norm(bool grad, int head_dim))(NormParams) {
-  if (head_dim <= 256) return grad ? mfa_norm_rope_any_kernel<T, true, 8> : mfa_norm_rope_any_kernel<T, false, 8>;
-  return grad ? mfa_norm_rope_any_kernel<T, true, 16> : mfa_norm_rope_any_kernel<T, false, 16>;
+static void (*any_norm(const NormParams& p, bool grad))(NormParams) {
+  return p.head_dim <= 256 ? any_norm<T, 8>(grad, p.fold > 0) : any_norm<T, 16>(grad, p.fold > 0);
 }
 
 // cudaFuncSetAttribute for a wide kernel's dynamic shared memory, once per device and kernel.
 static mfa_status ensure_norm_smem(int i, const void* fn, int dev) {
   constexpr int kMaxDevices = 64;
-  static std::atomic<bool> done[12][kMaxDevices];
+  static std::atomic<bool> done[18][kMaxDevices];
   const bool cacheable = dev >= 0 && dev < kMaxDevices;
   if (cacheable && done[i][dev].load(std::memory_order_acquire)) return MFA_OK;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormThreads * 256);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormThreads * 256 + 16 * kRopeMaxDim);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   if (cacheable) done[i][dev].store(true, std::memory_order_release);
   return MFA_OK;
@@ -805,20 +875,30 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
     int ctas = std::min({num_rows, 2 * sms, MFA_NORM_ROPE_GRAD_PARTS});
     int shares = 1;
     void (*fn)(NormParams);
+    // Where a thread's sum of the weights' gradient would have too many terms: the times between two folds of a warp's sums,
+    // each time after so many rows, and at least so many times (for as many warps to take turns).
+    auto set_fold = [&](int rows_at_once, int least) {
+      auto each = [&](int heads, int slots) { return slots > 0 ? (heads + slots * shares - 1) / (slots * shares) : 0; };
+      const int row = std::max(each(q.heads, p.q.slots), each(k.heads, p.k.slots));   // a row's terms
+      if (grad && (static_cast<long long>(num_rows) + ctas - 1) / ctas * row > kNormTerms)
+        p.fold = std::max(least, kNormTerms / row / rows_at_once);
+    };
     if (wide) {
       norm_slots(p, kNormThreads >> p.log_lanes);
       // few rows: a row's heads shared by CTAs, as far as there is room and each slot has a head
       const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1, p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
       shares = std::max(1, std::min({rounds, std::min(2 * sms, MFA_NORM_ROPE_GRAD_PARTS) / ctas, 65535}));
       cfg.blockDim = dim3(static_cast<unsigned>((((p.q.slots + p.k.slots) << p.log_lanes) + 31) / 32 * 32 + 32), 1, 1);
-      fn = bf16 ? wide_norm<__nv_bfloat16>(pairs, grad, cfg) : wide_norm<float>(pairs, grad, cfg);
-      if ((st = ensure_norm_smem((bf16 ? 0 : 6) + 2 * pairs + grad, reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
+      set_fold(kNormGradRows, static_cast<int>(cfg.blockDim.x) / 32 - 1);
+      fn = bf16 ? wide_norm<__nv_bfloat16>(pairs, p, grad, cfg) : wide_norm<float>(pairs, p, grad, cfg);
+      if ((st = ensure_norm_smem((bf16 ? 0 : 9) + 3 * pairs + grad + (p.fold > 0), reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
     } else {
       norm_slots(p, kNormAnyThreads / 32);
       cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) * 32), 1, 1);
-      fn = bf16 ? any_norm<__nv_bfloat16>(grad, p.head_dim) : any_norm<float>(grad, p.head_dim);
       ctas = std::min(num_rows, grad ? std::min(3 * sms, MFA_NORM_ROPE_GRAD_PARTS) : 6 * sms);
-      if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * 4;   // (8 warps x 512 at most)
+      set_fold(1, 1);
+      fn = bf16 ? any_norm<__nv_bfloat16>(p, grad) : any_norm<float>(p, grad);
+      if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * (p.fold > 0 ? 12 : 4);   // (8 warps x 512 at most)
     }
     p.parts = grad ? ctas * shares : 0;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(shares), 1);

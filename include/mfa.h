@@ -674,8 +674,9 @@ typedef struct mfa_norm_grad_rows {
  *     dx = r (g w - h sum(g w h) / head_dim),   dw = sum over the rows and a side's heads of g h.
  *   config .. norm : as given to the forward call, whose r is computed again from x.
  *   q_weight_grad, k_weight_grad : device fp32 [head_dim], written (zeros without rows or heads), or
- *               NULL.  Summed in fp32 in an order that depends on the sizes and the device alone: the same call
- *               gives the same bits.
+ *               NULL.  Summed in fp32, however many the rows (after some 256 terms a thread's sum goes to
+ *               one in 64 bits), in an order that depends on the sizes and the device alone: the same
+ *               call gives the same bits.
  *   workspace : device, 16-byte aligned, >= MFA_NORM_ROPE_GRAD_BYTES(head_dim) bytes; scratch.
  *               Two calls that may overlap on the GPU need one each.
  */
