@@ -127,9 +127,6 @@ __host__ __device__ __forceinline__ BlockView block_view(int L, int tokens, int 
   return v;
 }
 // The tokens that a sequence of L has to go over.
-__device__ __forceinline__ int block_length(const BlockDecodeParams& p, int L) {
-  return p.window > 0 ? block_view(L, p.tokens, p.window, p.sinks).L : L;
-}
 template <bool kWindow>
 __device__ __forceinline__ int view_length(const BlockDecodeParams& p, int L) {
   if constexpr (kWindow) return block_view(L, p.tokens, p.window, p.sinks).L;
@@ -160,11 +157,12 @@ __device__ __forceinline__ int even_parts(int T, int quantum) {
 }
 // A quantum with which the units' parts are no more than the slots: with W tiles in N units
 // (all readers), sum ceil(T / q) <= W / q + N, and W / q <= slots - N.  (One warp; out of the way.)
-static __device__ __noinline__ int wider_quantum(const BlockDecodeParams& p, int cap) {
+template <bool kWindow>
+__device__ __noinline__ int wider_quantum(const BlockDecodeParams& p, int cap) {
   long long tiles = 0, units = 0;
   bool bad = false;
   for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
-    const int T = (block_length(p, clamp_len(p.seq_lens[b], cap, bad)) + kBTile - 1) / kBTile;
+    const int T = (view_length<kWindow>(p, clamp_len(p.seq_lens[b], cap, bad)) + kBTile - 1) / kBTile;
     tiles += T;
     units += T > 0;
   }
@@ -292,14 +290,14 @@ __device__ __forceinline__ void even_segments(const BlockDecodeParams& p, int ca
       }
     }
     if (carry <= p.num_partials) return;
-    quantum = wider_quantum(p, cap);
+    quantum = wider_quantum<kWindow>(p, cap);
     nseg = tiles = 0;
   }
 }
 
-// I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).  kGrown: with a
-// boundary's cost of `boundary`; else of kBCostUnit, and false where a CTA's range could then hold too many units.
-template <typename I, bool kWindow, bool kGrown>
+// I: the type that holds G times the whole cost (32 bits nearly always: its divisions are short).  With a boundary's cost of
+// `boundary`; in 32 bits false where a CTA's range could then hold too many units.
+template <typename I, bool kWindow>
 __device__ __forceinline__ bool cost_segments(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                               bool& bad, I boundary) {
   const int lane = threadIdx.x & 31;
@@ -315,7 +313,7 @@ __device__ __forceinline__ bool cost_segments(const BlockDecodeParams& p, int ca
   // the whole cost; with less of it than a tile for each CTA the last CTAs have nothing, so that
   // no CTA lies between two tiles
   const I total = per * p.readers - boundary;
-  if (!kGrown && (total - 1) / kBMaxShare >= gridDim.x) return false;
+  if (sizeof(I) == 4 && (total - 1) / kBMaxShare >= gridDim.x) return false;
   const I G = min(static_cast<I>(gridDim.x), total / kBCostTile), g = blockIdx.x;
   if (g >= G) return true;
   const I X0 = g * total / G, X1 = (g + 1) * total / G;
@@ -353,12 +351,14 @@ __device__ __forceinline__ bool cost_segments(const BlockDecodeParams& p, int ca
   return true;
 }
 // A boundary's cost c with which no CTA's range holds more than kBMaxSeg units: units begin at least 4 + c apart, so a
-// range of X holds ceil(X / (4 + c)) + 1 at most, and with W tiles in N units X <= (4 W + c (N - 1)) / G + 1.  There is
-// one where N - 1 <= (kBMaxSeg - 2) G, which a plan sees to unless its grid is forced.
+// range of X holds ceil(X / (4 + c)) + 1 at most, and with W tiles in N units X <= (4 W + c (N - 1)) / G + 1.  The usual c
+// where that does, or where units are few; and with too few CTAs (N - 1 > (kBMaxSeg - 2) G), which a plan makes only where its
+// grid is forced.
 template <bool kWindow>
-__device__ __noinline__ long long grown_boundary(const BlockDecodeParams& p, int cap) {
+__device__ __forceinline__ long long grown_boundary(const BlockDecodeParams& p, int cap) {
   long long tiles = 0, units = 0;
   bool bad = false;
+#pragma unroll 1
   for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
     const int T = block_tiles(view_length<kWindow>(p, clamp_len(p.seq_lens[b], cap, bad)));
     tiles += T;
@@ -372,16 +372,16 @@ __device__ __noinline__ long long grown_boundary(const BlockDecodeParams& p, int
   tiles *= p.readers;
   units *= p.readers;
   const long long G = gridDim.x, spare = (kBMaxSeg - 1) * G - (units - 1);
-  if (units <= kBMaxSeg || spare < 1) return kBCostUnit;   // (few units; too few CTAs for so many)
-  const long long over = kBCostTile * (tiles - (kBMaxSeg - 1) * G);
-  return max((over + spare - 1) / spare, static_cast<long long>(kBCostUnit));
+  if (units <= kBMaxSeg || spare < 1 || kBCostTile * tiles + kBCostUnit * (units - 1) <= kBMaxShare * G) return kBCostUnit;
+  return max((kBCostTile * (tiles - (kBMaxSeg - 1) * G) + spare - 1) / spare, static_cast<long long>(kBCostUnit));
 }
-// The wide form, for problems of millions of tiles and lengths far past the plan's, out of the way of the usual one's code.
+// The wide form, for problems of millions of tiles and lengths far past the plan's, out of the way of the usual one's code and
+// in one copy: waits for instructions are a part of the decode's time (61 ragged sequences, two new tokens: 65.7 us, 67.8 with
+// two copies, 68.1 with the usual form out of line too).
 template <bool kWindow>
 __device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                                 bool& bad) {
-  if (!cost_segments<long long, kWindow, false>(p, cap, seg, nseg, tiles, bad, kBCostUnit))
-    cost_segments<long long, kWindow, true>(p, cap, seg, nseg, tiles, bad, grown_boundary<kWindow>(p, cap));
+  cost_segments<long long, kWindow>(p, cap, seg, nseg, tiles, bad, grown_boundary<kWindow>(p, cap));
 }
 
 // A unit's CTAs: only its own sequence's length is read.
@@ -407,7 +407,7 @@ __device__ __forceinline__ void block_segments(const BlockDecodeParams& p, int c
     unit_segment<kWindow>(p, cap, seg, nseg, tiles, bad);
   else if (p.quantum > 0)
     even_segments<kWindow>(p, cap, seg, nseg, tiles, bad);
-  else if (!p.narrow || !cost_segments<uint32_t, kWindow, false>(p, cap, seg, nseg, tiles, bad, kBCostUnit))
+  else if (!p.narrow || !cost_segments<uint32_t, kWindow>(p, cap, seg, nseg, tiles, bad, kBCostUnit))
     cost_segments_wide<kWindow>(p, cap, seg, nseg, tiles, bad);
   if (bad) atomicOr(p.status, MFA_DEV_BAD_LENGTH);
   tiles = __reduce_add_sync(0xffffffffu, tiles);

@@ -927,7 +927,7 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
 constexpr int kBHeld = 5;               // a lane's parts whose lse stays in a register
 constexpr int kBChunk = 32 * kBHeld;    // parts whose weights are held at a time
 
-template <int kDim, int kTeams>
+template <int kDim, int kTeams, bool kWindow>
 __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
   constexpr int kSlice = kDim < kBCombineThreads / kTeams ? kDim : kBCombineThreads / kTeams;   // elements of a CTA
   constexpr int kOcts = kBCombineThreads / (kTeams * kSlice);                                   // groups of eight rows
@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
   int2 at = make_int2(0, -1);
   const int cap = p.max_pages * kBPage;
   bool bad = false;
-  const int T = block_tiles(block_length(p, clamp_len(p.seq_lens[b], cap, bad)));
+  const int T = block_tiles(view_length<kWindow>(p, clamp_len(p.seq_lens[b], cap, bad)));
   if (p.quantum > 0) {
     int quantum = p.quantum;
 #pragma unroll 1
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
       long long all = 0;     // and of all
 #pragma unroll 1
       for (int i = lane; i < p.batch; i += 32) {
-        const int n = even_parts(block_tiles(block_length(p, clamp_len(p.seq_lens[i], cap, bad))), quantum);
+        const int n = even_parts(block_tiles(view_length<kWindow>(p, clamp_len(p.seq_lens[i], cap, bad))), quantum);
         all += n;
         before += i < b ? n : 0;
       }
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
         if (n > 1) at = make_int2(first_part, first_part + n - 1);
         break;
       }
-      quantum = wider_quantum(p, cap);
+      quantum = wider_quantum<kWindow>(p, cap);
     }
   }
   const int kvh = r / p.token_groups, tg = r - kvh * p.token_groups;
@@ -1086,6 +1086,13 @@ __global__ void __launch_bounds__(kBCombineThreads, 3) mfa_block_combine_kernel(
 // ------------------------------------------------------------------ host side
 
 using BlockCombineFn = void (*)(BlockDecodeParams);
+// The combine for 1, 2, 4 or 8 teams.
+template <int kDim, bool kWindow>
+static BlockCombineFn combine_kernel(int i) {
+  constexpr BlockCombineFn k[4] = {mfa_block_combine_kernel<kDim, 1, kWindow>, mfa_block_combine_kernel<kDim, 2, kWindow>,
+                                   mfa_block_combine_kernel<kDim, 4, kWindow>, mfa_block_combine_kernel<kDim, 8, kWindow>};
+  return k[i];
+}
 
 // The instance of a problem: width and rows padded to 16, 32 or 64.
 static int block_instance(const mfa_problem* pr, const BlockShape& sh, bool window, bool tree) {
@@ -1417,12 +1424,9 @@ static mfa_status block_run(const mfa_plan* plan, const mfa_problem* pr, int32_t
                        static_cast<unsigned>(pr->head_dim / slice));
     cfg.blockDim = dim3(kBCombineThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    const BlockCombineFn wide[] = {mfa_block_combine_kernel<256, 1>, mfa_block_combine_kernel<256, 2>,
-                                   mfa_block_combine_kernel<256, 4>, mfa_block_combine_kernel<256, 8>};
-    const BlockCombineFn narrow[] = {mfa_block_combine_kernel<128, 1>, mfa_block_combine_kernel<128, 2>,
-                                     mfa_block_combine_kernel<128, 4>, mfa_block_combine_kernel<128, 8>};
     const int at = teams == 8 ? 3 : teams / 2;
-    const BlockCombineFn fn = pr->head_dim == 256 ? wide[at] : narrow[at];
+    const BlockCombineFn fn = pr->head_dim == 256 ? (window ? combine_kernel<256, true>(at) : combine_kernel<256, false>(at))
+                                                  : (window ? combine_kernel<128, true>(at) : combine_kernel<128, false>(at));
     e = cudaLaunchKernelEx(&cfg, fn, p);
     if (e != cudaSuccess) return cuda_fail(e, "block combine launch");
   }
