@@ -834,7 +834,7 @@ class TreeDecoder(BlockDecoder):
     before the tree, and node j where bit j of its mask is set.  The other arguments, the cache and the rules of
     streams and workspaces are those of BlockDecoder.  A shorter tree takes its nodes first and masks that leave
     out the rest.  Once some nodes are accepted, ``append`` their rows again from the tree's first position, and
-    the cache goes on behind them.
+    the cache goes on behind them.  (Blocks whose scale a rejected node's row has raised keep that scale.)
     """
 
     def __init__(self, batch: int, max_pages_per_seq: int, num_blocks: int, tree_tokens: int, num_q_heads: int = NUM_Q_HEADS,

@@ -9,7 +9,7 @@
 // A unit is a sequence, a key/value head and as many new tokens as fit 64 rows (tokens x the head's
 // query heads); a tile is 128 tokens.  Both contractions run on the codes as they lie in the cache:
 //   S^T [128 tokens x rows] = K Q^T, q split into e4m3 hi + lo parts under one power of two a row
-//     (exact, but for elements under 2^-9 of the row's largest, which err by 2^-16 of it), in
+//     (exact, but for elements under 2^-8 of the row's largest, which err by up to 2^-16 of it), in
 //     columns of their own; a token's key scale multiplies its fp32 scores;
 //   O^T [128 of d x rows] += V^T P^T, the weights (with the token's value scale) split likewise.
 // Tokens as the MMAs' M = 128 keep the tensor core full however few the rows, and let a softmax

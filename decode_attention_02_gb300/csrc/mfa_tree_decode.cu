@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           uint64_t bd = smem_desc(base + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
           uint64_t ad = smem_desc(base + Lay::kOffQ, 16, 1024);
           // The product that reads the weights where these scores go is complete: two warps' MMAs into different
-          // accumulators have no order but this.  (Issued was not enough, and 58.2 us against 59.5 for eight of 4096 tokens.)
+          // accumulators have no order but this.  (Issued was not enough, and 57.8 us against 60.0 for eight of 4096 tokens.)
           if (ok && n >= 2) ok = wait_all(bar(kPvDone + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           }
 #pragma unroll
           for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          int sig = 0;   // the row's largest |q| goes to [128, 256): what is under 2^-10 of it errs by 2^-17 of it
+          int sig = 0;   // the row's largest |q| goes to [128, 256): what is under 2^-9 of it errs by up to 2^-17 of it
           if (m > 0.f) sig = min(126, max(-126, 7 + 127 - static_cast<int>(__float_as_uint(m) >> 23)));
           const float up = __uint_as_float(static_cast<uint32_t>(127 + sig) << 23);
 #pragma unroll

@@ -440,7 +440,8 @@ mfa_status mfa_block_decode_plan(const mfa_problem* problem, int32_t scale_token
  * Sums and lse are fp32.  A weight times its value scale is rounded to 8 significant bits (with
  * fp32 outputs too), the smallest of a row more coarsely: to 2^-16 of the largest about them, which
  * is followed along the sequence, so that thousands of small weights behind a far larger one keep
- * theirs.  Value scales under 2^-50 count as 2^-50 there.
+ * theirs.  Value scales under 2^-50 count as 2^-50 there.  An element of q under 2^-8 of its row's
+ * largest is off by up to 2^-16 of that (with a window: under 2^-12, by 2^-20).
  * A NaN code among the keys makes the rows that see its token NaN, one among the values their
  * element; a NaN among the values of a sequence's T newest tokens may also reach, in its head and
  * element, the rows of new tokens before it.
@@ -526,6 +527,9 @@ mfa_status mfa_window_decode_run(const mfa_plan* plan, const mfa_problem* proble
  * is set: usually its ancestors and itself.  Any mask is taken (bits from T on count for nothing; a
  * node whose mask is 0 sees what is before the tree); in a sequence of fewer than T tokens the nodes at
  * negative positions are not there.  A row that sees nothing gets out = 0 and lse = -inf.
+ * The append of the nodes may raise the scales of the blocks that they lie in, and code those blocks' older rows
+ * again; the accepted nodes' rows, appended once more, keep the raised scale.  So rejected nodes leave a trace
+ * there: what falls below e4m3's smallest step under the larger power of two.
  */
 #define MFA_TREE_MAX_NODES 64
 
@@ -540,10 +544,11 @@ mfa_status mfa_tree_decode_plan(const mfa_problem* problem, int32_t scale_tokens
  * As mfa_block_decode_run, with
  *   q, out, lse  : [B, T, num_q_heads, d] and [B, T, num_q_heads];
  *   tree         : device uint64 [B, T], 8-byte aligned.
- * Sums and lse are fp32.  A weight times its value scale is rounded to 7 significant bits (with fp32 outputs
- * too); one under 2^-3 of its row's largest of the 128 tokens about it may be rounded more coarsely, at
- * worst to 2^-3 of itself, 2^-10 of that largest at most, and 2^-14 of it is the smallest that is sure to
- * count.  Value scales under 2^-50 count as 2^-50 there.
+ * Sums and lse are fp32.  A weight times its value scale, W, is rounded (with fp32 outputs too) relative to
+ * its row's largest of the 128 tokens about it, M: to 7 significant bits where W >= 2^-4 M; a smaller one is
+ * off by at most 2^-3 of itself or 2^-14 M, whichever is more, and by no more than 2^-11 M.  Where M is under
+ * 2^-27 of the row's largest W before it, that takes M's place.  Value scales under 2^-50 count as 2^-50 there.
+ * An element of q under 2^-9 of its row's largest is off by up to 2^-17 of that.
  * A NaN code among the keys makes the rows that see its token NaN.  One among the values of a token
  * before the tree makes its element NaN; among those of the tree's T tokens it may also reach, in its
  * head and element, the rows that do not see it.
