@@ -66,8 +66,8 @@ EXPORTED_SYMBOLS = ("mfa_decode_plan", "mfa_decode_run", "mfa_combine", "mfa_rea
                     "mfa_status_string", "mfa_abi_version", "mfa_last_cuda_error",
                     "mfa_decode_run_static_workspace", "mfa_kv_append", "mfa_decode_run_host",
                     "mfa_decode_append_run", "mfa_block_decode_plan", "mfa_block_decode_run", "mfa_block_kv_append",
-                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_tree_decode_plan", "mfa_tree_decode_run", "mfa_rope_table", "mfa_rope_run",
-                    "mfa_norm_rope_run", "mfa_norm_rope_grad_run")
+                    "mfa_window_decode_plan", "mfa_window_decode_run", "mfa_tree_decode_plan", "mfa_tree_decode_run",
+                    "mfa_rope_table", "mfa_rope_run", "mfa_norm_rope_run", "mfa_norm_rope_grad_run")
 
 # Size of the library's own scratch array used by mfa_decode_run_static_workspace.
 MFA_STATIC_WORKSPACE_BYTES = 24 * 1024 * 1024

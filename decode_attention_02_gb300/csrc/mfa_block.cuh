@@ -106,9 +106,10 @@ struct BlockDecodeParams {
 // those rows of the values.
 //
 // What bounds it: a window's cache is read from the first row that counts (41 us of bytes for 128 sequences
-// with windows of 4096, 64 heads of 256: 58 us, 52 without a window, on a kernel that has less to do at a
-// tile's edges; grouped heads, 32 x 1024 of 16K to 128K tokens: 16.4 us, one sequence of 128 tokens 14.4, a
-// chain of latencies both).  The way there, for the 128: the edge looked for in every tile 74 us, edge tiles
+// with windows of 4096, 64 heads of 256: 55.5 us, 51.1 without a window, on a kernel that has less to do at a
+// tile's edges; grouped heads, 32 x 1024 of 16K to 128K tokens: 13.5 us, one sequence with a window of 128 11.5 and
+// of 512 without one 11.1, a chain of latencies both; in a graph of twelve calls over three states).  The way
+// there, for the 128 (a graph of one call, some 3 us more): the edge looked for in every tile 74 us, edge tiles
 // known a segment ahead and the others' plain path 62, MMAs issued by a converged warp 57.4, q's lo part 16
 // times larger (one multiplication more, log sums of a few tokens to 1e-7) 58.3.
 struct BlockView {
@@ -376,8 +377,8 @@ __device__ __forceinline__ long long grown_boundary(const BlockDecodeParams& p, 
   return max((kBCostTile * (tiles - (kBMaxSeg - 1) * G) + spare - 1) / spare, static_cast<long long>(kBCostUnit));
 }
 // The wide form, for problems of millions of tiles and lengths far past the plan's, out of the way of the usual one's code and
-// in one copy: waits for instructions are a part of the decode's time (61 ragged sequences, two new tokens: 65.7 us, 67.8 with
-// two copies, 68.1 with the usual form out of line too).
+// in one copy: waits for instructions are a part of the decode's time (61 ragged sequences, two new tokens, a graph of one
+// call: 65.7 us, 67.8 with two copies, 68.1 with the usual form out of line too).
 template <bool kWindow>
 __device__ __noinline__ void cost_segments_wide(const BlockDecodeParams& p, int cap, BlockSegment* seg, int& nseg, int& tiles,
                                                 bool& bad) {

@@ -364,7 +364,8 @@ mfa_block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
             if (!ok) break;
             if (kWindow && gap.v >> 1 == j) {
               uint8_t* box = smem + Lay::kOffRing + (kKSlots + slot) * Lay::kSlotBytes + (gap.v & 1) * 8192;
-              for (int r = gap.from + (lane >> 3); r < gap.to; r += 4) *reinterpret_cast<uint4*>(box + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              for (int r = gap.from + (lane >> 3); r < gap.to; r += 4)
+                *reinterpret_cast<uint4*>(box + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
               __syncwarp();
             }

@@ -14,13 +14,14 @@
 // side, q or k, and multiplies its weights with the angles' cosines and sines once a row in the forward
 // pass.  All sums are fp32; outputs are rounded once.
 //
-// Measured, bf16 unless said (the bytes at the copy rate of 6.7 TB/s in brackets):
-//   8191 rows of 65 heads of 256, three axes: 88 us, 6.2 TB/s (82); 128 such rows 8.2 us, launch and one
+// Measured in a graph of twelve calls over three states, bf16 unless said (the bytes at the copy rate of 6.7 TB/s in
+// brackets):
+//   8191 rows of 65 heads of 256, three axes: 85 us, 6.4 TB/s (82); 128 such rows 4.8 us, launch and one
 //   chain of loads: positions and angles, the elements, two sums;
-//   its gradient 156 us, 5.2 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 23 us (16),
-//   4000 rows of 65 of 256 in fp32 91 us forward (80), 132 the gradient (120).
+//   its gradient 151 us, 5.4 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 22 us (16),
+//   4000 rows of 65 of 256 in fp32 90 us forward (80), 129 the gradient (120).
 // What bounds the gradient: issue slots as much as memory, some 13 instructions an element beside the loads.
-// The steps that carried it, the prompt / its gradient: plain loads, one CTA on an SM 188 / 272; arithmetic
+// The steps that carried it, the prompt / its gradient (replays of a graph of one call, some 3 us more each): plain loads, one CTA on an SM 188 / 272; arithmetic
 // in pairs, two CTAs 108 / 240; copies ahead into shared memory, free of bank conflicts, 105 / 203; angles
 // by a warp of their own 88 / -; values read from shared memory again in place of kept, and the CTA's
 // meetings one in four rows, - / 156.  Asking L2 for the next rows gained nothing; three CTAs on an SM (fewer registers
@@ -174,9 +175,9 @@ __device__ __forceinline__ float sum_f32x2(uint64_t v) {
 }
 // ------------------------------------------------------------------ forward and gradient
 //
-// A CTA takes rows blockIdx.x, + gridDim.x, ... (with few rows, of each the share blockIdx.y of its heads).  Each thread copies its elements of the next kDepth heads,
-// of this row and those after it, into shared memory of its own ahead of their use, without registers and
-// without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
+// A CTA takes rows blockIdx.x, + gridDim.x, ... (with few rows, of each the share blockIdx.y of its heads).  Each thread
+// copies its elements of the next kDepth heads, of this row and those after it, into shared memory of its own ahead of
+// their use, without registers and without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
 // In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows (kNormTerms); each
 // CTA leaves one partial sum a side and element, and a second kernel adds those in a fixed order.
 template <typename T, NormPairs kPairs, bool kGrad>
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(kNormThreads + 32, 2) mfa_norm_rope_kernel(con
 #pragma unroll
         for (int v = 0; v < kVectors; ++v) {
           *reinterpret_cast<uint4*>(to + at.from[v]) = make_uint4(y.w[4 * v], y.w[4 * v + 1], y.w[4 * v + 2], y.w[4 * v + 3]);
-          if (at.two[v]) *reinterpret_cast<uint4*>(to + second + at.from[v]) = make_uint4(z.w[4 * v], z.w[4 * v + 1], z.w[4 * v + 2], z.w[4 * v + 3]);
+          if (at.two[v])
+            *reinterpret_cast<uint4*>(to + second + at.from[v]) = make_uint4(z.w[4 * v], z.w[4 * v + 1], z.w[4 * v + 2], z.w[4 * v + 3]);
         }
       }
       if constexpr (kFar) __syncwarp(at.mask);   // (read by all)
@@ -886,19 +888,22 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
     if (wide) {
       norm_slots(p, kNormThreads >> p.log_lanes);
       // few rows: a row's heads shared by CTAs, as far as there is room and each slot has a head
-      const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1, p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
+      const int rounds = std::max(p.q.slots ? (q.heads + p.q.slots - 1) / p.q.slots : 1,
+                                  p.k.slots ? (k.heads + p.k.slots - 1) / p.k.slots : 1);
       shares = std::max(1, std::min({rounds, std::min(2 * sms, MFA_NORM_ROPE_GRAD_PARTS) / ctas, 65535}));
       cfg.blockDim = dim3(static_cast<unsigned>((((p.q.slots + p.k.slots) << p.log_lanes) + 31) / 32 * 32 + 32), 1, 1);
       set_fold(kNormGradRows, static_cast<int>(cfg.blockDim.x) / 32 - 1);
       fn = bf16 ? wide_norm<__nv_bfloat16>(pairs, p, grad, cfg) : wide_norm<float>(pairs, p, grad, cfg);
-      if ((st = ensure_norm_smem((bf16 ? 0 : 9) + 3 * pairs + grad + (p.fold > 0), reinterpret_cast<const void*>(fn), dev)) != MFA_OK) return st;
+      st = ensure_norm_smem((bf16 ? 0 : 9) + 3 * pairs + grad + (p.fold > 0), reinterpret_cast<const void*>(fn), dev);
+      if (st != MFA_OK) return st;
     } else {
       norm_slots(p, kNormAnyThreads / 32);
       cfg.blockDim = dim3(static_cast<unsigned>((p.q.slots + p.k.slots) * 32), 1, 1);
       ctas = std::min(num_rows, grad ? std::min(3 * sms, MFA_NORM_ROPE_GRAD_PARTS) : 6 * sms);
       set_fold(1, 1);
       fn = bf16 ? any_norm<__nv_bfloat16>(p, grad) : any_norm<float>(p, grad);
-      if (grad) cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * (p.fold > 0 ? 12 : 4);   // (8 warps x 512 at most)
+      if (grad)   // (8 warps x 512 at most)
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * (p.fold > 0 ? 12 : 4);
     }
     p.parts = grad ? ctas * shares : 0;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(shares), 1);

@@ -28,15 +28,18 @@
 //
 // What bounds it: a tile's products are 128 x 128 x d for S and as many for O, each twice (hi and lo), 2048
 // clocks of the tensor cores at d = 256; operands from shared memory are 192 KB of it and the tile's TMA
-// writes 64 KB, 2048 clocks at 128 bytes a clock.  The first tiles take 2200 clocks; under that load the card's
-// power brings its clock from 1.94 GHz to 1.4.  At d = 128 a tile takes 2000 to 2600 clocks: the
-// softmax's chain (scores, maxima, their exchange, exponentials, two conversions to eight bits, stores) in two warps a
-// scheduler, which issue in half of the clocks; the tensor cores are active for 1024.  A unit's beginning and end take 8 us
-// beside its tiles, a boundary inside a CTA's range 4 to 5, parts and their combine 5.  Eight trees of 32 nodes over 4096
-// tokens, 64 heads of 256 over one: 57.4 us (1.2 PFLOP/s of the products' 1.9 in bf16); seven ragged ones of 61
-// nodes 90.6 us; 48 of 8 nodes, 64 heads of 128 over four: 65.3 us (214 MB); one of 8 over 2048 tokens 18.5 us.
+// writes 64 KB, 2048 clocks at 128 bytes a clock.  A tile takes some 2760 clocks, at 1.93 GHz (read in the kernel, from
+// tile 8 to 24 of 32): beside the products the waits between scores, weights and products, of which some 130 are
+// the one for the product under the next scores.  At d = 128 a tile takes 2400 clocks: the softmax's chain (scores,
+// maxima, their exchange, exponentials, two conversions to eight bits, stores) in two warps a scheduler, which
+// issue in half of the clocks; the tensor cores are active for 1024.  A unit's beginning and end take 8 us
+// beside its tiles, a boundary inside a CTA's range 4 to 5, parts and their combine 5.
+// Measured in a graph of twelve calls over three states: eight trees of 32 nodes over 4096 tokens, 64 heads of 256
+// over one, 58.1 us (1.2 PFLOP/s of the products' 1.9 in bf16); seven ragged ones of 61 nodes, 29400 tokens, 103 us;
+// 48 of 8 nodes, 64 heads of 128 over four, 64.8 us (214 MB); one of 8 over 2048 tokens 14.9 us.
 // Measured for the 48, and slower: sixteen softmax warps, with half the registers, 79.2 us against 77.9 at the time;
-// warpgroups that take the tiles in turn, each with an accumulator of its own, 88; P and V as f16, V by the warps that keep O, 77.
+// warpgroups that take the tiles in turn, each with an accumulator of its own, 88 against 65; P and V as f16, V by
+// the warps that keep O, 77.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -143,7 +146,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
   float4* meta = reinterpret_cast<float4*>(moved + 8);       // [2 tiles][2 pages][4 blocks] {K, V scales, log2 of V's}
   int* ctl = reinterpret_cast<int*>(meta + 16);                     // tensor memory, abort flag, segments, tiles
   volatile int* abort_flag = ctl + 1;
-  static_assert(sizeof(BlockSegment) * kBMaxSeg + (2 * kTWgs + 2 + 3) * kTRows * 4 + 2 * kTFin * 4 + 8 * 4 + 16 * 16 + 16 + 512 <= kTMisc, "misc");
+  static_assert(sizeof(BlockSegment) * kBMaxSeg + (2 * kTWgs + 2 + 3) * kTRows * 4 + 2 * kTFin * 4 + 8 * 4 + 16 * 16 + 16 + 512 <=
+                    kTMisc, "misc");
   const uint32_t bars = sbase + Lay::kOffMisc + kTMisc - 512;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   // slots: K's, then V's
@@ -263,7 +267,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           uint64_t bd = smem_desc(base + Lay::kOffRing + slot * Lay::kSlotBytes, 16, 1024);
           uint64_t ad = smem_desc(base + Lay::kOffQ, 16, 1024);
           // The product that reads the weights where these scores go is complete: two warps' MMAs into different
-          // accumulators have no order but this.  (Issued was not enough, and 57.8 us against 60.0 for eight of 4096 tokens.)
+          // accumulators have no order but this.  (With a wait for its issue alone, which is not enough, the eight of
+          // 4096 tokens took 56.0 us against 58.1, the ragged ones 99.9 against 103, the 48 64.0 against 64.8.)
           if (ok && n >= 2) ok = wait_all(bar(kPvDone + (n & 1)), ((n >> 1) - 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -722,7 +727,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
           for (int i = 0; i < 4; ++i) {
             const int r = row - (lane & 3) + i;
             if (r < valid)
-              *reinterpret_cast<uint4*>(out + static_cast<size_t>(row_off[r]) * 2 + c * 2 + (lane & 3) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              *reinterpret_cast<uint4*>(out + static_cast<size_t>(row_off[r]) * 2 + c * 2 + (lane & 3) * 16) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
         } else {   // (parts: rows as they are in the outputs)
           exchange_quarters<8>(o);
@@ -731,7 +737,8 @@ __global__ void __launch_bounds__(kTThreads, 1) mfa_tree_decode_kernel(const __g
             const int r = row - (lane & 3) + i;
             float* to = whole ? reinterpret_cast<float*>(out) + row_off[r] : part + static_cast<size_t>(r) * kDim;
             if (r < valid) {
-              const uint4 x = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]), y = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
+              const uint4 x = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]);
+              const uint4 y = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
               *reinterpret_cast<uint4*>(to + c + (lane & 3) * 8) = x;
               *reinterpret_cast<uint4*>(to + c + (lane & 3) * 8 + 4) = y;
             }
@@ -855,8 +862,14 @@ cudaError_t launch_tree_combine(const BlockDecodeParams& p, int units, int ctas,
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   BlockDecodeFn fn;
-  if (head_dim == 256) fn = teams == 8 ? mfa_tree_combine_kernel<256, 8> : teams == 4 ? mfa_tree_combine_kernel<256, 4> : mfa_tree_combine_kernel<256, 1>;
-  else fn = teams == 8 ? mfa_tree_combine_kernel<128, 8> : teams == 4 ? mfa_tree_combine_kernel<128, 4> : mfa_tree_combine_kernel<128, 1>;
+  if (head_dim == 256)
+    fn = teams == 8   ? mfa_tree_combine_kernel<256, 8>
+         : teams == 4 ? mfa_tree_combine_kernel<256, 4>
+                      : mfa_tree_combine_kernel<256, 1>;
+  else
+    fn = teams == 8   ? mfa_tree_combine_kernel<128, 8>
+         : teams == 4 ? mfa_tree_combine_kernel<128, 4>
+                      : mfa_tree_combine_kernel<128, 1>;
   return cudaLaunchKernelEx(&cfg, fn, p);
 }
 

@@ -234,8 +234,9 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f8f6f4 (A from shared or, four 8-bit elements a column, from tensor memory) by a converged warp, one lane of which (lead != 0) issues: a branch around the instruction would keep
-// its descriptors out of the uniform registers.
+// kind::f8f6f4 (A from shared or, four 8-bit elements a column, from tensor memory) by a converged warp, one lane
+// of which (lead != 0) issues: a branch around the instruction would keep its descriptors out of the uniform
+// registers.
 __device__ __forceinline__ void umma_f8_ss_by(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
