@@ -21,12 +21,12 @@
 //   its gradient 151 us, 5.4 TB/s (122); that of 1021 rows of 68 heads of 128, fp32, 96 turned, 22 us (16),
 //   4000 rows of 65 of 256 in fp32 90 us forward (80), 129 the gradient (120).
 // What bounds the gradient: issue slots as much as memory, some 13 instructions an element beside the loads.
-// The steps that carried it, the prompt / its gradient (replays of a graph of one call, some 3 us more each): plain loads, one CTA on an SM 188 / 272; arithmetic
-// in pairs, two CTAs 108 / 240; copies ahead into shared memory, free of bank conflicts, 105 / 203; angles
-// by a warp of their own 88 / -; values read from shared memory again in place of kept, and the CTA's
-// meetings one in four rows, - / 156.  Asking L2 for the next rows gained nothing; three CTAs on an SM (fewer registers
-// and copies ahead) 120 for the prompt.  fp32, a lane's two vectors side by side, so that each copy takes half of every
-// sector: 115 and 193 for the 4000 rows.
+// The steps that carried it, the prompt / its gradient (replays of a graph of one call, some 3 us more each): plain loads, one
+// CTA on an SM 188 / 272; arithmetic in pairs, two CTAs 108 / 240; copies ahead into shared memory, free of bank
+// conflicts, 105 / 203; angles by a warp of their own 88 / -; values read from shared memory again in place of kept, and
+// the CTA's meetings one in four rows, - / 156.  Asking L2 for the next rows gained nothing; three CTAs on an SM (fewer
+// registers and copies ahead) 120 for the prompt.  fp32, a lane's two vectors side by side, so that each copy takes half of
+// every sector: 115 and 193 for the 4000 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -177,7 +177,8 @@ __device__ __forceinline__ float sum_f32x2(uint64_t v) {
 //
 // A CTA takes rows blockIdx.x, + gridDim.x, ... (with few rows, of each the share blockIdx.y of its heads).  Each thread
 // copies its elements of the next kDepth heads, of this row and those after it, into shared memory of its own ahead of
-// their use, without registers and without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its own has made.
+// their use, without registers and without a barrier; the CTA meets once in one or a few rows, whose angles a warp of its
+// own has made.
 // In the gradient a thread's sums of the weights' gradient stay in registers over its heads and rows (kNormTerms); each
 // CTA leaves one partial sum a side and element, and a second kernel adds those in a fixed order.
 template <typename T, NormPairs kPairs, bool kGrad>
@@ -621,8 +622,10 @@ __global__ void __launch_bounds__(256) mfa_norm_rope_weights_kernel(const __grid
 template <typename T, bool kGrad, bool kFold, int kEach>
 __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_rope_any_kernel(const __grid_constant__ NormParams p) {
   __shared__ __align__(16) float cs[2][2][kRopeMaxDim / 2];
-  extern __shared__ __align__(16) uint8_t any_smem[];   // gradient: [warps][head_dim], with sums of many terms in 64 bits before it
-  float* const red = reinterpret_cast<float*>(any_smem) + (kFold ? 2 * (p.q.slots + p.k.slots) * p.head_dim : 0);
+  // gradient: [warps][head_dim], sums of many terms in 64 bits
+  extern __shared__ __align__(16) uint8_t any_smem[];
+  float* const red = reinterpret_cast<float*>(any_smem);
+  const int pitch = kFold ? 2 * p.head_dim : p.head_dim;   // of red: a warp's sums lie where its 64 bits were
   grid_dep_wait();
   if constexpr (!kGrad) grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -703,17 +706,23 @@ __global__ void __launch_bounds__(kNormAnyThreads, kEach <= 8 ? 3 : 1) mfa_norm_
   }
   if constexpr (kGrad) {
     grid_dep_launch();
+    if constexpr (kFold) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (lane + 32 * i < p.head_dim) dw[i] = static_cast<float>(sums[32 * i] + dw[i]);
+      __syncwarp();   // every lane has read its sums
+    }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int e = lane + 32 * i;
-      if (e < p.head_dim) red[warp * p.head_dim + e] = kFold ? static_cast<float>(sums[32 * i] + dw[i]) : dw[i];
+      if (e < p.head_dim) red[warp * pitch + e] = dw[i];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * p.head_dim; e += blockDim.x) {
       const bool on_k = e >= p.head_dim;
       const int from = on_k ? p.q.slots : 0, to = on_k ? p.q.slots + p.k.slots : p.q.slots;
       float v = 0.f;
-      for (int x = from; x < to; ++x) v += red[x * p.head_dim + (on_k ? e - p.head_dim : e)];
+      for (int x = from; x < to; ++x) v += red[x * pitch + (on_k ? e - p.head_dim : e)];
       p.partial[static_cast<size_t>(blockIdx.x) * 2 * p.head_dim + e] = v;
     }
   }
@@ -902,8 +911,8 @@ static mfa_status launch_norm(const mfa_rope_config* c, const mfa_rope_pair* tab
       ctas = std::min(num_rows, grad ? std::min(3 * sms, MFA_NORM_ROPE_GRAD_PARTS) : 6 * sms);
       set_fold(1, 1);
       fn = bf16 ? any_norm<__nv_bfloat16>(p, grad) : any_norm<float>(p, grad);
-      if (grad)   // (8 warps x 512 at most)
-        cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * (p.fold > 0 ? 12 : 4);
+      if (grad)   // (8 warps x 512 at most: 32 KB beside the kernel's own 4)
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.q.slots + p.k.slots) * p.head_dim * (p.fold > 0 ? 8 : 4);
     }
     p.parts = grad ? ctas * shares : 0;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(shares), 1);

@@ -41,6 +41,29 @@ def test_equal_rows(dim, sections, rows, slots, ctas, dtype, pairing):
     assert bool((off <= tol).all()), float((off / tol).max())
 
 
+@pytest.mark.parametrize("dim, dtype", [(511, torch.bfloat16), (512, torch.float32), (250, torch.bfloat16)])
+def test_equal_rows_of_many_wide_heads(dim, dtype):
+    """Heads of up to 512 on every warp of a CTA, each with sums of many terms."""
+    heads, rows, sections = (7, 1), 120000, (50,)
+    gen = torch.Generator().manual_seed(dim)
+    x = [torch.randn((1, n, dim), generator=gen).to(dtype) for n in heads]
+    w = [(1 + torch.randn((dim,), generator=gen) / 4).to(dtype) for _ in heads]
+    pos = torch.tensor([[7]], dtype=torch.int32)
+    op = mfa.NormRope(dim, sections, eps=EPS, pairing="adjacent")
+    ww = [t.to(DEV) for t in w]
+    y = op(*[t.to(DEV) for t in x], *ww, pos.to(DEV))
+    xs, ys = ([t.to(DEV).expand(rows, -1, -1).contiguous() for t in z] for z in (x, y))
+    grads = op.grad(*ys, *xs, *ww, pos.to(DEV).expand(-1, rows).contiguous())
+    for i in range(2):
+        _, _, dw, _ = norm.gradient(x[i], y[i].cpu(), w[i], pos, sections, EPS, pairing="adjacent")
+        h = (x[i].double() * norm.scale(x[i], EPS)).abs()
+        big = 2 * y[i].cpu().double().abs().amax(-1, keepdim=True)
+        own = (norm.turn(y[i].cpu(), pos, sections, 1e4, "adjacent", sign=-1).abs() * h).sum((0, 1))
+        tol = rows * ((big * h).sum((0, 1)) * 2.0 ** -18 + own * additions(rows, 1, 8, CTAS) * 2.0 ** -24)
+        off = (grads[2 + i].cpu().double() - rows * dw).abs()
+        assert bool((off <= tol).all()), float((off / tol).max())
+
+
 @pytest.mark.parametrize("dim, sections, heads, rows, pairing, dtype", [
     (64, (32,), (2, 1), 300000, "half", torch.bfloat16), (256, (44, 42, 42), (64, 1), 22000, "half", torch.bfloat16),
     (33, (3, 5), (9, 2), 70000, "half", torch.bfloat16), (8, (4,), (3, 2), 90000, "adjacent", torch.bfloat16),
